@@ -494,6 +494,63 @@ kvc_status kvc_append_int8(void *out, int32_t out_dtype, const void *q, const vo
                            int32_t max_ctx, int32_t q_heads, float scale, void *stream);
 
 /*
+ * 4-bit pages.  A vector (one kv head at one position) is held as groups of 64 values, each with
+ * a scale and a minimum: x ~ scale * code + minimum, code 0 .. 15.  72 bytes a vector at head_dim
+ * 128 (INT8 pages 132, bf16 256).  (The pages stop at INT8; this follows their rules: quantised
+ * once, when the position is written, and not dequantised by attention.)
+ *   k_codes, v_codes    uint8 [num_pages][page_size][kv_heads][head_dim / 2], byte j holding
+ *                       dim 2 j in its low and dim 2 j + 1 in its high four bits; or
+ *                       [num_pages][kv_heads][page_size][head_dim / 2] with pool.layout = KVC_HND
+ *   k_params, v_params  bf16 [num_pages][kv_heads][page_size][head_dim / 64][2]: (scale, minimum)
+ *                       of each group (either layout)
+ * All four 16-byte aligned; `pool` describes them as it describes a bf16 pool.
+ *
+ * kvc_store_int4 -- quantise and store new K/V at their slots (kvc_store_int8's contract
+ * otherwise).  With lo and hi a group's smallest and largest value, in fp32 with round-to-nearest:
+ * scale = bf16((hi / 2 - lo / 2) / 7.5), code = clamp(rint((x / 2 - lo / 2) / (scale / 2)), 0, 15)
+ * (ties to even; 0 where scale is 0), minimum = lo.  Codes and parameters are exact by this
+ * definition.  A group that holds a NaN or an infinity stores NaN for scale and minimum (codes 0):
+ * attention over it is NaN.
+ */
+kvc_status kvc_store_int4(void *k_codes, void *v_codes, void *k_params, void *v_params,
+                          kvc_pool_desc pool, const void *k_new, const void *v_new,
+                          const int32_t *slot_mapping, int32_t num_tokens, void *stream);
+
+/*
+ * kvc_load_int4 -- the values that 4-bit pages hold at the given slots: k_out[t][g][:] = scale *
+ * code + minimum of slot slot_mapping[t], rounded once from fp32.  The way back to 16-bit pages (a
+ * cached prefix that kvc_append is to extend) or out of the cache.  slot_mapping[t] < 0 gives zeros;
+ * a slot past the pool too, and is flagged (kvc_device_errors).  A slot may be named repeatedly.
+ *   k_out, v_out  [num_tokens][kv_heads][head_dim], out_dtype KVC_BF16 or KVC_F32, 16-byte aligned
+ */
+kvc_status kvc_load_int4(void *k_out, void *v_out, int32_t out_dtype, const void *k_codes,
+                         const void *v_codes, const void *k_params, const void *v_params,
+                         kvc_pool_desc pool, const int32_t *slot_mapping, int32_t num_tokens,
+                         void *stream);
+
+/*
+ * kvc_decode_int4 -- kvc_decode over 4-bit pages (same arguments and outputs, page sizes, layouts
+ * and groups; out, q, block_table and context_lens may be pinned host memory).  Work is cut as in
+ * kvc_decode_int8, in 32-position blocks and with one warp per run: num_splits 0 = one wave of
+ * resident warps (the default), 1 = one warp per (sequence, kv head), no workspace and no
+ * merge, n > 1 = n runs per sequence.  kvc_decode_int4_plan: splits_out = the number of warps,
+ * chunk_out = 32, workspace_bytes_out = the workspace that the call needs (0 for num_splits = 1).
+ * The workspace belongs to one call at a time: calls that may overlap (two streams, two captured
+ * graphs) need one each.  A query row enters the products as fp16 times a power of two of its own
+ * (exact for elements down to 2^-23 of its largest), a probability times a value scale as fp16;
+ * sums are fp32.  A page id outside the pool reads as zeros and is flagged.
+ */
+kvc_status kvc_decode_int4_plan(int32_t num_seqs, int32_t q_heads, kvc_pool_desc pool,
+                                int32_t max_ctx, int32_t num_splits, int32_t *splits_out,
+                                int32_t *chunk_out, size_t *workspace_bytes_out);
+kvc_status kvc_decode_int4(void *out, int32_t out_dtype, const void *q, const void *k_codes,
+                           const void *v_codes, const void *k_params, const void *v_params,
+                           kvc_pool_desc pool, const int32_t *block_table, int32_t bt_stride,
+                           const int32_t *context_lens, int32_t num_seqs, int32_t max_ctx,
+                           int32_t q_heads, float scale, int32_t num_splits, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
  * kvc_copy_pages -- copy-on-write page copy ("KV Cache Management and PagedAttention", "Split
  * shared blocks when a write is needed": before a sequence writes into a page that other
  * sequences still reference, the page is copied to a new one and the writer's block-table

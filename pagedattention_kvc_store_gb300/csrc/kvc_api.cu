@@ -176,6 +176,46 @@ Int8Plan make_int8_plan(int32_t num_seqs, int32_t q_heads, const kvc_pool_desc &
     return p;
 }
 
+// 4-bit decode plan, as the INT8 one, with 32-position blocks and one warp per run: by default the
+// warps that one wave of the kernel's CTAs holds (2 CTAs of 8 warps per SM).
+constexpr int kInt4ResidentWarps = 16;
+
+struct Int4Plan {
+    int runs;            // per kv head
+    bool per_unit;
+    size_t ws_bytes, lse_offset, info_offset;
+};
+
+kvc_status make_int4_plan(int32_t num_seqs, int32_t q_heads, const kvc_pool_desc &pool,
+                          int32_t max_ctx, int32_t requested, Int4Plan *out)
+{
+    Int4Plan p{};
+    const int64_t seqs = num_seqs > 0 ? num_seqs : 1;
+    if (seqs * pool.kv_heads > (int64_t(1) << 28))
+        return fail(KVC_ERR_UNSUPPORTED, "num_seqs * kv_heads must be at most 2^28");
+    if (requested == 1) {
+        p.per_unit = true;
+        p.runs = static_cast<int>(seqs);
+        *out = p;
+        return KVC_OK;
+    }
+    const int64_t blocks = seqs * ceil_div(max_ctx > 0 ? max_ctx : 1, kvc::kInt4Block);
+    int64_t runs = requested <= 0 ? static_cast<int64_t>(kInt4ResidentWarps) * device_sm_count() /
+                                        pool.kv_heads
+                                  : static_cast<int64_t>(requested) * seqs;
+    runs = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(runs, blocks),
+                                                  (int64_t(1) << 29) / pool.kv_heads));
+    p.runs = static_cast<int>(runs);
+    const int64_t group = q_heads / pool.kv_heads;
+    const int64_t slots = pool.kv_heads * (seqs + runs);
+    p.lse_offset = static_cast<size_t>(round_up(slots * group * pool.head_dim * 4, 256));
+    p.info_offset = static_cast<size_t>(
+        round_up(static_cast<int64_t>(p.lse_offset) + slots * group * 4, 256));
+    p.ws_bytes = p.info_offset + static_cast<size_t>(seqs * pool.kv_heads) * 8;
+    *out = p;
+    return KVC_OK;
+}
+
 // ------------------------------------------------------------------------------------------
 // TMA tensor maps over a pool viewed as [num_pages * page_size][kv_heads][head_dim] bf16,
 // boxes of [page_size][1][64] with 128-byte swizzle.  Encoding is host work; the last few
@@ -507,6 +547,8 @@ uint32_t *current_error_word()
 {
     return g_error_word;
 }
+
+int current_sm_count() { return device_sm_count(); }
 }  // namespace kvc
 
 int kvc::set_last_error(int status, const char *message)
@@ -760,6 +802,154 @@ kvc_status kvc_decode_int8_store(void *out, int32_t out_dtype, const void *q, co
                             v_scales, pool, block_table, bt_stride, context_lens, num_seqs,
                             max_ctx, q_heads, scale, num_splits, workspace, workspace_bytes,
                             stream);
+}
+
+namespace {
+
+// The pools of a 4-bit call: shapes, pointers and alignment.
+kvc_status int4_pools(const void *k_codes, const void *v_codes, const void *k_params,
+                      const void *v_params, const kvc_pool_desc &pool, kvc::Int4Pools *out)
+{
+    if (!k_codes || !v_codes || !k_params || !v_params)
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_params) ||
+        !aligned16(v_params))
+        return fail(KVC_ERR_INVALID_ARG, "codes and parameters must be 16-byte aligned");
+    out->k_codes = const_cast<void *>(k_codes);
+    out->v_codes = const_cast<void *>(v_codes);
+    out->k_params = const_cast<void *>(k_params);
+    out->v_params = const_cast<void *>(v_params);
+    out->num_pages = pool.num_pages;
+    out->page_size = pool.page_size;
+    out->kv_heads = pool.kv_heads;
+    out->head_dim = pool.head_dim;
+    out->hnd = pool.layout == KVC_HND;
+    return KVC_OK;
+}
+
+}  // namespace
+
+kvc_status kvc_store_int4(void *k_codes, void *v_codes, void *k_params, void *v_params,
+                          kvc_pool_desc pool, const void *k_new, const void *v_new,
+                          const int32_t *slot_mapping, int32_t num_tokens, void *stream)
+{
+    kvc_status st = check_pool(pool);
+    if (st != KVC_OK)
+        return st;
+    if (num_tokens < 0)
+        return fail(KVC_ERR_INVALID_ARG, "num_tokens %d", num_tokens);
+    if (num_tokens == 0)
+        return ok();
+    kvc::Int4Pools p;
+    if ((st = int4_pools(k_codes, v_codes, k_params, v_params, pool, &p)) != KVC_OK)
+        return st;
+    if (!k_new || !v_new || !slot_mapping)
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(k_new) || !aligned16(v_new))
+        return fail(KVC_ERR_INVALID_ARG, "new K/V must be 16-byte aligned");
+    const cudaError_t err = kvc::launch_store_int4(p, k_new, v_new, slot_mapping, num_tokens,
+                                                   static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "store_int4 launch");
+}
+
+kvc_status kvc_load_int4(void *k_out, void *v_out, int32_t out_dtype, const void *k_codes,
+                         const void *v_codes, const void *k_params, const void *v_params,
+                         kvc_pool_desc pool, const int32_t *slot_mapping, int32_t num_tokens,
+                         void *stream)
+{
+    kvc_status st = check_pool(pool);
+    if (st != KVC_OK)
+        return st;
+    if (out_dtype != KVC_BF16 && out_dtype != KVC_F32)
+        return fail(KVC_ERR_INVALID_ARG, "out_dtype %d", out_dtype);
+    if (num_tokens < 0)
+        return fail(KVC_ERR_INVALID_ARG, "num_tokens %d", num_tokens);
+    if (num_tokens == 0)
+        return ok();
+    kvc::Int4Pools p;
+    if ((st = int4_pools(k_codes, v_codes, k_params, v_params, pool, &p)) != KVC_OK)
+        return st;
+    if (!k_out || !v_out || !slot_mapping)
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(k_out) || !aligned16(v_out))
+        return fail(KVC_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
+    const cudaError_t err =
+        kvc::launch_load_int4(p, k_out, v_out, out_dtype == KVC_F32, slot_mapping, num_tokens,
+                              static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "load_int4 launch");
+}
+
+kvc_status kvc_decode_int4_plan(int32_t num_seqs, int32_t q_heads, kvc_pool_desc pool,
+                                int32_t max_ctx, int32_t num_splits, int32_t *splits_out,
+                                int32_t *chunk_out, size_t *workspace_bytes_out)
+{
+    kvc_status st = check_pool(pool);
+    if (st != KVC_OK)
+        return st;
+    if (num_seqs < 0 || max_ctx < 0 || num_splits < 0)
+        return fail(KVC_ERR_INVALID_ARG, "negative num_seqs, max_ctx or num_splits");
+    if ((st = check_group(pool, q_heads)) != KVC_OK)
+        return st;
+    Int4Plan p;
+    if ((st = make_int4_plan(num_seqs, q_heads, pool, max_ctx, num_splits, &p)) != KVC_OK)
+        return st;
+    if (splits_out)
+        *splits_out = p.runs * pool.kv_heads;
+    if (chunk_out)
+        *chunk_out = kvc::kInt4Block;
+    if (workspace_bytes_out)
+        *workspace_bytes_out = p.ws_bytes;
+    return ok();
+}
+
+kvc_status kvc_decode_int4(void *out, int32_t out_dtype, const void *q, const void *k_codes,
+                           const void *v_codes, const void *k_params, const void *v_params,
+                           kvc_pool_desc pool, const int32_t *block_table, int32_t bt_stride,
+                           const int32_t *context_lens, int32_t num_seqs, int32_t max_ctx,
+                           int32_t q_heads, float scale, int32_t num_splits, void *workspace,
+                           size_t workspace_bytes, void *stream)
+{
+    kvc_status st = check_attention_args(out, out_dtype, q, k_codes, v_codes, pool, block_table,
+                                         bt_stride, context_lens, num_seqs, max_ctx, q_heads);
+    if (st != KVC_OK)
+        return st;
+    if (num_splits < 0)
+        return fail(KVC_ERR_INVALID_ARG, "num_splits %d", num_splits);
+    if (num_seqs == 0)
+        return ok();
+    kvc::DecodeInt4Launch l;
+    if ((st = int4_pools(k_codes, v_codes, k_params, v_params, pool, &l.pools)) != KVC_OK)
+        return st;
+    Int4Plan p;
+    if ((st = make_int4_plan(num_seqs, q_heads, pool, max_ctx, num_splits, &p)) != KVC_OK)
+        return st;
+    if (!p.per_unit) {
+        if (workspace == nullptr || workspace_bytes < p.ws_bytes)
+            return fail(KVC_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given",
+                        p.ws_bytes, workspace == nullptr ? size_t(0) : workspace_bytes);
+        if (!aligned16(workspace))
+            return fail(KVC_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+        l.part_o = static_cast<float *>(workspace);
+        l.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.lse_offset);
+        l.unit_info = static_cast<char *>(workspace) + p.info_offset;
+    }
+    if ((st = check_decode_out(out)) != KVC_OK || (st = check_reachable(q, "q")) != KVC_OK ||
+        (st = check_reachable(block_table, "block_table")) != KVC_OK ||
+        (st = check_reachable(context_lens, "context_lens")) != KVC_OK)
+        return st;
+    l.q = q;
+    l.out = out;
+    l.out_f32 = out_dtype == KVC_F32;
+    l.block_table = block_table;
+    l.bt_stride = bt_stride;
+    l.context_lens = context_lens;
+    l.num_seqs = num_seqs;
+    l.q_heads = q_heads;
+    l.runs = p.runs;
+    l.per_unit = p.per_unit;
+    l.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(pool.head_dim));
+    const cudaError_t err = kvc::launch_decode_int4(l, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "decode_int4 launch");
 }
 
 kvc_status kvc_copy_pages(void *k_pool, void *v_pool, kvc_pool_desc pool,
@@ -1307,6 +1497,12 @@ kvc_status kvc_device_errors(uint32_t *flags_out)
     e |= f;
     if (err == cudaSuccess)
         err = kvc::read_and_clear_append_int8_errors(&f);
+    e |= f;
+    if (err == cudaSuccess)
+        err = kvc::read_and_clear_store_int4_errors(&f);
+    e |= f;
+    if (err == cudaSuccess)
+        err = kvc::read_and_clear_decode_int4_errors(&f);
     e |= f;
     if (err != cudaSuccess)
         return cuda_fail(err, "reading the device error word");

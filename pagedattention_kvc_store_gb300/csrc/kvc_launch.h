@@ -12,6 +12,9 @@ namespace kvc {
 // kernels then set bits in their translation unit's own word, read by kvc_device_errors).
 uint32_t *current_error_word();
 
+// Streaming multiprocessors of the current device (152 where there is none).
+int current_sm_count();
+
 // Launch with programmatic stream serialisation (see pdl_wait / pdl_trigger in kvc_device.cuh):
 // the kernel may start before the previous launch on the stream has finished and waits for it
 // in its first instruction.
@@ -86,6 +89,42 @@ struct DecodeInt8Launch {
 cudaError_t launch_decode_int8(const DecodeInt8Launch &l, const CUtensorMap &tmap_k,
                                const CUtensorMap &tmap_v, cudaStream_t stream);
 cudaError_t read_and_clear_decode_int8_errors(uint32_t *flags);
+
+// Pools of 4-bit pages: codes [pages][P][Hkv][D / 2] (HND: [pages][Hkv][P][D / 2]), two to a byte;
+// parameters [pages][Hkv][P][D / 64] pairs of bf16 (scale, minimum).
+struct Int4Pools {
+    void *k_codes, *v_codes, *k_params, *v_params;
+    int num_pages, page_size, kv_heads, head_dim;
+    bool hnd;
+};
+cudaError_t launch_store_int4(const Int4Pools &p, const void *k_new, const void *v_new,
+                              const int32_t *slots, int num_tokens, cudaStream_t stream);
+cudaError_t launch_load_int4(const Int4Pools &p, void *k_out, void *v_out, bool out_f32,
+                             const int32_t *slots, int num_tokens, cudaStream_t stream);
+cudaError_t read_and_clear_store_int4_errors(uint32_t *flags);
+
+// Decode over 4-bit pages: the positions of all sequences, in kInt4Block-position blocks, are cut
+// into `runs` runs of equal cost per kv head (one warp each); per_unit: one run per sequence, no
+// workspace and no merge.
+constexpr int kInt4Block = 32;
+struct DecodeInt4Launch {
+    Int4Pools pools;
+    const void *q;
+    void *out;
+    bool out_f32;
+    float *part_o = nullptr;      // [Hkv (S + runs)][G][D]
+    float *part_lse = nullptr;    // [Hkv (S + runs)][G]
+    void *unit_info = nullptr;    // [S][Hkv] int2: first partial slot, piece count
+    const int32_t *block_table;
+    int bt_stride;
+    const int32_t *context_lens;
+    int num_seqs, q_heads;
+    int runs = 1;
+    bool per_unit = false;
+    float scale;
+};
+cudaError_t launch_decode_int4(const DecodeInt4Launch &l, cudaStream_t stream);
+cudaError_t read_and_clear_decode_int4_errors(uint32_t *flags);
 
 // Grouped decode over a shared prefix: for each group, the first prefix_len[g] positions are
 // the same pages for every member (the leader's block-table row lists them).

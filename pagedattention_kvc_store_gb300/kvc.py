@@ -31,7 +31,8 @@ EXPORTS = ("kvc_status_string", "kvc_last_error", "kvc_slot_mapping", "kvc_store
            "kvc_validate_workspace_size", "kvc_validate", "kvc_copy_pages", "kvc_store_int8",
            "kvc_decode_int8", "kvc_decode_int8_plan", "kvc_append_int8",
            "kvc_append_store", "kvc_shared_prefix_groups", "kvc_decode_store",
-           "kvc_selftest_wait", "kvc_decode_int8_store", "kvc_set_error_word")
+           "kvc_selftest_wait", "kvc_decode_int8_store", "kvc_set_error_word",
+           "kvc_store_int4", "kvc_load_int4", "kvc_decode_int4", "kvc_decode_int4_plan")
 
 # Size of the library's own split-partials scratch used by kvc_decode_noalloc (bytes).
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -126,6 +127,17 @@ def lib() -> ctypes.CDLL:
             L.kvc_decode_int8_store.restype = ctypes.c_int
             L.kvc_decode_int8_store.argtypes = [p, i32, p, p, p, p, p, p, p, PoolDesc, p, i32, p,
                                                 i32, i32, i32, f, i32, p, sz, p]
+            L.kvc_store_int4.restype = ctypes.c_int
+            L.kvc_store_int4.argtypes = [p, p, p, p, PoolDesc, p, p, p, i32, p]
+            L.kvc_load_int4.restype = ctypes.c_int
+            L.kvc_load_int4.argtypes = [p, p, i32, p, p, p, p, PoolDesc, p, i32, p]
+            L.kvc_decode_int4_plan.restype = ctypes.c_int
+            L.kvc_decode_int4_plan.argtypes = [i32, i32, PoolDesc, i32, i32,
+                                               ctypes.POINTER(i32), ctypes.POINTER(i32),
+                                               ctypes.POINTER(sz)]
+            L.kvc_decode_int4.restype = ctypes.c_int
+            L.kvc_decode_int4.argtypes = [p, i32, p, p, p, p, p, PoolDesc, p, i32, p, i32, i32,
+                                          i32, f, i32, p, sz, p]
             L.kvc_append_int8.restype = ctypes.c_int
             L.kvc_append_int8.argtypes = [p, i32, p, p, p, p, p, PoolDesc, p, i32, p, p, i32,
                                           i32, i32, i32, i32, f, p]
@@ -350,6 +362,119 @@ def kvc_append_int8(out: torch.Tensor, q: torch.Tensor, k_codes: torch.Tensor,
         _ptr(v_scales), pool, _ptr(block_table), int(block_table.shape[1]), _ptr(q_indptr),
         _ptr(context_lens), int(context_lens.shape[0]), int(q.shape[0]), int(max_q_len),
         int(max_ctx), int(q.shape[1]), float(scale), _stream(stream)))
+
+
+def int4_pool_desc(k_codes: torch.Tensor, layout: str = "nhd") -> PoolDesc:
+    """Descriptor of a 4-bit code pool: uint8 [num_pages, page_size, kv_heads, head_dim / 2]
+    (layout "nhd") or [num_pages, kv_heads, page_size, head_dim / 2] (layout "hnd")."""
+    if k_codes.dim() != 4 or k_codes.dtype != torch.uint8:
+        raise ValueError("4-bit codes are a uint8 4-D tensor")
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout {layout!r}: 'nhd' or 'hnd'")
+    n, a, b, d = k_codes.shape
+    page_size, kv_heads = (a, b) if layout == "nhd" else (b, a)
+    return PoolDesc(n, page_size, kv_heads, 2 * d, LAYOUTS[layout])
+
+
+def _int4_pools(k_codes, v_codes, k_params, v_params, layout):
+    pool = int4_pool_desc(_cuda("k_codes", k_codes, torch.uint8), layout)
+    _cuda("v_codes", v_codes, torch.uint8)
+    _cuda("k_params", k_params, torch.bfloat16)
+    _cuda("v_params", v_params, torch.bfloat16)
+    if v_codes.shape != k_codes.shape:
+        raise ValueError("k_codes and v_codes differ in shape")
+    want = (pool.num_pages, pool.kv_heads, pool.page_size, pool.head_dim // 64, 2)
+    if k_params.shape != want or v_params.shape != want:
+        raise ValueError(f"parameters are [num_pages, kv_heads, page_size, head_dim / 64, 2] "
+                         f"= {want}")
+    return pool
+
+
+def _new_vectors(name, t, pool, num_tokens, dtype=None):
+    _cuda(name, t, dtype)
+    want = (num_tokens, pool.kv_heads, pool.head_dim)
+    if t.shape != want:
+        raise ValueError(f"{name} is [num_tokens, kv_heads, head_dim] = {want}, "
+                         f"got {tuple(t.shape)}")
+
+
+def kvc_store_int4(k_codes: torch.Tensor, v_codes: torch.Tensor, k_params: torch.Tensor,
+                   v_params: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                   slot_mapping: torch.Tensor, stream=None, layout: str = "nhd") -> None:
+    """Quantise new tokens' K/V (bf16 [T, Hkv, D]) into 4-bit pages: codes uint8 [pages, P, Hkv,
+    D / 2] (or [pages, Hkv, P, D / 2] with layout "hnd"), parameters bf16 [pages, Hkv, P, D / 64,
+    2] (scale, minimum of each group of 64)."""
+    pool = _int4_pools(k_codes, v_codes, k_params, v_params, layout)
+    _cuda("slot_mapping", slot_mapping, torch.int32)
+    T = slot_mapping.numel()
+    _new_vectors("k_new", k_new, pool, T, torch.bfloat16)
+    _new_vectors("v_new", v_new, pool, T, torch.bfloat16)
+    _check("kvc_store_int4", lib().kvc_store_int4(
+        _ptr(k_codes), _ptr(v_codes), _ptr(k_params), _ptr(v_params), pool, _ptr(k_new),
+        _ptr(v_new), _ptr(slot_mapping), T, _stream(stream)))
+
+
+def kvc_load_int4(k_out: torch.Tensor, v_out: torch.Tensor, k_codes: torch.Tensor,
+                  v_codes: torch.Tensor, k_params: torch.Tensor, v_params: torch.Tensor,
+                  slot_mapping: torch.Tensor, stream=None, layout: str = "nhd") -> None:
+    """The values that 4-bit pages hold at slot_mapping's slots (bf16 or fp32 [T, Hkv, D]; zeros
+    where a slot is negative)."""
+    pool = _int4_pools(k_codes, v_codes, k_params, v_params, layout)
+    _cuda("slot_mapping", slot_mapping, torch.int32)
+    T = slot_mapping.numel()
+    _new_vectors("k_out", k_out, pool, T)
+    _new_vectors("v_out", v_out, pool, T, k_out.dtype)
+    _check("kvc_load_int4", lib().kvc_load_int4(
+        _ptr(k_out), _ptr(v_out), _out_dtype(k_out), _ptr(k_codes), _ptr(v_codes),
+        _ptr(k_params), _ptr(v_params), pool, _ptr(slot_mapping), T, _stream(stream)))
+
+
+def kvc_decode_int4_plan(num_seqs: int, q_heads: int, pool: PoolDesc, max_ctx: int,
+                         num_splits: int = 0) -> Tuple[int, int, int]:
+    """(warps, block, workspace_bytes) of kvc_decode_int4's plan (num_splits 0: one wave of
+    resident warps; 1: one warp per (sequence, kv head), no workspace; n: n runs per sequence)."""
+    splits, chunk, ws = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_size_t()
+    _check("kvc_decode_int4_plan", lib().kvc_decode_int4_plan(
+        int(num_seqs), int(q_heads), pool, int(max_ctx), int(num_splits), ctypes.byref(splits),
+        ctypes.byref(chunk), ctypes.byref(ws)))
+    return splits.value, chunk.value, ws.value
+
+
+def _decode_shapes(out, q, block_table, context_lens, pool):
+    """Shapes of a decode call's per-step arguments against the pool; the number of sequences."""
+    S = context_lens.shape[0]
+    if q.dim() != 3 or q.shape[0] != S or q.shape[2] != pool.head_dim:
+        raise ValueError(f"q is [num_seqs, q_heads, head_dim] with {S} sequences and head_dim "
+                         f"{pool.head_dim}, got {tuple(q.shape)}")
+    if out.shape != q.shape:
+        raise ValueError(f"out is {tuple(q.shape)}, got {tuple(out.shape)}")
+    if block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("block_table is [num_seqs, pages]")
+    return S
+
+
+def kvc_decode_int4(out: torch.Tensor, q: torch.Tensor, k_codes: torch.Tensor,
+                    v_codes: torch.Tensor, k_params: torch.Tensor, v_params: torch.Tensor,
+                    block_table: torch.Tensor, context_lens: torch.Tensor, max_ctx: int,
+                    scale: float = 0.0, num_splits: int = 0,
+                    workspace: Optional[torch.Tensor] = None, stream=None,
+                    layout: str = "nhd") -> None:
+    """kvc_decode over 4-bit pages."""
+    pool = _int4_pools(k_codes, v_codes, k_params, v_params, layout)
+    _decode_out(out)
+    _reachable("q", q, torch.bfloat16)
+    _reachable("block_table", block_table, torch.int32)
+    _reachable("context_lens", context_lens, torch.int32)
+    S = _decode_shapes(out, q, block_table, context_lens, pool)
+    ws = 0
+    if workspace is not None:
+        _cuda("workspace", workspace)
+        ws = workspace.numel() * workspace.element_size()
+    _check("kvc_decode_int4", lib().kvc_decode_int4(
+        _ptr(out), _out_dtype(out), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_params),
+        _ptr(v_params), pool, _ptr(block_table), block_table.shape[1], _ptr(context_lens), S,
+        int(max_ctx), q.shape[1], float(scale), int(num_splits), _ptr(workspace), ws,
+        _stream(stream)))
 
 
 def kvc_copy_pages(k_pool: torch.Tensor, v_pool: torch.Tensor, src_pages: torch.Tensor,
