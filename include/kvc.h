@@ -551,6 +551,68 @@ kvc_status kvc_decode_int4(void *out, int32_t out_dtype, const void *q, const vo
                            size_t workspace_bytes, void *stream);
 
 /*
+ * Eviction.  A cache that may not grow is cut back to a budget of positions per sequence, by how much
+ * attention each position has had (no counterpart on the pages, whose rewind only drops a
+ * sequence's end).  Two arrays go with the pools, one row per sequence that is kept up, fp32 and int32
+ * [num_rows][kv_heads][weight_stride]:
+ *   weights    the attention weight that each slot has had so far (sums over steps and over
+ *              the query heads of the kv head's group); the caller starts a row with zeros
+ *   positions  the original position that each slot holds for that kv head; the caller starts a row
+ *              with 0, 1, 2, ...; kvc_evict keeps it right, also for the tokens to come
+ * A slot here is an index below context_lens[s], the position of the address rule: once slots are
+ * evicted, the newest token is still the last of its sequence, but slot i no longer holds position
+ * i, and each kv head keeps its own positions.  Attention over the slots needs nothing else (keys
+ * carry their positions).  weight_rows[s] is the row of sequence s (NULL: row s); a negative one
+ * leaves that sequence out, one past num_rows too, flagged; rows are distinct within one call.
+ *
+ * kvc_decode_weights -- kvc_decode, bit for bit, and
+ *   weights[row(s)][h][p] += sum over the query heads g of kv head h of softmax_p(q[s][g] . K_s[p] scale)
+ * for every p < context_lens[s], in fp32.  Arguments as kvc_decode; the workspace is always needed
+ * (kvc_decode_weights_plan; splits and chunk are kvc_decode's) and holds the partials and the
+ * scores, 4 bytes per (position, query head); it belongs to one call at a time.  Pages may be
+ * shared between sequences, rows not.
+ *   weights        fp32 [num_rows][kv_heads][weight_stride], weight_stride >= max_ctx
+ *   weight_rows    int32 [num_seqs] or NULL (then num_rows >= num_seqs)
+ */
+kvc_status kvc_decode_weights_plan(int32_t num_seqs, int32_t q_heads, kvc_pool_desc pool,
+                                   int32_t max_ctx, int32_t num_splits, int32_t *splits_out,
+                                   int32_t *chunk_out, size_t *workspace_bytes_out);
+kvc_status kvc_decode_weights(void *out, int32_t out_dtype, float *weights,
+                              const int32_t *weight_rows, int32_t num_rows,
+                              int32_t weight_stride, const void *q, const void *k_pool,
+                              const void *v_pool, kvc_pool_desc pool, const int32_t *block_table,
+                              int32_t bt_stride, const int32_t *context_lens, int32_t num_seqs,
+                              int32_t max_ctx, int32_t q_heads, float scale, int32_t num_splits,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kvc_evict -- for every sequence s and kv head keep n = min(context_lens[s], budget) slots: first
+ * those whose position is among the newest `recent` (positions above that of the last slot minus
+ * recent), then those with the largest weight (NaN below every number), equal ones in slot order.
+ * The kept slots from n on move into the evicted ones below n, both in ascending order (K and V,
+ * raw 16-bit copies; weight and position with them), so that slots 0 .. n - 1 hold what is kept;
+ * new_lens[s] = n.  Pages after the n-th slot's are the caller's to free.  K and V of slots from n on
+ * stay as they are.  The call reads weights and positions and writes weights_out and positions_out,
+ * which may be the same arrays (in place) or others that overlap neither; of a row they get: slots
+ * below n as above, weights_out 0 for n .. context_lens[s] - 1 (the rest untouched), positions_out
+ * for n .. weight_stride - 1 the positions that the next tokens will have.
+ * A sequence within its budget keeps everything.  Pages that are written must be the
+ * sequence's own (kvc_copy_pages first where others list them); moves that touch a page id outside the
+ * pool are skipped and flagged, and that sequence's result is undefined.
+ *   budget         at least 1;  recent  0 .. budget
+ *   new_lens       int32 [num_seqs] (out, device), not context_lens itself: every kv head reads that
+ *   workspace      kvc_evict_plan's bytes (0 when budget >= max_ctx), 16-byte aligned
+ */
+kvc_status kvc_evict_plan(int32_t num_seqs, kvc_pool_desc pool, int32_t max_ctx, int32_t budget,
+                          size_t *workspace_bytes_out);
+kvc_status kvc_evict(void *k_pool, void *v_pool, kvc_pool_desc pool, const int32_t *block_table,
+                     int32_t bt_stride, const int32_t *context_lens, int32_t num_seqs,
+                     int32_t max_ctx, const float *weights, const int32_t *positions,
+                     float *weights_out, int32_t *positions_out, const int32_t *weight_rows,
+                     int32_t num_rows, int32_t weight_stride, int32_t budget, int32_t recent,
+                     int32_t *new_lens, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * kvc_copy_pages -- copy-on-write page copy ("KV Cache Management and PagedAttention", "Split
  * shared blocks when a write is needed": before a sequence writes into a page that other
  * sequences still reference, the page is copied to a new one and the writer's block-table

@@ -10,7 +10,8 @@ from .kvc import (EXPORTS, KVC_BF16, KVC_F32, KVC_HND, KVC_NHD, NOALLOC_SCRATCH_
                   kvc_decode_shared_prefix, kvc_decode_shared_prefix_plan, kvc_shared_prefix_groups,
                   kvc_decode_int8, kvc_decode_int8_plan, kvc_decode_int8_store, kvc_append_int8,
                   int4_pool_desc, kvc_store_int4, kvc_load_int4, kvc_decode_int4,
-                  kvc_decode_int4_plan,
+                  kvc_decode_int4_plan, kvc_decode_weights, kvc_decode_weights_plan, kvc_evict,
+                  kvc_evict_plan,
                   kvc_device_errors, kvc_selftest_wait, kvc_set_error_word, kvc_merge,
                   kvc_slot_mapping, kvc_store, kvc_store_int8, int8_pool_desc,
                   kvc_validate, kvc_validate_workspace_size, lib, library_path, pool_desc)
@@ -22,7 +23,8 @@ __all__ = ["EXPORTS", "KVC_BF16", "KVC_F32", "KVC_HND", "KVC_NHD", "NOALLOC_SCRA
            "kvc_decode_shared_prefix", "kvc_decode_shared_prefix_plan", "kvc_shared_prefix_groups",
            "kvc_decode_int8", "kvc_decode_int8_plan", "kvc_decode_int8_store", "kvc_append_int8",
            "int4_pool_desc", "kvc_store_int4", "kvc_load_int4", "kvc_decode_int4",
-           "kvc_decode_int4_plan",
+           "kvc_decode_int4_plan", "kvc_decode_weights", "kvc_decode_weights_plan", "kvc_evict",
+           "kvc_evict_plan",
            "kvc_device_errors", "kvc_selftest_wait", "kvc_set_error_word", "kvc_merge",
            "kvc_slot_mapping",
            "kvc_store", "kvc_store_int8", "int8_pool_desc",

@@ -1115,6 +1115,222 @@ kvc_status kvc_decode_store(void *out, int32_t out_dtype, const void *q, const v
                        workspace, workspace_bytes, stream);
 }
 
+}  // extern "C"
+
+namespace {
+
+// kvc_decode_weights' plan: kvc_decode's, with a partial for every split (also a single one), its
+// log-sum-exps, the exact base-2 ones, and the scores.
+struct WeightsPlan {
+    Plan p;
+    size_t lse_offset, lse2_offset, scores_offset, score_stride, ws_bytes;
+};
+
+WeightsPlan make_weights_plan(int32_t num_seqs, int32_t q_heads, const kvc_pool_desc &pool,
+                              int32_t max_ctx, int32_t requested)
+{
+    WeightsPlan w{};
+    w.p = make_plan(num_seqs, q_heads, pool, max_ctx, requested);
+    const size_t rows = static_cast<size_t>(num_seqs) * q_heads;
+    const size_t parts = rows * w.p.splits;
+    auto align = [](size_t x) { return (x + 255) / 256 * 256; };
+    w.lse_offset = align(parts * pool.head_dim * sizeof(float));
+    w.lse2_offset = align(w.lse_offset + parts * sizeof(float));
+    w.scores_offset = align(w.lse2_offset + parts * sizeof(float));
+    w.score_stride = static_cast<size_t>(w.p.splits) * w.p.chunk;
+    w.ws_bytes = w.scores_offset + rows * w.score_stride * sizeof(float);
+    return w;
+}
+
+// The rows of accumulated weights that a call names.
+kvc_status check_weight_rows(const void *weights, const int32_t *weight_rows, int32_t num_rows,
+                             int32_t weight_stride, int32_t num_seqs, int32_t max_ctx)
+{
+    if (!weights)
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument");
+    if (num_rows < 0 || (weight_rows == nullptr && num_rows < num_seqs))
+        return fail(KVC_ERR_INVALID_ARG, "num_rows %d for %d sequences", num_rows, num_seqs);
+    if (weight_stride < max_ctx)
+        return fail(KVC_ERR_INVALID_ARG, "weight_stride %d cannot hold max_ctx %d", weight_stride,
+                    max_ctx);
+    return KVC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvc_status kvc_decode_weights_plan(int32_t num_seqs, int32_t q_heads, kvc_pool_desc pool,
+                                   int32_t max_ctx, int32_t num_splits, int32_t *splits_out,
+                                   int32_t *chunk_out, size_t *workspace_bytes_out)
+{
+    kvc_status st = check_pool(pool);
+    if (st != KVC_OK)
+        return st;
+    if ((st = check_group(pool, q_heads)) != KVC_OK)
+        return st;
+    if (num_seqs < 0 || max_ctx < 0 || num_splits < 0)
+        return fail(KVC_ERR_INVALID_ARG, "negative num_seqs, max_ctx or num_splits");
+    const WeightsPlan w = make_weights_plan(num_seqs, q_heads, pool, max_ctx, num_splits);
+    if (splits_out)
+        *splits_out = w.p.splits;
+    if (chunk_out)
+        *chunk_out = w.p.chunk;
+    if (workspace_bytes_out)
+        *workspace_bytes_out = w.ws_bytes;
+    return ok();
+}
+
+kvc_status kvc_decode_weights(void *out, int32_t out_dtype, float *weights,
+                              const int32_t *weight_rows, int32_t num_rows,
+                              int32_t weight_stride, const void *q, const void *k_pool,
+                              const void *v_pool, kvc_pool_desc pool, const int32_t *block_table,
+                              int32_t bt_stride, const int32_t *context_lens, int32_t num_seqs,
+                              int32_t max_ctx, int32_t q_heads, float scale, int32_t num_splits,
+                              void *workspace, size_t workspace_bytes, void *stream)
+{
+    kvc_status st = check_attention_args(out, out_dtype, q, k_pool, v_pool, pool, block_table,
+                                         bt_stride, context_lens, num_seqs, max_ctx, q_heads);
+    if (st != KVC_OK)
+        return st;
+    if (num_splits < 0)
+        return fail(KVC_ERR_INVALID_ARG, "num_splits %d", num_splits);
+    if (num_seqs == 0)
+        return ok();
+    if ((st = check_weight_rows(weights, weight_rows, num_rows, weight_stride, num_seqs,
+                                max_ctx)) != KVC_OK)
+        return st;
+    const WeightsPlan w = make_weights_plan(num_seqs, q_heads, pool, max_ctx, num_splits);
+    if (workspace == nullptr || workspace_bytes < w.ws_bytes)
+        return fail(KVC_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", w.ws_bytes,
+                    workspace == nullptr ? size_t(0) : workspace_bytes);
+    if (!aligned16(workspace))
+        return fail(KVC_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    if ((st = check_decode_out(out)) != KVC_OK || (st = check_reachable(q, "q")) != KVC_OK ||
+        (st = check_reachable(block_table, "block_table")) != KVC_OK ||
+        (st = check_reachable(context_lens, "context_lens")) != KVC_OK)
+        return st;
+    CUtensorMap tk, tv;
+    if ((st = pool_tensor_map(k_pool, pool, &tk)) != KVC_OK)
+        return st;
+    if ((st = pool_tensor_map(v_pool, pool, &tv)) != KVC_OK)
+        return st;
+    char *ws = static_cast<char *>(workspace);
+    kvc::DecodeLaunch l;
+    l.q = q;
+    l.out = out;
+    l.out_f32 = out_dtype == KVC_F32;
+    l.part_o = reinterpret_cast<float *>(ws);
+    l.part_lse = reinterpret_cast<float *>(ws + w.lse_offset);
+    l.block_table = block_table;
+    l.bt_stride = bt_stride;
+    l.context_lens = context_lens;
+    l.num_seqs = num_seqs;
+    l.q_heads = q_heads;
+    l.kv_heads = pool.kv_heads;
+    l.head_dim = pool.head_dim;
+    l.page_size = pool.page_size;
+    l.chunk = w.p.chunk;
+    l.n_split = w.p.splits;
+    l.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(pool.head_dim));
+    l.hnd = pool.layout == KVC_HND;
+    kvc::WeightsLaunch wl;
+    wl.weights = weights;
+    wl.rows = weight_rows;
+    wl.num_rows = num_rows;
+    wl.weight_stride = weight_stride;
+    wl.max_ctx = max_ctx;
+    wl.scores = reinterpret_cast<float *>(ws + w.scores_offset);
+    wl.score_stride = w.score_stride;
+    wl.part_lse2 = reinterpret_cast<float *>(ws + w.lse2_offset);
+    const cudaError_t err =
+        kvc::launch_decode_weights(l, wl, tk, tv, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "decode_weights launch");
+}
+
+kvc_status kvc_evict_plan(int32_t num_seqs, kvc_pool_desc pool, int32_t max_ctx, int32_t budget,
+                          size_t *workspace_bytes_out)
+{
+    kvc_status st = check_pool(pool);
+    if (st != KVC_OK)
+        return st;
+    if (num_seqs < 0 || max_ctx < 0)
+        return fail(KVC_ERR_INVALID_ARG, "negative num_seqs or max_ctx");
+    if (budget < 1)
+        return fail(KVC_ERR_INVALID_ARG, "budget %d (at least 1)", budget);
+    const size_t cap = static_cast<size_t>(std::max(0, std::min(budget, max_ctx - budget)));
+    if (workspace_bytes_out)
+        *workspace_bytes_out =
+            static_cast<size_t>(num_seqs) * pool.kv_heads * 2 * cap * sizeof(int32_t);
+    return ok();
+}
+
+kvc_status kvc_evict(void *k_pool, void *v_pool, kvc_pool_desc pool, const int32_t *block_table,
+                     int32_t bt_stride, const int32_t *context_lens, int32_t num_seqs,
+                     int32_t max_ctx, const float *weights, const int32_t *positions,
+                     float *weights_out, int32_t *positions_out, const int32_t *weight_rows,
+                     int32_t num_rows, int32_t weight_stride, int32_t budget, int32_t recent,
+                     int32_t *new_lens, void *workspace, size_t workspace_bytes, void *stream)
+{
+    size_t need = 0;
+    kvc_status st = kvc_evict_plan(num_seqs, pool, max_ctx, budget, &need);
+    if (st != KVC_OK)
+        return st;
+    if (recent < 0 || recent > budget)
+        return fail(KVC_ERR_INVALID_ARG, "recent %d (0 .. budget %d)", recent, budget);
+    if (num_seqs > 65535)
+        return fail(KVC_ERR_INVALID_ARG, "num_seqs %d (0 .. 65535)", num_seqs);
+    if (bt_stride <= 0 || static_cast<int64_t>(bt_stride) * pool.page_size < max_ctx)
+        return fail(KVC_ERR_INVALID_ARG, "bt_stride %d cannot hold max_ctx %d", bt_stride,
+                    max_ctx);
+    if (num_seqs == 0)
+        return ok();
+    if (!k_pool || !v_pool || !block_table || !context_lens || !positions || !weights_out ||
+        !positions_out || !new_lens)
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(k_pool) || !aligned16(v_pool))
+        return fail(KVC_ERR_INVALID_ARG, "pools must be 16-byte aligned");
+    if (new_lens == context_lens)
+        return fail(KVC_ERR_INVALID_ARG, "new_lens must not be context_lens");
+    if ((st = check_weight_rows(weights, weight_rows, num_rows, weight_stride, num_seqs,
+                                max_ctx)) != KVC_OK)
+        return st;
+    if (need > 0) {
+        if (workspace == nullptr || workspace_bytes < need)
+            return fail(KVC_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                        workspace == nullptr ? size_t(0) : workspace_bytes);
+        if (!aligned16(workspace))
+            return fail(KVC_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    }
+    kvc::EvictLaunch l;
+    l.k_pool = k_pool;
+    l.v_pool = v_pool;
+    l.block_table = block_table;
+    l.bt_stride = bt_stride;
+    l.context_lens = context_lens;
+    l.num_seqs = num_seqs;
+    l.max_ctx = max_ctx;
+    l.weights = weights;
+    l.positions = positions;
+    l.weights_out = weights_out;
+    l.positions_out = positions_out;
+    l.rows = weight_rows;
+    l.num_rows = num_rows;
+    l.stride = weight_stride;
+    l.budget = budget;
+    l.recent = recent;
+    l.new_lens = new_lens;
+    l.lists = workspace;
+    l.list_cap = std::max(0, std::min(budget, max_ctx - budget));
+    l.kv_heads = pool.kv_heads;
+    l.head_dim = pool.head_dim;
+    l.page_size = pool.page_size;
+    l.num_pages = pool.num_pages;
+    l.hnd = pool.layout == KVC_HND;
+    const cudaError_t err = kvc::launch_evict(l, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "evict launch");
+}
+
 kvc_status kvc_shared_prefix_groups(const int32_t *block_table, int32_t bt_stride,
                                     const int32_t *context_lens, int32_t num_seqs,
                                     int32_t page_size, int32_t max_members,
@@ -1503,6 +1719,12 @@ kvc_status kvc_device_errors(uint32_t *flags_out)
     e |= f;
     if (err == cudaSuccess)
         err = kvc::read_and_clear_decode_int4_errors(&f);
+    e |= f;
+    if (err == cudaSuccess)
+        err = kvc::read_and_clear_weights_errors(&f);
+    e |= f;
+    if (err == cudaSuccess)
+        err = kvc::read_and_clear_evict_errors(&f);
     e |= f;
     if (err != cudaSuccess)
         return cuda_fail(err, "reading the device error word");

@@ -45,7 +45,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                          a.err ? a.err : &g_decode_errors);
 }
 
-// One warp per row: out[r] = sum_j exp(lse_j - M) o_j / sum_j exp(lse_j - M).
 template <int D>
 __global__ void __launch_bounds__(128) merge_kernel(void *out, int out_f32,
                                                     const float *__restrict__ part_o,
@@ -54,92 +53,9 @@ __global__ void __launch_bounds__(128) merge_kernel(void *out, int out_f32,
 {
     pdl_wait();
     pdl_trigger();
-    constexpr int V = D / 32;
     const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= rows)
-        return;
-    const float *lse = part_lse + static_cast<size_t>(row) * n_split;
-    const float *po = part_o + static_cast<size_t>(row) * n_split * D + lane * V;
-    // The first kPre splits' partials are requested together with the lse values (one memory
-    // round trip instead of two on the step's critical path); an empty split's values are
-    // loaded but never used.
-    constexpr int kPre = 4;
-    float pre[kPre][V];
-#pragma unroll
-    for (int j = 0; j < kPre; ++j) {
-        if (j < n_split) {
-            if constexpr (V == 4) {
-                const float4 t = *reinterpret_cast<const float4 *>(po + static_cast<size_t>(j) * D);
-                pre[j][0] = t.x;
-                pre[j][1] = t.y;
-                pre[j][2] = t.z;
-                pre[j][3] = t.w;
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    pre[j][v] = po[static_cast<size_t>(j) * D + v];
-            }
-        }
-    }
-    float M = -INFINITY;
-    for (int j = lane; j < n_split; j += 32)
-        M = fmaxf(M, lse[j]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float acc[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        acc[v] = 0.0f;
-    float sum = 0.0f;
-    if (M != -INFINITY) {
-        for (int j0 = 0; j0 < n_split; j0 += 32) {
-            const float mine = (j0 + lane < n_split) ? lse[j0 + lane] : -INFINITY;
-            const int cnt = min(32, n_split - j0);
-            for (int jj = 0; jj < cnt; ++jj) {
-                const float lj = __shfl_sync(0xffffffffu, mine, jj);
-                if (lj == -INFINITY)
-                    continue;   // empty split: its partial is not read
-                const float w = fast_exp2((lj - M) * kLog2e);
-                sum += w;
-                const int j = j0 + jj;
-                float val[V];
-                if (j < kPre) {   // select in registers (no dynamic index into pre)
-#pragma unroll
-                    for (int k = 0; k < kPre; ++k)
-                        if (k == j) {
-#pragma unroll
-                            for (int v = 0; v < V; ++v)
-                                val[v] = pre[k][v];
-                        }
-                } else if constexpr (V == 4) {
-                    const float4 t =
-                        *reinterpret_cast<const float4 *>(po + static_cast<size_t>(j) * D);
-                    val[0] = t.x;
-                    val[1] = t.y;
-                    val[2] = t.z;
-                    val[3] = t.w;
-                } else {
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        val[v] = po[static_cast<size_t>(j) * D + v];
-                }
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    acc[v] += w * val[v];
-            }
-        }
-    }
-    const float inv = (sum > 0.0f) ? 1.0f / sum : 0.0f;
-    const size_t base = static_cast<size_t>(row) * D + lane * V;
-    if constexpr (V == 4)
-        store_out4(out, out_f32, base,
-                   make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv));
-    else
-        store_out2(out, out_f32, base, make_float2(acc[0] * inv, acc[1] * inv));
-    if (lse_out != nullptr && lane == 0)
-        lse_out[row] = (M == -INFINITY) ? -INFINITY : M + logf(sum);
+    if (row < rows)
+        merge_row<D>(out, out_f32, part_o, part_lse, row, n_split, lse_out);
 }
 
 template <int D, bool SPLIT>

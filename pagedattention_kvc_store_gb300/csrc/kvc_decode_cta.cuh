@@ -30,8 +30,8 @@ struct DecodeGeom {
     static constexpr int kRingBytes = kStages * kStageBytes;
     // after the ring: full[kStages], empty[kStages] mbarriers
     static constexpr int kBarrierBytes = 2 * kStages * 8;
-    static constexpr int kCombineBytes =   // o rows, m, l per warp; weights per row
-        kConsumerWarps * kMaxGroup * (D + 8) * 4 + 3 * kConsumerWarps * kMaxGroup * 4;
+    static constexpr int kCombineBytes =   // o rows, m, l (two sums) per warp; weights per row
+        kConsumerWarps * kMaxGroup * (D + 8) * 4 + 4 * kConsumerWarps * kMaxGroup * 4;
     static_assert(kCombineBytes <= kRingBytes, "combine area aliases the ring");
     static constexpr size_t kSmemBytes = 1024 /* alignment slack */ + kRingBytes + kBarrierBytes;
 };
@@ -59,6 +59,11 @@ struct Args {
     uint4 *k_pool, *v_pool;
     int num_slots;
     uint32_t *err;   // the caller's device error word, or null (the kernel's own word)
+    // Attention weights (kvc_decode_weights, SCORES): every score in base-2 units, [S][Hq]
+    // [score_stride], and per partial the log2-sum-exp2 of its scores, unrounded.
+    float *scores = nullptr;
+    size_t score_stride = 0;
+    float *part_lse2 = nullptr;
 };
 
 // Kernel arguments from the host-side launch description.
@@ -95,8 +100,10 @@ inline Args make_args(const DecodeLaunch &l)
 
 // One CTA (kThreads threads, DecodeGeom<D>::kSmemBytes of dynamic shared memory, `smem`
 // 1024-byte aligned) on chunk `split` of kv head `kvh` of sequence `s`; device-side failures
-// are or-ed into *errors.
-template <int D, bool SPLIT>
+// are or-ed into *errors.  SCORES (with SPLIT) also leaves every score and each chunk's exact
+// log2-sum-exp2 for the attention weights; the output's sum stays the one over the rounded
+// probabilities that its numerator uses.
+template <int D, bool SPLIT, bool SCORES = false>
 __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUtensorMap *tmap_v,
                                            const Args &a, const int split, const int kvh,
                                            const int s, uint8_t *smem, uint32_t *errors)
@@ -143,6 +150,9 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUte
         if (SPLIT) {
             if (threadIdx.x < G)
                 a.part_lse[(row0 + threadIdx.x) * a.split_stride + a.split_base + split] =
+                    -INFINITY;
+            if (SCORES && threadIdx.x < G)
+                a.part_lse2[(row0 + threadIdx.x) * a.split_stride + a.split_base + split] =
                     -INFINITY;
         } else {
             for (int i = threadIdx.x; i < G * D; i += blockDim.x)
@@ -274,6 +284,11 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUte
         o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
     float m_run = -INFINITY;   // running max (base-2 scaled scores) of row r
     float l_run = 0.0f;        // this thread's part of the running sum of row r
+    float lx_run = 0.0f;       // SCORES: the same over the unrounded probabilities
+    float *score_row = nullptr;
+    if constexpr (SCORES)
+        score_row = a.scores + (row0 + (r < G ? r : 0)) * a.score_stride + k_begin +
+                    warp * kKeysPerWarp + cq;
 
     // ldmatrix lane addresses (row/column inside this warp's 16 positions of a stage)
     const int k_row = warp * kKeysPerWarp + (lane & 7) + ((lane >> 4) << 3);
@@ -310,6 +325,15 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUte
                     if ((i >> 1) * 8 + cq + (i & 1) >= n_valid)
                         x[i] = -INFINITY;
             }
+            if constexpr (SCORES) {
+                // past the context -inf: the row holds whole stages
+                if (r < G) {
+                    *reinterpret_cast<float2 *>(score_row + b * kStageKeys) =
+                        make_float2(x[0], x[1]);
+                    *reinterpret_cast<float2 *>(score_row + b * kStageKeys + 8) =
+                        make_float2(x[2], x[3]);
+                }
+            }
             float mb = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
             mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
             mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
@@ -322,6 +346,8 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUte
                     o[n][1] *= alpha;
                 }
                 l_run *= alpha;
+                if (SCORES)
+                    lx_run *= alpha;
                 m_run = m_new;
             }
             const float m_use = (m_run == -INFINITY) ? 0.0f : m_run;
@@ -332,6 +358,8 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUte
             const uint32_t pa0 = pack_bf16x2(p[0], p[1]);   // row r, positions cq, cq+1
             const uint32_t pa2 = pack_bf16x2(p[2], p[3]);   // row r, positions 8+cq, 9+cq
             l_run += bf16x2_sum(pa0) + bf16x2_sum(pa2);
+            if (SCORES)
+                lx_run += (p[0] + p[1]) + (p[2] + p[3]);
 #pragma unroll
             for (int dt = 0; dt < D / 16; ++dt) {
                 uint32_t v0, v1, v2, v3;
@@ -362,11 +390,16 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUte
     constexpr int kRowStride = D + 8;
     l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
     l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+    if (SCORES) {
+        lx_run += __shfl_xor_sync(0xffffffffu, lx_run, 1);
+        lx_run += __shfl_xor_sync(0xffffffffu, lx_run, 2);
+    }
     named_barrier(1, kConsumerWarps * 32);   // every warp is done with the ring
     float *red_o = reinterpret_cast<float *>(smem);                      // [W][8][D + 8]
     float *red_m = red_o + kConsumerWarps * kMaxGroup * kRowStride;       // [W][8]
     float *red_l = red_m + kConsumerWarps * kMaxGroup;                    // [W][8]
     float *row_w = red_l + kConsumerWarps * kMaxGroup;                    // [8][W]
+    float *red_lx = row_w + kConsumerWarps * kMaxGroup;                   // [W][8], SCORES
     if (r < G) {
         float *dst = red_o + (warp * kMaxGroup + r) * kRowStride + cq;
 #pragma unroll
@@ -375,6 +408,8 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUte
         if ((lane & 3) == 0) {
             red_m[warp * kMaxGroup + r] = m_run;
             red_l[warp * kMaxGroup + r] = l_run;
+            if (SCORES)
+                red_lx[warp * kMaxGroup + r] = lx_run;
         }
     }
     named_barrier(1, kConsumerWarps * 32);
@@ -399,6 +434,13 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUte
         if (SPLIT)
             a.part_lse[(row0 + row) * a.split_stride + a.split_base + split] =
                 (M + log2f(L)) * kLn2;
+        if constexpr (SCORES) {
+            float Lx = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kConsumerWarps; ++w)
+                Lx += f[w] * red_lx[w * kMaxGroup + row];
+            a.part_lse2[(row0 + row) * a.split_stride + a.split_base + split] = M + log2f(Lx);
+        }
     }
     named_barrier(1, kConsumerWarps * 32);
     constexpr int kVec = D / 4;
@@ -423,6 +465,98 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUte
             store_out4(a.out, a.out_f32, (row0 + row) * D + c, acc);
         }
     }
+}
+
+// One warp per row: out[r] = sum_j exp(lse_j - M) o_j / sum_j exp(lse_j - M).
+template <int D>
+__device__ __forceinline__ void merge_row(void *out, int out_f32,
+                                          const float *__restrict__ part_o,
+                                          const float *__restrict__ part_lse, int row,
+                                          int n_split, float *lse_out)
+{
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31;
+    const float *lse = part_lse + static_cast<size_t>(row) * n_split;
+    const float *po = part_o + static_cast<size_t>(row) * n_split * D + lane * V;
+    // The first kPre splits' partials are requested together with the lse values (one memory
+    // round trip instead of two on the step's critical path); an empty split's values are
+    // loaded but never used.
+    constexpr int kPre = 4;
+    float pre[kPre][V];
+#pragma unroll
+    for (int j = 0; j < kPre; ++j) {
+        if (j < n_split) {
+            if constexpr (V == 4) {
+                const float4 t = *reinterpret_cast<const float4 *>(po + static_cast<size_t>(j) * D);
+                pre[j][0] = t.x;
+                pre[j][1] = t.y;
+                pre[j][2] = t.z;
+                pre[j][3] = t.w;
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    pre[j][v] = po[static_cast<size_t>(j) * D + v];
+            }
+        }
+    }
+    float M = -INFINITY;
+    for (int j = lane; j < n_split; j += 32)
+        M = fmaxf(M, lse[j]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        acc[v] = 0.0f;
+    float sum = 0.0f;
+    if (M != -INFINITY) {
+        for (int j0 = 0; j0 < n_split; j0 += 32) {
+            const float mine = (j0 + lane < n_split) ? lse[j0 + lane] : -INFINITY;
+            const int cnt = min(32, n_split - j0);
+            for (int jj = 0; jj < cnt; ++jj) {
+                const float lj = __shfl_sync(0xffffffffu, mine, jj);
+                if (lj == -INFINITY)
+                    continue;   // empty split: its partial is not read
+                const float w = fast_exp2((lj - M) * kLog2e);
+                sum += w;
+                const int j = j0 + jj;
+                float val[V];
+                if (j < kPre) {   // select in registers (no dynamic index into pre)
+#pragma unroll
+                    for (int k = 0; k < kPre; ++k)
+                        if (k == j) {
+#pragma unroll
+                            for (int v = 0; v < V; ++v)
+                                val[v] = pre[k][v];
+                        }
+                } else if constexpr (V == 4) {
+                    const float4 t =
+                        *reinterpret_cast<const float4 *>(po + static_cast<size_t>(j) * D);
+                    val[0] = t.x;
+                    val[1] = t.y;
+                    val[2] = t.z;
+                    val[3] = t.w;
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        val[v] = po[static_cast<size_t>(j) * D + v];
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    acc[v] += w * val[v];
+            }
+        }
+    }
+    const float inv = (sum > 0.0f) ? 1.0f / sum : 0.0f;
+    const size_t base = static_cast<size_t>(row) * D + lane * V;
+    if constexpr (V == 4)
+        store_out4(out, out_f32, base,
+                   make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv));
+    else
+        store_out2(out, out_f32, base, make_float2(acc[0] * inv, acc[1] * inv));
+    if (lse_out != nullptr && lane == 0)
+        lse_out[row] = (M == -INFINITY) ? -INFINITY : M + logf(sum);
 }
 
 }  // namespace dec

@@ -126,6 +126,46 @@ struct DecodeInt4Launch {
 cudaError_t launch_decode_int4(const DecodeInt4Launch &l, cudaStream_t stream);
 cudaError_t read_and_clear_decode_int4_errors(uint32_t *flags);
 
+// kvc_decode_weights: the decode of `l` (its partials for every split, also when there is one), its
+// scores [S][Hq][score_stride] and exact log2-sum-exp2s [S][Hq][n_split], added up into weights
+// [num_rows][Hkv][weight_stride].
+struct WeightsLaunch {
+    float *weights;
+    const int32_t *rows;   // [S] or null
+    int num_rows, weight_stride, max_ctx;
+    float *scores;
+    size_t score_stride;
+    float *part_lse2;
+};
+cudaError_t launch_decode_weights(const DecodeLaunch &l, const WeightsLaunch &w,
+                                  const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                                  cudaStream_t stream);
+cudaError_t read_and_clear_weights_errors(uint32_t *flags);
+
+// kvc_evict: lists int32 [S][Hkv][2][list_cap] (the moves of each (sequence, kv head)).
+constexpr int kMaxCached = 48 * 1024;   // keys that a CTA keeps in shared memory
+struct EvictLaunch {
+    void *k_pool, *v_pool;
+    const int32_t *block_table;
+    int bt_stride;
+    const int32_t *context_lens;
+    int num_seqs, max_ctx;
+    const float *weights;
+    const int32_t *positions;
+    float *weights_out;
+    int32_t *positions_out;
+    const int32_t *rows;   // [S] or null
+    int num_rows, stride;
+    int budget, recent;
+    int32_t *new_lens;
+    void *lists;
+    int list_cap;
+    int kv_heads, head_dim, page_size, num_pages;
+    bool hnd;
+};
+cudaError_t launch_evict(const EvictLaunch &l, cudaStream_t stream);
+cudaError_t read_and_clear_evict_errors(uint32_t *flags);
+
 // Grouped decode over a shared prefix: for each group, the first prefix_len[g] positions are
 // the same pages for every member (the leader's block-table row lists them).
 struct GroupedPrefixLaunch {

@@ -32,7 +32,8 @@ EXPORTS = ("kvc_status_string", "kvc_last_error", "kvc_slot_mapping", "kvc_store
            "kvc_decode_int8", "kvc_decode_int8_plan", "kvc_append_int8",
            "kvc_append_store", "kvc_shared_prefix_groups", "kvc_decode_store",
            "kvc_selftest_wait", "kvc_decode_int8_store", "kvc_set_error_word",
-           "kvc_store_int4", "kvc_load_int4", "kvc_decode_int4", "kvc_decode_int4_plan")
+           "kvc_store_int4", "kvc_load_int4", "kvc_decode_int4", "kvc_decode_int4_plan",
+           "kvc_decode_weights", "kvc_decode_weights_plan", "kvc_evict", "kvc_evict_plan")
 
 # Size of the library's own split-partials scratch used by kvc_decode_noalloc (bytes).
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -138,6 +139,16 @@ def lib() -> ctypes.CDLL:
             L.kvc_decode_int4.restype = ctypes.c_int
             L.kvc_decode_int4.argtypes = [p, i32, p, p, p, p, p, PoolDesc, p, i32, p, i32, i32,
                                           i32, f, i32, p, sz, p]
+            L.kvc_decode_weights_plan.restype = ctypes.c_int
+            L.kvc_decode_weights_plan.argtypes = L.kvc_decode_int4_plan.argtypes
+            L.kvc_decode_weights.restype = ctypes.c_int
+            L.kvc_decode_weights.argtypes = [p, i32, p, p, i32, i32, p, p, p, PoolDesc, p, i32, p,
+                                             i32, i32, i32, f, i32, p, sz, p]
+            L.kvc_evict_plan.restype = ctypes.c_int
+            L.kvc_evict_plan.argtypes = [i32, PoolDesc, i32, i32, ctypes.POINTER(sz)]
+            L.kvc_evict.restype = ctypes.c_int
+            L.kvc_evict.argtypes = [p, p, PoolDesc, p, i32, p, i32, i32, p, p, p, p, p, i32, i32,
+                                    i32, i32, p, p, sz, p]
             L.kvc_append_int8.restype = ctypes.c_int
             L.kvc_append_int8.argtypes = [p, i32, p, p, p, p, p, PoolDesc, p, i32, p, p, i32,
                                           i32, i32, i32, i32, f, p]
@@ -550,6 +561,107 @@ def kvc_decode_store(out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor,
         _ptr(v_pool), pool_desc(k_pool, layout), _ptr(block_table), int(block_table.shape[1]),
         _ptr(context_lens), int(context_lens.shape[0]), int(max_ctx), int(q.shape[1]),
         float(scale), int(num_splits), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def kvc_decode_weights_plan(num_seqs: int, q_heads: int, pool: PoolDesc, max_ctx: int,
+                            num_splits: int = 0) -> Tuple[int, int, int]:
+    """(splits, chunk, workspace_bytes) that kvc_decode_weights will use."""
+    splits, chunk, ws = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_size_t()
+    _check("kvc_decode_weights_plan", lib().kvc_decode_weights_plan(
+        int(num_seqs), int(q_heads), pool, int(max_ctx), int(num_splits), ctypes.byref(splits),
+        ctypes.byref(chunk), ctypes.byref(ws)))
+    return splits.value, chunk.value, ws.value
+
+
+def _weight_rows(name, t, dtype, pool, like=None):
+    """An array [rows, kv_heads, stride] that goes with the pools."""
+    _cuda(name, t, dtype)
+    if t.dim() != 3 or t.shape[1] != pool.kv_heads or (like is not None and t.shape != like.shape):
+        raise ValueError(f"{name} is [rows, kv_heads = {pool.kv_heads}, stride], the same for "
+                         f"every such argument; got {tuple(t.shape)}")
+    return t
+
+
+def _sequence_rows(weight_rows, S):
+    if weight_rows is not None:
+        _cuda("weight_rows", weight_rows, torch.int32)
+        if weight_rows.numel() != S:
+            raise ValueError(f"weight_rows has an entry for each of the {S} sequences")
+    return _ptr(weight_rows)
+
+
+def kvc_decode_weights(out: torch.Tensor, weights: torch.Tensor, q: torch.Tensor,
+                       k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.Tensor,
+                       context_lens: torch.Tensor, max_ctx: int, scale: float = 0.0,
+                       num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
+                       weight_rows: Optional[torch.Tensor] = None, stream=None,
+                       layout: str = "nhd") -> None:
+    """kvc_decode that also adds every position's attention weight to weights (fp32 [rows, Hkv,
+    stride], summed over the query heads of each kv head; sequence s has row weight_rows[s], or
+    row s)."""
+    _decode_out(out)
+    _reachable("q", q, torch.bfloat16)
+    _cuda("k_pool", k_pool, torch.bfloat16)
+    _cuda("v_pool", v_pool, torch.bfloat16)
+    _reachable("block_table", block_table, torch.int32)
+    _reachable("context_lens", context_lens, torch.int32)
+    pool = pool_desc(k_pool, layout)
+    S = _decode_shapes(out, q, block_table, context_lens, pool)
+    _weight_rows("weights", weights, torch.float32, pool)
+    ws = 0
+    if workspace is not None:
+        _cuda("workspace", workspace)
+        ws = workspace.numel() * workspace.element_size()
+    _check("kvc_decode_weights", lib().kvc_decode_weights(
+        _ptr(out), _out_dtype(out), _ptr(weights), _sequence_rows(weight_rows, S),
+        weights.shape[0], weights.shape[2], _ptr(q), _ptr(k_pool), _ptr(v_pool), pool,
+        _ptr(block_table), block_table.shape[1], _ptr(context_lens), S, int(max_ctx), q.shape[1],
+        float(scale), int(num_splits), _ptr(workspace), ws, _stream(stream)))
+
+
+def kvc_evict_plan(num_seqs: int, pool: PoolDesc, max_ctx: int, budget: int) -> int:
+    """Workspace bytes kvc_evict needs."""
+    ws = ctypes.c_size_t()
+    _check("kvc_evict_plan", lib().kvc_evict_plan(int(num_seqs), pool, int(max_ctx), int(budget),
+                                                  ctypes.byref(ws)))
+    return ws.value
+
+
+def kvc_evict(k_pool: torch.Tensor, v_pool: torch.Tensor, weights_out: torch.Tensor,
+              positions_out: torch.Tensor, new_lens: torch.Tensor, weights: torch.Tensor,
+              positions: torch.Tensor, block_table: torch.Tensor, context_lens: torch.Tensor,
+              max_ctx: int, budget: int, recent: int = 0,
+              workspace: Optional[torch.Tensor] = None,
+              weight_rows: Optional[torch.Tensor] = None, stream=None,
+              layout: str = "nhd") -> None:
+    """Keep min(context, budget) slots of every (sequence, kv head): the newest `recent`, then
+    those with the largest weights; kept slots move into the evicted ones below the new length
+    (new_lens [S]).  weights / positions (fp32 / int32 [rows, Hkv, stride]) are read, weights_out /
+    positions_out written; passing the same tensors does it in place."""
+    _cuda("k_pool", k_pool, torch.bfloat16)
+    _cuda("v_pool", v_pool, torch.bfloat16)
+    pool = pool_desc(k_pool, layout)
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool and v_pool differ in shape")
+    _weight_rows("weights", weights, torch.float32, pool)
+    _weight_rows("weights_out", weights_out, torch.float32, pool, weights)
+    _weight_rows("positions", positions, torch.int32, pool, weights)
+    _weight_rows("positions_out", positions_out, torch.int32, pool, weights)
+    _cuda("block_table", block_table, torch.int32)
+    _cuda("context_lens", context_lens, torch.int32)
+    _cuda("new_lens", new_lens, torch.int32)
+    S = context_lens.shape[0]
+    if new_lens.numel() != S or block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("new_lens is [num_seqs] and block_table [num_seqs, pages]")
+    ws = 0
+    if workspace is not None:
+        _cuda("workspace", workspace)
+        ws = workspace.numel() * workspace.element_size()
+    _check("kvc_evict", lib().kvc_evict(
+        _ptr(k_pool), _ptr(v_pool), pool, _ptr(block_table), block_table.shape[1],
+        _ptr(context_lens), S, int(max_ctx), _ptr(weights), _ptr(positions), _ptr(weights_out),
+        _ptr(positions_out), _sequence_rows(weight_rows, S), weights.shape[0], weights.shape[2],
+        int(budget), int(recent), _ptr(new_lens), _ptr(workspace), ws, _stream(stream)))
 
 
 def kvc_merge(out: torch.Tensor, partial_o: torch.Tensor, partial_lse: torch.Tensor,
