@@ -1142,6 +1142,13 @@ WeightsPlan make_weights_plan(int32_t num_seqs, int32_t q_heads, const kvc_pool_
     return w;
 }
 
+// Moves that one (sequence, kv head) of kvc_evict can have: no more than slots that are kept, and no
+// more than slots that are not.
+int evict_list_cap(int32_t max_ctx, int32_t budget)
+{
+    return std::max(0, std::min(budget, max_ctx - budget));
+}
+
 // The rows of accumulated weights that a call names.
 kvc_status check_weight_rows(const void *weights, const int32_t *weight_rows, int32_t num_rows,
                              int32_t weight_stride, int32_t num_seqs, int32_t max_ctx)
@@ -1258,10 +1265,10 @@ kvc_status kvc_evict_plan(int32_t num_seqs, kvc_pool_desc pool, int32_t max_ctx,
         return fail(KVC_ERR_INVALID_ARG, "negative num_seqs or max_ctx");
     if (budget < 1)
         return fail(KVC_ERR_INVALID_ARG, "budget %d (at least 1)", budget);
-    const size_t cap = static_cast<size_t>(std::max(0, std::min(budget, max_ctx - budget)));
+    const size_t cap = evict_list_cap(max_ctx, budget);
+    const size_t units = static_cast<size_t>(num_seqs) * pool.kv_heads;
     if (workspace_bytes_out)
-        *workspace_bytes_out =
-            static_cast<size_t>(num_seqs) * pool.kv_heads * 2 * cap * sizeof(int32_t);
+        *workspace_bytes_out = cap ? units * (2 * cap + 1) * sizeof(int32_t) : 0;
     return ok();
 }
 
@@ -1320,8 +1327,11 @@ kvc_status kvc_evict(void *k_pool, void *v_pool, kvc_pool_desc pool, const int32
     l.budget = budget;
     l.recent = recent;
     l.new_lens = new_lens;
-    l.lists = workspace;
-    l.list_cap = std::max(0, std::min(budget, max_ctx - budget));
+    l.list_cap = evict_list_cap(max_ctx, budget);
+    if (need > 0) {
+        l.lists = static_cast<int32_t *>(workspace);
+        l.counts = l.lists + static_cast<size_t>(num_seqs) * pool.kv_heads * 2 * l.list_cap;
+    }
     l.kv_heads = pool.kv_heads;
     l.head_dim = pool.head_dim;
     l.page_size = pool.page_size;

@@ -10,18 +10,28 @@
 // row after the first gap).  `positions` keeps each slot's original position, which is what the
 // newest are told by.
 //
-// Selection.  A weight becomes a 32-bit key of the same order (NaN as the lowest, -0 as 0, the newest
-// slots above every weight), and the n-th largest key is found digit by digit: four histograms of
-// 8 bits, then the slots equal to it are kept in slot order until n is full.  One cluster of 1 to 8
-// CTAs per (sequence, kv head): the histograms meet through distributed shared memory, one
-// cluster barrier each.  The keys stay in shared memory between the passes (beyond kMaxCached slots a
-// CTA makes them anew from weights and positions).  Every warp owns consecutive slots, so ranks in
-// slot order are ballots and one prefix over warps and CTAs; nothing depends on the order of
-// atomics (the histograms only count).
+// Selection (select_kernel).  A weight becomes a 32-bit key of the same order (NaN as the lowest, -0
+// as 0, the newest slots above every weight), and the n-th largest key is found digit by digit:
+// histograms of 11, 11 and 10 bits, then the slots equal to it are kept in slot order until n is
+// full.  (Digits of 8 bits would be four passes, and the first one, sign and seven exponent bits,
+// would put all weights into a handful of counters that queue up.)  One cluster of 1 to 8 CTAs per
+// (sequence, kv head): the histograms meet through distributed shared memory, one cluster
+// barrier each.  The keys stay in shared memory between the passes (beyond kMaxCached slots a CTA makes
+// them anew from weights and positions).  Every warp owns consecutive slots and every lane four at a
+// time, so ranks in slot order are one warp scan per 128 slots and a prefix over warps and CTAs;
+// nothing depends on the order of atomics (the histograms only count).  The kernel leaves the
+// moves as two lists and does weights and positions itself.
+//
+// Moves (move_kernel).  One launch over all lists, 256 moves a CTA: rows differ in how much they
+// move (a batch's longest several times its average), so the copies are spread over the SMs
+// apart from the selection.  A warp reads 32 moves and their pages at once and then keeps 8 rows
+// in flight.
 //
 // Bound: the moved rows (4 D bytes read and written each) by HBM when there are many, else the chain of
 // barriers; the selection reads 8 and writes 8 bytes a slot.
 #include <cooperative_groups.h>
+
+#include <algorithm>
 
 #include "kvc_device.cuh"
 #include "kvc_launch.h"
@@ -34,10 +44,16 @@ namespace cg = cooperative_groups;
 
 __device__ uint32_t g_evict_errors;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 256;
+constexpr int kBins = 2048;
+constexpr int kWarpSlots = 128;   // slots of one step of a warp, four consecutive ones a lane
+constexpr int kAhead = 4;         // steps of global loads that a thread has in flight
+constexpr int kMaxCtas = 8;       // of a cluster
 constexpr uint32_t kNewest = 0xFFFFFFFFu;
+constexpr long long kSmemPerSm = 228 * 1024;
+constexpr int kMoveThreads = 256;
+constexpr int kMovesPerCta = kMoveThreads;
 
 struct Args {
     uint4 *k_pool, *v_pool;
@@ -54,21 +70,24 @@ struct Args {
     int budget, recent;
     int32_t *new_lens;
     int32_t *lists;      // [S][Hkv][2][list_cap]: destinations, sources
+    int32_t *counts;     // [S][Hkv]: moves
     int list_cap;
     int kv_heads, log2_page, num_pages, hnd;
     int cached;          // keys that fit a CTA's shared memory
+    int vec;             // rows of weights and positions start on 16 bytes
     uint32_t *err;
 };
 
-// Sums over the CTA's warps, and the ranks before each.
 struct Shared {
     uint32_t hist[2][kBins];
+    uint32_t coarse[kThreads];   // sums of the current histogram's bins, eight each, top first
     uint32_t warp_sum[2][kWarps];
-    uint32_t total[2];        // this CTA's counts, read by the cluster
-    uint32_t digit, above;    // the digit of the threshold and the keys above it in this pass
+    uint32_t equal_here, gaps, tails;   // this CTA's, read by the cluster
+    uint32_t digit, above, equal;       // the digit found, the keys above it and those in it
 };
 
-// The order of floats as unsigned integers: NaN is taken as -infinity, -0 as 0.
+// The order of floats as unsigned integers: NaN is taken as -infinity, -0 as 0.  Never 0, which
+// stands for no slot.
 __device__ __forceinline__ uint32_t weight_key(float w)
 {
     if (w != w)
@@ -77,8 +96,18 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) evict_kernel(const Args a)
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane)
+{
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off)
+            x += v;
+    }
+    return x;
+}
+
+__global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
 {
     pdl_wait();
     pdl_trigger();
@@ -94,6 +123,8 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args a)
     const int lane = threadIdx.x & 31;
     uint32_t *err = a.err ? a.err : &g_evict_errors;
 
+    for (int i = threadIdx.x; i < 2 * kBins; i += kThreads)
+        sh.hist[0][i] = 0;
     const int raw = a.context_lens[s];
     const long long cap = min(static_cast<long long>(a.bt_stride) << a.log2_page,
                               static_cast<long long>(min(a.max_ctx, a.stride)));
@@ -106,30 +137,27 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args a)
         if (row >= a.num_rows)
             atomicOr(err, kErrSlotRange);
     }
-    if (row < 0 || row >= a.num_rows) {   // a sequence without a row keeps everything
-        if (first)
-            a.new_lens[s] = raw;
-        return;
-    }
+    const bool none = row < 0 || row >= a.num_rows;   // a sequence without a row keeps everything
     const int n = min(N, a.budget);
+    if (first)
+        a.new_lens[s] = none ? raw : n;
+    if (a.counts != nullptr && cta == 0 && threadIdx.x == 0 && (none || N <= a.budget))
+        a.counts[unit] = 0;
+    if (none)
+        return;
     const size_t base = (static_cast<size_t>(row) * a.kv_heads + kvh) * a.stride;
     const float *w_in = a.weights + base;
     const int32_t *p_in = a.positions + base;
     float *w_out = a.weights_out + base;
     int32_t *p_out = a.positions_out + base;
     const int last = N > 0 ? p_in[N - 1] : -1;   // the newest token's original position
-    if (first)
-        a.new_lens[s] = n;
 
     // this warp's slots [lo, hi); the CTA's begin at cta_lo
-    const int per_warp = static_cast<int>(
-        (static_cast<long long>(N) + 32LL * kWarps * ctas - 1) / (32LL * kWarps * ctas)) * 32;
-    const int cta_lo = static_cast<int>(
-        min(static_cast<long long>(N), static_cast<long long>(per_warp) * kWarps * cta));
-    const int lo = static_cast<int>(min(static_cast<long long>(N),
-                                        cta_lo + static_cast<long long>(per_warp) * warp));
-    const int hi = static_cast<int>(min(static_cast<long long>(N),
-                                        lo + static_cast<long long>(per_warp)));
+    const long long per_warp = (N + static_cast<long long>(kWarpSlots) * kWarps * ctas - 1) /
+                               (kWarpSlots * kWarps * ctas) * kWarpSlots;
+    const int cta_lo = static_cast<int>(min(static_cast<long long>(N), per_warp * kWarps * cta));
+    const int lo = static_cast<int>(min(static_cast<long long>(N), cta_lo + per_warp * warp));
+    const int hi = static_cast<int>(min(static_cast<long long>(N), lo + per_warp));
 
     if (N <= a.budget) {   // nothing to evict
         for (int i = lo + lane; i < hi; i += 32) {
@@ -143,219 +171,310 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args a)
     }
 
     const long long newest = static_cast<long long>(last) - a.recent;   // positions above it
-    auto make_key = [&](int i) -> uint32_t {
-        const float w = w_in[i];
-        return p_in[i] > newest ? kNewest : weight_key(w);
+    auto key_of = [&](float w, int p) { return p > newest ? kNewest : weight_key(w); };
+    // keys of slots i .. i + 3 from weights and positions; 0 from hi on
+    auto make_keys = [&](int i) -> uint4 {
+        if (a.vec && i + 3 < hi) {
+            const float4 w = *reinterpret_cast<const float4 *>(w_in + i);
+            const int4 p = *reinterpret_cast<const int4 *>(p_in + i);
+            return make_uint4(key_of(w.x, p.x), key_of(w.y, p.y), key_of(w.z, p.z),
+                              key_of(w.w, p.w));
+        }
+        uint4 k;
+        k.x = i < hi ? key_of(w_in[i], p_in[i]) : 0u;
+        k.y = i + 1 < hi ? key_of(w_in[i + 1], p_in[i + 1]) : 0u;
+        k.z = i + 2 < hi ? key_of(w_in[i + 2], p_in[i + 2]) : 0u;
+        k.w = i + 3 < hi ? key_of(w_in[i + 3], p_in[i + 3]) : 0u;
+        return k;
     };
-    auto key_at = [&](int i) -> uint32_t {
+    auto keys_at = [&](int i) -> uint4 {
         const int c = i - cta_lo;
-        return c < a.cached ? keys[c] : make_key(i);
+        return c < a.cached ? *reinterpret_cast<const uint4 *>(keys + c) : make_keys(i);
     };
-#pragma unroll 4
-    for (int i = lo + lane; i < hi; i += 32) {
-        const uint32_t k = make_key(i);
-        if (i - cta_lo < a.cached)
-            keys[i - cta_lo] = k;
-    }
 
     // ---- the n-th largest key, and how many equal to it are kept ----
-    uint32_t prefix = 0;
-    uint32_t need = n;   // keys still wanted among those that share the prefix
-#pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        uint32_t *hist = sh.hist[pass & 1];
-        if (threadIdx.x < kBins)
-            hist[threadIdx.x] = 0;
-        __syncthreads();
-        for (int i0 = lo; i0 < hi; i0 += 32) {
-            const int i = i0 + lane;
-            const uint32_t k = i < hi ? key_at(i) : 0u;
-            const bool in = i < hi && (pass == 0 || (k >> (shift + 8)) == prefix);
-            const uint32_t bin = in ? (k >> shift) & 0xFFu : kBins;
-            // slots of one value (zeros, the newest) would queue up on one counter
-            int same;
-            __match_all_sync(0xffffffffu, bin, &same);
-            if (same) {
-                if (lane == 0 && in)
-                    atomicAdd(&hist[bin], 32u);
-            } else if (in) {
-                atomicAdd(&hist[bin], 1u);
+    __syncthreads();   // the histograms are zero
+    auto tally = [&](const uint4 k, int i) {   // the whole warp
+        if (i < hi && i - cta_lo < a.cached)
+            *reinterpret_cast<uint4 *>(keys + (i - cta_lo)) = k;
+        const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
+        // zeros and the newest come in runs, and would queue up on one counter
+        int same;
+        __match_all_sync(0xffffffffu, k.x, &same);
+        if (same && __all_sync(0xffffffffu, k.x == k.y && k.x == k.z && k.x == k.w)) {
+            if (lane == 0 && k.x != 0)
+                atomicAdd(&sh.hist[0][k.x >> 21], static_cast<uint32_t>(kWarpSlots));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (ks[e] != 0)
+                    atomicAdd(&sh.hist[0][ks[e] >> 21], 1u);
+        }
+    };
+    int i0 = lo;
+    if (a.vec) {   // kAhead steps' loads in flight
+        for (; i0 + kAhead * kWarpSlots <= hi; i0 += kAhead * kWarpSlots) {
+            float4 w[kAhead];
+            int4 p[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                w[u] = *reinterpret_cast<const float4 *>(w_in + i0 + u * kWarpSlots + 4 * lane);
+                p[u] = *reinterpret_cast<const int4 *>(p_in + i0 + u * kWarpSlots + 4 * lane);
             }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                tally(make_uint4(key_of(w[u].x, p[u].x), key_of(w[u].y, p[u].y),
+                                 key_of(w[u].z, p[u].z), key_of(w[u].w, p[u].w)),
+                      i0 + u * kWarpSlots + 4 * lane);
+        }
+    }
+    for (; i0 < hi; i0 += kWarpSlots) {
+        const int i = i0 + 4 * lane;
+        tally(i < hi ? make_keys(i) : make_uint4(0u, 0u, 0u, 0u), i);
+    }
+    uint32_t prefix = 0;   // the digits found so far
+    uint32_t need = n;     // keys still wanted among those that begin with them
+    uint32_t equal = 0;    // how many these are
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        uint32_t *hist = sh.hist[pass & 1];
+        if (pass > 0) {
+            const int skip = pass == 1 ? 21 : 10;    // bits below the digits found
+            const int shift = pass == 1 ? 10 : 0;
+            const uint32_t mask = pass == 1 ? 0x7FFu : 0x3FFu;
+            for (int i = lo + 4 * lane; i < hi; i += kWarpSlots) {
+                const uint4 k = keys_at(i);
+                const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (ks[e] != 0 && (ks[e] >> skip) == prefix)
+                        atomicAdd(&hist[(ks[e] >> shift) & mask], 1u);
+            }
+        }
+        // Every CTA gives away the sums of eight bins each, top first; only the thread whose eight
+        // bins hold the wanted key reads these bins of every CTA (all bins of all CTAs would be 64 KB
+        // through distributed shared memory).
+        __syncthreads();
+        const int top_bin = kBins - 1 - 8 * static_cast<int>(threadIdx.x);
+        {
+            const uint4 *h = reinterpret_cast<const uint4 *>(&hist[top_bin - 7]);
+            const uint4 x = h[0], y = h[1];
+            sh.coarse[threadIdx.x] = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
         }
         cluster.sync();
-        if (threadIdx.x < kBins) {
-            // bin b of the whole cluster to thread 255 - b: a prefix sum counts from the top
-            const int b = kBins - 1 - threadIdx.x;
-            uint32_t count = 0;
-            for (int c = 0; c < ctas; ++c)
-                count += *cluster.map_shared_rank(&hist[b], c);
-            uint32_t incl = count;
+        uint32_t mine = 0;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off)
-                    incl += v;
-            }
-            if (lane == 31)
-                sh.warp_sum[0][warp] = incl;
-            named_barrier(1, kBins);
-            uint32_t before = incl - count;
-            for (int v = 0; v < warp; ++v)
-                before += sh.warp_sum[0][v];
-            if (before < need && need <= before + count) {
-                sh.digit = b;
-                sh.above = before;
-            }
-        }
+        for (int c = 0; c < kMaxCtas; ++c)
+            if (c < ctas)
+                mine += *cluster.map_shared_rank(&sh.coarse[threadIdx.x], c);
+        const uint32_t incl = warp_scan(mine, lane);
+        if (lane == 31)
+            sh.warp_sum[0][warp] = incl;
         __syncthreads();
-        prefix = (prefix << 8) | sh.digit;
+        uint32_t before = incl - mine;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v)
+            before += v < warp ? sh.warp_sum[0][v] : 0u;
+        if (before < need && need <= before + mine) {
+            uint32_t c8[8] = {};
+#pragma unroll
+            for (int c = 0; c < kMaxCtas; ++c)
+                if (c < ctas) {
+                    const uint4 *h = reinterpret_cast<const uint4 *>(
+                        cluster.map_shared_rank(&hist[top_bin - 7], c));
+                    const uint4 x = h[0], y = h[1];
+                    c8[0] += y.w;
+                    c8[1] += y.z;
+                    c8[2] += y.y;
+                    c8[3] += y.x;
+                    c8[4] += x.w;
+                    c8[5] += x.z;
+                    c8[6] += x.y;
+                    c8[7] += x.x;
+                }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (before < need && need <= before + c8[e]) {
+                    sh.digit = top_bin - e;
+                    sh.above = before;
+                    sh.equal = c8[e];
+                }
+                before += c8[e];
+            }
+        }
+        if (pass == 1)   // past this barrier every CTA has read the first pass's bins: free again
+            for (int i = threadIdx.x; i < kBins; i += kThreads)
+                sh.hist[0][i] = 0;
+        __syncthreads();
+        prefix = (prefix << (pass == 2 ? 10 : 11)) | sh.digit;
         need -= sh.above;
+        equal = sh.equal;
     }
-    // The last pass counted the keys equal to the threshold (its own digit's bin): those of the
-    // CTAs before this one come first.
     const uint32_t threshold = prefix;
-    uint32_t eq_before = 0;
-    for (int c = 0; c < cta; ++c)
-        eq_before += *cluster.map_shared_rank(&sh.hist[1][threshold & 0xFFu], c);
 
-    // ---- ranks in slot order: equal keys, then gaps below n and kept slots from n on ----
-    uint32_t eq = 0;
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-        const int i = i0 + lane;
-        eq += __popc(__ballot_sync(0xffffffffu, i < hi && key_at(i) == threshold));
+    // ---- which slots stay.  Where only some of the keys equal to the threshold do, these take
+    // their ranks in slot order ----
+    const bool ties = need < equal;
+    uint32_t eq_first = 0;   // equal keys before this warp's
+    if (ties) {
+        uint32_t here = 0;
+        for (int i = lo + 4 * lane; i < hi; i += kWarpSlots) {
+            const uint4 k = keys_at(i);
+            here += (k.x == threshold) + (k.y == threshold) + (k.z == threshold) +
+                    (k.w == threshold);
+        }
+        here = __reduce_add_sync(0xffffffffu, here);
+        if (lane == 0)
+            sh.warp_sum[1][warp] = here;
+        __syncthreads();
+        uint32_t all = 0;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+            eq_first += v < warp ? sh.warp_sum[1][v] : 0u;
+            all += sh.warp_sum[1][v];
+        }
+        if (threadIdx.x == 0)
+            sh.equal_here = all;
+        cluster.sync();
+        for (int c = 0; c < cta; ++c)
+            eq_first += *cluster.map_shared_rank(&sh.equal_here, c);
     }
-    if (lane == 0)
-        sh.warp_sum[1][warp] = eq;
-    __syncthreads();
-    for (int v = 0; v < warp; ++v)
-        eq_before += sh.warp_sum[1][v];
-    auto kept_lanes = [&](int i0, uint32_t &eq_rank) -> uint32_t {
-        const int i = i0 + lane;
-        const uint32_t k = i < hi ? key_at(i) : 0u;
-        const bool is_eq = i < hi && k == threshold;
-        const uint32_t eqs = __ballot_sync(0xffffffffu, is_eq);
-        const uint32_t rank = eq_rank + __popc(eqs & ((1u << lane) - 1u));
-        eq_rank += __popc(eqs);
-        return __ballot_sync(0xffffffffu,
-                             i < hi && (k > threshold || (is_eq && rank < need)));
+    // The kept ones of slots i .. i + 3 (i = i0 + 4 lane) as four bits; the warp goes together.
+    auto kept = [&](int i, uint32_t &eq_rank) -> uint32_t {
+        const uint4 k = i < hi ? keys_at(i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
+        uint32_t m = 0;
+        if (!ties) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                m |= (ks[e] >= threshold ? 1u : 0u) << e;
+            return m;
+        }
+        uint32_t eq = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            m |= (ks[e] > threshold ? 1u : 0u) << e;
+            eq |= (ks[e] == threshold ? 1u : 0u) << e;
+        }
+        const uint32_t cnt = __popc(eq);
+        const uint32_t incl = warp_scan(cnt, lane);
+        uint32_t rank = eq_rank + incl - cnt;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if ((eq >> e) & 1u) {
+                m |= (rank < need ? 1u : 0u) << e;
+                ++rank;
+            }
+        eq_rank += __shfl_sync(0xffffffffu, incl, 31);
+        return m;
     };
-    uint32_t gaps = 0, tails = 0;
+    auto below_n = [&](int i) -> uint32_t {   // the slots of i .. i + 3 below n, as four bits
+        const int b = n - i;
+        return b >= 4 ? 15u : b <= 0 ? 0u : (1u << b) - 1u;
+    };
     {
-        uint32_t rank = eq_before;
-        for (int i0 = lo; i0 < hi; i0 += 32) {
-            const uint32_t kept = kept_lanes(i0, rank);
-            const int i = i0 + lane;
-            const bool keep = (kept >> lane) & 1u;
-            gaps += __popc(__ballot_sync(0xffffffffu, i < n && !keep));
-            tails += __popc(__ballot_sync(0xffffffffu, i >= n && keep));
+        uint32_t rank = eq_first, gaps = 0, tails = 0;
+        for (int i0 = lo; i0 < hi; i0 += kWarpSlots) {
+            const int i = i0 + 4 * lane;
+            const uint32_t m = kept(i, rank), in = below_n(i);
+            gaps += __popc(in & ~m);
+            tails += __popc(m & ~in);
+        }
+        gaps = __reduce_add_sync(0xffffffffu, gaps);
+        tails = __reduce_add_sync(0xffffffffu, tails);
+        __syncthreads();   // warp_sum is read
+        if (lane == 0) {
+            sh.warp_sum[0][warp] = gaps;
+            sh.warp_sum[1][warp] = tails;
         }
     }
-    __syncthreads();   // every warp has read the counts of equal keys
-    if (lane == 0) {
-        sh.warp_sum[0][warp] = gaps;
-        sh.warp_sum[1][warp] = tails;
-    }
     __syncthreads();
-    if (threadIdx.x < 2) {
-        uint32_t t = 0;
-        for (int v = 0; v < kWarps; ++v)
-            t += sh.warp_sum[threadIdx.x][v];
-        sh.total[threadIdx.x] = t;
+    uint32_t gap_at = 0, tail_at = 0, moves = 0;
+    {
+        uint32_t gaps = 0, tails = 0;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+            gap_at += v < warp ? sh.warp_sum[0][v] : 0u;
+            tail_at += v < warp ? sh.warp_sum[1][v] : 0u;
+            gaps += sh.warp_sum[0][v];
+            tails += sh.warp_sum[1][v];
+        }
+        if (threadIdx.x == 0) {
+            sh.gaps = gaps;
+            sh.tails = tails;
+        }
     }
     cluster.sync();
-    uint32_t gap_at = 0, tail_at = 0, moves = 0;
     for (int c = 0; c < ctas; ++c) {
-        const uint32_t *t = cluster.map_shared_rank(sh.total, c);
-        if (c < cta) {
-            gap_at += t[0];
-            tail_at += t[1];
-        }
-        moves += t[0];
-    }
-    for (int v = 0; v < warp; ++v) {
-        gap_at += sh.warp_sum[0][v];
-        tail_at += sh.warp_sum[1][v];
+        const uint32_t g = *cluster.map_shared_rank(&sh.gaps, c);
+        const uint32_t t = *cluster.map_shared_rank(&sh.tails, c);
+        gap_at += c < cta ? g : 0u;
+        tail_at += c < cta ? t : 0u;
+        moves += g;
     }
     int32_t *dst_list = a.lists + static_cast<size_t>(unit) * 2 * a.list_cap;
     int32_t *src_list = dst_list + a.list_cap;
+    if (cta == 0 && threadIdx.x == 0)
+        a.counts[unit] = static_cast<int32_t>(moves);
     {
-        uint32_t rank = eq_before;
-        for (int i0 = lo; i0 < hi; i0 += 32) {
-            const uint32_t kept = kept_lanes(i0, rank);
-            const int i = i0 + lane;
-            const bool keep = (kept >> lane) & 1u;
-            const uint32_t g = __ballot_sync(0xffffffffu, i < n && !keep);
-            const uint32_t t = __ballot_sync(0xffffffffu, i >= n && keep);
-            const uint32_t below = (1u << lane) - 1u;
-            if ((g >> lane) & 1u)
-                dst_list[gap_at + __popc(g & below)] = i;
-            if ((t >> lane) & 1u)
-                src_list[tail_at + __popc(t & below)] = i;
-            if (keep && i < n) {   // stays where it is
-                w_out[i] = w_in[i];
-                p_out[i] = p_in[i];
+        uint32_t rank = eq_first;
+        for (int i0 = lo; i0 < hi; i0 += kWarpSlots) {
+            const int i = i0 + 4 * lane;
+            const uint32_t m = kept(i, rank), in = below_n(i);
+            uint32_t g = in & ~m, t = m & ~in;
+            const uint32_t both = __popc(g) | (__popc(t) << 16);
+            const uint32_t incl = warp_scan(both, lane);
+            const uint32_t at = incl - both, all = __shfl_sync(0xffffffffu, incl, 31);
+            int32_t *d = dst_list + gap_at + (at & 0xFFFFu);
+            int32_t *f = src_list + tail_at + (at >> 16);
+            for (; g; g &= g - 1)
+                *d++ = i + __ffs(g) - 1;
+            for (; t; t &= t - 1)
+                *f++ = i + __ffs(t) - 1;
+            gap_at += all & 0xFFFFu;
+            tail_at += all >> 16;
+            // what lies below n stays where it is; the gaps are written over below
+            if (in == 15u && a.vec) {
+                if (w_out != w_in)
+                    *reinterpret_cast<float4 *>(w_out + i) =
+                        *reinterpret_cast<const float4 *>(w_in + i);
+                if (p_out != p_in)
+                    *reinterpret_cast<int4 *>(p_out + i) = *reinterpret_cast<const int4 *>(p_in + i);
+            } else {
+                for (int e = 0; e < 4; ++e)
+                    if ((in >> e) & 1u) {
+                        w_out[i + e] = w_in[i + e];
+                        p_out[i + e] = p_in[i + e];
+                    }
             }
-            gap_at += __popc(g);
-            tail_at += __popc(t);
         }
     }
     __threadfence();
     cluster.sync();
-
-    // ---- the moves ----
-    constexpr int kVec = D / 8;                 // 16-byte chunks of a vector
-    constexpr int kMoveLanes = 2 * kVec;        // K and V
-    constexpr int kPerWarp = 32 / kMoveLanes;   // moves that a warp makes at a time
-    constexpr int kUnroll = 4;
-    const int sub = lane / kMoveLanes;
-    const int in_move = lane % kMoveLanes;
-    uint4 *pool = in_move < kVec ? a.k_pool : a.v_pool;
-    const int chunk = in_move % kVec;
-    const int32_t *bt = a.block_table + static_cast<size_t>(s) * a.bt_stride;
-    const int P1 = (1 << a.log2_page) - 1;
-    auto place = [&](int slot, bool &ok) -> size_t {
-        const int page = bt[slot >> a.log2_page];
-        ok = ok && page >= 0 && page < a.num_pages;
-        const size_t off = slot & P1;
-        const size_t vec =
-            a.hnd ? ((static_cast<size_t>(page) * a.kv_heads + kvh) << a.log2_page) + off
-                  : ((static_cast<size_t>(page) << a.log2_page) + off) * a.kv_heads + kvh;
-        return vec * kVec + chunk;
-    };
-    const int movers = ctas * kWarps * kPerWarp;
-    for (int j0 = (cta * kWarps + warp) * kPerWarp + sub; j0 - sub < static_cast<int>(moves);
-         j0 += movers * kUnroll) {
-        size_t to[kUnroll];
-        uint4 x[kUnroll];
-        bool go[kUnroll];
+    for (int j0 = cta * kThreads + threadIdx.x; j0 < static_cast<int>(moves);
+         j0 += ctas * kThreads * kAhead) {
+        int src[kAhead], dst[kAhead], p[kAhead];
+        float w[kAhead];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int j = j0 + u * movers;
-            const bool in = j < static_cast<int>(moves);
-            go[u] = in;
-            if (in) {
-                const int src = __ldcg(src_list + j), dst = __ldcg(dst_list + j);
-                if (in_move == 0) {
-                    w_out[dst] = w_in[src];
-                    p_out[dst] = p_in[src];
-                }
-                const size_t from = place(src, go[u]);
-                to[u] = place(dst, go[u]);
-                if (go[u])
-                    x[u] = pool[from];
-                else if (in_move == 0)
-                    atomicOr(err, kErrPageRange);
-            }
+        for (int u = 0; u < kAhead; ++u) {
+            const int j = j0 + u * ctas * kThreads;
+            src[u] = j < static_cast<int>(moves) ? __ldcg(src_list + j) : -1;
+            dst[u] = j < static_cast<int>(moves) ? __ldcg(dst_list + j) : -1;
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (go[u])
-                pool[to[u]] = x[u];
+        for (int u = 0; u < kAhead; ++u)
+            if (src[u] >= 0) {
+                w[u] = w_in[src[u]];
+                p[u] = p_in[src[u]];
+            }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (src[u] >= 0) {
+                w_out[dst[u]] = w[u];
+                p_out[dst[u]] = p[u];
+            }
     }
     cluster.sync();   // the moved slots' weights and positions are read: the tail may be written
-
-    // ---- the slots from n on are free: weight 0, and the positions that tokens to come will have ----
     for (long long i = static_cast<long long>(n) + cta * kThreads + threadIdx.x; i < a.stride;
          i += ctas * kThreads) {
         if (i < N)
@@ -364,7 +483,69 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args a)
     }
 }
 
+// Copies the listed rows: CTA = (chunk of 256 moves, unit), unit fastest.
 template <int D>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const Args a, int units)
+{
+    pdl_wait();
+    pdl_trigger();
+    constexpr int kVec = D / 8;                 // 16-byte chunks of a vector
+    constexpr int kMoveLanes = 2 * kVec;        // K and V of one move
+    constexpr int kAtOnce = 32 / kMoveLanes;    // moves that a warp copies with one load
+    constexpr int kFly = 8;                     // loads in flight
+    const int unit = blockIdx.x % units;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int j0 = (blockIdx.x / units) * kMovesPerCta + warp * 32;
+    const int n = min(32, __ldcg(a.counts + unit) - j0);
+    if (n <= 0)
+        return;
+    const int kvh = unit % a.kv_heads;
+    const int s = unit / a.kv_heads;
+    const int32_t *dst_list = a.lists + static_cast<size_t>(unit) * 2 * a.list_cap;
+    const int32_t *bt = a.block_table + static_cast<size_t>(s) * a.bt_stride;
+    long long from = -1, to = -1;   // 16-byte chunks; below 0: no copy
+    if (lane < n) {
+        const int dst = __ldcg(dst_list + j0 + lane);
+        const int src = __ldcg(dst_list + a.list_cap + j0 + lane);
+        const int dp = bt[dst >> a.log2_page], sp = bt[src >> a.log2_page];
+        if (dp >= 0 && dp < a.num_pages && sp >= 0 && sp < a.num_pages) {
+            const int mask = (1 << a.log2_page) - 1;
+            auto place = [&](int page, int off) -> long long {
+                const long long vec =
+                    a.hnd ? ((static_cast<long long>(page) * a.kv_heads + kvh) << a.log2_page) + off
+                          : ((static_cast<long long>(page) << a.log2_page) + off) * a.kv_heads + kvh;
+                return vec * kVec;
+            };
+            from = place(sp, src & mask);
+            to = place(dp, dst & mask);
+        } else {
+            atomicOr(a.err ? a.err : &g_evict_errors, kErrPageRange);
+        }
+    }
+    const int sub = lane / kMoveLanes;
+    const int in_move = lane % kMoveLanes;
+    uint4 *pool = (in_move < kVec ? a.k_pool : a.v_pool) + in_move % kVec;
+    for (int u0 = 0; u0 < n; u0 += kFly * kAtOnce) {
+        uint4 x[kFly];
+        long long dst[kFly];
+#pragma unroll
+        for (int u = 0; u < kFly; ++u) {
+            const int m = u0 + u * kAtOnce + sub;   // below 64; past n the lane's places are -1
+            const long long f = __shfl_sync(0xffffffffu, from, m & 31);
+            dst[u] = __shfl_sync(0xffffffffu, to, m & 31);
+            if (m >= n)
+                dst[u] = -1;
+            if (dst[u] >= 0)
+                x[u] = __ldcg(pool + f);
+        }
+#pragma unroll
+        for (int u = 0; u < kFly; ++u)
+            if (dst[u] >= 0)
+                pool[dst[u]] = x[u];
+    }
+}
+
 cudaError_t launch_t(const EvictLaunch &l, const Args &args, cudaStream_t stream)
 {
     Args a = args;
@@ -372,20 +553,27 @@ cudaError_t launch_t(const EvictLaunch &l, const Args &args, cudaStream_t stream
     // Clusters only where (sequence, kv head) units alone leave SMs idle and rows are long
     // enough to share: a cluster barrier costs more than a CTA's.
     int ctas = 1;
-    while (ctas < 8 && units * ctas * 2 <= 4LL * current_sm_count() &&
+    while (ctas < kMaxCtas && units * ctas * 2 <= 4LL * current_sm_count() &&
            l.max_ctx / (ctas * 2) >= 1024)
         ctas *= 2;
-    const long long per_cta =
-        (static_cast<long long>(l.max_ctx) + 32LL * kWarps * ctas - 1) / (32LL * kWarps * ctas) *
-        32 * kWarps;
-    a.cached = static_cast<int>(per_cta < kMaxCached ? per_cta : kMaxCached);
+    const long long step = static_cast<long long>(kWarpSlots) * kWarps;
+    const long long per_cta = (l.max_ctx + step * ctas - 1) / (step * ctas) * step;
+    // As many keys in shared memory as leave every CTA of the launch room beside the others (the
+    // SM's threads and registers hold 4): on 64 rows of up to 131,072 slots all keys in shared
+    // memory mean two waves of clusters.
+    const int sms = current_sm_count();
+    const long long per_sm = std::min<long long>(4, (units * ctas + sms - 1) / sms);
+    const long long room = (kSmemPerSm / per_sm - 1024 - static_cast<long long>(sizeof(Shared))) /
+                           4 / kWarpSlots * kWarpSlots;
+    a.cached = static_cast<int>(std::min(per_cta, std::min<long long>(room, kMaxCached)));
     const size_t smem = static_cast<size_t>(a.cached) * 4 + sizeof(Shared);
-    auto kernel = evict_kernel<D>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           kMaxCached * 4 + static_cast<int>(sizeof(Shared)));
+    cudaError_t err =
+        cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxCached * 4 + static_cast<int>(sizeof(Shared)));
     if (err != cudaSuccess)
         return err;
-    if (units * ctas > 0x7FFFFFFFLL)
+    const long long chunks = (l.list_cap + kMovesPerCta - 1) / kMovesPerCta;
+    if (units * ctas > 0x7FFFFFFFLL || units * chunks > 0x7FFFFFFFLL)
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(units * ctas));
@@ -401,7 +589,12 @@ cudaError_t launch_t(const EvictLaunch &l, const Args &args, cudaStream_t stream
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    err = cudaLaunchKernelEx(&cfg, select_kernel, a);
+    if (err != cudaSuccess || l.list_cap == 0)
+        return err;
+    auto move = l.head_dim == 128 ? move_kernel<128> : move_kernel<64>;
+    return launch_pdl(move, dim3(static_cast<unsigned>(units * chunks)), dim3(kMoveThreads), 0,
+                      stream, a, static_cast<int>(units));
 }
 
 }  // namespace
@@ -428,14 +621,20 @@ cudaError_t launch_evict(const EvictLaunch &l, cudaStream_t stream)
     a.budget = l.budget;
     a.recent = l.recent;
     a.new_lens = l.new_lens;
-    a.lists = static_cast<int32_t *>(l.lists);
+    a.lists = l.lists;
+    a.counts = l.counts;
     a.list_cap = l.list_cap;
     a.kv_heads = l.kv_heads;
     a.log2_page = l.page_size == 16 ? 4 : l.page_size == 32 ? 5 : 6;
     a.num_pages = l.num_pages;
     a.hnd = l.hnd ? 1 : 0;
+    const uintptr_t rows = reinterpret_cast<uintptr_t>(l.weights) |
+                           reinterpret_cast<uintptr_t>(l.positions) |
+                           reinterpret_cast<uintptr_t>(l.weights_out) |
+                           reinterpret_cast<uintptr_t>(l.positions_out);
+    a.vec = (rows & 15) == 0 && l.stride % 4 == 0;
     a.err = current_error_word();
-    return l.head_dim == 128 ? launch_t<128>(l, a, stream) : launch_t<64>(l, a, stream);
+    return launch_t(l, a, stream);
 }
 
 cudaError_t read_and_clear_evict_errors(uint32_t *flags)

@@ -142,7 +142,7 @@ cudaError_t launch_decode_weights(const DecodeLaunch &l, const WeightsLaunch &w,
                                   cudaStream_t stream);
 cudaError_t read_and_clear_weights_errors(uint32_t *flags);
 
-// kvc_evict: lists int32 [S][Hkv][2][list_cap] (the moves of each (sequence, kv head)).
+// kvc_evict: the moves of each (sequence, kv head), lists [S][Hkv][2][list_cap] and counts [S][Hkv].
 constexpr int kMaxCached = 48 * 1024;   // keys that a CTA keeps in shared memory
 struct EvictLaunch {
     void *k_pool, *v_pool;
@@ -158,8 +158,8 @@ struct EvictLaunch {
     int num_rows, stride;
     int budget, recent;
     int32_t *new_lens;
-    void *lists;
-    int list_cap;
+    int32_t *lists = nullptr, *counts = nullptr;   // null without a possible move (list_cap 0)
+    int list_cap = 0;
     int kv_heads, head_dim, page_size, num_pages;
     bool hnd;
 };
