@@ -1268,7 +1268,7 @@ kvc_status kvc_evict_plan(int32_t num_seqs, kvc_pool_desc pool, int32_t max_ctx,
     const size_t cap = evict_list_cap(max_ctx, budget);
     const size_t units = static_cast<size_t>(num_seqs) * pool.kv_heads;
     if (workspace_bytes_out)
-        *workspace_bytes_out = cap ? units * (2 * cap + 1) * sizeof(int32_t) : 0;
+        *workspace_bytes_out = cap ? units * (2 * cap + 2) * sizeof(int32_t) : 0;
     return ok();
 }
 

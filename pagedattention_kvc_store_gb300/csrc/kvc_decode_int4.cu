@@ -9,9 +9,10 @@
 // Codes as operands.  A word's eight nibbles become four fp16 pairs with one AND each (and one
 // shift): the bits of a nibble alone are the fp16 subnormal u 2^-24 (u 2^-20 for the high nibble
 // of a byte), which the tensor cores take exactly; no bias has to be added or taken out.  For
-// K the two weights are evened out in the query (the dims in low nibbles carry 16 q), for V they
-// stay on the output rows until the end, where a multiplication takes both out.  Putting the
-// nibble under an exponent and subtracting the bias would double the conversion.  Query rows
+// K the two weights are evened out in the query (the dims in low nibbles carry 16 q); V's rows
+// accumulate whole bytes (low + 16 high, also an exact subnormal) and high nibbles, and the low
+// ones are their difference at the end.  Putting the nibble under an exponent and subtracting
+// the bias would double the conversion.  Query rows
 // enter as fp16 scaled by a power of two of their own (largest |q| in [2^9, 2^10), so bf16's
 // eight bits are exact wherever they matter); probabilities times value scales as fp16 scaled by a
 // power of two that follows the largest value scale seen (vnorm), because a scale may have any
@@ -189,11 +190,22 @@ struct __align__(16) Meta {
 // Where a warp fetches next in its kv head's block order.
 struct Cursor {
     int s, blk, nb, ctx;
-    long long left;        // blocks of the run not yet fetched
+    int left;              // blocks of the run not yet fetched
     int pbase;             // first page (index in the sequence) of the window below
     int page, page_next;   // this lane's page ids of the window and of the one after it
     bool fresh;            // the next block starts a piece
     bool from_start;       // the piece began at the sequence's first block
+};
+
+// What a lane's copies have in common, block after block.
+struct LaneCopies {
+    const uint8_t *k_row;      // K codes of its first row in page 0 (V: v_delta bytes on)
+    long long v_delta;
+    uint32_t row_bytes, page_bytes;   // from a position to the next, from a page to the next
+    const uint8_t *par;        // its parameters in page 0 (K for low lanes, V for high ones)
+    uint32_t par_page_bytes;
+    uint32_t dst0, dst1, dst_par;     // places in a stage (dst1: the row after, D = 128)
+    int row, par_half, par_pos;       // its first row and its parameters' half and first position
 };
 
 // Loads sequence c.s (passing by empty ones) and the page ids from block c.blk on; false when no
@@ -219,80 +231,63 @@ __device__ __forceinline__ bool open_sequence(Cursor &c, const Args &a, int lane
     return true;
 }
 
-// Fetches the cursor's block into a stage and moves the cursor on.
+// Fetches the cursor's block into a stage and moves the cursor on.  Rows past the context become
+// zeros (read from no memory); a page id outside the pool is flagged and reads as zeros.
 template <int D>
-__device__ __forceinline__ void fetch_block(Cursor &c, const Args &a, uint32_t stage, Meta *meta,
-                                            int kvh, int lane)
+__device__ __forceinline__ void fetch_block(Cursor &c, const Args &a, const LaneCopies &l,
+                                            uint32_t stage, Meta *meta, int lane)
 {
     using Geom = I4Geom<D>;
-    constexpr int kRow = Geom::kRow, kChunks = Geom::kChunks, kGroups = Geom::kGroups;
-    const int P = 1 << a.log2_page;
     const int pos = c.blk * kBlock;
     const int n_valid = min(kBlock, c.ctx - pos);
     int pi = pos >> a.log2_page;
     if (pi >= c.pbase + 32) {   // 32 pages hold whole blocks: a block's pages share a window
         c.pbase += 32;
         c.page = c.page_next;
-        const int pages = (c.ctx + P - 1) >> a.log2_page;
+        const int pages = (c.ctx + (1 << a.log2_page) - 1) >> a.log2_page;
         const int32_t *row = a.block_table + static_cast<size_t>(c.s) * a.bt_stride;
         c.page_next = c.pbase + 32 + lane < pages ? row[c.pbase + 32 + lane] : 0;
     }
     pi -= c.pbase;
-    const size_t row_bytes = a.hnd ? kRow : static_cast<size_t>(a.kv_heads) * kRow;
-    int pages2[2];
-    pages2[0] = __shfl_sync(0xffffffffu, c.page, pi);
-    pages2[1] = __shfl_sync(0xffffffffu, c.page, (pi + (16 >> a.log2_page)) & 31);
-    int off2[2] = {pos & (P - 1), (pos + 16) & (P - 1)};
-    int live2[2];   // valid positions of each half; none where the page id is outside the pool
+    uint32_t page[2], off[2];
+    page[0] = __shfl_sync(0xffffffffu, c.page, pi);
+    page[1] = __shfl_sync(0xffffffffu, c.page, (pi + (16 >> a.log2_page)) & 31);
+    off[0] = pos & ((1 << a.log2_page) - 1);
+    off[1] = (pos + 16) & ((1 << a.log2_page) - 1);
+    int live[2] = {n_valid, n_valid - 16};   // valid rows of each half
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        live2[h] = min(16, n_valid - 16 * h);
-        if (live2[h] > 0 && static_cast<unsigned>(pages2[h]) >= static_cast<unsigned>(a.num_pages)) {
-            if (lane == 0)
+    for (int h = 0; h < 2; ++h)
+        if (page[h] >= static_cast<uint32_t>(a.num_pages)) {
+            if (lane == 0 && live[h] > 0)
                 atomicOr(err_word(a), kErrPageRange);
-            live2[h] = 0;
+            page[h] = 0;
+            live[h] = 0;
         }
-        if (live2[h] <= 0) {
-            pages2[h] = 0;
-            off2[h] = 0;
-        }
-    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const size_t vec = a.hnd ? ((static_cast<size_t>(pages2[h]) * a.kv_heads + kvh) << a.log2_page)
-                                 : (static_cast<size_t>(pages2[h]) << a.log2_page) * a.kv_heads + kvh;
-        const size_t base = vec * kRow + static_cast<size_t>(off2[h]) * row_bytes;
-        // D = 128: four lanes a row, even rows then odd ones; D = 64: two lanes a row
-        constexpr int kSteps = kChunks == 4 ? 2 : 1;
-#pragma unroll
-        for (int e = 0; e < kSteps; ++e) {
-            const int slot = kChunks == 4 ? (lane >> 2) + 8 * e : lane >> 1;
-            const int chunk = lane & (kChunks - 1);
-            const int row = 2 * (slot & 7) + (slot >> 3);
-            const size_t src = base + static_cast<size_t>(row) * row_bytes + chunk * 16;
-            const uint32_t dst = stage + h * Geom::kHalfCodes + half_offset<D>(row, chunk);
-            const int bytes = row < live2[h] ? 16 : 0;
-            copy_async16(dst, a.k_codes + (bytes ? src : 0), bytes);
-            copy_async16(dst + Geom::kOffV, a.v_codes + (bytes ? src : 0), bytes);
+        const uint8_t *k = l.k_row + static_cast<unsigned long long>(page[h]) * l.page_bytes +
+                           off[h] * l.row_bytes;
+        const int b0 = l.row < live[h] ? 16 : 0;
+        const uint32_t d0 = stage + l.dst0 + h * Geom::kHalfCodes;
+        copy_async16(d0, k, b0);
+        copy_async16(d0 + Geom::kOffV, k + l.v_delta, b0);
+        if (D == 128) {   // four lanes a row: the next row too
+            const int b1 = l.row + 1 < live[h] ? 16 : 0;
+            const uint32_t d1 = stage + l.dst1 + h * Geom::kHalfCodes;
+            k += l.row_bytes;
+            copy_async16(d1, k, b1);
+            copy_async16(d1 + Geom::kOffV, k + l.v_delta, b1);
         }
     }
-    // parameters: 16 kGroups * 4 bytes a half, one 16-byte copy a lane (K: low lanes, V: high)
-    constexpr int kParLanes = 4 * kGroups;   // lanes of one half of one tensor
-    if (lane < 4 * kParLanes) {
-        const int h = (lane / kParLanes) & 1;
-        const int c16 = lane % kParLanes;
-        constexpr int kPer = 4 / kGroups;   // positions in 16 bytes
-        const int page = h ? pages2[1] : pages2[0];
-        const int off = h ? off2[1] : off2[0];
-        const int live = h ? live2[1] : live2[0];
-        const int bytes = max(0, min(16, (live - c16 * kPer) * 4 * kGroups));
-        const size_t src =
-            ((((static_cast<size_t>(page) * a.kv_heads + kvh) << a.log2_page) + off) * kGroups * 4 +
-             c16 * 16);
-        const bool is_v = lane >= 2 * kParLanes;
-        const uint32_t dst = stage + (is_v ? Geom::kOffVp : Geom::kOffKp) +
-                             (h * kParLanes + c16) * 16;
-        copy_async16(dst, (is_v ? a.v_params : a.k_params) + (bytes ? src : 0), bytes);
+    // parameters: 16 bytes a lane
+    if (D == 128 || lane < 16) {
+        const uint32_t pg = l.par_half ? page[1] : page[0], of = l.par_half ? off[1] : off[0];
+        const int lv = l.par_half ? live[1] : live[0];
+        constexpr int kPer = 4 * Geom::kGroups;   // bytes of a position
+        const int bytes = max(0, min(16, (lv - l.par_pos) * kPer));
+        copy_async16(stage + l.dst_par,
+                     l.par + static_cast<unsigned long long>(pg) * l.par_page_bytes + of * kPer,
+                     bytes);
     }
     ++c.blk;
     --c.left;
@@ -335,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
     const int kvh = gw % Hkv;
     const int run = gw / Hkv;
     Cursor c;
-    long long run_len = 0;
+    int run_len = 0;   // (a run's blocks: far below 2^31 for tables that fit the memory)
     const long long *bound_end = nullptr;   // the index of the first block past the run
     if (a.per_unit) {
         if (run >= a.num_seqs)
@@ -427,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
         }
         __syncthreads();
         const int i = run - run_lo;
-        run_len = bound_g[i + 1] - bound_g[i];
+        run_len = static_cast<int>(bound_g[i + 1] - bound_g[i]);
         if (run >= n_runs || run_len <= 0)
             return;
         c.s = static_cast<int>(bound_s[i]);
@@ -438,6 +433,29 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
     if (!open_sequence(c, a, lane))
         return;
 
+    LaneCopies l;
+    {
+        constexpr int kRow = Geom::kRow;
+        const int P = 1 << a.log2_page;
+        const int chunk = lane & (NC - 1);
+        l.row = NC == 4 ? 2 * (lane >> 2) : 2 * ((lane >> 1) & 7) + (lane >> 4);
+        l.row_bytes = a.hnd ? kRow : Hkv * kRow;
+        l.page_bytes = static_cast<uint32_t>(P) * Hkv * kRow;
+        l.k_row = a.k_codes + static_cast<size_t>(kvh) * (a.hnd ? P * kRow : kRow) +
+                  static_cast<size_t>(l.row) * l.row_bytes + chunk * 16;
+        l.v_delta = a.v_codes - a.k_codes;
+        l.dst0 = half_offset<D>(l.row, chunk);
+        l.dst1 = half_offset<D>(l.row + 1, chunk);
+        // 4 NG lanes hold the 16 positions of one half of one tensor, 4 / NG positions each
+        const bool is_v = lane >= 8 * NG;
+        l.par_half = (lane / (4 * NG)) & 1;
+        const int c16 = lane % (4 * NG);
+        l.par_pos = c16 * (4 / NG);
+        l.par_page_bytes = static_cast<uint32_t>(Hkv) * P * NG * 4;
+        l.par = (is_v ? a.v_params : a.k_params) + static_cast<size_t>(kvh) * P * NG * 4 + c16 * 16;
+        l.dst_par = (is_v ? Geom::kOffVp : Geom::kOffKp) + (l.par_half * 4 * NG + c16) * 16;
+    }
+
     // ---- the first blocks on their way ----
     const uint32_t ring32 = smem_addr(ring);
     int fetched = 0;   // stage of the next fetch
@@ -445,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
 #pragma unroll
     for (int i = 0; i < NS - 1; ++i) {
         if (c.left > 0) {
-            fetch_block<D>(c, a, ring32 + fetched * Geom::kStageBytes, &metas[fetched], kvh, lane);
+            fetch_block<D>(c, a, l, ring32 + fetched * Geom::kStageBytes, &metas[fetched], lane);
             ++pending;
         }
         copy_commit();
@@ -462,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
     const int v_off = half_offset<D>(lane & 15, lane >> 4);
 
     uint32_t qb[NG][2][2][2];   // B fragments: [group][word][nibble][register]
-    float o[NC][2][4];          // O^T: [32 dims][nibble][fragment]
+    float o[NC][2][4];          // O^T: [32 dims][whole byte, high half][fragment]
     float zacc[NG][2];          // sum of p lo, heads 2 t and 2 t + 1
     float m_run[2], l_run[2], m_thr[2], mf[2], f[2], hq[NG][2];
     float vnorm = 1.0f, v_thr = 0.0f;
@@ -485,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
         copy_wait<NS - 2>();
         __syncwarp();
         if (c.left > 0) {
-            fetch_block<D>(c, a, ring32 + fetched * Geom::kStageBytes, &metas[fetched], kvh, lane);
+            fetch_block<D>(c, a, l, ring32 + fetched * Geom::kStageBytes, &metas[fetched], lane);
             ++pending;
         }
         copy_commit();
@@ -715,10 +733,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
                 ldsm_x2_trans_b8(vb + (v_off ^ (32 * g)), e[0], e[1], e[2], e[3]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
+                    // whole bytes (low + 16 high) and their high halves: one operation a pair
+                    // each, where the low halves would also need the shift
                     const uint32_t x0 = e[2 * k], x1 = e[2 * k + 1];
-                    const uint32_t z0 = x0 >> 8, z1 = x1 >> 8;
-                    mma_f16_16816(o[2 * g + k][0], x0 & 0x000F000Fu, x1 & 0x000F000Fu,
-                                  z0 & 0x000F000Fu, z1 & 0x000F000Fu, pb[g][0], pb[g][1]);
+                    const uint32_t z0 = __byte_perm(x0, 0u, 0x4341u);   // bytes 1 and 3
+                    const uint32_t z1 = __byte_perm(x1, 0u, 0x4341u);
+                    mma_f16_16816(o[2 * g + k][0], x0 & 0x00FF00FFu, x1 & 0x00FF00FFu, z0, z1,
+                                  pb[g][0], pb[g][1]);
                     mma_f16_16816(o[2 * g + k][1], x0 & 0x00F000F0u, x1 & 0x00F000F0u,
                                   z0 & 0x00F000F0u, z1 & 0x00F000F0u, pb[g][0], pb[g][1]);
                 }
@@ -756,8 +777,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
                         for (int i = 0; i < 2; ++i) {   // dims 32 n + 16 i + 2 r, + 1
                             const float z = zacc[n / 2][j];
                             float2 v;
-                            v.x = fmaf(o[n][0][2 * i + j] * 16777216.0f, v_inv, z) * inv[j];
-                            v.y = fmaf(o[n][1][2 * i + j] * 1048576.0f, v_inv, z) * inv[j];
+                            const float whole_byte = o[n][0][2 * i + j], high = o[n][1][2 * i + j];
+                            v.x = fmaf((whole_byte - high) * 16777216.0f, v_inv, z) * inv[j];
+                            v.y = fmaf(high * 1048576.0f, v_inv, z) * inv[j];
                             const int dim = 32 * n + 16 * i + 2 * r;
                             if (whole)
                                 store_out2(a.out, a.out_f32, (row0 + head) * D + dim, v);

@@ -20,9 +20,9 @@
 // them anew from weights and positions).  Every warp owns consecutive slots and every lane four at a
 // time, so ranks in slot order are one warp scan per 128 slots and a prefix over warps and CTAs;
 // nothing depends on the order of atomics (the histograms only count).  The kernel leaves the
-// moves as two lists and does weights and positions itself.
+// moves as two lists.
 //
-// Moves (move_kernel).  One launch over all lists, 256 moves a CTA: rows differ in how much they
+// Moves (move_kernel).  One launch over all lists, 128 moves a CTA: rows differ in how much they
 // move (a batch's longest several times its average), so the copies are spread over the SMs
 // apart from the selection.  A warp reads 32 moves and their pages at once and then keeps 8 rows
 // in flight.
@@ -52,7 +52,7 @@ constexpr int kAhead = 4;         // steps of global loads that a thread has in 
 constexpr int kMaxCtas = 8;       // of a cluster
 constexpr uint32_t kNewest = 0xFFFFFFFFu;
 constexpr long long kSmemPerSm = 228 * 1024;
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128;
 constexpr int kMovesPerCta = kMoveThreads;
 
 struct Args {
@@ -70,7 +70,7 @@ struct Args {
     int budget, recent;
     int32_t *new_lens;
     int32_t *lists;      // [S][Hkv][2][list_cap]: destinations, sources
-    int32_t *counts;     // [S][Hkv]: moves
+    int2 *counts;        // [S][Hkv]: moves, and the position of a free slot i less i
     int list_cap;
     int kv_heads, log2_page, num_pages, hnd;
     int cached;          // keys that fit a CTA's shared memory
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     if (first)
         a.new_lens[s] = none ? raw : n;
     if (a.counts != nullptr && cta == 0 && threadIdx.x == 0 && (none || N <= a.budget))
-        a.counts[unit] = 0;
+        a.counts[unit] = make_int2(0, 0);
     if (none)
         return;
     const size_t base = (static_cast<size_t>(row) * a.kv_heads + kvh) * a.stride;
@@ -414,8 +414,11 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     }
     int32_t *dst_list = a.lists + static_cast<size_t>(unit) * 2 * a.list_cap;
     int32_t *src_list = dst_list + a.list_cap;
+    // A free slot gets weight 0 and the position that a token to come will have there.  The slots that
+    // rows move out of become free with the move.
+    const int32_t free_pos = static_cast<int32_t>(static_cast<long long>(last) + 1 - n);
     if (cta == 0 && threadIdx.x == 0)
-        a.counts[unit] = static_cast<int32_t>(moves);
+        a.counts[unit] = make_int2(static_cast<int>(moves), free_pos);
     {
         uint32_t rank = eq_first;
         for (int i0 = lo; i0 < hi; i0 += kWarpSlots) {
@@ -433,7 +436,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
                 *f++ = i + __ffs(t) - 1;
             gap_at += all & 0xFFFFu;
             tail_at += all >> 16;
-            // what lies below n stays where it is; the gaps are written over below
+            // What lies below n stays where it is (the moves write over the gaps), and what lies behind
+            // and is not kept is free.
             if (in == 15u && a.vec) {
                 if (w_out != w_in)
                     *reinterpret_cast<float4 *>(w_out + i) =
@@ -441,49 +445,26 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
                 if (p_out != p_in)
                     *reinterpret_cast<int4 *>(p_out + i) = *reinterpret_cast<const int4 *>(p_in + i);
             } else {
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 4; ++e) {
                     if ((in >> e) & 1u) {
                         w_out[i + e] = w_in[i + e];
                         p_out[i + e] = p_in[i + e];
+                    } else if (i + e < hi && !((m >> e) & 1u)) {
+                        w_out[i + e] = 0.0f;
+                        p_out[i + e] = free_pos + i + e;
                     }
+                }
             }
         }
     }
-    __threadfence();
-    cluster.sync();
-    for (int j0 = cta * kThreads + threadIdx.x; j0 < static_cast<int>(moves);
-         j0 += ctas * kThreads * kAhead) {
-        int src[kAhead], dst[kAhead], p[kAhead];
-        float w[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int j = j0 + u * ctas * kThreads;
-            src[u] = j < static_cast<int>(moves) ? __ldcg(src_list + j) : -1;
-            dst[u] = j < static_cast<int>(moves) ? __ldcg(dst_list + j) : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (src[u] >= 0) {
-                w[u] = w_in[src[u]];
-                p[u] = p_in[src[u]];
-            }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (src[u] >= 0) {
-                w_out[dst[u]] = w[u];
-                p_out[dst[u]] = p[u];
-            }
-    }
-    cluster.sync();   // the moved slots' weights and positions are read: the tail may be written
-    for (long long i = static_cast<long long>(n) + cta * kThreads + threadIdx.x; i < a.stride;
-         i += ctas * kThreads) {
-        if (i < N)
-            w_out[i] = 0.0f;
-        p_out[i] = static_cast<int32_t>(last + 1 + (i - n));
-    }
+    for (long long i = static_cast<long long>(N) + cta * kThreads + threadIdx.x; i < a.stride;
+         i += ctas * kThreads)
+        p_out[i] = free_pos + static_cast<int32_t>(i);
+    cluster.sync();   // the others' counts are read: shared memory may go
 }
 
-// Copies the listed rows: CTA = (chunk of 256 moves, unit), unit fastest.
+// Carries out the listed moves, K and V, weight and position: CTA = (chunk of kMovesPerCta moves, unit),
+// unit fastest.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Args a, int units)
 {
@@ -497,7 +478,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Args a, int un
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int j0 = (blockIdx.x / units) * kMovesPerCta + warp * 32;
-    const int n = min(32, __ldcg(a.counts + unit) - j0);
+    const int2 count = __ldcg(a.counts + unit);
+    const int n = min(32, count.x - j0);
     if (n <= 0)
         return;
     const int kvh = unit % a.kv_heads;
@@ -522,6 +504,14 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Args a, int un
         } else {
             atomicOr(a.err ? a.err : &g_evict_errors, kErrPageRange);
         }
+        const int row = a.rows ? a.rows[s] : s;
+        const size_t base = (static_cast<size_t>(row) * a.kv_heads + kvh) * a.stride;
+        const float w = a.weights[base + src];
+        const int32_t p = a.positions[base + src];
+        a.weights_out[base + dst] = w;
+        a.positions_out[base + dst] = p;
+        a.weights_out[base + src] = 0.0f;
+        a.positions_out[base + src] = count.y + src;
     }
     const int sub = lane / kMoveLanes;
     const int in_move = lane % kMoveLanes;
@@ -622,7 +612,7 @@ cudaError_t launch_evict(const EvictLaunch &l, cudaStream_t stream)
     a.recent = l.recent;
     a.new_lens = l.new_lens;
     a.lists = l.lists;
-    a.counts = l.counts;
+    a.counts = reinterpret_cast<int2 *>(l.counts);
     a.list_cap = l.list_cap;
     a.kv_heads = l.kv_heads;
     a.log2_page = l.page_size == 16 ? 4 : l.page_size == 32 ? 5 : 6;

@@ -142,7 +142,8 @@ cudaError_t launch_decode_weights(const DecodeLaunch &l, const WeightsLaunch &w,
                                   cudaStream_t stream);
 cudaError_t read_and_clear_weights_errors(uint32_t *flags);
 
-// kvc_evict: the moves of each (sequence, kv head), lists [S][Hkv][2][list_cap] and counts [S][Hkv].
+// kvc_evict: the moves of each (sequence, kv head), lists [S][Hkv][2][list_cap] and counts
+// [S][Hkv][2].
 constexpr int kMaxCached = 48 * 1024;   // keys that a CTA keeps in shared memory
 struct EvictLaunch {
     void *k_pool, *v_pool;

@@ -15,12 +15,16 @@
 // as in a bf16 pool ([slot][kv head], or [page][kv head][offset] for HND).  Parameters: bf16
 // (scale, lo) at [page][kv head][offset][group], so the page's run for one kv head is contiguous.
 //
-// Both kernels are bound by HBM (328 bytes a vector at D = 128).  Eight lanes take a group, one
-// 16-byte load of 8 values each; the K and V vectors of one (token, kv head) go to neighbouring
-// lanes.  The codes need a correctly rounded quotient, but a division per value would make the
-// store bound by instructions (about 12 a value): the product with the approximate reciprocal
-// is off by less than 1e-5 of a step, so only quotients that close to a tie take the division.
+// Both kernels are bound by HBM (328 bytes a vector at D = 128), but only if they spend few instructions:
+// a lane takes 16 values of K and the same of V at a time (four lanes a group), minima and maxima
+// go two to a word, the arithmetic two to an instruction (f32x2), and token and head come from a
+// multiplication by a reciprocal that the host makes.  The codes need a correctly rounded quotient.
+// A division per value would be about 12 instructions; the product with the approximate
+// reciprocal is off by less than 1e-5 of a step, so only a lane that holds a quotient within 1e-4
+// of a tie (or a scale too small for the reciprocal) takes the divisions.
 #include <math.h>
+
+#include <algorithm>
 
 #include "kvc_device.cuh"
 #include "kvc_launch.h"
@@ -33,162 +37,213 @@ __device__ uint32_t g_store_int4_errors;
 
 constexpr int kThreads = 256;
 
-// The vector (K or V of one token and kv head) that a lane works on, and its place in the pools.
-struct Place {
-    bool live;        // the token has a slot inside the pool
-    size_t code_row;  // vector index in the code pool
-    size_t par_row;   // vector index in the parameter pool
+// Work item = vector (token, kv head), K and V together.
+struct Shape {
+    int kv_heads, log2_page, num_slots, hnd;
+    unsigned long long recip;   // ceil(2^64 / kv_heads), 0 for one head
 };
 
-__device__ __forceinline__ Place place_of(int slot, int g, int kv_heads, int log2_page,
-                                          int num_slots, bool hnd, uint32_t *err, bool report)
+// Token and head of a vector, and its places in the pools.
+struct Place {
+    bool live;        // the token has a slot inside the pool
+    size_t code_row;  // vector index in the code pools
+    size_t par_row;   // vector index in the parameter pools
+};
+
+__device__ __forceinline__ Place place_of(const Shape &s, const int32_t *slots, uint32_t vec,
+                                          bool report, uint32_t *err)
 {
+    const uint32_t t = s.recip ? static_cast<uint32_t>(__umul64hi(s.recip, vec)) : vec;
+    const uint32_t g = vec - t * s.kv_heads;
+    const int slot = __ldcg(slots + t);
     Place p;
-    p.live = slot >= 0 && slot < num_slots;
-    if (slot >= num_slots && report)
+    p.live = slot >= 0 && slot < s.num_slots;
+    if (slot >= s.num_slots && report && g == 0)
         atomicOr(err, kErrSlotRange);
-    const int page = slot >> log2_page;
-    const int off = slot & ((1 << log2_page) - 1);
-    p.par_row = ((static_cast<size_t>(page) * kv_heads + g) << log2_page) + off;
-    p.code_row = hnd ? p.par_row : static_cast<size_t>(slot) * kv_heads + g;
+    const int page = slot >> s.log2_page;
+    const int off = slot & ((1 << s.log2_page) - 1);
+    p.par_row = ((static_cast<size_t>(page) * s.kv_heads + g) << s.log2_page) + off;
+    p.code_row = s.hnd ? p.par_row : static_cast<size_t>(slot) * s.kv_heads + g;
     return p;
 }
 
-// L lanes per vector (D = 8 L).  Work item w = (token, kv head, K or V), V fastest: 2 L lanes read
-// the K and V vectors of one (token, kv head).
+// The smaller of two bf16 pairs, element by element; a NaN on either side wins.
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ float approx_rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Codes (16 values: 8 bytes) and parameter of a quarter of a group; four neighbouring lanes hold one.
+__device__ __forceinline__ uint2 quantise16(const uint32_t (&x)[8], uint32_t &param)
+{
+    // lo and -hi of the lane's values, two to a word; then of the group
+    uint32_t lo2 = x[0], nhi2 = x[0] ^ 0x80008000u;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        lo2 = min2_nan(lo2, x[i]);
+        nhi2 = min2_nan(nhi2, x[i] ^ 0x80008000u);
+    }
+    uint32_t m = min2_nan(__byte_perm(lo2, nhi2, 0x5410), __byte_perm(lo2, nhi2, 0x7632));
+    m = min2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = min2_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const float lo_half = __uint_as_float(m << 16) * 0.5f;
+    const float hi_half = -__uint_as_float(m & 0xFFFF0000u) * 0.5f;
+    const __nv_bfloat16 scale16 = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi_half, lo_half), 7.5f));
+    const float scale_half = __bfloat162float(scale16) * 0.5f;
+    // NaN anywhere, or an infinite end: the exponent bits of either end are all ones
+    if (((m & 0x7F80u) == 0x7F80u) || ((m & 0x7F800000u) == 0x7F800000u)) {
+        param = 0x7FC07FC0u;
+        return make_uint2(0u, 0u);
+    }
+    param = static_cast<uint32_t>(__bfloat16_as_ushort(scale16)) | (m << 16);
+    if (!(scale_half > 0.0f))
+        return make_uint2(0u, 0u);
+    // a = x / 2 - lo / 2 (one rounding), q = a / (scale / 2), r the nearest integer: 1.5 2^23 added
+    // and taken away leaves it, ties to even.  scale is at most 2^-8 of itself off, so q is below
+    // 15.06 and r needs no clamp here.
+    const uint64_t half2 = f2_pack(0.5f, 0.5f), nlo2 = f2_pack(-lo_half, -lo_half);
+    const float inv = approx_rcp(scale_half);
+    const uint64_t inv2 = f2_pack(inv, inv), magic2 = f2_pack(12582912.0f, 12582912.0f);
+    uint64_t r2[8];
+    float off = scale_half >= 1e-30f ? 0.0f : 1.0f;   // a tiny scale: always divide
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint64_t v = f2_pack(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
+        const uint64_t q = f2_mul(f2_fma(v, half2, nlo2), inv2);
+        r2[i] = f2_sub(f2_add(q, magic2), magic2);
+        float d0, d1;
+        f2_unpack(f2_sub(q, r2[i]), d0, d1);
+        off = fmax3(off, fabsf(d0), fabsf(d1));
+    }
+    if (!(off < 0.4999f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a0 = fmaf(__uint_as_float(x[i] << 16), 0.5f, -lo_half);
+            const float a1 = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), 0.5f, -lo_half);
+            r2[i] = f2_pack(fminf(rintf(__fdiv_rn(a0, scale_half)), 15.0f),
+                            fminf(rintf(__fdiv_rn(a1, scale_half)), 15.0f));
+        }
+    }
+    // value pairs (even, odd) of four words make 8 codes: even ones weigh 1, 256, 65536, 2^24, odd
+    // ones 16 times that; sums of four stay below 2^24 in each half
+    const uint64_t w256 = f2_pack(256.0f, 256.0f);
+    uint32_t code[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float e0, o0, e1, o1;
+        f2_unpack(f2_fma(r2[4 * h + 1], w256, r2[4 * h]), e0, o0);
+        f2_unpack(f2_fma(r2[4 * h + 3], w256, r2[4 * h + 2]), e1, o1);
+        const uint32_t lo16 = __float_as_uint(fmaf(o0, 16.0f, e0) + 8388608.0f);
+        const uint32_t hi16 = __float_as_uint(fmaf(o1, 16.0f, e1) + 8388608.0f);
+        code[h] = __byte_perm(lo16, hi16, 0x5410);
+    }
+    return make_uint2(code[0], code[1]);
+}
+
+// L lanes per vector, 16 values each (D = 16 L).
 template <int L>
 __global__ void __launch_bounds__(kThreads)
-    store_int4_kernel(uint32_t *__restrict__ k_codes, uint32_t *__restrict__ v_codes,
+    store_int4_kernel(uint2 *__restrict__ k_codes, uint2 *__restrict__ v_codes,
                       uint32_t *__restrict__ k_params, uint32_t *__restrict__ v_params,
                       const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
-                      const int32_t *__restrict__ slots, int num_tokens, int kv_heads,
-                      int log2_page, int num_slots, bool hnd, uint32_t *word)
+                      const int32_t *__restrict__ slots, uint32_t vectors, const Shape shape,
+                      uint32_t *word)
 {
     pdl_wait();
     pdl_trigger();
     uint32_t *err = word ? word : &g_store_int4_errors;
-    const long long items = static_cast<long long>(num_tokens) * kv_heads * 2;
-    const long long step = static_cast<long long>(gridDim.x) * (kThreads / L);
-    const int c = threadIdx.x % L;   // 16-byte chunk of the vector
-    // every lane of a warp goes round together (the shuffles below), so the bound is the warp's
-    const long long w_first = static_cast<long long>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-    const long long warp_first = w_first - (threadIdx.x & 31) / L;
-    for (long long w0 = warp_first; w0 < items; w0 += step) {
-        const long long w = w0 + (threadIdx.x & 31) / L;
-        const bool in = w < items;
-        const bool is_v = w & 1;
-        const long long vec = in ? w >> 1 : 0;
-        const int t = static_cast<int>(vec / kv_heads);
-        const int g = static_cast<int>(vec - static_cast<long long>(t) * kv_heads);
-        const int slot = in ? __ldcg(slots + t) : -1;
-        const Place p = place_of(slot, g, kv_heads, log2_page, num_slots, hnd, err,
-                                 c == 0 && g == 0);
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (p.live)
-            x = load_streaming((is_v ? v_new : k_new) + vec * L + c);
-        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(xw[i] << 16);
-            f[2 * i + 1] = __uint_as_float(xw[i] & 0xFFFF0000u);
-        }
-        // smallest and largest value, and whether all are finite (|x| of the bits below the
-        // exponent of infinity)
-        float lo = f[0], hi = f[0];
-        bool finite = true;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo = fminf(lo, f[i]);
-            hi = fmaxf(hi, f[i]);
-            finite = finite && (__float_as_uint(f[i]) & 0x7F800000u) != 0x7F800000u;
-        }
-#pragma unroll
-        for (int off = 4; off > 0; off >>= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-        }
-        const uint32_t bad = __ballot_sync(0xffffffffu, !finite);
-        const bool group_ok = ((bad >> (threadIdx.x & 24)) & 0xFFu) == 0;
-        if (!p.live)
-            continue;
-        const float lo_half = lo * 0.5f;
-        const __nv_bfloat16 scale16 =
-            __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi * 0.5f, lo_half), 7.5f));
-        const float scale_half = __bfloat162float(scale16) * 0.5f;
-        uint32_t packed = 0;
-        uint32_t param = 0x7FC07FC0u;   // NaN, NaN
-        if (group_ok) {
-            param = static_cast<uint32_t>(__bfloat16_as_ushort(scale16)) |
-                    (__float_as_uint(lo) & 0xFFFF0000u);
-            if (scale_half > 0.0f) {
-                const float inv = __frcp_rn(scale_half);   // infinite for the smallest scales:
-                                                           // the quotient is then divided out
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float a = __fsub_rn(f[i] * 0.5f, lo_half);
-                    float q = a * inv;
-                    float r = rintf(q);
-                    if (!(fabsf(q - r) < 0.4999f))
-                        r = rintf(__fdiv_rn(a, scale_half));
-                    packed |= static_cast<uint32_t>(fminf(r, 15.0f)) << (4 * i);
-                }
+    const int c = threadIdx.x % L;
+    const uint32_t step = gridDim.x * (kThreads / L);
+    // a warp's lanes go round together (the group's shuffles)
+    const uint32_t in_warp = (threadIdx.x & 31) / L;
+    for (uint32_t w0 = (blockIdx.x * kThreads + (threadIdx.x & ~31u)) / L; w0 < vectors; w0 += step) {
+        const uint32_t vec = min(w0 + in_warp, vectors - 1);   // the last one again: stored alike
+        // padding tokens' values are read too: one round trip to memory instead of two
+        const size_t at = (static_cast<size_t>(vec) * L + c) * 2;
+        const uint4 k0 = __ldcs(k_new + at), k1 = __ldcs(k_new + at + 1);
+        const uint4 v0 = __ldcs(v_new + at), v1 = __ldcs(v_new + at + 1);
+        const Place p = place_of(shape, slots, vec, c == 0, err);
+        const uint32_t xk[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+        const uint32_t xv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        uint32_t kp, vp;
+        const uint2 kc = quantise16(xk, kp), vc = quantise16(xv, vp);
+        if (p.live) {
+            k_codes[p.code_row * L + c] = kc;
+            v_codes[p.code_row * L + c] = vc;
+            if ((c & 3) == 0) {
+                k_params[p.par_row * (L / 4) + c / 4] = kp;
+                v_params[p.par_row * (L / 4) + c / 4] = vp;
             }
         }
-        (is_v ? v_codes : k_codes)[p.code_row * L + c] = packed;
-        if ((c & 7) == 0)
-            (is_v ? v_params : k_params)[p.par_row * (L / 8) + c / 8] = param;
     }
 }
 
 // The values that 4-bit pages hold at the given slots, as bf16 (rounded to nearest even) or fp32:
-// scale * code is exact in fp32 (4 by 8 bits) and the sum with lo rounds once.
-template <int L, bool F32>
+// scale * code is exact in fp32 (4 by 8 bits) and the sum with lo rounds once.  A lane takes the
+// 8 values of chunk c and, at D = 128, of chunk c + 8, of K and V, so that stores are whole
+// 16-byte chunks side by side.  A nibble under the exponent of 2^23 is 2^23 + code.
+template <int D, bool F32>
 __global__ void __launch_bounds__(kThreads)
     load_int4_kernel(uint4 *__restrict__ k_out, uint4 *__restrict__ v_out,
                      const uint32_t *__restrict__ k_codes, const uint32_t *__restrict__ v_codes,
                      const uint32_t *__restrict__ k_params, const uint32_t *__restrict__ v_params,
-                     const int32_t *__restrict__ slots, int num_tokens, int kv_heads,
-                     int log2_page, int num_slots, bool hnd, uint32_t *word)
+                     const int32_t *__restrict__ slots, uint32_t vectors, const Shape shape,
+                     uint32_t *word)
 {
     pdl_wait();
     pdl_trigger();
     uint32_t *err = word ? word : &g_store_int4_errors;
-    const long long items = static_cast<long long>(num_tokens) * kv_heads * 2;
-    const long long step = static_cast<long long>(gridDim.x) * (kThreads / L);
+    constexpr int L = 8;            // lanes of a vector
+    constexpr int NG = D / 64;
     const int c = threadIdx.x % L;
-    for (long long w = static_cast<long long>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-         w < items; w += step) {
-        const bool is_v = w & 1;
-        const long long vec = w >> 1;
-        const int t = static_cast<int>(vec / kv_heads);
-        const int g = static_cast<int>(vec - static_cast<long long>(t) * kv_heads);
-        const Place p = place_of(__ldcg(slots + t), g, kv_heads, log2_page, num_slots, hnd, err,
-                                 c == 0 && g == 0);
-        float v[8];
+    const uint32_t step = gridDim.x * (kThreads / L);
+    for (uint32_t vec = blockIdx.x * (kThreads / L) + threadIdx.x / L; vec < vectors; vec += step) {
+        const Place p = place_of(shape, slots, vec, c == 0, err);
+        uint32_t codes[2][NG] = {}, par[2][NG] = {};
         if (p.live) {
-            const uint32_t codes = __ldcg((is_v ? v_codes : k_codes) + p.code_row * L + c);
-            const uint32_t par = __ldcg((is_v ? v_params : k_params) + p.par_row * (L / 8) + c / 8);
-            const float scale = __uint_as_float(par << 16);
-            const float lo = __uint_as_float(par & 0xFFFF0000u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = fmaf(scale, static_cast<float>((codes >> (4 * i)) & 15u), lo);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = 0.0f;
+            for (int g = 0; g < NG; ++g) {
+                codes[0][g] = __ldcg(k_codes + p.code_row * (NG * L) + g * L + c);
+                codes[1][g] = __ldcg(v_codes + p.code_row * (NG * L) + g * L + c);
+                par[0][g] = __ldcg(k_params + p.par_row * NG + g);
+                par[1][g] = __ldcg(v_params + p.par_row * NG + g);
+            }
         }
-        uint4 *out = is_v ? v_out : k_out;
-        if (F32) {
-            out += (vec * L + c) * 2;
-            out[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
-                                __float_as_uint(v[2]), __float_as_uint(v[3]));
-            out[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
-                                __float_as_uint(v[6]), __float_as_uint(v[7]));
-        } else {
-            out[vec * L + c] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float scale = __uint_as_float(par[which][g] << 16);
+                const float lo = __uint_as_float(par[which][g] & 0xFFFF0000u);
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t u = (codes[which][g] >> (4 * i)) & 15u;
+                    v[i] = fmaf(scale, __uint_as_float(0x4B000000u | u) - 8388608.0f, lo);
+                }
+                const size_t at = static_cast<size_t>(vec) * (NG * L) + g * L + c;
+                uint4 *out = which ? v_out : k_out;
+                if (F32) {
+                    __stcs(out + 2 * at, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                    __float_as_uint(v[2]), __float_as_uint(v[3])));
+                    __stcs(out + 2 * at + 1,
+                           make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
+                                      __float_as_uint(v[6]), __float_as_uint(v[7])));
+                } else {
+                    __stcs(out + at,
+                           make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+                }
+            }
         }
     }
 }
@@ -201,12 +256,29 @@ int log2_of(int x)
     return n;
 }
 
-// Blocks of kThreads for `items` work items of L lanes, at most 8 blocks per SM.
-int blocks_for(long long items, int lanes)
+// Blocks of kThreads for `vectors` work items of L lanes, at most 8 per SM.
+int blocks_for(long long vectors, int lanes)
 {
-    const long long wanted = (items * lanes + kThreads - 1) / kThreads;
+    const long long wanted = (vectors * lanes + kThreads - 1) / kThreads;
     const long long cap = static_cast<long long>(current_sm_count()) * 8;
     return static_cast<int>(wanted < cap ? wanted : cap);
+}
+
+Shape shape_of(const Int4Pools &p)
+{
+    Shape s;
+    s.kv_heads = p.kv_heads;
+    s.log2_page = log2_of(p.page_size);
+    s.num_slots = p.num_pages * p.page_size;
+    s.hnd = p.hnd;
+    s.recip = p.kv_heads == 1 ? 0 : ~0ull / p.kv_heads + 1;
+    return s;
+}
+
+// Tokens of one launch: vector indices stay below 2^31.
+long long tokens_per_launch(const Int4Pools &p)
+{
+    return std::max(1LL, (1LL << 30) / p.kv_heads);
 }
 
 }  // namespace
@@ -214,36 +286,44 @@ int blocks_for(long long items, int lanes)
 cudaError_t launch_store_int4(const Int4Pools &p, const void *k_new, const void *v_new,
                               const int32_t *slots, int num_tokens, cudaStream_t stream)
 {
-    if (num_tokens == 0)
-        return cudaSuccess;
-    const int lanes = p.head_dim / 8;
-    const int blocks = blocks_for(2LL * num_tokens * p.kv_heads, lanes);
-    auto kernel = lanes == 16 ? store_int4_kernel<16> : store_int4_kernel<8>;
-    return launch_pdl(kernel, dim3(blocks), dim3(kThreads), 0, stream,
-                      static_cast<uint32_t *>(p.k_codes), static_cast<uint32_t *>(p.v_codes),
-                      static_cast<uint32_t *>(p.k_params), static_cast<uint32_t *>(p.v_params),
-                      static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new), slots,
-                      num_tokens, p.kv_heads, log2_of(p.page_size), p.num_pages * p.page_size,
-                      p.hnd, current_error_word());
+    const int lanes = p.head_dim / 16;
+    auto kernel = lanes == 8 ? store_int4_kernel<8> : store_int4_kernel<4>;
+    const long long most = tokens_per_launch(p);
+    for (long long t = 0; t < num_tokens; t += most) {
+        const long long vectors = std::min(most, num_tokens - t) * p.kv_heads;
+        const size_t at = static_cast<size_t>(t) * p.kv_heads * lanes * 2;
+        const cudaError_t err = launch_pdl(
+            kernel, dim3(blocks_for(vectors, lanes)), dim3(kThreads), 0, stream,
+            static_cast<uint2 *>(p.k_codes), static_cast<uint2 *>(p.v_codes),
+            static_cast<uint32_t *>(p.k_params), static_cast<uint32_t *>(p.v_params),
+            static_cast<const uint4 *>(k_new) + at, static_cast<const uint4 *>(v_new) + at,
+            slots + t, static_cast<uint32_t>(vectors), shape_of(p), current_error_word());
+        if (err != cudaSuccess)
+            return err;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_load_int4(const Int4Pools &p, void *k_out, void *v_out, bool out_f32,
                              const int32_t *slots, int num_tokens, cudaStream_t stream)
 {
-    if (num_tokens == 0)
-        return cudaSuccess;
-    const int lanes = p.head_dim / 8;
-    const int blocks = blocks_for(2LL * num_tokens * p.kv_heads, lanes);
-    auto kernel = lanes == 16 ? (out_f32 ? load_int4_kernel<16, true> : load_int4_kernel<16, false>)
-                              : (out_f32 ? load_int4_kernel<8, true> : load_int4_kernel<8, false>);
-    return launch_pdl(kernel, dim3(blocks), dim3(kThreads), 0, stream,
-                      static_cast<uint4 *>(k_out), static_cast<uint4 *>(v_out),
-                      static_cast<const uint32_t *>(p.k_codes),
-                      static_cast<const uint32_t *>(p.v_codes),
-                      static_cast<const uint32_t *>(p.k_params),
-                      static_cast<const uint32_t *>(p.v_params), slots, num_tokens, p.kv_heads,
-                      log2_of(p.page_size), p.num_pages * p.page_size, p.hnd,
-                      current_error_word());
+    auto kernel = p.head_dim == 128
+                      ? (out_f32 ? load_int4_kernel<128, true> : load_int4_kernel<128, false>)
+                      : (out_f32 ? load_int4_kernel<64, true> : load_int4_kernel<64, false>);
+    const long long most = tokens_per_launch(p);
+    for (long long t = 0; t < num_tokens; t += most) {
+        const long long vectors = std::min(most, num_tokens - t) * p.kv_heads;
+        const size_t at = static_cast<size_t>(t) * p.kv_heads * (p.head_dim / 8) * (out_f32 ? 2 : 1);
+        const cudaError_t err = launch_pdl(
+            kernel, dim3(blocks_for(vectors, 8)), dim3(kThreads), 0, stream,
+            static_cast<uint4 *>(k_out) + at, static_cast<uint4 *>(v_out) + at,
+            static_cast<const uint32_t *>(p.k_codes), static_cast<const uint32_t *>(p.v_codes),
+            static_cast<const uint32_t *>(p.k_params), static_cast<const uint32_t *>(p.v_params),
+            slots + t, static_cast<uint32_t>(vectors), shape_of(p), current_error_word());
+        if (err != cudaSuccess)
+            return err;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t read_and_clear_store_int4_errors(uint32_t *flags)

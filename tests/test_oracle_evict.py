@@ -103,8 +103,8 @@ def test_evict_refusals(kw, code):
 
 def test_plans():
     pool = PoolDesc(2000, 16, 8, 128)
-    assert kvc.kvc_evict_plan(64, pool, 4096, 2048) == 64 * 8 * (2 * 2048 + 1) * 4
-    assert kvc.kvc_evict_plan(64, pool, 4096, 4000) == 64 * 8 * (2 * 96 + 1) * 4
+    assert kvc.kvc_evict_plan(64, pool, 4096, 2048) == 64 * 8 * (2 * 2048 + 2) * 4
+    assert kvc.kvc_evict_plan(64, pool, 4096, 4000) == 64 * 8 * (2 * 96 + 2) * 4
     assert kvc.kvc_evict_plan(64, pool, 4096, 5000) == 0
     s, c, ws = kvc.kvc_decode_weights_plan(64, 32, pool, 4096)
     assert (s, c) == kvc.kvc_decode_plan(64, 32, pool, 4096)[:2]
