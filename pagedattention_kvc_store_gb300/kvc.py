@@ -68,6 +68,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load libkvc.so (building it first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()
@@ -162,7 +164,7 @@ def lib() -> ctypes.CDLL:
             L.kvc_validate.restype = ctypes.c_int
             L.kvc_validate.argtypes = [PoolDesc, p, i32, p, i32, p, i32, p, sz,
                                        ctypes.POINTER(ctypes.c_int64), p]
-            _lib = L
+            _lib = L   # last: a thread that sees it needs no lock
     return _lib
 
 
@@ -173,7 +175,8 @@ def _check(call: str, status: int) -> None:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    """Address for a c_void_p argument (the declared argument types convert it)."""
+    return None if t is None else t.data_ptr()
 
 
 def _cuda(name: str, t: torch.Tensor, dtype=None, contiguous=True) -> torch.Tensor:
@@ -207,9 +210,11 @@ def _decode_out(t: torch.Tensor) -> torch.Tensor:
     return _reachable("out", t)
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream) -> int:
+    """Handle of the stream, or of the current device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _out_dtype(out: torch.Tensor) -> int:
