@@ -176,9 +176,8 @@ Int8Plan make_int8_plan(int32_t num_seqs, int32_t q_heads, const kvc_pool_desc &
     return p;
 }
 
-// 4-bit decode plan, as the INT8 one, with 32-position blocks and one warp per run: by default the
-// warps that one wave of the kernel's CTAs holds (2 CTAs of 8 warps per SM).
-constexpr int kInt4ResidentWarps = 16;
+// 4-bit decode plan, as the INT8 one, with 64-position blocks and one warp per run and kv head: by
+// default as many runs as one wave of the kernel's CTAs (one per SM) holds.
 
 struct Int4Plan {
     int runs;            // per kv head
@@ -200,8 +199,9 @@ kvc_status make_int4_plan(int32_t num_seqs, int32_t q_heads, const kvc_pool_desc
         return KVC_OK;
     }
     const int64_t blocks = seqs * ceil_div(max_ctx > 0 ? max_ctx : 1, kvc::kInt4Block);
-    int64_t runs = requested <= 0 ? static_cast<int64_t>(kInt4ResidentWarps) * device_sm_count() /
-                                        pool.kv_heads
+    const int heads = kvc::int4_group_heads(pool.kv_heads);
+    int64_t runs = requested <= 0 ? static_cast<int64_t>(kvc::kInt4Warps / heads) *
+                                        device_sm_count() / (pool.kv_heads / heads)
                                   : static_cast<int64_t>(requested) * seqs;
     runs = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(runs, blocks),
                                                   (int64_t(1) << 29) / pool.kv_heads));
@@ -243,14 +243,14 @@ struct MapKey {
     int device;
     int rank;
     bool int8 = false;   // uint8 elements (INT8 pages) instead of bf16
-    bool swizzle64 = false;   // 64-byte swizzle (rows of 64 bytes) instead of 128-byte
+    int swizzle = 128;   // bytes of a swizzled row: 128, 64 or 32 (0: none)
     cuuint64_t dims[4];
     cuuint64_t strides[3];
     cuuint32_t box[4];
     bool operator==(const MapKey &o) const
     {
         if (ptr != o.ptr || device != o.device || rank != o.rank || int8 != o.int8 ||
-            swizzle64 != o.swizzle64)
+            swizzle != o.swizzle)
             return false;
         for (int i = 0; i < rank; ++i)
             if (dims[i] != o.dims[i] || box[i] != o.box[i] ||
@@ -291,7 +291,10 @@ kvc_status tensor_map(MapKey key, CUtensorMap *out)
                     static_cast<cuuint32_t>(key.rank),
                     const_cast<void *>(key.ptr), key.dims, key.strides, key.box, elem_strides,
                     CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    key.swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    key.swizzle == 0    ? CU_TENSOR_MAP_SWIZZLE_NONE
+                    : key.swizzle == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                    : key.swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                        : CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)",
@@ -366,7 +369,7 @@ kvc_status pool_tensor_map_int8(const void *base, const kvc_pool_desc &pool, CUt
     k.ptr = base;
     k.rank = 3;
     k.int8 = true;
-    k.swizzle64 = pool.head_dim == 64;   // 64-byte code rows: the 64-byte swizzle
+    k.swizzle = pool.head_dim == 64 ? 64 : 128;   // the swizzle of the code rows' size
     if (pool.layout == KVC_HND) {
         k.dims[0] = static_cast<cuuint64_t>(pool.head_dim);
         k.dims[1] = static_cast<cuuint64_t>(pool.page_size);
@@ -386,6 +389,56 @@ kvc_status pool_tensor_map_int8(const void *base, const kvc_pool_desc &pool, CUt
     k.box[0] = static_cast<cuuint32_t>(pool.head_dim);
     k.box[1] = 1;
     k.box[2] = static_cast<cuuint32_t>(pool.page_size);
+    return tensor_map(k, out);
+}
+
+// 4-bit codes, rows of head_dim / 2 bytes, viewed as {bytes, slot, kv head} (NHD) or {bytes, offset,
+// page * kv_heads + kv head} (HND): a box is up to kInt4Block positions of a page for all kv heads
+// of a group of the decode's warps, [head][position][bytes] in shared memory from either layout.
+kvc_status pool_tensor_map_int4(const void *base, const kvc_pool_desc &pool, CUtensorMap *out)
+{
+    const cuuint64_t row = static_cast<cuuint64_t>(pool.head_dim) / 2;
+    const cuuint64_t heads = static_cast<cuuint64_t>(pool.kv_heads);
+    MapKey k{};
+    k.ptr = base;
+    k.rank = 3;
+    k.int8 = true;
+    k.swizzle = static_cast<int>(row);
+    k.dims[0] = row;
+    if (pool.layout == KVC_HND) {
+        k.dims[1] = static_cast<cuuint64_t>(pool.page_size);
+        k.dims[2] = static_cast<cuuint64_t>(pool.num_pages) * heads;
+        k.strides[0] = row;
+        k.strides[1] = static_cast<cuuint64_t>(pool.page_size) * row;
+    } else {
+        k.dims[1] = static_cast<cuuint64_t>(pool.num_pages) * pool.page_size;
+        k.dims[2] = heads;
+        k.strides[0] = heads * row;
+        k.strides[1] = row;
+    }
+    k.box[0] = static_cast<cuuint32_t>(row);
+    k.box[1] = static_cast<cuuint32_t>(std::min(pool.page_size, kvc::kInt4Block));
+    k.box[2] = static_cast<cuuint32_t>(kvc::int4_group_heads(pool.kv_heads));
+    return tensor_map(k, out);
+}
+
+// Their parameters, bf16 [page][kv head][position][group][2], viewed as {values, kv head, page}: a box
+// is the run of up to kInt4Block positions for all kv heads of a group.
+kvc_status params_tensor_map_int4(const void *base, const kvc_pool_desc &pool, CUtensorMap *out)
+{
+    const cuuint64_t per_position = static_cast<cuuint64_t>(pool.head_dim) / 64 * 2;
+    MapKey k{};
+    k.ptr = base;
+    k.rank = 3;
+    k.swizzle = 0;
+    k.dims[0] = static_cast<cuuint64_t>(pool.page_size) * per_position;
+    k.dims[1] = static_cast<cuuint64_t>(pool.kv_heads);
+    k.dims[2] = static_cast<cuuint64_t>(pool.num_pages);
+    k.strides[0] = k.dims[0] * 2;
+    k.strides[1] = k.dims[0] * k.dims[1] * 2;
+    k.box[0] = static_cast<cuuint32_t>(std::min(pool.page_size, kvc::kInt4Block) * per_position);
+    k.box[1] = static_cast<cuuint32_t>(kvc::int4_group_heads(pool.kv_heads));
+    k.box[2] = 1;
     return tensor_map(k, out);
 }
 
@@ -948,7 +1001,13 @@ kvc_status kvc_decode_int4(void *out, int32_t out_dtype, const void *q, const vo
     l.runs = p.runs;
     l.per_unit = p.per_unit;
     l.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(pool.head_dim));
-    const cudaError_t err = kvc::launch_decode_int4(l, static_cast<cudaStream_t>(stream));
+    CUtensorMap maps[4];
+    if ((st = pool_tensor_map_int4(k_codes, pool, &maps[0])) != KVC_OK ||
+        (st = pool_tensor_map_int4(v_codes, pool, &maps[1])) != KVC_OK ||
+        (st = params_tensor_map_int4(k_params, pool, &maps[2])) != KVC_OK ||
+        (st = params_tensor_map_int4(v_params, pool, &maps[3])) != KVC_OK)
+        return st;
+    const cudaError_t err = kvc::launch_decode_int4(l, maps, static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? ok() : cuda_fail(err, "decode_int4 launch");
 }
 

@@ -19,15 +19,20 @@
 // exponent of bf16: rounding errors stay at 2^-11 of each product.  Sums, maxima, the minimum's
 // part of both products and the accumulators are fp32.
 //
-// Work.  Every warp works alone: for each kv head the positions of all sequences, in 32-position
-// blocks (sequence-major), are cut into runs of equal cost, one per warp (kv head fastest, so the
-// warps of a CTA read the kv heads of the same positions, whose rows are neighbours in NHD pages).
-// A warp streams its run through a ring of its own in shared memory, filled with 16-byte cp.async
-// two blocks ahead, across the ends of sequences; there is no barrier wider than a warp after
-// the set-up.  TMA boxes were not taken: with rows of 64 bytes a box moves half of what it
-// moves with 128 and the per-page boxes (1 KB) would be its limit.  A piece (the blocks of one
-// sequence in a run) that is all of its sequence writes the output rows, the others a partial,
-// merged by a second launch.
+// Work.  For each kv head the positions of all sequences, in 64-position blocks (sequence-major), are
+// cut into runs of equal cost.  A group of warps, one per kv head (up to 8 heads, else the largest
+// divisor of their number up to 8), works through a run in step: a block of all its heads is one
+// stage of the group's ring in shared memory, and as many groups as fit 8 warps make a CTA (one per
+// SM).  One producer warp fills the rings: four lanes keep a group's cursor, each issues the TMA
+// boxes of one page (its codes and parameters for all heads of the group); page ids, and the next
+// sequence's length and first ids, are requested blocks ahead.  A TMA operation costs the SM about 85 cycles
+// whatever its size (1 and 2 KB boxes, one warp's heads apiece, took 84 us on the batched decode,
+// and 16-byte cp.async by every warp 56: their addresses were a quarter of its instructions).
+// Eight warps with 168 registers each, not 16 with 104: the products' operands and sums spill below
+// about 120, and a warp has 64 positions' independent products to overlap (XXXX).
+// Consumer warps never wait for one another except through a stage's release.  A piece (the blocks
+// of one sequence in a run) that is all of its sequence writes the output rows, the others a
+// partial, merged by a second launch.
 //
 // Products.  S^T = K Q^T and O^T += V^T P'^T on mma.sync m16n8k16 (16 positions, or dims, by the
 // query heads of the group padded to 8: too thin for tcgen05's 128-row tiles).  The contraction
@@ -46,9 +51,10 @@ namespace {
 
 __device__ uint32_t g_decode_int4_errors;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = kInt4Warps;   // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;   // and the producer
 constexpr int kBlock = kInt4Block;   // positions of one ring stage
+constexpr int kTiles = kBlock / 16;  // of 16 positions, the rows of a product
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 // The running maximum may lag the true one by this much (log2): probabilities reach 2^4, and
@@ -60,33 +66,45 @@ constexpr float kMaxScaled = 2048.0f;   // largest value scale times vnorm: 2^4 
 constexpr long long kBlockCost = 16;
 constexpr long long kPieceCost = 16;
 
-// Scratch of the cut (64-bit words): the warps' block sums, four arrays of up to kWarps + 1 bounds,
-// and the total cost and run count.
-constexpr int kScratchCost = kWarps + 4 * (kWarps + 1);
-constexpr int kScratchWords = kScratchCost + 2 + (kScratchCost & 1);
+// Scratch of the cut (64-bit words): the warps' block sums, four arrays of up to kWarps + 1 bounds.
+constexpr int kBlockWarps = kThreads / 32;
+constexpr int kScratchWords = kBlockWarps + 4 * (kWarps + 1);
 
 template <int D>
 struct I4Geom {
     static constexpr int kRow = D / 2;            // code bytes of a vector
     static constexpr int kChunks = kRow / 16;     // 16-byte chunks of a row
     static constexpr int kGroups = D / 64;
-    static constexpr int kStages = D == 128 ? 3 : 4;
-    static constexpr int kHalfCodes = 16 * kRow;  // codes of 16 positions
-    static constexpr int kOffV = 2 * kHalfCodes;
-    static constexpr int kOffKp = 2 * kOffV;      // parameters: 4 bytes a position and group
-    static constexpr int kParBytes = kBlock * kGroups * 4;
+    static constexpr int kStages = D == 128 ? 3 : 5;
+    static constexpr int kTileCodes = 16 * kRow;  // codes of 16 positions
+    static constexpr int kTilePar = 16 * kGroups * 4;
+    static constexpr int kOffV = kTiles * kTileCodes;
+    static constexpr int kOffKp = 2 * kOffV;      // parameters
+    // per head and tensor, 4 bytes a position and group; up to twice that is used at D = 64, where
+    // an odd number of heads' 64 bytes is padded to the 128 that a TMA destination is aligned to
+    static constexpr int kParBytes = 512;
     static constexpr int kOffVp = kOffKp + kParBytes;
-    static constexpr int kStageBytes = kOffVp + kParBytes;
-    static constexpr int kWarpBytes = kStages * kStageBytes;
-    static constexpr int kMetaBytes = kWarps * kStages * 16;
-    static constexpr int kScratchBytes = kScratchWords * 8;
-    static constexpr size_t kSmemBytes = kWarps * kWarpBytes + kMetaBytes + kScratchBytes;
-    static_assert(kStageBytes % 128 == 0, "stages keep the bank phase of their rows");
+    static constexpr int kStageBytes = kOffVp + kParBytes;   // of one head; a group's stage holds
+                                                             // K codes of all heads, V codes, ...
+    static constexpr int kOffMeta = kWarps * kStages * kStageBytes;
+    static constexpr int kOffBar = kOffMeta + kWarps * kStages * 16;   // full, empty
+    static constexpr int kOffScratch = kOffBar + 2 * kWarps * kStages * 8;
+    static constexpr size_t kSmemBytes = 1024 + kOffScratch + kScratchWords * 8;
+    static_assert(kStageBytes % (8 * kRow) == 0, "stages keep the phase of the swizzle");
+    // bytes from one page's parameters of `heads` heads to the next one's, `box` positions a page
+    static __host__ __device__ constexpr int page_par(int heads, int box)
+    {
+        return (heads * box * kGroups * 4 + 127) & ~127;
+    }
+    static_assert(4 * page_par(1, 16) <= kParBytes && 4 * page_par(3, 16) <= 3 * kParBytes &&
+                      4 * page_par(5, 16) <= 5 * kParBytes && 4 * page_par(7, 16) <= 7 * kParBytes &&
+                      4 * page_par(8, 16) <= 8 * kParBytes,
+                  "four pages' parameters");
+    static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
 struct Args {
     const __nv_bfloat16 *q;
-    const uint8_t *k_codes, *v_codes, *k_params, *v_params;
     void *out;
     int out_f32;
     float *part_o;      // [slots][G][D], rows normalised by their own sum
@@ -97,6 +115,8 @@ struct Args {
     int bt_stride;
     const int32_t *context_lens;
     int num_seqs, q_heads, kv_heads, group, log2_page, num_pages;
+    int heads;          // kv heads (warps) of a group of warps
+    int groups;         // groups of a CTA
     int per_unit;       // 1: run = sequence, no partials
     int hnd;
     float scale_log2;
@@ -151,163 +171,71 @@ __device__ __forceinline__ long long run_of(long long x, long long cost, long lo
     return mul_div(x + 1, n, -1, cost);
 }
 
-// Where 16-byte chunk c of a 16-position half's row (position) `row` lies: even positions in slots
-// 0 .. 7, odd ones in 8 .. 15, chunks turned so that both the K reads (8 bytes of rows 2 r for
-// eight consecutive r) and ldmatrix (one chunk of 8 consecutive rows) touch every bank once.
+// Where 16-byte chunk c of stage row `row` lies: rows of 64 bytes under the TMA's 64-byte swizzle
+// (chunk c of row r at c ^ (r / 2) % 4), or of 32 bytes under the 32-byte one (c ^ (r / 4) % 2).
+// The transposing loads touch every bank once; the K reads (8 bytes of rows 2 r) take two turns.
 template <int D>
-__device__ __forceinline__ int half_offset(int row, int c)
+__device__ __forceinline__ int code_offset(int row, int c)
 {
-    const int slot = (row >> 1) + ((row & 1) << 3);
-    if (D == 128) {
-        const int line = slot >> 1;
-        return slot * 64 + ((c ^ (((line & 1) << 1) | (line >> 2))) << 4);
-    }
-    return slot * 32 + ((c ^ (slot >> 3)) << 4);
+    return D == 128 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4)
+                    : row * 32 + ((c ^ ((row >> 2) & 1)) << 4);
 }
 
-// 16 bytes global -> shared, of which the first `bytes` are read and the rest become zero.
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, int bytes)
+// c = a[16x16] * b[16x8]: the first product of a sum.
+__device__ __forceinline__ void mma_f16_16816_zero(float (&c)[4], uint32_t a0, uint32_t a1,
+                                                   uint32_t a2, uint32_t a3, uint32_t b0,
+                                                   uint32_t b1)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
-                 : "memory");
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void copy_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// What the issuing side of a warp leaves for the computing side, per stage.
-constexpr int kFirst = 1, kLast = 2, kWhole = 4;
+// What the producer leaves for the consumer, per stage.
+constexpr int kFirst = 1, kLast = 2, kWhole = 4, kEnd = 8;
 struct __align__(16) Meta {
     int s, n_valid, flags, unused;
 };
 
-// Where a warp fetches next in its kv head's block order.
+constexpr int kAhead = 3;   // blocks whose page ids are requested ahead
+
+// A producer lane: where its group's run is, and what has been requested ahead.
 struct Cursor {
     int s, blk, nb, ctx;
-    int left;              // blocks of the run not yet fetched
-    int pbase;             // first page (index in the sequence) of the window below
-    int page, page_next;   // this lane's page ids of the window and of the one after it
-    bool fresh;            // the next block starts a piece
-    bool from_start;       // the piece began at the sequence's first block
+    int left;            // blocks of the run not yet fetched
+    int now[kAhead];     // the lane's page ids of blocks blk, blk + 1, ...
+    int next_ctx;        // of sequence s + 1 (clamped), and the page ids of its first blocks
+    int next[kAhead];
+    bool fresh;          // the next block starts a piece
+    bool from_start;     // the piece began at the sequence's first block
 };
 
-// What a lane's copies have in common, block after block.
-struct LaneCopies {
-    const uint8_t *k_row;      // K codes of its first row in page 0 (V: v_delta bytes on)
-    long long v_delta;
-    uint32_t row_bytes, page_bytes;   // from a position to the next, from a page to the next
-    const uint8_t *par;        // its parameters in page 0 (K for low lanes, V for high ones)
-    uint32_t par_page_bytes;
-    uint32_t dst0, dst1, dst_par;     // places in a stage (dst1: the row after, D = 128)
-    int row, par_half, par_pos;       // its first row and its parameters' half and first position
-};
-
-// Loads sequence c.s (passing by empty ones) and the page ids from block c.blk on; false when no
-// sequence is left (the contexts changed under the launch).
-__device__ __forceinline__ bool open_sequence(Cursor &c, const Args &a, int lane)
+// The id of page `sub` of a block (0 past the block-table row, and where the block has fewer pages).
+__device__ __forceinline__ int page_id(const Args &a, int s, int blk, int sub)
 {
-    for (; c.s < a.num_seqs; ++c.s) {
-        c.ctx = clamped_ctx(a, c.s);
-        c.nb = blocks_of(c.ctx);
-        if (c.blk < c.nb)
-            break;
-        c.blk = 0;
-    }
-    if (c.s >= a.num_seqs)
-        return false;
-    const int32_t *row = a.block_table + static_cast<size_t>(c.s) * a.bt_stride;
-    const int pages = (c.ctx + (1 << a.log2_page) - 1) >> a.log2_page;
-    c.pbase = (c.blk * kBlock) >> a.log2_page;
-    c.page = c.pbase + lane < pages ? row[c.pbase + lane] : 0;
-    c.page_next = c.pbase + 32 + lane < pages ? row[c.pbase + 32 + lane] : 0;
-    c.fresh = true;
-    c.from_start = c.blk == 0;
-    return true;
+    const int pi = ((blk * kBlock) >> a.log2_page) + sub;
+    return pi < a.bt_stride ? a.block_table[static_cast<size_t>(s) * a.bt_stride + pi] : 0;
 }
 
-// Fetches the cursor's block into a stage and moves the cursor on.  Rows past the context become
-// zeros (read from no memory); a page id outside the pool is flagged and reads as zeros.
-template <int D>
-__device__ __forceinline__ void fetch_block(Cursor &c, const Args &a, const LaneCopies &l,
-                                            uint32_t stage, Meta *meta, int lane)
+// Requests what a switch to sequence c.s + 1 needs; nothing here waits for it.
+__device__ __forceinline__ void request_next(Cursor &c, const Args &a, int sub)
 {
-    using Geom = I4Geom<D>;
-    const int pos = c.blk * kBlock;
-    const int n_valid = min(kBlock, c.ctx - pos);
-    int pi = pos >> a.log2_page;
-    if (pi >= c.pbase + 32) {   // 32 pages hold whole blocks: a block's pages share a window
-        c.pbase += 32;
-        c.page = c.page_next;
-        const int pages = (c.ctx + (1 << a.log2_page) - 1) >> a.log2_page;
-        const int32_t *row = a.block_table + static_cast<size_t>(c.s) * a.bt_stride;
-        c.page_next = c.pbase + 32 + lane < pages ? row[c.pbase + 32 + lane] : 0;
-    }
-    pi -= c.pbase;
-    uint32_t page[2], off[2];
-    page[0] = __shfl_sync(0xffffffffu, c.page, pi);
-    page[1] = __shfl_sync(0xffffffffu, c.page, (pi + (16 >> a.log2_page)) & 31);
-    off[0] = pos & ((1 << a.log2_page) - 1);
-    off[1] = (pos + 16) & ((1 << a.log2_page) - 1);
-    int live[2] = {n_valid, n_valid - 16};   // valid rows of each half
+    c.next_ctx = 0;
+    if (c.s + 1 < a.num_seqs) {
+        c.next_ctx = clamped_ctx(a, c.s + 1);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (page[h] >= static_cast<uint32_t>(a.num_pages)) {
-            if (lane == 0 && live[h] > 0)
-                atomicOr(err_word(a), kErrPageRange);
-            page[h] = 0;
-            live[h] = 0;
-        }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint8_t *k = l.k_row + static_cast<unsigned long long>(page[h]) * l.page_bytes +
-                           off[h] * l.row_bytes;
-        const int b0 = l.row < live[h] ? 16 : 0;
-        const uint32_t d0 = stage + l.dst0 + h * Geom::kHalfCodes;
-        copy_async16(d0, k, b0);
-        copy_async16(d0 + Geom::kOffV, k + l.v_delta, b0);
-        if (D == 128) {   // four lanes a row: the next row too
-            const int b1 = l.row + 1 < live[h] ? 16 : 0;
-            const uint32_t d1 = stage + l.dst1 + h * Geom::kHalfCodes;
-            k += l.row_bytes;
-            copy_async16(d1, k, b1);
-            copy_async16(d1 + Geom::kOffV, k + l.v_delta, b1);
-        }
-    }
-    // parameters: 16 bytes a lane
-    if (D == 128 || lane < 16) {
-        const uint32_t pg = l.par_half ? page[1] : page[0], of = l.par_half ? off[1] : off[0];
-        const int lv = l.par_half ? live[1] : live[0];
-        constexpr int kPer = 4 * Geom::kGroups;   // bytes of a position
-        const int bytes = max(0, min(16, (lv - l.par_pos) * kPer));
-        copy_async16(stage + l.dst_par,
-                     l.par + static_cast<unsigned long long>(pg) * l.par_page_bytes + of * kPer,
-                     bytes);
-    }
-    ++c.blk;
-    --c.left;
-    const bool last = c.blk == c.nb || c.left == 0;
-    if (lane == 0) {
-        const int flags = (c.fresh ? kFirst : 0) | (last ? kLast : 0) |
-                          (c.from_start && c.blk == c.nb ? kWhole : 0);
-        *reinterpret_cast<int4 *>(meta) = make_int4(c.s, n_valid, flags, 0);
-    }
-    c.fresh = false;
-    if (last && c.left > 0) {
-        ++c.s;
-        c.blk = 0;
-        if (!open_sequence(c, a, lane))
-            c.left = 0;
+        for (int i = 0; i < kAhead; ++i)
+            c.next[i] = page_id(a, c.s + 1, i, sub);
     }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Args a)
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_decode_int4_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                             const __grid_constant__ CUtensorMap tmap_v,
+                             const __grid_constant__ CUtensorMap tmap_kp,
+                             const __grid_constant__ CUtensorMap tmap_vp, const Args a)
 {
     pdl_wait();
     pdl_trigger();
@@ -315,40 +243,35 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
     constexpr int NG = Geom::kGroups;     // groups of a vector
     constexpr int NC = Geom::kChunks;     // 16-byte chunks of a row: 32 dims each
     constexpr int NS = Geom::kStages;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int G = a.group;
     const int Hkv = a.kv_heads;
-    uint8_t *ring = smem + warp * Geom::kWarpBytes;
-    Meta *metas = reinterpret_cast<Meta *>(smem + kWarps * Geom::kWarpBytes) + warp * NS;
-    long long *scratch =
-        reinterpret_cast<long long *>(smem + kWarps * Geom::kWarpBytes + Geom::kMetaBytes);
+    const int HW = a.heads;
+    const int head_groups = Hkv / HW;
+    Meta *metas = reinterpret_cast<Meta *>(smem + Geom::kOffMeta);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Geom::kOffBar);   // [groups][NS]
+    uint64_t *empty = full + kWarps * NS;
+    long long *scratch = reinterpret_cast<long long *>(smem + Geom::kOffScratch);
+    long long *bound_cost = scratch + kBlockWarps;       // [kWarps + 1]
+    long long *bound_g = bound_cost + kWarps + 1;        // first block at or past it
+    long long *bound_s = bound_g + kWarps + 1;           // its sequence
+    long long *bound_blk = bound_s + kWarps + 1;         // and its block in the sequence
 
-    // ---- this warp's run: kv head kvh, blocks [g0, g1) of its order, beginning in sequence s0 ----
-    const int gw = blockIdx.x * kWarps + warp;
-    const int kvh = gw % Hkv;
-    const int run = gw / Hkv;
-    Cursor c;
-    int run_len = 0;   // (a run's blocks: far below 2^31 for tables that fit the memory)
-    const long long *bound_end = nullptr;   // the index of the first block past the run
-    if (a.per_unit) {
-        if (run >= a.num_seqs)
-            return;
-        bool over;
-        c.ctx = clamped_ctx(a, run, &over);
-        if (over && lane == 0 && kvh == 0)
-            atomicOr(err_word(a), kErrContextRange);
-        if (c.ctx == 0) {   // no positions: the rows are 0
-            const size_t row0 = static_cast<size_t>(run) * a.q_heads + static_cast<size_t>(kvh) * G;
-            for (int i = lane; i < G * D; i += 32)
-                store_out(a.out, a.out_f32, row0 * D + i, 0.0f);
-            return;
-        }
-        c.s = run;
-        c.blk = 0;
-        run_len = blocks_of(c.ctx);
-    } else {
+    for (int i = threadIdx.x; i < kWarps * NS; i += kThreads) {
+        mbar_init(&full[i], 1);     // the producer's arrival and the bytes
+        mbar_init(&empty[i], HW);   // one arrival per warp of the group
+    }
+    fence_mbar_init();
+
+    // ---- the runs of this CTA's groups: blocks [g0, g1) of a kv head's order, first sequence ----
+    const int gg0 = blockIdx.x * a.groups;
+    const int run_lo = gg0 / head_groups;
+    long long n_runs = a.runs, cost = 0;
+    if (!a.per_unit) {
         // Prefix sums of the sequences' blocks over the CTA; then the bounds of the few runs this
         // CTA's warps have, each found by the thread whose sequences hold it.
         const int S = a.num_seqs;
@@ -374,27 +297,17 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
         __syncthreads();
         long long acc = incl - mine, total = 0;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
+        for (int i = 0; i < kBlockWarps; ++i) {
             const long long t = scratch[i];
             if (i < warp)
                 acc += t;
             total += t;
         }
-        const long long n_runs = min(static_cast<long long>(a.runs), total);
-        const long long cost = kBlockCost * total + kPieceCost * S;
-        const int run_lo = blockIdx.x * kWarps / Hkv;
-        const int n_bounds = (blockIdx.x * kWarps + kWarps - 1) / Hkv - run_lo + 2;   // 2 .. 9
-        long long *bound_cost = scratch + kWarps;            // [9]
-        long long *bound_g = bound_cost + kWarps + 1;        // [9] first block at or past it
-        long long *bound_s = bound_g + kWarps + 1;           // [9] its sequence
-        long long *bound_blk = bound_s + kWarps + 1;         // [9] and its block in the sequence
-        // (cost and n_runs are taken up again after the loop: scratch[kScratchCost], + 1)
         if (total == 0)
             return;   // every row is written by the merge
-        if (threadIdx.x == kThreads - 1) {
-            scratch[kScratchCost] = cost;
-            scratch[kScratchCost + 1] = n_runs;
-        }
+        n_runs = min(static_cast<long long>(a.runs), total);
+        cost = kBlockCost * total + kPieceCost * S;
+        const int n_bounds = (gg0 + a.groups - 1) / head_groups - run_lo + 2;   // 2 .. kWarps + 1
         if (threadIdx.x < n_bounds) {
             const long long b = run_lo + static_cast<long long>(threadIdx.x);
             bound_cost[threadIdx.x] = b < n_runs ? run_start(b, cost, n_runs) : cost;
@@ -420,78 +333,237 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
             }
             acc += nb;
         }
-        __syncthreads();
-        const int i = run - run_lo;
-        run_len = static_cast<int>(bound_g[i + 1] - bound_g[i]);
-        if (run >= n_runs || run_len <= 0)
-            return;
-        c.s = static_cast<int>(bound_s[i]);
-        c.blk = static_cast<int>(bound_blk[i]);
-        bound_end = &bound_g[i + 1];
     }
-    c.left = run_len;
-    if (!open_sequence(c, a, lane))
-        return;
+    __syncthreads();   // the bounds and the barriers
 
-    LaneCopies l;
-    {
-        constexpr int kRow = Geom::kRow;
+    // the group of this warp, or of this producer lane, and its run
+    const int grp = warp >= kWarps ? lane >> 2 : warp / HW;
+    const int head0 = (gg0 + grp) % head_groups * HW;
+    const int run = (gg0 + grp) / head_groups;
+    int run_len = 0;   // (a run's blocks: far below 2^31 for tables that fit the memory)
+    if (grp < a.groups) {
+        if (a.per_unit)
+            run_len = run < a.num_seqs ? blocks_of(clamped_ctx(a, run)) : 0;
+        else if (run < n_runs)
+            run_len = static_cast<int>(bound_g[run - run_lo + 1] - bound_g[run - run_lo]);
+    }
+    const uint32_t group_stage = HW * Geom::kStageBytes;
+    uint8_t *ring = smem + grp * NS * group_stage;
+
+    if (warp >= kWarps) {
+        // ------------- producer: lanes 4 g .. 4 g + 3 fill group g's ring, a page each -------------
         const int P = 1 << a.log2_page;
-        const int chunk = lane & (NC - 1);
-        l.row = NC == 4 ? 2 * (lane >> 2) : 2 * ((lane >> 1) & 7) + (lane >> 4);
-        l.row_bytes = a.hnd ? kRow : Hkv * kRow;
-        l.page_bytes = static_cast<uint32_t>(P) * Hkv * kRow;
-        l.k_row = a.k_codes + static_cast<size_t>(kvh) * (a.hnd ? P * kRow : kRow) +
-                  static_cast<size_t>(l.row) * l.row_bytes + chunk * 16;
-        l.v_delta = a.v_codes - a.k_codes;
-        l.dst0 = half_offset<D>(l.row, chunk);
-        l.dst1 = half_offset<D>(l.row + 1, chunk);
-        // 4 NG lanes hold the 16 positions of one half of one tensor, 4 / NG positions each
-        const bool is_v = lane >= 8 * NG;
-        l.par_half = (lane / (4 * NG)) & 1;
-        const int c16 = lane % (4 * NG);
-        l.par_pos = c16 * (4 / NG);
-        l.par_page_bytes = static_cast<uint32_t>(Hkv) * P * NG * 4;
-        l.par = (is_v ? a.v_params : a.k_params) + static_cast<size_t>(kvh) * P * NG * 4 + c16 * 16;
-        l.dst_par = (is_v ? Geom::kOffVp : Geom::kOffKp) + (l.par_half * 4 * NG + c16) * 16;
-    }
-
-    // ---- the first blocks on their way ----
-    const uint32_t ring32 = smem_addr(ring);
-    int fetched = 0;   // stage of the next fetch
-    int pending = 0;   // blocks fetched and not yet computed
+        const int box = min(P, kBlock);               // positions of a TMA box
+        const int sub = lane & 3;
+        const uint32_t page_tx = HW * box * (2 * Geom::kRow + 2 * NG * 4);
+        const uint64_t policy = l2_policy_evict_first();
+        Cursor c;
+        c.left = run_len;
+        c.s = a.per_unit ? run : 0;
+        c.blk = 0;
+        c.nb = 0;
+        c.from_start = true;
+        c.fresh = true;
+        if (run_len > 0) {
+            if (!a.per_unit) {
+                c.s = static_cast<int>(bound_s[run - run_lo]);
+                c.blk = static_cast<int>(bound_blk[run - run_lo]);
+                for (; c.s < a.num_seqs; ++c.s, c.blk = 0) {   // past empty sequences
+                    c.ctx = clamped_ctx(a, c.s);
+                    c.nb = blocks_of(c.ctx);
+                    if (c.blk < c.nb)
+                        break;
+                }
+            } else {
+                bool over;
+                c.ctx = clamped_ctx(a, c.s, &over);
+                c.nb = blocks_of(c.ctx);
+                if (over && head0 == 0 && sub == 0)
+                    atomicOr(err_word(a), kErrContextRange);
+            }
+            if (c.s < a.num_seqs) {
 #pragma unroll
-    for (int i = 0; i < NS - 1; ++i) {
-        if (c.left > 0) {
-            fetch_block<D>(c, a, l, ring32 + fetched * Geom::kStageBytes, &metas[fetched], lane);
-            ++pending;
+                for (int i = 0; i < kAhead; ++i)
+                    c.now[i] = page_id(a, c.s, c.blk + i, sub);
+                request_next(c, a, sub);
+            }
+            c.from_start = c.blk == 0;
         }
-        copy_commit();
-        fetched = fetched + 1 == NS ? 0 : fetched + 1;
+        int issued = 0, st = 0;
+        uint32_t phase = 1;   // of the empty barrier that the next fetch waits for, after NS fetches
+        bool ended = run_len <= 0;
+        bool ok = true;
+        long long since = clock64();
+        while (__any_sync(0xffffffffu, !ended)) {
+            bool ready = !ended && (issued < NS || mbar_test(&empty[grp * NS + st], phase));
+            ready = __shfl_sync(0xffffffffu, ready, lane & ~3);   // the group's lanes go together
+            if (!__any_sync(0xffffffffu, ready)) {
+                if (clock64() - since > kWaitLimitCycles) {
+                    ok = false;
+                    break;
+                }
+                __nanosleep(20);
+                continue;
+            }
+            since = clock64();
+            uint64_t *bar = &full[grp * NS + st];
+            const bool more = c.s < a.num_seqs;   // false: the contexts changed under the launch
+            const int pos = c.blk * kBlock;
+            const int n_valid = more ? min(kBlock, c.ctx - pos) : 0;
+            const int np = (n_valid + box - 1) >> (box == 16 ? 4 : box == 32 ? 5 : 6);
+            const bool last = c.blk + 1 == c.nb || c.left == 1;
+            const bool whole = c.from_start && c.blk + 1 == c.nb;
+            if (ready && sub == 0) {
+                const int flags = !more ? kEnd
+                                        : (c.fresh ? kFirst : 0) | (last ? kLast : 0) |
+                                              (whole ? kWhole : 0) | (c.left == 1 ? kEnd : 0);
+                *reinterpret_cast<int4 *>(&metas[grp * NS + st]) = make_int4(c.s, n_valid, flags, 0);
+                mbar_arrive_expect_tx(bar, np * page_tx);
+            }
+            __syncwarp();
+            if (ready) {
+                if (sub < np) {
+                    uint8_t *stage = ring + st * group_stage;
+                    const int off = pos & (P - 1);
+                    int page = c.now[0];
+                    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) {
+                        atomicOr(err_word(a), kErrPageRange);
+                        page = 0;
+                    }
+                    // boxes land as [head][position]; one page after all of the one before
+                    const int c1 = a.hnd ? off : (page << a.log2_page) + off;
+                    const int c2 = a.hnd ? page * Hkv + head0 : head0;
+                    uint8_t *codes = stage + sub * HW * box * Geom::kRow;
+                    uint8_t *par = stage + HW * Geom::kOffKp + sub * Geom::page_par(HW, box);
+                    tma_load_3d(codes, &tmap_k, 0, c1, c2, bar, policy);
+                    tma_load_3d(codes + HW * Geom::kOffV, &tmap_v, 0, c1, c2, bar, policy);
+                    tma_load_3d(par, &tmap_kp, off * (NG * 2), head0, page, bar, policy);
+                    tma_load_3d(par + HW * Geom::kParBytes, &tmap_vp, off * (NG * 2), head0, page, bar,
+                                policy);
+                }
+                ++c.blk;
+                --c.left;
+                c.fresh = false;
+                // where the merge finds the unit's pieces: nowhere, or from this run's slot to that
+                // of the run that holds the unit's last block
+                if (more && last && !a.per_unit && c.from_start && sub == 0) {
+                    int first = 0, count = 1;
+                    if (!whole) {
+                        const long long g_last = bound_g[run - run_lo + 1] - 1 + (c.nb - c.blk);
+                        first = c.s + run;
+                        count = static_cast<int>(run_of(block_cost(g_last, c.s), cost, n_runs) -
+                                                 run + 1);
+                    }
+                    for (int h = head0; h < head0 + HW; ++h)
+                        a.unit_info[static_cast<size_t>(c.s) * Hkv + h] =
+                            make_int2(h * (a.num_seqs + a.runs) + first, count);
+                }
+                if (!more || c.left == 0) {
+                    ended = true;
+                } else if (last) {   // on to the next sequence, requested long ago
+                    ++c.s;
+                    c.blk = 0;
+                    c.ctx = c.next_ctx;
+                    c.nb = blocks_of(c.ctx);
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i)
+                        c.now[i] = c.next[i];
+                    while (c.nb == 0 && ++c.s < a.num_seqs) {   // past empty sequences
+                        c.ctx = clamped_ctx(a, c.s);
+                        c.nb = blocks_of(c.ctx);
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i)
+                            c.now[i] = page_id(a, c.s, i, sub);
+                    }
+                    c.fresh = true;
+                    c.from_start = true;
+                    if (c.s < a.num_seqs)
+                        request_next(c, a, sub);
+                } else {
+#pragma unroll
+                    for (int i = 0; i + 1 < kAhead; ++i)
+                        c.now[i] = c.now[i + 1];
+                    c.now[kAhead - 1] = page_id(a, c.s, c.blk + kAhead - 1, sub);
+                }
+                ++issued;
+                if (++st == NS) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+            }
+            __syncwarp();
+        }
+        if (!ok) {
+            if (lane == 0)
+                atomicOr(err_word(a), kErrDecodeEmptyWait);
+            // every copy in flight lands before the CTA can exit
+            if (grp < a.groups && sub == 0)
+                for (int b = max(0, issued - NS); b < issued; ++b)
+                    if (!mbar_wait(&full[grp * NS + b % NS], (b / NS) & 1))
+                        atomicOr(err_word(a), kErrDrainWait);
+        }
+        return;
     }
-    __syncwarp();
 
+    // ------------------------------------ consumers ------------------------------------------
+    const int in_group = warp - grp * HW;
+    const int kvh = head0 + in_group;
+    if (run_len <= 0) {
+        if (a.per_unit && grp < a.groups && run < a.num_seqs) {   // no positions: the rows are 0
+            const size_t row0 = static_cast<size_t>(run) * a.q_heads + static_cast<size_t>(kvh) * G;
+            for (int i = lane; i < G * D; i += 32)
+                store_out(a.out, a.out_f32, row0 * D + i, 0.0f);
+        }
+        return;
+    }
+    const uint32_t ring32 = smem_addr(ring);
+    metas += grp * NS;
+    full += grp * NS;
+    empty += grp * NS;
+    // This head's tiles in a stage: the boxes of one page lie as [head][position], so tile 1 is the
+    // next 16 positions of the head or the next page (page size 16), tile 2 the next but one or the
+    // next page (32), and tile 3 as far from tile 2 as 1 from 0.
+    const int box = min(1 << a.log2_page, kBlock);
+    const int head_codes = in_group * box * Geom::kRow;
+    const int head_par = HW * Geom::kOffKp + in_group * box * NG * 4;
+    const int codes1 = box == 16 ? HW * Geom::kTileCodes : Geom::kTileCodes;
+    const int codes2 = box == 64 ? 2 * Geom::kTileCodes : 2 * HW * Geom::kTileCodes;
+    const int par1 = box == 16 ? Geom::page_par(HW, 16) : Geom::kTilePar;
+    const int par2 = box == 64   ? 2 * Geom::kTilePar
+                     : box == 32 ? Geom::page_par(HW, 32)
+                                 : 2 * Geom::page_par(HW, 16);
+    const int v_codes = HW * Geom::kOffV, v_par = HW * Geom::kParBytes;   // V's from K's
     const int r = lane >> 2;
     const int t = lane & 3;
     // K: the 8 bytes of group 0 that this thread reads of position 2 r (group 1: 32 bytes on, a
     // turn of the chunk) and of position 2 r + 1; V: this lane's row of the transposing loads
-    const int k_off[2] = {half_offset<D>(2 * r, t >> 1) + (t & 1) * 8,
-                          half_offset<D>(2 * r + 1, t >> 1) + (t & 1) * 8};
-    const int v_off = half_offset<D>(lane & 15, lane >> 4);
+    const int k_off[2] = {code_offset<D>(2 * r, t >> 1) + (t & 1) * 8,
+                          code_offset<D>(2 * r + 1, t >> 1) + (t & 1) * 8};
+    const int v_off = code_offset<D>(lane & 15, lane >> 4);
 
     uint32_t qb[NG][2][2][2];   // B fragments: [group][word][nibble][register]
     float o[NC][2][4];          // O^T: [32 dims][whole byte, high half][fragment]
     float zacc[NG][2];          // sum of p lo, heads 2 t and 2 t + 1
-    float m_run[2], l_run[2], m_thr[2], mf[2], f[2], hq[NG][2];
+    // heads 2 t and 2 t + 1: the sum; the maximum in use times f, and the y from which it moves
+    float l_run[2], mf[2], m_thr[2], f[2], hq[NG][2];
     float vnorm = 1.0f, v_thr = 0.0f;
     int stage = 0;
+    uint32_t phase = 0;
 
-    for (; pending > 0; --pending) {
+    while (true) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
+            if (lane == 0)
+                atomicOr(err_word(a), kErrDecodeFullWait);
+            return;
+        }
         const int4 mt = *reinterpret_cast<const int4 *>(&metas[stage]);
         const int s = mt.x, n_valid = mt.y, flags = mt.z;
+        if (n_valid == 0)
+            return;   // the contexts changed under the launch
         const size_t row0 = static_cast<size_t>(s) * a.q_heads + static_cast<size_t>(kvh) * G;
-        uint4 qw[NG][2];
-        if (flags & kFirst) {   // the query rows travel with the block's last bytes
+
+        if (flags & kFirst) {
+            uint4 qw[NG][2];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const uint4 *src = reinterpret_cast<const uint4 *>(
@@ -499,17 +571,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
                 qw[g][0] = src[0];
                 qw[g][1] = src[1];
             }
-        }
-        copy_wait<NS - 2>();
-        __syncwarp();
-        if (c.left > 0) {
-            fetch_block<D>(c, a, l, ring32 + fetched * Geom::kStageBytes, &metas[fetched], lane);
-            ++pending;
-        }
-        copy_commit();
-        fetched = fetched + 1 == NS ? 0 : fetched + 1;
-
-        if (flags & kFirst) {
             float qv[NG][16], qmax = 0.0f, qsum[NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
@@ -561,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
                     hq[g][j] = __shfl_sync(0xffffffffu, qsum[g] * h_scale, src);
-                m_run[j] = m_thr[j] = -INFINITY;
+                m_thr[j] = -INFINITY;
                 mf[j] = 0.0f;
                 l_run[j] = 0.0f;
 #pragma unroll
@@ -577,52 +638,49 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
             v_thr = 0.0f;   // any positive value scale sets vnorm
         }
 
-        const uint8_t *st = ring + stage * Geom::kStageBytes;
-        // parameters of this thread's positions: 16 T + 2 r and 16 T + 2 r + 1
-        uint32_t kp[2][2][NG], vp[2][2][NG];
-#pragma unroll
-        for (int T = 0; T < 2; ++T) {
-            const uint8_t *kpp = st + Geom::kOffKp + (16 * T + 2 * r) * NG * 4;
-            const uint8_t *vpp = st + Geom::kOffVp + (16 * T + 2 * r) * NG * 4;
+        const uint8_t *st = ring + stage * group_stage;
+        // this thread's positions are 16 T + 2 r and 16 T + 2 r + 1
+        auto load_params = [&](uint32_t (&w)[2][NG], const uint8_t *p) {
             if constexpr (NG == 2) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(kpp);
-                const uint4 y = *reinterpret_cast<const uint4 *>(vpp);
-                kp[T][0][0] = x.x;
-                kp[T][0][1] = x.y;
-                kp[T][1][0] = x.z;
-                kp[T][1][1] = x.w;
-                vp[T][0][0] = y.x;
-                vp[T][0][1] = y.y;
-                vp[T][1][0] = y.z;
-                vp[T][1][1] = y.w;
+                const uint4 x = *reinterpret_cast<const uint4 *>(p);
+                w[0][0] = x.x;
+                w[0][NG - 1] = x.y;
+                w[1][0] = x.z;
+                w[1][NG - 1] = x.w;
             } else {
-                const uint2 x = *reinterpret_cast<const uint2 *>(kpp);
-                const uint2 y = *reinterpret_cast<const uint2 *>(vpp);
-                kp[T][0][0] = x.x;
-                kp[T][1][0] = x.y;
-                vp[T][0][0] = y.x;
-                vp[T][1][0] = y.y;
+                const uint2 x = *reinterpret_cast<const uint2 *>(p);
+                w[0][0] = x.x;
+                w[1][0] = x.y;
             }
-        }
+        };
+        const uint8_t *par = st + head_par + 2 * r * NG * 4;
 
         // ---- scores: y[T][position][head] ----
-        float y[2][2][2];
+        float y[kTiles][2][2];
 #pragma unroll
-        for (int T = 0; T < 2; ++T) {
+        for (int T = 0; T < kTiles; ++T) {
+            const int at = (T & 1) * codes1 + (T >> 1) * codes2;
+            uint32_t kp[2][NG];
+            load_params(kp, par + (T & 1) * par1 + (T >> 1) * par2);
             float acc[NG][4];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.0f;
                 const uint2 w0 = *reinterpret_cast<const uint2 *>(
-                    st + T * Geom::kHalfCodes + (k_off[0] ^ (32 * g)));
+                    st + head_codes + at + (k_off[0] ^ (32 * g)));
                 const uint2 w1 = *reinterpret_cast<const uint2 *>(
-                    st + T * Geom::kHalfCodes + (k_off[1] ^ (32 * g)));
+                    st + head_codes + at + (k_off[1] ^ (32 * g)));
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint32_t x0 = j ? w0.y : w0.x, x1 = j ? w1.y : w1.x;
                     const uint32_t z0 = x0 >> 8, z1 = x1 >> 8;
-                    mma_f16_16816(acc[g], x0 & 0x000F000Fu, x1 & 0x000F000Fu, z0 & 0x000F000Fu,
-                                  z1 & 0x000F000Fu, qb[g][j][0][0], qb[g][j][0][1]);
+                    if (j == 0)
+                        mma_f16_16816_zero(acc[g], x0 & 0x000F000Fu, x1 & 0x000F000Fu,
+                                           z0 & 0x000F000Fu, z1 & 0x000F000Fu, qb[g][j][0][0],
+                                           qb[g][j][0][1]);
+                    else
+                        mma_f16_16816(acc[g], x0 & 0x000F000Fu, x1 & 0x000F000Fu,
+                                      z0 & 0x000F000Fu, z1 & 0x000F000Fu, qb[g][j][0][0],
+                                      qb[g][j][0][1]);
                     mma_f16_16816(acc[g], x0 & 0x00F000F0u, x1 & 0x00F000F0u, z0 & 0x00F000F0u,
                                   z1 & 0x00F000F0u, qb[g][j][1][0], qb[g][j][1][1]);
                 }
@@ -634,35 +692,47 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
                     float v = 0.0f;
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        const float sc = __uint_as_float(kp[T][i][g] << 16);
-                        const float lo = __uint_as_float(kp[T][i][g] & 0xFFFF0000u);
+                        const float sc = __uint_as_float(kp[i][g] << 16);
+                        const float lo = __uint_as_float(kp[i][g] & 0xFFFF0000u);
                         v = g == 0 ? sc * acc[g][2 * i + j] : fmaf(sc, acc[g][2 * i + j], v);
                         v = fmaf(lo, hq[g][j], v);
                     }
                     y[T][i][j] = v;
                 }
         }
+        uint32_t vp[kTiles][2][NG];
+#pragma unroll
+        for (int T = 0; T < kTiles; ++T)
+            load_params(vp[T], par + v_par + (T & 1) * par1 + (T >> 1) * par2);
         if (n_valid < kBlock) {
 #pragma unroll
-            for (int T = 0; T < 2; ++T)
+            for (int T = 0; T < kTiles; ++T)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    if (16 * T + 2 * r + i >= n_valid)
+                    if (16 * T + 2 * r + i >= n_valid) {
+                        // what lies in unused slots is any code and any parameter, NaN too
                         y[T][i][0] = y[T][i][1] = -INFINITY;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+                            vp[T][i][g] = 0u;
+                    }
         }
 
         // ---- running maxima, and the power of two on the value scales ----
         float mb[2], vmax = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            mb[j] = fmaxf(fmax3(y[0][0][j], y[0][1][j], y[1][0][j]), y[1][1][j]);
+        for (int j = 0; j < 2; ++j) {
+            mb[j] = fmaxf(y[0][0][j], y[0][1][j]);
 #pragma unroll
-        for (int T = 0; T < 2; ++T)
+            for (int T = 1; T < kTiles; ++T)
+                mb[j] = fmax3(mb[j], y[T][0][j], y[T][1][j]);
+        }
+#pragma unroll
+        for (int T = 0; T < kTiles; ++T)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    vmax = fmaxf(vmax, __uint_as_float(vp[T][i][g] << 16));
+                vmax = fmax3(vmax, __uint_as_float(vp[T][i][0] << 16),
+                             __uint_as_float(vp[T][i][NG - 1] << 16));
         if (__any_sync(0xffffffffu, mb[0] > m_thr[0] || mb[1] > m_thr[1] || vmax > v_thr)) {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
@@ -673,15 +743,17 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
             float fix[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float m_new = fmaxf(m_run[j], mb[j]);
-                fix[j] = m_run[j] == -INFINITY ? 0.0f : fast_exp2((m_run[j] - m_new) * f[j]);
-                l_run[j] *= fix[j];
+                fix[j] = 1.0f;
+                if (mb[j] > m_thr[j]) {   // the same in every lane of the head
+                    const float mf_new = mb[j] * f[j];
+                    fix[j] = m_thr[j] == -INFINITY ? 0.0f : fast_exp2(mf[j] - mf_new);
+                    l_run[j] *= fix[j];
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    zacc[g][j] *= fix[j];
-                m_run[j] = m_new;
-                m_thr[j] = m_new + kLagLog2 / f[j];
-                mf[j] = m_new == -INFINITY ? 0.0f : m_new * f[j];
+                    for (int g = 0; g < NG; ++g)
+                        zacc[g][j] *= fix[j];
+                    m_thr[j] = mb[j] + kLagLog2 / f[j];
+                    mf[j] = mf_new;
+                }
             }
             float turn = 1.0f;
             if (vmax > v_thr) {   // the same in every lane that shares the maximum: all of them
@@ -704,8 +776,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
         }
 
         // ---- probabilities, and out ----
+        const uint32_t vb = ring32 + stage * group_stage + v_codes + head_codes;
 #pragma unroll
-        for (int T = 0; T < 2; ++T) {
+        for (int T = 0; T < kTiles; ++T) {
             float p[2][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -725,12 +798,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
                     zacc[g][1] = fmaf(p[i][1], lo, zacc[g][1]);
                     pb[g][i] = movmatrix_trans(pack_f16x2(p[i][0] * sc, p[i][1] * sc));
                 }
-            const uint32_t vb = ring32 + stage * Geom::kStageBytes + Geom::kOffV +
-                                T * Geom::kHalfCodes;
+            const uint32_t va = vb + (T & 1) * codes1 + (T >> 1) * codes2;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {   // chunks 2 g and 2 g + 1
                 uint32_t e[4];
-                ldsm_x2_trans_b8(vb + (v_off ^ (32 * g)), e[0], e[1], e[2], e[3]);
+                ldsm_x2_trans_b8(va + (v_off ^ (32 * g)), e[0], e[1], e[2], e[3]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     // whole bytes (low + 16 high) and their high halves: one operation a pair
@@ -745,6 +817,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
                 }
             }
         }
+
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&empty[stage]);
 
         // ---- the end of a piece: normalised rows to the output or to the piece's slot ----
         if (flags & kLast) {
@@ -761,8 +837,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
                 inv[j] = 1.0f / l_run[j];   // the piece holds a position: the sum is at least 1
             }
             const bool whole = flags & kWhole;
-            if (whole && !a.per_unit && lane == 0)   // the merge has nothing to do for it
-                a.unit_info[static_cast<size_t>(s) * Hkv + kvh] = make_int2(0, 1);
             // pieces of kv head h own slots [h (S + R), (h + 1) (S + R)), piece (s, run) s + run
             // there: distinct for every piece, consecutive for one unit's
             const int slot = kvh * (a.num_seqs + a.runs) + s + run;
@@ -793,17 +867,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_int4_kernel(const Ar
                 }
             }
         }
-        stage = stage + 1 == NS ? 0 : stage + 1;
-    }
-    copy_wait<0>();
-    // A unit that begins in this run and goes on past it (only the run's last piece can): where its
-    // pieces' slots begin, and the run that holds its last block.
-    if (bound_end != nullptr && lane == 0 && c.from_start && c.blk < c.nb) {
-        const long long g_last = *bound_end - 1 + (c.nb - c.blk);
-        const long long last = run_of(block_cost(g_last, c.s), scratch[kScratchCost],
-                                      scratch[kScratchCost + 1]);
-        a.unit_info[static_cast<size_t>(c.s) * Hkv + kvh] = make_int2(
-            kvh * (a.num_seqs + a.runs) + c.s + run, static_cast<int>(last - run + 1));
+        if (flags & kEnd)
+            return;
+        if (++stage == NS) {
+            stage = 0;
+            phase ^= 1u;
+        }
     }
 }
 
@@ -884,14 +953,10 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) merge_int4_kernel(const
 }
 
 template <int D>
-cudaError_t launch_t(const DecodeInt4Launch &l, cudaStream_t stream)
+cudaError_t launch_t(const DecodeInt4Launch &l, const CUtensorMap (&maps)[4], cudaStream_t stream)
 {
     Args a;
     a.q = static_cast<const __nv_bfloat16 *>(l.q);
-    a.k_codes = static_cast<const uint8_t *>(l.pools.k_codes);
-    a.v_codes = static_cast<const uint8_t *>(l.pools.v_codes);
-    a.k_params = static_cast<const uint8_t *>(l.pools.k_params);
-    a.v_params = static_cast<const uint8_t *>(l.pools.v_params);
     a.out = l.out;
     a.out_f32 = l.out_f32;
     a.part_o = l.part_o;
@@ -907,6 +972,8 @@ cudaError_t launch_t(const DecodeInt4Launch &l, cudaStream_t stream)
     a.group = l.q_heads / l.pools.kv_heads;
     a.log2_page = l.pools.page_size == 16 ? 4 : l.pools.page_size == 32 ? 5 : 6;
     a.num_pages = l.pools.num_pages;
+    a.heads = int4_group_heads(l.pools.kv_heads);
+    a.groups = kWarps / a.heads;
     a.per_unit = l.per_unit ? 1 : 0;
     a.hnd = l.pools.hnd ? 1 : 0;
     a.scale_log2 = l.scale * kLog2e;
@@ -917,9 +984,10 @@ cudaError_t launch_t(const DecodeInt4Launch &l, cudaStream_t stream)
                                            static_cast<int>(smem));
     if (err != cudaSuccess)
         return err;
-    const long long warps = static_cast<long long>(a.runs) * a.kv_heads;
-    const unsigned grid = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
-    err = launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, a);
+    const long long groups = static_cast<long long>(a.runs) * (a.kv_heads / a.heads);
+    const unsigned grid = static_cast<unsigned>((groups + a.groups - 1) / a.groups);
+    err = launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, maps[0], maps[1], maps[2],
+                     maps[3], a);
     if (err != cudaSuccess || l.per_unit)
         return err;
     const int rows = l.num_seqs * l.q_heads;
@@ -930,11 +998,20 @@ cudaError_t launch_t(const DecodeInt4Launch &l, cudaStream_t stream)
 
 }  // namespace
 
-cudaError_t launch_decode_int4(const DecodeInt4Launch &l, cudaStream_t stream)
+int int4_group_heads(int kv_heads)
+{
+    int n = kv_heads < 8 ? kv_heads : 8;
+    while (kv_heads % n != 0)
+        --n;
+    return n;
+}
+
+cudaError_t launch_decode_int4(const DecodeInt4Launch &l, const CUtensorMap (&maps)[4],
+                               cudaStream_t stream)
 {
     if (l.num_seqs == 0)
         return cudaSuccess;
-    return l.pools.head_dim == 64 ? launch_t<64>(l, stream) : launch_t<128>(l, stream);
+    return l.pools.head_dim == 64 ? launch_t<64>(l, maps, stream) : launch_t<128>(l, maps, stream);
 }
 
 cudaError_t read_and_clear_decode_int4_errors(uint32_t *flags)

@@ -106,7 +106,10 @@ cudaError_t read_and_clear_store_int4_errors(uint32_t *flags);
 // Decode over 4-bit pages: the positions of all sequences, in kInt4Block-position blocks, are cut
 // into `runs` runs of equal cost per kv head (one warp each); per_unit: one run per sequence, no
 // workspace and no merge.
-constexpr int kInt4Block = 32;
+constexpr int kInt4Block = 64;
+constexpr int kInt4Warps = 8;   // consumer warps of a CTA, one CTA per SM
+// kv heads that a group of warps takes together: the largest divisor of their number up to 8.
+int int4_group_heads(int kv_heads);
 struct DecodeInt4Launch {
     Int4Pools pools;
     const void *q;
@@ -123,7 +126,10 @@ struct DecodeInt4Launch {
     bool per_unit = false;
     float scale;
 };
-cudaError_t launch_decode_int4(const DecodeInt4Launch &l, cudaStream_t stream);
+// maps: K and V codes, K and V parameters, with boxes of min(page_size, kInt4Block) positions of
+// int4_group_heads(kv_heads) kv heads, which land as [head][position][bytes].
+cudaError_t launch_decode_int4(const DecodeInt4Launch &l, const CUtensorMap (&maps)[4],
+                               cudaStream_t stream);
 cudaError_t read_and_clear_decode_int4_errors(uint32_t *flags);
 
 // kvc_decode_weights: the decode of `l` (its partials for every split, also when there is one), its

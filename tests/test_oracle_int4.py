@@ -134,12 +134,12 @@ def test_store_and_load_int4_refusals():
 
 def test_decode_int4_plan():
     pool = PoolDesc(100, 16, 8, 128)
-    assert kvc.kvc_decode_int4_plan(64, 32, pool, 4096, 1) == (64 * 8, 32, 0)
+    assert kvc.kvc_decode_int4_plan(64, 32, pool, 4096, 1) == (64 * 8, 64, 0)
     warps, block, ws = kvc.kvc_decode_int4_plan(64, 32, pool, 4096, 0)
-    assert block == 32 and warps % 8 == 0 and 0 < warps <= 64 * 128 * 8
+    assert block == 64 and warps % 8 == 0 and 0 < warps <= 64 * 128 * 8
     slots = 8 * (64 + warps // 8)
     assert ws >= slots * 4 * 129 * 4 + 64 * 8 * 8
-    assert kvc.kvc_decode_int4_plan(1, 32, pool, 33, 0)[0] == 2 * 8   # one run per block
+    assert kvc.kvc_decode_int4_plan(1, 32, pool, 65, 0)[0] == 2 * 8   # one run per block
     assert kvc.kvc_decode_int4_plan(0, 32, pool, 0, 0)[0] == 8
 
 
