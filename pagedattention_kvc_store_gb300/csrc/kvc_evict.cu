@@ -116,6 +116,12 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     const cg::cluster_group cluster = cg::this_cluster();
     const int cta = static_cast<int>(cluster.block_rank());
     const int ctas = static_cast<int>(cluster.num_blocks());
+    auto cluster_sync = [&] {   // a cluster barrier costs more, even for one CTA
+        if (ctas == 1)
+            __syncthreads();
+        else
+            cluster.sync();
+    };
     const int unit = blockIdx.x / ctas;
     const int kvh = unit % a.kv_heads;
     const int s = unit / a.kv_heads;
@@ -261,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
             const uint4 x = h[0], y = h[1];
             sh.coarse[threadIdx.x] = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
         }
-        cluster.sync();
+        cluster_sync();
         uint32_t mine = 0;
 #pragma unroll
         for (int c = 0; c < kMaxCtas; ++c)
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
         }
         if (threadIdx.x == 0)
             sh.equal_here = all;
-        cluster.sync();
+        cluster_sync();
         for (int c = 0; c < cta; ++c)
             eq_first += *cluster.map_shared_rank(&sh.equal_here, c);
     }
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
             sh.tails = tails;
         }
     }
-    cluster.sync();
+    cluster_sync();
     for (int c = 0; c < ctas; ++c) {
         const uint32_t g = *cluster.map_shared_rank(&sh.gaps, c);
         const uint32_t t = *cluster.map_shared_rank(&sh.tails, c);
@@ -460,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     for (long long i = static_cast<long long>(N) + cta * kThreads + threadIdx.x; i < a.stride;
          i += ctas * kThreads)
         p_out[i] = free_pos + static_cast<int32_t>(i);
-    cluster.sync();   // the others' counts are read: shared memory may go
+    cluster_sync();   // the others' counts are read: shared memory may go
 }
 
 // Carries out the listed moves, K and V, weight and position: CTA = (chunk of kMovesPerCta moves, unit),

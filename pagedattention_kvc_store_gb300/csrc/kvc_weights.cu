@@ -65,8 +65,9 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const FinishArgs
             merge_row<D>(a.out, a.out_f32, a.part_o, a.part_lse, row, a.n_split, nullptr);
         return;
     }
-    // block -> (tile of positions, kv head, sequence), tile fastest
-    const int b = blockIdx.x - f.merge_blocks;
+    // block -> (tile of positions, kv head, sequence), tile fastest, from the last: what the decode
+    // wrote last is still in L2
+    const int b = gridDim.x - 1 - blockIdx.x;
     const int tile = b % f.tiles;
     const int unit = b / f.tiles;
     const int kvh = unit % a.kv_heads;
