@@ -48,6 +48,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kWarpSlots = 128;   // slots of one step of a warp, four consecutive ones a lane
+constexpr int kListed = 1024;     // keys listed for the last pass; with more it goes over all
 constexpr int kAhead = 4;         // steps of global loads that a thread has in flight
 constexpr int kMaxCtas = 8;       // of a cluster
 constexpr uint32_t kNewest = 0xFFFFFFFFu;
@@ -80,7 +81,11 @@ struct Args {
 
 struct Shared {
     uint32_t hist[2][kBins];
-    uint32_t coarse[kThreads];   // sums of the current histogram's bins, eight each, top first
+    uint32_t listed[kListed];    // keys that share the first digit, for the last pass
+    uint32_t list_size;
+    // Sums of the histogram's bins, eight each, top first.  The passes alternate: a CTA may be in the
+    // next pass while another one still reads this pass's sums, but not in the next but one.
+    uint32_t coarse[2][kThreads];
     uint32_t warp_sum[2][kWarps];
     uint32_t equal_here, gaps, tails;   // this CTA's, read by the cluster
     uint32_t digit, above, equal;       // the digit found, the keys above it and those in it
@@ -131,6 +136,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
 
     for (int i = threadIdx.x; i < 2 * kBins; i += kThreads)
         sh.hist[0][i] = 0;
+    if (threadIdx.x == 0)
+        sh.list_size = 0;
     const int raw = a.context_lens[s];
     const long long cap = min(static_cast<long long>(a.bt_stride) << a.log2_page,
                               static_cast<long long>(min(a.max_ctx, a.stride)));
@@ -248,13 +255,25 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
             const int skip = pass == 1 ? 21 : 10;    // bits below the digits found
             const int shift = pass == 1 ? 10 : 0;
             const uint32_t mask = pass == 1 ? 0x7FFu : 0x3FFu;
-            for (int i = lo + 4 * lane; i < hi; i += kWarpSlots) {
-                const uint4 k = keys_at(i);
-                const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
+            if (pass == 2 && sh.list_size <= kListed) {
+                for (int i = threadIdx.x; i < static_cast<int>(sh.list_size); i += kThreads)
+                    if ((sh.listed[i] >> skip) == prefix)
+                        atomicAdd(&hist[sh.listed[i] & mask], 1u);
+            } else {
+                for (int i = lo + 4 * lane; i < hi; i += kWarpSlots) {
+                    const uint4 k = keys_at(i);
+                    const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (ks[e] != 0 && (ks[e] >> skip) == prefix)
-                        atomicAdd(&hist[(ks[e] >> shift) & mask], 1u);
+                    for (int e = 0; e < 4; ++e)
+                        if (ks[e] != 0 && (ks[e] >> skip) == prefix) {
+                            atomicAdd(&hist[(ks[e] >> shift) & mask], 1u);
+                            if (pass == 1) {
+                                const uint32_t at = atomicAdd(&sh.list_size, 1u);
+                                if (at < kListed)
+                                    sh.listed[at] = ks[e];
+                            }
+                        }
+                }
             }
         }
         // Every CTA gives away the sums of eight bins each, top first; only the thread whose eight
@@ -265,14 +284,14 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
         {
             const uint4 *h = reinterpret_cast<const uint4 *>(&hist[top_bin - 7]);
             const uint4 x = h[0], y = h[1];
-            sh.coarse[threadIdx.x] = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
+            sh.coarse[pass & 1][threadIdx.x] = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
         }
         cluster_sync();
         uint32_t mine = 0;
 #pragma unroll
         for (int c = 0; c < kMaxCtas; ++c)
             if (c < ctas)
-                mine += *cluster.map_shared_rank(&sh.coarse[threadIdx.x], c);
+                mine += *cluster.map_shared_rank(&sh.coarse[pass & 1][threadIdx.x], c);
         const uint32_t incl = warp_scan(mine, lane);
         if (lane == 31)
             sh.warp_sum[0][warp] = incl;
@@ -424,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     // rows move out of become free with the move.
     const int32_t free_pos = static_cast<int32_t>(static_cast<long long>(last) + 1 - n);
     if (cta == 0 && threadIdx.x == 0)
-        a.counts[unit] = make_int2(static_cast<int>(moves), free_pos);
+        a.counts[unit] = make_int2(min(static_cast<int>(moves), a.list_cap), free_pos);
     {
         uint32_t rank = eq_first;
         for (int i0 = lo; i0 < hi; i0 += kWarpSlots) {
@@ -434,12 +453,14 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
             const uint32_t both = __popc(g) | (__popc(t) << 16);
             const uint32_t incl = warp_scan(both, lane);
             const uint32_t at = incl - both, all = __shfl_sync(0xffffffffu, incl, 31);
-            int32_t *d = dst_list + gap_at + (at & 0xFFFFu);
-            int32_t *f = src_list + tail_at + (at >> 16);
-            for (; g; g &= g - 1)
-                *d++ = i + __ffs(g) - 1;
-            for (; t; t &= t - 1)
-                *f++ = i + __ffs(t) - 1;
+            // (both ranks are below list_cap unless the weights changed under the launch)
+            uint32_t d = gap_at + (at & 0xFFFFu), f = tail_at + (at >> 16);
+            for (; g; g &= g - 1, ++d)
+                if (d < static_cast<uint32_t>(a.list_cap))
+                    dst_list[d] = i + __ffs(g) - 1;
+            for (; t; t &= t - 1, ++f)
+                if (f < static_cast<uint32_t>(a.list_cap))
+                    src_list[f] = i + __ffs(t) - 1;
             gap_at += all & 0xFFFFu;
             tail_at += all >> 16;
             // What lies below n stays where it is (the moves write over the gaps), and what lies behind
@@ -493,9 +514,14 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Args a, int un
     const int32_t *dst_list = a.lists + static_cast<size_t>(unit) * 2 * a.list_cap;
     const int32_t *bt = a.block_table + static_cast<size_t>(s) * a.bt_stride;
     long long from = -1, to = -1;   // 16-byte chunks; below 0: no copy
+    int dst = -1, src = -1;
     if (lane < n) {
-        const int dst = __ldcg(dst_list + j0 + lane);
-        const int src = __ldcg(dst_list + a.list_cap + j0 + lane);
+        dst = __ldcg(dst_list + j0 + lane);
+        src = __ldcg(dst_list + a.list_cap + j0 + lane);
+    }
+    // (an entry that no slot was written to: the weights changed under the selection)
+    if (static_cast<uint32_t>(dst) < static_cast<uint32_t>(a.max_ctx) &&
+        static_cast<uint32_t>(src) < static_cast<uint32_t>(a.max_ctx)) {
         const int dp = bt[dst >> a.log2_page], sp = bt[src >> a.log2_page];
         if (dp >= 0 && dp < a.num_pages && sp >= 0 && sp < a.num_pages) {
             const int mask = (1 << a.log2_page) - 1;

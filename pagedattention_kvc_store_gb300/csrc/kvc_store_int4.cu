@@ -20,8 +20,8 @@
 // go two to a word, the arithmetic two to an instruction (f32x2), and token and head come from a
 // multiplication by a reciprocal that the host makes.  The codes need a correctly rounded quotient.
 // A division per value would be about 12 instructions; the product with the approximate
-// reciprocal is off by less than 1e-5 of a step, so only a lane that holds a quotient within 1e-4
-// of a tie (or a scale too small for the reciprocal) takes the divisions.
+// reciprocal is off by less than 15 (2^-23 + 2^-24) = 2.7e-6 of a step, so only a lane that holds a
+// quotient within 1e-5 of a tie (or a scale too small for the reciprocal) takes the divisions.
 #include <math.h>
 
 #include <algorithm>
@@ -124,7 +124,7 @@ __device__ __forceinline__ uint2 quantise16(const uint32_t (&x)[8], uint32_t &pa
         f2_unpack(f2_sub(q, r2[i]), d0, d1);
         off = fmax3(off, fabsf(d0), fabsf(d1));
     }
-    if (!(off < 0.4999f)) {
+    if (!(off < 0.49999f)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float a0 = fmaf(__uint_as_float(x[i] << 16), 0.5f, -lo_half);

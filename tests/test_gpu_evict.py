@@ -292,6 +292,40 @@ def test_evict_clusters(S, n, budget):
     run_evict(case, budget, 1, w, pos, in_place=True)
 
 
+def test_evict_clusters_in_quick_succession():
+    """Rows shared by 8 CTAs, 300 calls with nothing waited for in between: CTAs of a cluster drift
+    apart by whole passes, and every call gives the same bits."""
+    S, H, L, budget = 4, 2, 40000, 9000
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    w = torch.exp(torch.randn(S, H, L, generator=gen, device="cuda"))
+    pos = torch.arange(L, dtype=torch.int32, device="cuda").repeat(S, H, 1)
+    pages = S * (L // 64)
+    k = torch.randn(pages, 64, H, 64, generator=gen, device="cuda").bfloat16()
+    v = k.clone()
+    table = torch.randperm(pages, generator=gen, device="cuda").int().view(S, -1)
+    ctx = torch.tensor([L, L - 777, L // 2 + 1, L], dtype=torch.int32, device="cuda")
+    pool = kvc.pool_desc(k)
+    n = kvc.kvc_evict_plan(S, pool, L, budget)
+    outs = []
+    for i in range(300):
+        kk, vv = (k.clone(), v.clone()) if i in (0, 299) else (k, v)
+        o = [torch.zeros_like(w), torch.zeros_like(pos),
+             torch.zeros(S, dtype=torch.int32, device="cuda")]
+        work = torch.empty(n, dtype=torch.uint8, device="cuda")
+        if i == 299:
+            kk, vv = first_k.clone(), first_v.clone()
+        kvc.kvc_evict(kk, vv, *o, w, pos, table, ctx, L, budget, 100, workspace=work)
+        if i == 0:
+            first_k, first_v = kk, vv
+        outs.append(o)
+    torch.cuda.synchronize()
+    assert torch.equal(kk, first_k) and torch.equal(vv, first_v)   # moving again moves the same
+    for o in outs:
+        assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+    assert kvc.kvc_device_errors() == 0
+
+
 def test_evict_more_slots_than_the_cache_of_keys():
     """A row of 400,000 slots over 8 CTAs: more than they keep in shared memory."""
     n, P = 400000, 64
