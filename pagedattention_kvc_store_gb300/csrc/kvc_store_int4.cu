@@ -18,10 +18,10 @@
 // Both kernels are bound by HBM (328 bytes a vector at D = 128), but only if they spend few instructions:
 // a lane takes 16 values of K and the same of V at a time (four lanes a group), minima and maxima
 // go two to a word, the arithmetic two to an instruction (f32x2), and token and head come from a
-// multiplication by a reciprocal that the host makes.  The codes need a correctly rounded quotient.
-// A division per value would be about 12 instructions; the product with the approximate
-// reciprocal is off by less than 15 (2^-23 + 2^-24) = 2.7e-6 of a step, so only a lane that holds a
-// quotient within 1e-5 of a tie (or a scale too small for the reciprocal) takes the divisions.
+// multiplication by a reciprocal that the host makes.  The codes need a correctly rounded quotient;
+// a division per value would be about 12 instructions, and a cheaper check that falls back to it
+// falls back all the time, because bf16 values lie on exact ties often (78 us for the 50,000 tokens
+// that take 48 us with the corrected product below).
 #include <math.h>
 
 #include <algorithm>
@@ -107,24 +107,30 @@ __device__ __forceinline__ uint2 quantise16(const uint32_t (&x)[8], uint32_t &pa
     param = static_cast<uint32_t>(__bfloat16_as_ushort(scale16)) | (m << 16);
     if (!(scale_half > 0.0f))
         return make_uint2(0u, 0u);
-    // a = x / 2 - lo / 2 (one rounding), q = a / (scale / 2), r the nearest integer: 1.5 2^23 added
-    // and taken away leaves it, ties to even.  scale is at most 2^-8 of itself off, so q is below
-    // 15.06 and r needs no clamp here.
-    const uint64_t half2 = f2_pack(0.5f, 0.5f), nlo2 = f2_pack(-lo_half, -lo_half);
-    const float inv = approx_rcp(scale_half);
-    const uint64_t inv2 = f2_pack(inv, inv), magic2 = f2_pack(12582912.0f, 12582912.0f);
+    // a = x / 2 - lo / 2 (one rounding), b = scale / 2, and q the quotient a / b as a division rounds
+    // it: the product with the reciprocal, corrected by its remainder a - q b (a fused operation
+    // gives it to 2^-24 of itself), is off by 2^-44 before its last rounding.  That rounds as the
+    // exact quotient does wherever it matters, next to a half k + 1/2: (k + 1/2) b has 13 bits, so
+    // an a that is not equal to it is at least 2^-24 away, and a quotient of either kind stays
+    // 2^-37 off the point where the rounding would turn.  Equality gives k + 1/2 itself.  r is then
+    // the nearest integer: 1.5 2^23 added and taken away, ties to even.  scale is at most 2^-8 of
+    // itself off, so r needs no clamp.
     uint64_t r2[8];
-    float off = scale_half >= 1e-30f ? 0.0f : 1.0f;   // a tiny scale: always divide
+    if (scale_half >= 1e-30f) {
+        const float inv = approx_rcp(scale_half);
+        const uint64_t half2 = f2_pack(0.5f, 0.5f), nlo2 = f2_pack(-lo_half, -lo_half);
+        const uint64_t inv2 = f2_pack(inv, inv), nb2 = f2_pack(-scale_half, -scale_half);
+        const uint64_t magic2 = f2_pack(12582912.0f, 12582912.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint64_t v = f2_pack(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
-        const uint64_t q = f2_mul(f2_fma(v, half2, nlo2), inv2);
-        r2[i] = f2_sub(f2_add(q, magic2), magic2);
-        float d0, d1;
-        f2_unpack(f2_sub(q, r2[i]), d0, d1);
-        off = fmax3(off, fabsf(d0), fabsf(d1));
-    }
-    if (!(off < 0.49999f)) {
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t v =
+                f2_pack(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
+            const uint64_t a = f2_fma(v, half2, nlo2);
+            const uint64_t q = f2_mul(a, inv2);
+            const uint64_t q1 = f2_fma(f2_fma(q, nb2, a), inv2, q);
+            r2[i] = f2_sub(f2_add(q1, magic2), magic2);
+        }
+    } else {   // near and among the subnormals the products above would lose bits, and scale is coarse
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float a0 = fmaf(__uint_as_float(x[i] << 16), 0.5f, -lo_half);
