@@ -237,6 +237,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                              const __grid_constant__ CUtensorMap tmap_kp,
                              const __grid_constant__ CUtensorMap tmap_vp, const Args a)
 {
+    if (threadIdx.x == kWarps * 32) {   // before the wait: nothing writes these
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
+        prefetch_tensormap(&tmap_kp);
+        prefetch_tensormap(&tmap_vp);
+    }
     pdl_wait();
     pdl_trigger();
     using Geom = I4Geom<D>;
@@ -886,9 +892,11 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) merge_int4_kernel(const
     pdl_trigger();
     constexpr int V = D / 32;
     constexpr int kRows = W == 1 ? 4 : 1;
+    constexpr int kPre = 4;
     __shared__ float part[W == 1 ? 1 : W][D + 1];
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
+    const int w0 = W == 1 ? 0 : warp;   // this warp's first piece
     const int row = blockIdx.x * kRows + (W == 1 ? warp : 0);
     if (row >= a.num_seqs * a.q_heads)
         return;
@@ -910,16 +918,45 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) merge_int4_kernel(const
         const float *lse = a.part_lse + first;
         const float *po = a.part_o + first * D + lane * V;
         const size_t po_step = static_cast<size_t>(G) * D;
-        float M = -INFINITY;
-        for (int j = lane; j < count; j += 32)
+        // one round trip: every piece's lse (lane j holds pieces j, j + 32, ...) and the rows of
+        // this warp's first pieces
+        float pre[kPre][V];
+#pragma unroll
+        for (int u = 0; u < kPre; ++u) {
+            const int j = w0 + u * W;
+            if (j < count) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    pre[u][v] = __ldcg(po + static_cast<size_t>(j) * po_step + v);
+            }
+        }
+        const float mine = lane < count ? __ldcg(lse + static_cast<size_t>(lane) * G) : -INFINITY;
+        float M = mine;
+        for (int j = lane + 32; j < count; j += 32)
             M = fmaxf(M, __ldcg(lse + static_cast<size_t>(j) * G));
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
         const float mu = M == -INFINITY ? 0.0f : M;
+        auto weight = [&](int j) {
+            const float l = j < 32 ? __shfl_sync(0xffffffffu, mine, j)
+                                   : __ldcg(lse + static_cast<size_t>(j) * G);
+            return fast_exp2((l - mu) * kLog2e);
+        };
+#pragma unroll
+        for (int u = 0; u < kPre; ++u) {
+            const int j = w0 + u * W;
+            if (j < count) {
+                const float w = weight(j);
+                sum += w;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    acc[v] = fmaf(w, pre[u][v], acc[v]);
+            }
+        }
 #pragma unroll 4
-        for (int j = W == 1 ? 0 : warp; j < count; j += W) {
-            const float w = fast_exp2((__ldcg(lse + static_cast<size_t>(j) * G) - mu) * kLog2e);
+        for (int j = w0 + kPre * W; j < count; j += W) {
+            const float w = weight(j);
             sum += w;
             const float *src = po + static_cast<size_t>(j) * po_step;
 #pragma unroll
@@ -991,7 +1028,7 @@ cudaError_t launch_t(const DecodeInt4Launch &l, const CUtensorMap (&maps)[4], cu
     if (err != cudaSuccess || l.per_unit)
         return err;
     const int rows = l.num_seqs * l.q_heads;
-    if (l.runs > 8LL * l.num_seqs)
+    if (l.runs > 4LL * l.num_seqs)   // more than some four pieces a unit: 8 warps a row
         return launch_pdl(merge_int4_kernel<D, 8>, dim3(rows), dim3(256), 0, stream, a);
     return launch_pdl(merge_int4_kernel<D, 1>, dim3((rows + 3) / 4), dim3(128), 0, stream, a);
 }
