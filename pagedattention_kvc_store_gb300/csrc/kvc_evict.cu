@@ -22,10 +22,10 @@
 // nothing depends on the order of atomics (the histograms only count).  The kernel leaves the
 // moves as two lists.
 //
-// Moves (move_kernel).  One launch over all lists, 128 moves a CTA: rows differ in how much they
+// Moves (move_kernel).  One launch over all lists, 64 moves a CTA: rows differ in how much they
 // move (a batch's longest several times its average), so the copies are spread over the SMs
-// apart from the selection.  A warp reads 32 moves and their pages at once and then keeps 8 rows
-// in flight.
+// apart from the selection.  A warp reads 16 moves and their pages at once and then keeps 4 rows
+// in flight (8 to 32 moves and 4 or 8 rows are within 3%, 16 rows or 512 threads 20% slower).
 //
 // Bound: the moved rows (4 D bytes read and written each) by HBM when there are many, else the chain of
 // barriers; the selection reads 8 and writes 8 bytes a slot.
@@ -54,7 +54,8 @@ constexpr int kMaxCtas = 8;       // of a cluster
 constexpr uint32_t kNewest = 0xFFFFFFFFu;
 constexpr long long kSmemPerSm = 228 * 1024;
 constexpr int kMoveThreads = 128;
-constexpr int kMovesPerCta = kMoveThreads;
+constexpr int kWarpMoves = 16;    // moves of one warp
+constexpr int kMovesPerCta = kMoveThreads / 32 * kWarpMoves;
 
 struct Args {
     uint4 *k_pool, *v_pool;
@@ -200,14 +201,41 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
         k.w = i + 3 < hi ? key_of(w_in[i + 3], p_in[i + 3]) : 0u;
         return k;
     };
-    auto keys_at = [&](int i) -> uint4 {
-        const int c = i - cta_lo;
-        return c < a.cached ? *reinterpret_cast<const uint4 *>(keys + c) : make_keys(i);
+    // Calls f(i, keys of slots i .. i + 3) for the warp's slots in order, i = 4 lane past each step's
+    // first slot; all lanes go together, with keys 0 from hi on.  The slots below `from` come from
+    // shared memory, the others from memory, kAhead steps' loads in flight.
+    auto sweep = [&](int from, auto &&f) {
+        int i0 = lo;
+        for (; i0 < hi && i0 - cta_lo < from; i0 += kWarpSlots) {
+            const int i = i0 + 4 * lane;
+            f(i, i < hi ? *reinterpret_cast<const uint4 *>(keys + (i - cta_lo))
+                        : make_uint4(0u, 0u, 0u, 0u));
+        }
+        if (a.vec) {
+            for (; i0 + kAhead * kWarpSlots <= hi; i0 += kAhead * kWarpSlots) {
+                float4 w[kAhead];
+                int4 p[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    w[u] = *reinterpret_cast<const float4 *>(w_in + i0 + u * kWarpSlots + 4 * lane);
+                    p[u] = *reinterpret_cast<const int4 *>(p_in + i0 + u * kWarpSlots + 4 * lane);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    f(i0 + u * kWarpSlots + 4 * lane,
+                      make_uint4(key_of(w[u].x, p[u].x), key_of(w[u].y, p[u].y),
+                                 key_of(w[u].z, p[u].z), key_of(w[u].w, p[u].w)));
+            }
+        }
+        for (; i0 < hi; i0 += kWarpSlots) {
+            const int i = i0 + 4 * lane;
+            f(i, i < hi ? make_keys(i) : make_uint4(0u, 0u, 0u, 0u));
+        }
     };
 
     // ---- the n-th largest key, and how many equal to it are kept ----
     __syncthreads();   // the histograms are zero
-    auto tally = [&](const uint4 k, int i) {   // the whole warp
+    sweep(0, [&](int i, const uint4 k) {
         if (i < hi && i - cta_lo < a.cached)
             *reinterpret_cast<uint4 *>(keys + (i - cta_lo)) = k;
         const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
@@ -223,28 +251,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
                 if (ks[e] != 0)
                     atomicAdd(&sh.hist[0][ks[e] >> 21], 1u);
         }
-    };
-    int i0 = lo;
-    if (a.vec) {   // kAhead steps' loads in flight
-        for (; i0 + kAhead * kWarpSlots <= hi; i0 += kAhead * kWarpSlots) {
-            float4 w[kAhead];
-            int4 p[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                w[u] = *reinterpret_cast<const float4 *>(w_in + i0 + u * kWarpSlots + 4 * lane);
-                p[u] = *reinterpret_cast<const int4 *>(p_in + i0 + u * kWarpSlots + 4 * lane);
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                tally(make_uint4(key_of(w[u].x, p[u].x), key_of(w[u].y, p[u].y),
-                                 key_of(w[u].z, p[u].z), key_of(w[u].w, p[u].w)),
-                      i0 + u * kWarpSlots + 4 * lane);
-        }
-    }
-    for (; i0 < hi; i0 += kWarpSlots) {
-        const int i = i0 + 4 * lane;
-        tally(i < hi ? make_keys(i) : make_uint4(0u, 0u, 0u, 0u), i);
-    }
+    });
     uint32_t prefix = 0;   // the digits found so far
     uint32_t need = n;     // keys still wanted among those that begin with them
     uint32_t equal = 0;    // how many these are
@@ -260,8 +267,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
                     if ((sh.listed[i] >> skip) == prefix)
                         atomicAdd(&hist[sh.listed[i] & mask], 1u);
             } else {
-                for (int i = lo + 4 * lane; i < hi; i += kWarpSlots) {
-                    const uint4 k = keys_at(i);
+                sweep(a.cached, [&](int, const uint4 k) {
                     const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
                                     sh.listed[at] = ks[e];
                             }
                         }
-                }
+                });
             }
         }
         // Every CTA gives away the sums of eight bins each, top first; only the thread whose eight
@@ -343,11 +349,10 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     uint32_t eq_first = 0;   // equal keys before this warp's
     if (ties) {
         uint32_t here = 0;
-        for (int i = lo + 4 * lane; i < hi; i += kWarpSlots) {
-            const uint4 k = keys_at(i);
+        sweep(a.cached, [&](int, const uint4 k) {
             here += (k.x == threshold) + (k.y == threshold) + (k.z == threshold) +
                     (k.w == threshold);
-        }
+        });
         here = __reduce_add_sync(0xffffffffu, here);
         if (lane == 0)
             sh.warp_sum[1][warp] = here;
@@ -364,9 +369,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
         for (int c = 0; c < cta; ++c)
             eq_first += *cluster.map_shared_rank(&sh.equal_here, c);
     }
-    // The kept ones of slots i .. i + 3 (i = i0 + 4 lane) as four bits; the warp goes together.
-    auto kept = [&](int i, uint32_t &eq_rank) -> uint32_t {
-        const uint4 k = i < hi ? keys_at(i) : make_uint4(0u, 0u, 0u, 0u);
+    // The kept ones of four slots as four bits; the warp goes together.
+    auto kept = [&](const uint4 k, uint32_t &eq_rank) -> uint32_t {
         const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
         uint32_t m = 0;
         if (!ties) {
@@ -399,12 +403,11 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     };
     {
         uint32_t rank = eq_first, gaps = 0, tails = 0;
-        for (int i0 = lo; i0 < hi; i0 += kWarpSlots) {
-            const int i = i0 + 4 * lane;
-            const uint32_t m = kept(i, rank), in = below_n(i);
+        sweep(a.cached, [&](int i, const uint4 k) {
+            const uint32_t m = kept(k, rank), in = below_n(i);
             gaps += __popc(in & ~m);
             tails += __popc(m & ~in);
-        }
+        });
         gaps = __reduce_add_sync(0xffffffffu, gaps);
         tails = __reduce_add_sync(0xffffffffu, tails);
         __syncthreads();   // warp_sum is read
@@ -446,9 +449,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
         a.counts[unit] = make_int2(min(static_cast<int>(moves), a.list_cap), free_pos);
     {
         uint32_t rank = eq_first;
-        for (int i0 = lo; i0 < hi; i0 += kWarpSlots) {
-            const int i = i0 + 4 * lane;
-            const uint32_t m = kept(i, rank), in = below_n(i);
+        sweep(a.cached, [&](int i, const uint4 k) {
+            const uint32_t m = kept(k, rank), in = below_n(i);
             uint32_t g = in & ~m, t = m & ~in;
             const uint32_t both = __popc(g) | (__popc(t) << 16);
             const uint32_t incl = warp_scan(both, lane);
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
                     }
                 }
             }
-        }
+        });
     }
     for (long long i = static_cast<long long>(N) + cta * kThreads + threadIdx.x; i < a.stride;
          i += ctas * kThreads)
@@ -500,13 +502,13 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Args a, int un
     constexpr int kVec = D / 8;                 // 16-byte chunks of a vector
     constexpr int kMoveLanes = 2 * kVec;        // K and V of one move
     constexpr int kAtOnce = 32 / kMoveLanes;    // moves that a warp copies with one load
-    constexpr int kFly = 8;                     // loads in flight
+    constexpr int kFly = 4;                     // loads in flight
     const int unit = blockIdx.x % units;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int j0 = (blockIdx.x / units) * kMovesPerCta + warp * 32;
+    const int j0 = (blockIdx.x / units) * kMovesPerCta + warp * kWarpMoves;
     const int2 count = __ldcg(a.counts + unit);
-    const int n = min(32, count.x - j0);
+    const int n = min(kWarpMoves, count.x - j0);
     if (n <= 0)
         return;
     const int kvh = unit % a.kv_heads;
