@@ -531,10 +531,10 @@ kvc_status kvc_load_int4(void *k_out, void *v_out, int32_t out_dtype, const void
 /*
  * kvc_decode_int4 -- kvc_decode over 4-bit pages (same arguments and outputs, page sizes, layouts
  * and groups; out, q, block_table and context_lens may be pinned host memory).  Work is cut as in
- * kvc_decode_int8, with one warp per run and kv head: num_splits 0 = one wave of
- * resident warps (the default), 1 = one warp per (sequence, kv head), no workspace and no
- * merge, n > 1 = n runs per sequence.  kvc_decode_int4_plan: splits_out = the number of warps,
- * chunk_out = 64, workspace_bytes_out = the workspace that the call needs (0 for num_splits = 1).
+ * kvc_decode_int8, with one warp per run and kv head.  num_splits: 1 = one run per sequence, no
+ * workspace and no merge; n > 1 = n runs per sequence; 0 = one wave of resident warps, or one run
+ * per sequence where max_ctx is at most 128.  kvc_decode_int4_plan: splits_out = the number of warps,
+ * chunk_out = 64 (the block), workspace_bytes_out = the workspace that the call needs (0 without a merge).
  * The workspace belongs to one call at a time: calls that may overlap (two streams, two captured
  * graphs) need one each.  A query row enters the products as fp16 times a power of two of its own
  * (exact for elements down to 2^-23 of its largest), a probability times a value scale as fp16;

@@ -177,7 +177,10 @@ Int8Plan make_int8_plan(int32_t num_seqs, int32_t q_heads, const kvc_pool_desc &
 }
 
 // 4-bit decode plan, as the INT8 one, with 64-position blocks and one warp per run and kv head: by
-// default as many runs as one wave of the kernel's CTAs (one per SM) holds.
+// default as many runs as one wave of the kernel's CTAs (one per SM) holds, and for contexts of at
+// most two blocks one run per sequence, which needs no merge: 4 sequences of up to 128 positions
+// take 7.8 us against 9.3 (1,000: 15.8 against 18.1); at 256 positions it is 10.9 against 9.5.
+constexpr int kInt4WholeCtx = 2 * kvc::kInt4Block;
 
 struct Int4Plan {
     int runs;            // per kv head
@@ -192,7 +195,7 @@ kvc_status make_int4_plan(int32_t num_seqs, int32_t q_heads, const kvc_pool_desc
     const int64_t seqs = num_seqs > 0 ? num_seqs : 1;
     if (seqs * pool.kv_heads > (int64_t(1) << 28))
         return fail(KVC_ERR_UNSUPPORTED, "num_seqs * kv_heads must be at most 2^28");
-    if (requested == 1) {
+    if (requested == 1 || (requested <= 0 && max_ctx <= kInt4WholeCtx)) {
         p.per_unit = true;
         p.runs = static_cast<int>(seqs);
         *out = p;

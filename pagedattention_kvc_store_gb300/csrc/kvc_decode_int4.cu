@@ -911,7 +911,9 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) merge_int4_kernel(const
         acc[v] = 0.0f;
     if (ctx > 0) {
         const int2 info = __ldcg(a.unit_info + static_cast<size_t>(s) * a.kv_heads + kvh);
-        const int count = info.y;
+        // (a sequence whose context changes while the decode runs may have left no such slots)
+        const int count =
+            info.x >= 0 && info.y <= a.kv_heads * (a.num_seqs + a.runs) - info.x ? info.y : 0;
         if (count <= 1)
             return;
         const size_t first = static_cast<size_t>(info.x) * G + (h - kvh * G);

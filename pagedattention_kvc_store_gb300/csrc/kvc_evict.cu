@@ -55,6 +55,10 @@ constexpr uint32_t kNewest = 0xFFFFFFFFu;
 constexpr long long kSmemPerSm = 228 * 1024;
 constexpr int kMoveThreads = 128;
 constexpr int kWarpMoves = 16;    // moves of one warp
+#ifndef INL
+#define INL 256
+#endif
+constexpr int kInlineMoves = INL;
 constexpr int kMovesPerCta = kMoveThreads / 32 * kWarpMoves;
 
 struct Args {
@@ -77,6 +81,7 @@ struct Args {
     int kv_heads, log2_page, num_pages, hnd;
     int cached;          // keys that fit a CTA's shared memory
     int vec;             // rows of weights and positions start on 16 bytes
+    int inline_moves;    // one CTA per row, few moves: no second launch
     uint32_t *err;
 };
 
@@ -113,6 +118,76 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane)
     return x;
 }
 
+// Carries out moves j0 .. j0 + n - 1 (n at most kWarpMoves) of a unit's lists, K and V, weight and
+// position, by one warp.
+template <int D>
+__device__ __forceinline__ void move_rows(const Args &a, int unit, int j0, int n, int free_pos)
+{
+    const int lane = threadIdx.x & 31;
+    constexpr int kVec = D / 8;                 // 16-byte chunks of a vector
+    constexpr int kMoveLanes = 2 * kVec;        // K and V of one move
+    constexpr int kAtOnce = 32 / kMoveLanes;    // moves that a warp copies with one load
+    constexpr int kFly = 4;                     // loads in flight
+    const int kvh = unit % a.kv_heads;
+    const int s = unit / a.kv_heads;
+    const int32_t *dst_list = a.lists + static_cast<size_t>(unit) * 2 * a.list_cap;
+    const int32_t *bt = a.block_table + static_cast<size_t>(s) * a.bt_stride;
+    long long from = -1, to = -1;   // 16-byte chunks; below 0: no copy
+    int dst = -1, src = -1;
+    if (lane < n) {
+        dst = __ldcg(dst_list + j0 + lane);
+        src = __ldcg(dst_list + a.list_cap + j0 + lane);
+    }
+    // (an entry that no slot was written to: the weights changed under the selection)
+    if (static_cast<uint32_t>(dst) < static_cast<uint32_t>(a.max_ctx) &&
+        static_cast<uint32_t>(src) < static_cast<uint32_t>(a.max_ctx)) {
+        const int dp = bt[dst >> a.log2_page], sp = bt[src >> a.log2_page];
+        if (dp >= 0 && dp < a.num_pages && sp >= 0 && sp < a.num_pages) {
+            const int mask = (1 << a.log2_page) - 1;
+            auto place = [&](int page, int off) -> long long {
+                const long long vec =
+                    a.hnd ? ((static_cast<long long>(page) * a.kv_heads + kvh) << a.log2_page) + off
+                          : ((static_cast<long long>(page) << a.log2_page) + off) * a.kv_heads + kvh;
+                return vec * kVec;
+            };
+            from = place(sp, src & mask);
+            to = place(dp, dst & mask);
+        } else {
+            atomicOr(a.err ? a.err : &g_evict_errors, kErrPageRange);
+        }
+        const int row = a.rows ? a.rows[s] : s;
+        const size_t base = (static_cast<size_t>(row) * a.kv_heads + kvh) * a.stride;
+        const float w = a.weights[base + src];
+        const int32_t p = a.positions[base + src];
+        a.weights_out[base + dst] = w;
+        a.positions_out[base + dst] = p;
+        a.weights_out[base + src] = 0.0f;
+        a.positions_out[base + src] = free_pos + src;
+    }
+    const int sub = lane / kMoveLanes;
+    const int in_move = lane % kMoveLanes;
+    uint4 *pool = (in_move < kVec ? a.k_pool : a.v_pool) + in_move % kVec;
+    for (int u0 = 0; u0 < n; u0 += kFly * kAtOnce) {
+        uint4 x[kFly];
+        long long dst[kFly];
+#pragma unroll
+        for (int u = 0; u < kFly; ++u) {
+            const int m = u0 + u * kAtOnce + sub;   // below 64; past n the lane's places are -1
+            const long long f = __shfl_sync(0xffffffffu, from, m & 31);
+            dst[u] = __shfl_sync(0xffffffffu, to, m & 31);
+            if (m >= n)
+                dst[u] = -1;
+            if (dst[u] >= 0)
+                x[u] = __ldcg(pool + f);
+        }
+#pragma unroll
+        for (int u = 0; u < kFly; ++u)
+            if (dst[u] >= 0)
+                pool[dst[u]] = x[u];
+    }
+}
+
+template <int D>
 __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
 {
     pdl_wait();
@@ -489,85 +564,26 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     for (long long i = static_cast<long long>(N) + cta * kThreads + threadIdx.x; i < a.stride;
          i += ctas * kThreads)
         p_out[i] = free_pos + static_cast<int32_t>(i);
-    cluster_sync();   // the others' counts are read: shared memory may go
+    cluster_sync();   // the others' counts are read: shared memory may go; the lists are written
+    if (a.inline_moves) {
+        const int n_moves = min(static_cast<int>(moves), a.list_cap);
+        for (int j0 = warp * kWarpMoves; j0 < n_moves; j0 += kWarps * kWarpMoves)
+            move_rows<D>(a, unit, j0, min(kWarpMoves, n_moves - j0), free_pos);
+    }
 }
 
-// Carries out the listed moves, K and V, weight and position: CTA = (chunk of kMovesPerCta moves, unit),
-// unit fastest.
+// CTA = (chunk of kMovesPerCta moves, unit), unit fastest.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Args a, int units)
 {
     pdl_wait();
     pdl_trigger();
-    constexpr int kVec = D / 8;                 // 16-byte chunks of a vector
-    constexpr int kMoveLanes = 2 * kVec;        // K and V of one move
-    constexpr int kAtOnce = 32 / kMoveLanes;    // moves that a warp copies with one load
-    constexpr int kFly = 4;                     // loads in flight
     const int unit = blockIdx.x % units;
-    const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-    const int j0 = (blockIdx.x / units) * kMovesPerCta + warp * kWarpMoves;
+    const int j0 = (blockIdx.x / units) * kMovesPerCta + (threadIdx.x >> 5) * kWarpMoves;
     const int2 count = __ldcg(a.counts + unit);
     const int n = min(kWarpMoves, count.x - j0);
-    if (n <= 0)
-        return;
-    const int kvh = unit % a.kv_heads;
-    const int s = unit / a.kv_heads;
-    const int32_t *dst_list = a.lists + static_cast<size_t>(unit) * 2 * a.list_cap;
-    const int32_t *bt = a.block_table + static_cast<size_t>(s) * a.bt_stride;
-    long long from = -1, to = -1;   // 16-byte chunks; below 0: no copy
-    int dst = -1, src = -1;
-    if (lane < n) {
-        dst = __ldcg(dst_list + j0 + lane);
-        src = __ldcg(dst_list + a.list_cap + j0 + lane);
-    }
-    // (an entry that no slot was written to: the weights changed under the selection)
-    if (static_cast<uint32_t>(dst) < static_cast<uint32_t>(a.max_ctx) &&
-        static_cast<uint32_t>(src) < static_cast<uint32_t>(a.max_ctx)) {
-        const int dp = bt[dst >> a.log2_page], sp = bt[src >> a.log2_page];
-        if (dp >= 0 && dp < a.num_pages && sp >= 0 && sp < a.num_pages) {
-            const int mask = (1 << a.log2_page) - 1;
-            auto place = [&](int page, int off) -> long long {
-                const long long vec =
-                    a.hnd ? ((static_cast<long long>(page) * a.kv_heads + kvh) << a.log2_page) + off
-                          : ((static_cast<long long>(page) << a.log2_page) + off) * a.kv_heads + kvh;
-                return vec * kVec;
-            };
-            from = place(sp, src & mask);
-            to = place(dp, dst & mask);
-        } else {
-            atomicOr(a.err ? a.err : &g_evict_errors, kErrPageRange);
-        }
-        const int row = a.rows ? a.rows[s] : s;
-        const size_t base = (static_cast<size_t>(row) * a.kv_heads + kvh) * a.stride;
-        const float w = a.weights[base + src];
-        const int32_t p = a.positions[base + src];
-        a.weights_out[base + dst] = w;
-        a.positions_out[base + dst] = p;
-        a.weights_out[base + src] = 0.0f;
-        a.positions_out[base + src] = count.y + src;
-    }
-    const int sub = lane / kMoveLanes;
-    const int in_move = lane % kMoveLanes;
-    uint4 *pool = (in_move < kVec ? a.k_pool : a.v_pool) + in_move % kVec;
-    for (int u0 = 0; u0 < n; u0 += kFly * kAtOnce) {
-        uint4 x[kFly];
-        long long dst[kFly];
-#pragma unroll
-        for (int u = 0; u < kFly; ++u) {
-            const int m = u0 + u * kAtOnce + sub;   // below 64; past n the lane's places are -1
-            const long long f = __shfl_sync(0xffffffffu, from, m & 31);
-            dst[u] = __shfl_sync(0xffffffffu, to, m & 31);
-            if (m >= n)
-                dst[u] = -1;
-            if (dst[u] >= 0)
-                x[u] = __ldcg(pool + f);
-        }
-#pragma unroll
-        for (int u = 0; u < kFly; ++u)
-            if (dst[u] >= 0)
-                pool[dst[u]] = x[u];
-    }
+    if (n > 0)
+        move_rows<D>(a, unit, j0, n, count.y);
 }
 
 cudaError_t launch_t(const EvictLaunch &l, const Args &args, cudaStream_t stream)
@@ -591,8 +607,12 @@ cudaError_t launch_t(const EvictLaunch &l, const Args &args, cudaStream_t stream
                            4 / kWarpSlots * kWarpSlots;
     a.cached = static_cast<int>(std::min(per_cta, std::min<long long>(room, kMaxCached)));
     const size_t smem = static_cast<size_t>(a.cached) * 4 + sizeof(Shared);
+    // Few moves a row are made by the row's own CTA (XXX).
+    a.inline_moves = ctas == 1 && l.list_cap <= kInlineMoves;
+    auto select = l.head_dim == 128 ? select_kernel<128> : select_kernel<64>;
+    auto move = l.head_dim == 128 ? move_kernel<128> : move_kernel<64>;
     cudaError_t err =
-        cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kMaxCached * 4 + static_cast<int>(sizeof(Shared)));
     if (err != cudaSuccess)
         return err;
@@ -613,10 +633,9 @@ cudaError_t launch_t(const EvictLaunch &l, const Args &args, cudaStream_t stream
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    err = cudaLaunchKernelEx(&cfg, select_kernel, a);
-    if (err != cudaSuccess || l.list_cap == 0)
+    err = cudaLaunchKernelEx(&cfg, select, a);
+    if (err != cudaSuccess || l.list_cap == 0 || a.inline_moves)
         return err;
-    auto move = l.head_dim == 128 ? move_kernel<128> : move_kernel<64>;
     return launch_pdl(move, dim3(static_cast<unsigned>(units * chunks)), dim3(kMoveThreads), 0,
                       stream, a, static_cast<int>(units));
 }

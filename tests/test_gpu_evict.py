@@ -419,6 +419,7 @@ def test_serving_loop_with_eviction(layout):
                       layout=layout)
         ctx.copy_(new)
 
+    torch.cuda.synchronize()
     with torch.cuda.stream(torch.cuda.Stream()):
         step()
         cut()

@@ -349,6 +349,7 @@ def test_step_in_a_graph_with_growing_contexts_and_pinned_inputs():
         kvc.kvc_store_int4(*dev, kn, vn, slot)
         kvc.kvc_decode_int4(out, q, *dev, dt, ctx, 128, workspace=work)
 
+    torch.cuda.synchronize()
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
         step()

@@ -108,7 +108,7 @@ def decode(pool=POOL, q_heads=4, out=FAKE, kp=FAKE, bt=8, max_ctx=100, splits=1,
     (dict(pool=PoolDesc(32, 16, 2, 96)), 2), (dict(pool=PoolDesc(32, 8, 2, 64)), 2),
     (dict(pool=PoolDesc(32, 16, 2, 64, 5)), 1), (dict(q_heads=3), 1), (dict(q_heads=32), 2),
     (dict(out=ODD), 1), (dict(kp=ODD), 1), (dict(kp=None), 1), (dict(bt=4), 1),
-    (dict(splits=-1), 1), (dict(splits=0), 3), (dict(splits=2, ws=FAKE, nbytes=16), 3),
+    (dict(splits=-1), 1), (dict(splits=0, bt=16, max_ctx=200), 3), (dict(splits=2, ws=FAKE, nbytes=16), 3),
     (dict(dtype=7), 1), (dict(seqs=-1), 1), (dict(seqs=70000), 1), (dict(seqs=0), 0),
 ])
 def test_decode_int4_refusals(kw, code):
@@ -139,7 +139,8 @@ def test_decode_int4_plan():
     assert block == 64 and warps % 8 == 0 and 0 < warps <= 64 * 128 * 8
     slots = 8 * (64 + warps // 8)
     assert ws >= slots * 4 * 129 * 4 + 64 * 8 * 8
-    assert kvc.kvc_decode_int4_plan(1, 32, pool, 65, 0)[0] == 2 * 8   # one run per block
+    assert kvc.kvc_decode_int4_plan(1, 32, pool, 129, 0)[0] == 3 * 8   # one run per block
+    assert kvc.kvc_decode_int4_plan(5, 32, pool, 128, 0) == (5 * 8, 64, 0)   # short: whole units
     assert kvc.kvc_decode_int4_plan(0, 32, pool, 0, 0)[0] == 8
 
 
