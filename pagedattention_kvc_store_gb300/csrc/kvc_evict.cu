@@ -55,10 +55,7 @@ constexpr uint32_t kNewest = 0xFFFFFFFFu;
 constexpr long long kSmemPerSm = 228 * 1024;
 constexpr int kMoveThreads = 128;
 constexpr int kWarpMoves = 16;    // moves of one warp
-#ifndef INL
-#define INL 256
-#endif
-constexpr int kInlineMoves = INL;
+constexpr int kInlineMoves = 256;
 constexpr int kMovesPerCta = kMoveThreads / 32 * kWarpMoves;
 
 struct Args {
@@ -607,7 +604,10 @@ cudaError_t launch_t(const EvictLaunch &l, const Args &args, cudaStream_t stream
                            4 / kWarpSlots * kWarpSlots;
     a.cached = static_cast<int>(std::min(per_cta, std::min<long long>(room, kMaxCached)));
     const size_t smem = static_cast<size_t>(a.cached) * 4 + sizeof(Shared);
-    // Few moves a row are made by the row's own CTA (XXX).
+    // Few moves a row are made by the row's own CTA: 64 sequences of 4,096 slots giving up 256 take
+    // 41.7 us against 48.2 with a second launch, one short row 9.1 against 10.9; with thousands of
+    // moves in rows of different lengths it is the other way round (84 against 63 on 64 sequences of
+    // 512 to 4,096 slots cut to 2,048).
     a.inline_moves = ctas == 1 && l.list_cap <= kInlineMoves;
     auto select = l.head_dim == 128 ? select_kernel<128> : select_kernel<64>;
     auto move = l.head_dim == 128 ? move_kernel<128> : move_kernel<64>;
