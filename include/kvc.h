@@ -571,7 +571,8 @@ kvc_status kvc_decode_int4(void *out, int32_t out_dtype, const void *q, const vo
  * for every p < context_lens[s], in fp32.  Arguments as kvc_decode; the workspace is always needed
  * (kvc_decode_weights_plan; splits and chunk are kvc_decode's) and holds the partials and the
  * scores, 4 bytes per (position, query head); it belongs to one call at a time.  Pages may be
- * shared between sequences, rows not.
+ * shared between sequences, rows not.  A context past max_ctx is flagged (1 << 7) and gets no weights
+ * from max_ctx on.
  *   weights        fp32 [num_rows][kv_heads][weight_stride], weight_stride >= max_ctx
  *   weight_rows    int32 [num_seqs] or NULL (then num_rows >= num_seqs)
  */
@@ -592,12 +593,14 @@ kvc_status kvc_decode_weights(void *out, int32_t out_dtype, float *weights,
  * recent), then those with the largest weight (NaN below every number), equal ones in slot order.
  * The kept slots from n on move into the evicted ones below n, both in ascending order (K and V,
  * raw 16-bit copies; weight and position with them), so that slots 0 .. n - 1 hold what is kept;
- * new_lens[s] = n.  Pages after the n-th slot's are the caller's to free.  K and V of slots from n on
+ * new_lens[s] = n.  The last slot has to hold the sequence's newest token: one that was cut gets at
+ * least one more before the next call that names it (or its row is left out); where the position
+ * that slot context_lens[s] holds does not follow that of the last slot, 1 << 13 is flagged.  Pages after the n-th slot's are the caller's to free.  K and V of slots from n on
  * stay as they are.  The call reads weights and positions and writes weights_out and positions_out,
  * which may be the same arrays (in place) or others that overlap neither; of a row they get: slots
  * below n as above, weights_out 0 for n .. context_lens[s] - 1 (the rest untouched), positions_out
  * for n .. weight_stride - 1 the positions that the next tokens will have.
- * A sequence within its budget keeps everything.  Pages that are written must be the
+ * A sequence within its budget keeps everything; a context past max_ctx is cut to it and flagged.  Pages that are written must be the
  * sequence's own (kvc_copy_pages first where others list them); moves that touch a page id outside the
  * pool are skipped and flagged, and that sequence's result is undefined.
  *   budget         at least 1;  recent  0 .. budget

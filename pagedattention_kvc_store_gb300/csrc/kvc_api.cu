@@ -176,6 +176,24 @@ Int8Plan make_int8_plan(int32_t num_seqs, int32_t q_heads, const kvc_pool_desc &
     return p;
 }
 
+// Limits of the kernels' 32-bit indexes: positions of a sequence (a block past the last one is
+// looked at) and rows of q.
+kvc_status check_reach(int32_t max_ctx, int32_t bt_stride, int32_t page_size, int64_t rows)
+{
+    if (max_ctx > (1 << 30) || static_cast<int64_t>(bt_stride) * page_size > (int64_t(1) << 30))
+        return fail(KVC_ERR_UNSUPPORTED, "max_ctx and bt_stride * page_size must be at most 2^30");
+    if (rows > (int64_t(1) << 28))
+        return fail(KVC_ERR_UNSUPPORTED, "num_seqs * heads must be at most 2^28");
+    return KVC_OK;
+}
+
+// Whether two arrays of `bytes` each share some but not all of their memory.
+bool partly_overlap(const void *a, const void *b, uint64_t bytes)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x != y && (x < y ? y - x : x - y) < bytes;
+}
+
 // 4-bit decode plan, as the INT8 one, with 64-position blocks and one warp per run and kv head: by
 // default as many runs as one wave of the kernel's CTAs (one per SM) holds, and for contexts of at
 // most two blocks one run per sequence, which needs no merge: 4 sequences of up to 128 positions
@@ -193,8 +211,9 @@ kvc_status make_int4_plan(int32_t num_seqs, int32_t q_heads, const kvc_pool_desc
 {
     Int4Plan p{};
     const int64_t seqs = num_seqs > 0 ? num_seqs : 1;
-    if (seqs * pool.kv_heads > (int64_t(1) << 28))
-        return fail(KVC_ERR_UNSUPPORTED, "num_seqs * kv_heads must be at most 2^28");
+    const kvc_status st = check_reach(max_ctx, 0, pool.page_size, seqs * q_heads);
+    if (st != KVC_OK)
+        return st;
     if (requested == 1 || (requested <= 0 && max_ctx <= kInt4WholeCtx)) {
         p.per_unit = true;
         p.runs = static_cast<int>(seqs);
@@ -973,6 +992,8 @@ kvc_status kvc_decode_int4(void *out, int32_t out_dtype, const void *q, const vo
         return fail(KVC_ERR_INVALID_ARG, "num_splits %d", num_splits);
     if (num_seqs == 0)
         return ok();
+    if ((st = check_reach(max_ctx, bt_stride, pool.page_size, 0)) != KVC_OK)
+        return st;
     kvc::DecodeInt4Launch l;
     if ((st = int4_pools(k_codes, v_codes, k_params, v_params, pool, &l.pools)) != KVC_OK)
         return st;
@@ -1240,6 +1261,8 @@ kvc_status kvc_decode_weights_plan(int32_t num_seqs, int32_t q_heads, kvc_pool_d
         return st;
     if (num_seqs < 0 || max_ctx < 0 || num_splits < 0)
         return fail(KVC_ERR_INVALID_ARG, "negative num_seqs, max_ctx or num_splits");
+    if ((st = check_reach(max_ctx, 0, pool.page_size, int64_t(num_seqs) * q_heads)) != KVC_OK)
+        return st;
     const WeightsPlan w = make_weights_plan(num_seqs, q_heads, pool, max_ctx, num_splits);
     if (splits_out)
         *splits_out = w.p.splits;
@@ -1266,7 +1289,9 @@ kvc_status kvc_decode_weights(void *out, int32_t out_dtype, float *weights,
         return fail(KVC_ERR_INVALID_ARG, "num_splits %d", num_splits);
     if (num_seqs == 0)
         return ok();
-    if ((st = check_weight_rows(weights, weight_rows, num_rows, weight_stride, num_seqs,
+    if ((st = check_reach(max_ctx, bt_stride, pool.page_size, int64_t(num_seqs) * q_heads)) !=
+            KVC_OK ||
+        (st = check_weight_rows(weights, weight_rows, num_rows, weight_stride, num_seqs,
                                 max_ctx)) != KVC_OK)
         return st;
     const WeightsPlan w = make_weights_plan(num_seqs, q_heads, pool, max_ctx, num_splits);
@@ -1327,6 +1352,8 @@ kvc_status kvc_evict_plan(int32_t num_seqs, kvc_pool_desc pool, int32_t max_ctx,
         return fail(KVC_ERR_INVALID_ARG, "negative num_seqs or max_ctx");
     if (budget < 1)
         return fail(KVC_ERR_INVALID_ARG, "budget %d (at least 1)", budget);
+    if ((st = check_reach(max_ctx, 0, pool.page_size, int64_t(num_seqs) * pool.kv_heads)) != KVC_OK)
+        return st;
     const size_t cap = evict_list_cap(max_ctx, budget);
     const size_t units = static_cast<size_t>(num_seqs) * pool.kv_heads;
     if (workspace_bytes_out)
@@ -1359,11 +1386,17 @@ kvc_status kvc_evict(void *k_pool, void *v_pool, kvc_pool_desc pool, const int32
         return fail(KVC_ERR_INVALID_ARG, "null pointer argument");
     if (!aligned16(k_pool) || !aligned16(v_pool))
         return fail(KVC_ERR_INVALID_ARG, "pools must be 16-byte aligned");
-    if (new_lens == context_lens)
+    if (new_lens == context_lens || partly_overlap(new_lens, context_lens, uint64_t(num_seqs) * 4))
         return fail(KVC_ERR_INVALID_ARG, "new_lens must not be context_lens");
-    if ((st = check_weight_rows(weights, weight_rows, num_rows, weight_stride, num_seqs,
+    if ((st = check_reach(max_ctx, bt_stride, pool.page_size, 0)) != KVC_OK ||
+        (st = check_weight_rows(weights, weight_rows, num_rows, weight_stride, num_seqs,
                                 max_ctx)) != KVC_OK)
         return st;
+    const uint64_t row_bytes = uint64_t(num_rows) * pool.kv_heads * weight_stride * 4;
+    if (partly_overlap(weights, weights_out, row_bytes) ||
+        partly_overlap(positions, positions_out, row_bytes))
+        return fail(KVC_ERR_INVALID_ARG,
+                    "weights_out and positions_out: the arrays that are read, or apart from them");
     if (need > 0) {
         if (workspace == nullptr || workspace_bytes < need)
             return fail(KVC_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,

@@ -237,6 +237,9 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     float *w_out = a.weights_out + base;
     int32_t *p_out = a.positions_out + base;
     const int last = N > 0 ? p_in[N - 1] : -1;   // the newest token's original position
+    // (the slot after it holds the next one, which only this thread overwrites, at its end)
+    if (cta == 0 && threadIdx.x == 0 && N > 0 && N < a.stride && p_in[N] != last + 1)
+        atomicOr(err, kErrPositionOrder);
 
     // this warp's slots [lo, hi); the CTA's begin at cta_lo
     const long long per_warp = (N + static_cast<long long>(kWarpSlots) * kWarps * ctas - 1) /

@@ -48,7 +48,7 @@ struct FinishArgs {
     float *weights;
     const int32_t *rows;   // row of each sequence, or null (row s)
     int num_rows, weight_stride;
-    int num_seqs, merge_blocks, tiles;
+    int num_seqs, max_ctx, merge_blocks, tiles;
 };
 
 template <int D>
@@ -73,12 +73,10 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const FinishArgs
     const int kvh = unit % a.kv_heads;
     const int s = unit / a.kv_heads;
     const int raw = a.context_lens[s];
-    const int ctx = static_cast<int>(
-        min(static_cast<long long>(min(raw, f.weight_stride)),
-            static_cast<long long>(a.bt_stride) * a.page_size));
+    const int ctx = min(raw, f.max_ctx);   // which the rows, the scores and the table row hold
     const int row = f.rows ? f.rows[s] : s;
     if (threadIdx.x == 0 && tile == 0 && kvh == 0) {
-        if (raw > f.weight_stride && row >= 0)
+        if (raw > f.max_ctx && row >= 0)
             atomicOr(a.err ? a.err : &g_weights_errors, kErrContextRange);
         if (row >= f.num_rows)
             atomicOr(a.err ? a.err : &g_weights_errors, kErrSlotRange);
@@ -159,6 +157,7 @@ cudaError_t launch_t(const DecodeLaunch &l, const WeightsLaunch &w, const CUtens
     f.num_rows = w.num_rows;
     f.weight_stride = w.weight_stride;
     f.num_seqs = l.num_seqs;
+    f.max_ctx = w.max_ctx;
     const int rows_per_block = kFinishThreads / 32;
     f.merge_blocks = (l.num_seqs * l.q_heads + rows_per_block - 1) / rows_per_block;
     f.tiles = (w.max_ctx + kTile - 1) / kTile;

@@ -49,6 +49,7 @@ class Run:
         self.ctx = i32_tensor(case.context_lens, "cuda")
         self.pool = kvc.pool_desc(self.k, layout)
         self.stride = stride or case.max_ctx
+        self.max_ctx = case.max_ctx
         self.rows = rows
         self.drows = None if rows is None else i32_tensor(rows, "cuda")
         self.weights = torch.zeros(num_rows or case.num_seqs, case.kv_heads, self.stride,
@@ -58,10 +59,10 @@ class Run:
     def decode(self, splits=0, ctx=None, dtype=torch.bfloat16, scale=0.0, stream=None):
         c = self.case
         out = torch.full(self.q.shape, float("nan"), dtype=dtype, device="cuda")
-        n = kvc.kvc_decode_weights_plan(c.num_seqs, c.q_heads, self.pool, c.max_ctx, splits)[2]
+        n = kvc.kvc_decode_weights_plan(c.num_seqs, c.q_heads, self.pool, self.max_ctx, splits)[2]
         self.work = torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device="cuda")
         kvc.kvc_decode_weights(out, self.weights, self.q, self.k, self.v, self.table,
-                               self.ctx if ctx is None else i32_tensor(ctx, "cuda"), c.max_ctx,
+                               self.ctx if ctx is None else i32_tensor(ctx, "cuda"), self.max_ctx,
                                scale=scale, num_splits=splits, workspace=self.work,
                                weight_rows=self.drows, layout=self.layout, stream=stream)
         return out
@@ -69,10 +70,10 @@ class Run:
     def plain_decode(self, splits=0, ctx=None, dtype=torch.bfloat16, scale=0.0):
         c = self.case
         out = torch.full(self.q.shape, float("nan"), dtype=dtype, device="cuda")
-        n = kvc.kvc_decode_plan(c.num_seqs, c.q_heads, self.pool, c.max_ctx, splits)[2]
+        n = kvc.kvc_decode_plan(c.num_seqs, c.q_heads, self.pool, self.max_ctx, splits)[2]
         work = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
         kvc.kvc_decode(out, self.q, self.k, self.v, self.table,
-                       self.ctx if ctx is None else i32_tensor(ctx, "cuda"), c.max_ctx,
+                       self.ctx if ctx is None else i32_tensor(ctx, "cuda"), self.max_ctx,
                        scale=scale, num_splits=splits, workspace=work, layout=self.layout)
         return out
 
@@ -161,6 +162,22 @@ def test_rows_past_the_array_are_flagged():
     run.decode()
     assert kvc.kvc_device_errors() == 1 << 6
     assert not run.weights[1].any()
+
+
+def test_contexts_past_max_ctx_are_flagged():
+    """The scores of the launch hold max_ctx positions (here a chunk of 256): weights past it stay as
+    they are, in rows that could hold them."""
+    case = decode_case(9, 16, 2, 2, 64, [90, 700])
+    run = Run(case, stride=800)
+    run.weights.fill_(0.5)
+    run.max_ctx = 200
+    out = run.decode()
+    assert kvc.kvc_device_errors() == 1 << 7
+    assert torch.equal(out, run.plain_decode())
+    assert (run.weights[1, :, 200:] == 0.5).all() and (run.weights[0, :, 90:] == 0.5).all()
+    got = run.weights[0, :, :90].double().cpu().numpy() - 0.5
+    ref = evict.weights(case.q[:1], run.kp, case.block_table[:1], np.array([90]))[0]
+    assert np.abs(got - ref).max() <= 2.5 * run.relative_bound()
 
 
 def test_a_custom_scale_and_sharp_rows():
@@ -382,6 +399,59 @@ def test_evict_flags_bad_pages_rows_and_lengths():
     assert call(case.block_table, np.array([100, 101]), 100) == 1 << 7
     assert call(case.block_table, case.context_lens, 100, np.array([0, 2])) == 1 << 6
     assert new.cpu().tolist() == [30, 100]
+
+
+def test_rows_whose_last_slot_is_not_the_newest_are_flagged():
+    """An eviction straight after another one, and the same with a token in between."""
+    case = decode_case(84, 16, 2, 1, 64, [100, 90])
+    w, pos = state(case, 30, 8, earlier=False)
+    w[:, :, 29] = 1e6                    # stays, so the last slot of 30 is an old one
+    k, v = (bf16_tensor(x, "cuda") for x in full_pools(case))
+    dw, dp = torch.from_numpy(w).cuda(), torch.from_numpy(pos).cuda()
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    work = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    rows = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+
+    def call(ctx, budget):
+        kvc.kvc_evict(k, v, dw, dp, new, dw, dp, i32_tensor(case.block_table, "cuda"),
+                      i32_tensor(np.array(ctx), "cuda"), 100, budget, 5, workspace=work,
+                      weight_rows=rows)
+        return kvc.kvc_device_errors()
+
+    assert call([100, 90], 30) == 0
+    assert (dp[:, :, 29] == 29).all()
+    assert call([31, 31], 30) == 0
+    before = dp.clone()
+    rows[1] = -1
+    assert call([30, 31], 20) == 1 << 13
+    assert torch.equal(dp[1], before[1])
+
+
+def test_evictions_on_two_streams():
+    """Different sequences of the same pools, a workspace each."""
+    case = decode_case(85, 16, 3, 1, 128, lambda rng: rng.integers(1500, 3000, size=8))
+    budget, recent = 1000, 100
+    w, pos = state(case, budget, 9)
+    kp, vp = full_pools(case)
+    k, v = bf16_tensor(kp, "cuda"), bf16_tensor(vp, "cuda")
+    dw, dp = torch.from_numpy(w).cuda(), torch.from_numpy(pos).cuda()
+    table, ctx = i32_tensor(case.block_table, "cuda"), i32_tensor(case.context_lens, "cuda")
+    new = torch.zeros(8, dtype=torch.int32, device="cuda")
+    need = kvc.kvc_evict_plan(4, kvc.pool_desc(k), case.max_ctx, budget)
+    streams = [torch.cuda.Stream() for _ in "ab"]
+    works = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in "ab"]
+    torch.cuda.synchronize()
+    for i, s in enumerate(streams):
+        at = slice(4 * i, 4 * i + 4)
+        kvc.kvc_evict(k, v, dw[at], dp[at], new[at], dw[at], dp[at], table[at], ctx[at],
+                      case.max_ctx, budget, recent, workspace=works[i], stream=s)
+    torch.cuda.synchronize()
+    lens = evict.evict(kp, vp, w, pos, case.block_table, case.context_lens, budget, recent)
+    assert np.array_equal(new.cpu().numpy(), lens)
+    assert np.array_equal(bf16_bits_of(k), kp) and np.array_equal(bf16_bits_of(v), vp)
+    assert np.array_equal(dp.cpu().numpy(), pos)
+    assert np.array_equal(dw.cpu().numpy().view(np.uint32), w.view(np.uint32))
+    assert kvc.kvc_device_errors() == 0
 
 
 @pytest.mark.parametrize("layout", ["nhd", "hnd"])

@@ -186,6 +186,41 @@ def test_decode_ragged(H, G, D, P, layout):
     check(case, got, ref, pools, "bf16", bf16=True)
 
 
+@pytest.mark.parametrize("H,G,D,P", [(6, 2, 128, 16), (7, 1, 64, 32), (9, 4, 64, 16), (11, 1, 64, 16),
+                                     (12, 2, 128, 64), (16, 1, 128, 16), (10, 8, 64, 32)])
+def test_decode_head_counts(H, G, D, P):
+    """Numbers of kv heads that one group of warps does not take: several groups share a sequence, or
+    leave warps of a CTA idle."""
+    case = ragged(140 + H, P, H, G, D, lambda rng: rng.integers(1, 400, size=7))
+    layout = "hnd" if H % 2 else "nhd"
+    pools = filled(case, layout)
+    ref = int4.attention(case.q, *pools, case.block_table, case.context_lens, layout=layout)
+    for splits in (0, 1, 2):
+        got = run_decode(case.q, pools, case.block_table, case.context_lens, case.max_ctx, splits,
+                         layout=layout)
+        check(case, got, ref, pools, f"splits={splits}")
+
+
+def test_more_sequences_than_threads():
+    """700 sequences: each thread that cuts the runs counts several."""
+    case = ragged(150, 16, 1, 2, 64, lambda rng: rng.integers(1, 200, size=700))
+    pools = filled(case)
+    ref = int4.attention(case.q, *pools, case.block_table, case.context_lens)
+    for splits in (0, 7):
+        got = run_decode(case.q, pools, case.block_table, case.context_lens, case.max_ctx, splits)
+        check(case, got, ref, pools, f"splits={splits}")
+
+
+@pytest.mark.parametrize("max_ctx", [100, 129])
+def test_contexts_past_max_ctx(max_ctx):
+    """max_ctx only sizes the launch: what the block-table row holds is attended all the same."""
+    case = ragged(151, 16, 2, 4, 128, [700, 40, 129])
+    pools = filled(case)
+    ref = int4.attention(case.q, *pools, case.block_table, case.context_lens)
+    got = run_decode(case.q, pools, case.block_table, case.context_lens, max_ctx)
+    check(case, got, ref, pools, f"max_ctx={max_ctx}")
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_every_position_counts_once(D):
     """A query of zeros weighs every position the same, and then no product is rounded (a bf16
@@ -294,8 +329,8 @@ def test_the_result_is_the_same_every_time():
 
 
 def test_bad_pages_and_long_contexts_are_flagged():
-    """A page id outside the pool reads as zeros and is flagged; a context past its block-table row
-    attends over what the row holds."""
+    """A page id outside the pool is flagged and spoils its own sequence only; a context past its
+    block-table row attends over what the row holds."""
     case = ragged(31, 16, 2, 2, 64, [40, 40])
     pools = filled(case)
     table = case.block_table[:, :3].copy()

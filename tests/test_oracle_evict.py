@@ -65,6 +65,7 @@ def test_weights_against_the_attention_oracle():
 POOL = PoolDesc(32, 16, 2, 64)
 FAKE = ctypes.c_void_p(0x10000)   # never dereferenced: checks fail before any launch
 FAKE2 = ctypes.c_void_p(0x20000)
+FAKE3 = ctypes.c_void_p(0x30000)
 ODD = ctypes.c_void_p(0x10004)
 
 
@@ -73,6 +74,7 @@ ODD = ctypes.c_void_p(0x10004)
     (dict(weights=None), 1), (dict(num_rows=3), 1), (dict(num_rows=-1, rows=FAKE), 1),
     (dict(stride=99), 1), (dict(splits=-1), 1), (dict(splits=1), 3), (dict(ws=FAKE, nbytes=16), 3),
     (dict(ws=ODD, nbytes=1 << 30), 1), (dict(bt=4), 1), (dict(seqs=0), 0), (dict(seqs=-1), 1),
+    (dict(bt=1 << 27), 2),
 ])
 def test_decode_weights_refusals(kw, code):
     a = dict(pool=POOL, q_heads=4, out=FAKE, weights=FAKE, rows=None, num_rows=4, stride=100, bt=8,
@@ -90,13 +92,16 @@ def test_decode_weights_refusals(kw, code):
     (dict(recent=51), 1), (dict(new=FAKE), 1), (dict(new=None), 1), (dict(stride=99), 1),
     (dict(num_rows=3), 1), (dict(bt=4), 1), (dict(), 3), (dict(ws=FAKE, nbytes=100), 3),
     (dict(ws=ODD, nbytes=1 << 30), 1), (dict(seqs=0), 0), (dict(seqs=-1), 1), (dict(seqs=70000), 1),
+    (dict(bt=1 << 27), 2), (dict(new=ctypes.c_void_p(0x10008)), 1),
+    (dict(wout=ctypes.c_void_p(0x10010)), 1), (dict(pout=ctypes.c_void_p(0xff00)), 1),
+    (dict(wout=FAKE2, pout=FAKE3), 3),
 ])
 def test_evict_refusals(kw, code):
     a = dict(pool=POOL, k=FAKE, weights=FAKE, positions=FAKE, budget=50, recent=10, new=FAKE2,
-             stride=100, num_rows=4, bt=8, ws=None, nbytes=0, seqs=4)
+             stride=100, num_rows=4, bt=8, ws=None, nbytes=0, seqs=4, wout=FAKE, pout=FAKE)
     a.update(kw)
     assert lib().kvc_evict(a["k"], FAKE, a["pool"], FAKE, a["bt"], FAKE, a["seqs"], 100,
-                           a["weights"], a["positions"], FAKE, FAKE, None, a["num_rows"],
+                           a["weights"], a["positions"], a["wout"], a["pout"], None, a["num_rows"],
                            a["stride"], a["budget"], a["recent"], a["new"], a["ws"], a["nbytes"],
                            None) == code
 
@@ -110,6 +115,12 @@ def test_plans():
     assert (s, c) == kvc.kvc_decode_plan(64, 32, pool, 4096)[:2]
     assert ws >= 64 * 32 * (s * 130 + s * c) * 4
     assert kvc.kvc_decode_weights_plan(4, 32, pool, 10, 1)[2] > 0
+    for call in (lambda n: kvc.kvc_evict_plan(1, pool, n, 5),
+                 lambda n: kvc.kvc_decode_weights_plan(1, 8, pool, n, 0),
+                 lambda n: kvc.kvc_decode_int4_plan(1, 8, pool, n, 0)):
+        call(1 << 30)
+        with pytest.raises(RuntimeError, match="2\\^30"):
+            call((1 << 30) + 1)
 
 
 def test_binding_refuses_cpu_tensors():
