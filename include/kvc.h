@@ -603,7 +603,7 @@ kvc_status kvc_decode_weights(void *out, int32_t out_dtype, float *weights,
  * A sequence within its budget keeps everything; a context past max_ctx is cut to it and flagged.  Pages that are written must be the
  * sequence's own (kvc_copy_pages first where others list them); moves that touch a page id outside the
  * pool are skipped and flagged, and that sequence's result is undefined.
- *   budget         at least 1;  recent  0 .. budget
+ *   budget         at least 1;  recent  0 .. budget;  max_ctx  at most 2^22
  *   new_lens       int32 [num_seqs] (out, device), not context_lens itself: every kv head reads that
  *   workspace      kvc_evict_plan's bytes (0 when budget >= max_ctx), 16-byte aligned
  */

@@ -1352,6 +1352,8 @@ kvc_status kvc_evict_plan(int32_t num_seqs, kvc_pool_desc pool, int32_t max_ctx,
         return fail(KVC_ERR_INVALID_ARG, "negative num_seqs or max_ctx");
     if (budget < 1)
         return fail(KVC_ERR_INVALID_ARG, "budget %d (at least 1)", budget);
+    if (max_ctx > kvc::kEvictMaxCtx)
+        return fail(KVC_ERR_UNSUPPORTED, "max_ctx %d (at most 2^22)", max_ctx);
     if ((st = check_reach(max_ctx, 0, pool.page_size, int64_t(num_seqs) * pool.kv_heads)) != KVC_OK)
         return st;
     const size_t cap = evict_list_cap(max_ctx, budget);

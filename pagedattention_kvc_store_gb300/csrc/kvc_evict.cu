@@ -12,20 +12,25 @@
 //
 // Selection (select_kernel).  A weight becomes a 32-bit key of the same order (NaN as the lowest, -0
 // as 0, the newest slots above every weight), and the n-th largest key is found digit by digit:
-// histograms of 11, 11 and 10 bits, then the slots equal to it are kept in slot order until n is
-// full.  (Digits of 8 bits would be four passes, and the first one, sign and seven exponent bits,
-// would put all weights into a handful of counters that queue up.)  One cluster of 1 to 8 CTAs per
-// (sequence, kv head): the histograms meet through distributed shared memory, one cluster
-// barrier each.  The keys stay in shared memory between the passes (beyond kMaxCached slots a CTA makes
-// them anew from weights and positions).  Every warp owns consecutive slots and every lane four at a
-// time, so ranks in slot order are one warp scan per 128 slots and a prefix over warps and CTAs;
-// nothing depends on the order of atomics (the histograms only count).  The kernel leaves the
-// moves as two lists.
+// histograms of 11, 11 and 10 bits.  (Digits of 8 bits would be four passes, and the first one, sign
+// and seven exponent bits, would put all weights into a handful of counters that queue up.)  After the
+// first digit a slot is kept, evicted or one of a few per cent still open: two bits a slot and a list of
+// the open ones with their keys, so the weights and positions are read twice at most, and the other
+// digits and the ranks work on those.  (With every step going over the keys again the selection of
+// 64 rows of up to 131,072 slots took 74 us, now 58.)  Only a list that runs over sends the digits over
+// all keys again.  One cluster of 1 to 8 CTAs per (sequence, kv head): the histograms meet through
+// distributed shared memory, one cluster barrier each.  As many keys as fit stay in shared memory.
+// Every warp owns consecutive slots and every lane four at a time, so ranks in slot order are one warp
+// scan per 128 slots and a prefix over warps and CTAs; nothing depends on the order of atomics (the
+// histograms only count, the list is read as a set).  The kernel leaves the moves as two lists.
 //
 // Moves (move_kernel).  One launch over all lists, 64 moves a CTA: rows differ in how much they
 // move (a batch's longest several times its average), so the copies are spread over the SMs
-// apart from the selection.  A warp reads 16 moves and their pages at once and then keeps 4 rows
-// in flight (8 to 32 moves and 4 or 8 rows are within 3%, 16 rows or 512 threads 20% slower).
+// apart from the selection.  A warp looks up 16 moves and their pages at once and then keeps 3 rows
+// in flight.  What bounds it is how HBM takes 256-byte rows at random places, read and written at
+// once: 5.0 to 5.6 TB/s here, and more in flight makes it worse (64 sequences of up to 4,096 slots
+// cut to 2,048, selection and moves: 57.6 us with 3 rows of 16 moves, 58.1 with 4, 71 with 8, 70 with 8
+// moves looked up at once; the moves cut into equal ranges over one wave of CTAs 68).
 //
 // Bound: the moved rows (4 D bytes read and written each) by HBM when there are many, else the chain of
 // barriers; the selection reads 8 and writes 8 bytes a slot.
@@ -48,14 +53,18 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kWarpSlots = 128;   // slots of one step of a warp, four consecutive ones a lane
-constexpr int kListed = 1024;     // keys listed for the last pass; with more it goes over all
-constexpr int kAhead = 4;         // steps of global loads that a thread has in flight
+constexpr int kListed = 1024;     // slots of a CTA in the first digit's bin that are kept apart
+constexpr int kAhead = 2;         // steps of loads that a thread has in flight
 constexpr int kMaxCtas = 8;       // of a cluster
+static_assert(kEvictMaxCtx <= kMaxCtas * kEvictCtaSlots, "the masks of a row");
 constexpr uint32_t kNewest = 0xFFFFFFFFu;
 constexpr long long kSmemPerSm = 228 * 1024;
+constexpr long long kSmemPerCta = 227 * 1024;
 constexpr int kMoveThreads = 128;
-constexpr int kWarpMoves = 16;    // moves of one warp
+constexpr int kMoveCtas = 80;     // of the moves' launch, per SM (most of them find no move)
+constexpr int kWarpMoves = 16;    // moves that a warp looks up at once
 constexpr int kInlineMoves = 256;
+constexpr int kInlineUnits = 8;   // units per SM up to which rows make their own moves
 constexpr int kMovesPerCta = kMoveThreads / 32 * kWarpMoves;
 
 struct Args {
@@ -82,9 +91,10 @@ struct Args {
     uint32_t *err;
 };
 
-struct Shared {
+struct __align__(16) Shared {
     uint32_t hist[2][kBins];
-    uint32_t listed[kListed];    // keys that share the first digit, for the last pass
+    uint32_t listed[kListed];    // keys that share the first digit, and their slots in the CTA
+    int listed_slot[kListed];
     uint32_t list_size;
     // Sums of the histogram's bins, eight each, top first.  The passes alternate: a CTA may be in the
     // next pass while another one still reads this pass's sums, but not in the next but one.
@@ -98,10 +108,9 @@ struct Shared {
 // stands for no slot.
 __device__ __forceinline__ uint32_t weight_key(float w)
 {
-    if (w != w)
-        w = -__int_as_float(0x7F800000);
-    const uint32_t b = __float_as_uint(w + 0.0f);
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+    const int b = __float_as_int(w + 0.0f);
+    const uint32_t key = static_cast<uint32_t>(b) ^ (static_cast<uint32_t>(b >> 31) | 0x80000000u);
+    return w != w ? 0x007FFFFFu : key;
 }
 
 __device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane)
@@ -124,7 +133,7 @@ __device__ __forceinline__ void move_rows(const Args &a, int unit, int j0, int n
     constexpr int kVec = D / 8;                 // 16-byte chunks of a vector
     constexpr int kMoveLanes = 2 * kVec;        // K and V of one move
     constexpr int kAtOnce = 32 / kMoveLanes;    // moves that a warp copies with one load
-    constexpr int kFly = 4;                     // loads in flight
+    constexpr int kFly = 3;                     // loads in flight
     const int kvh = unit % a.kv_heads;
     const int s = unit / a.kv_heads;
     const int32_t *dst_list = a.lists + static_cast<size_t>(unit) * 2 * a.list_cap;
@@ -189,8 +198,11 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
 {
     pdl_wait();
     pdl_trigger();
-    extern __shared__ __align__(16) uint32_t keys[];   // [cached], then Shared
+    extern __shared__ __align__(16) uint32_t keys[];   // [cached], then Shared and the masks
     Shared &sh = *reinterpret_cast<Shared *>(keys + a.cached);
+    // A byte per four slots: bit e says that slot e of them is above the threshold, bit 4 + e that it
+    // is equal to it.
+    uint8_t *masks = reinterpret_cast<uint8_t *>(&sh + 1);
     const cg::cluster_group cluster = cg::this_cluster();
     const int cta = static_cast<int>(cluster.block_rank());
     const int ctas = static_cast<int>(cluster.num_blocks());
@@ -237,9 +249,6 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     float *w_out = a.weights_out + base;
     int32_t *p_out = a.positions_out + base;
     const int last = N > 0 ? p_in[N - 1] : -1;   // the newest token's original position
-    // (the slot after it holds the next one, which only this thread overwrites, at its end)
-    if (cta == 0 && threadIdx.x == 0 && N > 0 && N < a.stride && p_in[N] != last + 1)
-        atomicOr(err, kErrPositionOrder);
 
     // this warp's slots [lo, hi); the CTA's begin at cta_lo
     const long long per_warp = (N + static_cast<long long>(kWarpSlots) * kWarps * ctas - 1) /
@@ -249,6 +258,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     const int hi = static_cast<int>(min(static_cast<long long>(N), lo + per_warp));
 
     if (N <= a.budget) {   // nothing to evict
+        if (cta == 0 && threadIdx.x == 0 && N > 0 && N < a.stride && p_in[N] != last + 1)
+            atomicOr(err, kErrPositionOrder);
         for (int i = lo + lane; i < hi; i += 32) {
             w_out[i] = w_in[i];
             p_out[i] = p_in[i];
@@ -260,56 +271,97 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     }
 
     const long long newest = static_cast<long long>(last) - a.recent;   // positions above it
-    auto key_of = [&](float w, int p) { return p > newest ? kNewest : weight_key(w); };
-    // keys of slots i .. i + 3 from weights and positions; 0 from hi on
-    auto make_keys = [&](int i) -> uint4 {
-        if (a.vec && i + 3 < hi) {
-            const float4 w = *reinterpret_cast<const float4 *>(w_in + i);
-            const int4 p = *reinterpret_cast<const int4 *>(p_in + i);
-            return make_uint4(key_of(w.x, p.x), key_of(w.y, p.y), key_of(w.z, p.z),
-                              key_of(w.w, p.w));
+    // Below n a slot keeps its weight and position (the moves write over the gaps); a free slot gets
+    // weight 0 and the position that a token to come will have there.  Arrays apart from those that are
+    // read get this with the first pass; in place, the slots that rows move out of become free with
+    // the move.
+    const int32_t free_pos = static_cast<int32_t>(static_cast<long long>(last) + 1 - n);
+    const bool w_apart = w_out != w_in, p_apart = p_out != p_in;
+    auto hand_on = [&](int i, const float (&w)[4], const int (&p)[4]) {
+        if (a.vec && i + 3 < hi && (i >= n || i + 4 <= n)) {
+            if (w_apart)
+                *reinterpret_cast<float4 *>(w_out + i) =
+                    i < n ? make_float4(w[0], w[1], w[2], w[3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (p_apart)
+                *reinterpret_cast<int4 *>(p_out + i) =
+                    i < n ? make_int4(p[0], p[1], p[2], p[3])
+                          : make_int4(free_pos + i, free_pos + i + 1, free_pos + i + 2,
+                                      free_pos + i + 3);
+            return;
         }
-        uint4 k;
-        k.x = i < hi ? key_of(w_in[i], p_in[i]) : 0u;
-        k.y = i + 1 < hi ? key_of(w_in[i + 1], p_in[i + 1]) : 0u;
-        k.z = i + 2 < hi ? key_of(w_in[i + 2], p_in[i + 2]) : 0u;
-        k.w = i + 3 < hi ? key_of(w_in[i + 3], p_in[i + 3]) : 0u;
-        return k;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (i + e < hi) {
+                if (w_apart)
+                    w_out[i + e] = i + e < n ? w[e] : 0.0f;
+                if (p_apart)
+                    p_out[i + e] = i + e < n ? p[e] : free_pos + i + e;
+            }
     };
+    auto key_of = [&](float w, int p) { return p > newest ? kNewest : weight_key(w); };
     // Calls f(i, keys of slots i .. i + 3) for the warp's slots in order, i = 4 lane past each step's
     // first slot; all lanes go together, with keys 0 from hi on.  The slots below `from` come from
-    // shared memory, the others from memory, kAhead steps' loads in flight.
-    auto sweep = [&](int from, auto &&f) {
-        int i0 = lo;
-        for (; i0 < hi && i0 - cta_lo < from; i0 += kWarpSlots) {
-            const int i = i0 + 4 * lane;
-            f(i, i < hi ? *reinterpret_cast<const uint4 *>(keys + (i - cta_lo))
-                        : make_uint4(0u, 0u, 0u, 0u));
-        }
-        if (a.vec) {
-            for (; i0 + kAhead * kWarpSlots <= hi; i0 += kAhead * kWarpSlots) {
-                float4 w[kAhead];
-                int4 p[kAhead];
+    // shared memory, the others from memory, kAhead steps' loads in flight; the first sweep also
+    // hands weights and positions on.
+    auto sweep = [&](int from, auto &&f, bool first = false) {
+#pragma unroll 1
+        for (int i0 = lo; i0 < hi; i0 += kAhead * kWarpSlots) {
+            float w[kAhead][4];   // of cached slots the keys
+            int p[kAhead][4];
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    w[u] = *reinterpret_cast<const float4 *>(w_in + i0 + u * kWarpSlots + 4 * lane);
-                    p[u] = *reinterpret_cast<const int4 *>(p_in + i0 + u * kWarpSlots + 4 * lane);
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + u * kWarpSlots + 4 * lane;
+                if (!first && i0 + u * kWarpSlots - cta_lo < from) {
+                    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // the bits of no slot
+                    if (i < hi)
+                        x = *reinterpret_cast<const float4 *>(keys + (i - cta_lo));
+                    w[u][0] = x.x, w[u][1] = x.y, w[u][2] = x.z, w[u][3] = x.w;
+                } else if (a.vec && i + 3 < hi) {
+                    const float4 x = *reinterpret_cast<const float4 *>(w_in + i);
+                    const int4 y = *reinterpret_cast<const int4 *>(p_in + i);
+                    w[u][0] = x.x, w[u][1] = x.y, w[u][2] = x.z, w[u][3] = x.w;
+                    p[u][0] = y.x, p[u][1] = y.y, p[u][2] = y.z, p[u][3] = y.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (i + e < hi) {
+                            w[u][e] = w_in[i + e];
+                            p[u][e] = p_in[i + e];
+                        }
                 }
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u)
-                    f(i0 + u * kWarpSlots + 4 * lane,
-                      make_uint4(key_of(w[u].x, p[u].x), key_of(w[u].y, p[u].y),
-                                 key_of(w[u].z, p[u].z), key_of(w[u].w, p[u].w)));
             }
-        }
-        for (; i0 < hi; i0 += kWarpSlots) {
-            const int i = i0 + 4 * lane;
-            f(i, i < hi ? make_keys(i) : make_uint4(0u, 0u, 0u, 0u));
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + u * kWarpSlots + 4 * lane;
+                if (i0 + u * kWarpSlots >= hi)
+                    break;
+                if (first)
+                    hand_on(i, w[u], p[u]);
+                uint32_t k[4];
+                if (!first && i0 + u * kWarpSlots - cta_lo < from) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        k[e] = __float_as_uint(w[u][e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        k[e] = key_of(w[u][e], p[u][e]);
+                    if (i0 + (u + 1) * kWarpSlots > hi) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            k[e] = i + e < hi ? k[e] : 0u;
+                    }
+                }
+                f(i, make_uint4(k[0], k[1], k[2], k[3]));
+            }
         }
     };
 
     // ---- the n-th largest key, and how many equal to it are kept ----
     __syncthreads();   // the histograms are zero
+    // (the slot after the last holds the next position; only this thread overwrites it, at its end)
+    if (cta == 0 && threadIdx.x == 0 && N < a.stride && p_in[N] != last + 1)
+        atomicOr(err, kErrPositionOrder);
     sweep(0, [&](int i, const uint4 k) {
         if (i < hi && i - cta_lo < a.cached)
             *reinterpret_cast<uint4 *>(keys + (i - cta_lo)) = k;
@@ -326,37 +378,61 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
                 if (ks[e] != 0)
                     atomicAdd(&sh.hist[0][ks[e] >> 21], 1u);
         }
-    });
+    }, true);
     uint32_t prefix = 0;   // the digits found so far
     uint32_t need = n;     // keys still wanted among those that begin with them
     uint32_t equal = 0;    // how many these are
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
+    for (int pass = 0;; ++pass) {
         uint32_t *hist = sh.hist[pass & 1];
-        if (pass > 0) {
-            const int skip = pass == 1 ? 21 : 10;    // bits below the digits found
-            const int shift = pass == 1 ? 10 : 0;
-            const uint32_t mask = pass == 1 ? 0x7FFu : 0x3FFu;
-            if (pass == 2 && sh.list_size <= kListed) {
-                for (int i = threadIdx.x; i < static_cast<int>(sh.list_size); i += kThreads)
-                    if ((sh.listed[i] >> skip) == prefix)
-                        atomicAdd(&hist[sh.listed[i] & mask], 1u);
-            } else {
-                sweep(a.cached, [&](int, const uint4 k) {
-                    const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (ks[e] != 0 && (ks[e] >> skip) == prefix) {
-                            atomicAdd(&hist[(ks[e] >> shift) & mask], 1u);
-                            if (pass == 1) {
-                                const uint32_t at = atomicAdd(&sh.list_size, 1u);
-                                if (at < kListed)
-                                    sh.listed[at] = ks[e];
-                            }
-                        }
-                });
+        const int skip = pass == 1 ? 21 : pass == 2 ? 10 : 0;    // bits below the digits found
+        const int shift = pass == 1 ? 10 : 0;
+        const uint32_t mask = pass == 1 ? 0x7FFu : 0x3FFu;
+        if (pass >= 2 && sh.list_size <= kListed) {
+            for (int j = threadIdx.x; j < static_cast<int>(sh.list_size); j += kThreads) {
+                const uint32_t key = sh.listed[j];
+                const int slot = sh.listed_slot[j];
+                if (pass == 2) {
+                    if ((key >> skip) == prefix)
+                        atomicAdd(&hist[key & mask], 1u);
+                } else if (key >= prefix) {
+                    atomicOr(reinterpret_cast<uint32_t *>(masks) + slot / 16,
+                             1u << (slot / 4 % 4 * 8 + (key > prefix ? 0 : 4) + slot % 4));
+                }
             }
+        } else if (pass > 0) {
+            // what the first digit decides goes to the masks and the rest to the list; without a
+            // whole list the masks are made at the end
+            const uint32_t least = max(prefix << skip, 1u);   // of the keys that begin with them
+            const uint32_t most = prefix << skip | ((1u << skip) - 1u);
+            sweep(a.cached, [&](int i, const uint4 k) {
+                const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
+                uint32_t over = 0, in = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    over |= ks[e] > most ? 1u << e : 0u;
+                    in |= ks[e] >= least ? 1u << e : 0u;
+                }
+                in &= ~over;
+                if (pass != 2)
+                    masks[(i - cta_lo) / 4] = static_cast<uint8_t>(pass == 3 ? over | in << 4 : over);
+                if (pass == 3 || in == 0)
+                    return;
+                uint32_t at = pass == 1 ? atomicAdd(&sh.list_size, static_cast<uint32_t>(__popc(in)))
+                                        : static_cast<uint32_t>(kListed);
+                for (; in; in &= in - 1, ++at) {
+                    const int e = __ffs(in) - 1;
+                    const uint32_t key = e < 2 ? e == 0 ? k.x : k.y : e == 2 ? k.z : k.w;
+                    atomicAdd(&hist[(key >> shift) & mask], 1u);
+                    if (at < kListed) {
+                        sh.listed[at] = key;
+                        sh.listed_slot[at] = i + e - cta_lo;
+                    }
+                }
+            });
         }
+        if (pass == 3)
+            break;
         // Every CTA gives away the sums of eight bins each, top first; only the thread whose eight
         // bins hold the wanted key reads these bins of every CTA (all bins of all CTAs would be 64 KB
         // through distributed shared memory).
@@ -416,18 +492,22 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
         need -= sh.above;
         equal = sh.equal;
     }
-    const uint32_t threshold = prefix;
-
-    // ---- which slots stay.  Where only some of the keys equal to the threshold do, these take
-    // their ranks in slot order ----
+    __syncthreads();   // the masks
+    // Calls f(i, above, equal) for the warp's steps in order: slots i .. i + 3 above the threshold
+    // and equal to it, as four bits each.
+    auto visit = [&](auto &&f) {
+#pragma unroll 1
+        for (int i0 = lo; i0 < hi; i0 += kWarpSlots) {
+            const uint32_t m = masks[(i0 - cta_lo) / 4 + lane];
+            f(i0 + 4 * lane, m & 15u, m >> 4);
+        }
+    };
+    // Where only some of the keys equal to the threshold stay, these take their ranks in slot order.
     const bool ties = need < equal;
     uint32_t eq_first = 0;   // equal keys before this warp's
     if (ties) {
         uint32_t here = 0;
-        sweep(a.cached, [&](int, const uint4 k) {
-            here += (k.x == threshold) + (k.y == threshold) + (k.z == threshold) +
-                    (k.w == threshold);
-        });
+        visit([&](int, uint32_t, uint32_t eq) { here += __popc(eq); });
         here = __reduce_add_sync(0xffffffffu, here);
         if (lane == 0)
             sh.warp_sum[1][warp] = here;
@@ -445,32 +525,20 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
             eq_first += *cluster.map_shared_rank(&sh.equal_here, c);
     }
     // The kept ones of four slots as four bits; the warp goes together.
-    auto kept = [&](const uint4 k, uint32_t &eq_rank) -> uint32_t {
-        const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
-        uint32_t m = 0;
-        if (!ties) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                m |= (ks[e] >= threshold ? 1u : 0u) << e;
-            return m;
-        }
-        uint32_t eq = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            m |= (ks[e] > threshold ? 1u : 0u) << e;
-            eq |= (ks[e] == threshold ? 1u : 0u) << e;
-        }
+    auto kept = [&](uint32_t gt, uint32_t eq, uint32_t &eq_rank) -> uint32_t {
+        if (!ties)
+            return gt | eq;
         const uint32_t cnt = __popc(eq);
         const uint32_t incl = warp_scan(cnt, lane);
         uint32_t rank = eq_rank + incl - cnt;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if ((eq >> e) & 1u) {
-                m |= (rank < need ? 1u : 0u) << e;
+                gt |= (rank < need ? 1u : 0u) << e;
                 ++rank;
             }
         eq_rank += __shfl_sync(0xffffffffu, incl, 31);
-        return m;
+        return gt;
     };
     auto below_n = [&](int i) -> uint32_t {   // the slots of i .. i + 3 below n, as four bits
         const int b = n - i;
@@ -478,8 +546,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     };
     {
         uint32_t rank = eq_first, gaps = 0, tails = 0;
-        sweep(a.cached, [&](int i, const uint4 k) {
-            const uint32_t m = kept(k, rank), in = below_n(i);
+        visit([&](int i, uint32_t gt, uint32_t eq) {
+            const uint32_t m = kept(gt, eq, rank), in = below_n(i);
             gaps += __popc(in & ~m);
             tails += __popc(m & ~in);
         });
@@ -517,15 +585,12 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     }
     int32_t *dst_list = a.lists + static_cast<size_t>(unit) * 2 * a.list_cap;
     int32_t *src_list = dst_list + a.list_cap;
-    // A free slot gets weight 0 and the position that a token to come will have there.  The slots that
-    // rows move out of become free with the move.
-    const int32_t free_pos = static_cast<int32_t>(static_cast<long long>(last) + 1 - n);
     if (cta == 0 && threadIdx.x == 0)
         a.counts[unit] = make_int2(min(static_cast<int>(moves), a.list_cap), free_pos);
     {
         uint32_t rank = eq_first;
-        sweep(a.cached, [&](int i, const uint4 k) {
-            const uint32_t m = kept(k, rank), in = below_n(i);
+        visit([&](int i, uint32_t gt, uint32_t eq) {
+            const uint32_t m = kept(gt, eq, rank), in = below_n(i);
             uint32_t g = in & ~m, t = m & ~in;
             const uint32_t both = __popc(g) | (__popc(t) << 16);
             const uint32_t incl = warp_scan(both, lane);
@@ -540,25 +605,13 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
                     src_list[f] = i + __ffs(t) - 1;
             gap_at += all & 0xFFFFu;
             tail_at += all >> 16;
-            // What lies below n stays where it is (the moves write over the gaps), and what lies behind
-            // and is not kept is free.
-            if (in == 15u && a.vec) {
-                if (w_out != w_in)
-                    *reinterpret_cast<float4 *>(w_out + i) =
-                        *reinterpret_cast<const float4 *>(w_in + i);
-                if (p_out != p_in)
-                    *reinterpret_cast<int4 *>(p_out + i) = *reinterpret_cast<const int4 *>(p_in + i);
-            } else {
-                for (int e = 0; e < 4; ++e) {
-                    if ((in >> e) & 1u) {
-                        w_out[i + e] = w_in[i + e];
-                        p_out[i + e] = p_in[i + e];
-                    } else if (i + e < hi && !((m >> e) & 1u)) {
+            // in place the kept slots behind n are read by the moves first
+            if (!(w_apart && p_apart))
+                for (int e = 0; e < 4; ++e)
+                    if (i + e < hi && !(((m | in) >> e) & 1u)) {
                         w_out[i + e] = 0.0f;
                         p_out[i + e] = free_pos + i + e;
                     }
-                }
-            }
         });
     }
     for (long long i = static_cast<long long>(N) + cta * kThreads + threadIdx.x; i < a.stride;
@@ -572,18 +625,18 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     }
 }
 
-// CTA = (chunk of kMovesPerCta moves, unit), unit fastest.
+// CTA = (chunk of kMovesPerCta moves, unit), unit fastest, and as many chunks on as the grid has.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Args a, int units)
 {
     pdl_wait();
     pdl_trigger();
     const int unit = blockIdx.x % units;
-    const int j0 = (blockIdx.x / units) * kMovesPerCta + (threadIdx.x >> 5) * kWarpMoves;
     const int2 count = __ldcg(a.counts + unit);
-    const int n = min(kWarpMoves, count.x - j0);
-    if (n > 0)
-        move_rows<D>(a, unit, j0, n, count.y);
+    // (the grid's chunks are counted where they are needed: before the loop, 61 us instead of 57.6)
+    for (int j0 = (blockIdx.x / units) * kMovesPerCta + (threadIdx.x >> 5) * kWarpMoves;
+         j0 < count.x; j0 += gridDim.x / units * kMovesPerCta)
+        move_rows<D>(a, unit, j0, min(kWarpMoves, count.x - j0), count.y);
 }
 
 cudaError_t launch_t(const EvictLaunch &l, const Args &args, cudaStream_t stream)
@@ -593,8 +646,9 @@ cudaError_t launch_t(const EvictLaunch &l, const Args &args, cudaStream_t stream
     // Clusters only where (sequence, kv head) units alone leave SMs idle and rows are long
     // enough to share: a cluster barrier costs more than a CTA's.
     int ctas = 1;
-    while (ctas < kMaxCtas && units * ctas * 2 <= 4LL * current_sm_count() &&
-           l.max_ctx / (ctas * 2) >= 1024)
+    while (ctas < kMaxCtas && (l.max_ctx > ctas * kEvictCtaSlots ||
+                               (units * ctas * 2 <= 4LL * current_sm_count() &&
+                                l.max_ctx / (ctas * 2) >= 1024)))
         ctas *= 2;
     const long long step = static_cast<long long>(kWarpSlots) * kWarps;
     const long long per_cta = (l.max_ctx + step * ctas - 1) / (step * ctas) * step;
@@ -603,23 +657,27 @@ cudaError_t launch_t(const EvictLaunch &l, const Args &args, cudaStream_t stream
     // memory mean two waves of clusters.
     const int sms = current_sm_count();
     const long long per_sm = std::min<long long>(4, (units * ctas + sms - 1) / sms);
-    const long long room = (kSmemPerSm / per_sm - 1024 - static_cast<long long>(sizeof(Shared))) /
-                           4 / kWarpSlots * kWarpSlots;
-    a.cached = static_cast<int>(std::min(per_cta, std::min<long long>(room, kMaxCached)));
-    const size_t smem = static_cast<size_t>(a.cached) * 4 + sizeof(Shared);
-    // Few moves a row are made by the row's own CTA: 64 sequences of 4,096 slots giving up 256 take
-    // 41.7 us against 48.2 with a second launch, one short row 9.1 against 10.9; with thousands of
-    // moves in rows of different lengths it is the other way round (84 against 63 on 64 sequences of
-    // 512 to 4,096 slots cut to 2,048).
-    a.inline_moves = ctas == 1 && l.list_cap <= kInlineMoves;
+    const long long rest = static_cast<long long>(sizeof(Shared)) + per_cta / 4;
+    const long long room =
+        std::max(0LL, kSmemPerSm / per_sm - 1024 - rest) / 4 / kWarpSlots * kWarpSlots;
+    a.cached = static_cast<int>(std::min(per_cta, room));
+    const size_t smem = static_cast<size_t>(a.cached) * 4 + rest;
+    // Few moves a row are made by the row's own CTA, unless the selection's CTAs come in several
+    // rounds: 64 sequences (8 kv heads) of 300 slots cut to 256 take 13.3 us against 18.3 with a second
+    // launch, of 512 cut to 400 16.4 against 22.6, of 4,096 cut to 3,840 44.0 against 48.5; with 512
+    // cut to 256 it is 24.6 against 23.8, with 1,024 cut to 512 43.7 against 40.9, and on 256 sequences
+    // of 512 cut to 448 69.6 against 62.4.
+    a.inline_moves = ctas == 1 && l.list_cap <= kInlineMoves && units <= 1LL * kInlineUnits * sms;
     auto select = l.head_dim == 128 ? select_kernel<128> : select_kernel<64>;
     auto move = l.head_dim == 128 ? move_kernel<128> : move_kernel<64>;
     cudaError_t err =
         cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxCached * 4 + static_cast<int>(sizeof(Shared)));
+                             static_cast<int>(kSmemPerCta));
     if (err != cudaSuccess)
         return err;
-    const long long chunks = (l.list_cap + kMovesPerCta - 1) / kMovesPerCta;
+    const long long chunks =
+        std::min((l.list_cap + kMovesPerCta - 1LL) / kMovesPerCta,
+                 std::max(1LL, static_cast<long long>(kMoveCtas) * sms / units));
     if (units * ctas > 0x7FFFFFFFLL || units * chunks > 0x7FFFFFFFLL)
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};

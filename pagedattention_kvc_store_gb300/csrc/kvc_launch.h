@@ -150,7 +150,8 @@ cudaError_t read_and_clear_weights_errors(uint32_t *flags);
 
 // kvc_evict: the moves of each (sequence, kv head), lists [S][Hkv][2][list_cap] and counts
 // [S][Hkv][2].
-constexpr int kMaxCached = 48 * 1024;   // keys that a CTA keeps in shared memory
+constexpr int kEvictCtaSlots = 1 << 19;   // slots of one CTA (masks of 2 bits each)
+constexpr int kEvictMaxCtx = 1 << 22;     // slots of a row: 8 CTAs
 struct EvictLaunch {
     void *k_pool, *v_pool;
     const int32_t *block_table;

@@ -343,9 +343,10 @@ def test_evict_clusters_in_quick_succession():
     assert kvc.kvc_device_errors() == 0
 
 
-def test_evict_more_slots_than_the_cache_of_keys():
-    """A row of 400,000 slots over 8 CTAs: more than they keep in shared memory."""
-    n, P = 400000, 64
+@pytest.mark.parametrize("n", [400000, 1200000])
+def test_evict_more_slots_than_the_cache_of_keys(n):
+    """Rows over 8 CTAs that hold more slots than these keep in shared memory."""
+    P = 64
     S = 1
     pages = n // P + 1
     rng = np.random.default_rng(9)

@@ -115,12 +115,12 @@ def test_plans():
     assert (s, c) == kvc.kvc_decode_plan(64, 32, pool, 4096)[:2]
     assert ws >= 64 * 32 * (s * 130 + s * c) * 4
     assert kvc.kvc_decode_weights_plan(4, 32, pool, 10, 1)[2] > 0
-    for call in (lambda n: kvc.kvc_evict_plan(1, pool, n, 5),
-                 lambda n: kvc.kvc_decode_weights_plan(1, 8, pool, n, 0),
-                 lambda n: kvc.kvc_decode_int4_plan(1, 8, pool, n, 0)):
-        call(1 << 30)
-        with pytest.raises(RuntimeError, match="2\\^30"):
-            call((1 << 30) + 1)
+    for most, call in ((22, lambda n: kvc.kvc_evict_plan(1, pool, n, 5)),
+                       (30, lambda n: kvc.kvc_decode_weights_plan(1, 8, pool, n, 0)),
+                       (30, lambda n: kvc.kvc_decode_int4_plan(1, 8, pool, n, 0))):
+        call(1 << most)
+        with pytest.raises(RuntimeError, match=f"2\\^{most}"):
+            call((1 << most) + 1)
 
 
 def test_binding_refuses_cpu_tensors():
