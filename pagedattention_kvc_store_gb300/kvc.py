@@ -8,6 +8,7 @@ library or a GPU these functions raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Tuple
@@ -180,6 +181,11 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _cuda(name: str, t: torch.Tensor, dtype=None, contiguous=True) -> torch.Tensor:
+    try:   # what nearly every call passes, with as few steps as say so
+        if t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+            return t
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
@@ -194,6 +200,11 @@ def _cuda(name: str, t: torch.Tensor, dtype=None, contiguous=True) -> torch.Tens
 def _reachable(name: str, t: torch.Tensor, dtype=None) -> torch.Tensor:
     """An argument the kernels may reach in host memory: a CUDA tensor, or a pinned host
     tensor that they read or write across the host link directly."""
+    try:
+        if t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+            return t
+    except AttributeError:
+        pass
     if isinstance(t, torch.Tensor) and not t.is_cuda:
         if not t.is_pinned():
             raise ValueError(f"{name} must be a CUDA tensor or a pinned host tensor")
@@ -380,38 +391,51 @@ def kvc_append_int8(out: torch.Tensor, q: torch.Tensor, k_codes: torch.Tensor,
         int(max_ctx), int(q.shape[1]), float(scale), _stream(stream)))
 
 
+def _desc(num_pages, a, b, head_dim, layout):
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout {layout!r}: 'nhd' or 'hnd'")
+    page_size, kv_heads = (a, b) if layout == "nhd" else (b, a)
+    return PoolDesc(num_pages, page_size, kv_heads, head_dim, LAYOUTS[layout])
+
+
 def int4_pool_desc(k_codes: torch.Tensor, layout: str = "nhd") -> PoolDesc:
     """Descriptor of a 4-bit code pool: uint8 [num_pages, page_size, kv_heads, head_dim / 2]
     (layout "nhd") or [num_pages, kv_heads, page_size, head_dim / 2] (layout "hnd")."""
     if k_codes.dim() != 4 or k_codes.dtype != torch.uint8:
         raise ValueError("4-bit codes are a uint8 4-D tensor")
-    if layout not in LAYOUTS:
-        raise ValueError(f"layout {layout!r}: 'nhd' or 'hnd'")
     n, a, b, d = k_codes.shape
-    page_size, kv_heads = (a, b) if layout == "nhd" else (b, a)
-    return PoolDesc(n, page_size, kv_heads, 2 * d, LAYOUTS[layout])
+    return _desc(n, a, b, 2 * d, layout)
 
 
-def _int4_pools(k_codes, v_codes, k_params, v_params, layout):
-    pool = int4_pool_desc(_cuda("k_codes", k_codes, torch.uint8), layout)
-    _cuda("v_codes", v_codes, torch.uint8)
-    _cuda("k_params", k_params, torch.bfloat16)
-    _cuda("v_params", v_params, torch.bfloat16)
-    if v_codes.shape != k_codes.shape:
+# The shape checks below see nothing but shapes, and steps repeat theirs: the answers are kept.
+@functools.lru_cache(maxsize=256)
+def _int4_shapes(k_codes, v_codes, k_params, v_params, layout):
+    if len(k_codes) != 4:
+        raise ValueError("4-bit codes are a uint8 4-D tensor")
+    pool = _desc(*k_codes[:3], 2 * k_codes[3], layout)
+    if v_codes != k_codes:
         raise ValueError("k_codes and v_codes differ in shape")
     want = (pool.num_pages, pool.kv_heads, pool.page_size, pool.head_dim // 64, 2)
-    if k_params.shape != want or v_params.shape != want:
+    if k_params != want or v_params != want:
         raise ValueError(f"parameters are [num_pages, kv_heads, page_size, head_dim / 64, 2] "
                          f"= {want}")
     return pool
 
 
-def _new_vectors(name, t, pool, num_tokens, dtype=None):
-    _cuda(name, t, dtype)
-    want = (num_tokens, pool.kv_heads, pool.head_dim)
-    if t.shape != want:
-        raise ValueError(f"{name} is [num_tokens, kv_heads, head_dim] = {want}, "
-                         f"got {tuple(t.shape)}")
+def _int4_pools(k_codes, v_codes, k_params, v_params, layout):
+    _cuda("k_codes", k_codes, torch.uint8)
+    _cuda("v_codes", v_codes, torch.uint8)
+    _cuda("k_params", k_params, torch.bfloat16)
+    _cuda("v_params", v_params, torch.bfloat16)
+    return _int4_shapes(k_codes.shape, v_codes.shape, k_params.shape, v_params.shape, layout)
+
+
+@functools.lru_cache(maxsize=256)
+def _vector_shapes(k, v, kv_heads, head_dim, num_tokens):
+    want = (num_tokens, kv_heads, head_dim)
+    if k != want or v != want:
+        raise ValueError(f"vectors are [num_tokens, kv_heads, head_dim] = {want}, "
+                         f"got {tuple(k)} and {tuple(v)}")
 
 
 def kvc_store_int4(k_codes: torch.Tensor, v_codes: torch.Tensor, k_params: torch.Tensor,
@@ -423,8 +447,9 @@ def kvc_store_int4(k_codes: torch.Tensor, v_codes: torch.Tensor, k_params: torch
     pool = _int4_pools(k_codes, v_codes, k_params, v_params, layout)
     _cuda("slot_mapping", slot_mapping, torch.int32)
     T = slot_mapping.numel()
-    _new_vectors("k_new", k_new, pool, T, torch.bfloat16)
-    _new_vectors("v_new", v_new, pool, T, torch.bfloat16)
+    _cuda("k_new", k_new, torch.bfloat16)
+    _cuda("v_new", v_new, torch.bfloat16)
+    _vector_shapes(k_new.shape, v_new.shape, pool.kv_heads, pool.head_dim, T)
     _check("kvc_store_int4", lib().kvc_store_int4(
         _ptr(k_codes), _ptr(v_codes), _ptr(k_params), _ptr(v_params), pool, _ptr(k_new),
         _ptr(v_new), _ptr(slot_mapping), T, _stream(stream)))
@@ -438,8 +463,9 @@ def kvc_load_int4(k_out: torch.Tensor, v_out: torch.Tensor, k_codes: torch.Tenso
     pool = _int4_pools(k_codes, v_codes, k_params, v_params, layout)
     _cuda("slot_mapping", slot_mapping, torch.int32)
     T = slot_mapping.numel()
-    _new_vectors("k_out", k_out, pool, T)
-    _new_vectors("v_out", v_out, pool, T, k_out.dtype)
+    _cuda("k_out", k_out)
+    _cuda("v_out", v_out, k_out.dtype)
+    _vector_shapes(k_out.shape, v_out.shape, pool.kv_heads, pool.head_dim, T)
     _check("kvc_load_int4", lib().kvc_load_int4(
         _ptr(k_out), _ptr(v_out), _out_dtype(k_out), _ptr(k_codes), _ptr(v_codes),
         _ptr(k_params), _ptr(v_params), pool, _ptr(slot_mapping), T, _stream(stream)))
@@ -456,15 +482,16 @@ def kvc_decode_int4_plan(num_seqs: int, q_heads: int, pool: PoolDesc, max_ctx: i
     return splits.value, chunk.value, ws.value
 
 
-def _decode_shapes(out, q, block_table, context_lens, pool):
+@functools.lru_cache(maxsize=256)
+def _decode_shapes(out, q, block_table, context_lens, head_dim):
     """Shapes of a decode call's per-step arguments against the pool; the number of sequences."""
-    S = context_lens.shape[0]
-    if q.dim() != 3 or q.shape[0] != S or q.shape[2] != pool.head_dim:
+    S = context_lens[0]
+    if len(q) != 3 or q[0] != S or q[2] != head_dim:
         raise ValueError(f"q is [num_seqs, q_heads, head_dim] with {S} sequences and head_dim "
-                         f"{pool.head_dim}, got {tuple(q.shape)}")
-    if out.shape != q.shape:
-        raise ValueError(f"out is {tuple(q.shape)}, got {tuple(out.shape)}")
-    if block_table.dim() != 2 or block_table.shape[0] != S:
+                         f"{head_dim}, got {tuple(q)}")
+    if out != q:
+        raise ValueError(f"out is {tuple(q)}, got {tuple(out)}")
+    if len(block_table) != 2 or block_table[0] != S:
         raise ValueError("block_table is [num_seqs, pages]")
     return S
 
@@ -481,7 +508,7 @@ def kvc_decode_int4(out: torch.Tensor, q: torch.Tensor, k_codes: torch.Tensor,
     _reachable("q", q, torch.bfloat16)
     _reachable("block_table", block_table, torch.int32)
     _reachable("context_lens", context_lens, torch.int32)
-    S = _decode_shapes(out, q, block_table, context_lens, pool)
+    S = _decode_shapes(out.shape, q.shape, block_table.shape, context_lens.shape, pool.head_dim)
     ws = 0
     if workspace is not None:
         _cuda("workspace", workspace)
@@ -578,13 +605,19 @@ def kvc_decode_weights_plan(num_seqs: int, q_heads: int, pool: PoolDesc, max_ctx
     return splits.value, chunk.value, ws.value
 
 
-def _weight_rows(name, t, dtype, pool, like=None):
-    """An array [rows, kv_heads, stride] that goes with the pools."""
-    _cuda(name, t, dtype)
-    if t.dim() != 3 or t.shape[1] != pool.kv_heads or (like is not None and t.shape != like.shape):
-        raise ValueError(f"{name} is [rows, kv_heads = {pool.kv_heads}, stride], the same for "
-                         f"every such argument; got {tuple(t.shape)}")
-    return t
+@functools.lru_cache(maxsize=256)
+def _pool_shapes(k_pool, v_pool, layout, *rows):
+    """Descriptor of a bf16 pool whose arrays have these shapes; rows: of arrays that go with it."""
+    if len(k_pool) != 4:
+        raise ValueError("a pool is a 4-D tensor")
+    pool = _desc(*k_pool, layout)
+    if v_pool != k_pool:
+        raise ValueError("k_pool and v_pool differ in shape")
+    for shape in rows:
+        if len(shape) != 3 or shape[1] != pool.kv_heads or shape != rows[0]:
+            raise ValueError(f"weights and positions are [rows, kv_heads = {pool.kv_heads}, stride], "
+                             f"all the same; got {[tuple(s) for s in rows]}")
+    return pool
 
 
 def _sequence_rows(weight_rows, S):
@@ -610,16 +643,17 @@ def kvc_decode_weights(out: torch.Tensor, weights: torch.Tensor, q: torch.Tensor
     _cuda("v_pool", v_pool, torch.bfloat16)
     _reachable("block_table", block_table, torch.int32)
     _reachable("context_lens", context_lens, torch.int32)
-    pool = pool_desc(k_pool, layout)
-    S = _decode_shapes(out, q, block_table, context_lens, pool)
-    _weight_rows("weights", weights, torch.float32, pool)
+    _cuda("weights", weights, torch.float32)
+    rows = weights.shape
+    pool = _pool_shapes(k_pool.shape, v_pool.shape, layout, rows)
+    S = _decode_shapes(out.shape, q.shape, block_table.shape, context_lens.shape, pool.head_dim)
     ws = 0
     if workspace is not None:
         _cuda("workspace", workspace)
         ws = workspace.numel() * workspace.element_size()
     _check("kvc_decode_weights", lib().kvc_decode_weights(
         _ptr(out), _out_dtype(out), _ptr(weights), _sequence_rows(weight_rows, S),
-        weights.shape[0], weights.shape[2], _ptr(q), _ptr(k_pool), _ptr(v_pool), pool,
+        rows[0], rows[2], _ptr(q), _ptr(k_pool), _ptr(v_pool), pool,
         _ptr(block_table), block_table.shape[1], _ptr(context_lens), S, int(max_ctx), q.shape[1],
         float(scale), int(num_splits), _ptr(workspace), ws, _stream(stream)))
 
@@ -645,27 +679,27 @@ def kvc_evict(k_pool: torch.Tensor, v_pool: torch.Tensor, weights_out: torch.Ten
     positions_out written; passing the same tensors does it in place."""
     _cuda("k_pool", k_pool, torch.bfloat16)
     _cuda("v_pool", v_pool, torch.bfloat16)
-    pool = pool_desc(k_pool, layout)
-    if v_pool.shape != k_pool.shape:
-        raise ValueError("k_pool and v_pool differ in shape")
-    _weight_rows("weights", weights, torch.float32, pool)
-    _weight_rows("weights_out", weights_out, torch.float32, pool, weights)
-    _weight_rows("positions", positions, torch.int32, pool, weights)
-    _weight_rows("positions_out", positions_out, torch.int32, pool, weights)
+    _cuda("weights", weights, torch.float32)
+    _cuda("weights_out", weights_out, torch.float32)
+    _cuda("positions", positions, torch.int32)
+    _cuda("positions_out", positions_out, torch.int32)
+    rows = weights.shape
+    pool = _pool_shapes(k_pool.shape, v_pool.shape, layout, rows, weights_out.shape,
+                        positions.shape, positions_out.shape)
     _cuda("block_table", block_table, torch.int32)
     _cuda("context_lens", context_lens, torch.int32)
     _cuda("new_lens", new_lens, torch.int32)
-    S = context_lens.shape[0]
-    if new_lens.numel() != S or block_table.dim() != 2 or block_table.shape[0] != S:
+    S, table = context_lens.shape[0], block_table.shape
+    if new_lens.numel() != S or len(table) != 2 or table[0] != S:
         raise ValueError("new_lens is [num_seqs] and block_table [num_seqs, pages]")
     ws = 0
     if workspace is not None:
         _cuda("workspace", workspace)
         ws = workspace.numel() * workspace.element_size()
     _check("kvc_evict", lib().kvc_evict(
-        _ptr(k_pool), _ptr(v_pool), pool, _ptr(block_table), block_table.shape[1],
+        _ptr(k_pool), _ptr(v_pool), pool, _ptr(block_table), table[1],
         _ptr(context_lens), S, int(max_ctx), _ptr(weights), _ptr(positions), _ptr(weights_out),
-        _ptr(positions_out), _sequence_rows(weight_rows, S), weights.shape[0], weights.shape[2],
+        _ptr(positions_out), _sequence_rows(weight_rows, S), rows[0], rows[2],
         int(budget), int(recent), _ptr(new_lens), _ptr(workspace), ws, _stream(stream)))
 
 
