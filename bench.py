@@ -233,7 +233,7 @@ PROFILE_SOURCES = {
     "append_int8_rewind_p16": ("kvc_append_int8.cu", "kvc_append_items.cuh", "kvc_device.cuh"),
     "append_rewind_p64": ("kvc_append_tc.cu", "kvc_append_items.cuh", "kvc_device.cuh"),
     "long_decode": ("kvc_decode.cu", "kvc_decode_cta.cuh", "kvc_device.cuh"),
-    "merge_long_decode": ("kvc_decode.cu", "kvc_device.cuh"),
+    "merge_long_decode": ("kvc_decode.cu", "kvc_decode_cta.cuh", "kvc_device.cuh"),
     "store_rewind": ("kvc_store.cu", "kvc_device.cuh"),
 }
 

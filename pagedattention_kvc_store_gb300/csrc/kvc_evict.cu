@@ -49,6 +49,9 @@ namespace cg = cooperative_groups;
 
 __device__ uint32_t g_evict_errors;
 
+// Device error bit of this kernel alone: a row's last slot does not hold its newest position.
+constexpr uint32_t kErrPositionOrder = 1u << 13;
+
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
