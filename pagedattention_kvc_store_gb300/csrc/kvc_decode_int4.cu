@@ -894,8 +894,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, int W>
 __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) merge_int4_kernel(const Args a)
 {
-    pdl_wait();
-    pdl_trigger();
     constexpr int V = D / 32;
     constexpr int kRows = W == 1 ? 4 : 1;
     constexpr int kPre = 4;
@@ -910,13 +908,17 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) merge_int4_kernel(const
     const int h = row - s * a.q_heads;
     const int G = a.group;
     const int kvh = h / G;
-    const int ctx = clamped_ctx(a, s);
+    // Before the wait: this launch starts once every CTA of the decode has triggered, which they do
+    // after their own wait, so what ran before the decode is done.
+    const int raw = __ldcg(a.context_lens + s);
+    pdl_wait();
+    pdl_trigger();
+    const int2 info = __ldcg(a.unit_info + static_cast<size_t>(s) * a.kv_heads + kvh);
     float acc[V], sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
         acc[v] = 0.0f;
-    if (ctx > 0) {
-        const int2 info = __ldcg(a.unit_info + static_cast<size_t>(s) * a.kv_heads + kvh);
+    if (raw > 0) {
         // (a sequence whose context changes while the decode runs may have left no such slots)
         const int count =
             info.x >= 0 && info.y <= a.kv_heads * (a.num_seqs + a.runs) - info.x ? info.y : 0;
