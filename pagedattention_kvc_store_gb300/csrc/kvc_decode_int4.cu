@@ -9,10 +9,8 @@
 // Codes as operands.  A word's eight nibbles become four fp16 pairs with one AND each (and one
 // shift): the bits of a nibble alone are the fp16 subnormal u 2^-24 (u 2^-20 for the high nibble
 // of a byte), which the tensor cores take exactly; no bias has to be added or taken out.  For
-// K the two weights are evened out in the query (the dims in low nibbles carry 16 q); V's rows
-// accumulate whole bytes (low + 16 high, also an exact subnormal) and high nibbles, and the low
-// ones are their difference at the end.  Putting the nibble under an exponent and subtracting
-// the bias would double the conversion.  Query rows
+// K the two weights are evened out in the query (the dims in low nibbles carry 16 q), for V at the
+// end.  Putting the nibble under an exponent and subtracting the bias would double the conversion.  Query rows
 // enter as fp16 scaled by a power of two of their own (largest |q| in [2^9, 2^10), so bf16's
 // eight bits are exact wherever they matter); probabilities times value scales as fp16 scaled by a
 // power of two that follows the largest value scale seen (vnorm), because a scale may have any
@@ -554,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int v_off = code_offset<D>(lane & 15, lane >> 4);
 
     uint32_t qb[NG][2][2][2];   // B fragments: [group][word][nibble][register]
-    float o[NC][2][4];          // O^T: [32 dims][whole byte, high half][fragment]
+    float o[NC][2][4];          // O^T: [32 dims][low nibble, high nibble][fragment]
     float zacc[NG][2];          // sum of p lo, heads 2 t and 2 t + 1
     // heads 2 t and 2 t + 1: the sum; the maximum in use times f, and the y from which it moves
     float l_run[2], mf[2], m_thr[2], f[2], hq[NG][2];
@@ -788,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 
         // ---- probabilities, and out ----
-        const uint32_t vb = ring32 + stage * group_stage + v_codes + head_codes;
+        uint32_t pb[kTiles][NG][2];   // B fragments of the PV product
 #pragma unroll
         for (int T = 0; T < kTiles; ++T) {
             float p[2][2];
@@ -799,7 +797,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p[i][j] = fast_exp2(fmaf(y[T][i][j], f[j], -mf[j]));
                     l_run[j] += p[i][j];
                 }
-            uint32_t pb[NG][2];   // B fragments of the PV product
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -808,26 +805,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float lo = __uint_as_float(vp[T][i][g] & 0xFFFF0000u);
                     zacc[g][0] = fmaf(p[i][0], lo, zacc[g][0]);
                     zacc[g][1] = fmaf(p[i][1], lo, zacc[g][1]);
-                    pb[g][i] = movmatrix_trans(pack_f16x2(p[i][0] * sc, p[i][1] * sc));
+                    pb[T][g][i] = movmatrix_trans(pack_f16x2(p[i][0] * sc, p[i][1] * sc));
                 }
-            const uint32_t va = vb + (T & 1) * codes1 + (T >> 1) * codes2;
+        }
+        // The tensor cores cut their sums off instead of rounding them, all terms here are positive,
+        // and the sum of minima takes most of the result away again: over thousands of products
+        // the cuts add up to a part of what is left.  So a product's sum is a block's, and blocks are
+        // added up with rounding.
+        const uint32_t vb = ring32 + stage * group_stage + v_codes + head_codes;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {   // chunks 2 g and 2 g + 1
+        for (int g = 0; g < NG; ++g) {   // chunks 2 g and 2 g + 1
+            float part[2][2][4];
+#pragma unroll
+            for (int T = 0; T < kTiles; ++T) {
+                const uint32_t va = vb + (T & 1) * codes1 + (T >> 1) * codes2;
                 uint32_t e[4];
                 ldsm_x2_trans_b8(va + (v_off ^ (32 * g)), e[0], e[1], e[2], e[3]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    // whole bytes (low + 16 high) and their high halves: one operation a pair
-                    // each, where the low halves would also need the shift
                     const uint32_t x0 = e[2 * k], x1 = e[2 * k + 1];
-                    const uint32_t z0 = __byte_perm(x0, 0u, 0x4341u);   // bytes 1 and 3
-                    const uint32_t z1 = __byte_perm(x1, 0u, 0x4341u);
-                    mma_f16_16816(o[2 * g + k][0], x0 & 0x00FF00FFu, x1 & 0x00FF00FFu, z0, z1,
-                                  pb[g][0], pb[g][1]);
-                    mma_f16_16816(o[2 * g + k][1], x0 & 0x00F000F0u, x1 & 0x00F000F0u,
-                                  z0 & 0x00F000F0u, z1 & 0x00F000F0u, pb[g][0], pb[g][1]);
+                    const uint32_t z0 = x0 >> 8, z1 = x1 >> 8;
+                    if (T == 0) {
+                        mma_f16_16816_zero(part[k][0], x0 & 0x000F000Fu, x1 & 0x000F000Fu,
+                                           z0 & 0x000F000Fu, z1 & 0x000F000Fu, pb[T][g][0],
+                                           pb[T][g][1]);
+                        mma_f16_16816_zero(part[k][1], x0 & 0x00F000F0u, x1 & 0x00F000F0u,
+                                           z0 & 0x00F000F0u, z1 & 0x00F000F0u, pb[T][g][0],
+                                           pb[T][g][1]);
+                    } else {
+                        mma_f16_16816(part[k][0], x0 & 0x000F000Fu, x1 & 0x000F000Fu,
+                                      z0 & 0x000F000Fu, z1 & 0x000F000Fu, pb[T][g][0], pb[T][g][1]);
+                        mma_f16_16816(part[k][1], x0 & 0x00F000F0u, x1 & 0x00F000F0u,
+                                      z0 & 0x00F000F0u, z1 & 0x00F000F0u, pb[T][g][0], pb[T][g][1]);
+                    }
                 }
             }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[2 * g + k][b][i] += part[k][b][i];
         }
 
         __syncwarp();
@@ -863,9 +882,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 2; ++i) {   // dims 32 n + 16 i + 2 r, + 1
                             const float z = zacc[n / 2][j];
                             float2 v;
-                            const float whole_byte = o[n][0][2 * i + j], high = o[n][1][2 * i + j];
-                            v.x = fmaf((whole_byte - high) * 16777216.0f, v_inv, z) * inv[j];
-                            v.y = fmaf(high * 1048576.0f, v_inv, z) * inv[j];
+                            v.x = fmaf(o[n][0][2 * i + j] * 16777216.0f, v_inv, z) * inv[j];
+                            v.y = fmaf(o[n][1][2 * i + j] * 1048576.0f, v_inv, z) * inv[j];
                             const int dim = 32 * n + 16 * i + 2 * r;
                             if (whole)
                                 store_out2(a.out, a.out_f32, (row0 + head) * D + dim, v);

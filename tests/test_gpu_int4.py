@@ -320,6 +320,24 @@ def test_long_context_few_sequences():
         check(case, got, ref, pools, f"long {splits}")
 
 
+@pytest.mark.parametrize("D,splits", [(64, 1), (64, 0), (128, 1)])
+def test_long_sums_are_rounded_not_cut(D, splits):
+    """A query of zeros over 100,000 positions: the output is the mean of V, a small remainder of
+    sum(u) scale and the minima.  No probability is rounded (scales are exact in fp16).  A block's
+    products are cut at most 4 times, 2^-23 each, and add 2^-21 R to the mean; the sums over blocks and
+    the minima's over the positions of a thread (an eighth of all) are rounded, errors that grow with
+    the root of their number: 2^-24 sqrt(N / 8) of R and V; the division and the rest 2^-22 V."""
+    case = ragged(24, 64, 1, 2, D, [100001])
+    pools = filled(case)
+    q = np.zeros_like(case.q)
+    ref = int4.attention(q, *pools, case.block_table, case.context_lens)
+    got = run_decode(q, pools, case.block_table, case.context_lens, case.max_ctx, splits)
+    vp = int4.bf16_value(pools[3]).astype(np.float64)
+    R, V = np.nanmax(15 * vp[..., 0]), np.nanmax(np.abs(vp[..., 1]))
+    rms = np.sqrt(((got - ref) ** 2).mean())
+    assert rms <= 2.0 ** -21 * R + 2.0 ** -24 * math.sqrt(100001 / 8) * (R + V) + 2.0 ** -22 * V
+
+
 def test_the_result_is_the_same_every_time():
     case = ragged(29, 16, 8, 4, 128, lambda rng: rng.integers(1, 3000, size=20))
     pools = device_pools(filled(case))
