@@ -26,9 +26,10 @@
 // sequence's length and first ids, are requested blocks ahead.  A TMA operation costs the SM about 85 cycles
 // whatever its size (1 and 2 KB boxes, one warp's heads apiece, took 84 us on the batched decode,
 // and 16-byte cp.async by every warp 56: their addresses were a quarter of its instructions).
-// Eight warps with 168 registers each, not 16 with 104: the products' operands and sums spill below
-// about 120, and a warp has 64 positions' independent products to overlap (16 warps with 32-position
-// stages: 61 us on the batched decode, 251 on the long one; as it is 41.6 and 149.6).
+// Eight warps with 216 registers each, not 16 with 104: the products' operands and sums spill below
+// about 200, and a warp has 64 positions' independent products to overlap (16 warps with 32-position
+// stages: 61 us on the batched decode, 251 on the long one; 8 warps that the compiler held to 168
+// registers 43.3 and 162; as it is 41.6 and 153).
 // Consumer warps never wait for one another except through a stage's release.  A piece (the blocks
 // of one sequence in a run) that is all of its sequence writes the output rows, the others a
 // partial, merged by a second launch.
@@ -41,7 +42,7 @@
 // rows r and r + 8 are positions 2 r and 2 r + 1.
 //
 // Bound: HBM, 2 (D / 2 + D / 16) bytes a position and kv head.  8 sequences of up to 131,072 positions
-// (920 MB): 149.6 us, 6.15 TB/s, 91% of the measured copy.  64 sequences of up to 4,096 (172 MB): 41.6 us,
+// (920 MB): 153 us, 6.0 TB/s, 89% of the measured copy.  64 sequences of up to 4,096 (172 MB): 41.6 us,
 // of which 26 are streaming; the rest is the start (the cut of the runs, page ids and the first copies
 // one after the other, 5 us), runs that end apart, and the merge's launch.
 #include <math.h>
@@ -56,7 +57,13 @@ namespace {
 __device__ uint32_t g_decode_int4_errors;
 
 constexpr int kWarps = kInt4Warps;   // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;   // and the producer
+// ... and the producer's, in a warpgroup of its own: three of four have nothing to do, but registers move
+// between whole warpgroups.  A block is launched with 168 a thread (an SM quarter's 16,384 hold three
+// warps of up to 170); the producer's four warps keep 72 of them and the consumers get 216:
+// 128 * 72 + 256 * 216 = 384 * 168.
+constexpr int kThreads = (kWarps + 4) * 32;
+constexpr int kProducerRegs = 72, kConsumerRegs = 216;
+static_assert(128 * kProducerRegs + kWarps * 32 * kConsumerRegs <= kThreads * 168, "registers");
 constexpr int kBlock = kInt4Block;   // positions of one ring stage
 constexpr int kTiles = kBlock / 16;  // of 16 positions, the rows of a product
 constexpr float kLn2 = 0.6931471805599453f;
@@ -361,6 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *ring = smem + grp * NS * group_stage;
 
     if (warp >= kWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" : : "n"(kProducerRegs));
+        if (warp > kWarps)
+            return;
         // ------------- producer: lanes 4 g .. 4 g + 3 fill group g's ring, a page each -------------
         const int P = 1 << a.log2_page;
         const int box = min(P, kBlock);               // positions of a TMA box
@@ -516,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // ------------------------------------ consumers ------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" : : "n"(kConsumerRegs));
     const int in_group = warp - grp * HW;
     const int kvh = head0 + in_group;
     if (run_len <= 0) {
@@ -786,7 +797,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 
         // ---- probabilities, and out ----
-        uint32_t pb[kTiles][NG][2];   // B fragments of the PV product
+        // The tensor cores cut their sums off instead of rounding them, all terms here are positive,
+        // and the sum of minima takes most of the result away again: over thousands of products
+        // the cuts would add up to a part of what is left (a fifth of the output's norm at 131,072
+        // positions).  So their sums are a block's, and the blocks are added up with rounding.
+        const uint32_t vb = ring32 + stage * group_stage + v_codes + head_codes;
+        float part[NC][2][4];
 #pragma unroll
         for (int T = 0; T < kTiles; ++T) {
             float p[2][2];
@@ -797,6 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p[i][j] = fast_exp2(fmaf(y[T][i][j], f[j], -mf[j]));
                     l_run[j] += p[i][j];
                 }
+            uint32_t pb[NG][2];   // B fragments of the PV product
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -805,20 +822,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float lo = __uint_as_float(vp[T][i][g] & 0xFFFF0000u);
                     zacc[g][0] = fmaf(p[i][0], lo, zacc[g][0]);
                     zacc[g][1] = fmaf(p[i][1], lo, zacc[g][1]);
-                    pb[T][g][i] = movmatrix_trans(pack_f16x2(p[i][0] * sc, p[i][1] * sc));
+                    pb[g][i] = movmatrix_trans(pack_f16x2(p[i][0] * sc, p[i][1] * sc));
                 }
-        }
-        // The tensor cores cut their sums off instead of rounding them, all terms here are positive,
-        // and the sum of minima takes most of the result away again: over thousands of products
-        // the cuts add up to a part of what is left.  So a product's sum is a block's, and blocks are
-        // added up with rounding.
-        const uint32_t vb = ring32 + stage * group_stage + v_codes + head_codes;
+            const uint32_t va = vb + (T & 1) * codes1 + (T >> 1) * codes2;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {   // chunks 2 g and 2 g + 1
-            float part[2][2][4];
-#pragma unroll
-            for (int T = 0; T < kTiles; ++T) {
-                const uint32_t va = vb + (T & 1) * codes1 + (T >> 1) * codes2;
+            for (int g = 0; g < NG; ++g) {   // chunks 2 g and 2 g + 1
                 uint32_t e[4];
                 ldsm_x2_trans_b8(va + (v_off ^ (32 * g)), e[0], e[1], e[2], e[3]);
 #pragma unroll
@@ -826,28 +834,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t x0 = e[2 * k], x1 = e[2 * k + 1];
                     const uint32_t z0 = x0 >> 8, z1 = x1 >> 8;
                     if (T == 0) {
-                        mma_f16_16816_zero(part[k][0], x0 & 0x000F000Fu, x1 & 0x000F000Fu,
-                                           z0 & 0x000F000Fu, z1 & 0x000F000Fu, pb[T][g][0],
-                                           pb[T][g][1]);
-                        mma_f16_16816_zero(part[k][1], x0 & 0x00F000F0u, x1 & 0x00F000F0u,
-                                           z0 & 0x00F000F0u, z1 & 0x00F000F0u, pb[T][g][0],
-                                           pb[T][g][1]);
+                        mma_f16_16816_zero(part[2 * g + k][0], x0 & 0x000F000Fu, x1 & 0x000F000Fu,
+                                           z0 & 0x000F000Fu, z1 & 0x000F000Fu, pb[g][0], pb[g][1]);
+                        mma_f16_16816_zero(part[2 * g + k][1], x0 & 0x00F000F0u, x1 & 0x00F000F0u,
+                                           z0 & 0x00F000F0u, z1 & 0x00F000F0u, pb[g][0], pb[g][1]);
                     } else {
-                        mma_f16_16816(part[k][0], x0 & 0x000F000Fu, x1 & 0x000F000Fu,
-                                      z0 & 0x000F000Fu, z1 & 0x000F000Fu, pb[T][g][0], pb[T][g][1]);
-                        mma_f16_16816(part[k][1], x0 & 0x00F000F0u, x1 & 0x00F000F0u,
-                                      z0 & 0x00F000F0u, z1 & 0x00F000F0u, pb[T][g][0], pb[T][g][1]);
+                        mma_f16_16816(part[2 * g + k][0], x0 & 0x000F000Fu, x1 & 0x000F000Fu,
+                                      z0 & 0x000F000Fu, z1 & 0x000F000Fu, pb[g][0], pb[g][1]);
+                        mma_f16_16816(part[2 * g + k][1], x0 & 0x00F000F0u, x1 & 0x00F000F0u,
+                                      z0 & 0x00F000F0u, z1 & 0x00F000F0u, pb[g][0], pb[g][1]);
                     }
                 }
             }
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o[2 * g + k][b][i] += part[k][b][i];
         }
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[n][b][i] += part[n][b][i];
 
         __syncwarp();
         if (lane == 0)
