@@ -197,7 +197,9 @@ bool partly_overlap(const void *a, const void *b, uint64_t bytes)
 // 4-bit decode plan, as the INT8 one, with 64-position blocks and one warp per run and kv head: by
 // default as many runs as one wave of the kernel's CTAs (one per SM) holds, and for contexts of at
 // most two blocks one run per sequence, which needs no merge: 4 sequences of up to 128 positions
-// take 7.8 us against 9.3 (1,000: 15.8 against 18.1); at 256 positions it is 10.9 against 9.5.
+// take 7.8 us against 9.3 (1,000: 15.8 against 18.1).  Above it depends on how many there are: at up to
+// 192 positions (8 kv heads) 4 take 9.4 against 8.9 and 64 9.8 against 12.7, at 256 10.9 against 9.2
+// and 11.4 against 12.9, at 512 17.6 against 11.2 and 18.5 against 17.1.
 constexpr int kInt4WholeCtx = 2 * kvc::kInt4Block;
 
 struct Int4Plan {

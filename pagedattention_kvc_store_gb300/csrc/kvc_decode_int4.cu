@@ -10,8 +10,8 @@
 // shift): the bits of a nibble alone are the fp16 subnormal u 2^-24 (u 2^-20 for the high nibble
 // of a byte), which the tensor cores take exactly; no bias has to be added or taken out.  For
 // K the two weights are evened out in the query (the dims in low nibbles carry 16 q), for V at the
-// end.  Putting the nibble under an exponent and subtracting the bias would double the conversion.  Query rows
-// enter as fp16 scaled by a power of two of their own (largest |q| in [2^9, 2^10), so bf16's
+// end.  Putting the nibble under an exponent and subtracting the bias would double the conversion.
+// Query rows enter as fp16 scaled by a power of two of their own (largest |q| in [2^9, 2^10), so bf16's
 // eight bits are exact wherever they matter); probabilities times value scales as fp16 scaled by a
 // power of two that follows the largest value scale seen (vnorm), because a scale may have any
 // exponent of bf16: rounding errors stay at 2^-11 of each product.  Sums, maxima, the minimum's
@@ -912,9 +912,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// The row's unit: where its pieces' partials are.  Before the wait only its context is read: a merge
+// starts once every CTA of the decode has triggered, which they do after their own wait, so what ran
+// before the decode is done.
+struct Pieces {
+    int count;           // 0 or 1: nothing to merge, the decode wrote the row
+    const float *lse;    // piece j's at lse[j G]
+    const float *o;      // and its row at o + j G D
+};
+
+template <int D>
+__device__ __forceinline__ Pieces pieces_of(const Args &a, int s, int h)
+{
+    const int kvh = h / a.group;
+    const int2 info = __ldcg(a.unit_info + static_cast<size_t>(s) * a.kv_heads + kvh);
+    Pieces p;
+    // (a sequence whose context changes while the decode runs may have left no such slots)
+    p.count = info.x >= 0 && info.y <= a.kv_heads * (a.num_seqs + a.runs) - info.x ? info.y : 0;
+    const size_t first = static_cast<size_t>(info.x) * a.group + (h - kvh * a.group);
+    p.lse = a.part_lse + first;
+    p.o = a.part_o + first * D;
+    return p;
+}
+
+// V values of the output, from element `at` on.
+template <int V>
+__device__ __forceinline__ void store_values(const Args &a, size_t at, const float *v)
+{
+    if constexpr (V == 4)
+        store_out4(a.out, a.out_f32, at, make_float4(v[0], v[1], v[2], v[3]));
+    else
+        store_out2(a.out, a.out_f32, at, make_float2(v[0], v[1]));
+}
+
 // out[row] = sum_j exp(lse_j - M) o_j / sum_j exp(lse_j - M) over the pieces of the row's unit,
-// W warps a row (8 where a unit has many pieces: few sequences, long contexts).  Rows whose unit is
-// one whole piece were written by it; rows of a sequence with no positions are 0.
+// W warps a row.  Rows whose unit is one whole piece were written by it; rows of a sequence with no
+// positions are 0.
 template <int D, int W>
 __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) merge_int4_kernel(const Args a)
 {
@@ -929,28 +962,21 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) merge_int4_kernel(const
     if (row >= a.num_seqs * a.q_heads)
         return;
     const int s = row / a.q_heads;
-    const int h = row - s * a.q_heads;
     const int G = a.group;
-    const int kvh = h / G;
-    // Before the wait: this launch starts once every CTA of the decode has triggered, which they do
-    // after their own wait, so what ran before the decode is done.
     const int raw = __ldcg(a.context_lens + s);
     pdl_wait();
     pdl_trigger();
-    const int2 info = __ldcg(a.unit_info + static_cast<size_t>(s) * a.kv_heads + kvh);
+    const Pieces p = pieces_of<D>(a, s, row - s * a.q_heads);
     float acc[V], sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
         acc[v] = 0.0f;
     if (raw > 0) {
-        // (a sequence whose context changes while the decode runs may have left no such slots)
-        const int count =
-            info.x >= 0 && info.y <= a.kv_heads * (a.num_seqs + a.runs) - info.x ? info.y : 0;
+        const int count = p.count;
         if (count <= 1)
             return;
-        const size_t first = static_cast<size_t>(info.x) * G + (h - kvh * G);
-        const float *lse = a.part_lse + first;
-        const float *po = a.part_o + first * D + lane * V;
+        const float *lse = p.lse;
+        const float *po = p.o + lane * V;
         const size_t po_step = static_cast<size_t>(G) * D;
         // one round trip: every piece's lse (lane j holds pieces j, j + 32, ...) and the rows of
         // this warp's first pieces
@@ -1015,12 +1041,94 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) merge_int4_kernel(const
         }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const size_t base = static_cast<size_t>(row) * D + lane * V;
-    if constexpr (V == 4)
-        store_out4(a.out, a.out_f32, base,
-                   make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv));
-    else
-        store_out2(a.out, a.out_f32, base, make_float2(acc[0] * inv, acc[1] * inv));
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        acc[v] *= inv;
+    store_values<V>(a, static_cast<size_t>(row) * D + lane * V, acc);
+}
+
+// The same for units of many pieces (very few sequences, long contexts), a CTA for 32 dims of a row: a
+// thread per piece's weight, and eight warps that each take every eighth piece, kFly of them in
+// flight, so that 128 pieces are one round trip.
+constexpr int kWideThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kWideThreads) merge_wide_int4_kernel(const Args a)
+{
+    constexpr int W = kWideThreads / 32;
+    constexpr int kFly = 16;
+    constexpr int kParts = D / 32;
+    static_assert(kWideThreads % (kFly * W) == 0, "a batch of rows has its weights in one tile");
+    __shared__ float weight[kWideThreads], high[W], part[W][33];
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.x / kParts;
+    const int dim = blockIdx.x % kParts * 32 + lane;
+    const int s = row / a.q_heads;
+    const int raw = __ldcg(a.context_lens + s);
+    pdl_wait();
+    pdl_trigger();
+    const Pieces p = pieces_of<D>(a, s, row - s * a.q_heads);
+    float acc = 0.0f, sum = 0.0f;
+    if (raw > 0) {
+        if (p.count <= 1)
+            return;
+        const float *po = p.o + dim;
+        const size_t po_step = static_cast<size_t>(a.group) * D;
+        float x[kFly];   // of this warp's next pieces: those from j on
+        auto load = [&](int j) {
+#pragma unroll
+            for (int u = 0; u < kFly; ++u)
+                if (j + u * W < p.count)
+                    x[u] = __ldcg(po + (j + u * W) * po_step);
+        };
+        load(warp);
+        float M = -INFINITY;
+        for (int j = threadIdx.x; j < p.count; j += kWideThreads)
+            M = fmaxf(M, __ldcg(p.lse + static_cast<size_t>(j) * a.group));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        if (lane == 0)
+            high[warp] = M;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            M = fmaxf(M, high[w]);
+        const float mu = M == -INFINITY ? 0.0f : M;
+        for (int base = 0; base < p.count; base += kWideThreads) {
+            const int mine = base + threadIdx.x;
+            weight[threadIdx.x] =
+                mine < p.count
+                    ? fast_exp2((__ldcg(p.lse + static_cast<size_t>(mine) * a.group) - mu) * kLog2e)
+                    : 0.0f;
+            __syncthreads();
+#pragma unroll 1
+            for (int j = base + warp; j < min(p.count, base + kWideThreads); j += kFly * W) {
+                if (j > warp)
+                    load(j);
+#pragma unroll
+                for (int u = 0; u < kFly; ++u)
+                    if (j + u * W < p.count) {
+                        const float w = weight[j + u * W - base];
+                        sum += w;
+                        acc = fmaf(w, x[u], acc);
+                    }
+            }
+            __syncthreads();
+        }
+    }
+    part[warp][lane] = acc;
+    if (lane == 0)
+        part[warp][32] = sum;
+    __syncthreads();
+    if (warp != 0)
+        return;
+    for (int w = 1; w < W; ++w) {
+        sum += part[w][32];
+        acc += part[w][lane];
+    }
+    store_out(a.out, a.out_f32, static_cast<size_t>(row) * D + dim, sum == 0.0f ? 0.0f : acc / sum);
 }
 
 template <int D>
@@ -1062,7 +1170,13 @@ cudaError_t launch_t(const DecodeInt4Launch &l, const CUtensorMap (&maps)[4], cu
     if (err != cudaSuccess || l.per_unit)
         return err;
     const int rows = l.num_seqs * l.q_heads;
-    if (l.runs > 4LL * l.num_seqs)   // more than some four pieces a unit: 8 warps a row
+    // Few sequences have many pieces a row.  1 sequence of 65,536 positions: 24.4 us with the wide
+    // merge, 38.2 with 8 warps a row; 4 of 32,768: 35.9 and 38.6; 8 of 8,192: 25.0 and 23.8.  16 of 4,096
+    // take 21.4 with 8 warps a row and 27.4 with one, 32 31.0 and 33.3, 48 41.2 and 41.1, 64 52.8 and 51.3.
+    if (l.runs > 32LL * l.num_seqs)
+        return launch_pdl(merge_wide_int4_kernel<D>, dim3(rows * (D / 32)), dim3(kWideThreads), 0,
+                          stream, a);
+    if (l.runs > 4LL * l.num_seqs)
         return launch_pdl(merge_int4_kernel<D, 8>, dim3(rows), dim3(256), 0, stream, a);
     return launch_pdl(merge_int4_kernel<D, 1>, dim3((rows + 3) / 4), dim3(128), 0, stream, a);
 }

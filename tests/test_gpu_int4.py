@@ -315,7 +315,7 @@ def test_long_context_few_sequences():
     case = ragged(23, 64, 1, 8, 128, [40001, 3])
     pools = filled(case)
     ref = int4.attention(case.q, *pools, case.block_table, case.context_lens)
-    for splits in (0, 100):
+    for splits in (0, 9, 100, 300):
         got = run_decode(case.q, pools, case.block_table, case.context_lens, case.max_ctx, splits)
         check(case, got, ref, pools, f"long {splits}")
 
