@@ -45,7 +45,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                          a.err ? a.err : &g_decode_errors);
 }
 
-template <int D>
+// A warp per row, or (WIDE) per 32 dims of one.
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(128) merge_kernel(void *out, int out_f32,
                                                     const float *__restrict__ part_o,
                                                     const float *__restrict__ part_lse,
@@ -53,9 +54,15 @@ __global__ void __launch_bounds__(128) merge_kernel(void *out, int out_f32,
 {
     pdl_wait();
     pdl_trigger();
-    const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row < rows)
-        merge_row<D>(out, out_f32, part_o, part_lse, row, n_split, lse_out);
+    const long long warp = blockIdx.x * 4LL + (threadIdx.x >> 5);
+    if constexpr (WIDE) {
+        const int row = static_cast<int>(warp / (D / 32));
+        if (row < rows)
+            merge_row_part<D>(out, out_f32, part_o, part_lse, row, static_cast<int>(warp % (D / 32)),
+                              n_split, lse_out);
+    } else if (warp < rows) {
+        merge_row<D>(out, out_f32, part_o, part_lse, static_cast<int>(warp), n_split, lse_out);
+    }
 }
 
 template <int D, bool SPLIT>
@@ -105,17 +112,19 @@ cudaError_t launch_decode(const DecodeLaunch &l, const CUtensorMap &tk, const CU
 }
 
 cudaError_t launch_merge(void *out, int out_f32, const float *part_o, const float *part_lse,
-                         int rows, int n_split, int head_dim, float *lse_out,
-                         cudaStream_t stream)
+                         int rows, int n_split, int head_dim, float *lse_out, cudaStream_t stream)
 {
     if (rows == 0)
         return cudaSuccess;
-    const int blocks = (rows + 3) / 4;
-    if (head_dim == 128)
-        return launch_pdl(merge_kernel<128>, dim3(blocks), dim3(128), 0, stream, out, out_f32,
-                          part_o, part_lse, rows, n_split, lse_out);
-    return launch_pdl(merge_kernel<64>, dim3(blocks), dim3(128), 0, stream, out, out_f32, part_o,
-                      part_lse, rows, n_split, lse_out);
+    const bool wide = n_split > kWideMergeSplits;
+    const long long warps = static_cast<long long>(rows) * (wide ? head_dim / 32 : 1);
+    const long long blocks = (warps + 3) / 4;
+    if (blocks > 0x7FFFFFFFLL)
+        return cudaErrorInvalidValue;
+    auto kernel = head_dim == 128 ? (wide ? merge_kernel<128, true> : merge_kernel<128, false>)
+                                  : (wide ? merge_kernel<64, true> : merge_kernel<64, false>);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream, out, out_f32,
+                      part_o, part_lse, rows, n_split, lse_out);
 }
 
 cudaError_t launch_selftest_wait(cudaStream_t stream)

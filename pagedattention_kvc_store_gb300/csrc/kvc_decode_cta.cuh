@@ -559,5 +559,62 @@ __device__ __forceinline__ void merge_row(void *out, int out_f32,
         lse_out[row] = (M == -INFINITY) ? -INFINITY : M + logf(sum);
 }
 
+// Above so many splits a row is merged by D / 32 warps with kFly partials in flight each: the same
+// sums in the same order, but not one partial after the other.  kvc_decode of 1 sequence of 65,536
+// positions (147 splits, 32 / 8 heads): 58.2 us against 86.6; 4 of 32,768 (37): 89.3 and 96.4; 8 of 8,192
+// (19): 50.8 and 54.0; with 10 splits on 16 of 4,096 there is nothing to gain (49.4 and 49.2).
+constexpr int kWideMergeSplits = 16;
+
+// 32 dims (part) of a row.
+template <int D>
+__device__ __forceinline__ void merge_row_part(void *out, int out_f32,
+                                               const float *__restrict__ part_o,
+                                               const float *__restrict__ part_lse, int row, int part,
+                                               int n_split, float *lse_out)
+{
+    constexpr int kFly = 16;
+    const int lane = threadIdx.x & 31;
+    const int dim = part * 32 + lane;
+    const float *lse = part_lse + static_cast<size_t>(row) * n_split;
+    const float *po = part_o + static_cast<size_t>(row) * n_split * D + dim;
+    float x[kFly];   // an empty split's value is loaded but never used
+#pragma unroll
+    for (int u = 0; u < kFly; ++u)
+        x[u] = u < n_split ? po[static_cast<size_t>(u) * D] : 0.0f;
+    float M = -INFINITY;
+    for (int j = lane; j < n_split; j += 32)
+        M = fmaxf(M, lse[j]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float acc = 0.0f, sum = 0.0f;
+    if (M != -INFINITY) {
+#pragma unroll 1
+        for (int j0 = 0; j0 < n_split; j0 += kFly) {
+            const float mine = lane < kFly && j0 + lane < n_split ? lse[j0 + lane] : -INFINITY;
+            float next[kFly];
+#pragma unroll
+            for (int u = 0; u < kFly; ++u) {
+                const int j = j0 + kFly + u;
+                next[u] = j < n_split ? po[static_cast<size_t>(j) * D] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < kFly; ++u) {
+                const float lj = __shfl_sync(0xffffffffu, mine, u);
+                if (lj != -INFINITY) {
+                    const float w = fast_exp2((lj - M) * kLog2e);
+                    sum += w;
+                    acc += w * x[u];
+                }
+                x[u] = next[u];
+            }
+        }
+    }
+    const float inv = (sum > 0.0f) ? 1.0f / sum : 0.0f;
+    store_out(out, out_f32, static_cast<size_t>(row) * D + dim, acc * inv);
+    if (lse_out != nullptr && part == 0 && lane == 0)
+        lse_out[row] = (M == -INFINITY) ? -INFINITY : M + logf(sum);
+}
+
 }  // namespace dec
 }  // namespace kvc

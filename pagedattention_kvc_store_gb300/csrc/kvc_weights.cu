@@ -57,7 +57,8 @@ struct FinishArgs {
     int num_seqs, max_ctx, merge_blocks, tiles;
 };
 
-template <int D>
+// WIDE: the rows of many splits, merged by D / 32 warps each (more registers than the weights need).
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const FinishArgs f)
 {
     pdl_wait();
@@ -66,8 +67,15 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const FinishArgs
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (blockIdx.x < f.merge_blocks) {
-        const int row = blockIdx.x * (kFinishThreads / 32) + warp;
-        if (row < f.num_seqs * a.q_heads)
+        constexpr int kRowWarps = WIDE ? D / 32 : 1;
+        const int unit = blockIdx.x * (kFinishThreads / 32) + warp;
+        const int row = unit / kRowWarps;
+        if (row >= f.num_seqs * a.q_heads)
+            return;
+        if constexpr (WIDE)
+            merge_row_part<D>(a.out, a.out_f32, a.part_o, a.part_lse, row, unit % kRowWarps,
+                              a.n_split, nullptr);
+        else
             merge_row<D>(a.out, a.out_f32, a.part_o, a.part_lse, row, a.n_split, nullptr);
         return;
     }
@@ -164,14 +172,16 @@ cudaError_t launch_t(const DecodeLaunch &l, const WeightsLaunch &w, const CUtens
     f.weight_stride = w.weight_stride;
     f.num_seqs = l.num_seqs;
     f.max_ctx = w.max_ctx;
-    const int rows_per_block = kFinishThreads / 32;
-    f.merge_blocks = (l.num_seqs * l.q_heads + rows_per_block - 1) / rows_per_block;
+    const int rows_per_block = kFinishThreads / 32;   // (warps)
+    const bool wide = l.n_split > kWideMergeSplits;
+    f.merge_blocks =
+        (l.num_seqs * l.q_heads * (wide ? D / 32 : 1) + rows_per_block - 1) / rows_per_block;
     f.tiles = (w.max_ctx + kTile - 1) / kTile;
     const long long grid =
         f.merge_blocks + static_cast<long long>(f.tiles) * l.kv_heads * l.num_seqs;
     if (grid > 0x7FFFFFFFLL)
         return cudaErrorInvalidValue;
-    return launch_pdl(finish_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(kFinishThreads), 0,
+    return launch_pdl(wide ? finish_kernel<D, true> : finish_kernel<D, false>, dim3(static_cast<unsigned>(grid)), dim3(kFinishThreads), 0,
                       stream, f);
 }
 

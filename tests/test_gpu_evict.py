@@ -112,7 +112,7 @@ def test_weights_ragged(P, H, G, D, layout):
     case = decode_case(11 + G, P, H, G, D, lambda rng: rng.integers(1, 1500, size=9))
     run = Run(case, layout, stride=case.max_ctx + 3)
     per_seq = evict.weights(case.q, run.kp, case.block_table, case.context_lens, layout=layout)
-    for splits in (0, 1, 3):
+    for splits in (0, 1, 3, 20):
         run.weights.zero_()
         out = run.decode(splits)
         assert torch.equal(out, run.plain_decode(splits)), "the output is kvc_decode's"
