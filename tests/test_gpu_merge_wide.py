@@ -1,6 +1,6 @@
-"""kvc_merge over few and many splits against a 64-bit merge.  Weights exp(lse - M) are off by 2^-20 each
-(the difference's rounding, |lse - M| below 16 here, and 2^x), sums and products of up to 150 terms by
-150 * 2^-24: below 2^-16 of the largest partial together."""
+"""kvc_merge over few and many splits against a 64-bit merge.  |lse - M| stays below 32, so the
+difference and its product with log2(e) are off by 2^-18 at most and a weight by that much of itself;
+sums and products of up to 150 terms add 150 * 2^-24: below 2^-16 of the largest partial together."""
 import numpy as np
 import pytest
 import torch
