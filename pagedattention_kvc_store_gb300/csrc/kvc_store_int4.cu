@@ -75,6 +75,14 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b)
     return r;
 }
 
+// The larger ones, alike.
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 __device__ __forceinline__ float approx_rcp(float x)
 {
     float y;
@@ -85,13 +93,14 @@ __device__ __forceinline__ float approx_rcp(float x)
 // Codes (16 values: 8 bytes) and parameter of a quarter of a group; four neighbouring lanes hold one.
 __device__ __forceinline__ uint2 quantise16(const uint32_t (&x)[8], uint32_t &param)
 {
-    // lo and -hi of the lane's values, two to a word; then of the group
-    uint32_t lo2 = x[0], nhi2 = x[0] ^ 0x80008000u;
+    // lo and hi of the lane's values, two to a word; then lo and -hi of the group
+    uint32_t lo2 = x[0], hi2 = x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
         lo2 = min2_nan(lo2, x[i]);
-        nhi2 = min2_nan(nhi2, x[i] ^ 0x80008000u);
+        hi2 = max2_nan(hi2, x[i]);
     }
+    const uint32_t nhi2 = hi2 ^ 0x80008000u;
     uint32_t m = min2_nan(__byte_perm(lo2, nhi2, 0x5410), __byte_perm(lo2, nhi2, 0x7632));
     m = min2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = min2_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -115,6 +124,7 @@ __device__ __forceinline__ uint2 quantise16(const uint32_t (&x)[8], uint32_t &pa
     // 2^-37 off the point where the rounding would turn.  Equality gives k + 1/2 itself.  r is then
     // the nearest integer: 1.5 2^23 added and taken away, ties to even.  scale is at most 2^-8 of
     // itself off, so r needs no clamp.
+    // The codes come out as floats 1.5 2^23 + r: r in the low bits.
     uint64_t r2[8];
     if (scale_half >= 1e-30f) {
         const float inv = approx_rcp(scale_half);
@@ -128,30 +138,29 @@ __device__ __forceinline__ uint2 quantise16(const uint32_t (&x)[8], uint32_t &pa
             const uint64_t a = f2_fma(v, half2, nlo2);
             const uint64_t q = f2_mul(a, inv2);
             const uint64_t q1 = f2_fma(f2_fma(q, nb2, a), inv2, q);
-            r2[i] = f2_sub(f2_add(q1, magic2), magic2);
+            r2[i] = f2_add(q1, magic2);
         }
     } else {   // near and among the subnormals the products above would lose bits, and scale is coarse
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float a0 = fmaf(__uint_as_float(x[i] << 16), 0.5f, -lo_half);
             const float a1 = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), 0.5f, -lo_half);
-            r2[i] = f2_pack(fminf(rintf(__fdiv_rn(a0, scale_half)), 15.0f),
-                            fminf(rintf(__fdiv_rn(a1, scale_half)), 15.0f));
+            r2[i] = f2_pack(fminf(rintf(__fdiv_rn(a0, scale_half)), 15.0f) + 12582912.0f,
+                            fminf(rintf(__fdiv_rn(a1, scale_half)), 15.0f) + 12582912.0f);
         }
     }
-    // value pairs (even, odd) of four words make 8 codes: even ones weigh 1, 256, 65536, 2^24, odd
-    // ones 16 times that; sums of four stay below 2^24 in each half
-    const uint64_t w256 = f2_pack(256.0f, 256.0f);
-    uint32_t code[2];
+    // a byte is even + 16 odd: the floats' upper bits, 16 times too, stay above it
+    uint32_t byte[8], code[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float e0, o0, e1, o1;
-        f2_unpack(f2_fma(r2[4 * h + 1], w256, r2[4 * h]), e0, o0);
-        f2_unpack(f2_fma(r2[4 * h + 3], w256, r2[4 * h + 2]), e1, o1);
-        const uint32_t lo16 = __float_as_uint(fmaf(o0, 16.0f, e0) + 8388608.0f);
-        const uint32_t hi16 = __float_as_uint(fmaf(o1, 16.0f, e1) + 8388608.0f);
-        code[h] = __byte_perm(lo16, hi16, 0x5410);
+    for (int i = 0; i < 8; ++i) {
+        float even, odd;
+        f2_unpack(r2[i], even, odd);
+        byte[i] = __float_as_uint(even) + 16u * __float_as_uint(odd);
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        code[h] = __byte_perm(__byte_perm(byte[4 * h], byte[4 * h + 1], 0x0040),
+                              __byte_perm(byte[4 * h + 2], byte[4 * h + 3], 0x0040), 0x5410);
     return make_uint2(code[0], code[1]);
 }
 
