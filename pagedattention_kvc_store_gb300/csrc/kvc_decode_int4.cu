@@ -73,7 +73,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLagLog2 = 4.0f;
 constexpr float kMaxScaled = 2048.0f;   // largest value scale times vnorm: 2^4 * 2^11 < 65504
 
-// Cost of a block and of a piece's start in the cut of the runs.
+// Cost of a block and of a piece's start in the cut of the runs (a start as 12 or 16: 41.6 us on the
+// batched decode, as 8 or 24 42.4, as 4 or 32 42.7 and 43.2).
 constexpr long long kBlockCost = 16;
 constexpr long long kPieceCost = 16;
 
