@@ -467,7 +467,9 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUte
     }
 }
 
-// One warp per row: out[r] = sum_j exp(lse_j - M) o_j / sum_j exp(lse_j - M).
+// One warp per row: out[r] = sum_j exp(lse_j - M) o_j / sum_j exp(lse_j - M), 0 where every split is
+// empty (lse -infinity).  The largest lse skips NaN, so it may be -infinity for a row that is not empty:
+// it is then taken as 0, and the NaN goes through the sum.
 template <int D>
 __device__ __forceinline__ void merge_row(void *out, int out_f32,
                                           const float *__restrict__ part_o,
@@ -509,46 +511,45 @@ __device__ __forceinline__ void merge_row(void *out, int out_f32,
 #pragma unroll
     for (int v = 0; v < V; ++v)
         acc[v] = 0.0f;
+    const float mu = M == -INFINITY ? 0.0f : M;
     float sum = 0.0f;
-    if (M != -INFINITY) {
-        for (int j0 = 0; j0 < n_split; j0 += 32) {
-            const float mine = (j0 + lane < n_split) ? lse[j0 + lane] : -INFINITY;
-            const int cnt = min(32, n_split - j0);
-            for (int jj = 0; jj < cnt; ++jj) {
-                const float lj = __shfl_sync(0xffffffffu, mine, jj);
-                if (lj == -INFINITY)
-                    continue;   // empty split: its partial is not read
-                const float w = fast_exp2((lj - M) * kLog2e);
-                sum += w;
-                const int j = j0 + jj;
-                float val[V];
-                if (j < kPre) {   // select in registers (no dynamic index into pre)
+    for (int j0 = 0; j0 < n_split; j0 += 32) {
+        const float mine = (j0 + lane < n_split) ? lse[j0 + lane] : -INFINITY;
+        const int cnt = min(32, n_split - j0);
+        for (int jj = 0; jj < cnt; ++jj) {
+            const float lj = __shfl_sync(0xffffffffu, mine, jj);
+            if (lj == -INFINITY)
+                continue;   // empty split: its partial is not read
+            const float w = fast_exp2((lj - mu) * kLog2e);
+            sum += w;
+            const int j = j0 + jj;
+            float val[V];
+            if (j < kPre) {   // select in registers (no dynamic index into pre)
 #pragma unroll
-                    for (int k = 0; k < kPre; ++k)
-                        if (k == j) {
+                for (int k = 0; k < kPre; ++k)
+                    if (k == j) {
 #pragma unroll
-                            for (int v = 0; v < V; ++v)
-                                val[v] = pre[k][v];
-                        }
-                } else if constexpr (V == 4) {
-                    const float4 t =
-                        *reinterpret_cast<const float4 *>(po + static_cast<size_t>(j) * D);
-                    val[0] = t.x;
-                    val[1] = t.y;
-                    val[2] = t.z;
-                    val[3] = t.w;
-                } else {
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        val[v] = po[static_cast<size_t>(j) * D + v];
-                }
+                        for (int v = 0; v < V; ++v)
+                            val[v] = pre[k][v];
+                    }
+            } else if constexpr (V == 4) {
+                const float4 t =
+                    *reinterpret_cast<const float4 *>(po + static_cast<size_t>(j) * D);
+                val[0] = t.x;
+                val[1] = t.y;
+                val[2] = t.z;
+                val[3] = t.w;
+            } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    acc[v] += w * val[v];
+                    val[v] = po[static_cast<size_t>(j) * D + v];
             }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                acc[v] += w * val[v];
         }
     }
-    const float inv = (sum > 0.0f) ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const size_t base = static_cast<size_t>(row) * D + lane * V;
     if constexpr (V == 4)
         store_out4(out, out_f32, base,
@@ -556,7 +557,7 @@ __device__ __forceinline__ void merge_row(void *out, int out_f32,
     else
         store_out2(out, out_f32, base, make_float2(acc[0] * inv, acc[1] * inv));
     if (lse_out != nullptr && lane == 0)
-        lse_out[row] = (M == -INFINITY) ? -INFINITY : M + logf(sum);
+        lse_out[row] = sum == 0.0f ? -INFINITY : mu + logf(sum);
 }
 
 // Above so many splits a row is merged by D / 32 warps with kFly partials in flight each: the same
@@ -587,33 +588,32 @@ __device__ __forceinline__ void merge_row_part(void *out, int out_f32,
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    const float mu = M == -INFINITY ? 0.0f : M;
     float acc = 0.0f, sum = 0.0f;
-    if (M != -INFINITY) {
 #pragma unroll 1
-        for (int j0 = 0; j0 < n_split; j0 += kFly) {
-            const float mine = lane < kFly && j0 + lane < n_split ? lse[j0 + lane] : -INFINITY;
-            float next[kFly];
+    for (int j0 = 0; j0 < n_split; j0 += kFly) {
+        const float mine = lane < kFly && j0 + lane < n_split ? lse[j0 + lane] : -INFINITY;
+        float next[kFly];
 #pragma unroll
-            for (int u = 0; u < kFly; ++u) {
-                const int j = j0 + kFly + u;
-                next[u] = j < n_split ? po[static_cast<size_t>(j) * D] : 0.0f;
-            }
+        for (int u = 0; u < kFly; ++u) {
+            const int j = j0 + kFly + u;
+            next[u] = j < n_split ? po[static_cast<size_t>(j) * D] : 0.0f;
+        }
 #pragma unroll
-            for (int u = 0; u < kFly; ++u) {
-                const float lj = __shfl_sync(0xffffffffu, mine, u);
-                if (lj != -INFINITY) {
-                    const float w = fast_exp2((lj - M) * kLog2e);
-                    sum += w;
-                    acc += w * x[u];
-                }
-                x[u] = next[u];
+        for (int u = 0; u < kFly; ++u) {
+            const float lj = __shfl_sync(0xffffffffu, mine, u);
+            if (lj != -INFINITY) {
+                const float w = fast_exp2((lj - mu) * kLog2e);
+                sum += w;
+                acc += w * x[u];
             }
+            x[u] = next[u];
         }
     }
-    const float inv = (sum > 0.0f) ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     store_out(out, out_f32, static_cast<size_t>(row) * D + dim, acc * inv);
     if (lse_out != nullptr && part == 0 && lane == 0)
-        lse_out[row] = (M == -INFINITY) ? -INFINITY : M + logf(sum);
+        lse_out[row] = sum == 0.0f ? -INFINITY : mu + logf(sum);
 }
 
 }  // namespace dec

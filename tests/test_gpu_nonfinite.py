@@ -1,0 +1,135 @@
+"""NaN and infinity in queries, keys and values.
+
+The reference is the definition in 64 bits, where a score of NaN or +infinity makes its row NaN, one
+of -infinity weighs nothing, and an infinite value reaches its dim.  Finite outputs (fp32): a
+probability is rounded to bf16, half a step 2^-8 of itself, in the numerator and in the sum, so the
+weighted mean of values up to V moves by 2^-7 V (1 + 2^-8); a score, a sum of D products in fp32
+(2^-23 each, tensor cores may cut), by d = (D + 8) 2^-23 scale Q K and the mean by 2 d V; 2^x, the sums
+and the division by 2^-18 V."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import pagedattention_kvc_store_gb300 as kvc
+from oracle import int4
+from workloads.device import bf16_tensor, i32_tensor
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF, NEG_INF = 0x7FC0, 0x7F80, 0xFF80
+P, H, G = 16, 2, 2
+CTX = np.array([50, 2500, 300, 40, 200, 0, 33])
+
+
+class Case:
+    """Sequences over pages of their own; nothing below holds a position past its context."""
+
+    def __init__(self, D, seed=1):
+        rng = np.random.default_rng(seed)
+        width = -(-int(CTX.max()) // P)
+        self.D, self.S = D, len(CTX)
+        self.max_ctx = int(CTX.max())
+        self.table = rng.permutation(self.S * width).reshape(self.S, width).astype(np.int32)
+        shape = (self.S * width, P, H, D)
+        self.k, self.v = (int4.bf16_round(rng.standard_normal(shape).astype(np.float32))
+                          for _ in "kv")
+        self.q = int4.bf16_round(rng.standard_normal((self.S, H * G, D)).astype(np.float32))
+
+    def at(self, pool, s, p):
+        return pool[self.table[s, p // P], p % P]   # [H, D], a view
+
+    def reference(self):
+        q, k, v = (int4.bf16_value(x).astype(np.float64) for x in (self.q, self.k, self.v))
+        out = np.zeros(self.q.shape)
+        with np.errstate(invalid="ignore"):
+            for s, n in enumerate(CTX):
+                pos = np.arange(n)
+                page = self.table[s][pos // P], pos % P
+                for h in range(H * G if n else 0):
+                    x = k[page][:, h // G] @ q[s, h] / math.sqrt(self.D)
+                    w = np.exp(x - x.max())
+                    out[s, h] = w @ v[page][:, h // G] / w.sum()
+        return out
+
+    def check(self, got):
+        ref = self.reference()
+        got = got.double().cpu().numpy()
+        finite = np.isfinite(ref)
+        assert np.array_equal(np.isnan(got), np.isnan(ref))
+        assert np.array_equal(got[np.isinf(ref)], ref[np.isinf(ref)])
+        q, k, v = (np.abs(int4.bf16_value(x).astype(np.float64)) for x in (self.q, self.k, self.v))
+        Q, K, V = (x[np.isfinite(x)].max() for x in (q.sum(-1), k, v))
+        d = (self.D + 8) * 2.0 ** -23 / math.sqrt(self.D) * Q * K
+        bound = (2.0 ** -7 * (1 + 2.0 ** -8) + 2 * d + 2.0 ** -18) * V
+        assert np.abs(got[finite] - ref[finite]).max() <= bound
+
+    def upload(self):
+        self.dk, self.dv = bf16_tensor(self.k, "cuda"), bf16_tensor(self.v, "cuda")
+        self.dq, self.dt = bf16_tensor(self.q, "cuda"), i32_tensor(self.table, "cuda")
+        self.dc = i32_tensor(CTX, "cuda")
+        self.pool = kvc.pool_desc(self.dk)
+
+    def decode(self, splits, dtype=torch.float32):
+        out = torch.full(self.q.shape, 9.0, dtype=dtype, device="cuda")
+        n, _, ws = kvc.kvc_decode_plan(self.S, H * G, self.pool, self.max_ctx, splits)
+        work = torch.empty(max(ws, 16), dtype=torch.uint8, device="cuda")
+        kvc.kvc_decode(out, self.dq, self.dk, self.dv, self.dt, self.dc, self.max_ctx,
+                       num_splits=splits, workspace=work)
+        return out, n
+
+
+def spoiled(D):
+    """Rows of every kind, in a sequence of one chunk and of many; and which rows must be NaN."""
+    c = Case(D)
+    c.at(c.k, 0, 19)[1, 3] = NAN              # sequence 0 (50 positions), kv head 1
+    c.at(c.k, 1, 700)[0, 0] = NAN             # sequence 1 (2,500), kv head 0
+    c.q[2, 3, 5] = NAN                        # one query head
+    c.at(c.k, 3, 5)[1, 0] = INF               # scores of both infinities, by the query's sign
+    c.q[3, 2, 0], c.q[3, 3, 0] = int4.bf16_round(np.array([1.5, -1.5], np.float32))
+    c.at(c.v, 4, 100)[0, 7] = INF             # one dim
+    c.at(c.v, 6, 32)[1, 1] = NAN
+    return c
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_reference_says_what_the_cases_are_for(D):
+    ref = spoiled(D).reference()
+    nan = np.isnan(ref).all(-1)
+    assert nan.nonzero()[0].tolist() == [0, 0, 1, 1, 2, 3] and nan[3, 2] and not nan[3, 3]
+    assert np.isinf(ref[4, :2, 7]).all() and np.isnan(ref[6, 2:, 1]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_merge_of_nan_partials(D):
+    """Rows whose only non-empty splits are NaN are NaN, like rows with numbers beside them; rows of
+    empty splits are 0 as before."""
+    for splits in (1, 3, 5, 40):              # both forms of the merge
+        rows = 6
+        lse = np.full((rows, splits), -np.inf, np.float32)
+        o = np.full((rows, splits, D), 2.0, np.float32)
+        lse[0, splits // 2] = np.nan          # the only one
+        lse[1] = np.nan
+        lse[2] = np.log(np.float32(1.0))      # all numbers
+        lse[3, 0], lse[3, -1] = 0.5, np.nan   # (the same split where there is one)
+        lse[4, -1] = 3.0
+        out = torch.full((rows, D), 7.0, device="cuda")
+        back = torch.zeros(rows, device="cuda")
+        kvc.kvc_merge(out, torch.from_numpy(o).cuda(), torch.from_numpy(lse).cuda(), lse_out=back)
+        out, back = out.cpu().numpy(), back.cpu().numpy()
+        for row in (0, 1, 3):
+            assert np.isnan(out[row]).all() and np.isnan(back[row]), (splits, row)
+        assert np.abs(out[[2, 4]] - 2.0).max() <= 40 * 2.0 ** -22
+        assert not out[5].any() and back[5] == -np.inf
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [1, 3, 0, 20])
+def test_decode(D, splits):
+    c = spoiled(D)
+    c.upload()
+    out, n = c.decode(splits)
+    assert splits == 0 or n == splits         # 20: the wide merge
+    c.check(out)
+    assert kvc.kvc_device_errors() == 0
