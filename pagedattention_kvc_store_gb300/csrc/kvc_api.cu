@@ -1204,8 +1204,8 @@ kvc_status kvc_decode_store(void *out, int32_t out_dtype, const void *q, const v
 
 namespace {
 
-// kvc_decode_weights' plan: kvc_decode's, with a partial for every split (also a single one), its
-// log-sum-exps, the exact base-2 ones, and the scores.
+// kvc_decode_weights' plan: kvc_decode's, with a partial and its log-sum-exp for every split where there
+// are several, the exact base-2 log-sum-exps, and the scores.
 struct WeightsPlan {
     Plan p;
     size_t lse_offset, lse2_offset, scores_offset, score_stride, ws_bytes;
@@ -1219,8 +1219,9 @@ WeightsPlan make_weights_plan(int32_t num_seqs, int32_t q_heads, const kvc_pool_
     const size_t rows = static_cast<size_t>(num_seqs) * q_heads;
     const size_t parts = rows * w.p.splits;
     auto align = [](size_t x) { return (x + 255) / 256 * 256; };
-    w.lse_offset = align(parts * pool.head_dim * sizeof(float));
-    w.lse2_offset = align(w.lse_offset + parts * sizeof(float));
+    const size_t merged = w.p.splits > 1 ? parts : 0;
+    w.lse_offset = align(merged * pool.head_dim * sizeof(float));
+    w.lse2_offset = align(w.lse_offset + merged * sizeof(float));
     w.scores_offset = align(w.lse2_offset + parts * sizeof(float));
     w.score_stride = static_cast<size_t>(w.p.splits) * w.p.chunk;
     w.ws_bytes = w.scores_offset + rows * w.score_stride * sizeof(float);

@@ -100,7 +100,7 @@ inline Args make_args(const DecodeLaunch &l)
 
 // One CTA (kThreads threads, DecodeGeom<D>::kSmemBytes of dynamic shared memory, `smem`
 // 1024-byte aligned) on chunk `split` of kv head `kvh` of sequence `s`; device-side failures
-// are or-ed into *errors.  SCORES (with SPLIT) also leaves every score and each chunk's exact
+// are or-ed into *errors.  SCORES also leaves every score and each chunk's exact
 // log2-sum-exp2 for the attention weights; the output's sum stays the one over the rounded
 // probabilities that its numerator uses.
 template <int D, bool SPLIT, bool SCORES = false>
@@ -151,13 +151,12 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap *tmap_k, const CUte
             if (threadIdx.x < G)
                 a.part_lse[(row0 + threadIdx.x) * a.split_stride + a.split_base + split] =
                     -INFINITY;
-            if (SCORES && threadIdx.x < G)
-                a.part_lse2[(row0 + threadIdx.x) * a.split_stride + a.split_base + split] =
-                    -INFINITY;
         } else {
             for (int i = threadIdx.x; i < G * D; i += blockDim.x)
                 store_out(a.out, a.out_f32, row0 * D + i, 0.0f);
         }
+        if (SCORES && threadIdx.x < G)
+            a.part_lse2[(row0 + threadIdx.x) * a.split_stride + a.split_base + split] = -INFINITY;
         return;
     }
 

@@ -1,6 +1,7 @@
 // kvc_weights.cu -- paged decode attention that also adds up the attention weights.
 //
-// What it computes: kvc_decode's output, bit for bit, and for every position p and kv head h
+// What it computes: kvc_decode's output, bit for bit (the same kernel code, and a single split writes its
+// rows itself here too, NaN and all), and for every position p and kv head h
 //   weights[row(s)][h][p] += sum over the G query heads g of h's group of softmax_p(q_g . K[p] scale),
 // the measure by which kvc_evict keeps positions.
 //
@@ -8,7 +9,7 @@
 // score.  Reading K again for the weights would cost half of the pass once more; the scores are
 // 4 G bytes a position against the 4 D bytes of its K and V (G = 4, D = 128: 3%), so the decode CTAs
 // write them, and the launch that merges the partials also turns them into weights: its first
-// blocks merge (one warp a row), the others take 1,024 positions of one (sequence, kv head) each.
+// blocks merge (one warp a row; none where there is one split), the others take 1,024 positions of one (sequence, kv head) each.
 // Nothing is added with atomics: every position has one writer, and the sum over the group has
 // one order.  The weights' denominator is the sum of the unrounded probabilities (the output
 // divides by the sum of the bf16-rounded ones that its numerator uses, up to 2^-9 off for a single
@@ -35,7 +36,7 @@ static_assert(kFinishThreads / 32 >= kMaxGroup, "one warp per query head of a gr
 constexpr int kPerThread = 4;
 constexpr int kTile = kFinishThreads * kPerThread;   // positions of one weights block
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_decode_weights_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                 const __grid_constant__ CUtensorMap tmap_v, const Args a)
@@ -45,7 +46,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    decode_cta<D, true, true>(&tmap_k, &tmap_v, a, blockIdx.x, blockIdx.y, blockIdx.z, smem,
+    decode_cta<D, SPLIT, true>(&tmap_k, &tmap_v, a, blockIdx.x, blockIdx.y, blockIdx.z, smem,
                               a.err ? a.err : &g_weights_errors);
 }
 
@@ -155,7 +156,8 @@ cudaError_t launch_t(const DecodeLaunch &l, const WeightsLaunch &w, const CUtens
     a.score_stride = w.score_stride;
     a.part_lse2 = w.part_lse2;
     const size_t smem = DecodeGeom<D>::kSmemBytes;
-    auto kernel = paged_decode_weights_kernel<D>;
+    const bool split = l.n_split > 1;   // else the decode writes the rows
+    auto kernel = split ? paged_decode_weights_kernel<D, true> : paged_decode_weights_kernel<D, false>;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(smem));
     if (err != cudaSuccess)
@@ -175,7 +177,8 @@ cudaError_t launch_t(const DecodeLaunch &l, const WeightsLaunch &w, const CUtens
     const int rows_per_block = kFinishThreads / 32;   // (warps)
     const bool wide = l.n_split > kWideMergeSplits;
     f.merge_blocks =
-        (l.num_seqs * l.q_heads * (wide ? D / 32 : 1) + rows_per_block - 1) / rows_per_block;
+        split ? (l.num_seqs * l.q_heads * (wide ? D / 32 : 1) + rows_per_block - 1) / rows_per_block
+              : 0;
     f.tiles = (w.max_ctx + kTile - 1) / kTile;
     const long long grid =
         f.merge_blocks + static_cast<long long>(f.tiles) * l.kv_heads * l.num_seqs;

@@ -133,3 +133,61 @@ def test_decode(D, splits):
     assert splits == 0 or n == splits         # 20: the wide merge
     c.check(out)
     assert kvc.kvc_device_errors() == 0
+
+
+def decode_weights(c, splits, dtype=torch.float32):
+    out = torch.full(c.q.shape, 9.0, dtype=dtype, device="cuda")
+    weights = torch.zeros(c.S, H, c.max_ctx, device="cuda")
+    ws = kvc.kvc_decode_weights_plan(c.S, H * G, c.pool, c.max_ctx, splits)[2]
+    work = torch.full((ws,), 0xFF, dtype=torch.uint8, device="cuda")
+    kvc.kvc_decode_weights(out, weights, c.dq, c.dk, c.dv, c.dt, c.dc, c.max_ctx,
+                           num_splits=splits, workspace=work)
+    return out, weights.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [1, 3, 0, 20])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_decode_weights_is_decode(D, splits, dtype):
+    """The same output wherever it is not NaN, and NaN in the same places; among them rows whose
+    scores are all -infinity, whose softmax is 0 / 0."""
+    c = spoiled(D)
+    for p in range(CTX[6]):
+        c.at(c.k, 6, p)[0, 2] = NEG_INF
+    c.q[6, :2, 2] = int4.bf16_round(np.array([0.5, 2.0], np.float32))
+    c.upload()
+    out, _ = decode_weights(c, splits, dtype)
+    want, _ = c.decode(splits, dtype)
+    assert torch.equal(out.isnan(), want.isnan())
+    assert torch.equal(out.nan_to_num(nan=5.0), want.nan_to_num(nan=5.0))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [1, 0, 20])
+def test_weights(D, splits):
+    """A NaN softmax gives NaN weights to its kv head, for the sequence's positions alone; a score of
+    -infinity gives 0.  Finite weights: relative error 2 d of the score and the sum, 2^-24 each for the
+    six roundings of numbers up to X, 2^-20 for 2^x, the logarithm and the sums."""
+    c = spoiled(D)
+    c.q[3, 2, 0] = int4.bf16_round(np.array([-0.5], np.float32))[0]   # both -infinity now
+    c.upload()
+    out, got = decode_weights(c, splits)
+    q, k = (int4.bf16_value(x).astype(np.float64) for x in (c.q, c.k))
+    want = np.zeros(got.shape)
+    with np.errstate(invalid="ignore"):
+        for s, n in enumerate(CTX):
+            pos = np.arange(n)
+            for h in range(H * G if n else 0):
+                x = k[c.table[s][pos // P], pos % P][:, h // G] @ q[s, h] / math.sqrt(D)
+                w = np.exp(x - x.max())
+                want[s, h // G, :n] += w / w.sum()
+    assert np.isnan(want[0, 1, :50]).all() and want[3, 1, 5] == 0 and np.isfinite(want[3]).all()
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    Q = np.abs(q)[np.isfinite(q).all(-1)].sum(-1).max()
+    K = np.abs(k[np.isfinite(k)]).max()
+    d = (D + 8) * 2.0 ** -23 / math.sqrt(D) * Q * K
+    X = Q * K / math.sqrt(D) + math.log(c.max_ctx)
+    rho = 2 * d + 6 * 2.0 ** -24 * X / math.log(2) + 2.0 ** -20
+    fine = np.isfinite(want)
+    assert (np.abs(got[fine] - want[fine]) <= rho * want[fine] + 1e-37).all()
+    assert kvc.kvc_device_errors() == 0
