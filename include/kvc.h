@@ -561,7 +561,7 @@ kvc_status kvc_decode_int4(void *out, int32_t out_dtype, const void *q, const vo
  *   positions  the original position that each slot holds for that kv head; the caller starts a row
  *              with 0, 1, 2, ...; kvc_evict keeps it right, also for the tokens to come
  * A slot here is an index below context_lens[s], the position of the address rule: once slots are
- * evicted, the newest token is still the last of its sequence, but slot i no longer holds position
+ * evicted, a new token still goes to the end of its sequence, but slot i no longer holds position
  * i, and each kv head keeps its own positions.  Attention over the slots needs nothing else (keys
  * carry their positions).  weight_rows[s] is the row of sequence s (NULL: row s); a negative one
  * leaves that sequence out, one past num_rows too, flagged; rows are distinct within one call.
@@ -593,16 +593,21 @@ kvc_status kvc_decode_weights(void *out, int32_t out_dtype, float *weights,
  * recent), then those with the largest weight (NaN below every number), equal ones in slot order.
  * The kept slots from n on move into the evicted ones below n, both in ascending order (K and V,
  * raw 16-bit copies; weight and position with them), so that slots 0 .. n - 1 hold what is kept;
- * new_lens[s] = n.  The last slot has to hold the sequence's newest token: one that was cut gets at
- * least one more before the next call that names it (or its row is left out); where the position
- * that slot context_lens[s] holds does not follow that of the last slot, 1 << 13 is flagged.  Pages after the n-th slot's are the caller's to free.  K and V of slots from n on
- * stay as they are.  The call reads weights and positions and writes weights_out and positions_out,
- * which may be the same arrays (in place) or others that overlap neither; of a row they get: slots
- * below n as above, weights_out 0 for n .. context_lens[s] - 1 (the rest untouched), positions_out
- * for n .. weight_stride - 1 the positions that the next tokens will have.
- * A sequence within its budget keeps everything; a context past max_ctx is cut to it and flagged.  Pages that are written must be the
- * sequence's own (kvc_copy_pages first where others list them); moves that touch a page id outside the
- * pool are skipped and flagged, and that sequence's result is undefined.
+ * new_lens[s] = n.  The newest token's position is told by the first free slot, slot
+ * context_lens[s], whose position is the next token's (a full row: by its last slot): after a cut the
+ * last slot may hold any token, and a sequence may pause for any number of calls before its next one.
+ * 1 << 13 is flagged where a row is cut that has had no token since its last cut (its result is right
+ * all the same), and where the first free slot's position is not above that of the last slot (a row that
+ * was not started as above; the last slot then counts as the newest).  Pages after the n-th slot's are
+ * the caller's to free.  K and V of slots from n on stay as they are.  The call reads weights and
+ * positions and writes weights_out and positions_out, which may be the same arrays (in place; either
+ * of the two, or both) or others that overlap neither; of a row they get: slots below n as above,
+ * weights_out 0 for n .. context_lens[s] - 1 (the rest untouched), positions_out for n ..
+ * weight_stride - 1 the positions that the next tokens will have.
+ * A sequence within its budget keeps everything; a context past max_ctx is cut to it and flagged.
+ * Pages that are written must be the sequence's own (kvc_copy_pages first where others list them);
+ * moves that touch a page id outside the pool are skipped and flagged, and that sequence's result is
+ * undefined.
  *   budget         at least 1;  recent  0 .. budget;  max_ctx  at most 2^22
  *   new_lens       int32 [num_seqs] (out, device), not context_lens itself: every kv head reads that
  *   workspace      kvc_evict_plan's bytes (0 when budget >= max_ctx), 16-byte aligned

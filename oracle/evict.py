@@ -35,13 +35,14 @@ def weights(q, k_pool, block_table, context_lens, scale=None, layout="nhd") -> l
     return out
 
 
-def kept(w, pos, budget, recent) -> np.ndarray:
-    """Which of a row's slots stay (weights w and original positions pos of its slots)."""
+def kept(w, pos, budget, recent, last=None) -> np.ndarray:
+    """Which of a row's slots stay (weights w and original positions pos of its slots; last: the
+    newest token's position, by default the last slot's)."""
     n = min(len(w), budget)
     stay = np.zeros(len(w), bool)
     if len(w) == 0:
         return stay
-    newest = pos > int(pos[-1]) - recent
+    newest = pos > (int(pos[-1]) if last is None else last) - recent
     w = np.where(np.isnan(w), -np.inf, w.astype(np.float64))
     order = sorted(range(len(w)), key=lambda i: (not newest[i], 0.0 if newest[i] else -w[i], i))
     stay[order[:n]] = True
@@ -49,8 +50,10 @@ def kept(w, pos, budget, recent) -> np.ndarray:
 
 
 def evict(k_pool, v_pool, w, pos, block_table, context_lens, budget, recent, rows=None,
-          layout="nhd"):
-    """In place on the pools and on w, pos ([rows, Hkv, stride]); returns the new lengths."""
+          layout="nhd", newest=None):
+    """In place on the pools and on w, pos ([rows, Hkv, stride]); returns the new lengths.  newest[s]:
+    the position of sequence s's newest token, by default that of its last slot (a sequence that has
+    had no token since its last cut may hold any token there)."""
     kp, vp = _by_position(k_pool, layout), _by_position(v_pool, layout)
     P, H = kp.shape[1:3]
     new_lens = []
@@ -63,8 +66,9 @@ def evict(k_pool, v_pool, w, pos, block_table, context_lens, budget, recent, row
         new_lens.append(n)
         for h in range(H):
             ww, pp = w[row, h], pos[row, h]
-            total = int(pp[n_all - 1]) + 1 if n_all else 0
-            stay = kept(ww[:n_all], pp[:n_all], budget, recent)
+            last = -1 if n_all == 0 else int(pp[n_all - 1] if newest is None else newest[s])
+            total = last + 1
+            stay = kept(ww[:n_all], pp[:n_all], budget, recent, last)
             gaps = np.flatnonzero(~stay[:n])
             movers = n + np.flatnonzero(stay[n:])
             for g, m in zip(gaps, movers):

@@ -8,7 +8,8 @@
 // only what has to move leaves every slot either a source or a destination, never both: all moves
 // run at once, in place, at the least traffic (closing the gaps in order would move nearly every
 // row after the first gap).  `positions` keeps each slot's original position, which is what the
-// newest are told by.
+// newest are told by; the newest one itself is what the first free slot's position follows, because
+// after a cut the last slot may hold any token, and a sequence may pause before its next one.
 //
 // Selection (select_kernel).  A weight becomes a 32-bit key of the same order (NaN as the lowest, -0
 // as 0, the newest slots above every weight), and the n-th largest key is found digit by digit:
@@ -49,7 +50,8 @@ namespace cg = cooperative_groups;
 
 __device__ uint32_t g_evict_errors;
 
-// Device error bit of this kernel alone: a row's last slot does not hold its newest position.
+// Device error bit of this kernel alone: a row that is cut has had no token since its last cut (its
+// result is right all the same), or its first free slot's position is not above its last one's.
 constexpr uint32_t kErrPositionOrder = 1u << 13;
 
 constexpr int kThreads = 256;
@@ -251,7 +253,12 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     const int32_t *p_in = a.positions + base;
     float *w_out = a.weights_out + base;
     int32_t *p_out = a.positions_out + base;
-    const int last = N > 0 ? p_in[N - 1] : -1;   // the newest token's original position
+    // The newest token's original position.  In place one thread writes p_in[N] again: behind the
+    // cluster's barriers, or (nothing to evict) with a value from which the same `last` follows.
+    const int held = N > 0 ? p_in[N - 1] : -1;
+    const bool has_next = N > 0 && N < a.stride;
+    const int next = has_next ? p_in[N] : 0;
+    const int last = has_next && next > held ? next - 1 : held;
 
     // this warp's slots [lo, hi); the CTA's begin at cta_lo
     const long long per_warp = (N + static_cast<long long>(kWarpSlots) * kWarps * ctas - 1) /
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
     const int hi = static_cast<int>(min(static_cast<long long>(N), lo + per_warp));
 
     if (N <= a.budget) {   // nothing to evict
-        if (cta == 0 && threadIdx.x == 0 && N > 0 && N < a.stride && p_in[N] != last + 1)
+        if (cta == 0 && threadIdx.x == 0 && has_next && next <= held)
             atomicOr(err, kErrPositionOrder);
         for (int i = lo + lane; i < hi; i += 32) {
             w_out[i] = w_in[i];
@@ -362,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const Args a)
 
     // ---- the n-th largest key, and how many equal to it are kept ----
     __syncthreads();   // the histograms are zero
-    // (the slot after the last holds the next position; only this thread overwrites it, at its end)
-    if (cta == 0 && threadIdx.x == 0 && N < a.stride && p_in[N] != last + 1)
+    if (cta == 0 && threadIdx.x == 0 && has_next && (next <= held || next - 1 != held))
         atomicOr(err, kErrPositionOrder);
     sweep(0, [&](int i, const uint4 k) {
         if (i < hi && i - cta_lo < a.cached)

@@ -61,6 +61,24 @@ def test_weights_against_the_attention_oracle():
         np.testing.assert_allclose(got[s].sum(-1), case.q_heads // case.kv_heads)
 
 
+def test_a_row_that_is_cut_twice():
+    """A cut may leave an old token in the last slot: the newest position is then given."""
+    table = np.arange(2)[None]
+    kp, vp = (np.arange(2 * 16 * 64, dtype=np.uint16).reshape(2, 16, 1, 64) + i for i in (0, 9))
+    w = np.zeros((1, 1, 30), np.float32)
+    w[0, 0, 7] = 1.0
+    pos = np.arange(30, dtype=np.int32)[None, None].copy()
+    assert evict.evict(kp, vp, w, pos, table, [20], 8, 3).tolist() == [8]
+    # 17 .. 19 are the newest, 7 the heaviest, 0 .. 3 the first of equal weight
+    assert pos[0, 0, :9].tolist() == [0, 1, 2, 3, 17, 18, 19, 7, 20]
+    before = pos.copy()
+    assert evict.evict(kp, vp, w, pos, table, [8], 8, 3, newest=[19]).tolist() == [8]
+    assert np.array_equal(pos, before)
+    assert evict.evict(kp, vp, w, pos, table, [8], 4, 3, newest=[19]).tolist() == [4]
+    assert sorted(pos[0, 0, :4]) == [7, 17, 18, 19]
+    assert pos[0, 0, 4:].tolist() == list(range(20, 46))
+
+
 # --------------------------------------------------------------------- argument checks
 POOL = PoolDesc(32, 16, 2, 64)
 FAKE = ctypes.c_void_p(0x10000)   # never dereferenced: checks fail before any launch
