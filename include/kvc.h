@@ -537,8 +537,9 @@ kvc_status kvc_load_int4(void *k_out, void *v_out, int32_t out_dtype, const void
  * chunk_out = 64 (the block), workspace_bytes_out = the workspace that the call needs (0 without a merge).
  * The workspace belongs to one call at a time: calls that may overlap (two streams, two captured
  * graphs) need one each.  A query row enters the products as fp16 times a power of two of its own
- * (exact for elements down to 2^-23 of its largest), a probability times a value scale as fp16;
- * sums are fp32.  A page id outside the pool is not followed but flagged; that sequence's output is
+ * (exact for elements down to 2^-23 of its largest), a probability times a value scale as fp16 times
+ * a power of two of each group of 64 dims that follows the group's largest scale in the sequence: off
+ * by 2^-11 of itself, or by 2^-35 of that largest scale where the latter is more; sums are fp32.  A page id outside the pool is not followed but flagged; that sequence's output is
  * undefined.
  */
 kvc_status kvc_decode_int4_plan(int32_t num_seqs, int32_t q_heads, kvc_pool_desc pool,

@@ -13,9 +13,11 @@
 // end.  Putting the nibble under an exponent and subtracting the bias would double the conversion.
 // Query rows enter as fp16 scaled by a power of two of their own (largest |q| in [2^9, 2^10), so bf16's
 // eight bits are exact wherever they matter); probabilities times value scales as fp16 scaled by a
-// power of two that follows the largest value scale seen (vnorm), because a scale may have any
-// exponent of bf16: rounding errors stay at 2^-11 of each product.  Sums, maxima, the minimum's
-// part of both products and the accumulators are fp32.
+// power of two of each group of 64 dims that follows the group's largest value scale seen (vnorm),
+// because a scale may have any exponent of bf16.  A product is rounded by at most 2^-11 of itself or,
+// where it is an fp16 subnormal, by 2^-35 of that largest scale: a position whose scale is 2^24 below
+// another one's of the same group loses bits, and so does one that weighs 2^-24 of the heaviest.  Sums,
+// maxima, the minimum's part of both products and the accumulators are fp32.
 //
 // Work.  For each kv head the positions of all sequences, in 64-position blocks (sequence-major), are
 // cut into runs of equal cost.  A group of warps, one per kv head (up to 8 heads, else the largest
@@ -568,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float zacc[NG][2];          // sum of p lo, heads 2 t and 2 t + 1
     // heads 2 t and 2 t + 1: the sum; the maximum in use times f, and the y from which it moves
     float l_run[2], mf[2], m_thr[2], f[2], hq[NG][2];
-    float vnorm = 1.0f, v_thr = 0.0f;
+    float vnorm[NG], v_thr[NG];   // and the value scale from which vnorm moves
     int stage = 0;
     uint32_t phase = 0;
 
@@ -656,8 +658,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
                     o[n][b][0] = o[n][b][1] = o[n][b][2] = o[n][b][3] = 0.0f;
-            vnorm = 1.0f;
-            v_thr = 0.0f;   // any positive value scale sets vnorm
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                vnorm[g] = 1.0f;
+                v_thr[g] = 0.0f;   // any positive value scale sets vnorm
+            }
         }
 
         const uint8_t *st = ring + stage * group_stage;
@@ -740,8 +745,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
         }
 
-        // ---- running maxima, and the power of two on the value scales ----
-        float mb[2], vmax = 0.0f;
+        // ---- running maxima, and the powers of two on the value scales ----
+        float mb[2], vmax[NG];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             mb[j] = fmaxf(y[0][0][j], y[0][1][j]);
@@ -750,17 +755,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mb[j] = fmax3(mb[j], y[T][0][j], y[T][1][j]);
         }
 #pragma unroll
-        for (int T = 0; T < kTiles; ++T)
+        for (int g = 0; g < NG; ++g) {
+            vmax[g] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                vmax = fmax3(vmax, __uint_as_float(vp[T][i][0] << 16),
-                             __uint_as_float(vp[T][i][NG - 1] << 16));
-        if (__any_sync(0xffffffffu, mb[0] > m_thr[0] || mb[1] > m_thr[1] || vmax > v_thr)) {
+            for (int T = 0; T < kTiles; ++T)
+                vmax[g] = fmax3(vmax[g], __uint_as_float(vp[T][0][g] << 16),
+                                __uint_as_float(vp[T][1][g] << 16));
+        }
+        if (__any_sync(0xffffffffu, mb[0] > m_thr[0] || mb[1] > m_thr[1] || vmax[0] > v_thr[0] ||
+                                        vmax[NG - 1] > v_thr[NG - 1])) {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
                 mb[0] = fmaxf(mb[0], __shfl_xor_sync(0xffffffffu, mb[0], off));
                 mb[1] = fmaxf(mb[1], __shfl_xor_sync(0xffffffffu, mb[1], off));
-                vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    vmax[g] = fmaxf(vmax[g], __shfl_xor_sync(0xffffffffu, vmax[g], off));
             }
             float fix[2];
 #pragma unroll
@@ -777,24 +787,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mf[j] = mf_new;
                 }
             }
-            float turn = 1.0f;
-            if (vmax > v_thr) {   // the same in every lane that shares the maximum: all of them
-                // vnorm = 2^(10 - e) for the largest scale's exponent e: vmax vnorm in [2^10, 2^11)
-                const int e = max(-100, static_cast<int>(__float_as_uint(vmax) >> 23) - 127);
-                const float vn = __uint_as_float(static_cast<uint32_t>(127 + 10 - e) << 23);
-                turn = v_thr > 0.0f ? vn / vnorm : 1.0f;   // unset: every code product was 0
-                vnorm = vn;
-                v_thr = kMaxScaled / vn;
-            }
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    o[n][b][0] *= fix[0] * turn;
-                    o[n][b][1] *= fix[1] * turn;
-                    o[n][b][2] *= fix[0] * turn;
-                    o[n][b][3] *= fix[1] * turn;
+            for (int g = 0; g < NG; ++g) {
+                float turn = 1.0f;
+                if (vmax[g] > v_thr[g]) {   // the same in every lane that shares the maximum: all of them
+                    // vnorm = 2^(10 - e) for the largest scale's exponent e: vmax vnorm in [2^10, 2^11)
+                    const int e = max(-100, static_cast<int>(__float_as_uint(vmax[g]) >> 23) - 127);
+                    const float vn = __uint_as_float(static_cast<uint32_t>(127 + 10 - e) << 23);
+                    turn = v_thr[g] > 0.0f ? vn / vnorm[g] : 1.0f;   // unset: every code product was 0
+                    vnorm[g] = vn;
+                    v_thr[g] = kMaxScaled / vn;
                 }
+#pragma unroll
+                for (int n = 2 * g; n < 2 * g + 2; ++n)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        o[n][b][0] *= fix[0] * turn;
+                        o[n][b][1] *= fix[1] * turn;
+                        o[n][b][2] *= fix[0] * turn;
+                        o[n][b][3] *= fix[1] * turn;
+                    }
+            }
         }
 
         // ---- probabilities, and out ----
@@ -819,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int g = 0; g < NG; ++g)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float sc = __uint_as_float(vp[T][i][g] << 16) * vnorm;
+                    const float sc = __uint_as_float(vp[T][i][g] << 16) * vnorm[g];
                     const float lo = __uint_as_float(vp[T][i][g] & 0xFFFF0000u);
                     zacc[g][0] = fmaf(p[i][0], lo, zacc[g][0]);
                     zacc[g][1] = fmaf(p[i][1], lo, zacc[g][1]);
@@ -878,7 +891,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // pieces of kv head h own slots [h (S + R), (h + 1) (S + R)), piece (s, run) s + run
             // there: distinct for every piece, consecutive for one unit's
             const int slot = kvh * (a.num_seqs + a.runs) + s + run;
-            const float v_inv = 1.0f / vnorm;   // a power of two: exact
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int head = 2 * t + j;
@@ -888,6 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {   // dims 32 n + 16 i + 2 r, + 1
                             const float z = zacc[n / 2][j];
+                            const float v_inv = 1.0f / vnorm[n / 2];   // a power of two: exact
                             float2 v;
                             v.x = fmaf(o[n][0][2 * i + j] * 16777216.0f, v_inv, z) * inv[j];
                             v.y = fmaf(o[n][1][2 * i + j] * 1048576.0f, v_inv, z) * inv[j];

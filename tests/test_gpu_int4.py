@@ -484,3 +484,29 @@ def test_load_brings_a_prefix_back_for_append():
     assert np.abs(out.double().cpu().numpy() - ref).max() <= 1e-2
     want = int4.load(pools[0], pools[2], slots).astype(np.float32)
     assert torch.equal(k.cpu(), torch.from_numpy(want).bfloat16())
+
+
+def test_groups_of_any_exponent():
+    """Value scales of a vector's two groups 2^60 apart, either way round: each group of dims is right in
+    its own measure, also after one of them grows late."""
+    case = ragged(63, 16, 2, 4, 128, [300, 77, 500])
+    pools = filled(case)
+    powers = np.zeros((case.num_seqs, 2))
+    powers[0], powers[1], powers[2] = (30, -30), (-30, 30), (-30, 12)
+    for s in range(case.num_seqs):
+        for i, page in enumerate(case.block_table[s][:-(-int(case.context_lens[s]) // 16)]):
+            p = pools[3][page]
+            up = powers[s].copy()
+            if s == 2 and i < 20:
+                up[1] = 0                    # group 1 of sequence 2 grows at position 320
+            v = int4.bf16_value(p) * (2.0 ** up[:, None]).astype(np.float32)
+            pools[3][page] = np.where(p == int4.NAN_BITS, p, int4.bf16_round(np.nan_to_num(v)))
+    ref = int4.attention(case.q, *pools, case.block_table, case.context_lens)
+    same = ragged(63, 16, 2, 4, 128, [300, 77, 500])
+    d = bounds(same, filled(same))[0]        # of the pools before they were scaled
+    for splits in (1, 0, 3):
+        got = run_decode(case.q, pools, case.block_table, case.context_lens, case.max_ctx, splits)
+        for s in range(case.num_seqs):
+            for g in range(2):
+                err = np.abs(got[s] - ref[s])[:, 64 * g:64 * g + 64].max()
+                assert err <= d * 2.0 ** powers[s, g], (splits, s, g)
