@@ -83,7 +83,9 @@ cudaError_t launch_decode_t(const DecodeLaunch &l, const CUtensorMap &tk, const 
 
 // The bounded wait every kernel uses, on an mbarrier phase that nothing completes: it gives
 // up after kWaitLimitCycles and the CTA records kErrSelftestWait and returns, leaving the
-// context usable.  A diagnostic of the failure path, with no fault and no hang.
+// context usable.  Then the wait of a warp that polls for itself (warp_wait_over), its lanes' clocks as
+// far apart as half the limit: all of them have to give up in the same turn.  A diagnostic of the
+// failure path, with no fault and no hang.
 __global__ void __launch_bounds__(32) selftest_wait_kernel(uint32_t *word)
 {
     __shared__ uint64_t bar;
@@ -92,7 +94,14 @@ __global__ void __launch_bounds__(32) selftest_wait_kernel(uint32_t *word)
         fence_mbar_init();
     }
     __syncwarp();
-    if (!__all_sync(0xffffffffu, mbar_wait(&bar, 0)) && threadIdx.x == 0)
+    const bool waited = __all_sync(0xffffffffu, mbar_wait(&bar, 0));
+    const long long since = clock64() - threadIdx.x * (kWaitLimitCycles / 64);
+    unsigned turns = 0;
+    while (!mbar_test(&bar, 0) && !warp_wait_over(since))
+        ++turns;
+    int together;
+    __match_all_sync(0xffffffffu, turns, &together);
+    if (!waited && together && threadIdx.x == 0)
         atomicOr(word ? word : &g_decode_errors, kErrSelftestWait);
 }
 

@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ready = !ended && (issued < NS || mbar_test(&empty[grp * NS + st], phase));
             ready = __shfl_sync(0xffffffffu, ready, lane & ~3);   // the group's lanes go together
             if (!__any_sync(0xffffffffu, ready)) {
-                if (clock64() - since > kWaitLimitCycles) {
+                if (warp_wait_over(since)) {
                     ok = false;
                     break;
                 }

@@ -121,6 +121,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity)
     return true;
 }
 
+// Whether a wait that the whole warp is in, and that began at `since` (each lane's own clock), has taken
+// longer than kWaitLimitCycles: the same answer in every lane, so that none goes on alone into a vote or
+// shuffle of all of them.
+__device__ __forceinline__ bool warp_wait_over(long long since)
+{
+    return __any_sync(0xffffffffu, clock64() - since > kWaitLimitCycles);
+}
+
 // Named barrier over `count` threads (a multiple of 32), id 1..15.
 __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t count)
 {
