@@ -398,8 +398,8 @@ kvc_status kvc_set_error_word(uint32_t *device_word);
 /*
  * kvc_selftest_wait -- a diagnostic of the failure path every kernel shares: one CTA waits on
  * an mbarrier phase that nothing completes, with the bounded waits the kernels use (a thread's own, then
- * a polling warp's, whose lanes give up together); after a second or two it has given up, sets bit 1 << 12 of the device error word (kvc_device_errors)
- * and returns.  Nothing faults or hangs, and later calls run as usual.
+ * a polling warp's, whose lanes give up together); after a second or two it has given up, sets bit
+ * 1 << 12 of the device error word (kvc_device_errors) and returns.  Nothing faults or hangs, and later calls run as usual.
  */
 kvc_status kvc_selftest_wait(void *stream);
 

@@ -30,6 +30,8 @@ enum DeviceErrorBits : uint32_t {
     kErrPageRange = 1u << 10,      // a page copy named a page outside the pool: skipped
     kErrScaleRange = 1u << 11,     // INT8 append: a value scale above its fp16 limit (4000)
     kErrSelftestWait = 1u << 12,   // kvc_selftest_wait: its wait ran out, as it must
+    kErrPositionOrder = 1u << 13,  // eviction: a row cut twice with no token in between (its result
+                                   // is right), or positions that do not go on behind its last slot
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p)

@@ -50,10 +50,6 @@ namespace cg = cooperative_groups;
 
 __device__ uint32_t g_evict_errors;
 
-// Device error bit of this kernel alone: a row that is cut has had no token since its last cut (its
-// result is right all the same), or its first free slot's position is not above its last one's.
-constexpr uint32_t kErrPositionOrder = 1u << 13;
-
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
