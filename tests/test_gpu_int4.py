@@ -510,3 +510,69 @@ def test_groups_of_any_exponent():
             for g in range(2):
                 err = np.abs(got[s] - ref[s])[:, 64 * g:64 * g + 64].max()
                 assert err <= d * 2.0 ** powers[s, g], (splits, s, g)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_position_counts_once_to_the_derived_bound(D):
+    """A query of zeros, so the output is the mean of V; held for every sequence of n positions to what
+    its own sums can lose.  V the largest |minimum|, R the largest 15 scale.  No probability and no
+    product is rounded (probabilities are 1, a bf16 scale is exact in fp16).
+      * minima: a thread adds n / 8 of them one after the other, the j-th sum up to j V is off by half a
+        step, 2^-24 j V: n^2 / 128 2^-24 V a thread, n^2 / 16 for the eight, n / 16 2^-24 V of the mean;
+        three more sums join the threads: 3 2^-24 V;
+      * codes: a block of 64 positions is four products whose sums the tensor cores cut, 2^-23 each:
+        2^-21 R of the mean; the n / 64 blocks are added one after the other: n / 128 2^-24 R;
+      * joining the pieces: a log-sum-exp up to 8 in base e, rounded three times (2^-21 each, the
+        logarithm included), 2^x (2^-22): a weight is off by 2^-19, numerator and sum 2^-18 (V + R);
+        the division and the last product are below 2^-22 (V + R).
+    A position lost, doubled or of another sequence moves the mean by about |v| / n, above the bound
+    for all but the smallest |v| at the longest sequence."""
+    ctx = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 100, 511, 512, 513, 1030, 2500]
+    case = ragged(7, 16, 2, 4, D, ctx)
+    pools = filled(case)
+    q = np.zeros_like(case.q)
+    ref = int4.attention(q, *pools, case.block_table, case.context_lens)
+    vp = int4.bf16_value(pools[3]).astype(np.float64)
+    V, R = np.nanmax(np.abs(vp[..., 1])), np.nanmax(15 * vp[..., 0])
+    n = case.context_lens.astype(np.float64)
+    bound = ((n / 16 + 3) * V + n / 128 * R) * 2.0 ** -24 + 2.0 ** -21 * R
+    for splits in (0, 1, 2, 5):
+        got = run_decode(q, pools, case.block_table, case.context_lens, case.max_ctx, splits)
+        joined = (2.0 ** -18 + 2.0 ** -22) * (V + R)
+        err = np.abs(got - ref).max((1, 2))
+        assert (err <= bound + joined).all(), (splits, (err / (bound + joined)).max())
+
+
+def test_append_over_a_loaded_prefix_is_append_over_its_values():
+    """kvc_append over pages that kvc_load_int4 filled, and over pages that the oracle's values (rounded
+    to bf16) were put into without the GPU: the same bits."""
+    case = build_case(61, name="int4-append", page_size=16, q_heads=8, kv_heads=2, head_dim=128,
+                      context_lens=lambda rng: np.array([40, 77]), q_lens=lambda c: np.array([9, 20]))
+    pages, P, H, D = case.k_pool.shape
+    slots = np.concatenate([case.block_table[s][np.arange(n) // P] * P + np.arange(n) % P
+                            for s, n in enumerate(case.context_lens - np.array([9, 20]))])
+    pools = empty_pools(pages, P, H, D, "nhd")
+    flat = [x.reshape(pages * P, H, D)[slots] for x in (case.k_pool, case.v_pool)]
+    int4.store(*pools, *flat, slots)
+    dev, ds = device_pools(pools), i32_tensor(slots, "cuda")
+    loaded = [torch.empty(len(slots), H, D, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    kvc.kvc_load_int4(*loaded, *dev, ds)
+    first = [torch.zeros(pages, P, H, D, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    kvc.kvc_store(*first, *loaded, ds)
+    second = []
+    for codes, params in zip(pools[:2], pools[2:]):
+        bits = np.zeros((pages * P, H, D), np.uint16)
+        bits[slots] = int4.bf16_round(int4.load(codes, params, slots).astype(np.float32))
+        second.append(bf16_tensor(bits.reshape(pages, P, H, D), "cuda"))
+    bt, ctx = i32_tensor(case.block_table, "cuda"), i32_tensor(case.context_lens, "cuda")
+    ind = i32_tensor(case.q_indptr, "cuda")
+    new = torch.empty(case.num_tokens, dtype=torch.int32, device="cuda")
+    kvc.kvc_slot_mapping(new, bt, ctx, ind, P, max_q_len=case.max_q_len)
+    outs = []
+    for kp, vp in (first, second):
+        kvc.kvc_store(kp, vp, bf16_tensor(case.k_new, "cuda"), bf16_tensor(case.v_new, "cuda"), new)
+        outs.append(torch.full((case.num_tokens, 8, D), float("nan"), device="cuda"))
+        kvc.kvc_append(outs[-1], bf16_tensor(case.q, "cuda"), kp, vp, bt, ind, ctx, case.max_q_len,
+                       case.max_ctx)
+    assert torch.isfinite(outs[0]).all() and torch.equal(*outs)
+    assert all(torch.equal(a, b) for a, b in zip(first, second))
