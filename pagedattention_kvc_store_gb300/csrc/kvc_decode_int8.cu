@@ -875,13 +875,13 @@ __global__ void __launch_bounds__(kThreads, 3)
                 f[k] = (mw == -INFINITY) ? 0.0f : fast_exp2(mw - M);
                 L += f[k] * red_l[k * kMaxGroup + row];
             }
-            const float inv = (L > 0.0f) ? 1.0f / L : 0.0f;
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // NaN stays NaN
 #pragma unroll
             for (int k = 0; k < kConsumerWarps; ++k)
                 row_w[row * kConsumerWarps + k] = f[k] * inv;
             if (!whole)
                 a.part_lse[static_cast<size_t>(slot) * G + row] =
-                    (L > 0.0f) ? (M + log2f(L)) * kLn2 : -INFINITY;
+                    L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
         }
         named_barrier(1, kConsumerWarps * 32);
         constexpr int kVec = D / 4;
@@ -1012,30 +1012,30 @@ __global__ void __launch_bounds__(128) merge_flat_kernel(const Args a)
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        if (M != -INFINITY) {
+        // (the largest lse skips NaN: of pieces that are all NaN it is -infinity)
+        const float mu = M == -INFINITY ? 0.0f : M;
 #pragma unroll
-            for (int j = 0; j < kPre; ++j) {
-                if (j < count) {
-                    const float wj = fast_exp2((__shfl_sync(0xffffffffu, mine, j) - M) * kLog2e);
-                    sum += wj;
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        acc[v] = fmaf(wj, pre[j][v], acc[v]);
-                }
-            }
-            for (int j = kPre; j < count; ++j) {
-                const float lj = j < 32 ? __shfl_sync(0xffffffffu, mine, j)
-                                        : __ldcg(lse + static_cast<size_t>(j) * G);
-                const float wj = fast_exp2((lj - M) * kLog2e);
+        for (int j = 0; j < kPre; ++j) {
+            if (j < count) {
+                const float wj = fast_exp2((__shfl_sync(0xffffffffu, mine, j) - mu) * kLog2e);
                 sum += wj;
-                const float *src = po + static_cast<size_t>(j) * G * D;
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    acc[v] = fmaf(wj, __ldcg(src + v), acc[v]);
+                    acc[v] = fmaf(wj, pre[j][v], acc[v]);
             }
         }
+        for (int j = kPre; j < count; ++j) {
+            const float lj = j < 32 ? __shfl_sync(0xffffffffu, mine, j)
+                                    : __ldcg(lse + static_cast<size_t>(j) * G);
+            const float wj = fast_exp2((lj - mu) * kLog2e);
+            sum += wj;
+            const float *src = po + static_cast<size_t>(j) * G * D;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                acc[v] = fmaf(wj, __ldcg(src + v), acc[v]);
+        }
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const size_t o = static_cast<size_t>(row) * D + lane * V;
     if constexpr (V == 4) {
         store_out4(a.out, a.out_f32, o,

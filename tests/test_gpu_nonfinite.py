@@ -191,3 +191,30 @@ def test_weights(D, splits):
     fine = np.isfinite(want)
     assert (np.abs(got[fine] - want[fine]) <= rho * want[fine] + 1e-37).all()
     assert kvc.kvc_device_errors() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [1, 2, 0, 9])
+def test_decode_int8(D, splits):
+    """A NaN scale makes NaN of the rows that attend over its position, in a sequence of one piece and of
+    many, and of no other; a NaN in the query makes NaN of its row, all of whose pieces are NaN."""
+    c = Case(D)
+    rng = np.random.default_rng(3)
+    shape = (len(c.k), P, H, D)
+    codes = [torch.from_numpy(rng.integers(-127, 128, shape, dtype=np.int8)).cuda() for _ in "kv"]
+    scales = [np.full((len(c.k), H, P), 0.01, np.float32) for _ in "kv"]
+    scales[0][c.table[0, 19 // P], 1, 19 % P] = np.nan        # sequence 0 (50), K of kv head 1
+    scales[0][c.table[1, 700 // P], 0, 700 % P] = np.nan      # sequence 1 (2,500), K of kv head 0
+    scales[1][c.table[2, 250 // P], 1, 250 % P] = np.nan      # sequence 2 (300), V of kv head 1
+    c.q[1, 3, 5] = NAN                                        # every piece of one query head
+    nan_rows = np.zeros((c.S, H * G), bool)
+    nan_rows[0, 2:] = nan_rows[1, :2] = nan_rows[1, 3] = nan_rows[2, 2:] = True
+    dev = codes + [torch.from_numpy(x).cuda() for x in scales]
+    c.upload()
+    out = torch.full(c.q.shape, 9.0, device="cuda")
+    ws = kvc.kvc_decode_int8_plan(c.S, H * G, kvc.int8_pool_desc(dev[0]), c.max_ctx, splits)[2]
+    work = torch.empty(max(ws, 16), dtype=torch.uint8, device="cuda")
+    kvc.kvc_decode_int8(out, c.dq, *dev, c.dt, c.dc, c.max_ctx, num_splits=splits, workspace=work)
+    got = out.cpu().numpy()
+    assert np.isnan(got[nan_rows]).all() and np.isfinite(got[~nan_rows]).all()
+    assert not got[CTX == 0].any() and kvc.kvc_device_errors() == 0
