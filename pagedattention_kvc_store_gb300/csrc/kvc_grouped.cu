@@ -619,7 +619,7 @@ __device__ __forceinline__ bool prefix_cta(const CUtensorMap *tmap_k, const CUte
             f[w] = (mw == -INFINITY) ? 0.0f : fast_exp2(mw - M);
             L += f[w] * red_l[slot0 + w * 16];
         }
-        const float inv = (L > 0.0f) ? 1.0f / L : 0.0f;
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // NaN stays NaN
 #pragma unroll
         for (int w = 0; w < kWarpsPerTile; ++w)
             row_w[r * kWarpsPerTile + w] = f[w] * inv;
@@ -630,7 +630,7 @@ __device__ __forceinline__ bool prefix_cta(const CUtensorMap *tmap_k, const CUte
             (static_cast<long long>(seq) * a.q_heads + static_cast<long long>(kvh) * G + gh) *
                 a.split_stride + split;
         row_slot[r] = prow;
-        a.part_lse[prow] = (L > 0.0f) ? (M + log2f(L)) * kLn2 : -INFINITY;
+        a.part_lse[prow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
     }
     named_barrier(1, kConsumerWarps * 32);
     constexpr int kVec = D / 4;

@@ -218,3 +218,25 @@ def test_decode_int8(D, splits):
     got = out.cpu().numpy()
     assert np.isnan(got[nan_rows]).all() and np.isfinite(got[~nan_rows]).all()
     assert not got[CTX == 0].any() and kvc.kvc_device_errors() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_shared_prefix(D):
+    """A NaN key in pages that a group shares reaches every member's rows of that kv head, in positions
+    of its own those of one member; a NaN query one row.  Groups of 2 and 1, 96 and 16 shared."""
+    c = Case(D)
+    c.table[2, :6] = c.table[1, :6]           # sequences 1 and 2 share 96 positions
+    c.at(c.k, 1, 30)[0, 4] = NAN
+    c.at(c.k, 2, 200)[1, 0] = NAN
+    c.at(c.k, 4, 3)[0, 9] = NAN               # sequence 4, alone in its group
+    c.q[1, 3, 5] = NAN
+    c.upload()
+    i32 = lambda x: i32_tensor(np.array(x), "cuda")
+    ws = kvc.kvc_decode_shared_prefix_plan(c.S, H * G, c.pool, c.max_ctx, 2, 96)
+    work = torch.full((ws,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full(c.q.shape, 9.0, device="cuda")
+    kvc.kvc_decode_shared_prefix(out, c.dq, c.dk, c.dv, c.dt, c.dc, c.max_ctx, i32([0, 2, 3]),
+                                 i32([1, 2, 4]), i32([96, 16]), 2, 96, work)
+    c.check(out)
+    nan = np.isnan(c.reference()).all(-1)
+    assert nan.sum() == 2 + 1 + 2 + 2 + 2 and kvc.kvc_device_errors() == 0
