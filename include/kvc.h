@@ -309,8 +309,8 @@ kvc_status kvc_decode_noalloc(void *out, int32_t out_dtype, const void *q,
  *   out[r] = sum_j w_j partial_o[r][j] / sum_j w_j;   lse_out[r] = M + log(sum_j w_j).
  * Splits with lse = -inf hold no key: their partial_o is not used (the first few splits'
  * partials are loaded with the lse values, so partial_o must span every split).  A row whose
- * splits are all empty gets out = 0 and lse_out = -inf.  out may be pinned host memory, as for
- * kvc_decode.  (The pages leave partitioning and combining
+ * splits are all empty gets out = 0 and lse_out = -inf; a NaN lse makes its row and lse_out NaN.
+ * out may be pinned host memory, as for kvc_decode.  (The pages leave partitioning and combining
  * inside the kernel open -- "KV Cache Management and PagedAttention", "Compute attention
  * over scattered KV"; this is the plain combination of softmax-normalised pieces.)
  *   partial_o    fp32 [rows][num_splits][head_dim]
@@ -399,7 +399,8 @@ kvc_status kvc_set_error_word(uint32_t *device_word);
  * kvc_selftest_wait -- a diagnostic of the failure path every kernel shares: one CTA waits on
  * an mbarrier phase that nothing completes, with the bounded waits the kernels use (a thread's own, then
  * a polling warp's, whose lanes give up together); after a second or two it has given up, sets bit
- * 1 << 12 of the device error word (kvc_device_errors) and returns.  Nothing faults or hangs, and later calls run as usual.
+ * 1 << 12 of the device error word (kvc_device_errors) and returns.  Nothing faults or hangs, and
+ * later calls run as usual.
  */
 kvc_status kvc_selftest_wait(void *stream);
 
@@ -539,8 +540,8 @@ kvc_status kvc_load_int4(void *k_out, void *v_out, int32_t out_dtype, const void
  * graphs) need one each.  A query row enters the products as fp16 times a power of two of its own
  * (exact for elements down to 2^-23 of its largest), a probability times a value scale as fp16 times
  * a power of two of each group of 64 dims that follows the group's largest scale in the sequence: off
- * by 2^-11 of itself, or by 2^-35 of that largest scale where the latter is more; sums are fp32.  A page id outside the pool is not followed but flagged; that sequence's output is
- * undefined.
+ * by 2^-11 of itself, or by 2^-35 of that largest scale where the latter is more; sums are fp32.  A
+ * page id outside the pool is not followed but flagged; that sequence's output is undefined.
  */
 kvc_status kvc_decode_int4_plan(int32_t num_seqs, int32_t q_heads, kvc_pool_desc pool,
                                 int32_t max_ctx, int32_t num_splits, int32_t *splits_out,

@@ -1197,6 +1197,12 @@ cudaError_t launch_t(const DecodeInt4Launch &l, const CUtensorMap (&maps)[4], cu
 
 }  // namespace
 
+// A divisor, because a box holds the heads of a whole group: the eight warps of a CTA are all busy for 1,
+// 2, 4, 8 and 16 heads, seven for 7, six for 3, 6, 9 and 12, five for 5 and 10, and 11 and 13 take groups
+// of one head, whose boxes cost the most TMA operations.  64 sequences of up to 4,096 positions
+// (G = 4, D = 128), share of the HBM floor: 4 heads 30.0 us (42%), 5 40.7 (39%), 7 41.8 (53%), 8 42.3
+// (60%), 9 66.1 (43%), 12 67.7 (56%), 16 69.9 (72%), but 11 118 (29%) and 13 137 (30%); 8 of up to
+// 131,072: 3 heads 83 (61%), 4 85 (80%), 5 151 (56%), 8 153 (89%), 9 222 (69%), 11 265 (70%).
 int int4_group_heads(int kv_heads)
 {
     int n = kv_heads < 8 ? kv_heads : 8;

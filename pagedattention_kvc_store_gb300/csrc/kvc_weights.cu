@@ -16,8 +16,9 @@
 // position).
 //
 // Bound: HBM.  64 sequences of up to 4,096 positions (32 / 8 heads, D = 128, 617 MB): 108 us, 97 of them
-// the decode with its scores and 12 the second launch; 8 of up to 131,072 (64 / 8 heads, 3.3 GB): 563 us,
-// 5.9 TB/s, 508 and 45, the scores (205 MB, written and read) going through HBM.
+// the decode with its scores and 11 the second launch; 8 of up to 131,072 (64 / 8 heads, 3.3 GB): 569 to
+// 582 us call after call, 5.7 to 5.8 TB/s (510 and 43 each by itself), the scores (205 MB, written and
+// read) going through HBM.
 #include <math.h>
 
 #include "kvc_decode_cta.cuh"
