@@ -240,3 +240,33 @@ def test_decode_shared_prefix(D):
     c.check(out)
     nan = np.isnan(c.reference()).all(-1)
     assert nan.sum() == 2 + 1 + 2 + 2 + 2 and kvc.kvc_device_errors() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [1, 2, 0, 9])
+def test_decode_int4(D, splits):
+    """NaN parameters (a group that held a NaN or an infinity) reach the rows that attend over them, V's
+    only the group's dims; a NaN in the query its row, all of whose pieces are NaN."""
+    c = Case(D)
+    rng = np.random.default_rng(4)
+    codes = [torch.from_numpy(rng.integers(0, 256, (len(c.k), P, H, D // 2), dtype=np.uint8)).cuda()
+             for _ in "kv"]
+    params = [np.empty((len(c.k), H, P, D // 64, 2), np.uint16) for _ in "kv"]
+    for x in params:
+        x[..., 0] = int4.bf16_round(np.float32(0.25))
+        x[..., 1] = int4.bf16_round(rng.standard_normal(x.shape[:-1]).astype(np.float32))
+    params[0][c.table[0, 19 // P], 1, 19 % P, 0] = NAN        # sequence 0 (50), K of kv head 1
+    params[0][c.table[1, 700 // P], 0, 700 % P, -1] = NAN     # sequence 1 (2,500), K of kv head 0
+    params[1][c.table[2, 250 // P], 1, 250 % P, -1] = NAN     # sequence 2 (300), V of kv head 1, last group
+    c.q[1, 3, 5] = NAN
+    nan = np.zeros((c.S, H * G, D), bool)
+    nan[0, 2:] = nan[1, :2] = nan[1, 3] = nan[2, 2:, D - 64:] = True
+    dev = codes + [bf16_tensor(x, "cuda") for x in params]
+    c.upload()
+    out = torch.full(c.q.shape, 9.0, device="cuda")
+    ws = kvc.kvc_decode_int4_plan(c.S, H * G, kvc.int4_pool_desc(dev[0]), c.max_ctx, splits)[2]
+    work = torch.full((max(ws, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+    kvc.kvc_decode_int4(out, c.dq, *dev, c.dt, c.dc, c.max_ctx, num_splits=splits, workspace=work)
+    got = out.cpu().numpy()
+    assert np.isnan(got[nan]).all() and np.isfinite(got[~nan]).all()
+    assert not got[CTX == 0].any() and kvc.kvc_device_errors() == 0
