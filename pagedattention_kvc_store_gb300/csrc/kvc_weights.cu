@@ -9,7 +9,8 @@
 // score.  Reading K again for the weights would cost half of the pass once more; the scores are
 // 4 G bytes a position against the 4 D bytes of its K and V (G = 4, D = 128: 3%), so the decode CTAs
 // write them, and the launch that merges the partials also turns them into weights: its first
-// blocks merge (one warp a row; none where there is one split), the others take 1,024 positions of one (sequence, kv head) each.
+// blocks merge (one warp a row; none where there is one split), the others take 1,024 positions of one
+// (sequence, kv head) each.
 // Nothing is added with atomics: every position has one writer, and the sum over the group has
 // one order.  The weights' denominator is the sum of the unrounded probabilities (the output
 // divides by the sum of the bf16-rounded ones that its numerator uses, up to 2^-9 off for a single
