@@ -26,19 +26,19 @@ def listed():
              page=64, layout="hnd", rotary=64, pairing="adjacent", axes=2, far=1000),
         # a handful of short sources, one to three queries each: latency
         dict(name="cross tiny", op="cross", sources=4, lo=1, hi=100, lens=1, empty=0, q_lo=1, q_hi=3,
-             kv_heads=2, group=2, head_dim=64, page=16, layout="nhd"),
+             kv_heads=2, group=2, head_dim=64, page=16, layout="nhd", lse=True),
         # a decode step of 64 requests with 4 beams each over their sources
         dict(name="cross beams", op="cross", sources=64, lo=512, hi=4096, lens=2, empty=0, q_lo=4,
-             q_hi=4, kv_heads=8, group=4, head_dim=128, page=16, layout="nhd"),
+             q_hi=4, kv_heads=8, group=4, head_dim=128, page=16, layout="nhd", lse=False),
         # prompts of up to 400 tokens over the same sources
         dict(name="cross prompts", op="cross", sources=64, lo=512, hi=4096, lens=2, empty=0, q_lo=200,
-             q_hi=400, kv_heads=8, group=4, head_dim=128, page=16, layout="nhd"),
-        # few sources of long contexts, 16 tokens each
+             q_hi=400, kv_heads=8, group=4, head_dim=128, page=16, layout="nhd", lse=False),
+        # few sources of long contexts, 16 tokens each, to be joined with others by their log-sum-exps
         dict(name="cross long", op="cross", sources=8, lo=32768, hi=131072, lens=3, empty=0, q_lo=16,
-             q_hi=16, kv_heads=8, group=8, head_dim=128, page=64, layout="nhd"),
+             q_hi=16, kv_heads=8, group=8, head_dim=128, page=64, layout="nhd", lse=True),
         # ragged: sources without a state, requests without a token, head-major pages
         dict(name="cross ragged", op="cross", sources=19, lo=1, hi=2001, lens=4, empty=7, q_lo=0,
-             q_hi=201, kv_heads=5, group=1, head_dim=64, page=32, layout="hnd"),
+             q_hi=201, kv_heads=5, group=1, head_dim=64, page=32, layout="hnd", lse=True),
         # two branches of each of four short sequences, one layer, one more token each
         dict(name="branches tiny", op="branch", seqs=4, lo=1, hi=100, lens=1, empty=0, branches=2,
              grow=1, layers=1, kv_heads=2, head_dim=64, page=16, layout="nhd"),
@@ -77,7 +77,7 @@ def draw(rng):
         room = min((1 << 23) // (hi * q_hi), (1 << 20) // hi)
         c.update(hi=hi, lo=rng.choice([1, max(1, hi // 8), max(1, hi // 2), hi]), group=group,
                  q_hi=q_hi, q_lo=rng.choice([0, 1, max(1, q_hi // 2), q_hi]),
-                 sources=_log_int(rng, 1, max(1, min(256, room))))
+                 sources=_log_int(rng, 1, max(1, min(256, room))), lse=rng.random() < 0.5)
         if hi * q_hi > (1 << 23):
             c["q_hi"] = max(1, (1 << 23) // hi)
             c["q_lo"] = min(c["q_lo"], c["q_hi"])
@@ -131,7 +131,7 @@ def work(case):
         G = case["group"]
         pairs = list(zip(_lengths(case), _query_lens(case)))
         rows = sum(n for _, n in pairs) * H * G
-        return {"bytes": sum(L for L, n in pairs if n) * H * D * 4 + rows * (4 * D + 4),
+        return {"bytes": sum(L for L, n in pairs if n) * H * D * 4 + rows * (4 * D + 4 * case["lse"]),
                 "flops": 4 * D * H * G * sum(L * n for L, n in pairs)}
     arrays = 2 * case["layers"]
     page = P * H * D * 2
@@ -230,7 +230,7 @@ def prepare(case, seed):
             k_pool=_values(gen, _pool_shape(case, pages), channel),
             v_pool=_values(gen, _pool_shape(case, pages), 1.0),
             out=torch.empty(T, H * G, D, dtype=torch.bfloat16, device="cuda"),
-            lse=torch.empty(T, H * G, device="cuda"))
+            lse=torch.empty(T, H * G, device="cuda") if case["lse"] else None)
         # the query of each (source, index) pair, T where there is none
         i = torch.arange(max(n), device="cuda")
         first = torch.tensor(starts[:-1], device="cuda")[:, None]
@@ -340,7 +340,7 @@ def _plain_cross(st):
     out[st["row"]] = o.flatten(2, 3)
     logs = lse.new_empty(T + 1, H * G)
     logs[st["row"]] = lse.flatten(2)
-    return [out[:T].bfloat16(), logs[:T].contiguous()]
+    return [out[:T].bfloat16()] + ([logs[:T].contiguous()] if case["lse"] else [])
 
 
 def _pages_of(lens, P):
@@ -453,7 +453,7 @@ def _own_cross(st):
     kvc.kvc_cross(st["out"], st["q"], st["k_pool"], st["v_pool"], st["table"], st["q_indptr"],
                   st["ctx"], st["max_q"], st["max_src"], lse_out=st["lse"], workspace=st["work"],
                   layout=st["layout"])
-    return [st["out"], st["lse"]]
+    return [st["out"]] + ([st["lse"]] if st["case"]["lse"] else [])
 
 
 def _own_branch(st):
@@ -534,7 +534,7 @@ def _exact_cross(case, st):
                 lse[t:t + n, h] = torch.logsumexp(x, 1)
                 out[t:t + n, h] = torch.softmax(x, 1) @ v[:, h // G]
         t += n
-    return [out, lse]
+    return [out] + ([lse] if case["lse"] else [])
 
 
 def _exact_reserve(table, lens, grow, refs, pools, P):
