@@ -624,6 +624,127 @@ kvc_status kvc_evict(void *k_pool, void *v_pool, kvc_pool_desc pool, const int32
                      int32_t *new_lens, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Rotary positions with several axes (time, height and width of images and video; one axis for text).
+ * (No counterpart on the pages, whose keys come rotated: this is the step between a model's projections
+ * and kvc_store.)  Of each head the first rotary_dim dims turn, in rotary_dim / 2 pairs; pair f by
+ *   a = positions[axis[f]][t] * inv_freq[f]:   y0 = x0 cos a - x1 sin a,   y1 = x1 cos a + x0 sin a,
+ * in fp32, rounded once to bf16; the other dims go through unchanged.  Angles are taken modulo a turn in
+ * 64-bit fixed point, so they are as good at position 2^31 - 1 as at 1 (off by 2^-53 of position *
+ * inv_freq, and 2^-23 radians); positions may be negative.
+ *   inv_freq   host double [rotary_dim / 2], radians per unit of position, up to 1e6 (any scaling of long
+ *              contexts is the caller's, in these)
+ *   axis       host int32 [rotary_dim / 2], the row of positions of each pair; NULL: row 0
+ *   pairing    KVC_ROPE_HALVES: dims f and f + rotary_dim / 2; KVC_ROPE_ADJACENT: dims 2 f and 2 f + 1
+ * Both host arrays are read during the call only.
+ */
+typedef enum kvc_rope_pairing {
+    KVC_ROPE_HALVES = 0,
+    KVC_ROPE_ADJACENT = 1
+} kvc_rope_pairing;
+
+typedef struct kvc_rope_desc {
+    int32_t num_axes;         /* 1 .. 8                                                     */
+    int32_t rotary_dim;       /* a multiple of 16, at most head_dim                         */
+    int32_t pairing;          /* kvc_rope_pairing                                           */
+    const double *inv_freq;
+    const int32_t *axis;
+} kvc_rope_desc;
+
+/*
+ * kvc_rope -- rotated queries and keys as rows, for the calls that take new keys (kvc_store_int8,
+ * kvc_store_int4, kvc_append_store, kvc_decode_store, kvc_decode_int8_store).
+ *   q, k, q_out, k_out  bf16 rows of heads: head h of token t at t * stride + h * head_dim, strides in
+ *                       elements (a multiple of 8, at least heads * head_dim): parts of one projection's
+ *                       output need no copy.  An output may be its own input, with the same stride;
+ *                       otherwise the rows of outputs share no memory with other rows.
+ *   positions           int32 [num_axes][num_tokens], device
+ * q_heads or kv_heads may be 0 (q or k is then not read).  head_dim 64 or 128.
+ *
+ * kvc_rope_store -- rotated queries as rows [num_tokens][q_heads][head_dim], rotated keys and the values (raw
+ * 16-bit copies) at their slots: kvc_rope and kvc_store in one pass, the same bits.  Slots as in kvc_store: a
+ * token with slot_mapping[t] < 0 stores nothing (its query is rotated all the same), one past the pool
+ * neither, and is flagged (kvc_device_errors).
+ *   q, k_new, v_new     as above;  q_out may be q where q's rows are contiguous
+ */
+kvc_status kvc_rope(void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, const void *q,
+                    int64_t q_stride, const void *k, int64_t k_stride, int32_t q_heads,
+                    int32_t kv_heads, int32_t head_dim, kvc_rope_desc rope, const int32_t *positions,
+                    int32_t num_tokens, void *stream);
+kvc_status kvc_rope_store(void *q_out, void *k_pool, void *v_pool, kvc_pool_desc pool, const void *q,
+                          int64_t q_stride, const void *k_new, int64_t k_stride, const void *v_new,
+                          int64_t v_stride, int32_t q_heads, kvc_rope_desc rope,
+                          const int32_t *positions, const int32_t *slot_mapping, int32_t num_tokens,
+                          void *stream);
+
+/*
+ * Pages on the device.  A table (block_table [num_seqs][bt_stride], context_lens [num_seqs]: positions that
+ * each row holds) and page_refs, int32 [num_pages]: how many rows list each page, over all tables and
+ * whatever else holds pages; 0 is a free page.  The caller starts them with zeros and may hold pages of its
+ * own by raising their counts.  The four calls below are what the pages' host allocators do (TileInfer.jl
+ * "KV cache", "Growing, rolling back, releasing"; "KV Cache Management and PagedAttention", "Share common KV
+ * across responses", "Split shared blocks when a write is needed" and "Return blocks after a request
+ * ends"), without the host: nothing is read back, so a captured step can grow, branch and end sequences.
+ * Results are whole numbers with one right answer, whatever runs at the same time on the device; calls on
+ * one table or one page_refs are ordered by the caller (one stream).  All arrays are device memory.  A length
+ * past the row (bt_stride * page_size) is flagged (kvc_device_errors, 1 << 7) and taken as the row's; a page
+ * outside the pool is flagged (1 << 10) and left out; a page with fewer references than rows that list it is
+ * flagged (1 << 14), and what is said of its rows is undefined.  num_seqs 0 .. 65535, bt_stride * page_size
+ * at most 2^30; any page_size.
+ *
+ * arrays  host, num_arrays of them, read during the call only: every array whose pages travel with the
+ *         table's, page p being the page_bytes bytes from data + p * page_bytes (bf16 pools of all layers,
+ *         INT8 codes and scales, 4-bit codes and parameters: anything with the page as its first axis).
+ *         data 16-byte aligned, page_bytes a multiple of 16.  Raw copies.
+ *
+ * kvc_truncate -- rows give back the pages past new_lens[s] positions: context_lens[s] becomes min(itself,
+ * max(new_lens[s], 0)).  new_lens NULL: every row ends.  Also what follows kvc_evict, with its new_lens.
+ *
+ * kvc_fork -- new rows that begin with the pages of others: row s of block_table_out [num_out]
+ * [out_stride] lists the pages of row parents[s], and context_lens_out[s] is that row's length, or the smaller
+ * share_lens[s] (NULL: the whole row; a partly filled last page is shared too).  parents[s] < 0 gives an empty
+ * row; one past num_seqs too, flagged (1 << 15); a row longer than out_stride covers is cut, flagged (1 << 7).
+ * Table entries past a row's pages are left as they are.  The new arrays share no memory with the old ones.
+ *
+ * kvc_reserve -- pages for new_tokens[s] more positions of every row (NULL: one; negative: none), and
+ * context_lens[s] += new_tokens[s]: what the attention calls then take, the new tokens counted.  Rows go in
+ * order.  A row that grows into a partly filled last page with more than one reference left gets a copy of it
+ * (every array) and drops its reference; then pages for the further positions.  New pages are the lowest free
+ * ones in order, the copy's first.  A row without room for its new tokens (bt_stride * page_size) is flagged
+ * (1 << 7) and stays as it is.  missing, int32 [1] (out): 0, or how many pages too few are free; then nothing
+ * else is changed.
+ *
+ * kvc_compact -- moves pages so that the n pages in use are 0 .. n - 1: the used pages from n on, in order, go
+ * to the free ones below n, in order, with their references and their contents; the rows of the table follow.
+ * page_map int32 [num_pages] (out): where every page went (itself where it stayed, -1 for a free one), for
+ * tables that the call was not given; num_live int32 [1] (out): n.
+ *
+ *   workspace  kvc_reserve_plan's / kvc_compact_plan's bytes, 16-byte aligned, one call at a time
+ */
+typedef struct kvc_page_array {
+    void *data;
+    int64_t page_bytes;
+} kvc_page_array;
+
+kvc_status kvc_truncate(const int32_t *block_table, int32_t bt_stride, int32_t *context_lens,
+                        const int32_t *new_lens, int32_t num_seqs, int32_t *page_refs, int32_t num_pages,
+                        int32_t page_size, void *stream);
+kvc_status kvc_fork(int32_t *block_table_out, int32_t out_stride, int32_t *context_lens_out,
+                    const int32_t *parents, const int32_t *share_lens, int32_t num_out,
+                    const int32_t *block_table, int32_t bt_stride, const int32_t *context_lens,
+                    int32_t num_seqs, int32_t *page_refs, int32_t num_pages, int32_t page_size,
+                    void *stream);
+kvc_status kvc_reserve_plan(int32_t num_seqs, int32_t num_pages, size_t *workspace_bytes_out);
+kvc_status kvc_reserve(const kvc_page_array *arrays, int32_t num_arrays, int32_t *block_table,
+                       int32_t bt_stride, int32_t *context_lens, const int32_t *new_tokens,
+                       int32_t num_seqs, int32_t *page_refs, int32_t num_pages, int32_t page_size,
+                       int32_t *missing, void *workspace, size_t workspace_bytes, void *stream);
+kvc_status kvc_compact_plan(int32_t num_pages, size_t *workspace_bytes_out);
+kvc_status kvc_compact(const kvc_page_array *arrays, int32_t num_arrays, int32_t *block_table,
+                       int32_t bt_stride, const int32_t *context_lens, int32_t num_seqs,
+                       int32_t *page_refs, int32_t num_pages, int32_t page_size, int32_t *page_map,
+                       int32_t *num_live, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * kvc_copy_pages -- copy-on-write page copy ("KV Cache Management and PagedAttention", "Split
  * shared blocks when a write is needed": before a sequence writes into a page that other
  * sequences still reference, the page is copied to a new one and the writer's block-table

@@ -1057,6 +1057,382 @@ kvc_status kvc_decode_int4(void *out, int32_t out_dtype, const void *q, const vo
     return err == cudaSuccess ? ok() : cuda_fail(err, "decode_int4 launch");
 }
 
+}  // extern "C"
+
+namespace {
+
+// Whether two pieces of memory share a byte.
+bool overlap(const void *a, uint64_t a_bytes, const void *b, uint64_t b_bytes)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a_bytes > 0 && b_bytes > 0 && (x < y ? y - x < a_bytes : x - y < b_bytes);
+}
+
+// Rows of heads: `bytes` of each of n rows, `stride` bytes apart.
+struct HeadRows {
+    const void *base;
+    uint64_t stride, bytes;
+};
+
+// Whether rows of two sets share a byte.  Sets of the same stride may lie between each other.
+bool rows_overlap(const HeadRows &a, const HeadRows &b, uint64_t n)
+{
+    if (n == 0 || a.bytes == 0 || b.bytes == 0 ||
+        !overlap(a.base, (n - 1) * a.stride + a.bytes, b.base, (n - 1) * b.stride + b.bytes))
+        return false;
+    if (n == 1 || a.stride != b.stride)
+        return true;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.base), y = reinterpret_cast<uintptr_t>(b.base);
+    const uint64_t behind = x <= y ? (y - x) % a.stride : (a.stride - (x - y) % a.stride) % a.stride;
+    return behind < a.bytes || a.stride - behind < b.bytes;   // where b's rows begin behind a's
+}
+
+kvc_status check_rows(const char *name, const HeadRows &r, int32_t heads, int32_t num_tokens)
+{
+    if (heads == 0)
+        return KVC_OK;
+    if (r.base == nullptr)
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument (%s)", name);
+    if (!aligned16(r.base) || r.stride % 16 != 0)
+        return fail(KVC_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", name);
+    if (num_tokens > 1 && r.stride < r.bytes)
+        return fail(KVC_ERR_INVALID_ARG, "%s: a stride smaller than its rows", name);
+    return KVC_OK;
+}
+
+// The checks of a rotary description, and its angles as fractions of a turn.
+kvc_status rope_angles(const kvc_rope_desc &rope, int32_t head_dim, kvc::RopeAngles *out)
+{
+    if (rope.num_axes < 1 || rope.num_axes > kvc::kRopeAxes)
+        return fail(KVC_ERR_INVALID_ARG, "num_axes %d (1 .. %d)", rope.num_axes, kvc::kRopeAxes);
+    if (rope.rotary_dim <= 0 || rope.rotary_dim > head_dim)
+        return fail(KVC_ERR_INVALID_ARG, "rotary_dim %d (at most head_dim %d)", rope.rotary_dim, head_dim);
+    if (rope.rotary_dim % 16 != 0)
+        return fail(KVC_ERR_UNSUPPORTED, "rotary_dim %d (a multiple of 16)", rope.rotary_dim);
+    if (rope.pairing != KVC_ROPE_HALVES && rope.pairing != KVC_ROPE_ADJACENT)
+        return fail(KVC_ERR_INVALID_ARG, "pairing %d", rope.pairing);
+    if (rope.inv_freq == nullptr)
+        return fail(KVC_ERR_INVALID_ARG, "inv_freq is null");
+    for (int f = 0; f < rope.rotary_dim / 2; ++f) {
+        const double x = rope.inv_freq[f];
+        if (!(fabs(x) <= 1e6))
+            return fail(KVC_ERR_INVALID_ARG, "inv_freq[%d] is not a number of up to 1e6 radians", f);
+        const int axis = rope.axis ? rope.axis[f] : 0;
+        if (axis < 0 || axis >= rope.num_axes)
+            return fail(KVC_ERR_INVALID_ARG, "axis[%d] is %d (0 .. %d)", f, axis, rope.num_axes - 1);
+        const double turns = fabs(x) / 6.283185307179586476925286766559;
+        const double part = (turns - floor(turns)) * 18446744073709551616.0;   // * 2^64, exact
+        const uint64_t whole = part < 18446744073709551616.0 ? static_cast<uint64_t>(part) : 0;
+        out->turns[f] = x < 0 ? 0 - whole : whole;
+        out->axis[f] = static_cast<uint8_t>(axis);
+    }
+    return KVC_OK;
+}
+
+kvc_status check_rope_sizes(int32_t q_heads, int32_t kv_heads, int32_t num_tokens)
+{
+    if (q_heads < 0 || kv_heads < 0 || num_tokens < 0)
+        return fail(KVC_ERR_INVALID_ARG, "negative size: q_heads %d, kv_heads %d, num_tokens %d", q_heads,
+                    kv_heads, num_tokens);
+    if (q_heads > 65536 || kv_heads > 65536)
+        return fail(KVC_ERR_UNSUPPORTED, "more than 65536 heads");
+    return KVC_OK;
+}
+
+// The arguments that all page calls share.
+kvc_status check_pages(const void *block_table, int32_t bt_stride, const void *context_lens,
+                       int32_t num_seqs, const void *page_refs, int32_t num_pages, int32_t page_size)
+{
+    if (num_pages <= 0 || page_size <= 0 || bt_stride <= 0)
+        return fail(KVC_ERR_INVALID_ARG, "num_pages %d, page_size %d, bt_stride %d", num_pages, page_size,
+                    bt_stride);
+    if (num_seqs < 0 || num_seqs > 65535)
+        return fail(KVC_ERR_INVALID_ARG, "num_seqs %d (0 .. 65535)", num_seqs);
+    if (static_cast<int64_t>(num_pages) * page_size >= (int64_t(1) << 31))
+        return fail(KVC_ERR_UNSUPPORTED, "num_pages * page_size must be below 2^31");
+    if (static_cast<int64_t>(bt_stride) * page_size > (int64_t(1) << 30))
+        return fail(KVC_ERR_UNSUPPORTED, "bt_stride * page_size must be at most 2^30");
+    if (page_refs == nullptr || (num_seqs > 0 && (block_table == nullptr || context_lens == nullptr)))
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument");
+    return KVC_OK;
+}
+
+static_assert(sizeof(kvc_page_array) == sizeof(kvc::PageArray), "the same fields");
+
+kvc_status check_arrays(const kvc_page_array *arrays, int32_t num_arrays)
+{
+    if (num_arrays < 0 || (num_arrays > 0 && arrays == nullptr))
+        return fail(KVC_ERR_INVALID_ARG, "arrays missing or num_arrays %d", num_arrays);
+    for (int i = 0; i < num_arrays; ++i) {
+        if (arrays[i].data == nullptr || !aligned16(arrays[i].data))
+            return fail(KVC_ERR_INVALID_ARG, "arrays[%d]: null or not 16-byte aligned", i);
+        if (arrays[i].page_bytes <= 0 || arrays[i].page_bytes % 16 != 0 ||
+            arrays[i].page_bytes > (int64_t(1) << 30))
+            return fail(KVC_ERR_UNSUPPORTED, "arrays[%d]: pages of %lld bytes (a multiple of 16, at most "
+                        "2^30)", i, static_cast<long long>(arrays[i].page_bytes));
+    }
+    return KVC_OK;
+}
+
+kvc_status check_workspace(const void *workspace, size_t given, size_t need)
+{
+    if (workspace == nullptr || given < need)
+        return fail(KVC_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                    workspace == nullptr ? size_t(0) : given);
+    if (!aligned16(workspace))
+        return fail(KVC_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    return KVC_OK;
+}
+
+kvc::PagesLaunch pages_launch(const int32_t *block_table, int32_t bt_stride, const int32_t *context_lens,
+                              int32_t num_seqs, int32_t *page_refs, int32_t num_pages, int32_t page_size)
+{
+    kvc::PagesLaunch l;
+    l.block_table = const_cast<int32_t *>(block_table);   // written by the calls that say so
+    l.bt_stride = bt_stride;
+    l.context_lens = const_cast<int32_t *>(context_lens);
+    l.num_seqs = num_seqs;
+    l.page_refs = page_refs;
+    l.num_pages = num_pages;
+    l.page_size = page_size;
+    return l;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvc_status kvc_rope(void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, const void *q,
+                    int64_t q_stride, const void *k, int64_t k_stride, int32_t q_heads,
+                    int32_t kv_heads, int32_t head_dim, kvc_rope_desc rope, const int32_t *positions,
+                    int32_t num_tokens, void *stream)
+{
+    if (head_dim != 64 && head_dim != 128)
+        return fail(KVC_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", head_dim);
+    kvc_status st = check_rope_sizes(q_heads, kv_heads, num_tokens);
+    if (st != KVC_OK)
+        return st;
+    kvc::RopeLaunch l;
+    if ((st = rope_angles(rope, head_dim, &l.angles)) != KVC_OK)
+        return st;
+    if (q_stride < 0 || k_stride < 0 || q_out_stride < 0 || k_out_stride < 0)
+        return fail(KVC_ERR_INVALID_ARG, "negative stride");
+    if (num_tokens == 0 || q_heads + kv_heads == 0)
+        return ok();
+    const uint64_t q_bytes = uint64_t(q_heads) * head_dim * 2, k_bytes = uint64_t(kv_heads) * head_dim * 2;
+    const HeadRows qi{q, uint64_t(q_stride) * 2, q_bytes}, ki{k, uint64_t(k_stride) * 2, k_bytes};
+    const HeadRows qo{q_out, uint64_t(q_out_stride) * 2, q_bytes},
+        ko{k_out, uint64_t(k_out_stride) * 2, k_bytes};
+    if ((st = check_rows("q", qi, q_heads, num_tokens)) != KVC_OK ||
+        (st = check_rows("k", ki, kv_heads, num_tokens)) != KVC_OK ||
+        (st = check_rows("q_out", qo, q_heads, num_tokens)) != KVC_OK ||
+        (st = check_rows("k_out", ko, kv_heads, num_tokens)) != KVC_OK)
+        return st;
+    const bool q_same = q_out == q && (q_out_stride == q_stride || num_tokens == 1);
+    const bool k_same = k_out == k && (k_out_stride == k_stride || num_tokens == 1);
+    const uint64_t n = static_cast<uint64_t>(num_tokens);
+    if ((!q_same && rows_overlap(qo, qi, n)) || (!k_same && rows_overlap(ko, ki, n)) ||
+        rows_overlap(qo, ki, n) || rows_overlap(ko, qi, n) || rows_overlap(qo, ko, n))
+        return fail(KVC_ERR_INVALID_ARG, "outputs: their own inputs with the same stride, or apart from all "
+                    "other rows");
+    if (positions == nullptr)
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument (positions)");
+    l.q = q;
+    l.k = k;
+    l.v = nullptr;
+    l.q_stride = q_stride;
+    l.k_stride = k_stride;
+    l.v_stride = 0;
+    l.q_out = q_out;
+    l.k_out = k_out;
+    l.v_out = nullptr;
+    l.q_out_stride = q_out_stride;
+    l.k_out_stride = k_out_stride;
+    l.positions = positions;
+    l.num_tokens = num_tokens;
+    l.q_heads = q_heads;
+    l.kv_heads = kv_heads;
+    l.head_dim = head_dim;
+    l.rotary_dim = rope.rotary_dim;
+    l.adjacent = rope.pairing == KVC_ROPE_ADJACENT;
+    const cudaError_t err = kvc::launch_rope(l, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "rope launch");
+}
+
+kvc_status kvc_rope_store(void *q_out, void *k_pool, void *v_pool, kvc_pool_desc pool, const void *q,
+                          int64_t q_stride, const void *k_new, int64_t k_stride, const void *v_new,
+                          int64_t v_stride, int32_t q_heads, kvc_rope_desc rope,
+                          const int32_t *positions, const int32_t *slot_mapping, int32_t num_tokens,
+                          void *stream)
+{
+    kvc_status st = check_pool(pool);
+    if (st != KVC_OK || (st = check_rope_sizes(q_heads, pool.kv_heads, num_tokens)) != KVC_OK)
+        return st;
+    kvc::RopeLaunch l;
+    if ((st = rope_angles(rope, pool.head_dim, &l.angles)) != KVC_OK)
+        return st;
+    if (q_stride < 0 || k_stride < 0 || v_stride < 0)
+        return fail(KVC_ERR_INVALID_ARG, "negative stride");
+    if (num_tokens == 0)
+        return ok();
+    const uint64_t q_bytes = uint64_t(q_heads) * pool.head_dim * 2;
+    const uint64_t k_bytes = uint64_t(pool.kv_heads) * pool.head_dim * 2;
+    const HeadRows qi{q, uint64_t(q_stride) * 2, q_bytes}, qo{q_out, q_bytes, q_bytes};
+    const HeadRows ki{k_new, uint64_t(k_stride) * 2, k_bytes}, vi{v_new, uint64_t(v_stride) * 2, k_bytes};
+    if ((st = check_rows("q", qi, q_heads, num_tokens)) != KVC_OK ||
+        (st = check_rows("q_out", qo, q_heads, num_tokens)) != KVC_OK ||
+        (st = check_rows("k_new", ki, pool.kv_heads, num_tokens)) != KVC_OK ||
+        (st = check_rows("v_new", vi, pool.kv_heads, num_tokens)) != KVC_OK)
+        return st;
+    const uint64_t n = static_cast<uint64_t>(num_tokens);
+    const bool q_same = q_out == q && (qi.stride == qo.stride || num_tokens == 1);
+    if ((!q_same && rows_overlap(qo, qi, n)) || rows_overlap(qo, ki, n) || rows_overlap(qo, vi, n))
+        return fail(KVC_ERR_INVALID_ARG, "q_out: q itself where its rows are contiguous, or apart from all "
+                    "other rows");
+    if (!k_pool || !v_pool || !positions || !slot_mapping)
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(k_pool) || !aligned16(v_pool))
+        return fail(KVC_ERR_INVALID_ARG, "pools must be 16-byte aligned");
+    l.q = q;
+    l.k = k_new;
+    l.v = v_new;
+    l.q_stride = q_stride;
+    l.k_stride = k_stride;
+    l.v_stride = v_stride;
+    l.q_out = q_out;
+    l.k_out = k_pool;
+    l.v_out = v_pool;
+    l.q_out_stride = static_cast<long long>(q_heads) * pool.head_dim;
+    l.positions = positions;
+    l.slots = slot_mapping;
+    l.num_tokens = num_tokens;
+    l.q_heads = q_heads;
+    l.kv_heads = pool.kv_heads;
+    l.head_dim = pool.head_dim;
+    l.rotary_dim = rope.rotary_dim;
+    l.page_size = pool.page_size;
+    l.num_slots = pool.num_pages * pool.page_size;
+    l.hnd = pool.layout == KVC_HND;
+    l.adjacent = rope.pairing == KVC_ROPE_ADJACENT;
+    const cudaError_t err = kvc::launch_rope(l, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "rope_store launch");
+}
+
+kvc_status kvc_truncate(const int32_t *block_table, int32_t bt_stride, int32_t *context_lens,
+                        const int32_t *new_lens, int32_t num_seqs, int32_t *page_refs, int32_t num_pages,
+                        int32_t page_size, void *stream)
+{
+    kvc_status st = check_pages(block_table, bt_stride, context_lens, num_seqs, page_refs, num_pages,
+                                page_size);
+    if (st != KVC_OK)
+        return st;
+    if (new_lens != context_lens && partly_overlap(new_lens, context_lens, uint64_t(num_seqs) * 4))
+        return fail(KVC_ERR_INVALID_ARG, "new_lens and context_lens overlap");
+    const kvc::PagesLaunch l = pages_launch(block_table, bt_stride, context_lens, num_seqs, page_refs,
+                                            num_pages, page_size);
+    const cudaError_t err = kvc::launch_truncate(l, new_lens, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "truncate launch");
+}
+
+kvc_status kvc_fork(int32_t *block_table_out, int32_t out_stride, int32_t *context_lens_out,
+                    const int32_t *parents, const int32_t *share_lens, int32_t num_out,
+                    const int32_t *block_table, int32_t bt_stride, const int32_t *context_lens,
+                    int32_t num_seqs, int32_t *page_refs, int32_t num_pages, int32_t page_size,
+                    void *stream)
+{
+    kvc_status st = check_pages(block_table, bt_stride, context_lens, num_seqs, page_refs, num_pages,
+                                page_size);
+    if (st != KVC_OK || (st = check_pages(block_table_out, out_stride, context_lens_out, num_out, page_refs,
+                                          num_pages, page_size)) != KVC_OK)
+        return st;
+    if (num_out == 0)
+        return ok();
+    if (parents == nullptr)
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument (parents)");
+    const uint64_t in_rows = uint64_t(num_seqs) * bt_stride * 4, in_lens = uint64_t(num_seqs) * 4;
+    const uint64_t out_rows = uint64_t(num_out) * out_stride * 4, out_lens = uint64_t(num_out) * 4;
+    if (overlap(block_table_out, out_rows, block_table, in_rows) ||
+        overlap(block_table_out, out_rows, context_lens, in_lens) ||
+        overlap(context_lens_out, out_lens, context_lens, in_lens) ||
+        overlap(context_lens_out, out_lens, block_table, in_rows) ||
+        overlap(context_lens_out, out_lens, parents, out_lens) ||
+        overlap(context_lens_out, out_lens, share_lens, share_lens ? out_lens : 0))
+        return fail(KVC_ERR_INVALID_ARG, "the new rows and lengths must be apart from what is read");
+    const kvc::PagesLaunch l = pages_launch(block_table, bt_stride, context_lens, num_seqs, page_refs,
+                                            num_pages, page_size);
+    const cudaError_t err = kvc::launch_fork(l, block_table_out, out_stride, context_lens_out, parents,
+                                             share_lens, num_out, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "fork launch");
+}
+
+kvc_status kvc_reserve_plan(int32_t num_seqs, int32_t num_pages, size_t *workspace_bytes_out)
+{
+    if (num_seqs < 0 || num_seqs > 65535 || num_pages <= 0)
+        return fail(KVC_ERR_INVALID_ARG, "num_seqs %d (0 .. 65535), num_pages %d", num_seqs, num_pages);
+    if (workspace_bytes_out)
+        *workspace_bytes_out = kvc::reserve_workspace_bytes(num_seqs, num_pages);
+    return ok();
+}
+
+kvc_status kvc_reserve(const kvc_page_array *arrays, int32_t num_arrays, int32_t *block_table,
+                       int32_t bt_stride, int32_t *context_lens, const int32_t *new_tokens,
+                       int32_t num_seqs, int32_t *page_refs, int32_t num_pages, int32_t page_size,
+                       int32_t *missing, void *workspace, size_t workspace_bytes, void *stream)
+{
+    kvc_status st = check_pages(block_table, bt_stride, context_lens, num_seqs, page_refs, num_pages,
+                                page_size);
+    if (st != KVC_OK || (st = check_arrays(arrays, num_arrays)) != KVC_OK)
+        return st;
+    if (missing == nullptr)
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument (missing)");
+    if (overlap(new_tokens, new_tokens ? uint64_t(num_seqs) * 4 : 0, context_lens, uint64_t(num_seqs) * 4))
+        return fail(KVC_ERR_INVALID_ARG, "new_tokens and context_lens overlap");
+    if ((st = check_workspace(workspace, workspace_bytes,
+                              kvc::reserve_workspace_bytes(num_seqs, num_pages))) != KVC_OK)
+        return st;
+    kvc::PagesLaunch l = pages_launch(block_table, bt_stride, context_lens, num_seqs, page_refs, num_pages,
+                                      page_size);
+    l.arrays = reinterpret_cast<const kvc::PageArray *>(arrays);
+    l.num_arrays = num_arrays;
+    const cudaError_t err =
+        kvc::launch_reserve(l, new_tokens, missing, workspace, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "reserve launch");
+}
+
+kvc_status kvc_compact_plan(int32_t num_pages, size_t *workspace_bytes_out)
+{
+    if (num_pages <= 0)
+        return fail(KVC_ERR_INVALID_ARG, "num_pages %d", num_pages);
+    if (workspace_bytes_out)
+        *workspace_bytes_out = kvc::compact_workspace_bytes(num_pages);
+    return ok();
+}
+
+kvc_status kvc_compact(const kvc_page_array *arrays, int32_t num_arrays, int32_t *block_table,
+                       int32_t bt_stride, const int32_t *context_lens, int32_t num_seqs,
+                       int32_t *page_refs, int32_t num_pages, int32_t page_size, int32_t *page_map,
+                       int32_t *num_live, void *workspace, size_t workspace_bytes, void *stream)
+{
+    kvc_status st = check_pages(block_table, bt_stride, context_lens, num_seqs, page_refs, num_pages,
+                                page_size);
+    if (st != KVC_OK || (st = check_arrays(arrays, num_arrays)) != KVC_OK)
+        return st;
+    if (page_map == nullptr || num_live == nullptr)
+        return fail(KVC_ERR_INVALID_ARG, "null pointer argument");
+    if (overlap(page_map, uint64_t(num_pages) * 4, page_refs, uint64_t(num_pages) * 4))
+        return fail(KVC_ERR_INVALID_ARG, "page_map and page_refs overlap");
+    if ((st = check_workspace(workspace, workspace_bytes, kvc::compact_workspace_bytes(num_pages))) !=
+        KVC_OK)
+        return st;
+    kvc::PagesLaunch l = pages_launch(block_table, bt_stride, context_lens, num_seqs, page_refs, num_pages,
+                                      page_size);
+    l.arrays = reinterpret_cast<const kvc::PageArray *>(arrays);
+    l.num_arrays = num_arrays;
+    const cudaError_t err =
+        kvc::launch_compact(l, page_map, num_live, workspace, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "compact launch");
+}
+
 kvc_status kvc_copy_pages(void *k_pool, void *v_pool, kvc_pool_desc pool,
                           const int32_t *src_pages, const int32_t *dst_pages,
                           int32_t num_copies, void *stream)
@@ -1855,6 +2231,12 @@ kvc_status kvc_device_errors(uint32_t *flags_out)
     e |= f;
     if (err == cudaSuccess)
         err = kvc::read_and_clear_evict_errors(&f);
+    e |= f;
+    if (err == cudaSuccess)
+        err = kvc::read_and_clear_rope_errors(&f);
+    e |= f;
+    if (err == cudaSuccess)
+        err = kvc::read_and_clear_pages_errors(&f);
     e |= f;
     if (err != cudaSuccess)
         return cuda_fail(err, "reading the device error word");

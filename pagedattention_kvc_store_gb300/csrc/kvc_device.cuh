@@ -32,6 +32,9 @@ enum DeviceErrorBits : uint32_t {
     kErrSelftestWait = 1u << 12,   // kvc_selftest_wait: its wait ran out, as it must
     kErrPositionOrder = 1u << 13,  // eviction: a row cut twice with no token in between (its result
                                    // is right), or positions that do not go on behind its last slot
+    kErrPageRefs = 1u << 14,       // a page with fewer references than rows that list it
+    kErrRowRange = 1u << 15,       // a fork named a row past the table: an empty one
+    kErrCrossWait = 1u << 16,      // the cross attention gave up a wait
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p)

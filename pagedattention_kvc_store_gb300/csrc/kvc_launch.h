@@ -174,6 +174,56 @@ struct EvictLaunch {
 cudaError_t launch_evict(const EvictLaunch &l, cudaStream_t stream);
 cudaError_t read_and_clear_evict_errors(uint32_t *flags);
 
+// Rotary positions: of each pair its angle per unit of position, as a 64-bit fraction of a turn, and the
+// axis (row of positions) that it goes by.
+constexpr int kRopePairs = 64;
+constexpr int kRopeAxes = 8;
+struct RopeAngles {
+    uint64_t turns[kRopePairs];
+    uint8_t axis[kRopePairs];
+};
+struct RopeLaunch {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;         // elements between tokens
+    void *q_out, *k_out, *v_out;                    // with slots: k_out and v_out are the pools
+    long long q_out_stride, k_out_stride = 0;
+    const int32_t *positions;                       // [axes][num_tokens]
+    const int32_t *slots = nullptr;                 // null: k_out takes the rows, no values
+    int num_tokens, q_heads, kv_heads, head_dim, rotary_dim;
+    int page_size = 1, num_slots = 0;
+    bool hnd = false, adjacent = false;
+    RopeAngles angles;
+};
+cudaError_t launch_rope(const RopeLaunch &l, cudaStream_t stream);
+cudaError_t read_and_clear_rope_errors(uint32_t *flags);
+
+// Pages handed out, shared, given back and closed up: a table of rows, the references of every page, and the
+// arrays whose pages are copied along.
+struct PageArray {
+    void *data;
+    long long page_bytes;
+};
+struct PagesLaunch {
+    int32_t *block_table;
+    int bt_stride;
+    int32_t *context_lens;
+    int num_seqs;
+    int32_t *page_refs;
+    int num_pages, page_size;
+    const PageArray *arrays = nullptr;   // host
+    int num_arrays = 0;
+};
+size_t reserve_workspace_bytes(int num_seqs, int num_pages);
+size_t compact_workspace_bytes(int num_pages);
+cudaError_t launch_truncate(const PagesLaunch &l, const int32_t *new_lens, cudaStream_t stream);
+cudaError_t launch_fork(const PagesLaunch &l, int32_t *out_rows, int out_stride, int32_t *out_lens,
+                        const int32_t *parents, const int32_t *share_lens, int num_out, cudaStream_t stream);
+cudaError_t launch_reserve(const PagesLaunch &l, const int32_t *new_tokens, int32_t *missing,
+                           void *workspace, cudaStream_t stream);
+cudaError_t launch_compact(const PagesLaunch &l, int32_t *page_map, int32_t *num_live, void *workspace,
+                           cudaStream_t stream);
+cudaError_t read_and_clear_pages_errors(uint32_t *flags);
+
 // Grouped decode over a shared prefix: for each group, the first prefix_len[g] positions are
 // the same pages for every member (the leader's block-table row lists them).
 struct GroupedPrefixLaunch {

@@ -34,7 +34,9 @@ EXPORTS = ("kvc_status_string", "kvc_last_error", "kvc_slot_mapping", "kvc_store
            "kvc_append_store", "kvc_shared_prefix_groups", "kvc_decode_store",
            "kvc_selftest_wait", "kvc_decode_int8_store", "kvc_set_error_word",
            "kvc_store_int4", "kvc_load_int4", "kvc_decode_int4", "kvc_decode_int4_plan",
-           "kvc_decode_weights", "kvc_decode_weights_plan", "kvc_evict", "kvc_evict_plan")
+           "kvc_decode_weights", "kvc_decode_weights_plan", "kvc_evict", "kvc_evict_plan",
+           "kvc_rope", "kvc_rope_store", "kvc_truncate", "kvc_fork", "kvc_reserve",
+           "kvc_reserve_plan", "kvc_compact", "kvc_compact_plan")
 
 # Size of the library's own split-partials scratch used by kvc_decode_noalloc (bytes).
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -56,6 +58,20 @@ class PoolDesc(ctypes.Structure):
     _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("layout", ctypes.c_int32)]
+
+
+ROPE_PAIRINGS = {"halves": 0, "adjacent": 1}
+
+
+class RopeDesc(ctypes.Structure):
+    """Angles of rotary positions (rope_desc); holds the arrays that it points at."""
+    _fields_ = [("num_axes", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+                ("axis", ctypes.POINTER(ctypes.c_int32))]
+
+
+class PageArray(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -152,6 +168,24 @@ def lib() -> ctypes.CDLL:
             L.kvc_evict.restype = ctypes.c_int
             L.kvc_evict.argtypes = [p, p, PoolDesc, p, i32, p, i32, i32, p, p, p, p, p, i32, i32,
                                     i32, i32, p, p, sz, p]
+            i64, szp, arrays = ctypes.c_int64, ctypes.POINTER(sz), ctypes.POINTER(PageArray)
+            L.kvc_rope.restype = ctypes.c_int
+            L.kvc_rope.argtypes = [p, i64, p, i64, p, i64, p, i64, i32, i32, i32, RopeDesc, p, i32, p]
+            L.kvc_rope_store.restype = ctypes.c_int
+            L.kvc_rope_store.argtypes = [p, p, p, PoolDesc, p, i64, p, i64, p, i64, i32, RopeDesc, p,
+                                         p, i32, p]
+            L.kvc_truncate.restype = ctypes.c_int
+            L.kvc_truncate.argtypes = [p, i32, p, p, i32, p, i32, i32, p]
+            L.kvc_fork.restype = ctypes.c_int
+            L.kvc_fork.argtypes = [p, i32, p, p, p, i32, p, i32, p, i32, p, i32, i32, p]
+            L.kvc_reserve_plan.restype = ctypes.c_int
+            L.kvc_reserve_plan.argtypes = [i32, i32, szp]
+            L.kvc_reserve.restype = ctypes.c_int
+            L.kvc_reserve.argtypes = [arrays, i32, p, i32, p, p, i32, p, i32, i32, p, p, sz, p]
+            L.kvc_compact_plan.restype = ctypes.c_int
+            L.kvc_compact_plan.argtypes = [i32, szp]
+            L.kvc_compact.restype = ctypes.c_int
+            L.kvc_compact.argtypes = [arrays, i32, p, i32, p, i32, p, i32, i32, p, p, p, sz, p]
             L.kvc_append_int8.restype = ctypes.c_int
             L.kvc_append_int8.argtypes = [p, i32, p, p, p, p, p, PoolDesc, p, i32, p, p, i32,
                                           i32, i32, i32, i32, f, p]
@@ -518,6 +552,227 @@ def kvc_decode_int4(out: torch.Tensor, q: torch.Tensor, k_codes: torch.Tensor,
         _ptr(v_params), pool, _ptr(block_table), block_table.shape[1], _ptr(context_lens), S,
         int(max_ctx), q.shape[1], float(scale), int(num_splits), _ptr(workspace), ws,
         _stream(stream)))
+
+
+def rope_desc(inv_freq, axis=None, pairing: str = "halves",
+              num_axes: Optional[int] = None) -> RopeDesc:
+    """Rotary positions for kvc_rope and kvc_rope_store: inv_freq, radians per unit of position of each
+    of the rotary_dim / 2 pairs (fp64); axis, the row of positions that each goes by (None: row 0);
+    pairing "halves" (dims f and f + rotary_dim / 2) or "adjacent" (2 f and 2 f + 1).  num_axes: rows
+    of positions (None: as many as axis names)."""
+    if pairing not in ROPE_PAIRINGS:
+        raise ValueError(f"pairing {pairing!r}: 'halves' or 'adjacent'")
+    freqs = [float(x) for x in inv_freq]
+    axes = [0] * len(freqs) if axis is None else [int(x) for x in axis]
+    if len(axes) != len(freqs):
+        raise ValueError(f"axis has an entry for each of the {len(freqs)} frequencies")
+    n = max(axes, default=0) + 1 if num_axes is None else int(num_axes)
+    return RopeDesc(n, 2 * len(freqs), ROPE_PAIRINGS[pairing], (ctypes.c_double * len(freqs))(*freqs),
+                    (ctypes.c_int32 * len(axes))(*axes))
+
+
+def _head_rows(name, t):
+    """Checks of rows of heads [T, H, D] whose heads are contiguous; the stride between tokens."""
+    _cuda(name, t, torch.bfloat16, contiguous=False)
+    if t.dim() != 3:
+        raise ValueError(f"{name} is [num_tokens, heads, head_dim]")
+    (T, H, D), (st, sh, sd) = t.shape, t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st if T > 1 else H * D
+
+
+def _positions(positions, rope, T):
+    if not isinstance(rope, RopeDesc):
+        raise TypeError("rope is a rope_desc(...)")
+    _cuda("positions", positions, torch.int32)
+    want = (rope.num_axes, T)
+    if tuple(positions.shape) != want and not (rope.num_axes == 1 and tuple(positions.shape) == (T,)):
+        raise ValueError(f"positions are [num_axes, num_tokens] = {want}, got {tuple(positions.shape)}")
+    return _ptr(positions)
+
+
+def kvc_rope(q_out: Optional[torch.Tensor], k_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
+             k: Optional[torch.Tensor], positions: torch.Tensor, rope: RopeDesc, stream=None) -> None:
+    """Rotate queries [T, Hq, D] and keys [T, Hkv, D] (either may be None) by positions int32
+    [num_axes, T] ([T] for one axis).  The heads of a token are contiguous; tokens may be apart, as in
+    parts of one projection's output.  Outputs may be their inputs."""
+    sizes, rows = [], []
+    for name, t, out in (("q", q, q_out), ("k", k, k_out)):
+        if t is None:
+            sizes.append((None, 0))
+            rows += [None, 0, None, 0]
+            continue
+        stride = _head_rows(name, t)
+        if out is None or out.shape != t.shape:
+            raise ValueError(f"{name}_out has the shape of {name}")
+        rows += [_ptr(out), _head_rows(name + "_out", out), _ptr(t), stride]
+        sizes.append((t.shape[0], t.shape[1], t.shape[2]))
+    known = [s for s in sizes if s[0] is not None]
+    if not known or any(s[0] != known[0][0] or s[2] != known[0][2] for s in known):
+        raise ValueError("q and k: one of them at least, with the same tokens and head_dim")
+    T, D = known[0][0], known[0][2]
+    where = _positions(positions, rope, T)
+    _check("kvc_rope", lib().kvc_rope(
+        rows[0], rows[1], rows[4], rows[5], rows[2], rows[3], rows[6], rows[7], sizes[0][1],
+        sizes[1][1], D, rope, where, T, _stream(stream)))
+
+
+def kvc_rope_store(q_out: Optional[torch.Tensor], k_pool: torch.Tensor, v_pool: torch.Tensor,
+                   q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor,
+                   positions: torch.Tensor, slot_mapping: torch.Tensor, rope: RopeDesc, stream=None,
+                   layout: str = "nhd") -> None:
+    """kvc_rope into q_out [T, Hq, D] and the pages, and the values too: rotated keys and values at
+    slot_mapping's slots.  q, k_new and v_new as in kvc_rope; q None: no queries."""
+    _cuda("k_pool", k_pool, torch.bfloat16)
+    _cuda("v_pool", v_pool, torch.bfloat16)
+    pool = _pool_shapes(k_pool.shape, v_pool.shape, layout)
+    _cuda("slot_mapping", slot_mapping, torch.int32)
+    T = slot_mapping.numel()
+    k_stride, v_stride = _head_rows("k_new", k_new), _head_rows("v_new", v_new)
+    _vector_shapes(k_new.shape, v_new.shape, pool.kv_heads, pool.head_dim, T)
+    q_heads, q_stride = 0, 0
+    if q is not None:
+        q_stride, q_heads = _head_rows("q", q), q.shape[1]
+        _cuda("q_out", q_out, torch.bfloat16)
+        if q.shape[0] != T or q.shape[2] != pool.head_dim or q_out.shape != q.shape:
+            raise ValueError(f"q and q_out are [num_tokens, q_heads, head_dim] with {T} tokens and "
+                             f"head_dim {pool.head_dim}")
+    where = _positions(positions, rope, T)
+    _check("kvc_rope_store", lib().kvc_rope_store(
+        _ptr(q_out) if q is not None else None, _ptr(k_pool), _ptr(v_pool), pool, _ptr(q), q_stride,
+        _ptr(k_new), k_stride, _ptr(v_new), v_stride, q_heads, rope, where, _ptr(slot_mapping), T,
+        _stream(stream)))
+
+
+class PageArrays:
+    """Arrays whose first axis is the page, as kvc_reserve and kvc_compact move them (page_arrays)."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        for i, t in enumerate(self.tensors):
+            _cuda(f"arrays[{i}]", t)
+            if t.dim() == 0 or t.shape[0] != self.tensors[0].shape[0] or t.shape[0] == 0:
+                raise ValueError("arrays: the first axis of each is the page, as many in all of them")
+        self.num_pages = self.tensors[0].shape[0] if self.tensors else None
+        self.table = (PageArray * len(self.tensors))(
+            *((t.data_ptr(), t.numel() // t.shape[0] * t.element_size()) for t in self.tensors))
+
+
+def page_arrays(tensors) -> PageArrays:
+    """The pools of all layers (K, V, codes, scales, parameters: anything with the page as its first
+    axis), laid out once for kvc_reserve and kvc_compact."""
+    return PageArrays(tensors)
+
+
+def _table(block_table, context_lens, page_refs, arrays=None):
+    """Checks of a table, its lengths and the references; the number of sequences."""
+    _cuda("block_table", block_table, torch.int32)
+    _cuda("context_lens", context_lens, torch.int32)
+    _cuda("page_refs", page_refs, torch.int32)
+    S = context_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("block_table is [num_seqs, pages]")
+    if arrays is not None:
+        if not isinstance(arrays, PageArrays):
+            raise TypeError("arrays is a page_arrays(...)")
+        if arrays.num_pages not in (None, page_refs.numel()):
+            raise ValueError(f"arrays have {arrays.num_pages} pages, page_refs {page_refs.numel()}")
+    return S
+
+
+def _row_values(name, t, n):
+    if t is None:
+        return None
+    _cuda(name, t, torch.int32)
+    if t.numel() != n:
+        raise ValueError(f"{name} has an entry for each of the {n} rows")
+    return t.data_ptr()
+
+
+def _one(name, t):
+    _cuda(name, t, torch.int32)
+    if t.numel() != 1:
+        raise ValueError(f"{name} is one int32")
+    return t.data_ptr()
+
+
+def _workspace_of(workspace):
+    if workspace is None:
+        return None, 0
+    _cuda("workspace", workspace)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def kvc_truncate(block_table: torch.Tensor, context_lens: torch.Tensor,
+                 new_lens: Optional[torch.Tensor], page_refs: torch.Tensor, page_size: int,
+                 stream=None) -> None:
+    """Rows give back the pages past new_lens positions (None: all of them); context_lens follows."""
+    S = _table(block_table, context_lens, page_refs)
+    _check("kvc_truncate", lib().kvc_truncate(
+        _ptr(block_table), block_table.shape[1], _ptr(context_lens), _row_values("new_lens", new_lens, S),
+        S, _ptr(page_refs), page_refs.numel(), int(page_size), _stream(stream)))
+
+
+def kvc_fork(block_table_out: torch.Tensor, context_lens_out: torch.Tensor, parents: torch.Tensor,
+             block_table: torch.Tensor, context_lens: torch.Tensor, page_refs: torch.Tensor,
+             page_size: int, share_lens: Optional[torch.Tensor] = None, stream=None) -> None:
+    """New rows that share the pages of rows parents (negative: empty rows), the first share_lens
+    positions of them where that is given."""
+    S = _table(block_table, context_lens, page_refs)
+    n = _table(block_table_out, context_lens_out, page_refs)
+    if parents is None:
+        raise ValueError("parents: a row for each new one")
+    _check("kvc_fork", lib().kvc_fork(
+        _ptr(block_table_out), block_table_out.shape[1], _ptr(context_lens_out),
+        _row_values("parents", parents, n), _row_values("share_lens", share_lens, n), n,
+        _ptr(block_table), block_table.shape[1], _ptr(context_lens), S, _ptr(page_refs),
+        page_refs.numel(), int(page_size), _stream(stream)))
+
+
+def kvc_reserve_plan(num_seqs: int, num_pages: int) -> int:
+    """Workspace bytes kvc_reserve needs."""
+    ws = ctypes.c_size_t()
+    _check("kvc_reserve_plan", lib().kvc_reserve_plan(int(num_seqs), int(num_pages), ctypes.byref(ws)))
+    return ws.value
+
+
+def kvc_reserve(block_table: torch.Tensor, context_lens: torch.Tensor,
+                new_tokens: Optional[torch.Tensor], page_refs: torch.Tensor, missing: torch.Tensor,
+                page_size: int, arrays: Optional[PageArrays] = None,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Pages for new_tokens more positions of every row (None: one); shared partly filled last pages
+    are copied first, in every array.  missing (int32 [1]): 0, or how many free pages are wanting;
+    then nothing else is changed."""
+    S = _table(block_table, context_lens, page_refs, arrays)
+    ws, ws_bytes = _workspace_of(workspace)
+    _check("kvc_reserve", lib().kvc_reserve(
+        arrays.table if arrays else None, len(arrays.tensors) if arrays else 0, _ptr(block_table),
+        block_table.shape[1], _ptr(context_lens), _row_values("new_tokens", new_tokens, S), S,
+        _ptr(page_refs), page_refs.numel(), int(page_size), _one("missing", missing), ws, ws_bytes,
+        _stream(stream)))
+
+
+def kvc_compact_plan(num_pages: int) -> int:
+    """Workspace bytes kvc_compact needs."""
+    ws = ctypes.c_size_t()
+    _check("kvc_compact_plan", lib().kvc_compact_plan(int(num_pages), ctypes.byref(ws)))
+    return ws.value
+
+
+def kvc_compact(block_table: torch.Tensor, context_lens: torch.Tensor, page_refs: torch.Tensor,
+                page_map: torch.Tensor, num_live: torch.Tensor, page_size: int,
+                arrays: Optional[PageArrays] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> None:
+    """Move the pages in use to the front of the pool; the rows of the table follow.  page_map int32
+    [num_pages]: where every page went (-1: free); num_live int32 [1]: pages in use."""
+    S = _table(block_table, context_lens, page_refs, arrays)
+    ws, ws_bytes = _workspace_of(workspace)
+    _check("kvc_compact", lib().kvc_compact(
+        arrays.table if arrays else None, len(arrays.tensors) if arrays else 0, _ptr(block_table),
+        block_table.shape[1], _ptr(context_lens), S, _ptr(page_refs), page_refs.numel(),
+        int(page_size), _row_values("page_map", page_map, page_refs.numel()),
+        _one("num_live", num_live), ws, ws_bytes, _stream(stream)))
 
 
 def kvc_copy_pages(k_pool: torch.Tensor, v_pool: torch.Tensor, src_pages: torch.Tensor,
