@@ -341,6 +341,38 @@ kvc_status kvc_append(void *out, int32_t out_dtype, const void *q, const void *k
                       void *stream);
 
 /*
+ * kvc_cross -- attention of queries to the states of a source of another length (an encoder's keys and values
+ * in pages, or a prefix that all queries see): no causal limit.  (No counterpart on the pages, whose
+ * queries always follow their keys; the addressing is theirs: "KV Cache Management and PagedAttention",
+ * "Compute attention over scattered KV".)  Every query token of source s, q_indptr[s] .. q_indptr[s + 1] - 1
+ * (a prompt, the single tokens of its beams, or none), attends to all its source_lens[s] positions:
+ *   out[t][h] = softmax_{p < source_lens[s]}( q[t][h] . K_s[p][h/G] * scale ) . V_s[p][h/G]
+ * and lse_out[t][h] is the logarithm of that softmax's sum (natural; with kvc_merge it joins this
+ * result to one over other positions).  A source without positions gives out = 0 and lse = -inf.  Rows of
+ * out and lse_out that belong to no source (before q_indptr[0], from q_indptr[num_sources] on) are left as
+ * they are.  The positions are cut into consecutive chunks as in kvc_decode (kvc_cross_plan); the result
+ * depends on their number only by fp32 rounding.
+ *   q, out        [num_tokens][q_heads][head_dim]; q bf16, out per out_dtype
+ *   lse_out       fp32 [num_tokens][q_heads] or NULL
+ *   block_table   int32 [num_sources][bt_stride];  source_lens int32 [num_sources]
+ *   q_indptr      int32 [num_sources + 1], not decreasing
+ *   max_q_len, max_src  host upper bounds on every source's tokens and positions; more are flagged
+ *                 (kvc_device_errors, 1 << 7): positions past max_src are not seen, rows past max_q_len undefined
+ *   num_splits    0 = choose, 1 = no split, n > 1 = at most n chunks
+ *   workspace     kvc_cross_plan's bytes when the plan has more than one split, 16-byte aligned; it belongs to
+ *                 one call at a time
+ */
+kvc_status kvc_cross_plan(int32_t num_sources, int32_t num_tokens, int32_t q_heads, kvc_pool_desc pool,
+                          int32_t max_q_len, int32_t max_src, int32_t num_splits, int32_t *splits_out,
+                          int32_t *chunk_out, size_t *workspace_bytes_out);
+kvc_status kvc_cross(void *out, int32_t out_dtype, float *lse_out, const void *q, const void *k_pool,
+                     const void *v_pool, kvc_pool_desc pool, const int32_t *block_table,
+                     int32_t bt_stride, const int32_t *q_indptr, const int32_t *source_lens,
+                     int32_t num_sources, int32_t num_tokens, int32_t max_q_len, int32_t max_src,
+                     int32_t q_heads, float scale, int32_t num_splits, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
  * kvc_append_store -- kvc_slot_mapping + kvc_store + kvc_append in one pass over the chunk
  * (TileInfer.jl "KV cache": the store is fused into the kernel that stages K/V for attention).
  * Stores every new token's k_new / v_new row at the slot its position gets from the block

@@ -13,6 +13,7 @@ from .kvc import (EXPORTS, KVC_BF16, KVC_F32, KVC_HND, KVC_NHD, NOALLOC_SCRATCH_
                   kvc_decode_int4_plan, kvc_decode_weights, kvc_decode_weights_plan, kvc_evict,
                   kvc_evict_plan, RopeDesc, rope_desc, kvc_rope, kvc_rope_store, PageArrays, page_arrays,
                   kvc_truncate, kvc_fork, kvc_reserve, kvc_reserve_plan, kvc_compact, kvc_compact_plan,
+                  kvc_cross, kvc_cross_plan,
                   kvc_device_errors, kvc_selftest_wait, kvc_set_error_word, kvc_merge,
                   kvc_slot_mapping, kvc_store, kvc_store_int8, int8_pool_desc,
                   kvc_validate, kvc_validate_workspace_size, lib, library_path, pool_desc)
@@ -27,7 +28,7 @@ __all__ = ["EXPORTS", "KVC_BF16", "KVC_F32", "KVC_HND", "KVC_NHD", "NOALLOC_SCRA
            "kvc_decode_int4_plan", "kvc_decode_weights", "kvc_decode_weights_plan", "kvc_evict",
            "kvc_evict_plan", "RopeDesc", "rope_desc", "kvc_rope", "kvc_rope_store", "PageArrays",
            "page_arrays", "kvc_truncate", "kvc_fork", "kvc_reserve", "kvc_reserve_plan", "kvc_compact",
-           "kvc_compact_plan",
+           "kvc_compact_plan", "kvc_cross", "kvc_cross_plan",
            "kvc_device_errors", "kvc_selftest_wait", "kvc_set_error_word", "kvc_merge",
            "kvc_slot_mapping",
            "kvc_store", "kvc_store_int8", "int8_pool_desc",

@@ -2055,6 +2055,139 @@ kvc_status kvc_append(void *out, int32_t out_dtype, const void *q, const void *k
     return err == cudaSuccess ? ok() : cuda_fail(err, "append launch");
 }
 
+}  // extern "C"
+
+namespace {
+
+struct CrossPlan {
+    int splits, chunk;
+    size_t ws_bytes, lse_offset;
+};
+
+// Chunks of a multiple of the kernel's block; by default as many as give every SM several work items
+// (pairs of row tiles of one source, kv head and chunk).
+kvc_status make_cross_plan(int32_t num_sources, int32_t num_tokens, int32_t q_heads,
+                           const kvc_pool_desc &pool, int32_t max_q_len, int32_t max_src,
+                           int32_t requested, CrossPlan *out)
+{
+    kvc_status st = check_pool(pool);
+    if (st != KVC_OK || (st = check_group(pool, q_heads)) != KVC_OK)
+        return st;
+    if (num_sources < 0 || num_sources > 65535)
+        return fail(KVC_ERR_INVALID_ARG, "num_sources %d (0 .. 65535)", num_sources);
+    if (num_tokens < 0 || max_q_len < 0 || max_src < 0 || requested < 0)
+        return fail(KVC_ERR_INVALID_ARG, "negative num_tokens %d, max_q_len %d, max_src %d or num_splits %d",
+                    num_tokens, max_q_len, max_src, requested);
+    if ((st = check_reach(max_src, 0, pool.page_size, static_cast<int64_t>(num_tokens) * q_heads)) !=
+        KVC_OK)
+        return st;
+    const int group = q_heads / pool.kv_heads;
+    if (static_cast<int64_t>(max_q_len) * group > (int64_t(1) << 28))
+        return fail(KVC_ERR_UNSUPPORTED, "max_q_len * q_heads / kv_heads must be at most 2^28");
+    const int64_t src = std::max(max_src, 1), block = kvc::kCrossBlock;
+    int64_t want = requested;
+    if (requested == 0) {
+        const int64_t pairs = ceil_div(std::max<int64_t>(1, static_cast<int64_t>(max_q_len) * group), 256);
+        const int64_t units = pairs * pool.kv_heads * std::max(num_sources, 1);
+        want = ceil_div(4 * static_cast<int64_t>(device_sm_count()), units);
+    }
+    int64_t chunk = round_up(ceil_div(src, want), block);
+    if (requested == 0)
+        chunk = std::max<int64_t>(chunk, std::min<int64_t>(512, round_up(src, block)));
+    CrossPlan p{};
+    p.chunk = static_cast<int>(chunk);
+    p.splits = static_cast<int>(ceil_div(src, chunk));
+    if (p.splits > 1) {
+        const int64_t rows = static_cast<int64_t>(num_tokens) * q_heads;
+        p.lse_offset = static_cast<size_t>(round_up(rows * p.splits * pool.head_dim * 4, 256));
+        p.ws_bytes = p.lse_offset + static_cast<size_t>(rows * p.splits) * 4;
+    }
+    *out = p;
+    return KVC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvc_status kvc_cross_plan(int32_t num_sources, int32_t num_tokens, int32_t q_heads, kvc_pool_desc pool,
+                          int32_t max_q_len, int32_t max_src, int32_t num_splits, int32_t *splits_out,
+                          int32_t *chunk_out, size_t *workspace_bytes_out)
+{
+    CrossPlan p;
+    const kvc_status st = make_cross_plan(num_sources, num_tokens, q_heads, pool, max_q_len, max_src,
+                                          num_splits, &p);
+    if (st != KVC_OK)
+        return st;
+    if (splits_out)
+        *splits_out = p.splits;
+    if (chunk_out)
+        *chunk_out = p.chunk;
+    if (workspace_bytes_out)
+        *workspace_bytes_out = p.ws_bytes;
+    return ok();
+}
+
+kvc_status kvc_cross(void *out, int32_t out_dtype, float *lse_out, const void *q, const void *k_pool,
+                     const void *v_pool, kvc_pool_desc pool, const int32_t *block_table,
+                     int32_t bt_stride, const int32_t *q_indptr, const int32_t *source_lens,
+                     int32_t num_sources, int32_t num_tokens, int32_t max_q_len, int32_t max_src,
+                     int32_t q_heads, float scale, int32_t num_splits, void *workspace,
+                     size_t workspace_bytes, void *stream)
+{
+    CrossPlan p;
+    kvc_status st = make_cross_plan(num_sources, num_tokens, q_heads, pool, max_q_len, max_src, num_splits,
+                                    &p);
+    if (st != KVC_OK)
+        return st;
+    if (num_tokens == 0)
+        return ok();
+    if ((st = check_attention_args(out, out_dtype, q, k_pool, v_pool, pool, block_table, bt_stride,
+                                   source_lens, num_sources, max_src, q_heads)) != KVC_OK ||
+        (st = check_reach(max_src, bt_stride, pool.page_size, 0)) != KVC_OK)
+        return st;
+    if (num_sources > 0 && q_indptr == nullptr)
+        return fail(KVC_ERR_INVALID_ARG, "q_indptr is required");
+    if ((reinterpret_cast<uintptr_t>(lse_out) & 3u) != 0)
+        return fail(KVC_ERR_INVALID_ARG, "lse_out not 4-byte aligned");
+    if (num_sources == 0 || max_q_len == 0)
+        return ok();
+    if (p.splits > 1 && (st = check_workspace(workspace, workspace_bytes, p.ws_bytes)) != KVC_OK)
+        return st;
+    CUtensorMap tq, tk, tv;
+    if ((st = pool_tensor_map_halves(k_pool, pool, &tk)) != KVC_OK ||
+        (st = pool_tensor_map_halves(v_pool, pool, &tv)) != KVC_OK ||
+        (st = query_tensor_map(q, num_tokens, pool.kv_heads, q_heads / pool.kv_heads, pool.head_dim,
+                               &tq)) != KVC_OK)
+        return st;
+    kvc::CrossLaunch l;
+    l.out = out;
+    l.out_f32 = out_dtype == KVC_F32;
+    l.lse = lse_out;
+    if (p.splits > 1) {
+        l.part_o = static_cast<float *>(workspace);
+        l.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.lse_offset);
+    }
+    l.block_table = block_table;
+    l.bt_stride = bt_stride;
+    l.q_indptr = q_indptr;
+    l.source_lens = source_lens;
+    l.num_sources = num_sources;
+    l.num_tokens = num_tokens;
+    l.max_q_len = max_q_len;
+    l.max_src = max_src;
+    l.q_heads = q_heads;
+    l.kv_heads = pool.kv_heads;
+    l.head_dim = pool.head_dim;
+    l.page_size = pool.page_size;
+    l.chunk = p.chunk;
+    l.n_split = p.splits;
+    l.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(pool.head_dim));
+    l.hnd = pool.layout == KVC_HND;
+    const cudaError_t err = kvc::launch_cross(l, tq, tk, tv, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ok() : cuda_fail(err, "cross launch");
+}
+
 kvc_status kvc_append_store(void *out, int32_t out_dtype, const void *q, const void *k_new,
                             const void *v_new, void *k_pool, void *v_pool, kvc_pool_desc pool,
                             const int32_t *block_table, int32_t bt_stride,
@@ -2237,6 +2370,9 @@ kvc_status kvc_device_errors(uint32_t *flags_out)
     e |= f;
     if (err == cudaSuccess)
         err = kvc::read_and_clear_pages_errors(&f);
+    e |= f;
+    if (err == cudaSuccess)
+        err = kvc::read_and_clear_cross_errors(&f);
     e |= f;
     if (err != cudaSuccess)
         return cuda_fail(err, "reading the device error word");

@@ -279,6 +279,27 @@ struct AppendInt8Launch {
     bool hnd = false;   // codes [pages][Hkv][P][D] (the tensor maps follow it too)
 };
 
+// kvc_cross: queries against a source's pages, every position seen by every query; positions in n_split
+// chunks of `chunk` (a multiple of kCrossBlock), joined by a second launch when there are several.
+constexpr int kCrossBlock = 128;
+struct CrossLaunch {
+    void *out;
+    bool out_f32;
+    float *lse;                                      // [T][Hq] or null
+    float *part_o = nullptr, *part_lse = nullptr;    // [T][Hq][n_split][D], [T][Hq][n_split]
+    const int32_t *block_table;
+    int bt_stride;
+    const int32_t *q_indptr, *source_lens;
+    int num_sources, num_tokens, max_q_len, max_src, q_heads, kv_heads, head_dim, page_size;
+    int chunk, n_split;
+    float scale;
+    bool hnd;
+};
+// maps as for launch_append_tc
+cudaError_t launch_cross(const CrossLaunch &l, const CUtensorMap &tmap_q, const CUtensorMap &tmap_k,
+                         const CUtensorMap &tmap_v, cudaStream_t stream);
+cudaError_t read_and_clear_cross_errors(uint32_t *flags);
+
 // kvc_validate: the smallest offending index of each check (INT32_MAX when it passed), then two
 // bitmaps over the pool's slots.
 constexpr int kValidateChecks = 4;

@@ -36,7 +36,7 @@ EXPORTS = ("kvc_status_string", "kvc_last_error", "kvc_slot_mapping", "kvc_store
            "kvc_store_int4", "kvc_load_int4", "kvc_decode_int4", "kvc_decode_int4_plan",
            "kvc_decode_weights", "kvc_decode_weights_plan", "kvc_evict", "kvc_evict_plan",
            "kvc_rope", "kvc_rope_store", "kvc_truncate", "kvc_fork", "kvc_reserve",
-           "kvc_reserve_plan", "kvc_compact", "kvc_compact_plan")
+           "kvc_reserve_plan", "kvc_compact", "kvc_compact_plan", "kvc_cross", "kvc_cross_plan")
 
 # Size of the library's own split-partials scratch used by kvc_decode_noalloc (bytes).
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -174,6 +174,12 @@ def lib() -> ctypes.CDLL:
             L.kvc_rope_store.restype = ctypes.c_int
             L.kvc_rope_store.argtypes = [p, p, p, PoolDesc, p, i64, p, i64, p, i64, i32, RopeDesc, p,
                                          p, i32, p]
+            L.kvc_cross_plan.restype = ctypes.c_int
+            L.kvc_cross_plan.argtypes = [i32, i32, i32, PoolDesc, i32, i32, i32, ctypes.POINTER(i32),
+                                         ctypes.POINTER(i32), szp]
+            L.kvc_cross.restype = ctypes.c_int
+            L.kvc_cross.argtypes = [p, i32, p, p, p, p, PoolDesc, p, i32, p, p, i32, i32, i32, i32, i32,
+                                    f, i32, p, sz, p]
             L.kvc_truncate.restype = ctypes.c_int
             L.kvc_truncate.argtypes = [p, i32, p, p, i32, p, i32, i32, p]
             L.kvc_fork.restype = ctypes.c_int
@@ -989,6 +995,58 @@ def kvc_append(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor, v_pool:
         _ptr(block_table), int(block_table.shape[1]), _ptr(q_indptr), _ptr(context_lens),
         int(context_lens.shape[0]), int(q.shape[0]), int(max_q_len), int(max_ctx),
         int(q.shape[1]), float(scale), _stream(stream)))
+
+
+def kvc_cross_plan(num_sources: int, num_tokens: int, q_heads: int, pool: PoolDesc, max_q_len: int,
+                   max_src: int, num_splits: int = 0) -> Tuple[int, int, int]:
+    """(splits, chunk, workspace_bytes) that kvc_cross will use."""
+    splits, chunk, ws = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_size_t()
+    _check("kvc_cross_plan", lib().kvc_cross_plan(
+        int(num_sources), int(num_tokens), int(q_heads), pool, int(max_q_len), int(max_src),
+        int(num_splits), ctypes.byref(splits), ctypes.byref(chunk), ctypes.byref(ws)))
+    return splits.value, chunk.value, ws.value
+
+
+@functools.lru_cache(maxsize=256)
+def _cross_shapes(out, q, lse, block_table, source_lens, q_indptr, head_dim):
+    """Shapes of a cross attention's arguments; the number of sources."""
+    S = source_lens[0]
+    if len(q) != 3 or q[2] != head_dim or out != q:
+        raise ValueError(f"q and out are [num_tokens, q_heads, head_dim = {head_dim}], got {tuple(q)} "
+                         f"and {tuple(out)}")
+    if lse is not None and lse != q[:2]:
+        raise ValueError(f"lse_out is [num_tokens, q_heads] = {tuple(q[:2])}, got {tuple(lse)}")
+    if len(block_table) != 2 or block_table[0] != S or q_indptr != (S + 1,):
+        raise ValueError(f"block_table is [num_sources, pages] and q_indptr [num_sources + 1], with {S} "
+                         f"sources")
+    return S
+
+
+def kvc_cross(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+              block_table: torch.Tensor, q_indptr: torch.Tensor, source_lens: torch.Tensor,
+              max_q_len: int, max_src: int, lse_out: Optional[torch.Tensor] = None,
+              scale: float = 0.0, num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
+              stream=None, layout: str = "nhd") -> None:
+    """Cross attention: query tokens q_indptr[s] .. q_indptr[s + 1] - 1 to all source_lens[s]
+    positions of source s; lse_out (fp32 [T, Hq]) gets the log-sum-exps."""
+    _cuda("out", out)
+    _cuda("q", q, torch.bfloat16)
+    _cuda("k_pool", k_pool, torch.bfloat16)
+    _cuda("v_pool", v_pool, torch.bfloat16)
+    _cuda("block_table", block_table, torch.int32)
+    _cuda("q_indptr", q_indptr, torch.int32)
+    _cuda("source_lens", source_lens, torch.int32)
+    if lse_out is not None:
+        _cuda("lse_out", lse_out, torch.float32)
+    pool = _pool_shapes(k_pool.shape, v_pool.shape, layout)
+    S = _cross_shapes(out.shape, q.shape, None if lse_out is None else lse_out.shape, block_table.shape,
+                      source_lens.shape, q_indptr.shape, pool.head_dim)
+    ws, ws_bytes = _workspace_of(workspace)
+    _check("kvc_cross", lib().kvc_cross(
+        _ptr(out), _out_dtype(out), _ptr(lse_out), _ptr(q), _ptr(k_pool), _ptr(v_pool), pool,
+        _ptr(block_table), block_table.shape[1], _ptr(q_indptr), _ptr(source_lens), S, q.shape[0],
+        int(max_q_len), int(max_src), q.shape[1], float(scale), int(num_splits), ws, ws_bytes,
+        _stream(stream)))
 
 
 def kvc_append_store(out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor,
