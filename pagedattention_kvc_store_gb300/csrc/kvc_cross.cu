@@ -13,17 +13,17 @@
 //               by parallel lanes) in one ring, filled in the order K(0), K(1), V(0), K(2), V(1), ...
 //   warp 1      allocates TMEM (512 columns) and issues S_w = Q_w K(b)^T (M 128, N 128, K head_dim) and
 //               O_w += P_w V(b) (N head_dim, K 128, P from TMEM) of the tiles w from one thread; S_w(b + 1)
-//               right behind the PV product that reads P_w(b) from the same columns.  The V rows past the
-//               source's end, up to the next multiple of 16, are zeroed first, so that NaN in unused slots
-//               never meets a zero probability.
+//               right behind the PV product that reads P_w(b) from the same columns
 //   warp 2      TMA, the item's query tiles
-//   warps 3-6   softmax of tile 0, warps 7-10 of tile 1: a thread a row: the running maximum (O rescaled only
-//               when it grows by more than 2^8) and sum, P as bf16 over the first half of S's columns, and
-//               O / l at the end.
+//   warps 4-11  softmax of tile 0, warps 12-19 of tile 1: two threads a row: the running maximum (O rescaled
+//               only when it grows by more than 2^8) and sum, P as bf16 over the first half of S's columns,
+//               and O / l at the end.
+// An item of a single tile puts its blocks in turn on both halves of TMEM, so that the softmax of one runs
+// beside the products of the other as it does with two tiles, and joins the two at the end.
 // Few rows and many positions: the positions are cut into chunks (splits), partial rows and their
 // log-sum-exps go to the workspace and cross_merge_kernel joins them.
-// Sums: P is rounded to bf16 for the product and l sums the rounded values, so that numerator and denominator
-// weigh a position alike; a log-sum-exp that is asked for sums the unrounded ones.
+// Sums: P is rounded to bf16 for the product (2^-8 of each, the same the append makes), l sums the unrounded
+// values in fp32, which the log-sum-exp needs; summing the rounded ones besides took 128 more steps a row.
 #include <math.h>
 
 #include "kvc_device.cuh"
@@ -37,13 +37,19 @@ __device__ uint32_t g_cross_errors;
 
 constexpr int kM = 128;           // rows per tile
 constexpr int kBN = kCrossBlock;  // positions per K or V stage (the N of S = Q K^T)
-constexpr int kRoleWarps = 3;     // K/V loads, MMA issue, query loads
-constexpr int kSoftmaxWarps = 8;  // two groups of four
+constexpr int kRoleWarps = 4;     // K/V loads, MMA issue, query loads, one idle: a warpgroup
+constexpr int kSoftmaxWarps = 16; // a group of eight for each tile, two threads to a row
 constexpr int kThreads = (kRoleWarps + kSoftmaxWarps) * 32;
 constexpr int kMaxStages = 8;
+// Registers a thread: the launch's, and after the role warps gave theirs to the softmax warps.  128 * 64 +
+// 512 * 104 is 640 * 96: what the block was launched with.
+constexpr int kLaunchRegs = 96, kRoleRegs = 64, kSoftmaxRegs = 104;
+static_assert(kRoleWarps * kRoleRegs + kSoftmaxWarps * kSoftmaxRegs <=
+                  (kRoleWarps + kSoftmaxWarps) * kLaunchRegs, "registers of the launch");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
+constexpr uint32_t kBothTiles = 9;   // named barrier of all softmax warps; 1 .. 8 are of the pairs
 
 template <int D>
 struct Geom {
@@ -52,7 +58,8 @@ struct Geom {
     static constexpr int kStageBytes = kHalves * kBN * 128;  // K or V of 128 positions
     static constexpr int kStages = D == 128 ? 5 : 8;
     static constexpr int kOffStages = 2 * kQBytes;           // Q: [tile]
-    static constexpr int kOffBar = kOffStages + kStages * kStageBytes;
+    static constexpr int kOffExchange = kOffStages + kStages * kStageBytes;   // [tile][half][row] floats
+    static constexpr int kOffBar = kOffExchange + 4 * kM * 4;
     static constexpr size_t kSmemBytes = kOffBar + 512;      // base is 1024-aligned
     // TMEM, per tile w at w * 256: O [0, D), S [D, D + 128); P overwrites S [D, D + 64).
     static constexpr uint32_t kTmemCols = 512;
@@ -83,7 +90,8 @@ enum BarIndex : int {
     kBarQFull = kBarKvEmpty + kMaxStages,   // [tile]
     kBarQEmpty = kBarQFull + 2,             // [tile], one MMA commit after its last S product
     kBarSFull = kBarQEmpty + 2,             // [tile]
-    kBarPFull = kBarSFull + 2,              // [tile], 128 arrivals
+    kBarPHalf = kBarSFull + 2,              // [tile], an arrival of each of its four warps
+    kBarPFull = kBarPHalf + 2,              // [tile], the same
     kBarPvDone = kBarPFull + 2,             // [tile], once per item
     kBarDrain = kBarPvDone + 2,
     kBarCount = kBarDrain + 1
@@ -94,6 +102,7 @@ struct Item {
     int s, kvh, tp, split;
     int tok0, rows, row_begin;   // row_begin: first row of tile 2 tp
     bool has_b;                  // tile 2 tp + 1 exists
+    bool dual;                   // it does not: the blocks in turn on both halves of TMEM, joined at the end
     int key0, n_keys, n_blocks;  // n_keys 0: nothing to attend to, rows are written all the same
 };
 
@@ -132,6 +141,7 @@ struct Walker {
         x.key0 = x.split * a.chunk;
         x.n_keys = min(max(len - x.key0, 0), a.chunk);
         x.n_blocks = (x.n_keys + kBN - 1) / kBN;
+        x.dual = !x.has_b && x.n_blocks > 1;
         return true;
     }
     __device__ __forceinline__ void prefetch(const Args &a, int idx)
@@ -168,7 +178,7 @@ struct Walker {
     }
 };
 
-template <int D, bool LSE>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                  const __grid_constant__ CUtensorMap tmap_v, const Args a)
@@ -199,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBarCount; ++i)
-            mbar_init(&bars[i], (i == kBarPFull || i == kBarPFull + 1) ? 128u : 1u);
+            mbar_init(&bars[i], (i >= kBarPHalf && i < kBarPvDone) ? 4u : 1u);
         fence_mbar_init();
     }
     if (warp == 1)
@@ -210,6 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
 
+    if (warp < kRoleWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
     if (warp == 0) {
         // ------------------------------ K / V loads --------------------------------------
         if (lane == 0) {
@@ -305,285 +317,328 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issue ----------------------------------------
-        constexpr uint32_t kIdescPV = umma_idesc_bf16(kM, D, 1);
-        const uint32_t stage_addr = smem_addr(sStages);
-        auto stage_of = [&](int n) { return stage_addr + (n % kStages) * G_::kStageBytes; };
-        auto wait_slot = [&](int n) {
-            return __all_sync(0xffffffffu,
-                              mbar_wait(&bars[kBarKvFull + n % kStages], (n / kStages) & 1));
-        };
-        // S_t = Q_t K^T over n_cols positions (a multiple of 16)
-        auto issue_qk = [&](int t, uint32_t k_addr, int n_cols) {
-            const uint32_t idesc = umma_idesc_bf16(kM, n_cols, 0);
-            const uint32_t q_addr = smem_addr(q_tile(t));
+        // One thread for all of it: a vote of the warp after each wait costs as much as two products.
+        if (elect_one()) {
+            constexpr uint32_t kIdescPV = umma_idesc_bf16(kM, D, 1);
+            const uint32_t stage_addr = smem_addr(sStages);
+            auto stage_of = [&](int n) { return stage_addr + (n % kStages) * G_::kStageBytes; };
+            auto wait_slot = [&](int n) {
+                return mbar_wait(&bars[kBarKvFull + n % kStages], (n / kStages) & 1);
+            };
+            // Descriptors are made once for an operand and moved on by adding to their address field (in
+            // 16-byte units).
+            // S_t = Q_q K^T over n_cols positions (a multiple of 16)
+            auto issue_qk = [&](int t, int q, uint32_t k_addr, int n_cols) {
+                const uint32_t idesc = umma_idesc_bf16(kM, n_cols, 0);
+                const uint64_t da = umma_desc_sw128(smem_addr(q_tile(q)), 16, 1024);
+                const uint64_t db = umma_desc_sw128(k_addr, 16, 1024);
+                const uint32_t d = tmem + t * 256 + G_::kColS;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint64_t da =
-                    umma_desc_sw128(q_addr + (k >> 2) * kM * 128 + (k & 3) * 32, 16, 1024);
-                const uint64_t db =
-                    umma_desc_sw128(k_addr + (k >> 2) * kBN * 128 + (k & 3) * 32, 16, 1024);
-                umma_bf16_ss(tmem + t * 256 + G_::kColS, da, db, idesc, k > 0 ? 1u : 0u);
-            }
-        };
-        // O_t (+)= P_t V over k_steps x 16 positions
-        auto issue_pv = [&](int t, uint32_t v_addr, int k_steps, bool first) {
-            for (int k = 0; k < k_steps; ++k) {
-                const uint64_t db = umma_desc_sw128(v_addr + k * 16 * 128, kBN * 128, 1024);
-                umma_bf16_ts(tmem + t * 256, tmem + t * 256 + G_::kColS + k * 8, db, kIdescPV,
-                             (!first || k > 0) ? 1u : 0u);
-            }
-        };
-        Walker w;
-        int n0 = 0;             // ring index of the item's first slot
-        int qi[2] = {0, 0};     // items of tile 0 / tile 1
-        int tb[2] = {0, 0};     // blocks of tile 0 / tile 1
-        for (w.start(a, err_word); ok && !w.done; w.next(a, err_word)) {
-            const Item &x = w.x;
-            const int nt = x.has_b ? 2 : 1;
-            const int nb = x.n_blocks;
-            if (nb == 0)
-                continue;
-            const int last_valid = x.n_keys - (nb - 1) * kBN;   // positions in the last block
-            const int last_cols = (last_valid + 15) & ~15;
-            // ring indices in the producer's fill order K(0), K(1), V(0), K(2), V(1), ...
-            auto k_slot = [&](int b) { return n0 + (b == 0 ? 0 : 2 * b - 1); };
-            auto v_slot = [&](int b) { return n0 + (b == nb - 1 ? 2 * nb - 1 : 2 * b + 2); };
-            if (!wait_slot(k_slot(0))) {
-                ok = false;
-                break;
-            }
-            for (int t = 0; t < nt && ok; ++t) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarQFull + t], qi[t] & 1))) {
-                    ok = false;
-                    break;
+                for (int k = 0; k < D / 16; ++k)
+                    umma_bf16_ss(d, da + (k >> 2) * (kM * 128 / 16) + (k & 3) * 2,
+                                 db + (k >> 2) * (kBN * 128 / 16) + (k & 3) * 2, idesc, k > 0 ? 1u : 0u);
+            };
+            // O_t (+)= P_t V over positions 64 half .. of a block: a whole half, or the first 16 k_steps
+            auto issue_pv = [&](int t, uint32_t v_addr, int half, int k_steps, bool first) {
+                const uint64_t db = umma_desc_sw128(v_addr, kBN * 128, 1024) + half * (kBN / 2 * 128 / 16);
+                const uint32_t d = tmem + t * 256;
+                const uint32_t p = d + G_::kColS + half * (kBN / 4);
+                if (k_steps >= kBN / 32) {
+#pragma unroll
+                    for (int k = 0; k < kBN / 32; ++k)
+                        umma_bf16_ts(d, p + k * 8, db + k * 128, kIdescPV, (!first || k > 0) ? 1u : 0u);
+                } else {
+                    for (int k = 0; k < k_steps; ++k)
+                        umma_bf16_ts(d, p + k * 8, db + k * 128, kIdescPV, (!first || k > 0) ? 1u : 0u);
                 }
-                tc_fence_after_sync();
-                if (lane == 0) {
-                    issue_qk(t, stage_of(k_slot(0)), nb == 1 ? last_cols : kBN);
+            };
+            Walker w;
+            int n0 = 0;             // ring index of the item's first slot
+            int qi[2] = {0, 0};     // items of tile 0 / tile 1
+            int tb[2] = {0, 0};     // blocks of tile 0 / tile 1
+            for (w.start(a, err_word); ok && !w.done; w.next(a, err_word)) {
+                const Item &x = w.x;
+                const int nt = x.has_b ? 2 : 1;
+                const int nb = x.n_blocks;
+                if (nb == 0)
+                    continue;
+                const int last_cols = (x.n_keys - (nb - 1) * kBN + 15) & ~15;
+                // ring indices in the producer's fill order K(0), K(1), V(0), K(2), V(1), ...
+                auto k_slot = [&](int b) { return n0 + (b == 0 ? 0 : 2 * b - 1); };
+                auto v_slot = [&](int b) { return n0 + (b == nb - 1 ? 2 * nb - 1 : 2 * b + 2); };
+                auto cols = [&](int b) { return b + 1 == nb ? last_cols : kBN; };
+                if (x.dual) {
+                    // block b on half b % 2, in the order S(0), S(1), PV(0), S(2), PV(1), ...
+                    ok = mbar_wait(&bars[kBarQFull], qi[0] & 1);
+                    for (int b = -2; b < nb && ok; ++b) {
+                        const int t = b & 1;
+                        if (b >= 0) {
+                            const int vn = v_slot(b);
+                            if (!(ok = wait_slot(vn) && mbar_wait(&bars[kBarPHalf + t], tb[t] & 1)))
+                                break;
+                            tc_fence_after_sync();
+                            issue_pv(t, stage_of(vn), 0, cols(b) / 16, b < 2);
+                            if (!(ok = mbar_wait(&bars[kBarPFull + t], tb[t] & 1)))
+                                break;
+                            ++tb[t];
+                            tc_fence_after_sync();
+                            issue_pv(t, stage_of(vn), 1, cols(b) / 16 - kBN / 32, false);
+                            umma_commit(&bars[kBarKvEmpty + vn % kStages]);
+                            if (b + 2 >= nb)
+                                umma_commit(&bars[kBarPvDone + t]);
+                        }
+                        if (b + 2 < nb) {
+                            const int kn = k_slot(b + 2);
+                            if (!(ok = wait_slot(kn)))
+                                break;
+                            tc_fence_after_sync();
+                            issue_qk(t, 0, stage_of(kn), cols(b + 2));
+                            umma_commit(&bars[kBarSFull + t]);
+                            umma_commit(&bars[kBarKvEmpty + kn % kStages]);
+                            if (b + 3 == nb)
+                                umma_commit(&bars[kBarQEmpty]);
+                        }
+                    }
+                    if (!ok)
+                        break;
+                    ++qi[0];
+                    n0 += 2 * nb;
+                    continue;
+                }
+                ok = wait_slot(k_slot(0));
+                for (int t = 0; t < nt && ok; ++t) {
+                    if (!(ok = mbar_wait(&bars[kBarQFull + t], qi[t] & 1)))
+                        break;
+                    tc_fence_after_sync();
+                    issue_qk(t, t, stage_of(k_slot(0)), nb == 1 ? last_cols : kBN);
                     umma_commit(&bars[kBarSFull + t]);
                     if (nb == 1)
                         umma_commit(&bars[kBarQEmpty + t]);
                 }
-                __syncwarp();
-            }
-            if (!ok)
-                break;
-            if (lane == 0)
-                umma_commit(&bars[kBarKvEmpty + k_slot(0) % kStages]);
-            __syncwarp();
-            for (int b = 0; b < nb && ok; ++b) {
-                const bool last = b + 1 == nb;
-                const int vn = v_slot(b);
-                if (!wait_slot(vn)) {
-                    ok = false;
+                if (!ok)
                     break;
-                }
-                if (last && last_valid < last_cols) {
-                    // V rows last_valid .. last_cols - 1 of every column half
-                    uint8_t *vt = sStages + (vn % kStages) * G_::kStageBytes;
-                    const int rows_to_zero = last_cols - last_valid;
-                    for (int idx = lane; idx < rows_to_zero * kHalves * 8; idx += 32) {
-                        const int chunk = idx & 7;
-                        const int rest = idx >> 3;
-                        const int h = rest % kHalves;
-                        const int r = last_valid + rest / kHalves;
-                        *reinterpret_cast<uint4 *>(vt + h * kBN * 128 + r * 128 + chunk * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const int kn = last ? 0 : k_slot(b + 1);
-                for (int t = 0; t < nt; ++t) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarPFull + t], tb[t] & 1))) {
-                        ok = false;
-                        break;
-                    }
-                    ++tb[t];
-                    tc_fence_after_sync();
-                    if (lane == 0) {
-                        issue_pv(t, stage_of(vn), last ? last_cols / 16 : kBN / 16, b == 0);
-                        if (last)
+                umma_commit(&bars[kBarKvEmpty + k_slot(0) % kStages]);
+                for (int b = 0; b < nb && ok; ++b) {
+                    const bool last = b + 1 == nb;
+                    const int vn = v_slot(b);
+                    const int kn = last ? 0 : k_slot(b + 1);
+                    const int k_steps = last ? last_cols / 16 : kBN / 16;
+                    ok = wait_slot(vn);
+                    for (int t = 0; t < nt && ok; ++t) {
+                        if (!(ok = mbar_wait(&bars[kBarPHalf + t], tb[t] & 1)))
+                            break;
+                        tc_fence_after_sync();
+                        issue_pv(t, stage_of(vn), 0, k_steps, b == 0);
+                        // K(b + 1) is waited for only once PV(b) of tile 0 is on its way
+                        if (!(ok = (last || t > 0 || wait_slot(kn)) &&
+                                   mbar_wait(&bars[kBarPFull + t], tb[t] & 1)))
+                            break;
+                        ++tb[t];
+                        tc_fence_after_sync();
+                        issue_pv(t, stage_of(vn), 1, k_steps - kBN / 32, false);
+                        if (last) {
                             umma_commit(&bars[kBarPvDone + t]);
-                    }
-                    __syncwarp();
-                    if (last)
-                        continue;
-                    // K(b + 1) is waited for only once PV(b) of tile 0 is on its way
-                    if (t == 0 && !wait_slot(kn)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    if (lane == 0) {
-                        issue_qk(t, stage_of(kn), b + 2 == nb ? last_cols : kBN);
+                            continue;
+                        }
+                        issue_qk(t, t, stage_of(kn), b + 2 == nb ? last_cols : kBN);
                         umma_commit(&bars[kBarSFull + t]);
                         if (b + 2 == nb)
                             umma_commit(&bars[kBarQEmpty + t]);
                     }
-                    __syncwarp();
-                }
-                if (!ok)
-                    break;
-                if (lane == 0) {
+                    if (!ok)
+                        break;
                     umma_commit(&bars[kBarKvEmpty + vn % kStages]);
                     if (!last)
                         umma_commit(&bars[kBarKvEmpty + kn % kStages]);
                 }
-                __syncwarp();
+                if (!ok)
+                    break;
+                for (int t = 0; t < nt; ++t)
+                    ++qi[t];
+                n0 += 2 * nb;
             }
             if (!ok)
-                break;
-            for (int t = 0; t < nt; ++t)
-                ++qi[t];
-            n0 += 2 * nb;
-        }
-        if (!ok && lane == 0)
-            atomicOr(err_word, kErrCrossWait);
-        // every product that this thread issued must be complete before TMEM is released
-        if (lane == 0) {
+                atomicOr(err_word, kErrCrossWait);
+            // every product that this thread issued must be complete before TMEM is released
             umma_commit(&bars[kBarDrain]);
             if (!mbar_wait(&bars[kBarDrain], 0))
                 atomicOr(err_word, kErrDrainWait);
         }
         __syncwarp();
+    }
     } else {
         // ------------------------------ softmax + epilogue -------------------------------
-        const int t = (warp - kRoleWarps) >> 2;      // tile
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        // Two threads to a row, one for each half of a block's columns (and of O's): the one warp of a
+        // scheduler that had whole rows took 1,750 cycles from S to P, and the tensor pipe waited.
+        const int t = (warp - kRoleWarps) >> 3;      // tile
+        const int half = ((warp - kRoleWarps) >> 2) & 1;
         const int quad = warp & 3;                   // TMEM lanes 32 quad ..
         const int row = quad * 32 + lane;            // row of the tile = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t tmem_o = tmem + t * 256 + lane_off;
-        const uint32_t tmem_s = tmem + t * 256 + G_::kColS + lane_off;
+        const uint32_t tmem_o = tmem + lane_off + half * (D / 2);   // tile 0's; tile 1's 256 columns on
+        const uint32_t tmem_s = tmem + t * 256 + G_::kColS + lane_off + half * (kBN / 2);
+        const uint32_t tmem_p = tmem + t * 256 + G_::kColS + lane_off + half * (kBN / 4);
+        float *exchange = reinterpret_cast<float *>(smem + G_::kOffExchange);
+        float *mine = exchange + (t * 2 + half) * kM + row, *other = exchange + (t * 2 + 1 - half) * kM + row;
+        const uint32_t pair_bar = 1 + t * 4 + quad;  // the two warps of the same rows
         const float sl2 = a.scale_log2;
+        const uint64_t sl2x2 = f2_pack(sl2, sl2);
+        // A wait that runs out is the last one: the warp then goes through the rest of its items without
+        // waiting, so that no other is left alone at a named barrier.
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (ok)
+                ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+        };
         Walker w;
         int tb = 0;   // blocks of this tile so far
         int ti = 0;   // items of this tile so far
-        for (w.start(a, err_word); ok && !w.done; w.next(a, err_word)) {
+        int n0 = 0;   // ring index of the item's first slot
+        for (w.start(a, err_word); !w.done; n0 += 2 * w.x.n_blocks, w.next(a, err_word)) {
             const Item &x = w.x;
-            if (t == 1 && !x.has_b)
+            if (t == 1 && !x.has_b && !x.dual)
                 continue;
-            const int gr = x.row_begin + t * kM + row;
+            const int gr = x.row_begin + (x.dual ? 0 : t * kM) + row;
             const bool valid = gr < x.rows;
             const int tok = gr / G;
-            const bool warp_valid = __any_sync(0xffffffffu, valid);
-            float m_used = -INFINITY;
-            float l_sum = 0.0f, l_exact = 0.0f;
-            for (int b = 0; b < x.n_blocks; ++b, ++tb) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarSFull + t], tb & 1))) {
-                    ok = false;
-                    break;
-                }
+            const bool warp_valid = __any_sync(0xffffffffu, valid);   // the same in both warps of the rows
+            float m_used = -INFINITY, l = 0.0f;
+            const int b0 = x.dual ? t : 0;
+            for (int b = b0; b < x.n_blocks; b += x.dual ? 2 : 1, ++tb) {
+                wait(&bars[kBarSFull + t], tb & 1);
                 tc_fence_after_sync();
                 const int n_vis = min(x.n_keys - b * kBN, kBN);   // positions of this block
-                float alpha = 1.0f;
-                bool moved = false;
+                if ((n_vis & 15) != 0 && half == 0 && (x.dual || t == 0)) {
+                    // The last block's V rows n_vis .. up to the next multiple of 16 become zeros before P is
+                    // handed over (this PV product is the first to read them), so that NaN in unused slots
+                    // never meets a zero probability.  A warp takes every fourth row.
+                    const int vn = n0 + 2 * x.n_blocks - 1;
+                    wait(&bars[kBarKvFull + vn % kStages], (vn / kStages) & 1);
+                    uint8_t *vt = sStages + (vn % kStages) * G_::kStageBytes;
+                    for (int r = n_vis + quad; r < ((n_vis + 15) & ~15); r += 4)
+                        if (lane < kHalves * 8)
+                            *reinterpret_cast<uint4 *>(vt + (lane >> 3) * kBN * 128 + r * 128 +
+                                                       (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                }
                 if (warp_valid) {
-                    // pass 1: the row maximum; masked columns become -inf in TMEM as well
-                    float xs[4][32];
+                    const int n_mine = n_vis - half * (kBN / 2);   // of this thread's 64 columns
+                    float mx[4];
+                    uint32_t pk[2][16];
+                    uint64_t sum2[2];
+                    // S to registers, p = 2^(s * scale * log2(e) - m) as bf16 pairs, their sum before the
+                    // rounding, and the largest s
+                    auto probabilities = [&]() {
+                        float xs[2][32];
+                        tmem_ld32(tmem_s, xs[0]);
+                        tmem_ld32(tmem_s + 32, xs[1]);
+                        tmem_wait_ld();
+                        if (n_mine < kBN / 2) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tmem_ld32(tmem_s + 32 * c, xs[c]);
-                    tmem_wait_ld();
-                    float mx = -INFINITY;
-                    if (n_vis == kBN) {
-#pragma unroll
-                        for (int j = 0; j < kBN; j += 2)
-                            mx = fmax3(mx, xs[j >> 5][j & 31], xs[j >> 5][(j & 31) + 1]);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (32 * c + j >= n_vis)
-                                    xs[c][j] = -INFINITY;
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2)
-                                mx = fmax3(mx, xs[c][j], xs[c][j + 1]);
-                            tmem_st32(tmem_s + 32 * c, xs[c]);
+                            for (int i = 0; i < 64; ++i)
+                                if (i >= n_mine)
+                                    xs[i >> 5][i & 31] = -INFINITY;
                         }
-                        tmem_wait_st();
-                    }
-                    const float mb = mx * sl2;   // base-2 scaled maximum of this block
-                    if (mb > m_used + kRescaleLog2) {
-                        alpha = (m_used == -INFINITY) ? 0.0f : fast_exp2(m_used - mb);
-                        m_used = mb;
-                        moved = true;
-                    }
-                }
-                // O holds every earlier PV product (S(b) was committed after them): rescale
-                // it in place when the maximum moved.
-                if (b > 0 && __any_sync(0xffffffffu, moved)) {
-                    const float f = moved ? alpha : 1.0f;
+                        const float neg_mu = (m_used == -INFINITY) ? 0.0f : -m_used;
+                        const uint64_t nm2 = f2_pack(neg_mu, neg_mu);
+                        sum2[0] = sum2[1] = f2_pack(0.0f, 0.0f);
 #pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        float o[32];
-                        tmem_ld32(tmem_o + c0, o);
-                        tmem_wait_ld();
+                        for (int j = 0; j < 4; ++j)
+                            mx[j] = -INFINITY;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            o[j] *= f;
-                        tmem_st32(tmem_o + c0, o);
-                    }
-                }
-                // pass 2, 32 columns at a time: p = 2^(s * scale * log2(e) - m); the bf16 pairs of
-                // chunk c go to S columns [16 c, 16 c + 16), which hold only chunks already read
-                const float neg_mu = (m_used == -INFINITY) ? 0.0f : -m_used;
-                const uint64_t sl2x2 = f2_pack(sl2, sl2);
-                const uint64_t nm2 = f2_pack(neg_mu, neg_mu);
-                uint64_t psum2 = f2_pack(0.0f, 0.0f), pexact2 = f2_pack(0.0f, 0.0f);
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
-                    if (warp_valid) {
-                        float v[32];
-                        tmem_ld32(tmem_s + 32 * c, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
+                        for (int i = 0; i < 32; ++i) {
+                            const float x0 = xs[i >> 4][2 * (i & 15)], x1 = xs[i >> 4][2 * (i & 15) + 1];
                             float e0, e1;
-                            f2_unpack(f2_fma(f2_pack(v[2 * j], v[2 * j + 1]), sl2x2, nm2), e0, e1);
+                            f2_unpack(f2_fma(f2_pack(x0, x1), sl2x2, nm2), e0, e1);
                             e0 = fast_exp2(e0);
                             e1 = fast_exp2(e1);
-                            pk[j] = pack_bf16x2(e0, e1);
-                            psum2 = f2_add(psum2, f2_pack(__uint_as_float(pk[j] << 16),
-                                                          __uint_as_float(pk[j] & 0xFFFF0000u)));
-                            if (LSE)
-                                pexact2 = f2_add(pexact2, f2_pack(e0, e1));
+                            pk[i >> 4][i & 15] = pack_bf16x2(e0, e1);
+                            sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(e0, e1));
+                            mx[i & 3] = fmax3(mx[i & 3], x0, x1);
                         }
-                    } else {
+                    };
+                    // With the maximum of the blocks before, which nearly always still holds (it may be
+                    // passed by 2^8).  The two warps of the rows go on together: P overwrites columns that
+                    // half 0 reads.
+                    probabilities();
+                    float mb = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl2;   // base 2
+                    tc_fence_before_sync();
+                    const bool again = barrier_or(pair_bar, 64, mb > m_used + kRescaleLog2);
+                    tc_fence_after_sync();
+                    if (again) {
+                        *mine = mb;
+                        named_barrier(pair_bar, 64);
+                        mb = fmaxf(mb, *other);
+                        float alpha = 1.0f;
+                        if (mb > m_used + kRescaleLog2) {
+                            alpha = (m_used == -INFINITY) ? 0.0f : fast_exp2(m_used - mb);
+                            m_used = mb;
+                        }
+                        l *= alpha;
+                        // O holds every earlier PV product (S(b) was committed after them): its columns of
+                        // this half are rescaled in place
+                        if (b > b0) {
+#pragma unroll 1
+                            for (int c0 = 0; c0 < D / 2; c0 += 16) {
+                                float o[16];
+                                tmem_ld16(tmem_o + t * 256 + c0, o);
+                                tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)   // a warp of padding rows: P = 0
-                            pk[j] = 0u;
+                                for (int j = 0; j < 16; ++j)
+                                    o[j] *= alpha;
+                                tmem_st16(tmem_o + t * 256 + c0, o);
+                            }
+                            tmem_wait_st();
+                        }
+                        probabilities();
+                        tc_fence_before_sync();
+                        named_barrier(pair_bar, 64);
+                        tc_fence_after_sync();
                     }
-                    tmem_st16u(tmem_s + 16 * c, pk);
+                    tmem_st16u(tmem_p, pk[0]);
+                    tmem_st16u(tmem_p + 16, pk[1]);
+                    float p0, p1;
+                    f2_unpack(f2_add(sum2[0], sum2[1]), p0, p1);
+                    l += p0 + p1;
+                    tmem_wait_st();
                 }
-                float p0, p1;
-                f2_unpack(psum2, p0, p1);
-                l_sum = l_sum * alpha + (p0 + p1);
-                if (LSE) {
-                    f2_unpack(pexact2, p0, p1);
-                    l_exact = l_exact * alpha + (p0 + p1);
-                }
-                tmem_wait_st();
+                // (rows of padding: whatever P holds stays in rows of O that nobody reads)
                 tc_fence_before_sync();
-                mbar_arrive(&bars[kBarPFull + t]);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars[(half == 0 ? kBarPHalf : kBarPFull) + t]);
             }
-            if (!ok)
-                break;
             // epilogue: once this tile's last PV is done, O / l -> global
             if (x.n_blocks > 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarPvDone + t], ti & 1))) {
-                    ok = false;
-                    break;
-                }
+                wait(&bars[kBarPvDone + t], ti & 1);
                 ++ti;
                 tc_fence_after_sync();
             }
-            const float inv = (l_sum > 0.0f) ? 1.0f / l_sum : 0.0f;
-            const int g = gr - tok * G;
+            *mine = l;
+            named_barrier(pair_bar, 64);
+            l += *other;
+            named_barrier(pair_bar, 64);
+            float f[2] = {1.0f, 0.0f};   // weights of the two halves of TMEM
+            if (x.dual) {
+                // (m, l) of both, read by both; each writes half of its thread's columns
+                *mine = half == 0 ? m_used : l;
+                tc_fence_before_sync();
+                named_barrier(kBothTiles, kSoftmaxWarps * 32);
+                tc_fence_after_sync();
+                const float m0 = exchange[row], l0 = exchange[kM + row];
+                const float m1 = exchange[2 * kM + row], l1 = exchange[3 * kM + row];
+                m_used = fmaxf(m0, m1);
+                f[0] = m0 == -INFINITY && m_used != m0 ? 0.0f : fast_exp2(m0 - m_used);
+                f[1] = m1 == -INFINITY && m_used != m1 ? 0.0f : fast_exp2(m1 - m_used);
+                if (m_used == -INFINITY)   // no score above -inf (or NaN alone, which l and O hold)
+                    f[0] = f[1] = 1.0f;
+                l = l0 * f[0] + l1 * f[1];
+            }
+            const float inv = (l == 0.0f) ? 0.0f : 1.0f / l;
+            f[0] *= inv;
+            f[1] *= inv;
             size_t out_row = static_cast<size_t>(x.tok0 + tok) * a.q_heads +
-                             static_cast<size_t>(x.kvh) * G + g;
+                             static_cast<size_t>(x.kvh) * G + (gr - tok * G);
             void *out = a.out;
             int out_f32 = a.out_f32;
             float *lse = a.lse;
@@ -593,47 +648,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 out_f32 = 1;
                 lse = a.part_lse;
             }
-            if (valid && lse != nullptr) {
-                const float l = LSE ? l_exact : l_sum;
-                // no position: -inf; a NaN sum stays one
-                lse[out_row] = l == 0.0f ? -INFINITY : m_used * kLn2 + logf(l);
-            }
+            if (valid && lse != nullptr && half == 0 && !(x.dual && t == 1))
+                lse[out_row] = l == 0.0f ? -INFINITY : m_used * kLn2 + logf(l);   // no position: -inf
             if (x.n_blocks == 0 && a.n_split > 1)
                 continue;   // an empty split's row is not read
-            out_row *= D;
+            const int c_begin = x.dual ? t * (D / 4) : 0, c_end = x.dual ? c_begin + D / 4 : D / 2;
+#pragma unroll 1
+            for (int c0 = c_begin; c0 < c_end; c0 += 16) {
+                float o[16];
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                float o[32];
+                for (int j = 0; j < 16; ++j)
+                    o[j] = 0.0f;
                 if (x.n_blocks > 0) {
-                    tmem_ld32(tmem_o + c0, o);
+                    tmem_ld16(tmem_o + (x.dual ? 0 : t * 256) + c0, o);
                     tmem_wait_ld();
-                } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        o[j] = 0.0f;
+                    for (int j = 0; j < 16; ++j)
+                        o[j] *= f[0];
+                }
+                if (x.dual) {
+                    float o1[16];
+                    tmem_ld16(tmem_o + 256 + c0, o1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        o[j] = fmaf(o1[j], f[1], o[j]);
                 }
                 if (valid) {
-                    if (out_f32) {
-                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) +
-                                                                 out_row + c0);
+                    const size_t at = out_row * D + half * (D / 2) + c0;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[j] = make_float4(o[4 * j] * inv, o[4 * j + 1] * inv,
-                                                 o[4 * j + 2] * inv, o[4 * j + 3] * inv);
-                    } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(
-                            static_cast<__nv_bfloat16 *>(out) + out_row + c0);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            dst[c] = make_uint4(pack_bf16x2(o[8 * c] * inv, o[8 * c + 1] * inv),
-                                                pack_bf16x2(o[8 * c + 2] * inv, o[8 * c + 3] * inv),
-                                                pack_bf16x2(o[8 * c + 4] * inv, o[8 * c + 5] * inv),
-                                                pack_bf16x2(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
+                    for (int j = 0; j < 16; j += 8) {
+                        if (out_f32) {
+                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) + at + j);
+                            dst[0] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                            dst[1] = make_float4(o[j + 4], o[j + 5], o[j + 6], o[j + 7]);
+                        } else {
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + at + j) =
+                                make_uint4(pack_bf16x2(o[j], o[j + 1]), pack_bf16x2(o[j + 2], o[j + 3]),
+                                           pack_bf16x2(o[j + 4], o[j + 5]), pack_bf16x2(o[j + 6], o[j + 7]));
+                        }
                     }
                 }
                 __syncwarp();
             }
             tc_fence_before_sync();
+            if (x.dual)   // nobody overwrites what the other still reads
+                named_barrier(kBothTiles, kSoftmaxWarps * 32);
         }
         if (!ok)
             atomicOr(err_word, kErrCrossWait);
@@ -698,7 +758,7 @@ __global__ void __launch_bounds__(128)
         lse_out[row] = nan ? NAN : (total > 0.0f ? M + logf(total) : -INFINITY);
 }
 
-template <int D, bool LSE>
+template <int D>
 cudaError_t launch_t(const CrossLaunch &l, const CUtensorMap &tq, const CUtensorMap &tk,
                      const CUtensorMap &tv, cudaStream_t stream)
 {
@@ -730,10 +790,17 @@ cudaError_t launch_t(const CrossLaunch &l, const CUtensorMap &tq, const CUtensor
     if (items > 0x7FFFFFFFLL)
         return cudaErrorInvalidValue;
     a.num_items = static_cast<int>(items);
-    auto kernel = cross_kernel<D, LSE>;
+    auto kernel = cross_kernel<D>;
+    // the split of registers draws on what the block is launched with
+    cudaFuncAttributes attr;
+    cudaError_t err = cudaFuncGetAttributes(&attr, kernel);
+    if (err != cudaSuccess)
+        return err;
+    if (attr.numRegs < kLaunchRegs)
+        return cudaErrorLaunchOutOfResources;
     const size_t smem = Geom<D>::kSmemBytes;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(smem));
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(smem));
     if (err != cudaSuccess)
         return err;
     const int sms = current_sm_count();
@@ -753,11 +820,8 @@ cudaError_t launch_t(const CrossLaunch &l, const CUtensorMap &tq, const CUtensor
 cudaError_t launch_cross(const CrossLaunch &l, const CUtensorMap &tmap_q, const CUtensorMap &tmap_k,
                          const CUtensorMap &tmap_v, cudaStream_t stream)
 {
-    if (l.head_dim == 128)
-        return l.lse ? launch_t<128, true>(l, tmap_q, tmap_k, tmap_v, stream)
-                     : launch_t<128, false>(l, tmap_q, tmap_k, tmap_v, stream);
-    return l.lse ? launch_t<64, true>(l, tmap_q, tmap_k, tmap_v, stream)
-                 : launch_t<64, false>(l, tmap_q, tmap_k, tmap_v, stream);
+    return l.head_dim == 128 ? launch_t<128>(l, tmap_q, tmap_k, tmap_v, stream)
+                             : launch_t<64>(l, tmap_q, tmap_k, tmap_v, stream);
 }
 
 cudaError_t read_and_clear_cross_errors(uint32_t *flags)
