@@ -2060,12 +2060,13 @@ kvc_status kvc_append(void *out, int32_t out_dtype, const void *q, const void *k
 namespace {
 
 struct CrossPlan {
+    bool few;   // rows of a (source, kv head) few enough for the kernel that holds them in registers
     int splits, chunk;
     size_t ws_bytes, lse_offset;
 };
 
-// Chunks of a multiple of the kernel's block; by default as many as give every SM several work items
-// (pairs of row tiles of one source, kv head and chunk).
+// Few rows: kvc_decode's chunks.  Otherwise chunks of a multiple of the kernel's block; by default as many as
+// give every SM several work items (pairs of row tiles of one source, kv head and chunk).
 kvc_status make_cross_plan(int32_t num_sources, int32_t num_tokens, int32_t q_heads,
                            const kvc_pool_desc &pool, int32_t max_q_len, int32_t max_src,
                            int32_t requested, CrossPlan *out)
@@ -2081,20 +2082,27 @@ kvc_status make_cross_plan(int32_t num_sources, int32_t num_tokens, int32_t q_he
     if ((st = check_reach(max_src, 0, pool.page_size, static_cast<int64_t>(num_tokens) * q_heads)) !=
         KVC_OK)
         return st;
-    const int group = q_heads / pool.kv_heads;
-    if (static_cast<int64_t>(max_q_len) * group > (int64_t(1) << 28))
+    const int64_t rows_each = static_cast<int64_t>(max_q_len) * (q_heads / pool.kv_heads);
+    if (rows_each > (int64_t(1) << 28))
         return fail(KVC_ERR_UNSUPPORTED, "max_q_len * q_heads / kv_heads must be at most 2^28");
     const int64_t src = std::max(max_src, 1), block = kvc::kCrossBlock;
-    int64_t want = requested;
-    if (requested == 0) {
-        const int64_t pairs = ceil_div(std::max<int64_t>(1, static_cast<int64_t>(max_q_len) * group), 256);
-        const int64_t units = pairs * pool.kv_heads * std::max(num_sources, 1);
-        want = ceil_div(4 * static_cast<int64_t>(device_sm_count()), units);
+    int64_t chunk;
+    const bool few = rows_each <= kvc::kCrossFewRows && pool.kv_heads <= 65535;
+    if (few) {
+        chunk = make_plan(num_sources, q_heads, pool, max_src, requested).chunk;
+    } else {
+        int64_t want = requested;
+        if (requested == 0) {
+            const int64_t pairs = ceil_div(std::max<int64_t>(1, rows_each), 256);
+            const int64_t units = pairs * pool.kv_heads * std::max(num_sources, 1);
+            want = ceil_div(4 * static_cast<int64_t>(device_sm_count()), units);
+        }
+        chunk = round_up(ceil_div(src, want), block);
+        if (requested == 0)
+            chunk = std::max<int64_t>(chunk, std::min<int64_t>(512, round_up(src, block)));
     }
-    int64_t chunk = round_up(ceil_div(src, want), block);
-    if (requested == 0)
-        chunk = std::max<int64_t>(chunk, std::min<int64_t>(512, round_up(src, block)));
     CrossPlan p{};
+    p.few = few;
     p.chunk = static_cast<int>(chunk);
     p.splits = static_cast<int>(ceil_div(src, chunk));
     if (p.splits > 1) {
@@ -2155,12 +2163,18 @@ kvc_status kvc_cross(void *out, int32_t out_dtype, float *lse_out, const void *q
     if (p.splits > 1 && (st = check_workspace(workspace, workspace_bytes, p.ws_bytes)) != KVC_OK)
         return st;
     CUtensorMap tq, tk, tv;
-    if ((st = pool_tensor_map_halves(k_pool, pool, &tk)) != KVC_OK ||
-        (st = pool_tensor_map_halves(v_pool, pool, &tv)) != KVC_OK ||
-        (st = query_tensor_map(q, num_tokens, pool.kv_heads, q_heads / pool.kv_heads, pool.head_dim,
-                               &tq)) != KVC_OK)
+    if (p.few) {
+        if ((st = pool_tensor_map(k_pool, pool, &tk)) != KVC_OK ||
+            (st = pool_tensor_map(v_pool, pool, &tv)) != KVC_OK)
+            return st;
+    } else if ((st = pool_tensor_map_halves(k_pool, pool, &tk)) != KVC_OK ||
+               (st = pool_tensor_map_halves(v_pool, pool, &tv)) != KVC_OK ||
+               (st = query_tensor_map(q, num_tokens, pool.kv_heads, q_heads / pool.kv_heads,
+                                      pool.head_dim, &tq)) != KVC_OK) {
         return st;
+    }
     kvc::CrossLaunch l;
+    l.q = q;
     l.out = out;
     l.out_f32 = out_dtype == KVC_F32;
     l.lse = lse_out;
@@ -2184,7 +2198,10 @@ kvc_status kvc_cross(void *out, int32_t out_dtype, float *lse_out, const void *q
     l.n_split = p.splits;
     l.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(pool.head_dim));
     l.hnd = pool.layout == KVC_HND;
-    const cudaError_t err = kvc::launch_cross(l, tq, tk, tv, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err = p.few ? kvc::launch_cross_rows(l, tk, tv, s) : kvc::launch_cross(l, tq, tk, tv, s);
+    if (err == cudaSuccess && p.splits > 1)
+        err = kvc::launch_cross_merge(l, s);
     return err == cudaSuccess ? ok() : cuda_fail(err, "cross launch");
 }
 
@@ -2373,6 +2390,9 @@ kvc_status kvc_device_errors(uint32_t *flags_out)
     e |= f;
     if (err == cudaSuccess)
         err = kvc::read_and_clear_cross_errors(&f);
+    e |= f;
+    if (err == cudaSuccess)
+        err = kvc::read_and_clear_cross_rows_errors(&f);
     e |= f;
     if (err != cudaSuccess)
         return cuda_fail(err, "reading the device error word");

@@ -804,15 +804,8 @@ cudaError_t launch_t(const CrossLaunch &l, const CUtensorMap &tq, const CUtensor
     if (err != cudaSuccess)
         return err;
     const int sms = current_sm_count();
-    err = launch_pdl(kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kThreads), smem,
-                     stream, tq, tk, tv, a);
-    if (err != cudaSuccess || l.n_split == 1)
-        return err;
-    const long long rows = static_cast<long long>(l.num_tokens) * l.q_heads;
-    return launch_pdl(cross_merge_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0,
-                      stream, l.out, l.out_f32 ? 1 : 0, l.lse, static_cast<const float *>(l.part_o),
-                      static_cast<const float *>(l.part_lse), l.q_indptr, l.num_sources, l.num_tokens,
-                      l.q_heads, l.n_split);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kThreads), smem,
+                      stream, tq, tk, tv, a);
 }
 
 }  // namespace
@@ -822,6 +815,16 @@ cudaError_t launch_cross(const CrossLaunch &l, const CUtensorMap &tmap_q, const 
 {
     return l.head_dim == 128 ? launch_t<128>(l, tmap_q, tmap_k, tmap_v, stream)
                              : launch_t<64>(l, tmap_q, tmap_k, tmap_v, stream);
+}
+
+cudaError_t launch_cross_merge(const CrossLaunch &l, cudaStream_t stream)
+{
+    const long long rows = static_cast<long long>(l.num_tokens) * l.q_heads;
+    return launch_pdl(l.head_dim == 128 ? cross_merge_kernel<128> : cross_merge_kernel<64>,
+                      dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream, l.out,
+                      l.out_f32 ? 1 : 0, l.lse, static_cast<const float *>(l.part_o),
+                      static_cast<const float *>(l.part_lse), l.q_indptr, l.num_sources, l.num_tokens,
+                      l.q_heads, l.n_split);
 }
 
 cudaError_t read_and_clear_cross_errors(uint32_t *flags)

@@ -282,7 +282,9 @@ struct AppendInt8Launch {
 // kvc_cross: queries against a source's pages, every position seen by every query; positions in n_split
 // chunks of `chunk` (a multiple of kCrossBlock), joined by a second launch when there are several.
 constexpr int kCrossBlock = 128;
+constexpr int kCrossFewRows = 32;   // rows of a (source, kv head) up to which launch_cross_rows may take them
 struct CrossLaunch {
+    const void *q;
     void *out;
     bool out_f32;
     float *lse;                                      // [T][Hq] or null
@@ -295,6 +297,12 @@ struct CrossLaunch {
     float scale;
     bool hnd;
 };
+// A (source, kv head) has few rows: chunks of a multiple of kStageKeys, maps as for launch_decode.
+cudaError_t launch_cross_rows(const CrossLaunch &l, const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                              cudaStream_t stream);
+// The join of either kernel's splits.
+cudaError_t launch_cross_merge(const CrossLaunch &l, cudaStream_t stream);
+cudaError_t read_and_clear_cross_rows_errors(uint32_t *flags);
 // maps as for launch_append_tc
 cudaError_t launch_cross(const CrossLaunch &l, const CUtensorMap &tmap_q, const CUtensorMap &tmap_k,
                          const CUtensorMap &tmap_v, cudaStream_t stream);

@@ -121,8 +121,26 @@ def test_ragged_sources_and_queries(Hkv, G, D, P, layout, splits):
     check(c, b, None, bf16=True)
 
 
+@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("Hkv,G,D,P,layout,most", [(2, 4, 128, 16, "nhd", 4), (3, 1, 64, 32, "hnd", 9),
+                                                   (1, 8, 128, 64, "hnd", 4), (4, 2, 64, 16, "nhd", 16),
+                                                   (2, 8, 64, 64, "nhd", 3), (2, 2, 128, 32, "hnd", 17)])
+def test_ragged_sources_and_few_queries(Hkv, G, D, P, layout, most, splits):
+    """Up to 16, up to 32 and just over 32 rows a kv head."""
+    q_lens = [most, 0, 1, 2, most - 1, 1, 3, most, 2, most]
+    c = Case(RAGGED, q_lens, Hkv, G, D, P, layout, seed=most, pad=2)
+    out, lse = c.run(splits=splits)
+    check(c, out, lse)
+    assert (out[c.T:] == 7.25).all() and (lse[c.T:] == 7.25).all()
+    assert kvc.kvc_device_errors() == 0
+    none = slice(c.indptr[8], c.indptr[9])
+    assert (out[none] == 0).all() and torch.isinf(lse[none]).all()
+    b, _ = c.run(torch.bfloat16, splits, lse=False)
+    check(c, b, None, bf16=True)
+
+
 @pytest.mark.parametrize("splits", [0, 1, 2, 9])
-@pytest.mark.parametrize("rows", [1, 4])
+@pytest.mark.parametrize("rows", [1, 4, 8, 10])
 def test_beams_over_long_sources(rows, splits):
     c = Case([5000, 2049, 4096], [rows] * 3, 8, 4, 128, 16, seed=rows)
     out, lse = c.run(splits=splits)
