@@ -269,9 +269,9 @@ struct MapKey {
     int rank;
     bool int8 = false;   // uint8 elements (INT8 pages) instead of bf16
     int swizzle = 128;   // bytes of a swizzled row: 128, 64 or 32 (0: none)
-    cuuint64_t dims[4];
-    cuuint64_t strides[3];
-    cuuint32_t box[4];
+    cuuint64_t dims[5];
+    cuuint64_t strides[4];
+    cuuint32_t box[5];
     bool operator==(const MapKey &o) const
     {
         if (ptr != o.ptr || device != o.device || rank != o.rank || int8 != o.int8 ||
@@ -325,7 +325,7 @@ kvc_status tensor_map(MapKey key, CUtensorMap *out)
     auto fn = encode_fn();
     if (fn == nullptr)
         return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+    const cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
     CUtensorMap map;
     CUresult r = fn(&map,
                     key.int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -522,6 +522,42 @@ kvc_status pool_tensor_map(const void *base, const kvc_pool_desc &pool, CUtensor
     k.box[1] = static_cast<cuuint32_t>(pool.page_size);
     k.box[2] = static_cast<cuuint32_t>(pool.head_dim / 64);
     k.box[3] = 1;
+    return tensor_map(k, out);
+}
+
+// A pool viewed as {64 columns, position in a group of 8, column half, group, kv head} (HND: the last two are a
+// block's groups and the block): one box is a whole page of one kv head and lands in shared memory as [group]
+// [half][8 rows][64 columns], in which both halves of consecutive pages are operands of one stride for the
+// tensor cores (cross attention).
+kvc_status pool_tensor_map_groups(const void *base, const kvc_pool_desc &pool, CUtensorMap *out)
+{
+    const cuuint64_t vec = static_cast<cuuint64_t>(pool.head_dim) * 2;
+    const cuuint64_t heads = static_cast<cuuint64_t>(pool.kv_heads);
+    const cuuint64_t page_groups = static_cast<cuuint64_t>(pool.page_size) / 8;
+    const cuuint64_t row = pool.layout == KVC_HND ? vec : heads * vec;   // between positions
+    MapKey k{};
+    k.ptr = base;
+    k.rank = 5;
+    k.dims[0] = 64;
+    k.dims[1] = 8;
+    k.dims[2] = static_cast<cuuint64_t>(pool.head_dim) / 64;
+    k.strides[0] = row;
+    k.strides[1] = 128;
+    k.strides[2] = 8 * row;
+    if (pool.layout == KVC_HND) {
+        k.dims[3] = page_groups;
+        k.dims[4] = static_cast<cuuint64_t>(pool.num_pages) * heads;
+        k.strides[3] = static_cast<cuuint64_t>(pool.page_size) * vec;
+    } else {
+        k.dims[3] = static_cast<cuuint64_t>(pool.num_pages) * page_groups;
+        k.dims[4] = heads;
+        k.strides[3] = vec;
+    }
+    k.box[0] = 64;
+    k.box[1] = 8;
+    k.box[2] = static_cast<cuuint32_t>(k.dims[2]);
+    k.box[3] = static_cast<cuuint32_t>(page_groups);
+    k.box[4] = 1;
     return tensor_map(k, out);
 }
 
@@ -2167,8 +2203,8 @@ kvc_status kvc_cross(void *out, int32_t out_dtype, float *lse_out, const void *q
         if ((st = pool_tensor_map(k_pool, pool, &tk)) != KVC_OK ||
             (st = pool_tensor_map(v_pool, pool, &tv)) != KVC_OK)
             return st;
-    } else if ((st = pool_tensor_map_halves(k_pool, pool, &tk)) != KVC_OK ||
-               (st = pool_tensor_map_halves(v_pool, pool, &tv)) != KVC_OK ||
+    } else if ((st = pool_tensor_map_groups(k_pool, pool, &tk)) != KVC_OK ||
+               (st = pool_tensor_map_groups(v_pool, pool, &tv)) != KVC_OK ||
                (st = query_tensor_map(q, num_tokens, pool.kv_heads, q_heads / pool.kv_heads,
                                       pool.head_dim, &tq)) != KVC_OK) {
         return st;

@@ -9,8 +9,10 @@
 // positions (the whole source where there is one split); both tiles see the same pages, so every K or V
 // stage feeds two products.  One persistent CTA per SM walks items c, c + grid, ...; its roles run ahead
 // across items:
-//   warp 0      TMA, K and V: 128-position stages (a box per page and 64-column half, 128-byte swizzle, issued
-//               by parallel lanes) in one ring, filled in the order K(0), K(1), V(0), K(2), V(1), ...
+//   warp 0      TMA, K and V: 128-position stages in one ring, filled in the order K(0), K(1), V(0), K(2),
+//               V(1), ...; a box per page, issued by parallel lanes, that lands as [8 positions][column half]
+//               [8 rows][128 bytes, swizzled], so that a stage is one operand whatever the page size (a box
+//               per page and half took twice as many, and 16-position pages 37% more time)
 //   warp 1      allocates TMEM (512 columns) and issues S_w = Q_w K(b)^T (M 128, N 128, K head_dim) and
 //               O_w += P_w V(b) (N head_dim, K 128, P from TMEM) of the tiles w from one thread; S_w(b + 1)
 //               right behind the PV product that reads P_w(b) from the same columns
@@ -259,16 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     cached_base = lp0;
                     cached_page = (lp0 + lane < n_pages) ? bt_row[lp0 + lane] : 0;
                 }
-                // lane i * kHalves + h issues the box of page i, column half h
-                const int i = lane / kHalves;
-                const int h = lane % kHalves;
+                // lane i issues the box of page i; NHD maps end in {group, kv head}, HND maps in {group of
+                // the block, block}
                 const int page =
-                    __shfl_sync(0xffffffffu, cached_page, (lp0 - cached_base + i) & 31);
-                // NHD maps {head_dim, kv head, slot}; HND maps {head_dim, offset, block}
-                if (i < np)
-                    tma_load_3d(dst + h * kBN * 128 + i * P * 128, is_k ? &tmap_k : &tmap_v, h * 64,
-                                a.hnd ? 0 : x.kvh, a.hnd ? page * a.kv_heads + x.kvh : page * P,
-                                &bars[kBarKvFull + st], policy);
+                    __shfl_sync(0xffffffffu, cached_page, (lp0 - cached_base + lane) & 31);
+                if (lane < np)
+                    tma_load_5d_hint(dst + lane * P * (D * 2), is_k ? &tmap_k : &tmap_v, 0, 0, 0,
+                                     a.hnd ? 0 : page * (P / 8), a.hnd ? page * a.kv_heads + x.kvh : x.kvh,
+                                     &bars[kBarKvFull + st], policy);
             }
             if (!ok)
                 break;
@@ -331,25 +331,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto issue_qk = [&](int t, int q, uint32_t k_addr, int n_cols) {
                 const uint32_t idesc = umma_idesc_bf16(kM, n_cols, 0);
                 const uint64_t da = umma_desc_sw128(smem_addr(q_tile(q)), 16, 1024);
-                const uint64_t db = umma_desc_sw128(k_addr, 16, 1024);
+                const uint64_t db = umma_desc_sw128(k_addr, 16, kHalves * 1024);
                 const uint32_t d = tmem + t * 256 + G_::kColS;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     umma_bf16_ss(d, da + (k >> 2) * (kM * 128 / 16) + (k & 3) * 2,
-                                 db + (k >> 2) * (kBN * 128 / 16) + (k & 3) * 2, idesc, k > 0 ? 1u : 0u);
+                                 db + (k >> 2) * (1024 / 16) + (k & 3) * 2, idesc, k > 0 ? 1u : 0u);
             };
+            constexpr int kStep = 2 * kHalves * 1024 / 16;   // 16 positions of V
             // O_t (+)= P_t V over positions 64 half .. of a block: a whole half, or the first 16 k_steps
             auto issue_pv = [&](int t, uint32_t v_addr, int half, int k_steps, bool first) {
-                const uint64_t db = umma_desc_sw128(v_addr, kBN * 128, 1024) + half * (kBN / 2 * 128 / 16);
+                const uint64_t db = umma_desc_sw128(v_addr, 1024, kHalves * 1024) + half * 4 * kStep;
                 const uint32_t d = tmem + t * 256;
                 const uint32_t p = d + G_::kColS + half * (kBN / 4);
                 if (k_steps >= kBN / 32) {
 #pragma unroll
                     for (int k = 0; k < kBN / 32; ++k)
-                        umma_bf16_ts(d, p + k * 8, db + k * 128, kIdescPV, (!first || k > 0) ? 1u : 0u);
+                        umma_bf16_ts(d, p + k * 8, db + k * kStep, kIdescPV, (!first || k > 0) ? 1u : 0u);
                 } else {
                     for (int k = 0; k < k_steps; ++k)
-                        umma_bf16_ts(d, p + k * 8, db + k * 128, kIdescPV, (!first || k > 0) ? 1u : 0u);
+                        umma_bf16_ts(d, p + k * 8, db + k * kStep, kIdescPV, (!first || k > 0) ? 1u : 0u);
                 }
             };
             Walker w;
@@ -517,8 +518,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint8_t *vt = sStages + (vn % kStages) * G_::kStageBytes;
                     for (int r = n_vis + quad; r < ((n_vis + 15) & ~15); r += 4)
                         if (lane < kHalves * 8)
-                            *reinterpret_cast<uint4 *>(vt + (lane >> 3) * kBN * 128 + r * 128 +
-                                                       (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4 *>(vt + ((r >> 3) * kHalves + (lane >> 3)) * 1024 +
+                                                       (r & 7) * 128 + (lane & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
                 if (warp_valid) {

@@ -303,7 +303,7 @@ cudaError_t launch_cross_rows(const CrossLaunch &l, const CUtensorMap &tmap_k, c
 // The join of either kernel's splits.
 cudaError_t launch_cross_merge(const CrossLaunch &l, cudaStream_t stream);
 cudaError_t read_and_clear_cross_rows_errors(uint32_t *flags);
-// maps as for launch_append_tc
+// tmap_q as for launch_append_tc; tmap_k / tmap_v with a box per page, [group of 8 positions][column half][8][64]
 cudaError_t launch_cross(const CrossLaunch &l, const CUtensorMap &tmap_q, const CUtensorMap &tmap_k,
                          const CUtensorMap &tmap_v, cudaStream_t stream);
 cudaError_t read_and_clear_cross_errors(uint32_t *flags);
