@@ -7,8 +7,7 @@
 // Tiling: the rows of one (source, kv head) are its (token, query head of the group) pairs, token-major, in
 // tiles of 128 (the tcgen05 M).  A work item is a pair of consecutive tiles over one chunk of the source's
 // positions (the whole source where there is one split); both tiles see the same pages, so every K or V
-// stage feeds two products.  One persistent CTA per SM walks items c, c + grid, ...; its roles run ahead
-// across items:
+// stage feeds two products.  One CTA per SM goes on from item to item, its roles running ahead across them:
 //   warp 0      TMA, K and V: 128-position stages in one ring, filled in the order K(0), K(1), V(0), K(2),
 //               V(1), ...; a box per page, issued by parallel lanes, that lands as [8 positions][column half]
 //               [8 rows][128 bytes, swizzled], so that a stage is one operand whatever the page size (a box
@@ -17,6 +16,7 @@
 //               O_w += P_w V(b) (N head_dim, K 128, P from TMEM) of the tiles w from one thread; S_w(b + 1)
 //               right behind the PV product that reads P_w(b) from the same columns
 //   warp 2      TMA, the item's query tiles
+//   warp 3      the items: cancels blocks of the grid that have not started and hands theirs round
 //   warps 4-11  softmax of tile 0, warps 12-19 of tile 1: two threads a row: the running maximum (O rescaled
 //               only when it grows by more than 2^8) and sum, P as bf16 over the first half of S's columns,
 //               and O / l at the end.
@@ -39,7 +39,7 @@ __device__ uint32_t g_cross_errors;
 
 constexpr int kM = 128;           // rows per tile
 constexpr int kBN = kCrossBlock;  // positions per K or V stage (the N of S = Q K^T)
-constexpr int kRoleWarps = 4;     // K/V loads, MMA issue, query loads, one idle: a warpgroup
+constexpr int kRoleWarps = 4;     // K/V loads, MMA issue, query loads, items
 constexpr int kSoftmaxWarps = 16; // a group of eight for each tile, two threads to a row
 constexpr int kThreads = (kRoleWarps + kSoftmaxWarps) * 32;
 constexpr int kMaxStages = 8;
@@ -51,7 +51,8 @@ static_assert(kRoleWarps * kRoleRegs + kSoftmaxWarps * kSoftmaxRegs <=
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr uint32_t kBothTiles = 9;   // named barrier of all softmax warps; 1 .. 8 are of the pairs
+// named barriers of all softmax warps; 1 .. 8 are of the pairs
+constexpr uint32_t kBothTiles = 9, kAllSoftmax = 10;
 
 template <int D>
 struct Geom {
@@ -62,6 +63,8 @@ struct Geom {
     static constexpr int kOffStages = 2 * kQBytes;           // Q: [tile]
     static constexpr int kOffExchange = kOffStages + kStages * kStageBytes;   // [tile][half][row] floats
     static constexpr int kOffBar = kOffExchange + 4 * kM * 4;
+    static constexpr int kOffItem = kOffBar + 384;           // after the barriers: the item, an answer
+    static constexpr int kOffAnswer = kOffItem + 64;
     static constexpr size_t kSmemBytes = kOffBar + 512;      // base is 1024-aligned
     // TMEM, per tile w at w * 256: O [0, D), S [D, D + 128); P overwrites S [D, D + 64).
     static constexpr uint32_t kTmemCols = 512;
@@ -96,87 +99,84 @@ enum BarIndex : int {
     kBarPFull = kBarPHalf + 2,              // [tile], the same
     kBarPvDone = kBarPFull + 2,             // [tile], once per item
     kBarDrain = kBarPvDone + 2,
-    kBarCount = kBarDrain + 1
+    kBarItemFull = kBarDrain + 1,           // the item in shared memory is the next one
+    kBarItemEmpty = kBarItemFull + 1,       // an arrival of every warp that reads items
+    kBarCancel = kBarItemEmpty + 1,         // the answer to a request for a block that has not started
+    kBarCount = kBarCancel + 1
 };
+constexpr int kItemReaders = 3 + kSoftmaxWarps;
 
 // Tiles 2 tp and 2 tp + 1 of one (source, kv head) over positions key0 .. key0 + n_keys - 1.
-struct Item {
-    int s, kvh, tp, split;
-    int tok0, rows, row_begin;   // row_begin: first row of tile 2 tp
-    bool has_b;                  // tile 2 tp + 1 exists
-    bool dual;                   // it does not: the blocks in turn on both halves of TMEM, joined at the end
+struct __align__(16) Item {
+    int s, kvh, split, tok0;
+    int rows, row_begin;         // row_begin: first row of tile 2 tp
     int key0, n_keys, n_blocks;  // n_keys 0: nothing to attend to, rows are written all the same
+    int has_b;                   // tile 2 tp + 1 exists
+    int dual;                    // it does not: the blocks in turn on both halves of TMEM, joined at the end
+    int done;                    // no item: the last one was
 };
 
-// Walks this CTA's items, skipping those without rows.  The next item's lengths are requested one item
-// ahead: a load under a full memory pipe takes microseconds.
-struct Walker {
-    int it;
-    bool done;
-    Item x;
-    int pit, p_tok0, p_tok1, p_len;
+// Item `it` from its source's lengths; false where it has no rows.
+__device__ __forceinline__ bool make_item(const Args &a, int it, Item &x, uint32_t *err)
+{
+    const int tp = it % a.pairs_per_seq;
+    int rest = it / a.pairs_per_seq;
+    x.kvh = rest % a.kv_heads;
+    rest /= a.kv_heads;
+    x.split = rest % a.n_split;
+    x.s = rest / a.n_split;
+    x.tok0 = a.q_indptr[x.s];
+    const int n_tok = a.q_indptr[x.s + 1] - x.tok0;
+    int len = a.source_lens[x.s];
+    const int most = min(a.max_src, a.bt_stride * a.page_size);
+    if (len > most || n_tok > a.max_q_len) {
+        atomicOr(err, kErrContextRange);
+        len = min(len, most);
+    }
+    x.rows = min(n_tok, a.max_q_len) * a.group;
+    x.row_begin = tp * 2 * kM;
+    if (x.row_begin >= x.rows)
+        return false;
+    x.has_b = x.row_begin + kM < x.rows;
+    x.key0 = x.split * a.chunk;
+    x.n_keys = min(max(len - x.key0, 0), a.chunk);
+    x.n_blocks = (x.n_keys + kBN - 1) / kBN;
+    x.dual = !x.has_b && x.n_blocks > 1;
+    x.done = 0;
+    return true;
+}
 
-    __device__ __forceinline__ static int seq_of(const Args &a, int it)
+// A role's view of the items: each is read from shared memory by every warp that works on it.
+struct Feed {
+    Item x;
+    int n = 0;   // items read
+    // Waits for the next item; false if that takes too long.  `lanes`: of a whole warp, or one thread.
+    __device__ __forceinline__ bool wait(uint64_t *bars)
     {
-        return it / a.pairs_per_seq / a.kv_heads / a.n_split;
+        return mbar_wait(&bars[kBarItemFull], n & 1);
     }
-    __device__ __forceinline__ bool make(const Args &a, int tok0, int tok1, int len, uint32_t *err)
+    __device__ __forceinline__ void read(const Item *slot)
     {
-        x.tp = it % a.pairs_per_seq;
-        int rest = it / a.pairs_per_seq;
-        x.kvh = rest % a.kv_heads;
-        rest /= a.kv_heads;
-        x.split = rest % a.n_split;
-        x.s = rest / a.n_split;
-        const int most = min(a.max_src, a.bt_stride * a.page_size);
-        if (len > most || tok1 - tok0 > a.max_q_len) {
-            if (threadIdx.x == 0)
-                atomicOr(err, kErrContextRange);
-            len = min(len, most);
-        }
-        x.tok0 = tok0;
-        x.rows = min(tok1 - tok0, a.max_q_len) * a.group;
-        x.row_begin = x.tp * 2 * kM;
-        if (x.row_begin >= x.rows)
+        const int4 *from = reinterpret_cast<const int4 *>(slot);
+        int4 *to = reinterpret_cast<int4 *>(&x);
+        static_assert(sizeof(Item) == 48, "three words of 16 bytes");
+        to[0] = from[0];
+        to[1] = from[1];
+        to[2] = from[2];
+        ++n;
+    }
+    // The same for a warp.  False at the end, or if the wait ran out (then ok is false).
+    __device__ __forceinline__ bool next(uint64_t *bars, const Item *slot, bool &ok)
+    {
+        if (!__all_sync(0xffffffffu, wait(bars))) {
+            ok = false;
             return false;
-        x.has_b = x.row_begin + kM < x.rows;
-        x.key0 = x.split * a.chunk;
-        x.n_keys = min(max(len - x.key0, 0), a.chunk);
-        x.n_blocks = (x.n_keys + kBN - 1) / kBN;
-        x.dual = !x.has_b && x.n_blocks > 1;
-        return true;
-    }
-    __device__ __forceinline__ void prefetch(const Args &a, int idx)
-    {
-        pit = idx;
-        if (idx < a.num_items) {
-            const int s = seq_of(a, idx);
-            p_tok0 = a.q_indptr[s];
-            p_tok1 = a.q_indptr[s + 1];
-            p_len = a.source_lens[s];
         }
-    }
-    __device__ __forceinline__ void next(const Args &a, uint32_t *err)
-    {
-        for (;;) {
-            if (it > a.num_items - 1 - static_cast<int>(gridDim.x)) {
-                done = true;
-                return;
-            }
-            it += gridDim.x;
-            if (it != pit)
-                prefetch(a, it);
-            if (make(a, p_tok0, p_tok1, p_len, err))
-                break;
-        }
-        prefetch(a, it < a.num_items - static_cast<int>(gridDim.x) ? it + gridDim.x : a.num_items);
-    }
-    __device__ __forceinline__ void start(const Args &a, uint32_t *err)
-    {
-        it = static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x);
-        done = false;
-        pit = -1;
-        next(a, err);
+        read(slot);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            mbar_arrive(&bars[kBarItemEmpty]);
+        return !x.done;
     }
 };
 
@@ -201,7 +201,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     uint8_t *sStages = smem + G_::kOffStages;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + G_::kOffBar);
+    static_assert(kBarCount * 8 + 4 <= 384, "barriers");
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBarCount);
+    Item *item = reinterpret_cast<Item *>(smem + G_::kOffItem);
     auto q_tile = [&](int tile) { return smem + tile * G_::kQBytes; };
 
     const int warp = threadIdx.x >> 5;
@@ -211,7 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBarCount; ++i)
-            mbar_init(&bars[i], (i >= kBarPHalf && i < kBarPvDone) ? 4u : 1u);
+            mbar_init(&bars[i], (i >= kBarPHalf && i < kBarPvDone) ? 4u
+                                : i == kBarItemEmpty               ? static_cast<uint32_t>(kItemReaders)
+                                                                   : 1u);
         fence_mbar_init();
     }
     if (warp == 1)
@@ -232,10 +236,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // tiles past the first pair read the pages again: only pages read once may leave L2 early
         const uint64_t policy = a.pairs_per_seq > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-        Walker w;
+        Feed w;
         int n = 0;   // ring slots filled so far
-        for (w.start(a, err_word); ok && !w.done; w.next(a, err_word)) {
+        while (w.next(bars, item, ok)) {
             const Item &x = w.x;
+            if (!ok)
+                continue;   // a wait ran out: the rest of the items are only taken note of
             const int32_t *bt_row =
                 a.block_table + static_cast<size_t>(x.s) * a.bt_stride + x.key0 / P;
             const int n_pages = (x.n_keys + P - 1) / P;
@@ -270,8 +276,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      a.hnd ? 0 : page * (P / 8), a.hnd ? page * a.kv_heads + x.kvh : x.kvh,
                                      &bars[kBarKvFull + st], policy);
             }
-            if (!ok)
-                break;
         }
         if (!ok && lane == 0) {
             atomicOr(err_word, kErrCrossWait);
@@ -284,11 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------ query loads --------------------------------------
         if (lane == 0)
             prefetch_tensormap(&tmap_q);
-        Walker w;
+        Feed w;
         int qi[2] = {0, 0};   // items whose query tile t was requested
-        for (w.start(a, err_word); ok && !w.done; w.next(a, err_word)) {
+        while (w.next(bars, item, ok)) {
             const Item &x = w.x;
-            if (x.n_blocks == 0)
+            if (!ok || x.n_blocks == 0)
                 continue;
             // lane h loads column half h of the tile's 128 / G tokens x G heads, token-major
             for (int t = 0; t < (x.has_b ? 2 : 1); ++t) {
@@ -305,8 +309,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 x.tok0 + (x.row_begin + t * kM) / G, &bars[kBarQFull + t]);
                 ++qi[t];
             }
-            if (!ok)
-                break;
         }
         if (!ok && lane == 0) {
             atomicOr(err_word, kErrCrossWait);
@@ -353,15 +355,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         umma_bf16_ts(d, p + k * 8, db + k * kStep, kIdescPV, (!first || k > 0) ? 1u : 0u);
                 }
             };
-            Walker w;
+            Feed w;
             int n0 = 0;             // ring index of the item's first slot
             int qi[2] = {0, 0};     // items of tile 0 / tile 1
             int tb[2] = {0, 0};     // blocks of tile 0 / tile 1
-            for (w.start(a, err_word); ok && !w.done; w.next(a, err_word)) {
+            for (;;) {
+                if (!w.wait(bars)) {
+                    ok = false;
+                    break;
+                }
+                w.read(item);
+                mbar_arrive(&bars[kBarItemEmpty]);
                 const Item &x = w.x;
+                if (x.done)
+                    break;
                 const int nt = x.has_b ? 2 : 1;
                 const int nb = x.n_blocks;
-                if (nb == 0)
+                if (!ok || nb == 0)
                     continue;
                 const int last_cols = (x.n_keys - (nb - 1) * kBN + 15) & ~15;
                 // ring indices in the producer's fill order K(0), K(1), V(0), K(2), V(1), ...
@@ -401,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (!ok)
-                        break;
+                        continue;
                     ++qi[0];
                     n0 += 2 * nb;
                     continue;
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         umma_commit(&bars[kBarQEmpty + t]);
                 }
                 if (!ok)
-                    break;
+                    continue;
                 umma_commit(&bars[kBarKvEmpty + k_slot(0) % kStages]);
                 for (int b = 0; b < nb && ok; ++b) {
                     const bool last = b + 1 == nb;
@@ -453,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         umma_commit(&bars[kBarKvEmpty + kn % kStages]);
                 }
                 if (!ok)
-                    break;
+                    continue;
                 for (int t = 0; t < nt; ++t)
                     ++qi[t];
                 n0 += 2 * nb;
@@ -466,6 +476,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 atomicOr(err_word, kErrDrainWait);
         }
         __syncwarp();
+    } else if (elect_one()) {
+        // ------------------------------ items --------------------------------------------
+        // The grid has a block for every item.  This one's own is the first; then it asks for blocks that
+        // have not started, and takes their items in their place, until none is left: items are of very
+        // different lengths (a static deal of them left SMs idle for a fifth of the time).
+        const uint32_t answer = smem_addr(smem + G_::kOffAnswer);
+        int it = blockIdx.x;
+        int published = 0, asked = 0;
+        bool more = true;
+        while (more) {
+            Item x;
+            if (make_item(a, it, x, err_word)) {
+                if (published > 0 && !mbar_wait_long(&bars[kBarItemEmpty], (published - 1) & 1))
+                    break;
+                *item = x;
+                mbar_arrive(&bars[kBarItemFull]);
+                ++published;
+            }
+            more = false;
+            mbar_arrive_expect_tx(&bars[kBarCancel], 16);
+            try_cancel_block(answer, &bars[kBarCancel]);
+            if (!mbar_wait(&bars[kBarCancel], asked & 1)) {
+                atomicOr(err_word, kErrCrossWait);
+                break;
+            }
+            ++asked;
+            more = cancelled_block(answer, it);
+            fence_proxy_async_smem();
+        }
+        if (published > 0 && !mbar_wait_long(&bars[kBarItemEmpty], (published - 1) & 1))
+            atomicOr(err_word, kErrCrossWait);
+        item->done = 1;
+        mbar_arrive(&bars[kBarItemFull]);
     }
     } else {
         // ------------------------------ softmax + epilogue -------------------------------
@@ -491,11 +534,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok)
                 ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
         };
-        Walker w;
+        Feed w;
         int tb = 0;   // blocks of this tile so far
         int ti = 0;   // items of this tile so far
         int n0 = 0;   // ring index of the item's first slot
-        for (w.start(a, err_word); !w.done; n0 += 2 * w.x.n_blocks, w.next(a, err_word)) {
+        for (;; n0 += 2 * w.x.n_blocks) {
+            bool got = true;
+            const bool going = w.next(bars, item, got);
+            // all softmax warps go on or none: they meet at named barriers
+            if (barrier_or(kAllSoftmax, kSoftmaxWarps * 32, !got)) {
+                ok = false;
+                break;
+            }
+            if (!going)
+                break;
             const Item &x = w.x;
             if (t == 1 && !x.has_b && !x.dual)
                 continue;
@@ -805,9 +857,8 @@ cudaError_t launch_t(const CrossLaunch &l, const CUtensorMap &tq, const CUtensor
                                static_cast<int>(smem));
     if (err != cudaSuccess)
         return err;
-    const int sms = current_sm_count();
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kThreads), smem,
-                      stream, tq, tk, tv, a);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(kThreads), smem, stream, tq, tk, tv,
+                      a);
 }
 
 }  // namespace

@@ -126,6 +126,42 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity)
     return true;
 }
 
+// The same for waits that are as long as another warp's work item may be: gives up after 64 times as long.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity)
+{
+    for (int i = 0; i < 64; ++i)
+        if (mbar_wait(bar, parity))
+            return true;
+    return false;
+}
+
+// Asks for a block of this grid that has not started (cluster launch control): the answer, 16 bytes of shared
+// memory, lands on `bar`.  Not to be asked again after an answer that was none.
+__device__ __forceinline__ void try_cancel_block(uint32_t answer, uint64_t *bar)
+{
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            answer),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Whether the answer is a block, which then will not start; x: its index.
+__device__ __forceinline__ bool cancelled_block(uint32_t answer, int &x)
+{
+    uint32_t yes, ix;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\tld.shared.b128 a, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\tselp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+        : "=r"(yes), "=r"(ix)
+        : "r"(answer)
+        : "memory");
+    x = static_cast<int>(ix);
+    return yes != 0;
+}
+
 // Whether a wait that the whole warp is in, and that began at `since` (each lane's own clock), has taken
 // longer than kWaitLimitCycles: the same answer in every lane, so that none goes on alone into a vote or
 // shuffle of all of them.
