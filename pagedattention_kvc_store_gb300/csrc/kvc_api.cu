@@ -2101,8 +2101,9 @@ struct CrossPlan {
     size_t ws_bytes, lse_offset;
 };
 
-// Few rows: kvc_decode's chunks.  Otherwise chunks of a multiple of the kernel's block; by default as many as
-// give every SM several work items (pairs of row tiles of one source, kv head and chunk).
+// Few rows: kvc_decode's chunks.  Otherwise chunks of a multiple of the kernel's block; by default one where
+// there are several work items (pairs of row tiles of one source and kv head) to an SM, else as many as
+// make 8 (8 sources of 32k-131k positions x 8 kv heads: 10 chunks 545 us, 16 468, 32 479, 64 537).
 kvc_status make_cross_plan(int32_t num_sources, int32_t num_tokens, int32_t q_heads,
                            const kvc_pool_desc &pool, int32_t max_q_len, int32_t max_src,
                            int32_t requested, CrossPlan *out)
@@ -2127,15 +2128,20 @@ kvc_status make_cross_plan(int32_t num_sources, int32_t num_tokens, int32_t q_he
     if (few) {
         chunk = make_plan(num_sources, q_heads, pool, max_src, requested).chunk;
     } else {
-        int64_t want = requested;
+        // By default several items to an SM where they are fewer, but no chunk so short that its partial rows
+        // (fp32, written and read again) weigh as much as its keys: 8 positions a row where half the SMs
+        // would have nothing else, 16 otherwise.  256 rows an item: 64 items of 2,048 positions 50 us, cut in
+        // two 51, in four 63; 512 items of up to 3,000 159, 189 and 233.
+        int64_t want = requested, least = block;
         if (requested == 0) {
             const int64_t pairs = ceil_div(std::max<int64_t>(1, rows_each), 256);
             const int64_t units = pairs * pool.kv_heads * std::max(num_sources, 1);
-            want = ceil_div(4 * static_cast<int64_t>(device_sm_count()), units);
+            const int64_t sms = device_sm_count();
+            want = units < 4 * sms ? ceil_div(8 * sms, units) : 1;
+            least = std::max<int64_t>(512, (2 * units < sms ? 8 : 16) * std::min<int64_t>(rows_each, 256));
         }
-        chunk = round_up(ceil_div(src, want), block);
-        if (requested == 0)
-            chunk = std::max<int64_t>(chunk, std::min<int64_t>(512, round_up(src, block)));
+        chunk = std::max(round_up(ceil_div(src, want), block),
+                         std::min(round_up(least, block), round_up(src, block)));
     }
     CrossPlan p{};
     p.few = few;
