@@ -778,30 +778,40 @@ __global__ void __launch_bounds__(128)
     if (tok < q_indptr[0] || tok >= q_indptr[num_sources])   // rows of no source: left as they were
         return;
     const float *lse = part_lse + row * n_split;
-    float M = -INFINITY;
-    bool nan = false;
-    for (int j = lane; j < n_split; j += 32) {
-        const float v = lse[j];
-        nan |= isnan(v);
-        M = fmaxf(M, v);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    nan = __any_sync(0xffffffffu, nan);
     constexpr int E = D / 32;
     float acc[E] = {};
-    float total = 0.0f;
+    float total = 0.0f, M = -INFINITY;
+    bool nan = false;
     const float *o = part_o + row * n_split * D + lane * E;
-    for (int j = 0; j < n_split; ++j) {
-        const float v = lse[j];
-        if (v == -INFINITY)
-            continue;
-        const float w = expf(v - M);
-        total += w;
+    // four splits at a time, their rows loaded with their log-sum-exps (an empty one's row is any memory of the
+    // workspace, and is not used)
+    for (int j0 = 0; j0 < n_split; j0 += 4) {
+        float v[4], x[4][E];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = j0 + j < n_split ? lse[j0 + j] : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[j][e] = j0 + j < n_split ? o[static_cast<size_t>(j0 + j) * D + e] : 0.0f;
+        }
+        const float m = fmaxf(fmaxf(M, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
+        nan |= isnan(v[0]) || isnan(v[1]) || isnan(v[2]) || isnan(v[3]);
+        const float keep = M == -INFINITY ? 0.0f : expf(M - m);
+        total *= keep;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            acc[e] += w * o[static_cast<size_t>(j) * D + e];
+            acc[e] *= keep;
+        M = m;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (v[j] == -INFINITY)
+                continue;
+            const float w = expf(v[j] - M);
+            total += w;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] += w * x[j][e];
+        }
     }
     const float inv = nan ? NAN : (total > 0.0f ? 1.0f / total : 0.0f);
     const size_t idx = static_cast<size_t>(row) * D + lane * E;

@@ -32,6 +32,13 @@ __device__ uint32_t g_pages_errors;
 
 constexpr int kThreads = 256;
 constexpr int kRowThreads = 1024;
+constexpr int kClusterBlocks = 8;
+
+// All threads of the cluster; what they wrote before is seen after.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 constexpr int kPageSegment = 4096;   // pages that a block looks at
 constexpr int kMaxCopyArrays = 128;  // arrays of one launch (its parameters are limited)
@@ -150,11 +157,13 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const Table t, int32_t *
         out_lens[s] = n;
 }
 
-// Pages src[i] -> dst[i] of every array, i < n.  No page is both a source and a destination.
+// Pages src[i] -> dst[i] of every array, i < n, by all blocks of N threads.  No page is both a source and a
+// destination.
+template <int N>
 __device__ __forceinline__ void copy_listed(const CopyArrays &arrays, const int32_t *src, const int32_t *dst,
                                             int n)
 {
-    constexpr int kLoads = kPieceChunks / kThreads;
+    constexpr int kLoads = kPieceChunks / N;
     const long long per_page = static_cast<long long>(arrays.num) * arrays.pieces;
     for (long long u = blockIdx.x; u < n * per_page; u += gridDim.x) {
         const int i = static_cast<int>(u / per_page);
@@ -163,17 +172,17 @@ __device__ __forceinline__ void copy_listed(const CopyArrays &arrays, const int3
         const unsigned c0 = (rest - array * arrays.pieces) * kPieceChunks + threadIdx.x;
         const size_t chunks = arrays.chunks[array];
         uint4 *data = reinterpret_cast<uint4 *>(arrays.data[array]);
-        const uint4 *from = data + src[i] * chunks;
-        uint4 *to = data + dst[i] * chunks;
+        const uint4 *from = data + __ldcg(src + i) * chunks;
+        uint4 *to = data + __ldcg(dst + i) * chunks;
         uint4 x[kLoads];
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
-            if (c0 + j * kThreads < chunks)
-                x[j] = __ldcs(from + c0 + j * kThreads);
+            if (c0 + j * N < chunks)
+                x[j] = __ldcs(from + c0 + j * N);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
-            if (c0 + j * kThreads < chunks)
-                to[c0 + j * kThreads] = x[j];
+            if (c0 + j * N < chunks)
+                to[c0 + j * N] = x[j];
     }
 }
 
@@ -376,6 +385,194 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     }
 }
 
+// Up to kOneBlockPages pages looked at by one block at once, a bit for each: all loads are on their way
+// together, and one scan gives every word the number of set bits before it.
+constexpr int kOneBlockPages = 16384;
+constexpr int kPageWords = kOneBlockPages / 32;
+
+struct PageBits {
+    unsigned word[kPageWords];
+    int before[kPageWords];
+
+    // Bits of the pages that are used (or free); by all threads, which need a barrier before count().
+    __device__ __forceinline__ void load(const int32_t *refs, int num_pages, bool used)
+    {
+        constexpr int kEach = kOneBlockPages / kRowThreads;
+        int32_t n[kEach];
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int p = j * kRowThreads + threadIdx.x;
+            n[j] = p < num_pages ? refs[p] : (used ? 0 : 1);
+        }
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const unsigned bits = __ballot_sync(0xffffffffu, (n[j] > 0) == used);
+            if ((threadIdx.x & 31) == 0)
+                word[(j * kRowThreads + threadIdx.x) / 32] = bits;
+        }
+    }
+    // Of all pages, and the numbers before each word.
+    __device__ __forceinline__ int count(long long *red)
+    {
+        const int i = threadIdx.x;
+        long long total;
+        const long long n = scan_exclusive<kRowThreads>(i < kPageWords ? __popc(word[i]) : 0, red, &total);
+        if (i < kPageWords)
+            before[i] = static_cast<int>(n);
+        __syncthreads();
+        return static_cast<int>(total);
+    }
+    __device__ __forceinline__ bool has(int p) const { return (word[p >> 5] >> (p & 31) & 1) != 0; }
+    // How many are below page p.
+    __device__ __forceinline__ int below(int p) const
+    {
+        return p >= kOneBlockPages ? before[kPageWords - 1] + __popc(word[kPageWords - 1])
+                                   : before[p >> 5] + __popc(word[p >> 5] & ((1u << (p & 31)) - 1));
+    }
+};
+
+// The whole of it but the copies by one block, for at most kRowThreads rows and kOneBlockPages pages: a thread a
+// row, the sharers of a page counted in a hash table in shared memory.
+constexpr int kHashSlots = 2 * kRowThreads;
+
+struct DecideShared {
+    long long red[32];
+    int start[kRowThreads], len[kRowThreads], copy_at[kRowThreads];
+    PageBits free_pages;
+    union {
+        struct {
+            int key[kHashSlots], sharers[kHashSlots], last_row[kHashSlots];
+        };
+        uint16_t page[kHashSlots * 6];   // the free pages in order, up to as many (the hash table is done with)
+    };
+};
+static_assert(sizeof(DecideShared) <= 48 * 1024, "shared memory");
+constexpr int kListed = kHashSlots * 6;
+
+__device__ void reserve_decide(const Table &t, const int32_t *new_tokens, const ReserveSpace &w,
+                               int32_t *missing, uint32_t *err, DecideShared &sh)
+{
+    const int s = threadIdx.x;
+    const bool row = s < t.num_seqs;
+    for (int i = s; i < kHashSlots; i += kRowThreads) {
+        sh.key[i] = -1;
+        sh.sharers[i] = 0;
+        sh.last_row[i] = -1;
+    }
+    sh.free_pages.load(t.refs, t.num_pages, false);
+    int len = 0, grow = 0, last = -1, refs = 0;
+    if (row) {
+        row_wants(t, new_tokens, s, true, err, &len, &grow, &last);
+        if (last >= 0)
+            refs = t.refs[last];
+    }
+    __syncthreads();
+    int slot = 0;
+    if (last >= 0) {
+        slot = static_cast<int>((static_cast<unsigned>(last) * 2654435761u) >> 16) % kHashSlots;
+        for (;;) {   // ends: half of the slots stay empty
+            const int held = atomicCAS(&sh.key[slot], -1, last);
+            if (held == -1 || held == last)
+                break;
+            slot = (slot + 1) % kHashSlots;
+        }
+        atomicAdd(&sh.sharers[slot], 1);
+        atomicMax(&sh.last_row[slot], s);
+    }
+    __syncthreads();
+    int copy = 0;
+    if (last >= 0) {
+        if (sh.sharers[slot] > refs)   // more rows list the page than are counted
+            atomicOr(err, kErrPageRefs);
+        copy = !(sh.sharers[slot] >= refs && sh.last_row[slot] == s);
+    }
+    const int need = row ? copy + pages_of(len + grow, t.page_size) - pages_of(len, t.page_size) : 0;
+    // both sums in one: copies above bit 48, pages below (less than 2^10 rows of at most 2^30)
+    long long totals;
+    const long long both =
+        scan_exclusive<kRowThreads>((static_cast<long long>(copy) << 48) + need, sh.red, &totals);
+    constexpr long long kLow = (1LL << 48) - 1;
+    const long long needed = totals & kLow, start = both & kLow;
+    const int at = static_cast<int>(both >> 48);
+    const int there = sh.free_pages.count(sh.red);
+    const bool fits = needed <= there;
+    if (row) {
+        sh.start[s] = static_cast<int>(min(start, static_cast<long long>(0x7FFFFFFF)));
+        sh.len[s] = len;
+        sh.copy_at[s] = copy ? at : -1;
+    }
+    if (s == 0) {
+        *w.copies = fits ? static_cast<int>(totals >> 48) : 0;
+        *missing = fits ? 0 : static_cast<int>(min(needed - there, static_cast<long long>(0x7FFFFFFF)));
+    }
+    __syncthreads();
+    if (!fits)
+        return;
+    for (long long first = 0; first < needed; first += kListed) {
+        // pages of rank first .. first + kListed - 1
+        for (int p = s; p < t.num_pages; p += kRowThreads) {
+            const int r = sh.free_pages.below(p);
+            if (sh.free_pages.has(p) && r >= first && r < first + kListed)
+                sh.page[r - first] = static_cast<uint16_t>(p);
+        }
+        __syncthreads();
+        const int n = static_cast<int>(min(needed - first, static_cast<long long>(kListed)));
+        for (int i = s; i < n; i += kRowThreads) {
+            const int r = static_cast<int>(first) + i, p = sh.page[i];
+            int lo = 0, hi = t.num_seqs - 1;   // the last row that starts at or below r
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (sh.start[mid] <= r)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int j = r - sh.start[lo];
+            const int c = sh.copy_at[lo];
+            int entry = pages_of(sh.len[lo], t.page_size) + j - (c >= 0);
+            if (c >= 0 && j == 0) {
+                entry = sh.len[lo] / t.page_size;
+                w.copy_dst[c] = p;
+            }
+            t.rows[static_cast<size_t>(lo) * t.stride + entry] = p;
+            t.refs[p] = 1;
+        }
+        __syncthreads();
+    }
+    if (row) {
+        t.lens[s] = t.lens[s] + grow;
+        if (copy) {
+            w.copy_src[at] = last;
+            atomicSub(t.refs + last, 1);
+        }
+    }
+}
+
+// The decision and the copies in one launch: a cluster, whose first block decides.  For copies that eight SMs
+// make as fast as a second launch would start.
+__global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kRowThreads, 1)
+    reserve_cluster_kernel(const Table t, const int32_t *new_tokens, ReserveSpace w, int32_t *missing,
+                           const CopyArrays arrays, uint32_t *word)
+{
+    pdl_wait();
+    pdl_trigger();
+    __shared__ DecideShared sh;
+    if (blockIdx.x == 0)
+        reserve_decide(t, new_tokens, w, missing, word ? word : &g_pages_errors, sh);
+    cluster_sync();
+    copy_listed<kRowThreads>(arrays, w.copy_src, w.copy_dst, __ldcg(w.copies));
+}
+
+__global__ void __launch_bounds__(kRowThreads, 1)
+    reserve_decide_kernel(const Table t, const int32_t *new_tokens, ReserveSpace w, int32_t *missing,
+                          uint32_t *word)
+{
+    pdl_wait();
+    pdl_trigger();
+    __shared__ DecideShared sh;
+    reserve_decide(t, new_tokens, w, missing, word ? word : &g_pages_errors, sh);
+}
+
 // The rows' lengths and the copied pages' counts, once every block of the assignment has read them, and
 // the copies.
 __global__ void __launch_bounds__(kThreads)
@@ -391,7 +588,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = i0; i < copies; i += step)
             atomicSub(t.refs + w.copy_src[i], 1);
     }
-    copy_listed(arrays, w.copy_src, w.copy_dst, copies);
+    copy_listed<kThreads>(arrays, w.copy_src, w.copy_dst, copies);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -409,7 +606,37 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         w.seg_counts[blockIdx.x] = n;
 }
 
-// A page that moves is marked -2 - i in the map, i its place in the list of moves.
+// Where page p goes, `rank` used ones lying below it: those below the border (the number in use) stay, `stay`
+// of them in all.  A page that moves is marked -2 - i, i its place in the list of moves.
+__device__ __forceinline__ void map_page(int p, bool used, int rank, int border, int stay,
+                                         const CompactSpace &w, int32_t *page_map)
+{
+    int to = used ? p : -1;
+    if (used && p >= border) {
+        const int i = rank - stay;
+        w.copy_src[i] = p;
+        to = -2 - i;
+    } else if (!used && p < border) {
+        w.copy_dst[p - rank] = p;
+    }
+    page_map[p] = to;
+}
+
+// The same for pages begin .. end - 1, `before` used ones lying below them.
+__device__ __forceinline__ void map_pages(const int32_t *refs, int begin, int end, long long before, int border,
+                                          int stay, const CompactSpace &w, int32_t *page_map, long long *red)
+{
+    for (int p0 = begin; p0 < end; p0 += kRowThreads) {
+        const int p = p0 + threadIdx.x;
+        const bool used = p < end && refs[p] > 0;
+        long long total;
+        const int rank = static_cast<int>(before + scan_exclusive<kRowThreads>(used, red, &total));
+        before += total;
+        if (p < end)
+            map_page(p, used, rank, border, stay, w, page_map);
+    }
+}
+
 __global__ void __launch_bounds__(kRowThreads, 1)
     compact_map_kernel(const int32_t *refs, int num_pages, CompactSpace w, int segments, int32_t *page_map,
                        int32_t *num_live)
@@ -444,42 +671,39 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         *num_live = border;
         *w.copies = static_cast<int>(live - stay);
     }
-    const int begin = seg * kPageSegment, end = min(begin + kPageSegment, num_pages);
-    for (int p0 = begin; p0 < end; p0 += kRowThreads) {
-        const int p = p0 + threadIdx.x;
-        const bool used = p < end && refs[p] > 0;
-        long long total;
-        const int rank = static_cast<int>(before + scan_exclusive<kRowThreads>(used, red, &total));
-        before += total;
-        if (p >= end)
-            continue;
-        int to = used ? p : -1;
-        if (used && p >= border) {
-            const int i = rank - static_cast<int>(stay);
-            w.copy_src[i] = p;
-            to = -2 - i;
-        } else if (!used && p < border) {
-            w.copy_dst[p - rank] = p;
-        }
-        page_map[p] = to;
-    }
+    const int begin = seg * kPageSegment;
+    map_pages(refs, begin, min(begin + kPageSegment, num_pages), before, border, static_cast<int>(stay), w,
+              page_map, red);
 }
 
-// The tables, the counts and the map follow the moves, and the copies.  A table entry reads a mark or what
-// has already replaced it: the same page either way.
-__global__ void __launch_bounds__(kThreads)
-    compact_finish_kernel(const Table t, CompactSpace w, int32_t *page_map, const CopyArrays arrays,
-                          uint32_t *word)
+// The map by one block, for at most kOneBlockPages pages.
+__device__ void compact_decide(const int32_t *refs, int num_pages, const CompactSpace &w, int32_t *page_map,
+                               int32_t *num_live, long long *red, PageBits &used)
 {
-    pdl_wait();
-    pdl_trigger();
-    uint32_t *err = word ? word : &g_pages_errors;
-    const int moves = *w.copies;
+    used.load(refs, num_pages, true);
+    __syncthreads();
+    const int border = used.count(red);
+    const int stay = used.below(border);
+    if (threadIdx.x == 0) {
+        *num_live = border;
+        *w.copies = border - stay;
+    }
+    for (int p = threadIdx.x; p < num_pages; p += kRowThreads)
+        map_page(p, used.has(p), used.below(p), border, stay, w, page_map);
+}
+
+// The tables, the counts and the map follow the moves, and the copies, by all blocks of N threads.  A table
+// entry reads a mark or what has already replaced it: the same page either way.
+template <int N>
+__device__ __forceinline__ void compact_finish(const Table &t, const CompactSpace &w, int32_t *page_map,
+                                               const CopyArrays &arrays, uint32_t *err)
+{
+    const int moves = __ldcg(w.copies);
     for (int s = blockIdx.x; s < t.num_seqs; s += gridDim.x) {
         const int n = row_len(t.lens, s, t.stride, t.page_size, threadIdx.x == 0, err);
         int32_t *row = t.rows + static_cast<size_t>(s) * t.stride;
         const int end = pages_of(n, t.page_size);
-        for (int i = threadIdx.x; i < end; i += kThreads) {
+        for (int i = threadIdx.x; i < end; i += N) {
             const int page = row[i];
             if (page < 0 || page >= t.num_pages) {
                 atomicOr(err, kErrPageRange);
@@ -489,16 +713,50 @@ __global__ void __launch_bounds__(kThreads)
             if (to == -1)
                 atomicOr(err, kErrPageRefs);   // a page that nothing counts: left as it is
             else if (to != page)
-                row[i] = to >= 0 ? to : w.copy_dst[-2 - to];
+                row[i] = to >= 0 ? to : __ldcg(w.copy_dst + (-2 - to));
         }
     }
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < moves; i += gridDim.x * kThreads) {
-        const int src = w.copy_src[i], dst = w.copy_dst[i];
+    for (int i = blockIdx.x * N + threadIdx.x; i < moves; i += gridDim.x * N) {
+        const int src = __ldcg(w.copy_src + i), dst = __ldcg(w.copy_dst + i);
         t.refs[dst] = t.refs[src];
         t.refs[src] = 0;
         page_map[src] = dst;
     }
-    copy_listed(arrays, w.copy_src, w.copy_dst, moves);
+    copy_listed<N>(arrays, w.copy_src, w.copy_dst, moves);
+}
+
+__global__ void __launch_bounds__(kThreads)
+    compact_finish_kernel(const Table t, CompactSpace w, int32_t *page_map, const CopyArrays arrays,
+                          uint32_t *word)
+{
+    pdl_wait();
+    pdl_trigger();
+    compact_finish<kThreads>(t, w, page_map, arrays, word ? word : &g_pages_errors);
+}
+
+__global__ void __launch_bounds__(kRowThreads, 1)
+    compact_decide_kernel(const int32_t *refs, int num_pages, CompactSpace w, int32_t *page_map,
+                          int32_t *num_live)
+{
+    pdl_wait();
+    pdl_trigger();
+    __shared__ long long red[32];
+    __shared__ PageBits used;
+    compact_decide(refs, num_pages, w, page_map, num_live, red, used);
+}
+
+__global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kRowThreads, 1)
+    compact_cluster_kernel(const Table t, CompactSpace w, int32_t *page_map, int32_t *num_live,
+                           const CopyArrays arrays, uint32_t *word)
+{
+    pdl_wait();
+    pdl_trigger();
+    __shared__ long long red[32];
+    __shared__ PageBits used;
+    if (blockIdx.x == 0)
+        compact_decide(t.refs, t.num_pages, w, page_map, num_live, red, used);
+    cluster_sync();
+    compact_finish<kRowThreads>(t, w, page_map, arrays, word ? word : &g_pages_errors);
 }
 
 // More arrays than one launch takes.
@@ -507,7 +765,7 @@ __global__ void __launch_bounds__(kThreads)
 {
     pdl_wait();
     pdl_trigger();
-    copy_listed(arrays, src, dst, *count);
+    copy_listed<kThreads>(arrays, src, dst, *count);
 }
 
 int segments_of(int num_pages) { return (num_pages + kPageSegment - 1) / kPageSegment; }
@@ -547,6 +805,18 @@ unsigned copy_blocks(const CopyArrays &c, long long most, long long other)
     const long long cap = static_cast<long long>(current_sm_count()) * 8;
     return static_cast<unsigned>(std::max<long long>(1, std::min(work, cap)));
 }
+
+// Bytes of a page in all arrays.
+long long page_bytes(const PagesLaunch &l)
+{
+    long long n = 0;
+    for (int i = 0; i < l.num_arrays; ++i)
+        n += l.arrays[i].page_bytes;
+    return n;
+}
+
+// Copies of at most this much are left to a cluster of eight SMs (which move about 1 TB/s).
+constexpr long long kClusterBytes = 4LL << 20;
 
 cudaError_t copy_the_rest(const PagesLaunch &l, const int32_t *src, const int32_t *dst,
                           const int32_t *count, long long most, cudaStream_t stream)
@@ -642,19 +912,34 @@ cudaError_t launch_reserve(const PagesLaunch &l, const int32_t *new_tokens, int3
     size_t bytes;
     const ReserveSpace w = reserve_space(workspace, l.num_seqs, l.num_pages, &bytes);
     const Table t = table_of(l);
-    const int segments = segments_of(l.num_pages);
-    cudaError_t err = launch_pdl(reserve_count_kernel, dim3(segments + 1), dim3(kRowThreads), 0, stream, t,
-                                 new_tokens, w, current_error_word());
-    if (err != cudaSuccess)
-        return err;
-    err = launch_pdl(reserve_assign_kernel, dim3(segments), dim3(kRowThreads), 0, stream, t, w, segments,
-                     missing);
-    if (err != cudaSuccess)
-        return err;
     const CopyArrays c = some_arrays(l, 0);
-    err = launch_pdl(reserve_finish_kernel,
-                     dim3(copy_blocks(c, l.num_seqs, (l.num_seqs + kThreads - 1) / kThreads)),
-                     dim3(kThreads), 0, stream, t, w, static_cast<const int32_t *>(missing), c);
+    const bool one_block = l.num_seqs <= kRowThreads && l.num_pages <= kOneBlockPages;
+    if (one_block && page_bytes(l) * l.num_seqs <= kClusterBytes && l.num_arrays <= kMaxCopyArrays)
+        return launch_pdl(reserve_cluster_kernel, dim3(kClusterBlocks), dim3(kRowThreads), 0, stream, t,
+                          new_tokens, w, missing, c, current_error_word());
+    cudaError_t err;
+    if (one_block) {
+        err = launch_pdl(reserve_decide_kernel, dim3(1), dim3(kRowThreads), 0, stream, t, new_tokens, w,
+                         missing, current_error_word());
+        if (err == cudaSuccess && l.num_arrays > 0)
+            err = launch_pdl(copy_listed_kernel, dim3(copy_blocks(c, l.num_seqs, 1)), dim3(kThreads), 0,
+                             stream, c, static_cast<const int32_t *>(w.copy_src),
+                             static_cast<const int32_t *>(w.copy_dst),
+                             static_cast<const int32_t *>(w.copies));
+    } else {
+        const int segments = segments_of(l.num_pages);
+        err = launch_pdl(reserve_count_kernel, dim3(segments + 1), dim3(kRowThreads), 0, stream, t,
+                         new_tokens, w, current_error_word());
+        if (err != cudaSuccess)
+            return err;
+        err = launch_pdl(reserve_assign_kernel, dim3(segments), dim3(kRowThreads), 0, stream, t, w,
+                         segments, missing);
+        if (err != cudaSuccess)
+            return err;
+        err = launch_pdl(reserve_finish_kernel,
+                         dim3(copy_blocks(c, l.num_seqs, (l.num_seqs + kThreads - 1) / kThreads)),
+                         dim3(kThreads), 0, stream, t, w, static_cast<const int32_t *>(missing), c);
+    }
     return err != cudaSuccess ? err : copy_the_rest(l, w.copy_src, w.copy_dst, w.copies, l.num_seqs, stream);
 }
 
@@ -664,16 +949,27 @@ cudaError_t launch_compact(const PagesLaunch &l, int32_t *page_map, int32_t *num
     size_t bytes;
     const CompactSpace w = compact_space(workspace, l.num_pages, &bytes);
     const Table t = table_of(l);
-    const int segments = segments_of(l.num_pages);
-    cudaError_t err = launch_pdl(compact_count_kernel, dim3(segments), dim3(kRowThreads), 0, stream,
-                                 static_cast<const int32_t *>(t.refs), t.num_pages, w);
-    if (err != cudaSuccess)
-        return err;
-    err = launch_pdl(compact_map_kernel, dim3(segments), dim3(kRowThreads), 0, stream,
-                     static_cast<const int32_t *>(t.refs), t.num_pages, w, segments, page_map, num_live);
-    if (err != cudaSuccess)
-        return err;
     const CopyArrays c = some_arrays(l, 0);
+    const bool one_block = l.num_pages <= kOneBlockPages;
+    if (one_block && page_bytes(l) * (l.num_pages / 2) <= kClusterBytes && l.num_arrays <= kMaxCopyArrays &&
+        l.num_seqs <= kRowThreads)
+        return launch_pdl(compact_cluster_kernel, dim3(kClusterBlocks), dim3(kRowThreads), 0, stream, t, w,
+                          page_map, num_live, c, current_error_word());
+    cudaError_t err;
+    if (one_block) {
+        err = launch_pdl(compact_decide_kernel, dim3(1), dim3(kRowThreads), 0, stream,
+                         static_cast<const int32_t *>(t.refs), t.num_pages, w, page_map, num_live);
+    } else {
+        const int segments = segments_of(l.num_pages);
+        err = launch_pdl(compact_count_kernel, dim3(segments), dim3(kRowThreads), 0, stream,
+                         static_cast<const int32_t *>(t.refs), t.num_pages, w);
+        if (err != cudaSuccess)
+            return err;
+        err = launch_pdl(compact_map_kernel, dim3(segments), dim3(kRowThreads), 0, stream,
+                         static_cast<const int32_t *>(t.refs), t.num_pages, w, segments, page_map, num_live);
+    }
+    if (err != cudaSuccess)
+        return err;
     err = launch_pdl(compact_finish_kernel, dim3(copy_blocks(c, l.num_pages / 2, l.num_seqs)),
                      dim3(kThreads), 0, stream, t, w, page_map, c, current_error_word());
     return err != cudaSuccess ? err

@@ -143,6 +143,17 @@ def test_more_rows_than_a_block_and_more_pages_than_a_segment():
     d.reserve(new, rng.integers(0, 40, 1100))
 
 
+def test_most_of_a_pool_at_once():
+    """More new pages than one block lists at a time, in the largest pool that one block takes and the next."""
+    for pages in (16384, 16385):
+        d = Device(pages, 2, width=80, arrays=((16,),))
+        t = d.empty(200)
+        assert d.reserve(t, np.full(200, 140)) == 0
+        assert d.reserve(t, np.full(200, 40)) == 200 * 20 - (pages - 14000)
+        d.truncate(t, np.arange(200) % 3)
+        d.compact(t)
+
+
 def test_more_arrays_than_a_launch_takes():
     d = Device(30, 4, width=8, arrays=[(16 * (1 + i % 3),) for i in range(131)] + [(40000,)])
     t = d.empty(3)
@@ -151,6 +162,30 @@ def test_more_arrays_than_a_launch_takes():
     d.reserve(new, None)
     d.truncate(t, None)
     d.compact(new)
+
+
+@pytest.mark.parametrize("pages,page_bytes", [(60, 400000), (60, 48), (17000, 48)])
+def test_large_and_small_copies(pages, page_bytes):
+    """Copies that are left to the deciding launch, that have one of their own, and a pool past one block's."""
+    rng = np.random.default_rng(pages)
+    d = Device(pages, 4, width=8, arrays=((page_bytes,), (16,)))
+    t = d.empty(12)
+    d.reserve(t, rng.integers(1, 10, 12))
+    new = d.fork(t, rng.integers(0, 12, 12))
+    d.reserve(new, rng.integers(0, 4, 12))
+    d.truncate(t, None)
+    d.compact(new)
+    d.reserve(new, None)
+
+
+@pytest.mark.parametrize("rows", [1023, 1024, 1025])
+def test_row_counts_about_a_block(rows):
+    d = Device(4000, 2, width=4, arrays=((16,),))
+    t = d.empty(rows)
+    d.reserve(t, np.arange(rows) % 4)
+    new = d.fork(t, np.arange(rows) // 2)
+    d.truncate(t, np.zeros(rows, dtype=np.int64))
+    d.reserve(new, None)
 
 
 def test_no_arrays_and_no_rows():
