@@ -579,6 +579,12 @@ def rope_desc(inv_freq, axis=None, pairing: str = "halves",
 
 def _head_rows(name, t):
     """Checks of rows of heads [T, H, D] whose heads are contiguous; the stride between tokens."""
+    try:   # what nearly every call passes, with as few steps as say so
+        (T, H, D), (st, sh, sd) = t.shape, t.stride()
+        if t.is_cuda and t.dtype is torch.bfloat16 and sd == 1 and (sh == D or H == 1):
+            return st if T > 1 else H * D
+    except (AttributeError, ValueError):
+        pass
     _cuda(name, t, torch.bfloat16, contiguous=False)
     if t.dim() != 3:
         raise ValueError(f"{name} is [num_tokens, heads, head_dim]")
@@ -632,23 +638,34 @@ def kvc_rope_store(q_out: Optional[torch.Tensor], k_pool: torch.Tensor, v_pool: 
     slot_mapping's slots.  q, k_new and v_new as in kvc_rope; q None: no queries."""
     _cuda("k_pool", k_pool, torch.bfloat16)
     _cuda("v_pool", v_pool, torch.bfloat16)
-    pool = _pool_shapes(k_pool.shape, v_pool.shape, layout)
     _cuda("slot_mapping", slot_mapping, torch.int32)
     T = slot_mapping.numel()
     k_stride, v_stride = _head_rows("k_new", k_new), _head_rows("v_new", v_new)
-    _vector_shapes(k_new.shape, v_new.shape, pool.kv_heads, pool.head_dim, T)
-    q_heads, q_stride = 0, 0
+    q_heads, q_stride, q_ptr, q_out_ptr = 0, 0, None, None
+    q_shape = q_out_shape = None
     if q is not None:
-        q_stride, q_heads = _head_rows("q", q), q.shape[1]
+        q_stride, q_shape = _head_rows("q", q), q.shape
         _cuda("q_out", q_out, torch.bfloat16)
-        if q.shape[0] != T or q.shape[2] != pool.head_dim or q_out.shape != q.shape:
-            raise ValueError(f"q and q_out are [num_tokens, q_heads, head_dim] with {T} tokens and "
-                             f"head_dim {pool.head_dim}")
+        q_heads, q_out_shape = q_shape[1], q_out.shape
+        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
+    pool = _rope_shapes(k_pool.shape, v_pool.shape, layout, k_new.shape, v_new.shape, q_shape,
+                        q_out_shape, T)
     where = _positions(positions, rope, T)
     _check("kvc_rope_store", lib().kvc_rope_store(
-        _ptr(q_out) if q is not None else None, _ptr(k_pool), _ptr(v_pool), pool, _ptr(q), q_stride,
-        _ptr(k_new), k_stride, _ptr(v_new), v_stride, q_heads, rope, where, _ptr(slot_mapping), T,
+        q_out_ptr, k_pool.data_ptr(), v_pool.data_ptr(), pool, q_ptr, q_stride, k_new.data_ptr(),
+        k_stride, v_new.data_ptr(), v_stride, q_heads, rope, where, slot_mapping.data_ptr(), T,
         _stream(stream)))
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_shapes(k_pool, v_pool, layout, k_new, v_new, q, q_out, T):
+    """Shapes of kvc_rope_store's arguments; the pool's descriptor."""
+    pool = _pool_shapes(k_pool, v_pool, layout)
+    _vector_shapes(k_new, v_new, pool.kv_heads, pool.head_dim, T)
+    if q is not None and (q[0] != T or q[2] != pool.head_dim or q_out != q):
+        raise ValueError(f"q and q_out are [num_tokens, q_heads, head_dim] with {T} tokens and "
+                         f"head_dim {pool.head_dim}")
+    return pool
 
 
 class PageArrays:
@@ -673,11 +690,16 @@ def page_arrays(tensors) -> PageArrays:
 
 def _table(block_table, context_lens, page_refs, arrays=None):
     """Checks of a table, its lengths and the references; the number of sequences."""
-    _cuda("block_table", block_table, torch.int32)
-    _cuda("context_lens", context_lens, torch.int32)
-    _cuda("page_refs", page_refs, torch.int32)
-    S = context_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != S:
+    for name, t in (("block_table", block_table), ("context_lens", context_lens),
+                    ("page_refs", page_refs)):
+        try:
+            if t.is_cuda and t.dtype is torch.int32 and t.is_contiguous():
+                continue
+        except AttributeError:
+            pass
+        _cuda(name, t, torch.int32)
+    S, table = context_lens.numel(), block_table.shape
+    if len(table) != 2 or table[0] != S:
         raise ValueError("block_table is [num_seqs, pages]")
     if arrays is not None:
         if not isinstance(arrays, PageArrays):

@@ -146,7 +146,7 @@ def test_more_rows_than_a_block_and_more_pages_than_a_segment():
 def test_most_of_a_pool_at_once():
     """More new pages than one block lists at a time, in the largest pool that one block takes and the next."""
     for pages in (16384, 16385):
-        d = Device(pages, 2, width=80, arrays=((16,),))
+        d = Device(pages, 2, width=96, arrays=((16,),))
         t = d.empty(200)
         assert d.reserve(t, np.full(200, 140)) == 0
         assert d.reserve(t, np.full(200, 40)) == 200 * 20 - (pages - 14000)
