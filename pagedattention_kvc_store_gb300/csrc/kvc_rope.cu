@@ -58,6 +58,27 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int c0 = (ADJACENT || !turns) ? 2 * piece : piece;
     const int c1 = (ADJACENT || !turns) ? 2 * piece + 1 : piece + a.pairs;
 
+    const int heads = a.q_heads + a.kv_heads + a.v_heads;
+    uint4 x[kRows][2];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int h = h0 + u * lanes;
+            const uint8_t *src;
+            if (h < a.q_heads)
+                src = a.q + t * a.q_stride + h * (D * 2);
+            else if (h < a.q_heads + a.kv_heads)
+                src = a.k + t * a.k_stride + (h - a.q_heads) * (D * 2);
+            else
+                src = a.v + t * a.v_stride + (h - a.q_heads - a.kv_heads) * (D * 2);
+            if (h < heads) {
+                x[u][0] = __ldcs(reinterpret_cast<const uint4 *>(src) + c0);
+                x[u][1] = __ldcs(reinterpret_cast<const uint4 *>(src) + c1);
+            }
+        }
+    };
+    load(lane);   // on its way while the angles are made
+
     long long k_row = 0, k_head = D * 2;    // bytes: this token's first key row, and between heads
     bool store = true;
     if (STORE) {
@@ -87,42 +108,20 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         }
     }
 
-    const int heads = a.q_heads + a.kv_heads + a.v_heads;
-    for (int h0 = lane; h0 < heads; h0 += kRows * lanes) {
-        uint4 x[kRows][2];
-        uint8_t *dst[kRows];
-        bool rotate[kRows];
+    for (int h0 = lane;;) {
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
             const int h = h0 + u * lanes;
-            const uint8_t *src = nullptr;
-            dst[u] = nullptr;
-            rotate[u] = turns;
-            if (h < a.q_heads) {
-                src = a.q + t * a.q_stride + h * (D * 2);
-                dst[u] = a.q_out + t * a.q_out_stride + h * (D * 2);
-            } else if (h < a.q_heads + a.kv_heads) {
-                if (store) {
-                    src = a.k + t * a.k_stride + (h - a.q_heads) * (D * 2);
-                    dst[u] = a.k_out + k_row + (h - a.q_heads) * k_head;
-                }
-            } else if (h < heads) {
-                rotate[u] = false;
-                if (store) {
-                    src = a.v + t * a.v_stride + (h - a.q_heads - a.kv_heads) * (D * 2);
-                    dst[u] = a.v_out + k_row + (h - a.q_heads - a.kv_heads) * k_head;
-                }
-            }
-            if (src != nullptr) {
-                x[u][0] = __ldcs(reinterpret_cast<const uint4 *>(src) + c0);
-                x[u][1] = __ldcs(reinterpret_cast<const uint4 *>(src) + c1);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            if (dst[u] == nullptr)
+            uint8_t *dst;
+            if (h < a.q_heads)
+                dst = a.q_out + t * a.q_out_stride + h * (D * 2);
+            else if (h < a.q_heads + a.kv_heads)
+                dst = a.k_out + k_row + (h - a.q_heads) * k_head;
+            else
+                dst = a.v_out + k_row + (h - a.q_heads - a.kv_heads) * k_head;
+            if (h >= heads || (h >= a.q_heads && !store))
                 continue;
-            if (rotate[u]) {
+            if (turns && h < a.q_heads + a.kv_heads) {
                 uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w,
                                  x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
                 if (ADJACENT) {
@@ -150,9 +149,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                 x[u][0] = make_uint4(w[0], w[1], w[2], w[3]);
                 x[u][1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
-            reinterpret_cast<uint4 *>(dst[u])[c0] = x[u][0];
-            reinterpret_cast<uint4 *>(dst[u])[c1] = x[u][1];
+            reinterpret_cast<uint4 *>(dst)[c0] = x[u][0];
+            reinterpret_cast<uint4 *>(dst)[c1] = x[u][1];
         }
+        h0 += kRows * lanes;
+        if (h0 >= heads)
+            break;
+        load(h0);
     }
 }
 

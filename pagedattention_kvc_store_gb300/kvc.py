@@ -1030,18 +1030,18 @@ def kvc_cross_plan(num_sources: int, num_tokens: int, q_heads: int, pool: PoolDe
 
 
 @functools.lru_cache(maxsize=256)
-def _cross_shapes(out, q, lse, block_table, source_lens, q_indptr, head_dim):
-    """Shapes of a cross attention's arguments; the number of sources."""
-    S = source_lens[0]
-    if len(q) != 3 or q[2] != head_dim or out != q:
-        raise ValueError(f"q and out are [num_tokens, q_heads, head_dim = {head_dim}], got {tuple(q)} "
-                         f"and {tuple(out)}")
+def _cross_shapes(k_pool, v_pool, layout, out, q, lse, block_table, source_lens, q_indptr):
+    """Shapes of a cross attention's arguments; the pool's descriptor and the number of sources."""
+    pool, S = _pool_shapes(k_pool, v_pool, layout), source_lens[0]
+    if len(q) != 3 or q[2] != pool.head_dim or out != q:
+        raise ValueError(f"q and out are [num_tokens, q_heads, head_dim = {pool.head_dim}], got "
+                         f"{tuple(q)} and {tuple(out)}")
     if lse is not None and lse != q[:2]:
         raise ValueError(f"lse_out is [num_tokens, q_heads] = {tuple(q[:2])}, got {tuple(lse)}")
     if len(block_table) != 2 or block_table[0] != S or q_indptr != (S + 1,):
         raise ValueError(f"block_table is [num_sources, pages] and q_indptr [num_sources + 1], with {S} "
                          f"sources")
-    return S
+    return pool, S
 
 
 def kvc_cross(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -1058,17 +1058,19 @@ def kvc_cross(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor, v_pool: 
     _cuda("block_table", block_table, torch.int32)
     _cuda("q_indptr", q_indptr, torch.int32)
     _cuda("source_lens", source_lens, torch.int32)
+    lse = lse_ptr = None
     if lse_out is not None:
         _cuda("lse_out", lse_out, torch.float32)
-    pool = _pool_shapes(k_pool.shape, v_pool.shape, layout)
-    S = _cross_shapes(out.shape, q.shape, None if lse_out is None else lse_out.shape, block_table.shape,
-                      source_lens.shape, q_indptr.shape, pool.head_dim)
+        lse, lse_ptr = lse_out.shape, lse_out.data_ptr()
+    q_shape, table = q.shape, block_table.shape
+    pool, S = _cross_shapes(k_pool.shape, v_pool.shape, layout, out.shape, q_shape, lse, table,
+                            source_lens.shape, q_indptr.shape)
     ws, ws_bytes = _workspace_of(workspace)
     _check("kvc_cross", lib().kvc_cross(
-        _ptr(out), _out_dtype(out), _ptr(lse_out), _ptr(q), _ptr(k_pool), _ptr(v_pool), pool,
-        _ptr(block_table), block_table.shape[1], _ptr(q_indptr), _ptr(source_lens), S, q.shape[0],
-        int(max_q_len), int(max_src), q.shape[1], float(scale), int(num_splits), ws, ws_bytes,
-        _stream(stream)))
+        out.data_ptr(), _out_dtype(out), lse_ptr, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+        pool, block_table.data_ptr(), table[1], q_indptr.data_ptr(), source_lens.data_ptr(), S,
+        q_shape[0], int(max_q_len), int(max_src), q_shape[1], float(scale), int(num_splits), ws,
+        ws_bytes, _stream(stream)))
 
 
 def kvc_append_store(out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor,
