@@ -718,10 +718,10 @@ kvc_status kvc_rope_store(void *q_out, void *k_pool, void *v_pool, kvc_pool_desc
  * ends"), without the host: nothing is read back, so a captured step can grow, branch and end sequences.
  * Results are whole numbers with one right answer, whatever runs at the same time on the device; calls on
  * one table or one page_refs are ordered by the caller (one stream).  All arrays are device memory.  A length
- * past the row (bt_stride * page_size) is flagged (kvc_device_errors, 1 << 7) and taken as the row's; a page
- * outside the pool is flagged (1 << 10) and left out; a page with fewer references than rows that list it is
- * flagged (1 << 14), and what is said of its rows is undefined.  num_seqs 0 .. 65535, bt_stride * page_size
- * at most 2^30; any page_size.
+ * past the row (bt_stride * page_size) is flagged (kvc_device_errors, 1 << 7) and taken as the row's, a negative
+ * one as 0; a page outside the pool is flagged (1 << 10) and left out; a page with fewer references than rows
+ * that list it is flagged (1 << 14), and what is said of its rows is undefined.  num_seqs 0 .. 65535,
+ * bt_stride * page_size at most 2^30; any page_size.
  *
  * arrays  host, num_arrays of them, read during the call only: every array whose pages travel with the
  *         table's, page p being the page_bytes bytes from data + p * page_bytes (bf16 pools of all layers,

@@ -18,8 +18,7 @@
 //   warp 2      TMA, the item's query tiles
 //   warp 3      the items: cancels blocks of the grid that have not started and hands theirs round
 //   warps 4-11  softmax of tile 0, warps 12-19 of tile 1: two threads a row: the running maximum (O rescaled
-//               only when it grows by more than 2^8) and sum, P as bf16 over the first half of S's columns,
-//               and O / l at the end.
+//               only when it grows by more than 2^8) and sum, P as bf16 over S's columns, and O / l at the end.
 // An item of a single tile puts its blocks in turn on both halves of TMEM, so that the softmax of one runs
 // beside the products of the other as it does with two tiles, and joins the two at the end.
 // Few rows and many positions: the positions are cut into chunks (splits), partial rows and their
@@ -66,7 +65,7 @@ struct Geom {
     static constexpr int kOffItem = kOffBar + 384;           // after the barriers: the item, an answer
     static constexpr int kOffAnswer = kOffItem + 64;
     static constexpr size_t kSmemBytes = kOffBar + 512;      // base is 1024-aligned
-    // TMEM, per tile w at w * 256: O [0, D), S [D, D + 128); P overwrites S [D, D + 64).
+    // TMEM, per tile w at w * 256: O [0, D), S [D, D + 128); P overwrites S, half h from D + 64 h on.
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kColS = D;
     static_assert(D + kBN <= 256, "TMEM layout");
@@ -345,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto issue_pv = [&](int t, uint32_t v_addr, int half, int k_steps, bool first) {
                 const uint64_t db = umma_desc_sw128(v_addr, 1024, kHalves * 1024) + half * 4 * kStep;
                 const uint32_t d = tmem + t * 256;
-                const uint32_t p = d + G_::kColS + half * (kBN / 4);
+                const uint32_t p = d + G_::kColS + half * (kBN / 2);
                 if (k_steps >= kBN / 32) {
 #pragma unroll
                     for (int k = 0; k < kBN / 32; ++k)
@@ -522,7 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tmem_o = tmem + lane_off + half * (D / 2);   // tile 0's; tile 1's 256 columns on
         const uint32_t tmem_s = tmem + t * 256 + G_::kColS + lane_off + half * (kBN / 2);
-        const uint32_t tmem_p = tmem + t * 256 + G_::kColS + lane_off + half * (kBN / 4);
         float *exchange = reinterpret_cast<float *>(smem + G_::kOffExchange);
         float *mine = exchange + (t * 2 + half) * kM + row, *other = exchange + (t * 2 + 1 - half) * kM + row;
         const uint32_t pair_bar = 1 + t * 4 + quad;  // the two warps of the same rows
@@ -577,48 +575,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (warp_valid) {
                     const int n_mine = n_vis - half * (kBN / 2);   // of this thread's 64 columns
-                    float mx[4];
-                    uint32_t pk[2][16];
+                    float xs[2][32], mx[4];
                     uint64_t sum2[2];
-                    // S to registers, p = 2^(s * scale * log2(e) - m) as bf16 pairs, their sum before the
-                    // rounding, and the largest s
-                    auto probabilities = [&]() {
-                        float xs[2][32];
-                        tmem_ld32(tmem_s, xs[0]);
-                        tmem_ld32(tmem_s + 32, xs[1]);
-                        tmem_wait_ld();
+                    auto mask = [&](int c) {
                         if (n_mine < kBN / 2) {
 #pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (i >= n_mine)
-                                    xs[i >> 5][i & 31] = -INFINITY;
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * c + i >= n_mine)
+                                    xs[c][i] = -INFINITY;
                         }
+                    };
+                    // p = 2^(s * scale * log2(e) - m) of 32 columns as bf16 pairs over the first of S's own
+                    // columns, their sum before the rounding, and the largest s
+                    auto probabilities = [&](int c) {
                         const float neg_mu = (m_used == -INFINITY) ? 0.0f : -m_used;
                         const uint64_t nm2 = f2_pack(neg_mu, neg_mu);
-                        sum2[0] = sum2[1] = f2_pack(0.0f, 0.0f);
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mx[j] = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float x0 = xs[i >> 4][2 * (i & 15)], x1 = xs[i >> 4][2 * (i & 15) + 1];
+                        for (int i = 0; i < 16; ++i) {
+                            const float x0 = xs[c][2 * i], x1 = xs[c][2 * i + 1];
                             float e0, e1;
                             f2_unpack(f2_fma(f2_pack(x0, x1), sl2x2, nm2), e0, e1);
                             e0 = fast_exp2(e0);
                             e1 = fast_exp2(e1);
-                            pk[i >> 4][i & 15] = pack_bf16x2(e0, e1);
+                            pk[i] = pack_bf16x2(e0, e1);
                             sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(e0, e1));
                             mx[i & 3] = fmax3(mx[i & 3], x0, x1);
                         }
+                        tmem_st16u(tmem_s + 16 * c, pk);
                     };
+                    sum2[0] = sum2[1] = f2_pack(0.0f, 0.0f);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mx[j] = -INFINITY;
                     // With the maximum of the blocks before, which nearly always still holds (it may be
-                    // passed by 2^8).  The two warps of the rows go on together: P overwrites columns that
-                    // half 0 reads.
-                    probabilities();
+                    // passed by 2^8); whether it does for the rows' two warps is known while P is on its way.
+                    // S's columns 32 .. 63 stay in TMEM and 0 .. 31 in registers for the case that it does not.
+                    tmem_ld32(tmem_s, xs[0]);
+                    tmem_ld32(tmem_s + 32, xs[1]);
+                    tmem_wait_ld();
+                    mask(0);
+                    mask(1);
+                    probabilities(1);
+                    probabilities(0);
                     float mb = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl2;   // base 2
-                    tc_fence_before_sync();
                     const bool again = barrier_or(pair_bar, 64, mb > m_used + kRescaleLog2);
-                    tc_fence_after_sync();
                     if (again) {
                         *mine = mb;
                         named_barrier(pair_bar, 64);
@@ -629,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             m_used = mb;
                         }
                         l *= alpha;
+                        tmem_wait_st();
                         // O holds every earlier PV product (S(b) was committed after them): its columns of
                         // this half are rescaled in place
                         if (b > b0) {
@@ -642,15 +644,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     o[j] *= alpha;
                                 tmem_st16(tmem_o + t * 256 + c0, o);
                             }
-                            tmem_wait_st();
                         }
-                        probabilities();
+                        sum2[0] = sum2[1] = f2_pack(0.0f, 0.0f);
+                        tmem_ld32(tmem_s + 32, xs[1]);
+                        tmem_wait_ld();
+                        mask(1);
+                        probabilities(1);
+                        probabilities(0);
+                        tmem_wait_st();
                         tc_fence_before_sync();
                         named_barrier(pair_bar, 64);
                         tc_fence_after_sync();
                     }
-                    tmem_st16u(tmem_p, pk[0]);
-                    tmem_st16u(tmem_p + 16, pk[1]);
                     float p0, p1;
                     f2_unpack(f2_add(sum2[0], sum2[1]), p0, p1);
                     l += p0 + p1;

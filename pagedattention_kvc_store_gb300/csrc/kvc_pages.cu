@@ -540,7 +540,8 @@ __device__ void reserve_decide(const Table &t, const int32_t *new_tokens, const 
         __syncthreads();
     }
     if (row) {
-        t.lens[s] = t.lens[s] + grow;
+        if (grow > 0)   // (a negative length is none)
+            t.lens[s] = len + grow;
         if (copy) {
             w.copy_src[at] = last;
             atomicSub(t.refs + last, 1);
@@ -584,7 +585,8 @@ __global__ void __launch_bounds__(kThreads)
     if (*missing == 0) {
         const int i0 = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
         for (int s = i0; s < t.num_seqs; s += step)
-            t.lens[s] += w.grow[s];
+            if (w.grow[s] > 0)   // (a negative length is none)
+                t.lens[s] = max(t.lens[s], 0) + w.grow[s];
         for (int i = i0; i < copies; i += step)
             atomicSub(t.refs + w.copy_src[i], 1);
     }

@@ -277,3 +277,45 @@ def test_captured_call_follows_its_lengths_and_two_graphs_with_workspaces_of_the
     torch.cuda.synchronize()
     for _, out, _ in graphs:
         check(c, out, None)
+
+
+@pytest.mark.parametrize("most", [4, 200])
+def test_sources_without_positions_alone(most):
+    """Nothing to attend to anywhere: zeros and -inf, both kernels, one and several splits."""
+    c = Case([0, 0], [most, 1], 2, 4, 128, 16)
+    for splits, src in ((1, 0), (1, 256), (2, 256)):
+        c.table = np.zeros((2, 16), dtype=np.int32)
+        out, lse = c.run(splits=splits, max_src=src)
+        assert (out == 0).all() and torch.isinf(lse).all() and (lse < 0).all()
+
+
+@pytest.mark.parametrize("most", [4, 200])
+def test_two_calls_at_once_on_two_streams(most):
+    """Each with its workspace; results as one after the other, bit for bit."""
+    cases = [Case([1200, 700], [most, most // 2], 2, 4, 128, 16, seed=s) for s in range(2)]
+    alone = [c.run(splits=3) for c in cases]
+    args = []
+    for c in cases:
+        kd, vd = bf16_tensor(c.k, "cuda"), bf16_tensor(c.v, "cuda")
+        ws = kvc.kvc_cross_plan(2, c.T, 8, kvc.pool_desc(kd), most, 1200, 3)[2]
+        args.append((torch.empty(c.T, 8, 128, device="cuda"), c.q.cuda(), kd, vd,
+                     i32_tensor(c.table, "cuda"), i32_tensor(c.indptr, "cuda"),
+                     i32_tensor(np.array(c.lens), "cuda"), most, 1200,
+                     torch.empty(ws, dtype=torch.uint8, device="cuda")))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for a, s in zip(args, streams):
+            kvc.kvc_cross(*a[:9], num_splits=3, workspace=a[9], stream=s)
+    torch.cuda.synchronize()
+    for a, (out, _) in zip(args, alone):
+        assert torch.equal(a[0], out)
+
+
+@pytest.mark.parametrize("most", [4, 200])
+def test_results_do_not_depend_on_where_pages_lie(most):
+    a, b = (Case([500, 300], [most, 3], 2, 4, 64, 32, seed=1) for _ in range(2))
+    perm = np.random.default_rng(5).permutation(b.k.shape[0])
+    b.k[perm], b.v[perm], b.table = a.k, a.v, perm[a.table].astype(np.int32)
+    for splits in (1, 2):
+        assert all(torch.equal(x, y) for x, y in zip(a.run(splits=splits), b.run(splits=splits)))

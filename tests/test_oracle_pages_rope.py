@@ -233,6 +233,39 @@ def test_outputs_of_reserve_and_compact_are_checked():
     assert kvc.kvc_reserve_plan(0, 1) > 0 and kvc.kvc_compact_plan(1) > 0
 
 
+CROSS_POOL = PoolDesc(2000, 16, 8, 128)
+
+
+def _cross(pool=CROSS_POOL, out=FAKE, dtype=0, lse=None, q=FAKE, table=FAKE, stride=256, indptr=FAKE, lens=FAKE,
+           S=4, T=8, most=2, src=4096, heads=32, splits=0, ws=None, ws_bytes=0):
+    return lib().kvc_cross(out, dtype, lse, q, FAKE, FAKE, pool, table, stride, indptr, lens, S, T, most, src,
+                           heads, 0.0, splits, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(pool=PoolDesc(32, 16, 2, 96)), 2), (dict(pool=PoolDesc(32, 8, 2, 64)), 2), (dict(heads=31), 1),
+    (dict(heads=128), 2), (dict(S=-1), 1), (dict(S=65536), 1), (dict(T=-1), 1), (dict(most=-1), 1),
+    (dict(src=-1), 1), (dict(splits=-1), 1), (dict(stride=10), 1), (dict(dtype=2), 1), (dict(out=None), 1),
+    (dict(q=None), 1), (dict(table=None), 1), (dict(lens=None), 1), (dict(indptr=None), 1),
+    (dict(lse=ctypes.c_void_p(0x10002)), 1), (dict(out=ctypes.c_void_p(0x10008)), 1),
+    (dict(), 3), (dict(ws=FAKE, ws_bytes=16), 3), (dict(T=1 << 24), 2), (dict(most=1 << 29), 2),
+])
+def test_cross_checks_its_arguments(change, status):
+    assert _cross(**change) == status and lib().kvc_last_error()
+
+
+def test_cross_calls_with_nothing_to_do_and_their_plan():
+    assert _cross(T=0) == 0 and _cross(S=0) == 0 and _cross(most=0) == 0
+    for most in (1, 8, 9, 400):
+        for n in (0, 1, 3, 50):
+            splits, chunk, ws = kvc.kvc_cross_plan(4, 4 * most, 32, CROSS_POOL, most, 4096, n)
+            assert splits * chunk >= 4096 > (splits - 1) * chunk and chunk % 64 == 0
+            rows = 4 * most * 32
+            assert ws == (0 if splits == 1 else -(-rows * splits * 128 * 4 // 256) * 256 + rows * splits * 4)
+            assert n == 0 or splits <= n
+    assert kvc.kvc_cross_plan(4, 4, 32, CROSS_POOL, 1, 0)[0] == 1
+
+
 def test_bindings_refuse_cpu_tensors_and_odd_descriptions():
     t = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     i = torch.zeros(4, dtype=torch.int32)
