@@ -2101,9 +2101,39 @@ struct CrossPlan {
     size_t ws_bytes, lse_offset;
 };
 
-// Few rows: kvc_decode's chunks.  Otherwise chunks of a multiple of the kernel's block; by default one where
-// there are several work items (pairs of row tiles of one source and kv head) to an SM, else as many as
-// make 8 (8 sources of 32k-131k positions x 8 kv heads: 10 chunks 545 us, 16 468, 32 479, 64 537).
+// Chunks of the positions for many rows: of a few numbers the one that the kernel's own times make the
+// shortest.  A work item is a pair of row tiles of one source and kv head over a chunk: 6 us and 1.75 us for a block
+// of 128 positions (1.25 with one tile).  Where there are more items than SMs, these take them as they get free:
+// the last may leave an item's time idle, and sources are taken to be 0.7 of the longest.  Several chunks
+// cost a join, 5 us and their partial rows (fp32, written and read at 4.5 TB/s).  Measured against it, us: 64 items
+// of 16 blocks, 256 rows: 1 chunk 49, 2 48, 4 60; 8 items of 128 blocks: 1 243, 4 86, 8 58, 16 52; 64 items of up to
+// 1,024 blocks, 128 rows: 2 581, 8 639, 16 539, 24 540, 48 589.
+int64_t cross_splits(int32_t num_sources, int32_t num_tokens, int32_t q_heads, const kvc_pool_desc &pool,
+                     int64_t rows_each, int64_t src)
+{
+    const double blocks = static_cast<double>(ceil_div(src, kvc::kCrossBlock));
+    const double units = static_cast<double>(ceil_div(std::max<int64_t>(1, rows_each), 256) * pool.kv_heads *
+                                             std::max(num_sources, 1));
+    const double sms = device_sm_count(), block_us = rows_each > 128 ? 1.75 : 1.25;
+    const double part_us = 2.0 * num_tokens * q_heads * pool.head_dim * 4 / 4.5e6;
+    static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
+    double best = 0.0;
+    int64_t splits = 1;
+    for (int n : kSplits) {
+        if (n > blocks)
+            break;
+        const double rounds = units * n / sms;
+        const double us = (rounds > 1.0 ? 0.7 * rounds + 1.0 : 1.0) * (ceil(blocks / n) * block_us + 6.0) +
+                          (n > 1 ? 5.0 + n * part_us : 0.0);
+        if (n == 1 || us < best) {
+            best = us;
+            splits = n;
+        }
+    }
+    return splits;
+}
+
+// Few rows: kvc_decode's chunks.  Otherwise chunks of a multiple of the kernel's block.
 kvc_status make_cross_plan(int32_t num_sources, int32_t num_tokens, int32_t q_heads,
                            const kvc_pool_desc &pool, int32_t max_q_len, int32_t max_src,
                            int32_t requested, CrossPlan *out)
@@ -2128,20 +2158,10 @@ kvc_status make_cross_plan(int32_t num_sources, int32_t num_tokens, int32_t q_he
     if (few) {
         chunk = make_plan(num_sources, q_heads, pool, max_src, requested).chunk;
     } else {
-        // By default several items to an SM where they are fewer, but no chunk so short that its partial rows
-        // (fp32, written and read again) weigh as much as its keys: 8 positions a row where half the SMs
-        // would have nothing else, 16 otherwise.  256 rows an item: 64 items of 2,048 positions 50 us, cut in
-        // two 51, in four 63; 512 items of up to 3,000 159, 189 and 233.
-        int64_t want = requested, least = block;
-        if (requested == 0) {
-            const int64_t pairs = ceil_div(std::max<int64_t>(1, rows_each), 256);
-            const int64_t units = pairs * pool.kv_heads * std::max(num_sources, 1);
-            const int64_t sms = device_sm_count();
-            want = units < 4 * sms ? ceil_div(8 * sms, units) : 1;
-            least = std::max<int64_t>(512, (2 * units < sms ? 8 : 16) * std::min<int64_t>(rows_each, 256));
-        }
-        chunk = std::max(round_up(ceil_div(src, want), block),
-                         std::min(round_up(least, block), round_up(src, block)));
+        const int64_t want = requested > 0 ? requested
+                                           : cross_splits(num_sources, num_tokens, q_heads, pool, rows_each,
+                                                          src);
+        chunk = round_up(ceil_div(src, want), block);
     }
     CrossPlan p{};
     p.few = few;
