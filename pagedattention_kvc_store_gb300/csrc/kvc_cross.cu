@@ -8,15 +8,16 @@
 // tiles of 128 (the tcgen05 M).  A work item is a pair of consecutive tiles over one chunk of the source's
 // positions (the whole source where there is one split); both tiles see the same pages, so every K or V
 // stage feeds two products.  One CTA per SM goes on from item to item, its roles running ahead across them:
-//   warp 0      TMA, K and V: 128-position stages in one ring, filled in the order K(0), K(1), V(0), K(2),
-//               V(1), ...; a box per page, issued by parallel lanes, that lands as [8 positions][column half]
-//               [8 rows][128 bytes, swizzled], so that a stage is one operand whatever the page size (a box
-//               per page and half took twice as many, and 16-position pages 37% more time)
+//   warps 0, 2  TMA, K and V: 128-position stages in one ring in the order K(0), K(1), V(0), K(2), V(1), ...; a
+//               box per page, issued by parallel lanes, that lands as [8 positions][column half][8 rows]
+//               [128 bytes, swizzled], so that a stage is one operand whatever the page size (a box per page and
+//               half took twice as many, and 16-position pages 37% more time).  A warp issues a box in some
+//               150 cycles: one for both K and V held 16-position pages back (766 us for prompts over them, 670 with two)
 //   warp 1      allocates TMEM (512 columns) and issues S_w = Q_w K(b)^T (M 128, N 128, K head_dim) and
 //               O_w += P_w V(b) (N head_dim, K 128, P from TMEM) of the tiles w from one thread; S_w(b + 1)
 //               right behind the PV product that reads P_w(b) from the same columns
-//   warp 2      TMA, the item's query tiles
-//   warp 3      the items: cancels blocks of the grid that have not started and hands theirs round
+//   warp 3      the items (cancels blocks of the grid that have not started and hands theirs round), and
+//               their query tiles
 //   warps 4-11  softmax of tile 0, warps 12-19 of tile 1: two threads a row: the running maximum (O rescaled
 //               only when it grows by more than 2^8) and sum, P as bf16 over S's columns, and O / l at the end.
 // An item of a single tile puts its blocks in turn on both halves of TMEM, so that the softmax of one runs
@@ -38,7 +39,7 @@ __device__ uint32_t g_cross_errors;
 
 constexpr int kM = 128;           // rows per tile
 constexpr int kBN = kCrossBlock;  // positions per K or V stage (the N of S = Q K^T)
-constexpr int kRoleWarps = 4;     // K/V loads, MMA issue, query loads, items
+constexpr int kRoleWarps = 4;     // K loads, MMA issue, V loads, items and queries
 constexpr int kSoftmaxWarps = 16; // a group of eight for each tile, two threads to a row
 constexpr int kThreads = (kRoleWarps + kSoftmaxWarps) * 32;
 constexpr int kMaxStages = 8;
@@ -227,17 +228,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kRoleWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
-    if (warp == 0) {
-        // ------------------------------ K / V loads --------------------------------------
-        if (lane == 0) {
-            prefetch_tensormap(&tmap_k);
-            prefetch_tensormap(&tmap_v);
-        }
+    if (warp == 0 || warp == 2) {
+        // ------------------------------ K loads (warp 0), V loads (warp 2) -----------------
+        const bool is_k = warp == 0;
+        const CUtensorMap *map = is_k ? &tmap_k : &tmap_v;
+        if (lane == 0)
+            prefetch_tensormap(map);
         // tiles past the first pair read the pages again: only pages read once may leave L2 early
         const uint64_t policy = a.pairs_per_seq > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
         Feed w;
-        int n = 0;   // ring slots filled so far
-        while (w.next(bars, item, ok)) {
+        int n0 = 0;          // ring index of the item's first slot
+        int begun = 0;       // ring index behind the last slot that this warp filled
+        for (; w.next(bars, item, ok); n0 += 2 * w.x.n_blocks) {
             const Item &x = w.x;
             if (!ok)
                 continue;   // a wait ran out: the rest of the items are only taken note of
@@ -247,11 +249,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             int cached_base = 0;
             int cached_page = lane < n_pages ? bt_row[lane] : 0;
             const int nb = x.n_blocks;
-            for (int j = 0; j < 2 * nb; ++j, ++n) {
-                const bool is_k = j == 0 || (j < 2 * nb - 1 && (j & 1));
-                const int b = is_k ? (j + 1) / 2 : (j == 2 * nb - 1 ? nb - 1 : j / 2 - 1);
+            for (int b = 0; b < nb; ++b) {
+                const int n = n0 + (is_k ? (b == 0 ? 0 : 2 * b - 1) : (b == nb - 1 ? 2 * nb - 1 : 2 * b + 2));
                 const int np = (min(kBN, x.n_keys - b * kBN) + P - 1) / P;
                 const int st = n % kStages;
+                const int lp0 = b * kBN / P;   // first page of the block
+                if (lp0 + np > cached_base + 32) {
+                    cached_base = lp0;
+                    cached_page = (lp0 + lane < n_pages) ? bt_row[lp0 + lane] : 0;
+                }
+                // lane i issues the box of page i; NHD maps end in {group, kv head}, HND maps in {group of
+                // the block, block}
+                const int page =
+                    __shfl_sync(0xffffffffu, cached_page, (lp0 - cached_base + lane) & 31);
+                uint8_t *dst = sStages + st * G_::kStageBytes + lane * P * (D * 2);
                 if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(&bars[kBarKvEmpty + st],
                                                                        ((n / kStages) - 1) & 1))) {
                     ok = false;
@@ -260,60 +271,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0)
                     mbar_arrive_expect_tx(&bars[kBarKvFull + st], static_cast<uint32_t>(np * P * D * 2));
                 __syncwarp();
-                uint8_t *dst = sStages + st * G_::kStageBytes;
-                const int lp0 = b * kBN / P;   // first page of the block
-                if (lp0 < cached_base || lp0 + np > cached_base + 32) {
-                    cached_base = lp0;
-                    cached_page = (lp0 + lane < n_pages) ? bt_row[lp0 + lane] : 0;
-                }
-                // lane i issues the box of page i; NHD maps end in {group, kv head}, HND maps in {group of
-                // the block, block}
-                const int page =
-                    __shfl_sync(0xffffffffu, cached_page, (lp0 - cached_base + lane) & 31);
                 if (lane < np)
-                    tma_load_5d_hint(dst + lane * P * (D * 2), is_k ? &tmap_k : &tmap_v, 0, 0, 0,
-                                     a.hnd ? 0 : page * (P / 8), a.hnd ? page * a.kv_heads + x.kvh : x.kvh,
-                                     &bars[kBarKvFull + st], policy);
+                    tma_load_5d_hint(dst, map, 0, 0, 0, a.hnd ? 0 : page * (P / 8),
+                                     a.hnd ? page * a.kv_heads + x.kvh : x.kvh, &bars[kBarKvFull + st],
+                                     policy);
+                begun = n + 1;
             }
         }
         if (!ok && lane == 0) {
             atomicOr(err_word, kErrCrossWait);
-            // let every copy in flight land before the CTA can exit
-            for (int m = max(0, n - kStages); m < n; ++m)
+            // let every copy in flight land before the CTA can exit: the slots of the other warp too
+            for (int m = max(0, begun - kStages); m < begun; ++m)
                 if (!mbar_wait(&bars[kBarKvFull + m % kStages], (m / kStages) & 1))
-                    atomicOr(err_word, kErrDrainWait);
-        }
-    } else if (warp == 2) {
-        // ------------------------------ query loads --------------------------------------
-        if (lane == 0)
-            prefetch_tensormap(&tmap_q);
-        Feed w;
-        int qi[2] = {0, 0};   // items whose query tile t was requested
-        while (w.next(bars, item, ok)) {
-            const Item &x = w.x;
-            if (!ok || x.n_blocks == 0)
-                continue;
-            // lane h loads column half h of the tile's 128 / G tokens x G heads, token-major
-            for (int t = 0; t < (x.has_b ? 2 : 1); ++t) {
-                if (qi[t] > 0 &&
-                    !__all_sync(0xffffffffu, mbar_wait(&bars[kBarQEmpty + t], (qi[t] - 1) & 1))) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&bars[kBarQFull + t], static_cast<uint32_t>(G_::kQBytes));
-                __syncwarp();
-                if (lane < kHalves)
-                    tma_load_4d(q_tile(t) + lane * kM * 128, &tmap_q, lane * 64, 0, x.kvh,
-                                x.tok0 + (x.row_begin + t * kM) / G, &bars[kBarQFull + t]);
-                ++qi[t];
-            }
-        }
-        if (!ok && lane == 0) {
-            atomicOr(err_word, kErrCrossWait);
-            // the last requests may still be in flight
-            for (int t = 0; t < 2; ++t)
-                if (qi[t] > 0 && !mbar_wait(&bars[kBarQFull + t], (qi[t] - 1) & 1))
                     atomicOr(err_word, kErrDrainWait);
         }
     } else if (warp == 1) {
@@ -476,28 +445,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (elect_one()) {
-        // ------------------------------ items --------------------------------------------
+        // ------------------------------ items and query loads ------------------------------
         // The grid has a block for every item.  This one's own is the first; then it asks for blocks that
         // have not started, and takes their items in their place, until none is left: items are of very
-        // different lengths (a static deal of them left SMs idle for a fifth of the time).
+        // different lengths (a static deal of them left SMs idle for a fifth of the time).  An item is handed
+        // round as soon as all have read the one before, its query tiles follow as each is free.
+        prefetch_tensormap(&tmap_q);
         const uint32_t answer = smem_addr(smem + G_::kOffAnswer);
         int it = blockIdx.x;
         int published = 0, asked = 0;
+        int qi[2] = {0, 0};   // items whose query tile t was requested
         bool more = true;
         while (more) {
             Item x;
             if (make_item(a, it, x, err_word)) {
-                if (published > 0 && !mbar_wait_long(&bars[kBarItemEmpty], (published - 1) & 1))
+                if (published > 0 && !mbar_wait_long(&bars[kBarItemEmpty], (published - 1) & 1)) {
+                    ok = false;
                     break;
+                }
                 *item = x;
                 mbar_arrive(&bars[kBarItemFull]);
                 ++published;
+                // the tile's 128 / G tokens x G heads, token-major, by column halves
+                for (int t = 0; ok && x.n_blocks > 0 && t < (x.has_b ? 2 : 1); ++t) {
+                    if (qi[t] > 0 && !mbar_wait_long(&bars[kBarQEmpty + t], (qi[t] - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&bars[kBarQFull + t], static_cast<uint32_t>(G_::kQBytes));
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+                        tma_load_4d(q_tile(t) + h * kM * 128, &tmap_q, h * 64, 0, x.kvh,
+                                    x.tok0 + (x.row_begin + t * kM) / G, &bars[kBarQFull + t]);
+                    ++qi[t];
+                }
             }
             more = false;
             mbar_arrive_expect_tx(&bars[kBarCancel], 16);
             try_cancel_block(answer, &bars[kBarCancel]);
             if (!mbar_wait(&bars[kBarCancel], asked & 1)) {
-                atomicOr(err_word, kErrCrossWait);
+                ok = false;
                 break;
             }
             ++asked;
@@ -505,9 +492,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
         }
         if (published > 0 && !mbar_wait_long(&bars[kBarItemEmpty], (published - 1) & 1))
-            atomicOr(err_word, kErrCrossWait);
+            ok = false;
         item->done = 1;
         mbar_arrive(&bars[kBarItemFull]);
+        if (!ok) {
+            atomicOr(err_word, kErrCrossWait);
+            // the last requests may still be in flight
+            for (int t = 0; t < 2; ++t)
+                if (qi[t] > 0 && !mbar_wait(&bars[kBarQFull + t], (qi[t] - 1) & 1))
+                    atomicOr(err_word, kErrDrainWait);
+        }
     }
     } else {
         // ------------------------------ softmax + epilogue -------------------------------
