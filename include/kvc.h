@@ -359,8 +359,8 @@ kvc_status kvc_append(void *out, int32_t out_dtype, const void *q, const void *k
  *   max_q_len, max_src  host upper bounds on every source's tokens and positions; more are flagged
  *                 (kvc_device_errors, 1 << 7): positions past max_src are not seen, rows past max_q_len undefined
  *   num_splits    0 = choose, 1 = no split, n > 1 = at most n chunks
- *   workspace     kvc_cross_plan's bytes when the plan has more than one split, 16-byte aligned; it belongs to
- *                 one call at a time
+ *   workspace     kvc_cross_plan's bytes for the call's own scalars when the plan has more than one split, 16-byte
+ *                 aligned; it belongs to one call at a time
  */
 kvc_status kvc_cross_plan(int32_t num_sources, int32_t num_tokens, int32_t q_heads, kvc_pool_desc pool,
                           int32_t max_q_len, int32_t max_src, int32_t num_splits, int32_t *splits_out,

@@ -150,10 +150,10 @@ __device__ __forceinline__ bool make_item(const Args &a, int it, Item &x, uint32
 struct Feed {
     Item x;
     int n = 0;   // items read
-    // Waits for the next item; false if that takes too long.  `lanes`: of a whole warp, or one thread.
+    // Waits for the next item, which may be as long as the one before takes; false if that is too long.
     __device__ __forceinline__ bool wait(uint64_t *bars)
     {
-        return mbar_wait(&bars[kBarItemFull], n & 1);
+        return mbar_wait_long(&bars[kBarItemFull], n & 1);
     }
     __device__ __forceinline__ void read(const Item *slot)
     {
@@ -234,8 +234,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap *map = is_k ? &tmap_k : &tmap_v;
         if (lane == 0)
             prefetch_tensormap(map);
-        // tiles past the first pair read the pages again: only pages read once may leave L2 early
-        const uint64_t policy = a.pairs_per_seq > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+        // (the tile pairs of a source read its pages at about the same time: to keep them in L2 beyond that
+        // made it 1% slower)
+        const uint64_t policy = l2_policy_evict_first();
         Feed w;
         int n0 = 0;          // ring index of the item's first slot
         int begun = 0;       // ring index behind the last slot that this warp filled

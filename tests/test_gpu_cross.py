@@ -248,25 +248,26 @@ def test_lengths_past_the_bounds_are_flagged():
     assert kvc.kvc_device_errors() == 1 << 7
 
 
-def test_captured_call_follows_its_lengths_and_two_graphs_with_workspaces_of_their_own():
-    c = Case([1500, 800], [4, 4], 2, 4, 128, 16)
+@pytest.mark.parametrize("most", [4, 100])
+def test_captured_call_follows_its_lengths_and_two_graphs_with_workspaces_of_their_own(most):
+    c = Case([1500, 800], [most, most], 2, 4, 128, 16)
     kd, vd = bf16_tensor(c.k, "cuda"), bf16_tensor(c.v, "cuda")
     q, table = c.q.cuda(), i32_tensor(c.table, "cuda")
     indptr, lens = i32_tensor(c.indptr, "cuda"), i32_tensor(np.array(c.lens), "cuda")
     pool = kvc.pool_desc(kd)
     graphs = []
     for splits in (3, 5):
-        ws = kvc.kvc_cross_plan(2, 8, 8, pool, 4, 1500, splits)[2]
+        ws = kvc.kvc_cross_plan(2, c.T, 8, pool, most, 1500, splits)[2]
         work = torch.empty(ws, dtype=torch.uint8, device="cuda")
-        out = torch.zeros(8, 8, 128, device="cuda")
-        call = lambda: kvc.kvc_cross(out, q, kd, vd, table, indptr, lens, 4, 1500,   # noqa: E731
+        out = torch.zeros(c.T, 8, 128, device="cuda")
+        call = lambda: kvc.kvc_cross(out, q, kd, vd, table, indptr, lens, most, 1500,   # noqa: E731
                                      num_splits=splits, workspace=work)
         call()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             call()
         graphs.append((g, out, work))
-    c.lens = [700, 801 - 1]
+    c.lens = [700, 800]
     lens.copy_(i32_tensor(np.array(c.lens), "cuda"))
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
