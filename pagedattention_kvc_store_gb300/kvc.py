@@ -690,14 +690,18 @@ def page_arrays(tensors) -> PageArrays:
 
 def _table(block_table, context_lens, page_refs, arrays=None):
     """Checks of a table, its lengths and the references; the number of sequences."""
-    for name, t in (("block_table", block_table), ("context_lens", context_lens),
-                    ("page_refs", page_refs)):
-        try:
-            if t.is_cuda and t.dtype is torch.int32 and t.is_contiguous():
-                continue
-        except AttributeError:
-            pass
-        _cuda(name, t, torch.int32)
+    i32 = torch.int32
+    try:   # what nearly every call passes, with as few steps as say so
+        plain = (block_table.is_cuda and context_lens.is_cuda and page_refs.is_cuda
+                 and block_table.dtype is i32 and context_lens.dtype is i32 and page_refs.dtype is i32
+                 and block_table.is_contiguous() and context_lens.is_contiguous()
+                 and page_refs.is_contiguous())
+    except AttributeError:
+        plain = False
+    if not plain:
+        _cuda("block_table", block_table, i32)
+        _cuda("context_lens", context_lens, i32)
+        _cuda("page_refs", page_refs, i32)
     S, table = context_lens.numel(), block_table.shape
     if len(table) != 2 or table[0] != S:
         raise ValueError("block_table is [num_seqs, pages]")
@@ -738,8 +742,9 @@ def kvc_truncate(block_table: torch.Tensor, context_lens: torch.Tensor,
     """Rows give back the pages past new_lens positions (None: all of them); context_lens follows."""
     S = _table(block_table, context_lens, page_refs)
     _check("kvc_truncate", lib().kvc_truncate(
-        _ptr(block_table), block_table.shape[1], _ptr(context_lens), _row_values("new_lens", new_lens, S),
-        S, _ptr(page_refs), page_refs.numel(), int(page_size), _stream(stream)))
+        block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
+        _row_values("new_lens", new_lens, S), S, page_refs.data_ptr(), page_refs.numel(),
+        int(page_size), _stream(stream)))
 
 
 def kvc_fork(block_table_out: torch.Tensor, context_lens_out: torch.Tensor, parents: torch.Tensor,
@@ -752,9 +757,9 @@ def kvc_fork(block_table_out: torch.Tensor, context_lens_out: torch.Tensor, pare
     if parents is None:
         raise ValueError("parents: a row for each new one")
     _check("kvc_fork", lib().kvc_fork(
-        _ptr(block_table_out), block_table_out.shape[1], _ptr(context_lens_out),
+        block_table_out.data_ptr(), block_table_out.shape[1], context_lens_out.data_ptr(),
         _row_values("parents", parents, n), _row_values("share_lens", share_lens, n), n,
-        _ptr(block_table), block_table.shape[1], _ptr(context_lens), S, _ptr(page_refs),
+        block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(), S, page_refs.data_ptr(),
         page_refs.numel(), int(page_size), _stream(stream)))
 
 
@@ -775,9 +780,9 @@ def kvc_reserve(block_table: torch.Tensor, context_lens: torch.Tensor,
     S = _table(block_table, context_lens, page_refs, arrays)
     ws, ws_bytes = _workspace_of(workspace)
     _check("kvc_reserve", lib().kvc_reserve(
-        arrays.table if arrays else None, len(arrays.tensors) if arrays else 0, _ptr(block_table),
-        block_table.shape[1], _ptr(context_lens), _row_values("new_tokens", new_tokens, S), S,
-        _ptr(page_refs), page_refs.numel(), int(page_size), _one("missing", missing), ws, ws_bytes,
+        arrays.table if arrays else None, len(arrays.tensors) if arrays else 0, block_table.data_ptr(),
+        block_table.shape[1], context_lens.data_ptr(), _row_values("new_tokens", new_tokens, S), S,
+        page_refs.data_ptr(), page_refs.numel(), int(page_size), _one("missing", missing), ws, ws_bytes,
         _stream(stream)))
 
 
@@ -797,8 +802,8 @@ def kvc_compact(block_table: torch.Tensor, context_lens: torch.Tensor, page_refs
     S = _table(block_table, context_lens, page_refs, arrays)
     ws, ws_bytes = _workspace_of(workspace)
     _check("kvc_compact", lib().kvc_compact(
-        arrays.table if arrays else None, len(arrays.tensors) if arrays else 0, _ptr(block_table),
-        block_table.shape[1], _ptr(context_lens), S, _ptr(page_refs), page_refs.numel(),
+        arrays.table if arrays else None, len(arrays.tensors) if arrays else 0, block_table.data_ptr(),
+        block_table.shape[1], context_lens.data_ptr(), S, page_refs.data_ptr(), page_refs.numel(),
         int(page_size), _row_values("page_map", page_map, page_refs.numel()),
         _one("num_live", num_live), ws, ws_bytes, _stream(stream)))
 
