@@ -234,9 +234,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap *map = is_k ? &tmap_k : &tmap_v;
         if (lane == 0)
             prefetch_tensormap(map);
-        // (the tile pairs of a source read its pages at about the same time: to keep them in L2 beyond that
-        // made it 1% slower)
-        const uint64_t policy = l2_policy_evict_first();
+        // K and V that several tile pairs read stay in L2 like anything else (64 sources of 512 to 4,096
+        // positions x 200-400 queries with the L2 cold: 644 us, marked to leave first 669 and 1.7 GB from
+        // memory instead of 0.9, marked to leave last 644); what is read once leaves first
+        const uint64_t policy = a.pairs_per_seq > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
         Feed w;
         int n0 = 0;          // ring index of the item's first slot
         int begun = 0;       // ring index behind the last slot that this warp filled
