@@ -66,10 +66,12 @@ struct Geom {
     static constexpr int kOffItem = kOffBar + 384;           // after the barriers: the item, an answer
     static constexpr int kOffAnswer = kOffItem + 64;
     static constexpr size_t kSmemBytes = kOffBar + 512;      // base is 1024-aligned
-    // TMEM, per tile w at w * 256: O [0, D), S [D, D + 128); P overwrites S, half h from D + 64 h on.
+    // TMEM: O of tile w at w * D, then as many slots of 128 columns as fit, for the scores of a tile and block
+    // each; P overwrites S, half h from 64 h on.
     static constexpr uint32_t kTmemCols = 512;
-    static constexpr uint32_t kColS = D;
-    static_assert(D + kBN <= 256, "TMEM layout");
+    static constexpr uint32_t kColS = 2 * D;
+    static constexpr int kSlots = (kTmemCols - kColS) / kBN;
+    static_assert(kSlots == 2 || kSlots == 3, "score slots");
     static_assert(kStages <= kMaxStages, "ring barriers");
     static_assert(kSmemBytes <= 232448, "shared memory");
 };
@@ -94,10 +96,9 @@ enum BarIndex : int {
     kBarKvEmpty = kBarKvFull + kMaxStages,  // [ring slot], one MMA commit
     kBarQFull = kBarKvEmpty + kMaxStages,   // [tile]
     kBarQEmpty = kBarQFull + 2,             // [tile], one MMA commit after its last S product
-    kBarSFull = kBarQEmpty + 2,             // [tile]
-    kBarPHalf = kBarSFull + 2,              // [tile], an arrival of each of its four warps
-    kBarPFull = kBarPHalf + 2,              // [tile], the same
-    kBarPvDone = kBarPFull + 2,             // [tile], once per item
+    kBarSFull = kBarQEmpty + 2,             // [tile][its blocks in turn]
+    kBarPFull = kBarSFull + 4,              // [tile][its blocks in turn], an arrival of each of its eight warps
+    kBarPvDone = kBarPFull + 4,             // [tile], once per item with two slots, once per block with three
     kBarDrain = kBarPvDone + 2,
     kBarItemFull = kBarDrain + 1,           // the item in shared memory is the next one
     kBarItemEmpty = kBarItemFull + 1,       // an arrival of every warp that reads items
@@ -114,6 +115,13 @@ struct __align__(16) Item {
     int has_b;                   // tile 2 tp + 1 exists
     int dual;                    // it does not: the blocks in turn on both halves of TMEM, joined at the end
     int done;                    // no item: the last one was
+
+    // Its units (a tile and a block each, the tile of unit u being u & 1 where there is more than one).  All
+    // units of a CTA take the score slots in turn.
+    __device__ __forceinline__ int units() const
+    {
+        return has_b ? 2 * n_blocks : n_blocks;
+    }
 };
 
 // Item `it` from its source's lengths; false where it has no rows.
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBarCount; ++i)
-            mbar_init(&bars[i], (i >= kBarPHalf && i < kBarPvDone) ? 4u
+            mbar_init(&bars[i], (i >= kBarPFull && i < kBarPvDone) ? 8u
                                 : i == kBarItemEmpty               ? static_cast<uint32_t>(kItemReaders)
                                                                    : 1u);
         fence_mbar_init();
@@ -289,162 +297,182 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issue ----------------------------------------
-        // One thread for all of it: a vote of the warp after each wait costs as much as two products.
-        if (elect_one()) {
-            constexpr uint32_t kIdescPV = umma_idesc_bf16(kM, D, 1);
-            const uint32_t stage_addr = smem_addr(sStages);
-            auto stage_of = [&](int n) { return stage_addr + (n % kStages) * G_::kStageBytes; };
-            auto wait_slot = [&](int n) {
-                return mbar_wait(&bars[kBarKvFull + n % kStages], (n / kStages) & 1);
-            };
-            // Descriptors are made once for an operand and moved on by adding to their address field (in
-            // 16-byte units).
-            // S_t = Q_q K^T over n_cols positions (a multiple of 16)
-            auto issue_qk = [&](int t, int q, uint32_t k_addr, int n_cols) {
-                const uint32_t idesc = umma_idesc_bf16(kM, n_cols, 0);
-                const uint64_t da = umma_desc_sw128(smem_addr(q_tile(q)), 16, 1024);
-                const uint64_t db = umma_desc_sw128(k_addr, 16, kHalves * 1024);
-                const uint32_t d = tmem + t * 256 + G_::kColS;
+        // What lies between P and the products that wait for it are this warp's own steps, and registers that
+        // spill there cost more than the steps: the whole warp goes through them, so that what they are made of
+        // lives in uniform registers (one thread alone took 1,800 cycles for the products of 128 positions of
+        // two tiles), ring positions are carried along, and waits are one instruction sequence each without a
+        // branch on their result.  A wait that runs out makes the others go through at once, up to the item's end.
+        const bool leader = elect_one();
+        constexpr uint32_t kIdescPV = umma_idesc_bf16(kM, D, 1), kIdescQK = umma_idesc_bf16(kM, kBN, 0);
+        constexpr uint32_t kStageLo = G_::kStageBytes / 16;
+        constexpr uint64_t kHighQ = umma_desc_sw128_high(1024), kHighKv = umma_desc_sw128_high(kHalves * 1024);
+        const uint32_t ring_k = umma_desc_sw128_low(smem_addr(sStages), 16);
+        const uint32_t ring_v = umma_desc_sw128_low(smem_addr(sStages), 1024);
+        const uint32_t q_low = umma_desc_sw128_low(smem_addr(smem), 16);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        uint32_t failed = 0;
+        auto wait = [&](int bar, uint32_t parity) { mbar_wait_plain(&bars[bar], parity, failed); };
+        // S = Q_q K^T into a score slot, K at a stage
+        auto issue_qk = [&](int slot, int q, int stage, uint32_t idesc) {
+            const uint32_t low = q_low + q * (G_::kQBytes / 16), k_low = ring_k + stage * kStageLo;
+            const uint32_t d = tm + G_::kColS + slot * kBN;
+            if (leader) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma_bf16_ss(d, da + (k >> 2) * (kM * 128 / 16) + (k & 3) * 2,
-                                 db + (k >> 2) * (1024 / 16) + (k & 3) * 2, idesc, k > 0 ? 1u : 0u);
-            };
-            constexpr int kStep = 2 * kHalves * 1024 / 16;   // 16 positions of V
-            // O_t (+)= P_t V over positions 64 half .. of a block: a whole half, or the first 16 k_steps
-            auto issue_pv = [&](int t, uint32_t v_addr, int half, int k_steps, bool first) {
-                const uint64_t db = umma_desc_sw128(v_addr, 1024, kHalves * 1024) + half * 4 * kStep;
-                const uint32_t d = tmem + t * 256;
-                const uint32_t p = d + G_::kColS + half * (kBN / 2);
-                if (k_steps >= kBN / 32) {
-#pragma unroll
-                    for (int k = 0; k < kBN / 32; ++k)
-                        umma_bf16_ts(d, p + k * 8, db + k * kStep, kIdescPV, (!first || k > 0) ? 1u : 0u);
-                } else {
-                    for (int k = 0; k < k_steps; ++k)
-                        umma_bf16_ts(d, p + k * 8, db + k * kStep, kIdescPV, (!first || k > 0) ? 1u : 0u);
-                }
-            };
-            Feed w;
-            int n0 = 0;             // ring index of the item's first slot
-            int qi[2] = {0, 0};     // items of tile 0 / tile 1
-            int tb[2] = {0, 0};     // blocks of tile 0 / tile 1
-            for (;;) {
-                if (!w.wait(bars)) {
-                    ok = false;
-                    break;
-                }
-                w.read(item);
-                mbar_arrive(&bars[kBarItemEmpty]);
-                const Item &x = w.x;
-                if (x.done)
-                    break;
-                const int nt = x.has_b ? 2 : 1;
-                const int nb = x.n_blocks;
-                if (!ok || nb == 0)
-                    continue;
-                const int last_cols = (x.n_keys - (nb - 1) * kBN + 15) & ~15;
-                // ring indices in the producer's fill order K(0), K(1), V(0), K(2), V(1), ...
-                auto k_slot = [&](int b) { return n0 + (b == 0 ? 0 : 2 * b - 1); };
-                auto v_slot = [&](int b) { return n0 + (b == nb - 1 ? 2 * nb - 1 : 2 * b + 2); };
-                auto cols = [&](int b) { return b + 1 == nb ? last_cols : kBN; };
-                if (x.dual) {
-                    // block b on half b % 2, in the order S(0), S(1), PV(0), S(2), PV(1), ...
-                    ok = mbar_wait(&bars[kBarQFull], qi[0] & 1);
-                    for (int b = -2; b < nb && ok; ++b) {
-                        const int t = b & 1;
-                        if (b >= 0) {
-                            const int vn = v_slot(b);
-                            if (!(ok = wait_slot(vn) && mbar_wait(&bars[kBarPHalf + t], tb[t] & 1)))
-                                break;
-                            tc_fence_after_sync();
-                            issue_pv(t, stage_of(vn), 0, cols(b) / 16, b < 2);
-                            if (!(ok = mbar_wait(&bars[kBarPFull + t], tb[t] & 1)))
-                                break;
-                            ++tb[t];
-                            tc_fence_after_sync();
-                            issue_pv(t, stage_of(vn), 1, cols(b) / 16 - kBN / 32, false);
-                            umma_commit(&bars[kBarKvEmpty + vn % kStages]);
-                            if (b + 2 >= nb)
-                                umma_commit(&bars[kBarPvDone + t]);
-                        }
-                        if (b + 2 < nb) {
-                            const int kn = k_slot(b + 2);
-                            if (!(ok = wait_slot(kn)))
-                                break;
-                            tc_fence_after_sync();
-                            issue_qk(t, 0, stage_of(kn), cols(b + 2));
-                            umma_commit(&bars[kBarSFull + t]);
-                            umma_commit(&bars[kBarKvEmpty + kn % kStages]);
-                            if (b + 3 == nb)
-                                umma_commit(&bars[kBarQEmpty]);
-                        }
-                    }
-                    if (!ok)
-                        continue;
-                    ++qi[0];
-                    n0 += 2 * nb;
-                    continue;
-                }
-                ok = wait_slot(k_slot(0));
-                for (int t = 0; t < nt && ok; ++t) {
-                    if (!(ok = mbar_wait(&bars[kBarQFull + t], qi[t] & 1)))
-                        break;
-                    tc_fence_after_sync();
-                    issue_qk(t, t, stage_of(k_slot(0)), nb == 1 ? last_cols : kBN);
-                    umma_commit(&bars[kBarSFull + t]);
-                    if (nb == 1)
-                        umma_commit(&bars[kBarQEmpty + t]);
-                }
-                if (!ok)
-                    continue;
-                umma_commit(&bars[kBarKvEmpty + k_slot(0) % kStages]);
-                for (int b = 0; b < nb && ok; ++b) {
-                    const bool last = b + 1 == nb;
-                    const int vn = v_slot(b);
-                    const int kn = last ? 0 : k_slot(b + 1);
-                    const int k_steps = last ? last_cols / 16 : kBN / 16;
-                    ok = wait_slot(vn);
-                    for (int t = 0; t < nt && ok; ++t) {
-                        if (!(ok = mbar_wait(&bars[kBarPHalf + t], tb[t] & 1)))
-                            break;
-                        tc_fence_after_sync();
-                        issue_pv(t, stage_of(vn), 0, k_steps, b == 0);
-                        // K(b + 1) is waited for only once PV(b) of tile 0 is on its way
-                        if (!(ok = (last || t > 0 || wait_slot(kn)) &&
-                                   mbar_wait(&bars[kBarPFull + t], tb[t] & 1)))
-                            break;
-                        ++tb[t];
-                        tc_fence_after_sync();
-                        issue_pv(t, stage_of(vn), 1, k_steps - kBN / 32, false);
-                        if (last) {
-                            umma_commit(&bars[kBarPvDone + t]);
-                            continue;
-                        }
-                        issue_qk(t, t, stage_of(kn), b + 2 == nb ? last_cols : kBN);
-                        umma_commit(&bars[kBarSFull + t]);
-                        if (b + 2 == nb)
-                            umma_commit(&bars[kBarQEmpty + t]);
-                    }
-                    if (!ok)
-                        break;
-                    umma_commit(&bars[kBarKvEmpty + vn % kStages]);
-                    if (!last)
-                        umma_commit(&bars[kBarKvEmpty + kn % kStages]);
-                }
-                if (!ok)
-                    continue;
-                for (int t = 0; t < nt; ++t)
-                    ++qi[t];
-                n0 += 2 * nb;
+                    umma_bf16_ss(d, kHighQ | (low + (k >> 2) * (kM * 128 / 16) + (k & 3) * 2),
+                                 kHighKv | (k_low + (k >> 2) * (1024 / 16) + (k & 3) * 2), idesc, k > 0 ? 1u : 0u);
             }
-            if (!ok)
-                atomicOr(err_word, kErrCrossWait);
-            // every product that this thread issued must be complete before TMEM is released
-            umma_commit(&bars[kBarDrain]);
-            if (!mbar_wait(&bars[kBarDrain], 0))
-                atomicOr(err_word, kErrDrainWait);
+        };
+        constexpr int kStep = 2 * kHalves * 1024 / 16;   // 16 positions of V
+        // O_t (+)= P V over the first 16 k_steps positions of a block
+        auto issue_pv = [&](int t, int slot, int stage, int k_steps, uint32_t keep) {
+            const uint32_t d = tm + t * D, p = tm + G_::kColS + slot * kBN, v_low = ring_v + stage * kStageLo;
+            if (k_steps == kBN / 16) {
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < kBN / 16; ++k)
+                        umma_bf16_ts(d, p + (k >> 2) * (kBN / 2) + (k & 3) * 8, kHighKv | (v_low + k * kStep), kIdescPV,
+                                     k > 0 ? 1u : keep);
+                }
+            } else if (leader) {
+                for (int k = 0; k < k_steps; ++k)
+                    umma_bf16_ts(d, p + (k >> 2) * (kBN / 2) + (k & 3) * 8, kHighKv | (v_low + k * kStep), kIdescPV,
+                                 k > 0 ? 1u : keep);
+            }
+        };
+        auto commit = [&](int bar) {
+            if (leader)
+                umma_commit(&bars[bar]);
+        };
+        Feed w;
+        int s_slot = 0, p_slot = 0;   // score slots of the next unit's S and of the next unit's P
+        uint32_t s_count[2] = {0, 0}, p_count[2] = {0, 0};   // the tiles' S products and P so far
+        uint32_t q_count[2] = {0, 0};                        // and their items
+        int kst = 0;        // ring stage of the current K, in the producers' order K(0), K(1), V(0), ...
+        uint32_t kph = 0;   // and its phase
+        auto advance = [](int &stage, uint32_t &phase, int n) {
+            stage += n;
+            if (stage >= kStages) {
+                stage -= kStages;
+                phase ^= 1;
+            }
+        };
+        auto next_slot = [](int slot) { return slot + 1 == G_::kSlots ? 0 : slot + 1; };
+        while (w.next(bars, item, ok)) {
+            const int nb = __shfl_sync(0xffffffffu, w.x.n_blocks, 0);
+            const int two = __shfl_sync(0xffffffffu, w.x.has_b, 0);
+            const int dual = __shfl_sync(0xffffffffu, w.x.dual, 0);
+            const int last_cols = (__shfl_sync(0xffffffffu, w.x.n_keys, 0) - (nb - 1) * kBN + 15) & ~15;
+            if (!ok || nb == 0)
+                continue;
+            const uint32_t idesc_last = umma_idesc_bf16(kM, last_cols, 0);
+            int vst = kst;
+            uint32_t vph = kph;
+            advance(vst, vph, nb == 1 ? 1 : 2);
+            // S of tile t's block b (K at the current stage) into the next slot
+            auto scores = [&](int t, int q, int b) {
+                tc_fence_after_sync();
+                issue_qk(s_slot, q, kst, b + 1 == nb ? idesc_last : kIdescQK);
+                commit(kBarSFull + 2 * t + (s_count[t] & 1));
+                if (b + 1 == nb)
+                    commit(kBarQEmpty + q);
+                ++s_count[t];
+                s_slot = next_slot(s_slot);
+            };
+            // PV of tile t's block b (V at the current stage) once its P is there
+            auto products = [&](int t, int b, bool first) {
+                wait(kBarPFull + 2 * t + (p_count[t] & 1), (p_count[t] >> 1) & 1);
+                tc_fence_after_sync();
+                issue_pv(t, p_slot, vst, b + 1 == nb ? last_cols / 16 : kBN / 16, first ? 0u : 1u);
+                ++p_count[t];
+                p_slot = next_slot(p_slot);
+            };
+            auto next_k = [&](int b) {   // from K(b - 1) to K(b)
+                advance(kst, kph, b == 1 ? 1 : 2);
+                wait(kBarKvFull + kst, kph);
+            };
+            wait(kBarQFull, q_count[0] & 1);
+            wait(kBarKvFull + kst, kph);
+            if (dual) {
+                // block b is a unit of tile b % 2, in the order S(0) .. S(kSlots - 1), PV(0), S(kSlots), PV(1), ...
+                for (int b = -G_::kSlots; b < nb; ++b) {
+                    if (b >= 0) {
+                        wait(kBarKvFull + vst, vph);
+                        if (b & 1)
+                            products(1, b, b < 2);
+                        else
+                            products(0, b, b < 2);
+                        commit(kBarKvEmpty + vst);
+                        if (G_::kSlots > 2 || b + 2 >= nb)
+                            commit(kBarPvDone + (b & 1));
+                        advance(vst, vph, b + 2 >= nb ? 1 : 2);
+                    }
+                    const int next = b + G_::kSlots;
+                    if (next < nb) {
+                        if (next > 0)
+                            next_k(next);
+                        if (next & 1)
+                            scores(1, 0, next);
+                        else
+                            scores(0, 0, next);
+                        commit(kBarKvEmpty + kst);
+                    }
+                }
+            } else {
+                // units in the order S(0) .. S(kSlots - 1), PV(0), S(kSlots), PV(1), ..., S right behind the
+                // product that has read P from its slot; K is done with after tile 1's S
+                scores(0, 0, 0);
+                if (two) {
+                    wait(kBarQFull + 1, q_count[1] & 1);
+                    scores(1, 1, 0);
+                }
+                commit(kBarKvEmpty + kst);
+                if (G_::kSlots == 3 && nb > 1) {
+                    next_k(1);
+                    scores(0, 0, 1);
+                }
+                for (int b = 0; b < nb; ++b) {
+                    wait(kBarKvFull + vst, vph);
+                    products(0, b, b == 0);
+                    if (G_::kSlots > 2 || b + 1 == nb)
+                        commit(kBarPvDone);
+                    if (G_::kSlots == 2 && b + 1 < nb) {
+                        next_k(b + 1);
+                        scores(0, 0, b + 1);
+                    } else if (G_::kSlots == 3 && b + 1 < nb) {
+                        scores(1, 1, b + 1);
+                        commit(kBarKvEmpty + kst);
+                    }
+                    if (two) {
+                        products(1, b, b == 0);
+                        if (G_::kSlots > 2 || b + 1 == nb)
+                            commit(kBarPvDone + 1);
+                        if (G_::kSlots == 2 && b + 1 < nb) {
+                            scores(1, 1, b + 1);
+                            commit(kBarKvEmpty + kst);
+                        } else if (G_::kSlots == 3 && b + 2 < nb) {
+                            next_k(b + 2);
+                            scores(0, 0, b + 2);
+                        }
+                    }
+                    commit(kBarKvEmpty + vst);
+                    advance(vst, vph, b + 2 >= nb ? 1 : 2);
+                }
+                if (two)
+                    ++q_count[1];
+            }
+            ++q_count[0];
+            // behind the last V the next item's K(0)
+            kst = vst;
+            kph = vph;
+            ok = !__any_sync(0xffffffffu, failed != 0);
         }
+        if (!ok && lane == 0)
+            atomicOr(err_word, kErrCrossWait);
+        // every product that was issued must be complete before TMEM is released
+        commit(kBarDrain);
+        if (!mbar_wait(&bars[kBarDrain], 0) && lane == 0)
+            atomicOr(err_word, kErrDrainWait);
         __syncwarp();
     } else if (elect_one()) {
         // ------------------------------ items and query loads ------------------------------
@@ -515,8 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quad = warp & 3;                   // TMEM lanes 32 quad ..
         const int row = quad * 32 + lane;            // row of the tile = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t tmem_o = tmem + lane_off + half * (D / 2);   // tile 0's; tile 1's 256 columns on
-        const uint32_t tmem_s = tmem + t * 256 + G_::kColS + lane_off + half * (kBN / 2);
+        const uint32_t tmem_o = tmem + lane_off + half * (D / 2);   // tile 0's; tile 1's D columns on
         float *exchange = reinterpret_cast<float *>(smem + G_::kOffExchange);
         float *mine = exchange + (t * 2 + half) * kM + row, *other = exchange + (t * 2 + 1 - half) * kM + row;
         const uint32_t pair_bar = 1 + t * 4 + quad;  // the two warps of the same rows
@@ -532,7 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int tb = 0;   // blocks of this tile so far
         int ti = 0;   // items of this tile so far
         int n0 = 0;   // ring index of the item's first slot
-        for (;; n0 += 2 * w.x.n_blocks) {
+        int u0 = 0;   // units of the CTA before the item
+        for (;; n0 += 2 * w.x.n_blocks, u0 += w.x.units()) {
             bool got = true;
             const bool going = w.next(bars, item, got);
             // all softmax warps go on or none: they meet at named barriers
@@ -552,7 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_used = -INFINITY, l = 0.0f;
             const int b0 = x.dual ? t : 0;
             for (int b = b0; b < x.n_blocks; b += x.dual ? 2 : 1, ++tb) {
-                wait(&bars[kBarSFull + t], tb & 1);
+                const uint32_t slot = static_cast<uint32_t>(u0 + (x.has_b ? 2 * b + t : b)) % G_::kSlots;
+                const uint32_t tmem_s = tmem + G_::kColS + slot * kBN + lane_off + half * (kBN / 2);
+                // A barrier for every other block of the tile: S of the next may be ready before this one was
+                // waited for, S of the one after that comes behind this one's P.
+                wait(&bars[kBarSFull + 2 * t + (tb & 1)], (tb >> 1) & 1);
                 tc_fence_after_sync();
                 const int n_vis = min(x.n_keys - b * kBN, kBN);   // positions of this block
                 if ((n_vis & 15) != 0 && half == 0 && (x.dual || t == 0)) {
@@ -627,18 +659,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         l *= alpha;
                         tmem_wait_st();
-                        // O holds every earlier PV product (S(b) was committed after them): its columns of
-                        // this half are rescaled in place
+                        // O holds every earlier PV product (with two slots S(b) was committed after them): its
+                        // columns of this half are rescaled in place
                         if (b > b0) {
+                            if (G_::kSlots > 2) {
+                                wait(&bars[kBarPvDone + t], (tb - 1) & 1);
+                                tc_fence_after_sync();
+                            }
 #pragma unroll 1
                             for (int c0 = 0; c0 < D / 2; c0 += 16) {
                                 float o[16];
-                                tmem_ld16(tmem_o + t * 256 + c0, o);
+                                tmem_ld16(tmem_o + t * D + c0, o);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int j = 0; j < 16; ++j)
                                     o[j] *= alpha;
-                                tmem_st16(tmem_o + t * 256 + c0, o);
+                                tmem_st16(tmem_o + t * D + c0, o);
                             }
                         }
                         sum2[0] = sum2[1] = f2_pack(0.0f, 0.0f);
@@ -661,11 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&bars[(half == 0 ? kBarPHalf : kBarPFull) + t]);
+                    mbar_arrive(&bars[kBarPFull + 2 * t + (tb & 1)]);
             }
             // epilogue: once this tile's last PV is done, O / l -> global
             if (x.n_blocks > 0) {
-                wait(&bars[kBarPvDone + t], ti & 1);
+                wait(&bars[kBarPvDone + t], (G_::kSlots > 2 ? tb - 1 : ti) & 1);
                 ++ti;
                 tc_fence_after_sync();
             }
@@ -715,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 16; ++j)
                     o[j] = 0.0f;
                 if (x.n_blocks > 0) {
-                    tmem_ld16(tmem_o + (x.dual ? 0 : t * 256) + c0, o);
+                    tmem_ld16(tmem_o + (x.dual ? 0 : t * D) + c0, o);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -723,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (x.dual) {
                     float o1[16];
-                    tmem_ld16(tmem_o + 256 + c0, o1);
+                    tmem_ld16(tmem_o + D + c0, o1);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 16; ++j)

@@ -126,6 +126,24 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity)
     return true;
 }
 
+// The same without a branch on the result: `failed` becomes 1 where the wait ran out, and where it is 1 already
+// the barrier is only looked at once.
+__device__ __forceinline__ void mbar_wait_plain(uint64_t *bar, uint32_t parity, uint32_t &failed)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .u64 t0, t1;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "mov.u64 t0, %%clock64;\n"
+        "AGAIN:\n\tsetp.ne.u32 p, %0, 0;\n\t@p bra DONE;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "mov.u64 t1, %%clock64;\n\tsub.u64 t1, t1, t0;\n\tsetp.gt.u64 p, t1, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tbra AGAIN;\n"
+        "DONE:\n\t}"
+        : "+r"(failed)
+        : "r"(smem_addr(bar)), "r"(parity), "l"(static_cast<uint64_t>(kWaitLimitCycles))
+        : "memory");
+}
+
 // The same for waits that are as long as another warp's work item may be: gives up after 64 times as long.
 __device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity)
 {
@@ -237,13 +255,6 @@ __device__ __forceinline__ uint64_t l2_policy_evict_normal()
     return policy;
 }
 
-__device__ __forceinline__ uint64_t l2_policy_evict_last()
-{
-    uint64_t policy;
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
-    return policy;
-}
-
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -308,6 +319,16 @@ __device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t smem_byte_addr, uin
     d |= 1ull << 46;   // descriptor version for tcgen05
     d |= 2ull << 61;   // 128-byte swizzle
     return d;
+}
+
+// The same in two parts, of which only the low word depends on the address (and grows with it, 16 bytes a unit).
+__device__ __forceinline__ uint32_t umma_desc_sw128_low(uint32_t smem_byte_addr, uint32_t lbo)
+{
+    return ((smem_byte_addr & 0x3FFFFu) >> 4) | (((lbo >> 4) & 0x3FFFu) << 16);
+}
+__host__ __device__ constexpr uint64_t umma_desc_sw128_high(uint32_t sbo)
+{
+    return (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
 // Instruction descriptor, kind::f16: bf16 A and B, fp32 D, M x N, K-major A; B K-major
