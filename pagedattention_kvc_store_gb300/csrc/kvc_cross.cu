@@ -19,7 +19,7 @@
 //   warp 3      the items (cancels blocks of the grid that have not started and hands theirs round), and
 //               their query tiles
 //   warps 4-11  softmax of tile 0, warps 12-19 of tile 1: two threads a row: the running maximum (O rescaled
-//               only when it grows by more than 2^8) and sum, P as bf16 over S's columns, and O / l at the end.
+//               only when p of the maximum before add up to more than 2^8) and sum, P as bf16 over S's columns, and O / l at the end.
 // An item of a single tile puts its blocks in turn on both halves of TMEM, so that the softmax of one runs
 // beside the products of the other as it does with two tiles, and joins the two at the end.
 // Few rows and many positions: the positions are cut into chunks (splits), partial rows and their
@@ -50,7 +50,7 @@ static_assert(kRoleWarps * kRoleRegs + kSoftmaxWarps * kSoftmaxRegs <=
                   (kRoleWarps + kSoftmaxWarps) * kLaunchRegs, "registers of the launch");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleLog2 = 8.0f;
+constexpr float kRescaleSum = 256.0f;   // of the p of a thread's 64 columns
 // named barriers of all softmax warps; 1 .. 8 are of the pairs
 constexpr uint32_t kBothTiles = 9, kAllSoftmax = 10;
 
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (warp_valid) {
                     const int n_mine = n_vis - half * (kBN / 2);   // of this thread's 64 columns
-                    float xs[2][32], mx[4];
+                    float xs[2][32];
                     uint64_t sum2[2];
                     auto mask = [&](int c) {
                         if (n_mine < kBN / 2) {
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     };
                     // p = 2^(s * scale * log2(e) - m) of 32 columns as bf16 pairs over the first of S's own
-                    // columns, their sum before the rounding, and the largest s
+                    // columns, and their sum before the rounding
                     auto probabilities = [&](int c) {
                         const float neg_mu = (m_used == -INFINITY) ? 0.0f : -m_used;
                         const uint64_t nm2 = f2_pack(neg_mu, neg_mu);
@@ -628,37 +628,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                             e1 = fast_exp2(e1);
                             pk[i] = pack_bf16x2(e0, e1);
                             sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(e0, e1));
-                            mx[i & 3] = fmax3(mx[i & 3], x0, x1);
                         }
                         tmem_st16u(tmem_s + 16 * c, pk);
                     };
                     sum2[0] = sum2[1] = f2_pack(0.0f, 0.0f);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mx[j] = -INFINITY;
-                    // With the maximum of the blocks before, which nearly always still holds (it may be
-                    // passed by 2^8); whether it does for the rows' two warps is known while P is on its way.
-                    // S's columns 32 .. 63 stay in TMEM and 0 .. 31 in registers for the case that it does not.
+                    // With the maximum of the blocks before, which nearly always still holds; whether it does
+                    // (no sum of a thread's 64 is past 2^8, then no p is) is known for the rows' two warps while
+                    // P is on its way.  S's columns 32 .. 63 stay in TMEM and 0 .. 31 in registers for the case
+                    // that it does not.  The first block has none before it.
                     tmem_ld32(tmem_s, xs[0]);
                     tmem_ld32(tmem_s + 32, xs[1]);
                     tmem_wait_ld();
                     mask(0);
                     mask(1);
-                    probabilities(1);
-                    probabilities(0);
-                    float mb = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl2;   // base 2
-                    const bool again = barrier_or(pair_bar, 64, mb > m_used + kRescaleLog2);
+                    bool again = true;
+                    if (b > b0) {
+                        probabilities(1);
+                        probabilities(0);
+                        float p0, p1;
+                        f2_unpack(f2_add(sum2[0], sum2[1]), p0, p1);
+                        again = barrier_or(pair_bar, 64, !(p0 + p1 <= kRescaleSum) || m_used == -INFINITY);
+                    }
                     if (again) {
+                        tmem_wait_st();
+                        tmem_ld32(tmem_s + 32, xs[1]);
+                        tmem_wait_ld();
+                        mask(1);
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            mx[i & 3] = fmax3(mx[i & 3], xs[0][i], xs[1][i]);
+                        float mb = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl2;   // base 2
                         *mine = mb;
                         named_barrier(pair_bar, 64);
                         mb = fmaxf(mb, *other);
                         float alpha = 1.0f;
-                        if (mb > m_used + kRescaleLog2) {
+                        if (mb > m_used) {
                             alpha = (m_used == -INFINITY) ? 0.0f : fast_exp2(m_used - mb);
                             m_used = mb;
                         }
                         l *= alpha;
-                        tmem_wait_st();
                         // O holds every earlier PV product (with two slots S(b) was committed after them): its
                         // columns of this half are rescaled in place
                         if (b > b0) {
@@ -678,9 +687,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         sum2[0] = sum2[1] = f2_pack(0.0f, 0.0f);
-                        tmem_ld32(tmem_s + 32, xs[1]);
-                        tmem_wait_ld();
-                        mask(1);
                         probabilities(1);
                         probabilities(0);
                         tmem_wait_st();
