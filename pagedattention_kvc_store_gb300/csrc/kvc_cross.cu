@@ -52,7 +52,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleSum = 256.0f;   // of the p of a thread's 64 columns
 // named barriers of all softmax warps; 1 .. 8 are of the pairs
-constexpr uint32_t kBothTiles = 9, kAllSoftmax = 10;
+constexpr uint32_t kBothTiles = 9;
+constexpr int kItemWaits = 6;   // warp 3's waits between two items: three long ones and a short one, and one at the end
 
 template <int D>
 struct Geom {
@@ -159,9 +160,12 @@ struct Feed {
     Item x;
     int n = 0;   // items read
     // Waits for the next item, which may be as long as the one before takes; false if that is too long.
-    __device__ __forceinline__ bool wait(uint64_t *bars)
+    __device__ __forceinline__ bool wait(uint64_t *bars, int times)
     {
-        return mbar_wait_long(&bars[kBarItemFull], n & 1);
+        bool there = false;
+        for (int i = 0; i < times && !there; ++i)
+            there = mbar_wait_long(&bars[kBarItemFull], n & 1);
+        return there;
     }
     __device__ __forceinline__ void read(const Item *slot)
     {
@@ -174,9 +178,9 @@ struct Feed {
         ++n;
     }
     // The same for a warp.  False at the end, or if the wait ran out (then ok is false).
-    __device__ __forceinline__ bool next(uint64_t *bars, const Item *slot, bool &ok)
+    __device__ __forceinline__ bool next(uint64_t *bars, const Item *slot, bool &ok, int times = 1)
     {
-        if (!__all_sync(0xffffffffu, wait(bars))) {
+        if (!__all_sync(0xffffffffu, wait(bars, times))) {
             ok = false;
             return false;
         }
@@ -561,14 +565,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n0 = 0;   // ring index of the item's first slot
         int u0 = 0;   // units of the CTA before the item
         for (;; n0 += 2 * w.x.n_blocks, u0 += w.x.units()) {
-            bool got = true;
-            const bool going = w.next(bars, item, got);
-            // all softmax warps go on or none: they meet at named barriers
-            if (barrier_or(kAllSoftmax, kSoftmaxWarps * 32, !got)) {
-                ok = false;
-                break;
-            }
-            if (!going)
+            // (The softmax warps meet at named barriers, so none may leave before the others: they wait for an
+            // item for longer than warp 3 can take to hand one round, the end included, with every wait of
+            // its own run out.  A barrier of all of them here kept tile 0 until tile 1 was written.)
+            if (!w.next(bars, item, ok, kItemWaits))
                 break;
             const Item &x = w.x;
             if (t == 1 && !x.has_b && !x.dual)
@@ -749,10 +749,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lse[out_row] = l == 0.0f ? -INFINITY : m_used * kLn2 + logf(l);   // no position: -inf
             if (x.n_blocks == 0 && a.n_split > 1)
                 continue;   // an empty split's row is not read
-            const int c_begin = x.dual ? t * (D / 4) : 0, c_end = x.dual ? c_begin + D / 4 : D / 2;
-#pragma unroll 1
-            for (int c0 = c_begin; c0 < c_end; c0 += 16) {
-                float o[16];
+            // Four lanes turn their rows' 64 bytes each into one row's 64 bytes at a time: 8 lines a store and not
+            // 32, of which the stores of both tiles took 4,096 cycles.  (Row numbers fit 32 bits: a row is 128
+            // bytes or more.)
+            const uint32_t no_row = 0xffffffffu;
+            uint32_t rows[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                rows[j] = __shfl_sync(0xffffffffu, valid ? static_cast<uint32_t>(out_row) : no_row, (lane & ~3) + j);
+            const size_t row_bytes = D * (out_f32 ? 4u : 2u);
+            // 16 words of each lane's row, `at` bytes into the row
+            auto put = [&](uint32_t (&v)[16], uint32_t at) {
+#pragma unroll
+                for (int bit = 1; bit <= 2; bit *= 2) {
+                    const bool upper = lane & bit;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c & bit)
+                            continue;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t &lo = v[4 * c + j], &hi = v[4 * (c + bit) + j];
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, bit);
+                            if (upper)
+                                lo = got;
+                            else
+                                hi = got;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (rows[j] != no_row)
+                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(out) + rows[j] * row_bytes + at +
+                                                   (lane & 3) * 16) =
+                            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            };
+            // joined halves: each tile's warps write half of their columns, or tile 0's all where that is under 32
+            constexpr bool kShare = D / 4 >= 32;
+            const int c_begin = x.dual && kShare ? t * (D / 4) : 0;
+            const int c_end = !x.dual ? D / 2 : kShare ? c_begin + D / 4 : t == 0 ? D / 2 : 0;
+            auto load = [&](int c0, float (&o)[16]) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     o[j] = 0.0f;
@@ -771,22 +808,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 16; ++j)
                         o[j] = fmaf(o1[j], f[1], o[j]);
                 }
-                if (valid) {
-                    const size_t at = out_row * D + half * (D / 2) + c0;
+            };
+#pragma unroll 1
+            for (int c0 = c_begin; c0 < c_end; c0 += out_f32 ? 16 : 32) {
+                float o[16];
+                uint32_t v[16];
+                load(c0, o);
+                if (out_f32) {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 8) {
-                        if (out_f32) {
-                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) + at + j);
-                            dst[0] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                            dst[1] = make_float4(o[j + 4], o[j + 5], o[j + 6], o[j + 7]);
-                        } else {
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + at + j) =
-                                make_uint4(pack_bf16x2(o[j], o[j + 1]), pack_bf16x2(o[j + 2], o[j + 3]),
-                                           pack_bf16x2(o[j + 4], o[j + 5]), pack_bf16x2(o[j + 6], o[j + 7]));
-                        }
-                    }
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = __float_as_uint(o[j]);
+                    put(v, (half * (D / 2) + c0) * 4);
+                    continue;
                 }
-                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
+                load(c0 + 16, o);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[8 + j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
+                put(v, (half * (D / 2) + c0) * 2);
             }
             tc_fence_before_sync();
             if (x.dual)   // nobody overwrites what the other still reads
