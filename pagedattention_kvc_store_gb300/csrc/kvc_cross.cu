@@ -185,10 +185,15 @@ struct Feed {
             return false;
         }
         read(slot);
+        if (times == 1)
+            has_read(bars);
+        return !x.done;
+    }
+    __device__ __forceinline__ void has_read(uint64_t *bars)
+    {
         __syncwarp();
         if ((threadIdx.x & 31) == 0)
             mbar_arrive(&bars[kBarItemEmpty]);
-        return !x.done;
     }
 };
 
@@ -571,6 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!w.next(bars, item, ok, kItemWaits))
                 break;
             const Item &x = w.x;
+            // That it has read the item a warp says behind its first scores: an arrival waits for the warp's
+            // stores, and the rows of the item before are still on their way.
+            if ((t == 1 && !x.has_b && !x.dual) || x.n_blocks == 0)
+                w.has_read(bars);
             if (t == 1 && !x.has_b && !x.dual)
                 continue;
             const int gr = x.row_begin + (x.dual ? 0 : t * kM) + row;
@@ -585,6 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // A barrier for every other block of the tile: S of the next may be ready before this one was
                 // waited for, S of the one after that comes behind this one's P.
                 wait(&bars[kBarSFull + 2 * t + (tb & 1)], (tb >> 1) & 1);
+                if (b == b0)
+                    w.has_read(bars);
                 tc_fence_after_sync();
                 const int n_vis = min(x.n_keys - b * kBN, kBN);   // positions of this block
                 if ((n_vis & 15) != 0 && half == 0 && (x.dual || t == 0)) {
@@ -789,46 +800,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr bool kShare = D / 4 >= 32;
             const int c_begin = x.dual && kShare ? t * (D / 4) : 0;
             const int c_end = !x.dual ? D / 2 : kShare ? c_begin + D / 4 : t == 0 ? D / 2 : 0;
-            auto load = [&](int c0, float (&o)[16]) {
+#pragma unroll 1
+            for (int c0 = c_begin; c0 < c_end; c0 += 32) {
+                float o[32];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int j = 0; j < 32; ++j)
                     o[j] = 0.0f;
                 if (x.n_blocks > 0) {
-                    tmem_ld16(tmem_o + (x.dual ? 0 : t * D) + c0, o);
+                    tmem_ld32(tmem_o + (x.dual ? 0 : t * D) + c0, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < 32; ++j)
                         o[j] *= f[0];
                 }
                 if (x.dual) {
-                    float o1[16];
-                    tmem_ld16(tmem_o + D + c0, o1);
+                    float o1[32];
+                    tmem_ld32(tmem_o + D + c0, o1);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < 32; ++j)
                         o[j] = fmaf(o1[j], f[1], o[j]);
                 }
-            };
-#pragma unroll 1
-            for (int c0 = c_begin; c0 < c_end; c0 += out_f32 ? 16 : 32) {
-                float o[16];
                 uint32_t v[16];
-                load(c0, o);
                 if (out_f32) {
 #pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = __float_as_uint(o[16 * i + j]);
+                        put(v, (half * (D / 2) + c0 + 16 * i) * 4);
+                    }
+                } else {
+#pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        v[j] = __float_as_uint(o[j]);
-                    put(v, (half * (D / 2) + c0) * 4);
-                    continue;
+                        v[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
+                    put(v, (half * (D / 2) + c0) * 2);
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
-                load(c0 + 16, o);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[8 + j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
-                put(v, (half * (D / 2) + c0) * 2);
             }
             tc_fence_before_sync();
             if (x.dual)   // nobody overwrites what the other still reads
