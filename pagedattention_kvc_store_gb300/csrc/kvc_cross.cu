@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto wait = [&](int bar, uint32_t parity) { mbar_wait_plain(&bars[bar], parity, failed); };
         // S = Q_q K^T into a score slot, K at a stage
         auto issue_qk = [&](int slot, int q, int stage, uint32_t idesc) {
-            const uint32_t low = q_low + q * (G_::kQBytes / 16), k_low = ring_k + stage * kStageLo;
+            uint32_t low = q_low + q * (G_::kQBytes / 16), k_low = ring_k + stage * kStageLo;
+            asm volatile("" : "+r"(low));   // or all of Q's descriptors are kept in registers, and spill
             const uint32_t d = tm + G_::kColS + slot * kBN;
             if (leader) {
 #pragma unroll
