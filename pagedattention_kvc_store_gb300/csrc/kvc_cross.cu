@@ -341,12 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < kBN / 16; ++k)
-                        umma_bf16_ts(d, p + (k >> 2) * (kBN / 2) + (k & 3) * 8, kHighKv | (v_low + k * kStep), kIdescPV,
+                        umma_bf16_ts(d, p + k * 8, kHighKv | (v_low + k * kStep), kIdescPV,
                                      k > 0 ? 1u : keep);
                 }
             } else if (leader) {
                 for (int k = 0; k < k_steps; ++k)
-                    umma_bf16_ts(d, p + (k >> 2) * (kBN / 2) + (k & 3) * 8, kHighKv | (v_low + k * kStep), kIdescPV,
+                    umma_bf16_ts(d, p + k * 8, kHighKv | (v_low + k * kStep), kIdescPV,
                                  k > 0 ? 1u : keep);
             }
         };
@@ -546,17 +546,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------ softmax + epilogue -------------------------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        // Two threads to a row, one for each half of a block's columns (and of O's): the one warp of a
-        // scheduler that had whole rows took 1,750 cycles from S to P, and the tensor pipe waited.
+        // A warp has 16 rows, a thread every fourth pair of columns of two of them (the 16-lane shapes of tensor
+        // memory): all of a row is in one warp, which decides by a vote.  (Two warps with 32 rows and half of the
+        // columns each met at a barrier for every block; one warp of a scheduler with 32 whole rows took 1,750
+        // cycles from S to P, and the tensor pipe waited.)
         const int t = (warp - kRoleWarps) >> 3;      // tile
         const int half = ((warp - kRoleWarps) >> 2) & 1;
-        const int quad = warp & 3;                   // TMEM lanes 32 quad ..
-        const int row = quad * 32 + lane;            // row of the tile = TMEM lane
-        const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t tmem_o = tmem + lane_off + half * (D / 2);   // tile 0's; tile 1's D columns on
-        float *exchange = reinterpret_cast<float *>(smem + G_::kOffExchange);
-        float *mine = exchange + (t * 2 + half) * kM + row, *other = exchange + (t * 2 + 1 - half) * kM + row;
-        const uint32_t pair_bar = 1 + t * 4 + quad;  // the two warps of the same rows
+        const int quad = warp & 3;                   // TMEM lanes 32 quad + 16 half ..
+        const int row0 = quad * 32 + half * 16 + (lane >> 2);   // rows row0 and row0 + 8 of the tile
+        const int col = 2 * (lane & 3);              // columns col, col + 1 of every 8
+        const uint32_t tmem_w = tmem + (static_cast<uint32_t>(quad * 32 + half * 16) << 16);
+        float *exchange = reinterpret_cast<float *>(smem + G_::kOffExchange);   // [m, l][tile][row]
         const float sl2 = a.scale_log2;
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
         // A wait that runs out is the last one: the warp then goes through the rest of its items without
@@ -583,15 +583,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w.has_read(bars);
             if (t == 1 && !x.has_b && !x.dual)
                 continue;
-            const int gr = x.row_begin + (x.dual ? 0 : t * kM) + row;
-            const bool valid = gr < x.rows;
-            const int tok = gr / G;
-            const bool warp_valid = __any_sync(0xffffffffu, valid);   // the same in both warps of the rows
-            float m_used = -INFINITY, l = 0.0f;
+            const int gr = x.row_begin + (x.dual ? 0 : t * kM) + row0;
+            const bool warp_valid = __any_sync(0xffffffffu, gr < x.rows);
+            float m_used[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
             const int b0 = x.dual ? t : 0;
             for (int b = b0; b < x.n_blocks; b += x.dual ? 2 : 1, ++tb) {
                 const uint32_t slot = static_cast<uint32_t>(u0 + (x.has_b ? 2 * b + t : b)) % G_::kSlots;
-                const uint32_t tmem_s = tmem + G_::kColS + slot * kBN + lane_off + half * (kBN / 2);
+                const uint32_t tmem_s = tmem_w + G_::kColS + slot * kBN;
                 // A barrier for every other block of the tile: S of the next may be ready before this one was
                 // waited for, S of the one after that comes behind this one's P.
                 wait(&bars[kBarSFull + 2 * t + (tb & 1)], (tb >> 1) & 1);
@@ -614,42 +612,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                 }
                 if (warp_valid) {
-                    const int n_mine = n_vis - half * (kBN / 2);   // of this thread's 64 columns
-                    float xs[2][32];
-                    uint64_t sum2[2];
+                    float xs[2][32];     // columns 64 c + 8 g + col + j of row r: xs[c][4 g + 2 r + j]
+                    uint64_t sum2[2];    // of the two rows
                     auto mask = [&](int c) {
-                        if (n_mine < kBN / 2) {
+                        if (n_vis < kBN) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (32 * c + i >= n_mine)
+                                if (64 * c + 8 * (i >> 2) + (i & 1) + col >= n_vis)
                                     xs[c][i] = -INFINITY;
                         }
                     };
-                    // p = 2^(s * scale * log2(e) - m) of 32 columns as bf16 pairs over the first of S's own
-                    // columns, and their sum before the rounding
+                    // p = 2^(s * scale * log2(e) - m) of 64 columns as bf16 pairs over the first of S's columns,
+                    // and their sum before the rounding
                     auto probabilities = [&](int c) {
-                        const float neg_mu = (m_used == -INFINITY) ? 0.0f : -m_used;
-                        const uint64_t nm2 = f2_pack(neg_mu, neg_mu);
+                        uint64_t nm2[2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float neg_mu = (m_used[r] == -INFINITY) ? 0.0f : -m_used[r];
+                            nm2[r] = f2_pack(neg_mu, neg_mu);
+                        }
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float x0 = xs[c][2 * i], x1 = xs[c][2 * i + 1];
                             float e0, e1;
-                            f2_unpack(f2_fma(f2_pack(x0, x1), sl2x2, nm2), e0, e1);
+                            f2_unpack(f2_fma(f2_pack(xs[c][2 * i], xs[c][2 * i + 1]), sl2x2, nm2[i & 1]), e0, e1);
                             e0 = fast_exp2(e0);
                             e1 = fast_exp2(e1);
                             pk[i] = pack_bf16x2(e0, e1);
                             sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(e0, e1));
                         }
-                        tmem_st16u(tmem_s + 16 * c, pk);
+                        tmem_st_16x128_x8(tmem_s + 32 * c, pk);
+                    };
+                    auto sum_of = [&](int r) {
+                        float p0, p1;
+                        f2_unpack(sum2[r], p0, p1);
+                        return p0 + p1;
                     };
                     sum2[0] = sum2[1] = f2_pack(0.0f, 0.0f);
                     // With the maximum of the blocks before, which nearly always still holds; whether it does
-                    // (no sum of a thread's 64 is past 2^8, then no p is) is known for the rows' two warps while
-                    // P is on its way.  S's columns 32 .. 63 stay in TMEM and 0 .. 31 in registers for the case
-                    // that it does not.  The first block has none before it.
-                    tmem_ld32(tmem_s, xs[0]);
-                    tmem_ld32(tmem_s + 32, xs[1]);
+                    // (no sum of a thread's 32 is past 2^8, then no p is) is known while P is on its way.  S's
+                    // columns 64 .. 127 stay in TMEM and 0 .. 63 in registers for the case that it does not.
+                    // The first block has none before it.
+                    tmem_ld_16x256_x8(tmem_s, xs[0]);
+                    tmem_ld_16x256_x8(tmem_s + 64, xs[1]);
                     tmem_wait_ld();
                     mask(0);
                     mask(1);
@@ -657,58 +662,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (b > b0) {
                         probabilities(1);
                         probabilities(0);
-                        float p0, p1;
-                        f2_unpack(f2_add(sum2[0], sum2[1]), p0, p1);
-                        again = barrier_or(pair_bar, 64, !(p0 + p1 <= kRescaleSum) || m_used == -INFINITY);
+                        again = __any_sync(0xffffffffu, !(sum_of(0) <= kRescaleSum) || !(sum_of(1) <= kRescaleSum) ||
+                                                            fminf(m_used[0], m_used[1]) == -INFINITY);
                     }
                     if (again) {
                         tmem_wait_st();
-                        tmem_ld32(tmem_s + 32, xs[1]);
+                        tmem_ld_16x256_x8(tmem_s + 64, xs[1]);
                         tmem_wait_ld();
                         mask(1);
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        float alpha[2];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            mx[i & 3] = fmax3(mx[i & 3], xs[0][i], xs[1][i]);
-                        float mb = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl2;   // base 2
-                        *mine = mb;
-                        named_barrier(pair_bar, 64);
-                        mb = fmaxf(mb, *other);
-                        float alpha = 1.0f;
-                        if (mb > m_used) {
-                            alpha = (m_used == -INFINITY) ? 0.0f : fast_exp2(m_used - mb);
-                            m_used = mb;
+                        for (int r = 0; r < 2; ++r) {
+                            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                            for (int g = 0; g < 8; ++g) {
+                                m0 = fmax3(m0, xs[0][4 * g + 2 * r], xs[0][4 * g + 2 * r + 1]);
+                                m1 = fmax3(m1, xs[1][4 * g + 2 * r], xs[1][4 * g + 2 * r + 1]);
+                            }
+                            m0 = fmaxf(m0, m1);
+                            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
+                            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 2)) * sl2;   // base 2
+                            alpha[r] = 1.0f;
+                            if (m0 > m_used[r]) {
+                                alpha[r] = (m_used[r] == -INFINITY) ? 0.0f : fast_exp2(m_used[r] - m0);
+                                m_used[r] = m0;
+                            }
+                            l[r] *= alpha[r];
                         }
-                        l *= alpha;
                         // O holds every earlier PV product (with two slots S(b) was committed after them): its
-                        // columns of this half are rescaled in place
+                        // rows of this warp are rescaled in place
                         if (b > b0) {
                             if (G_::kSlots > 2) {
                                 wait(&bars[kBarPvDone + t], (tb - 1) & 1);
                                 tc_fence_after_sync();
                             }
 #pragma unroll 1
-                            for (int c0 = 0; c0 < D / 2; c0 += 16) {
+                            for (int c0 = 0; c0 < D; c0 += 32) {
                                 float o[16];
-                                tmem_ld16(tmem_o + t * D + c0, o);
+                                tmem_ld_16x256_x4(tmem_w + t * D + c0, o);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int j = 0; j < 16; ++j)
-                                    o[j] *= alpha;
-                                tmem_st16(tmem_o + t * D + c0, o);
+                                    o[j] *= alpha[(j >> 1) & 1];
+                                tmem_st_16x256_x4(tmem_w + t * D + c0, o);
                             }
                         }
                         sum2[0] = sum2[1] = f2_pack(0.0f, 0.0f);
                         probabilities(1);
                         probabilities(0);
-                        tmem_wait_st();
-                        tc_fence_before_sync();
-                        named_barrier(pair_bar, 64);
-                        tc_fence_after_sync();
                     }
-                    float p0, p1;
-                    f2_unpack(f2_add(sum2[0], sum2[1]), p0, p1);
-                    l += p0 + p1;
+                    l[0] += sum_of(0);
+                    l[1] += sum_of(1);
                     tmem_wait_st();
                 }
                 // (rows of padding: whatever P holds stays in rows of O that nobody reads)
@@ -723,119 +727,115 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++ti;
                 tc_fence_after_sync();
             }
-            *mine = l;
-            named_barrier(pair_bar, 64);
-            l += *other;
-            named_barrier(pair_bar, 64);
-            float f[2] = {1.0f, 0.0f};   // weights of the two halves of TMEM
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            }
+            float f[2][2] = {{1.0f, 1.0f}, {0.0f, 0.0f}};   // weights of the two halves of TMEM, for both rows
             if (x.dual) {
-                // (m, l) of both, read by both; each writes half of its thread's columns
-                *mine = half == 0 ? m_used : l;
+                // (m, l) of both, read by both; each writes half of the columns
+                if ((lane & 3) == 0) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        exchange[t * kM + row0 + 8 * r] = m_used[r];
+                        exchange[(2 + t) * kM + row0 + 8 * r] = l[r];
+                    }
+                }
                 tc_fence_before_sync();
                 named_barrier(kBothTiles, kSoftmaxWarps * 32);
                 tc_fence_after_sync();
-                const float m0 = exchange[row], l0 = exchange[kM + row];
-                const float m1 = exchange[2 * kM + row], l1 = exchange[3 * kM + row];
-                m_used = fmaxf(m0, m1);
-                f[0] = m0 == -INFINITY && m_used != m0 ? 0.0f : fast_exp2(m0 - m_used);
-                f[1] = m1 == -INFINITY && m_used != m1 ? 0.0f : fast_exp2(m1 - m_used);
-                if (m_used == -INFINITY)   // no score above -inf (or NaN alone, which l and O hold)
-                    f[0] = f[1] = 1.0f;
-                l = l0 * f[0] + l1 * f[1];
-            }
-            const float inv = (l == 0.0f) ? 0.0f : 1.0f / l;
-            f[0] *= inv;
-            f[1] *= inv;
-            size_t out_row = static_cast<size_t>(x.tok0 + tok) * a.q_heads +
-                             static_cast<size_t>(x.kvh) * G + (gr - tok * G);
-            void *out = a.out;
-            int out_f32 = a.out_f32;
-            float *lse = a.lse;
-            if (a.n_split > 1) {
-                out_row = out_row * a.n_split + x.split;
-                out = a.part_o;
-                out_f32 = 1;
-                lse = a.part_lse;
-            }
-            if (valid && lse != nullptr && half == 0 && !(x.dual && t == 1))
-                lse[out_row] = l == 0.0f ? -INFINITY : m_used * kLn2 + logf(l);   // no position: -inf
-            if (x.n_blocks == 0 && a.n_split > 1)
-                continue;   // an empty split's row is not read
-            // Four lanes turn their rows' 64 bytes each into one row's 64 bytes at a time: 8 lines a store and not
-            // 32, of which the stores of both tiles took 4,096 cycles.  (Row numbers fit 32 bits: a row is 128
-            // bytes or more.)
-            const uint32_t no_row = 0xffffffffu;
-            uint32_t rows[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                rows[j] = __shfl_sync(0xffffffffu, valid ? static_cast<uint32_t>(out_row) : no_row, (lane & ~3) + j);
-            const size_t row_bytes = D * (out_f32 ? 4u : 2u);
-            // 16 words of each lane's row, `at` bytes into the row
-            auto put = [&](uint32_t (&v)[16], uint32_t at) {
-#pragma unroll
-                for (int bit = 1; bit <= 2; bit *= 2) {
-                    const bool upper = lane & bit;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (c & bit)
-                            continue;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t &lo = v[4 * c + j], &hi = v[4 * (c + bit) + j];
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, bit);
-                            if (upper)
-                                lo = got;
-                            else
-                                hi = got;
-                        }
-                    }
+                for (int r = 0; r < 2; ++r) {
+                    const float *at = exchange + row0 + 8 * r;
+                    const float m0 = at[0], m1 = at[kM];
+                    m_used[r] = fmaxf(m0, m1);
+                    f[0][r] = m0 == -INFINITY && m_used[r] != m0 ? 0.0f : fast_exp2(m0 - m_used[r]);
+                    f[1][r] = m1 == -INFINITY && m_used[r] != m1 ? 0.0f : fast_exp2(m1 - m_used[r]);
+                    if (m_used[r] == -INFINITY)   // no score above -inf (or NaN alone, which l and O hold)
+                        f[0][r] = f[1][r] = 1.0f;
+                    l[r] = at[2 * kM] * f[0][r] + at[3 * kM] * f[1][r];
                 }
+            }
+            // rows of the output, or of the splits' results
+            const bool parts = a.n_split > 1;
+            uint8_t *out = static_cast<uint8_t *>(parts ? a.part_o : a.out);
+            const bool out_f32 = parts || a.out_f32;
+            float *lse = parts ? a.part_lse : a.lse;
+            uint8_t *to[2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (rows[j] != no_row)
-                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(out) + rows[j] * row_bytes + at +
-                                                   (lane & 3) * 16) =
-                            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            };
-            // joined halves: each tile's warps write half of their columns, or tile 0's all where that is under 32
-            constexpr bool kShare = D / 4 >= 32;
-            const int c_begin = x.dual && kShare ? t * (D / 4) : 0;
-            const int c_end = !x.dual ? D / 2 : kShare ? c_begin + D / 4 : t == 0 ? D / 2 : 0;
+            for (int r = 0; r < 2; ++r) {
+                const int at = gr + 8 * r, tok = at / G;
+                size_t out_row = static_cast<size_t>(x.tok0 + tok) * a.q_heads + static_cast<size_t>(x.kvh) * G +
+                                 (at - tok * G);
+                if (parts)
+                    out_row = out_row * a.n_split + x.split;
+                if (at < x.rows && lse != nullptr && (lane & 3) == 0 && !(x.dual && t == 1))
+                    lse[out_row] = l[r] == 0.0f ? -INFINITY : m_used[r] * kLn2 + logf(l[r]);   // no position: -inf
+                to[r] = at < x.rows ? out + out_row * (D * (out_f32 ? 4u : 2u)) : nullptr;
+                const float inv = (l[r] == 0.0f) ? 0.0f : 1.0f / l[r];
+                f[0][r] *= inv;
+                f[1][r] *= inv;
+            }
+            if (x.n_blocks == 0 && parts)
+                continue;   // an empty split's row is not read
+            const int c_begin = x.dual ? t * (D / 2) : 0, c_end = x.dual ? c_begin + D / 2 : D;
 #pragma unroll 1
             for (int c0 = c_begin; c0 < c_end; c0 += 32) {
-                float o[32];
+                float o[16];   // columns c0 + 8 g + col + j of row r: o[4 g + 2 r + j]
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < 16; ++j)
                     o[j] = 0.0f;
                 if (x.n_blocks > 0) {
-                    tmem_ld32(tmem_o + (x.dual ? 0 : t * D) + c0, o);
+                    tmem_ld_16x256_x4(tmem_w + (x.dual ? 0 : t * D) + c0, o);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        o[j] *= f[0];
-                }
-                if (x.dual) {
-                    float o1[32];
-                    tmem_ld32(tmem_o + D + c0, o1);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        o[j] = fmaf(o1[j], f[1], o[j]);
-                }
-                uint32_t v[16];
-                if (out_f32) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            v[j] = __float_as_uint(o[16 * i + j]);
-                        put(v, (half * (D / 2) + c0 + 16 * i) * 4);
-                    }
-                } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        v[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
-                    put(v, (half * (D / 2) + c0) * 2);
+                        o[j] *= f[0][(j >> 1) & 1];
+                }
+                if (x.dual) {
+                    float o1[16];
+                    tmem_ld_16x256_x4(tmem_w + D + c0, o1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        o[j] = fmaf(o1[j], f[1][(j >> 1) & 1], o[j]);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    if (out_f32) {
+                        if (to[r] != nullptr) {
+#pragma unroll
+                            for (int g = 0; g < 4; ++g)
+                                *reinterpret_cast<float2 *>(to[r] + (c0 + 8 * g + col) * 4) =
+                                    make_float2(o[4 * g + 2 * r], o[4 * g + 2 * r + 1]);
+                        }
+                        continue;
+                    }
+                    // the four lanes of a row turn their words, one of every group of 8 columns each, into
+                    // 16 bytes of one group each: 64 bytes of a row at a time (8 lines a store, not 32, of
+                    // which the stores of both tiles took 4,096 cycles)
+                    uint32_t v[4];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        v[g] = pack_bf16x2(o[4 * g + 2 * r], o[4 * g + 2 * r + 1]);
+#pragma unroll
+                    for (int bit = 1; bit <= 2; bit *= 2) {
+                        const bool upper = lane & bit;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            if (g & bit)
+                                continue;
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? v[g] : v[g + bit], bit);
+                            if (upper)
+                                v[g] = got;
+                            else
+                                v[g + bit] = got;
+                        }
+                    }
+                    if (to[r] != nullptr)
+                        *reinterpret_cast<uint4 *>(to[r] + c0 * 2 + (lane & 3) * 16) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
                 }
             }
             tc_fence_before_sync();
