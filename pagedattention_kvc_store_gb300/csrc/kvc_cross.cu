@@ -99,8 +99,8 @@ enum BarIndex : int {
     kBarQEmpty = kBarQFull + 2,             // [tile], one MMA commit after its last S product
     kBarSFull = kBarQEmpty + 2,             // [tile][its blocks in turn]
     kBarPFull = kBarSFull + 4,              // [tile][its blocks in turn], an arrival of each of its eight warps
-    kBarPvDone = kBarPFull + 4,             // [tile], once per item with two slots, once per block with three
-    kBarDrain = kBarPvDone + 2,
+    kBarPvDone = kBarPFull + 4,             // [tile][its blocks in turn]
+    kBarDrain = kBarPvDone + 4,
     kBarItemFull = kBarDrain + 1,           // the item in shared memory is the next one
     kBarItemEmpty = kBarItemFull + 1,       // an arrival of every warp that reads items
     kBarCancel = kBarItemEmpty + 1,         // the answer to a request for a block that has not started
@@ -394,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(kBarPFull + 2 * t + (p_count[t] & 1), (p_count[t] >> 1) & 1);
                 tc_fence_after_sync();
                 issue_pv(t, p_slot, vst, b + 1 == nb ? last_cols / 16 : kBN / 16, first ? 0u : 1u);
+                commit(kBarPvDone + 2 * t + (p_count[t] & 1));
                 ++p_count[t];
                 p_slot = next_slot(p_slot);
             };
@@ -413,8 +414,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else
                             products(0, b, b < 2);
                         commit(kBarKvEmpty + vst);
-                        if (G_::kSlots > 2 || b + 2 >= nb)
-                            commit(kBarPvDone + (b & 1));
                         advance(vst, vph, b + 2 >= nb ? 1 : 2);
                     }
                     const int next = b + G_::kSlots;
@@ -444,8 +443,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = 0; b < nb; ++b) {
                     wait(kBarKvFull + vst, vph);
                     products(0, b, b == 0);
-                    if (G_::kSlots > 2 || b + 1 == nb)
-                        commit(kBarPvDone);
                     if (G_::kSlots == 2 && b + 1 < nb) {
                         next_k(b + 1);
                         scores(0, 0, b + 1);
@@ -455,8 +452,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (two) {
                         products(1, b, b == 0);
-                        if (G_::kSlots > 2 || b + 1 == nb)
-                            commit(kBarPvDone + 1);
                         if (G_::kSlots == 2 && b + 1 < nb) {
                             scores(1, 1, b + 1);
                             commit(kBarKvEmpty + kst);
@@ -567,7 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         Feed w;
         int tb = 0;   // blocks of this tile so far
-        int ti = 0;   // items of this tile so far
+        // The products of the tile's last block before tb.  (S of block b is committed behind the products of
+        // block b - 2, no later ones: a barrier for every other block, or a wait for those of b - 1 could take the
+        // end of b - 2's for theirs.)
+        auto pv_wait = [&] { wait(&bars[kBarPvDone + 2 * t + ((tb - 1) & 1)], ((tb - 1) >> 1) & 1); };
         int n0 = 0;   // ring index of the item's first slot
         int u0 = 0;   // units of the CTA before the item
         for (;; n0 += 2 * w.x.n_blocks, u0 += w.x.units()) {
@@ -693,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // rows of this warp are rescaled in place
                         if (b > b0) {
                             if (G_::kSlots > 2) {
-                                wait(&bars[kBarPvDone + t], (tb - 1) & 1);
+                                pv_wait();
                                 tc_fence_after_sync();
                             }
 #pragma unroll 1
@@ -723,8 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // epilogue: once this tile's last PV is done, O / l -> global
             if (x.n_blocks > 0) {
-                wait(&bars[kBarPvDone + t], (G_::kSlots > 2 ? tb - 1 : ti) & 1);
-                ++ti;
+                pv_wait();
                 tc_fence_after_sync();
             }
 #pragma unroll

@@ -320,3 +320,70 @@ def test_results_do_not_depend_on_where_pages_lie(most):
     b.k[perm], b.v[perm], b.table = a.k, a.v, perm[a.table].astype(np.int32)
     for splits in (1, 2):
         assert all(torch.equal(x, y) for x, y in zip(a.run(splits=splits), b.run(splits=splits)))
+
+
+# q_len * G rows of a kv head: 100 in one tile, 400 in two pairs of tiles (the last without its second), 340
+# with a last tile of 84 rows
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("D,P,layout", [(64, 32, "hnd"), (128, 16, "nhd")])
+@pytest.mark.parametrize("most,sharp,top", [(50, 8.0, 3.0), (200, 8.0, 3.0), (170, 30.0, 1.0)])
+def test_a_growing_maximum_under_many_rows(most, sharp, top, D, P, layout, splits):
+    """Maxima that move by more than 2^8 from block to block, at different blocks for different rows, while
+    products of earlier blocks are in flight."""
+    c = Case([900, 129], [most, most // 2], 2, 2, D, P, layout, sharp=sharp)
+    k_max = 0.0
+    for s, n in enumerate(c.lens):
+        p = np.arange(n)
+        at = c.table[s][p // P], p % P
+        k = f32_from_bf16(c.k[at]) * np.linspace(0.1, top, n, dtype=np.float32)[:, None, None]
+        c.k[at] = torch.from_numpy(k).bfloat16().view(torch.int16).numpy().view(np.uint16)
+        k_max = max(k_max, np.abs(k).max())
+    out, lse = c.run(splits=splits)
+    want, logs, weighed = c.exact()
+    # fp32 sums of D products are off by up to D 2^-24 sum |q k| scale <= D 2^-24 D q k scale (2^-10 D q k scale
+    # 2^-20 with D <= 128: below `reach`)
+    reach = np.abs(c.q.float().numpy()).max() * k_max * D / math.sqrt(D) * 2.0 ** -20
+    assert np.isfinite(out.cpu().numpy()).all()
+    assert (np.abs(out.cpu().numpy() - want) <= (2.0 ** -7 + 2 * reach) * weighed + 1e-6).all()
+    assert (np.abs(lse.cpu().numpy() - logs) <= reach + 2.0 ** -14 + 2.0 ** -20 * np.abs(logs)).all()
+    assert kvc.kvc_device_errors() == 0
+
+
+@pytest.mark.parametrize("splits", [1, 4])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("most", [3, 60, 200])
+def test_scores_of_minus_infinity_before_the_first_finite_one(most, D, splits):
+    """Positions whose keys make every score -inf weigh nothing, be they whole blocks at the start, some
+    inside a block or the end; a source of nothing else gives zeros and -inf."""
+    c = Case([900, 140, 300], [most, most, most], 2, 2, D, 16)
+    c.q[..., 0] = c.q[..., 0].abs() + 0.25
+    minus = torch.tensor([-math.inf]).bfloat16().view(torch.int16).numpy().view(np.uint16)[0]
+    for s, gone in enumerate((list(range(0, 300)) + [301, 500, 899], [139], list(range(300)))):
+        p = np.array(gone)
+        c.k[c.table[s][p // 16], p % 16, :, 0] = minus
+    out, lse = c.run(splits=splits)
+    seen = slice(0, int(c.indptr[2]))
+    c.lens = c.lens[:2]
+    want, logs, weighed = c.exact()
+    x, y = out.cpu().numpy(), lse.cpu().numpy()
+    assert (np.abs(x - want) <= 2.0 ** -7 * weighed + 1e-6)[seen].all()
+    assert (np.abs(y[seen] - logs[seen]) <= 2.0 ** -14 + 2.0 ** -20 * np.abs(logs[seen])).all()
+    assert (x[c.indptr[2]:] == 0).all() and np.isneginf(y[c.indptr[2]:]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [1, 2])
+def test_nan_stays_with_its_row_among_many(splits, D):
+    c = Case([400, 700], [40, 200], 2, 2, D, 16)
+    q = c.q.clone()
+    q[1, 2, 5] = math.nan      # one tile
+    q[45, 1, 0] = math.nan     # two
+    out, lse = c.run(splits=splits, q=q)
+    bad = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
+    bad[1, 2] = bad[45, 1] = True
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    want, logs, weighed = c.exact()
+    err = np.abs(out.cpu().numpy() - want)
+    good = ~bad.cpu().numpy()
+    assert (err <= 2.0 ** -7 * weighed + 1e-6)[good].all()
+    assert (np.abs(lse.cpu().numpy() - logs) <= 2.0 ** -14 + 2.0 ** -20 * np.abs(logs))[good].all()
