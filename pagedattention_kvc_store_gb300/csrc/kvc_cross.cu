@@ -99,7 +99,7 @@ enum BarIndex : int {
     kBarQEmpty = kBarQFull + 2,             // [tile], one MMA commit after its last S product
     kBarSFull = kBarQEmpty + 2,             // [tile][its blocks in turn]
     kBarPFull = kBarSFull + 4,              // [tile][its blocks in turn], an arrival of each of its eight warps
-    kBarPvDone = kBarPFull + 4,             // [tile][its blocks in turn]
+    kBarPvDone = kBarPFull + 4,             // [tile][its blocks in turn]; with two slots [tile][0], once per item
     kBarDrain = kBarPvDone + 4,
     kBarItemFull = kBarDrain + 1,           // the item in shared memory is the next one
     kBarItemEmpty = kBarItemFull + 1,       // an arrival of every warp that reads items
@@ -394,7 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(kBarPFull + 2 * t + (p_count[t] & 1), (p_count[t] >> 1) & 1);
                 tc_fence_after_sync();
                 issue_pv(t, p_slot, vst, b + 1 == nb ? last_cols / 16 : kBN / 16, first ? 0u : 1u);
-                commit(kBarPvDone + 2 * t + (p_count[t] & 1));
+                if (G_::kSlots > 2)
+                    commit(kBarPvDone + 2 * t + (p_count[t] & 1));
+                else if (b + (dual ? 2 : 1) >= nb)
+                    commit(kBarPvDone + 2 * t);
                 ++p_count[t];
                 p_slot = next_slot(p_slot);
             };
@@ -562,10 +565,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         Feed w;
         int tb = 0;   // blocks of this tile so far
-        // The products of the tile's last block before tb.  (S of block b is committed behind the products of
-        // block b - 2, no later ones: a barrier for every other block, or a wait for those of b - 1 could take the
-        // end of b - 2's for theirs.)
-        auto pv_wait = [&] { wait(&bars[kBarPvDone + 2 * t + ((tb - 1) & 1)], ((tb - 1) >> 1) & 1); };
+        int ti = 0;   // items of this tile so far
+        // The products of the tile's last block before tb, or with two slots of its last one.  (With three S of
+        // block b is committed behind the products of block b - 2, no later ones: hence a barrier for every other
+        // block, or a wait for those of b - 1 could take the end of b - 2's for theirs.)
+        auto pv_wait = [&] {
+            if (G_::kSlots > 2)
+                wait(&bars[kBarPvDone + 2 * t + ((tb - 1) & 1)], ((tb - 1) >> 1) & 1);
+            else
+                wait(&bars[kBarPvDone + 2 * t], ti & 1);
+        };
         int n0 = 0;   // ring index of the item's first slot
         int u0 = 0;   // units of the CTA before the item
         for (;; n0 += 2 * w.x.n_blocks, u0 += w.x.units()) {
@@ -722,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // epilogue: once this tile's last PV is done, O / l -> global
             if (x.n_blocks > 0) {
                 pv_wait();
+                ++ti;
                 tc_fence_after_sync();
             }
 #pragma unroll
