@@ -12,16 +12,23 @@
 //               box per page, issued by parallel lanes, that lands as [8 positions][column half][8 rows]
 //               [128 bytes, swizzled], so that a stage is one operand whatever the page size (a box per page and
 //               half took twice as many, and 16-position pages 37% more time).  A warp issues a box in some
-//               150 cycles: one for both K and V held 16-position pages back (766 us for prompts over them, 670 with two)
-//   warp 1      allocates TMEM (512 columns) and issues S_w = Q_w K(b)^T (M 128, N 128, K head_dim) and
-//               O_w += P_w V(b) (N head_dim, K 128, P from TMEM) of the tiles w from one thread; S_w(b + 1)
-//               right behind the PV product that reads P_w(b) from the same columns
+//               150 cycles: one for both K and V held 16-position pages back (prompts over them 766 us, with
+//               two 670)
+//   warp 1      allocates TMEM (512 columns) and issues S = Q_w K(b)^T (M 128, N 128, K head_dim) of the tiles w
+//               into score slots in turn (two at head dim 128, three at 64) and O_w += P V(b) (N head_dim, K 128,
+//               P from the slot); the next S into a slot right behind the product that reads P from it
 //   warp 3      the items (cancels blocks of the grid that have not started and hands theirs round), and
 //               their query tiles
-//   warps 4-11  softmax of tile 0, warps 12-19 of tile 1: two threads a row: the running maximum (O rescaled
-//               only when p of the maximum before add up to more than 2^8) and sum, P as bf16 over S's columns, and O / l at the end.
-// An item of a single tile puts its blocks in turn on both halves of TMEM, so that the softmax of one runs
+//   warps 4-11  softmax of tile 0, warps 12-19 of tile 1, 16 rows each: the running maximum (O rescaled only when
+//               p of the maximum before add up to more than 2^8) and sum, P as bf16 over S's columns, and O / l
+//               at the end
+// An item of a single tile puts its blocks in turn on the O of both tiles, so that the softmax of one runs
 // beside the products of the other as it does with two tiles, and joins the two at the end.
+// 64 sources of 2,048 positions x 512 queries, 32 / 8 heads: 735 us at head dim 128 (1,495 TFLOP/s, 79% of the
+// burst rate of a library product), 550 at 64.  Bound by a tile's chain at 128: scores 512 cycles, softmax some
+// 1,600 (its loads from TMEM 150, 900-1,100 for the exponentials, vote and hand-over 500), products 512; the
+// other tile's products fit into that, the two exposed ends do not.  At 64 by the softmax warps: 58% of all issue
+// slots, 39% of the exponential unit's.
 // Few rows and many positions: the positions are cut into chunks (splits), partial rows and their
 // log-sum-exps go to the workspace and cross_merge_kernel joins them.
 // Sums: P is rounded to bf16 for the product (2^-8 of each, the same the append makes), l sums the unrounded
@@ -40,7 +47,7 @@ __device__ uint32_t g_cross_errors;
 constexpr int kM = 128;           // rows per tile
 constexpr int kBN = kCrossBlock;  // positions per K or V stage (the N of S = Q K^T)
 constexpr int kRoleWarps = 4;     // K loads, MMA issue, V loads, items and queries
-constexpr int kSoftmaxWarps = 16; // a group of eight for each tile, two threads to a row
+constexpr int kSoftmaxWarps = 16; // eight for each tile
 constexpr int kThreads = (kRoleWarps + kSoftmaxWarps) * 32;
 constexpr int kMaxStages = 8;
 // Registers a thread: the launch's, and after the role warps gave theirs to the softmax warps.  128 * 64 +
@@ -50,9 +57,9 @@ static_assert(kRoleWarps * kRoleRegs + kSoftmaxWarps * kSoftmaxRegs <=
                   (kRoleWarps + kSoftmaxWarps) * kLaunchRegs, "registers of the launch");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleSum = 256.0f;   // of the p of a thread's 64 columns
-// named barriers of all softmax warps; 1 .. 8 are of the pairs
-constexpr uint32_t kBothTiles = 9;
+constexpr float kRescaleSum = 256.0f;   // of the p of a thread's 32 columns of a row
+// named barrier of all softmax warps
+constexpr uint32_t kBothTiles = 1;
 constexpr int kItemWaits = 6;   // warp 3's waits between two items: three long ones and a short one, and one at the end
 
 template <int D>
@@ -62,7 +69,7 @@ struct Geom {
     static constexpr int kStageBytes = kHalves * kBN * 128;  // K or V of 128 positions
     static constexpr int kStages = D == 128 ? 5 : 8;
     static constexpr int kOffStages = 2 * kQBytes;           // Q: [tile]
-    static constexpr int kOffExchange = kOffStages + kStages * kStageBytes;   // [tile][half][row] floats
+    static constexpr int kOffExchange = kOffStages + kStages * kStageBytes;   // [m, l][tile][row] floats
     static constexpr int kOffBar = kOffExchange + 4 * kM * 4;
     static constexpr int kOffItem = kOffBar + 384;           // after the barriers: the item, an answer
     static constexpr int kOffAnswer = kOffItem + 64;

@@ -202,19 +202,6 @@ __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t count)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// The same, and whether any of the threads said so.
-__device__ __forceinline__ bool barrier_or(uint32_t id, uint32_t count, bool mine)
-{
-    uint32_t any;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(any)
-        : "r"(mine ? 1u : 0u), "r"(id), "r"(count)
-        : "memory");
-    return any != 0;
-}
-
 // ---------------------------------------------------------------------------------------
 // TMA: 3-D tiled tensor load into shared memory, completion counted on an mbarrier.
 // ---------------------------------------------------------------------------------------
@@ -474,32 +461,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         v[i] = __uint_as_float(r[i]);
-}
-
-// 16 consecutive fp32 columns of this thread's TMEM lane (warp-collective).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
-{
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16])
-{
-    uint32_t r[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        r[i] = __float_as_uint(v[i]);
-    tmem_st16u(taddr, r);
 }
 
 // 16 lanes of TMEM (from lane 0 or 16 of the warp's quarter): a thread's registers 4 g + 2 r + j are the columns
