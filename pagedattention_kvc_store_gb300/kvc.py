@@ -265,7 +265,7 @@ def _stream(stream) -> int:
     """Handle of the stream, or of the current device's current one."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _out_dtype(out: torch.Tensor) -> int:
@@ -598,10 +598,10 @@ def _positions(positions, rope, T):
     if not isinstance(rope, RopeDesc):
         raise TypeError("rope is a rope_desc(...)")
     _cuda("positions", positions, torch.int32)
-    want = (rope.num_axes, T)
-    if tuple(positions.shape) != want and not (rope.num_axes == 1 and tuple(positions.shape) == (T,)):
+    want, shape = (rope.num_axes, T), positions.shape
+    if shape != want and not (rope.num_axes == 1 and shape == (T,)):
         raise ValueError(f"positions are [num_axes, num_tokens] = {want}, got {tuple(positions.shape)}")
-    return _ptr(positions)
+    return positions.data_ptr()
 
 
 def kvc_rope(q_out: Optional[torch.Tensor], k_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
@@ -636,9 +636,17 @@ def kvc_rope_store(q_out: Optional[torch.Tensor], k_pool: torch.Tensor, v_pool: 
                    layout: str = "nhd") -> None:
     """kvc_rope into q_out [T, Hq, D] and the pages, and the values too: rotated keys and values at
     slot_mapping's slots.  q, k_new and v_new as in kvc_rope; q None: no queries."""
-    _cuda("k_pool", k_pool, torch.bfloat16)
-    _cuda("v_pool", v_pool, torch.bfloat16)
-    _cuda("slot_mapping", slot_mapping, torch.int32)
+    bf16, i32 = torch.bfloat16, torch.int32
+    try:   # what nearly every call passes, with as few steps as say so
+        plain = (k_pool.is_cuda and v_pool.is_cuda and slot_mapping.is_cuda and k_pool.dtype is bf16
+                 and v_pool.dtype is bf16 and slot_mapping.dtype is i32 and k_pool.is_contiguous()
+                 and v_pool.is_contiguous() and slot_mapping.is_contiguous())
+    except AttributeError:
+        plain = False
+    if not plain:
+        _cuda("k_pool", k_pool, bf16)
+        _cuda("v_pool", v_pool, bf16)
+        _cuda("slot_mapping", slot_mapping, i32)
     T = slot_mapping.numel()
     k_stride, v_stride = _head_rows("k_new", k_new), _head_rows("v_new", v_new)
     q_heads, q_stride, q_ptr, q_out_ptr = 0, 0, None, None
@@ -1056,13 +1064,25 @@ def kvc_cross(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor, v_pool: 
               stream=None, layout: str = "nhd") -> None:
     """Cross attention: query tokens q_indptr[s] .. q_indptr[s + 1] - 1 to all source_lens[s]
     positions of source s; lse_out (fp32 [T, Hq]) gets the log-sum-exps."""
-    _cuda("out", out)
-    _cuda("q", q, torch.bfloat16)
-    _cuda("k_pool", k_pool, torch.bfloat16)
-    _cuda("v_pool", v_pool, torch.bfloat16)
-    _cuda("block_table", block_table, torch.int32)
-    _cuda("q_indptr", q_indptr, torch.int32)
-    _cuda("source_lens", source_lens, torch.int32)
+    bf16, i32 = torch.bfloat16, torch.int32
+    try:   # what nearly every call passes, with as few steps as say so
+        plain = (out.is_cuda and q.is_cuda and k_pool.is_cuda and v_pool.is_cuda
+                 and block_table.is_cuda and q_indptr.is_cuda and source_lens.is_cuda
+                 and q.dtype is bf16 and k_pool.dtype is bf16 and v_pool.dtype is bf16
+                 and block_table.dtype is i32 and q_indptr.dtype is i32 and source_lens.dtype is i32
+                 and out.is_contiguous() and q.is_contiguous() and k_pool.is_contiguous()
+                 and v_pool.is_contiguous() and block_table.is_contiguous()
+                 and q_indptr.is_contiguous() and source_lens.is_contiguous())
+    except AttributeError:
+        plain = False
+    if not plain:
+        _cuda("out", out)
+        _cuda("q", q, bf16)
+        _cuda("k_pool", k_pool, bf16)
+        _cuda("v_pool", v_pool, bf16)
+        _cuda("block_table", block_table, i32)
+        _cuda("q_indptr", q_indptr, i32)
+        _cuda("source_lens", source_lens, i32)
     lse = lse_ptr = None
     if lse_out is not None:
         _cuda("lse_out", lse_out, torch.float32)
