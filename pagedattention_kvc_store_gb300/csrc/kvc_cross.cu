@@ -184,16 +184,22 @@ struct Feed {
         to[2] = from[2];
         ++n;
     }
-    // The same for a warp.  False at the end, or if the wait ran out (then ok is false).
-    __device__ __forceinline__ bool next(uint64_t *bars, const Item *slot, bool &ok, int times = 1)
+    // The same for a warp; false (and ok) if the wait ran out.
+    __device__ __forceinline__ bool get(uint64_t *bars, const Item *slot, bool &ok, int times)
     {
         if (!__all_sync(0xffffffffu, wait(bars, times))) {
             ok = false;
             return false;
         }
         read(slot);
-        if (times == 1)
-            has_read(bars);
+        return true;
+    }
+    // And acknowledges it.  False at the end too.
+    __device__ __forceinline__ bool next(uint64_t *bars, const Item *slot, bool &ok)
+    {
+        if (!get(bars, slot, ok, 1))
+            return false;
+        has_read(bars);
         return !x.done;
     }
     __device__ __forceinline__ void has_read(uint64_t *bars)
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (The softmax warps meet at named barriers, so none may leave before the others: they wait for an
             // item for longer than warp 3 can take to hand one round, the end included, with every wait of
             // its own run out.  A barrier of all of them here kept tile 0 until tile 1 was written.)
-            if (!w.next(bars, item, ok, kItemWaits))
+            if (!w.get(bars, item, ok, kItemWaits) || w.x.done)
                 break;
             const Item &x = w.x;
             // That it has read the item a warp says behind its first scores: an arrival waits for the warp's
