@@ -387,3 +387,21 @@ def test_nan_stays_with_its_row_among_many(splits, D):
     good = ~bad.cpu().numpy()
     assert (err <= 2.0 ** -7 * weighed + 1e-6)[good].all()
     assert (np.abs(lse.cpu().numpy() - logs) <= 2.0 ** -14 + 2.0 ** -20 * np.abs(logs))[good].all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("S", [2, 33, 255, 256, 257])
+def test_many_sources_of_any_length_in_any_order(S, D):
+    """More items than SMs: whatever order they are worked off in, every source gets its rows."""
+    rng = np.random.default_rng(S)
+    lens = [int(n) for n in rng.choice([0, 1, 17, 128, 300, 640, 1100], S)]
+    lens[0], lens[-1] = 1100, 1500
+    q_lens = [int(n) for n in rng.choice([0, 1, 20, 40], S)]
+    q_lens[0], q_lens[1] = 40, 40
+    if S == 2:
+        q_lens = [3000, 2100]
+    c = Case(lens, q_lens, 2, 2, D, 16, seed=S)
+    for max_src in (1500, 1536):   # the longest, and what the table's rows hold
+        out, lse = c.run(splits=1, max_src=max_src)
+        check(c, out, lse)
+        assert kvc.kvc_device_errors() == 0
