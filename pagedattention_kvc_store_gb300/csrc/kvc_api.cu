@@ -2102,19 +2102,20 @@ struct CrossPlan {
 };
 
 // Chunks of the positions for many rows: of a few numbers the one that the kernel's own times make the
-// shortest.  A work item is a pair of row tiles of one source and kv head over a chunk: 6 us and 1.75 us for a block
-// of 128 positions (1.25 with one tile).  Where there are more items than SMs, these take them as they get free:
-// the last may leave an item's time idle, and sources are taken to be 0.7 of the longest.  Several chunks
-// cost a join, 5 us and their partial rows (fp32, written and read at 4.5 TB/s).  Measured against it, us: 64 items
-// of 16 blocks, 256 rows: 1 chunk 49, 2 48, 4 60; 8 items of 128 blocks: 1 243, 4 86, 8 58, 16 52; 64 items of up to
-// 1,024 blocks, 128 rows: 2 581, 8 639, 16 539, 24 540, 48 589.
+// shortest.  A work item is a pair of row tiles of one source and kv head over a chunk: 6 us and 1.6 us for a block
+// of 128 positions (1.15 with one tile).  Where there are more items than SMs, these take them as they get free, the
+// longest first, and sources are taken to be 0.6 of the longest.  Several chunks cost a join, 5 us and their partial
+// rows (fp32, written and read at 4.5 TB/s).  Measured against it, us: 64 items of 16 blocks, 256 rows: 1 chunk 45,
+// 2 44, 4 51; 8 items of 128 blocks: 1 195, 4 71, 8 50, 16 48; 64 items of up to 1,024 blocks, 128 rows: 8 455, 12 440,
+// 16 428, 32 442; 5 sources of 100 to 4,000 positions x up to 300 tokens, 32 / 8 heads: 1 65, 2 82, 3 73; 8 of them with
+// 8 / 4 heads: 1 54, 2 44, 3 54.
 int64_t cross_splits(int32_t num_sources, int32_t num_tokens, int32_t q_heads, const kvc_pool_desc &pool,
                      int64_t rows_each, int64_t src)
 {
     const double blocks = static_cast<double>(ceil_div(src, kvc::kCrossBlock));
     const double units = static_cast<double>(ceil_div(std::max<int64_t>(1, rows_each), 256) * pool.kv_heads *
                                              std::max(num_sources, 1));
-    const double sms = device_sm_count(), block_us = rows_each > 128 ? 1.75 : 1.25;
+    const double sms = device_sm_count(), block_us = rows_each > 128 ? 1.6 : 1.15;
     const double part_us = 2.0 * num_tokens * q_heads * pool.head_dim * 4 / 4.5e6;
     static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
     double best = 0.0;
@@ -2123,7 +2124,7 @@ int64_t cross_splits(int32_t num_sources, int32_t num_tokens, int32_t q_heads, c
         if (n > blocks)
             break;
         const double rounds = units * n / sms;
-        const double us = (rounds > 1.0 ? 0.7 * rounds + 1.0 : 1.0) * (ceil(blocks / n) * block_us + 6.0) +
+        const double us = (rounds > 1.0 ? 0.6 * rounds + 0.4 : 1.0) * (ceil(blocks / n) * block_us + 6.0) +
                           (n > 1 ? 5.0 + n * part_us : 0.0);
         if (n == 1 || us < best) {
             best = us;
