@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         }
         const int s = lo;
         const int j = static_cast<int>(r) - w.start[s];
-        const int len = t.lens[s];
+        const int len = max(t.lens[s], 0);   // (a negative length is none)
         const int copy = w.copy_at[s];
         int32_t *row = t.rows + static_cast<size_t>(s) * t.stride;
         int entry = pages_of(len, t.page_size) + j - (copy >= 0);
