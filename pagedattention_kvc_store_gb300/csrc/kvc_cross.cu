@@ -149,12 +149,10 @@ __device__ __forceinline__ bool make_item(const Args &a, int it, const uint16_t 
         x.s = order[x.s];
     x.tok0 = a.q_indptr[x.s];
     const int n_tok = a.q_indptr[x.s + 1] - x.tok0;
-    int len = a.source_lens[x.s];
-    const int most = min(a.max_src, a.bt_stride * a.page_size);
-    if (len > most || n_tok > a.max_q_len) {
+    const int given = a.source_lens[x.s], most = min(a.max_src, a.bt_stride * a.page_size);
+    if (given > most || n_tok > a.max_q_len)
         atomicOr(err, kErrContextRange);
-        len = min(len, most);
-    }
+    const int len = min(max(given, 0), most);   // a negative length is none
     x.rows = min(n_tok, a.max_q_len) * a.group;
     x.row_begin = tp * 2 * kM;
     if (x.row_begin >= x.rows)
