@@ -355,7 +355,8 @@ kvc_status kvc_append(void *out, int32_t out_dtype, const void *q, const void *k
  *   q, out        [num_tokens][q_heads][head_dim]; q bf16, out per out_dtype
  *   lse_out       fp32 [num_tokens][q_heads] or NULL
  *   block_table   int32 [num_sources][bt_stride];  source_lens int32 [num_sources], a negative one counts as 0
- *   q_indptr      int32 [num_sources + 1], not decreasing
+ *   q_indptr      int32 [num_sources + 1], not decreasing, 0 .. num_tokens; a source with tokens outside of that is
+ *                 flagged (kvc_device_errors, 1 << 7), its rows are undefined, and nothing outside is written
  *   max_q_len, max_src  host upper bounds on every source's tokens and positions; more are flagged
  *                 (kvc_device_errors, 1 << 7): positions past max_src are not seen, rows past max_q_len undefined
  *   num_splits    0 = choose, 1 = no split, n > 1 = at most n chunks

@@ -95,7 +95,7 @@ struct Args {
     int bt_stride;
     const int32_t *q_indptr, *source_lens;
     int kv_heads, q_heads, group, page_size, pairs_per_seq, num_items;
-    int max_q_len, max_src, chunk, n_split;
+    int num_tokens, max_q_len, max_src, chunk, n_split;
     float scale_log2;
     int ordered;   // sources whose items go by their lengths, the longest first; 0: as they come
     int hnd;   // HND pools: half boxes addressed by (offset, page * kv_heads + kv head)
@@ -148,9 +148,10 @@ __device__ __forceinline__ bool make_item(const Args &a, int it, const uint16_t 
     if (a.ordered > 0)
         x.s = order[x.s];
     x.tok0 = a.q_indptr[x.s];
-    const int n_tok = a.q_indptr[x.s + 1] - x.tok0;
+    bool in_range;
+    const int n_tok = source_tokens(x.tok0, a.q_indptr[x.s + 1], a.num_tokens, in_range);
     const int given = a.source_lens[x.s], most = min(a.max_src, a.bt_stride * a.page_size);
-    if (given > most || n_tok > a.max_q_len)
+    if (given > most || n_tok > a.max_q_len || !in_range)
         atomicOr(err, kErrContextRange);
     const int len = min(max(given, 0), most);   // a negative length is none
     x.rows = min(n_tok, a.max_q_len) * a.group;
@@ -1003,6 +1004,7 @@ cudaError_t launch_t(const CrossLaunch &l, const CUtensorMap &tq, const CUtensor
     a.q_heads = l.q_heads;
     a.group = l.q_heads / l.kv_heads;
     a.page_size = l.page_size;
+    a.num_tokens = l.num_tokens;
     a.max_q_len = l.max_q_len;
     a.max_src = l.max_src;
     a.chunk = l.chunk;

@@ -50,7 +50,7 @@ struct Args {
     int bt_stride;
     const int32_t *q_indptr, *source_lens;
     int q_heads, kv_heads, group, page_size;
-    int max_q_len, max_src, chunk, n_split;
+    int num_tokens, max_q_len, max_src, chunk, n_split;
     float scale_log2;
     int hnd;
     uint32_t *err;
@@ -81,10 +81,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int G = a.group;
     const int P = a.page_size;
     const int tok0 = a.q_indptr[src];
-    const int n_tok = a.q_indptr[src + 1] - tok0;
+    bool in_range;
+    const int n_tok = source_tokens(tok0, a.q_indptr[src + 1], a.num_tokens, in_range);
     const int len = a.source_lens[src];
     const int most = min(a.max_src, a.bt_stride * P);
-    if ((len > most || n_tok > a.max_q_len) && threadIdx.x == 0)
+    if ((len > most || n_tok > a.max_q_len || !in_range) && threadIdx.x == 0)
         atomicOr(err_word, kErrContextRange);
     const int rows = min(n_tok, a.max_q_len) * G;
     if (rows <= 0)
@@ -439,6 +440,7 @@ cudaError_t launch_t(const CrossLaunch &l, const CUtensorMap &tk, const CUtensor
     a.kv_heads = l.kv_heads;
     a.group = l.q_heads / l.kv_heads;
     a.page_size = l.page_size;
+    a.num_tokens = l.num_tokens;
     a.max_q_len = l.max_q_len;
     a.max_src = l.max_src;
     a.chunk = l.chunk;

@@ -188,6 +188,14 @@ __device__ __forceinline__ bool warp_wait_over(long long since)
     return __any_sync(0xffffffffu, clock64() - since > kWaitLimitCycles);
 }
 
+// Tokens of a source, whose first is tok0 and the next source's `end`, that lie among the call's num_tokens (all of
+// them where in_range; none where tok0 itself does not).
+__device__ __forceinline__ int source_tokens(int tok0, int end, int num_tokens, bool &in_range)
+{
+    in_range = tok0 >= 0 && end <= num_tokens;
+    return tok0 < 0 ? 0 : max(min(end, num_tokens), tok0) - tok0;
+}
+
 // True in one lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one()
 {
