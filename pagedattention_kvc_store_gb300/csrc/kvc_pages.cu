@@ -226,13 +226,19 @@ __device__ __forceinline__ long long scan_exclusive(long long v, long long *red,
     return before;
 }
 
-// Pages in use (or free) of a segment, by all threads of a block; every thread gets the sum.
+// Pages of a segment (a sum of its begin and kPageSegment may not be an int).
+__device__ __forceinline__ int segment_pages(int begin, int num_pages)
+{
+    return min(kPageSegment, num_pages - begin);
+}
+
+// Pages in use (or free) of `pages` ones from begin on, by all threads of a block; every thread gets the sum.
 template <int N>
-__device__ __forceinline__ int count_pages(const int32_t *refs, int begin, int end, bool used, long long *red)
+__device__ __forceinline__ int count_pages(const int32_t *refs, int begin, int pages, bool used, long long *red)
 {
     int n = 0;
-    for (int p = begin + threadIdx.x; p < end; p += N)
-        n += (refs[p] > 0) == used;
+    for (int i = threadIdx.x; i < pages; i += N)
+        n += (refs[begin + i] > 0) == used;
     long long total;
     scan_exclusive<N>(n, red, &total);
     return static_cast<int>(total);
@@ -275,8 +281,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     if (blockIdx.x > 0) {
         const int seg = blockIdx.x - 1;
         const int begin = seg * kPageSegment;
-        const int n = count_pages<kRowThreads>(t.refs, begin, min(begin + kPageSegment, t.num_pages),
-                                               false, red);
+        const int n =
+            count_pages<kRowThreads>(t.refs, begin, segment_pages(begin, t.num_pages), false, red);
         if (threadIdx.x == 0)
             w.seg_counts[seg] = n;
         return;
@@ -355,10 +361,10 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     }
     if (!fits)
         return;
-    const int begin = seg * kPageSegment, end = min(begin + kPageSegment, t.num_pages);
-    for (int p0 = begin; p0 < end && before < needed; p0 += kRowThreads) {
-        const int p = p0 + threadIdx.x;
-        const bool free_page = p < end && t.refs[p] <= 0;
+    const int begin = seg * kPageSegment, pages = segment_pages(begin, t.num_pages);
+    for (int i0 = 0; i0 < pages && before < needed; i0 += kRowThreads) {
+        const int i = i0 + threadIdx.x, p = begin + i;
+        const bool free_page = i < pages && t.refs[p] <= 0;
         long long total;
         const long long r = before + scan_exclusive<kRowThreads>(free_page, red, &total);
         before += total;
@@ -607,7 +613,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     pdl_trigger();
     __shared__ long long red[32];
     const int begin = blockIdx.x * kPageSegment;
-    const int n = count_pages<kRowThreads>(refs, begin, min(begin + kPageSegment, num_pages), true, red);
+    const int n = count_pages<kRowThreads>(refs, begin, segment_pages(begin, num_pages), true, red);
     if (threadIdx.x == 0)
         w.seg_counts[blockIdx.x] = n;
 }
@@ -628,17 +634,18 @@ __device__ __forceinline__ void map_page(int p, bool used, int rank, int border,
     page_map[p] = to;
 }
 
-// The same for pages begin .. end - 1, `before` used ones lying below them.
-__device__ __forceinline__ void map_pages(const int32_t *refs, int begin, int end, long long before, int border,
-                                          int stay, const CompactSpace &w, int32_t *page_map, long long *red)
+// The same for `pages` ones from begin on, `before` used ones lying below them.
+__device__ __forceinline__ void map_pages(const int32_t *refs, int begin, int pages, long long before,
+                                          int border, int stay, const CompactSpace &w, int32_t *page_map,
+                                          long long *red)
 {
-    for (int p0 = begin; p0 < end; p0 += kRowThreads) {
-        const int p = p0 + threadIdx.x;
-        const bool used = p < end && refs[p] > 0;
+    for (int i0 = 0; i0 < pages; i0 += kRowThreads) {
+        const int i = i0 + threadIdx.x, p = begin + i;
+        const bool used = i < pages && refs[p] > 0;
         long long total;
         const int rank = static_cast<int>(before + scan_exclusive<kRowThreads>(used, red, &total));
         before += total;
-        if (p < end)
+        if (i < pages)
             map_page(p, used, rank, border, stay, w, page_map);
     }
 }
@@ -671,14 +678,14 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         for (int i = threadIdx.x; i < whole; i += kRowThreads)
             b += w.seg_counts[i];
         scan_exclusive<kRowThreads>(b, red, &stay);
-        stay += count_pages<kRowThreads>(refs, whole * kPageSegment, border, true, red);
+        stay += count_pages<kRowThreads>(refs, whole * kPageSegment, border % kPageSegment, true, red);
     }
     if (seg == 0 && threadIdx.x == 0) {
         *num_live = border;
         *w.copies = static_cast<int>(live - stay);
     }
     const int begin = seg * kPageSegment;
-    map_pages(refs, begin, min(begin + kPageSegment, num_pages), before, border, static_cast<int>(stay), w,
+    map_pages(refs, begin, segment_pages(begin, num_pages), before, border, static_cast<int>(stay), w,
               page_map, red);
 }
 
@@ -774,7 +781,7 @@ __global__ void __launch_bounds__(kThreads)
     copy_listed<kThreads>(arrays, src, dst, *count);
 }
 
-int segments_of(int num_pages) { return (num_pages + kPageSegment - 1) / kPageSegment; }
+int segments_of(int num_pages) { return (num_pages - 1) / kPageSegment + 1; }
 
 // Arrays first .. first + kMaxCopyArrays - 1.
 CopyArrays some_arrays(const PagesLaunch &l, int first)

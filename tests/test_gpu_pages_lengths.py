@@ -84,3 +84,34 @@ def test_a_negative_length_is_shared_given_back_and_moved_as_none(pages, rows):
     assert live.item() == n and where.tolist() == to and torch.equal(new[2], before)
     new[2].clamp_(min=0)
     d.same(new)
+
+
+def test_the_largest_pool():
+    """2^31 - 1 pages (of one position): the last ones are handed out, counted and moved like any other."""
+    n = 2 ** 31 - 1
+    free = [5, 2 ** 30, n - 4096, n - 2, n - 1]
+    at = torch.tensor(free, device="cuda")
+    refs = torch.ones(n, dtype=torch.int32, device="cuda")
+    refs[at] = 0
+    table = torch.full((2, 8), -5, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    missing = torch.full((1,), -7, dtype=torch.int32, device="cuda")
+    ws = torch.empty(kvc.kvc_reserve_plan(2, n), dtype=torch.uint8, device="cuda")
+    for grow, want in (([3, 3], 1), ([3, 2], 0), ([0, 1], 1)):
+        kvc.kvc_reserve(table, lens, i32_tensor(np.array(grow), "cuda"), refs, missing, 1, workspace=ws)
+        assert missing.item() == want
+    assert table.tolist() == [free[:3] + [-5] * 5, free[3:] + [-5] * 6] and lens.tolist() == [3, 2]
+    assert int(refs.sum()) == n
+    del ws
+    refs.zero_()
+    refs[at] = torch.arange(1, 6, dtype=torch.int32, device="cuda")
+    ws = torch.empty(kvc.kvc_compact_plan(n), dtype=torch.uint8, device="cuda")
+    where = torch.empty(n, dtype=torch.int32, device="cuda")
+    live = torch.empty(1, dtype=torch.int32, device="cuda")
+    kvc.kvc_compact(table, lens, refs, where, live, 1, workspace=ws)
+    assert live.item() == 5
+    assert table.tolist() == [[0, 1, 2] + [-5] * 5, [3, 4] + [-5] * 6]
+    assert refs[:6].tolist() == [1, 2, 3, 4, 5, 0] and int(refs.sum()) == 15
+    assert where[at].tolist() == [0, 1, 2, 3, 4] and int((where >= 0).sum()) == 5
+    kvc.kvc_truncate(table, lens, None, refs, 1)
+    assert refs[:6].tolist() == [0, 1, 2, 3, 4, 0] and kvc.kvc_device_errors() == 0
