@@ -404,9 +404,19 @@ kvc_status kvc_append_store(void *out, int32_t out_dtype, const void *q, const v
 
 /*
  * kvc_device_errors -- read and clear the library's own device-side error words.  Kernels
- * bound every wait (about one second); a wait that runs out sets a bit and the kernel returns
+ * bound every wait (about one second; kvc_cross's waits for a whole chunk of another warp's work two, and
+ * one more for every 2^21 positions of a chunk, but no longer than the second in which some wait of the block
+ * has run out); a wait that runs out sets a bit and the kernel returns
  * early, leaving its outputs undefined; range checks (a slot past the pool, a context longer
- * than its block-table row, ...) set theirs and skip the offending token.  The bits of calls
+ * than its block-table row, ...) set theirs and skip the offending token:
+ *   1 << 0 .. 1 << 4, 1 << 8   a wait ran out in decode or append        1 << 16  in cross attention
+ *   1 << 5   copies or products that were still in flight after that did not end in time
+ *   1 << 6   a slot past the pool         1 << 7   a length past its row or its bound, or tokens past the call's
+ *   1 << 9   shared memory not where a kernel needs it (no work done)     1 << 10  a page outside the pool
+ *   1 << 11  INT8 append: a value scale above its limit                   1 << 12  kvc_selftest_wait
+ *   1 << 13  eviction: a row cut twice without a token in between         1 << 14  a page with fewer references
+ *            than rows that list it       1 << 15  a fork of a row past the table
+ * The bits of calls
  * made while no caller word is set (kvc_set_error_word) land in these words, one per kernel
  * family in each process, on the current device: calls from several threads or streams share
  * them, and this read (which synchronises with the device) clears them for all.  *flags_out
@@ -431,7 +441,8 @@ kvc_status kvc_set_error_word(uint32_t *device_word);
 /*
  * kvc_selftest_wait -- a diagnostic of the failure path every kernel shares: one CTA waits on
  * an mbarrier phase that nothing completes, with the bounded waits the kernels use (a thread's own, then
- * a polling warp's, whose lanes give up together); after a second or two it has given up, sets bit
+ * a polling warp's, whose lanes give up together, then one for work, which another's end cuts short); after
+ * some seconds it has given up, sets bit
  * 1 << 12 of the device error word (kvc_device_errors) and returns.  Nothing faults or hangs, and
  * later calls run as usual.
  */

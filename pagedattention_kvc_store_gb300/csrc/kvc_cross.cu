@@ -59,9 +59,9 @@ static_assert(kRoleWarps * kRoleRegs + kSoftmaxWarps * kSoftmaxRegs <=
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleSum = 256.0f;   // of the p of a thread's 32 columns of a row
-// named barrier of all softmax warps
-constexpr uint32_t kBothTiles = 1;
-constexpr int kItemWaits = 6;   // warp 3's waits between two items: three long ones and a short one, and one at the end
+// Waits for work are as long as a CTA's items: they may take two seconds and one more for every 2^21 positions of a
+// chunk (16,384 blocks, some 30 ms of work).
+constexpr int kPatienceLog2 = 21;
 
 template <int D>
 struct Geom {
@@ -114,7 +114,8 @@ enum BarIndex : int {
     kBarItemFull = kBarDrain + 1,           // the item in shared memory is the next one
     kBarItemEmpty = kBarItemFull + 1,       // an arrival of every warp that reads items
     kBarCancel = kBarItemEmpty + 1,         // the answer to a request for a block that has not started
-    kBarCount = kBarCancel + 1
+    kBarBoth = kBarCancel + 1,              // the softmax warps of both tiles meet, an arrival of each
+    kBarCount = kBarBoth + 1
 };
 constexpr int kItemReaders = 3 + kSoftmaxWarps;
 
@@ -171,14 +172,9 @@ __device__ __forceinline__ bool make_item(const Args &a, int it, const uint16_t 
 struct Feed {
     Item x;
     int n = 0;   // items read
-    // Waits for the next item, which may be as long as the one before takes; false if that is too long.
-    __device__ __forceinline__ bool wait(uint64_t *bars, int times)
-    {
-        bool there = false;
-        for (int i = 0; i < times && !there; ++i)
-            there = mbar_wait_long(&bars[kBarItemFull], n & 1);
-        return there;
-    }
+    int patience;
+    volatile uint32_t *gave_up;
+    __device__ __forceinline__ Feed(int times, volatile uint32_t *word) : patience(times), gave_up(word) {}
     __device__ __forceinline__ void read(const Item *slot)
     {
         const int4 *from = reinterpret_cast<const int4 *>(slot);
@@ -189,10 +185,10 @@ struct Feed {
         to[2] = from[2];
         ++n;
     }
-    // The same for a warp; false (and ok) if the wait ran out.
-    __device__ __forceinline__ bool get(uint64_t *bars, const Item *slot, bool &ok, int times)
+    // Waits for the next item, by a whole warp; false (and ok) if the wait ran out.
+    __device__ __forceinline__ bool get(uint64_t *bars, const Item *slot, bool &ok)
     {
-        if (!__all_sync(0xffffffffu, wait(bars, times))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_work(&bars[kBarItemFull], n & 1, patience, gave_up))) {
             ok = false;
             return false;
         }
@@ -202,7 +198,7 @@ struct Feed {
     // And acknowledges it.  False at the end too.
     __device__ __forceinline__ bool next(uint64_t *bars, const Item *slot, bool &ok)
     {
-        if (!get(bars, slot, ok, 1))
+        if (!get(bars, slot, ok))
             return false;
         has_read(bars);
         return !x.done;
@@ -236,8 +232,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     uint8_t *sStages = smem + G_::kOffStages;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + G_::kOffBar);
-    static_assert(kBarCount * 8 + 4 <= 384, "barriers");
+    static_assert(kBarCount * 8 + 8 <= 384, "barriers");
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBarCount);
+    // A wait that ran out: the other waits for work end too, and the rest of the grid's items are let go.
+    volatile uint32_t *gave_up = tmem_slot + 1;
+    const int patience = 2 + (a.chunk >> kPatienceLog2);
     Item *item = reinterpret_cast<Item *>(smem + G_::kOffItem);
     uint16_t *order = reinterpret_cast<uint16_t *>(smem + G_::kOffOrder);
     auto q_tile = [&](int tile) { return smem + tile * G_::kQBytes; };
@@ -251,8 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kBarCount; ++i)
             mbar_init(&bars[i], (i >= kBarPFull && i < kBarPvDone) ? 8u
                                 : i == kBarItemEmpty               ? static_cast<uint32_t>(kItemReaders)
+                                : i == kBarBoth                    ? static_cast<uint32_t>(kSoftmaxWarps)
                                                                    : 1u);
         fence_mbar_init();
+        *gave_up = 0;
     }
     if (warp == 1)
         tmem_alloc(tmem_slot, G_::kTmemCols);
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // positions x 200-400 queries with the L2 cold: 644 us, marked to leave first 669 and 1.7 GB from
         // memory instead of 0.9, marked to leave last 644); what is read once leaves first
         const uint64_t policy = a.pairs_per_seq > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
-        Feed w;
+        Feed w(patience, gave_up);
         int n0 = 0;          // ring index of the item's first slot
         int begun = 0;       // ring index behind the last slot that this warp filled
         for (; w.next(bars, item, ok); n0 += 2 * w.x.n_blocks) {
@@ -359,6 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      policy);
                 begun = n + 1;
             }
+            if (!ok)
+                *gave_up = 1;
         }
         if (!ok && lane == 0) {
             atomicOr(err_word, kErrCrossWait);
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader)
                 umma_commit(&bars[bar]);
         };
-        Feed w;
+        Feed w(patience, gave_up);
         int s_slot = 0, p_slot = 0;   // score slots of the next unit's S and of the next unit's P
         uint32_t s_count[2] = {0, 0}, p_count[2] = {0, 0};   // the tiles' S products and P so far
         uint32_t q_count[2] = {0, 0};                        // and their items
@@ -537,6 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             kst = vst;
             kph = vph;
             ok = !__any_sync(0xffffffffu, failed != 0);
+            if (!ok)
+                *gave_up = 1;
         }
         if (!ok && lane == 0)
             atomicOr(err_word, kErrCrossWait);
@@ -560,17 +565,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool more = true;
         while (more) {
             Item x;
-            if (make_item(a, it, order, x, err_word)) {
-                if (published > 0 && !mbar_wait_long(&bars[kBarItemEmpty], (published - 1) & 1)) {
-                    ok = false;
-                    break;
+            ok = ok && *gave_up == 0;   // if not, items are asked for and let go
+            if (ok && make_item(a, it, order, x, err_word)) {
+                if (published > 0)
+                    ok = mbar_wait_work(&bars[kBarItemEmpty], (published - 1) & 1, patience, gave_up);
+                if (ok) {
+                    *item = x;
+                    mbar_arrive(&bars[kBarItemFull]);
+                    ++published;
                 }
-                *item = x;
-                mbar_arrive(&bars[kBarItemFull]);
-                ++published;
                 // the tile's 128 / G tokens x G heads, token-major, by column halves
                 for (int t = 0; ok && x.n_blocks > 0 && t < (x.has_b ? 2 : 1); ++t) {
-                    if (qi[t] > 0 && !mbar_wait_long(&bars[kBarQEmpty + t], (qi[t] - 1) & 1)) {
+                    if (qi[t] > 0 &&
+                        !mbar_wait_work(&bars[kBarQEmpty + t], (qi[t] - 1) & 1, patience, gave_up)) {
                         ok = false;
                         break;
                     }
@@ -587,13 +594,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             try_cancel_block(answer, &bars[kBarCancel]);
             if (!mbar_wait(&bars[kBarCancel], asked & 1)) {
                 ok = false;
+                *gave_up = 1;
                 break;
             }
             ++asked;
             more = cancelled_block(answer, it);
             fence_proxy_async_smem();
         }
-        if (published > 0 && !mbar_wait_long(&bars[kBarItemEmpty], (published - 1) & 1))
+        if (published > 0 && !mbar_wait_work(&bars[kBarItemEmpty], (published - 1) & 1, patience, gave_up))
             ok = false;
         item->done = 1;
         mbar_arrive(&bars[kBarItemFull]);
@@ -622,12 +630,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sl2 = a.scale_log2;
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
         // A wait that runs out is the last one: the warp then goes through the rest of its items without
-        // waiting, so that no other is left alone at a named barrier.
+        // waiting.
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok)
                 ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
         };
-        Feed w;
+        // The softmax warps of both tiles meet, twice for every item that they join (hence the parity).  (Not at a
+        // named barrier: that has no limit, and one of them may have left.)
+        auto meet = [&](uint32_t parity) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars[kBarBoth]);
+            wait(&bars[kBarBoth], parity);
+            tc_fence_after_sync();
+        };
+        Feed w(patience, gave_up);
         int tb = 0;   // blocks of this tile so far
         int ti = 0;   // items of this tile so far
         // The products of the tile's last block before tb, or with two slots of its last one.  (With three S of
@@ -642,10 +660,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n0 = 0;   // ring index of the item's first slot
         int u0 = 0;   // units of the CTA before the item
         for (;; n0 += 2 * w.x.n_blocks, u0 += w.x.units()) {
-            // (The softmax warps meet at named barriers, so none may leave before the others: they wait for an
-            // item for longer than warp 3 can take to hand one round, the end included, with every wait of
-            // its own run out.  A barrier of all of them here kept tile 0 until tile 1 was written.)
-            if (!w.get(bars, item, ok, kItemWaits) || w.x.done)
+            if (!ok)
+                *gave_up = 1;
+            if (!w.get(bars, item, ok) || w.x.done)
                 break;
             const Item &x = w.x;
             // That it has read the item a warp says behind its first scores: an arrival waits for the warp's
@@ -813,9 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         exchange[(2 + t) * kM + row0 + 8 * r] = l[r];
                     }
                 }
-                tc_fence_before_sync();
-                named_barrier(kBothTiles, kSoftmaxWarps * 32);
-                tc_fence_after_sync();
+                meet(0);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float *at = exchange + row0 + 8 * r;
@@ -911,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before_sync();
             if (x.dual)   // nobody overwrites what the other still reads
-                named_barrier(kBothTiles, kSoftmaxWarps * 32);
+                meet(1);
         }
         if (!ok)
             atomicOr(err_word, kErrCrossWait);

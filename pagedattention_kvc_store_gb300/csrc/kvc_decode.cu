@@ -84,14 +84,17 @@ cudaError_t launch_decode_t(const DecodeLaunch &l, const CUtensorMap &tk, const 
 // The bounded wait every kernel uses, on an mbarrier phase that nothing completes: it gives
 // up after kWaitLimitCycles and the CTA records kErrSelftestWait and returns, leaving the
 // context usable.  Then the wait of a warp that polls for itself (warp_wait_over), its lanes' clocks as
-// far apart as half the limit: all of them have to give up in the same turn.  A diagnostic of the
-// failure path, with no fault and no hang.
+// far apart as half the limit: all of them have to give up in the same turn.  And a wait for work, first with its
+// one turn run out, then with many that the first one's end cuts short.  A diagnostic of the failure path, with
+// no fault and no hang.
 __global__ void __launch_bounds__(32) selftest_wait_kernel(uint32_t *word)
 {
     __shared__ uint64_t bar;
+    __shared__ uint32_t gave_up;
     if (threadIdx.x == 0) {
         mbar_init(&bar, 1);
         fence_mbar_init();
+        gave_up = 0;
     }
     __syncwarp();
     const bool waited = __all_sync(0xffffffffu, mbar_wait(&bar, 0));
@@ -101,7 +104,12 @@ __global__ void __launch_bounds__(32) selftest_wait_kernel(uint32_t *word)
         ++turns;
     int together;
     __match_all_sync(0xffffffffu, turns, &together);
-    if (!waited && together && threadIdx.x == 0)
+    bool ended = false;
+    if (threadIdx.x == 0) {
+        ended = !mbar_wait_work(&bar, 0, 1, &gave_up) && gave_up == 1;
+        ended = !mbar_wait_work(&bar, 0, 64, &gave_up) && ended;
+    }
+    if (!waited && together && ended)
         atomicOr(word ? word : &g_decode_errors, kErrSelftestWait);
 }
 

@@ -144,12 +144,18 @@ __device__ __forceinline__ void mbar_wait_plain(uint64_t *bar, uint32_t parity, 
         : "memory");
 }
 
-// The same for waits that are as long as another warp's work item may be: gives up after 64 times as long.
-__device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity)
+// The same for a wait that may be as long as another warp's work: gives up after `times` as long, but no later than
+// the end of the first of them after some wait of the block has (*gave_up, which it sets itself too).
+__device__ __forceinline__ bool mbar_wait_work(uint64_t *bar, uint32_t parity, int times,
+                                               volatile uint32_t *gave_up)
 {
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < times; ++i) {
         if (mbar_wait(bar, parity))
             return true;
+        if (*gave_up != 0)
+            break;
+    }
+    *gave_up = 1;
     return false;
 }
 
