@@ -350,8 +350,9 @@ kvc_status kvc_append(void *out, int32_t out_dtype, const void *q, const void *k
  * and lse_out[t][h] is the logarithm of that softmax's sum (natural; with kvc_merge it joins this
  * result to one over other positions).  A source without positions gives out = 0 and lse = -inf.  Rows of
  * out and lse_out that belong to no source (before q_indptr[0], from q_indptr[num_sources] on) are left as
- * they are.  The positions are cut into consecutive chunks as in kvc_decode (kvc_cross_plan); the result
- * depends on their number only by fp32 rounding.
+ * they are.  The positions are cut into consecutive chunks as in kvc_decode (kvc_cross_plan).  Scores, sums and the
+ * product with V are fp32; each probability is rounded to bf16 for that product (2^-8 of it), relative to its
+ * chunk's maximum, so results with other numbers of chunks differ by such roundings.
  *   q, out        [num_tokens][q_heads][head_dim]; q bf16, out per out_dtype
  *   lse_out       fp32 [num_tokens][q_heads] or NULL
  *   block_table   int32 [num_sources][bt_stride];  source_lens int32 [num_sources], a negative one counts as 0
@@ -673,7 +674,7 @@ kvc_status kvc_evict(void *k_pool, void *v_pool, kvc_pool_desc pool, const int32
  * and kvc_store.)  Of each head the first rotary_dim dims turn, in rotary_dim / 2 pairs; pair f by
  *   a = positions[axis[f]][t] * inv_freq[f]:   y0 = x0 cos a - x1 sin a,   y1 = x1 cos a + x0 sin a,
  * in fp32, rounded once to bf16; the other dims go through unchanged.  Angles are taken modulo a turn in
- * 64-bit fixed point, so they are as good at position 2^31 - 1 as at 1 (off by 2^-53 of position *
+ * 64-bit fixed point, so they are as good at position 2^31 - 1 as at 1 (off by 2^-52 of position *
  * inv_freq, and 2^-23 radians); positions may be negative.
  *   inv_freq   host double [rotary_dim / 2], radians per unit of position, up to 1e6 (any scaling of long
  *              contexts is the caller's, in these)

@@ -27,8 +27,8 @@
 // 64 sources of 2,048 positions x 512 queries, 32 / 8 heads: 735 us at head dim 128 (1,495 TFLOP/s, 79% of the
 // burst rate of a library product), 550 at 64.  Bound by a tile's chain at 128: scores 512 cycles, softmax some
 // 1,600 (its loads from TMEM 150, 900-1,100 for the exponentials, vote and hand-over 500), products 512; the
-// other tile's products fit into that, the two exposed ends do not.  At 64 by the softmax warps: 58% of all issue
-// slots, 39% of the exponential unit's.
+// other tile's products fit into that, the two exposed ends do not.  At 64 not established: the softmax warps issue
+// in 58% of their slots, the exponential unit is busy 39%.
 // Few rows and many positions: the positions are cut into chunks (splits), partial rows and their
 // log-sum-exps go to the workspace and cross_merge_kernel joins them.
 // Sums: P is rounded to bf16 for the product (2^-8 of each, the same the append makes), l sums the unrounded
@@ -77,7 +77,7 @@ struct Geom {
     static constexpr int kOffOrder = kOffBar + 512;          // sources, the longest first
     static constexpr size_t kSmemBytes = kOffOrder + 2 * kMaxOrdered;   // base is 1024-aligned
     // TMEM: O of tile w at w * D, then as many slots of 128 columns as fit, for the scores of a tile and block
-    // each; P overwrites S, half h from 64 h on.
+    // each; P, two positions a column, overwrites S's first 64, and S's columns 64 .. 127 stay for a second look.
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kColS = 2 * D;
     static constexpr int kSlots = (kTmemCols - kColS) / kBN;
@@ -94,7 +94,7 @@ struct Args {
     const int32_t *block_table;
     int bt_stride;
     const int32_t *q_indptr, *source_lens;
-    int kv_heads, q_heads, group, page_size, pairs_per_seq, num_items;
+    int kv_heads, q_heads, group, page_size, pairs_per_seq;
     int num_tokens, max_q_len, max_src, chunk, n_split;
     float scale_log2;
     int ordered;   // sources whose items go by their lengths, the longest first; 0: as they come
@@ -1033,7 +1033,6 @@ cudaError_t launch_t(const CrossLaunch &l, const CUtensorMap &tq, const CUtensor
         static_cast<long long>(a.pairs_per_seq) * l.kv_heads * l.n_split * l.num_sources;
     if (items > 0x7FFFFFFFLL)
         return cudaErrorInvalidValue;
-    a.num_items = static_cast<int>(items);
     // The longest sources' items first where there are more items than SMs (64 sources of 512 to 4,096 positions x
     // 200-400 queries: 595 us as they come, 583 ordered; 24 of 100 to 4,000 189, 162; 100 of 100 to 2,000 79, 68).  Not
     // where all are short: 250 sources of 10 to 400 went from 61 to 60 at head dim 64, from 98 to 102 at 128.

@@ -6,10 +6,12 @@
 // both column halves) through a ring of 64-position stages, and four warps hold the rows in tiles of 16 for
 // mma.sync, the warps of a tile splitting a stage's positions and joining at the end.  Two CTAs an SM, so that
 // one's start and end lie under the other's stream.
-// Against that kernel, us (64 sources of 512-4,096 positions, 8 kv heads, groups of 4, 16-position pages, between
-// events): 1 token 117 / 197, 4 tokens 121 / 200, 8 tokens (32 rows) 133 / 200; 8 sources of 32k-131k positions, 32
-// rows 410 / 557 (6.1 TB/s).  From 33 rows on the tensor cores' tiles win: 64 rows in tiles of this kind (the
-// shared-prefix decode's) took 241 against 142.
+// Against that kernel, us (calls back to back, with the join): 64 sources of 512-4,096 positions, 8 kv heads, groups
+// of 4, 16-position pages: 1 token 98 / 101, 4 tokens 101 / 100, 8 tokens (32 rows) 114 / 99; 64 sources of 150 x 4
+// tokens 11.5 / 24.7, 4 of 2,000 11.7 / 14.0, 16 of 500-3,000 x 4 with 20 kv heads of one query head and 64 dims 40 /
+// 48; 8 of 32k-131k, groups of 8, 1 token 412 / 420, 32 rows 424 / 416 (6.0 TB/s): ahead by most where sources are
+// short or rows few, behind at 32 rows of many positions.  64 rows in tiles of this kind (the shared-prefix
+// decode's) took 241 when the other kernel took 142.
 // P is rounded to bf16 for the product; sums are of the unrounded values, as there.
 #include <math.h>
 

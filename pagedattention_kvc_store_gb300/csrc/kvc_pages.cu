@@ -17,9 +17,13 @@
 //             finish: the rows' lengths, and the copied pages of every array.
 //   compact   count the pages in use per segment; map: the i-th used page at or past the number in use goes
 //             to the i-th free one below it; finish: tables, counts and the map follow, and the copies.
-// Up to kRowThreads rows and kOneBlockPages pages (what most pools have) one block makes the decision of either,
-// in one launch with the copies where these are small: no count and assignment to meet between launches.
+// Up to kRowThreads rows and kOneBlockPages pages one block makes the decision of either, in one launch with the
+// copies where these are small: no count and assignment to meet between launches.
 // 256 branches of 64 sequences in 8 arrays, with truncate and fork, 40 -> 33 us, 8 of 4 short ones 26 -> 20.
+// Past either (one call between events, which are some 10 us of each figure): a token each for 64 rows 22 us over
+// 16,384 pages and 25 over 100,000, 2,000 rows 32; these with 1,866 pages to copy in 8 arrays of 32 KB 193 (5.1 TB/s),
+// in 64 of 4 KB 268 (3.7); closing up 17,771 pages in use of 100,000, 8,892 of them moved, 768 and 1,088 (6.1 and 4.3
+// TB/s), without arrays 23.
 // Bytes: the pool's counts once or twice (4 bytes a page), the rows' entries, and each copied page read and
 // written once in every array: HBM-bound from some tens of pages on (4,400 pages of 4 x 32 KB: 178 us, 6.4
 // TB/s), launches and chains of dependent loads before (truncate and fork 4 us each, a decision 6 to 10).

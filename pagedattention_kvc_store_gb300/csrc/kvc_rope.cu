@@ -4,7 +4,7 @@
 //   y0 = x0 cos a - x1 sin a,   y1 = x1 cos a + x0 sin a.
 // Angles are held as turns in 64-bit fixed point: inv_freq / (2 pi) modulo 1 as a 64-bit fraction, so
 // position * fraction modulo 2^64 is the angle's fraction of a turn, exact to position * 2^-64 on top of
-// the fraction's own rounding (2^-53 of inv_freq / (2 pi)) however far the position is; in fp32 the angle
+// the fraction's own roundings (2^-52 of inv_freq / (2 pi)) however far the position is; in fp32 the angle
 // of position 131,072 would be off by up to 2^-8.  Its upper 32 bits become an fp32 number of half turns
 // in [-1, 1] for sincospif.  The rotation itself is fp32, rounded once to bf16.
 //
@@ -12,8 +12,9 @@
 // one pair of 16-byte chunks (dims 8 c .. and 8 c + rotary / 2 .., or two chunks in a row where pairs
 // are adjacent dims) and goes over heads of its token with them, kRows heads at a time so that all their
 // loads are in flight together; values, and dims past rotary, go through unchanged.  50,000 tokens of 32 + 8 + 8
-// heads of 128 dims (1.23 GB): 183 us, 6.7 TB/s; blocks of 256 threads 187 us, 3 heads at a time 181 us but
-// 70.3 us against 66.7 for 9,973 tokens of 64 + 8 + 8 heads.
+// heads of 128 dims into pages (1.15 GB from and to memory: one token in eleven is padding and stores nothing): 183 us,
+// 6.3 TB/s, 93% of a copy; blocks of 256 threads 187 us, 3 heads at a time 181 us but 70.3 us against 66.7 for 9,973
+// tokens of 64 + 8 + 8 heads.  Rows of the same queries and keys (1.02 GB), in place or not: 182 us, 5.6 TB/s.
 #include "kvc_device.cuh"
 #include "kvc_launch.h"
 
