@@ -748,7 +748,8 @@ kvc_status kvc_rope_store(void *q_out, void *k_pool, void *v_pool, kvc_pool_desc
  * [out_stride] lists the pages of row parents[s], and context_lens_out[s] is that row's length, or the smaller
  * share_lens[s] (NULL: the whole row; a partly filled last page is shared too).  parents[s] < 0 gives an empty
  * row; one past num_seqs too, flagged (1 << 15); a row longer than out_stride covers is cut, flagged (1 << 7).
- * Table entries past a row's pages are left as they are.  The new arrays share no memory with the old ones.
+ * Table entries past a row's pages are left as they are.  The new arrays share no memory with the old ones, with
+ * parents or share_lens, nor with each other.
  *
  * kvc_reserve -- pages for new_tokens[s] more positions of every row (NULL: one; negative: none), and
  * context_lens[s] += new_tokens[s]: what the attention calls then take, the new tokens counted.  Rows go in

@@ -1388,6 +1388,9 @@ kvc_status kvc_fork(int32_t *block_table_out, int32_t out_stride, int32_t *conte
     const uint64_t in_rows = uint64_t(num_seqs) * bt_stride * 4, in_lens = uint64_t(num_seqs) * 4;
     const uint64_t out_rows = uint64_t(num_out) * out_stride * 4, out_lens = uint64_t(num_out) * 4;
     if (overlap(block_table_out, out_rows, block_table, in_rows) ||
+        overlap(block_table_out, out_rows, context_lens_out, out_lens) ||
+        overlap(block_table_out, out_rows, parents, out_lens) ||
+        overlap(block_table_out, out_rows, share_lens, share_lens ? out_lens : 0) ||
         overlap(block_table_out, out_rows, context_lens, in_lens) ||
         overlap(context_lens_out, out_lens, context_lens, in_lens) ||
         overlap(context_lens_out, out_lens, block_table, in_rows) ||
